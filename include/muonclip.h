@@ -284,6 +284,53 @@ typedef struct {
 mc_status qk_attention_forward(const mc_attn_desc* attn, const mc_attn_out* out, float* smax,
                                int32_t accumulate, int32_t* status, mc_stream_t stream);
 
+/* Inputs beside q, k and k_shared, and outputs, of the attention backward.
+ * Everything is bf16 but lse; features have unit stride; the other strides are
+ * in elements, multiples of 8 (axes of one element: any), and pointers are
+ * 16-byte aligned.  Inputs may broadcast (stride 0); an output gives every
+ * element an address of its own and overlaps no input, no other output and not
+ * the workspace (outputs may interleave, as dk and dv in one buffer). */
+typedef struct {
+  const void* v;           /* device values [B, S, H, d_v]                          */
+  int32_t d_v;             /* value width, 16..128                                  */
+  int32_t _pad;
+  int64_t v_strides[3];    /* batch, sequence, head                                 */
+  const void* o;           /* device [B, S, H, d_v]: the forward's output           */
+  int64_t o_strides[3];
+  const float* lse;        /* device [B, H, S]: the forward's log-sum-exp           */
+  const void* d_o;         /* device [B, S, H, d_v]: gradient of o                  */
+  int64_t do_strides[3];
+  void* dq;                /* device [B, S, H, d_head + d_shared] (written)         */
+  int64_t dq_strides[3];
+  void* dk;                /* device [B, S, H, d_head] (written)                    */
+  int64_t dk_strides[3];
+  void* dk_shared;         /* device [B, S, d_shared] (written): the sum over the
+                              heads; unused when d_shared = 0                       */
+  int64_t dks_strides[2];  /* batch, sequence                                       */
+  void* dv;                /* device [B, S, H, d_v] (written)                       */
+  int64_t dv_strides[3];
+} mc_attn_grad;
+
+/* Bytes of workspace that qk_attention_backward needs for this shape (B, S, H,
+ * d_head, d_shared and dtype of *attn; its pointers are not looked at). */
+mc_status qk_attention_backward_workspace_size(const mc_attn_desc* attn, size_t* bytes);
+
+/* Gradients of qk_attention_forward's O with respect to q, k, k_shared and v
+ * ([K2-internals] "核心数学": O^h = softmax(scale Q^h K^h^T) V^h), from the o
+ * and lse that the forward wrote.  The probabilities are recomputed:
+ *   p_ij = exp(scale q_i.k_j - lse_i), ds_ij = p_ij (do_i.v_j - do_i.o_i),
+ *   dv_j = sum_i p_ij do_i, dq_i = scale sum_j ds_ij k_j,
+ *   dk_j = scale sum_i ds_ij q_i.
+ * Same shapes, types and limits as the forward (bf16; MC_ERR_UNSUPPORTED
+ * otherwise).  p and ds are rounded to bf16 as operands, sums are fp32, each
+ * gradient is rounded to bf16 once; no atomics, so equal inputs give equal
+ * bits.  workspace: device, 256-byte aligned, for this call alone while it
+ * runs.  S_max is a maximum for the clip, not part of the loss: it has no
+ * gradient.  A NaN/Inf gradient sets MC_STATUS_NONFINITE_UPDATE; NaN/Inf
+ * inputs may reach every gradient of their (batch, head). */
+mc_status qk_attention_backward(const mc_attn_desc* attn, const mc_attn_grad* grad, void* workspace,
+                                size_t workspace_bytes, int32_t* status, mc_stream_t stream);
+
 /* QK-Clip for one attention layer.  MC_CLIP_PER_HEAD: for every head with
  * smax[h] > tau, gamma_h = tau / smax[h] and every segment's rows of head h are
  * multiplied by gamma_h^exponent; heads with smax[h] <= tau are untouched bit

@@ -65,6 +65,16 @@ class McAttnOut(ctypes.Structure):
                 ("o", c_void_p), ("o_strides", c_int64 * 3), ("lse", c_void_p)]
 
 
+class McAttnGrad(ctypes.Structure):
+    _fields_ = [("v", c_void_p), ("d_v", c_int32), ("_pad", c_int32), ("v_strides", c_int64 * 3),
+                ("o", c_void_p), ("o_strides", c_int64 * 3), ("lse", c_void_p),
+                ("d_o", c_void_p), ("do_strides", c_int64 * 3),
+                ("dq", c_void_p), ("dq_strides", c_int64 * 3),
+                ("dk", c_void_p), ("dk_strides", c_int64 * 3),
+                ("dk_shared", c_void_p), ("dks_strides", c_int64 * 2),
+                ("dv", c_void_p), ("dv_strides", c_int64 * 3)]
+
+
 class McKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 24), ("launches", c_int32), ("ms", c_float)]
 
@@ -82,6 +92,9 @@ SIGNATURES = {
     "qk_max_logit": (c_int32, [POINTER(McAttnDesc), c_void_p, c_void_p, c_int32, c_void_p, c_void_p]),
     "qk_attention_forward": (c_int32, [POINTER(McAttnDesc), POINTER(McAttnOut), c_void_p, c_int32,
                                        c_void_p, c_void_p]),
+    "qk_attention_backward_workspace_size": (c_int32, [POINTER(McAttnDesc), POINTER(c_size_t)]),
+    "qk_attention_backward": (c_int32, [POINTER(McAttnDesc), POINTER(McAttnGrad), c_void_p, c_size_t,
+                                        c_void_p, c_void_p]),
     "qk_clip_apply": (c_int32, [c_void_p, c_int32, c_float, c_int32, POINTER(McClipSeg), c_int32,
                                 c_void_p, c_void_p, c_void_p, c_void_p]),
     "muonclip_step": (c_int32, [POINTER(McMat), POINTER(McMat), POINTER(McMat), c_int32,

@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from . import abi
-from .abi import McAttnDesc, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat, check
+from .abi import McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat, check
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 
@@ -193,6 +193,89 @@ def qk_attention_forward(q, k, v, k_shared=None, causal=True, scale=None, out=No
                                           int(bool(accumulate)), _ptr(status), _stream(stream)),
           "qk_attention_forward")
     return out, lse, smax
+
+
+def _same_device(**tensors):
+    """All given tensors on one CUDA device; returns it."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.device.type != "cuda":
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, not on {dev}")
+        dev = t.device
+    return dev
+
+
+def attention_backward_workspace_size(q, k, k_shared=None) -> int:
+    """Bytes of workspace that qk_attention_backward needs for these features."""
+    d = attn_desc(q, k, k_shared)
+    n = ctypes.c_size_t(0)
+    check(abi.load().qk_attention_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
+          "qk_attention_backward_workspace_size")
+    return n.value
+
+
+def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, scale=None, dq=None,
+                          dk=None, dv=None, dk_shared=None, workspace=None, status=None, stream=None):
+    """Gradients of qk_attention_forward's output: q [B,S,H,dq], k [B,S,H,dk],
+    k_shared [B,S,dr] or None, v, out and dout [B,S,H,dv] (bf16, contiguous
+    feature axes), lse [B,H,S] f32 as the forward returned it; causal and scale
+    as in the forward.  Returns (dq, dk, dv, dk_shared or None); outputs are
+    allocated unless given (any strides the features may have).  workspace: a
+    uint8 CUDA tensor of attention_backward_workspace_size bytes; without one,
+    one is allocated for the call."""
+    B, S, H, D = q.shape
+    dvw = v.shape[-1]
+    dev = _same_device(q=q, k=k, v=v, out=out, lse=lse, dout=dout, k_shared=k_shared, dq=dq, dk=dk, dv=dv,
+                       dk_shared=dk_shared, workspace=workspace, status=status)
+    for name, t, shape in (("k", k, (B, S, H, k.shape[-1])), ("v", v, (B, S, H, dvw)), ("out", out, (B, S, H, dvw)),
+                           ("dout", dout, (B, S, H, dvw))):
+        if tuple(t.shape) != shape or t.stride(3) != 1 or t.dtype != q.dtype:
+            raise ValueError(f"{name} must be {list(shape)} with a contiguous feature axis and q's dtype")
+    if k_shared is not None and tuple(k_shared.shape[:2]) != (B, S):
+        raise ValueError("k_shared must be [B, S, dr]")
+    if tuple(lse.shape) != (B, H, S) or not lse.is_contiguous() or lse.dtype != torch.float32:
+        raise ValueError("lse must be a contiguous [B, H, S] float32 tensor")
+    d = attn_desc(q, k, k_shared, causal, scale)
+
+    def output(name, t, shape):
+        if t is None:
+            return torch.empty(shape, dtype=q.dtype, device=dev)
+        if tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 or t.dtype != q.dtype:
+            raise ValueError(f"{name} must be {list(shape)} with a contiguous feature axis and q's dtype")
+        return t
+
+    dq = output("dq", dq, (B, S, H, D))
+    dk = output("dk", dk, k.shape)
+    dv = output("dv", dv, v.shape)
+    if k_shared is not None:
+        dk_shared = output("dk_shared", dk_shared, k_shared.shape)
+    elif dk_shared is not None:
+        raise ValueError("dk_shared without k_shared")
+    g = McAttnGrad()
+    g.d_v = dvw
+    g.lse = lse.data_ptr()
+    for ptr, st, t in (("v", "v_strides", v), ("o", "o_strides", out), ("d_o", "do_strides", dout),
+                       ("dq", "dq_strides", dq), ("dk", "dk_strides", dk), ("dv", "dv_strides", dv)):
+        setattr(g, ptr, t.data_ptr())
+        getattr(g, st)[:] = t.stride()[:3]
+    if dk_shared is not None:
+        g.dk_shared = dk_shared.data_ptr()
+        g.dks_strides[:] = dk_shared.stride()[:2]
+    lib = abi.load()
+    with torch.cuda.device(dev):
+        if workspace is None:
+            n = ctypes.c_size_t(0)
+            check(lib.qk_attention_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
+                  "qk_attention_backward_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        check(lib.qk_attention_backward(ctypes.byref(d), ctypes.byref(g), _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _ptr(status),
+                                        _stream(stream)), "qk_attention_backward")
+    return dq, dk, dv, dk_shared
 
 
 @dataclass

@@ -41,8 +41,8 @@ mc_status cuda_fail(cudaError_t e, const char* what) {
 }
 
 // ------------------------------------------------------------------ profiler
-enum ProfClass { kPrep, kNorms, kGemm, kApply, kClip, kMaxLogit, kAttnFwd, kNumProf };
-const char* kProfNames[kNumProf] = {"prep", "norms", "ns_gemm", "apply", "clip", "max_logit", "attn_fwd"};
+enum ProfClass { kPrep, kNorms, kGemm, kApply, kClip, kMaxLogit, kAttnFwd, kAttnBwd, kNumProf };
+const char* kProfNames[kNumProf] = {"prep", "norms", "ns_gemm", "apply", "clip", "max_logit", "attn_fwd", "attn_bwd"};
 
 struct Profiler {
   bool on = false;
@@ -946,6 +946,149 @@ mc_status qk_attention_forward(const mc_attn_desc* a, const mc_attn_out* out, fl
   if (e != cudaSuccess) {
     if (err[0]) return fail(MC_ERR_CUDA, "attention forward: %s", err);
     return cuda_fail(e, "attention forward launch");
+  }
+  return ok();
+}
+
+namespace {
+
+// Workspace of the attention backward, in 256-byte aligned parts.
+struct AttnBwdPlan {
+  size_t nlse, delta, part, bytes;
+};
+AttnBwdPlan plan_attn_bwd(int64_t B, int64_t S, int64_t H, int64_t d_shared) {
+  const size_t rows = (size_t)round_up(B * H * attn_bwd_padded_rows((int)S) * 4, 256);
+  AttnBwdPlan w;
+  w.nlse = 0;
+  w.delta = rows;
+  w.part = 2 * rows;
+  w.bytes = w.part + (size_t)round_up(B * H * S * d_shared * 4, 256);
+  return w;
+}
+
+mc_status check_attn_shape(const mc_attn_desc* a) {
+  if (!a) return fail(MC_ERR_INVALID_ARG, "attn: null");
+  if (a->B < 1 || a->S < 1 || a->H < 1 || a->d_head < 1 || a->d_shared < 0)
+    return fail(MC_ERR_INVALID_ARG, "attn: B, S, H, d_head must be >= 1 and d_shared >= 0");
+  if (a->dtype != MC_F32 && a->dtype != MC_BF16)
+    return fail(MC_ERR_INVALID_ARG, "attn: unknown dtype %d", a->dtype);
+  if (a->dtype != MC_BF16) return fail(MC_ERR_UNSUPPORTED, "attention backward: bf16 only");
+  if (a->S > (1 << 30) || (int64_t)a->B * a->H > (1ll << 30) ||
+      (int64_t)a->B * a->H * a->S > (1ll << 40))
+    return fail(MC_ERR_UNSUPPORTED, "attention backward: B %d, S %d, H %d are too large", a->B, a->S, a->H);
+  return MC_OK;
+}
+
+// One strided [B, S, H, width] (or [B, S, width]: H = 1) tensor of the attention
+// backward.  Copies its strides with those of axes of one element, which
+// address nothing, replaced by a valid value.  An output must give every
+// element an address of its own.
+mc_status check_attn_tensor(const char* name, const void* ptr, const int64_t* st, int n, const int64_t* extent,
+                            int64_t width, bool output, long long* out) {
+  if (!ptr) return fail(MC_ERR_INVALID_ARG, "attention backward: %s is null", name);
+  if (!aligned16(ptr)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s must be 16-byte aligned", name);
+  int64_t s[3], e[3];
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    out[i] = extent[i] == 1 ? round_up(width, 8) : st[i];
+    if (out[i] < 0) return fail(MC_ERR_INVALID_ARG, "attention backward: %s has a negative stride", name);
+    if (out[i] % 8) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides must be multiples of 8 elements", name);
+    if (out[i] >= (1ll << 38)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides are too large", name);
+    if (extent[i] > 1) { s[m] = st[i]; e[m] = extent[i]; ++m; }
+  }
+  if (!output) return MC_OK;
+  for (int i = 1; i < m; ++i)            // by ascending stride
+    for (int j = i; j > 0 && s[j] < s[j - 1]; --j) { std::swap(s[j], s[j - 1]); std::swap(e[j], e[j - 1]); }
+  int64_t span = width;                  // elements that the inner axes reach over
+  for (int i = 0; i < m; ++i) {
+    if (s[i] < span) return fail(MC_ERR_INVALID_ARG, "attention backward: elements of %s share addresses", name);
+    span += s[i] * (e[i] - 1);
+  }
+  return MC_OK;
+}
+
+}  // namespace
+
+mc_status qk_attention_backward_workspace_size(const mc_attn_desc* a, size_t* bytes) {
+  mc_status st = check_attn_shape(a);
+  if (st != MC_OK) return st;
+  if (!bytes) return fail(MC_ERR_INVALID_ARG, "bytes: null");
+  *bytes = plan_attn_bwd(a->B, a->S, a->H, a->d_shared).bytes;
+  return ok();
+}
+
+mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, void* workspace,
+                                size_t workspace_bytes, int32_t* status, mc_stream_t stream) {
+  mc_status st = check_attn_shape(a);
+  if (st != MC_OK) return st;
+  if (!g) return fail(MC_ERR_INVALID_ARG, "attention backward: null gradient descriptor");
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale))
+    return fail(MC_ERR_INVALID_ARG, "attn: scale must be finite and > 0");
+  AttnBwdParams p;
+  memset(&p, 0, sizeof p);
+  p.B = a->B; p.S = a->S; p.H = a->H; p.d_head = a->d_head; p.d_shared = a->d_shared;
+  p.d_v = g->d_v;
+  p.causal = a->causal != 0; p.scale = a->scale;
+  p.status = status;
+  char err[256] = {0};
+  if (!attn_bwd_supported(p, err, sizeof err)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s", err);
+  const int64_t ext[3] = {a->B, a->S, a->H};
+  const int64_t D = (int64_t)a->d_head + a->d_shared;
+  struct T { const char* name; const void* ptr; const int64_t* st; int n; int64_t width; bool out; long long* to; };
+  const T ts[] = {
+      {"q", a->q, a->q_strides, 3, D, false, p.qs},
+      {"k", a->k, a->k_strides, 3, a->d_head, false, p.kst},
+      {"v", g->v, g->v_strides, 3, g->d_v, false, p.vs},
+      {"o", g->o, g->o_strides, 3, g->d_v, false, p.os},
+      {"d_o", g->d_o, g->do_strides, 3, g->d_v, false, p.dos},
+      {"dq", g->dq, g->dq_strides, 3, D, true, p.dqs},
+      {"dk", g->dk, g->dk_strides, 3, a->d_head, true, p.dks},
+      {"dv", g->dv, g->dv_strides, 3, g->d_v, true, p.dvs},
+      {"k_shared", a->k_shared, a->ks_strides, 2, a->d_shared, false, p.kss},
+      {"dk_shared", g->dk_shared, g->dks_strides, 2, a->d_shared, true, p.dkshs},
+  };
+  const int nt = a->d_shared > 0 ? 10 : 8;
+  uintptr_t lo[10], hi[10];
+  for (int i = 0; i < nt; ++i) {
+    st = check_attn_tensor(ts[i].name, ts[i].ptr, ts[i].st, ts[i].n, ext, ts[i].width, ts[i].out, ts[i].to);
+    if (st != MC_OK) return st;
+    int64_t last = ts[i].width;
+    for (int d = 0; d < ts[i].n; ++d) last += (ext[d] - 1) * ts[i].to[d];
+    lo[i] = reinterpret_cast<uintptr_t>(ts[i].ptr);
+    hi[i] = lo[i] + (uintptr_t)last * 2;
+  }
+  // a launch reads its inputs while others' outputs are written: no output may
+  // lie among the inputs (two outputs may interleave, as dk and dv of one buffer)
+  for (int i = 0; i < nt; ++i)
+    for (int j = 0; j < nt; ++j)
+      if (ts[i].out && i != j) {
+        if (!ts[j].out && lo[i] < hi[j] && lo[j] < hi[i])
+          return fail(MC_ERR_INVALID_ARG, "attention backward: %s overlaps %s", ts[i].name, ts[j].name);
+        if (ts[j].out && lo[i] == lo[j])
+          return fail(MC_ERR_INVALID_ARG, "attention backward: %s and %s are the same memory", ts[i].name, ts[j].name);
+      }
+  if (!g->lse || (reinterpret_cast<uintptr_t>(g->lse) & 3u) != 0)
+    return fail(MC_ERR_INVALID_ARG, "attention backward: lse must be given, 4-byte aligned");
+  const AttnBwdPlan w = plan_attn_bwd(a->B, a->S, a->H, a->d_shared);
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(MC_ERR_WORKSPACE, "attention backward: workspace must be given, 256-byte aligned");
+  if (workspace_bytes < w.bytes)
+    return fail(MC_ERR_WORKSPACE, "attention backward: workspace of %zu bytes, %zu needed", workspace_bytes, w.bytes);
+  p.q = a->q; p.k = a->k; p.ks = a->k_shared; p.v = g->v; p.o = g->o; p.d_o = g->d_o;
+  p.lse = g->lse;
+  p.dq = g->dq; p.dk = g->dk; p.dksh = g->dk_shared; p.dv = g->dv;
+  char* base = static_cast<char*>(workspace);
+  p.nlse = reinterpret_cast<float*>(base + w.nlse);
+  p.delta = reinterpret_cast<float*>(base + w.delta);
+  p.part = reinterpret_cast<float*>(base + w.part);
+  cudaError_t e;
+  {
+    ProfScope ps(kAttnBwd, a->d_shared > 0 ? 4 : 3, (cudaStream_t)stream);
+    e = launch_attn_bwd(p, (cudaStream_t)stream, err, sizeof err);
+  }
+  if (e != cudaSuccess) {
+    if (err[0]) return fail(MC_ERR_CUDA, "attention backward: %s", err);
+    return cuda_fail(e, "attention backward launch");
   }
   return ok();
 }

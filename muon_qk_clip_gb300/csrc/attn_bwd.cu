@@ -1,0 +1,939 @@
+// Attention backward that recomputes the probabilities ([K2-internals]
+// "核心数学": O^h = softmax(scale * Q^h K^h^T) V^h), per (batch, head):
+//
+//   p_ij  = exp(scale q_i . k_j - lse_i)      (0 above the diagonal when causal)
+//   delta_i = do_i . o_i
+//   dv_j  = sum_i p_ij do_i
+//   ds_ij = p_ij (do_i . v_j - delta_i)
+//   dq_i  = scale sum_j ds_ij k_j
+//   dk_j  = scale sum_i ds_ij q_i             (its shared rotary columns summed over the heads)
+//
+// Four launches on the caller's stream, no atomics, so equal inputs give equal
+// bits:
+//   rows_kernel     delta and -lse log2(e) of every row, padded to whole tiles
+//   dkv_kernel      one CTA per 128 keys, loop over query tiles: S^T = K Q^T,
+//                   dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
+//   dq_kernel       one CTA per 128 queries, loop over key tiles: S = Q K^T,
+//                   dP = dO V^T, dQ += dS K
+//   shared_kernel   the shared key's gradient, summed over the heads in order
+// Two passes recompute S and dP (7 products for the 5 that the formulas need),
+// but dQ never leaves the chip as partial sums: one pass would add a 128 x D
+// fp32 tile to global memory per tile pair and hold dQ, dK, dV, S and dP in
+// tensor memory at once (640 or more of its 512 columns).
+//
+// P and dS go from the compute warps to the tensor core through tensor memory
+// (the A operand of dV, dK and dQ), written over the columns of the S / dP that
+// they came from, rounded to bf16 like every operand; sums are fp32.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "common.cuh"
+#include "fastdiv.cuh"
+#include "kernels.h"
+
+namespace mc {
+namespace {
+namespace ab {
+
+constexpr int BM = 128;                  // rows of a work item: keys (dkv) or queries (dq)
+constexpr int kThreads = 320;            // producer, MMA issuer, 8 compute warps
+constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk (128-byte swizzle)
+constexpr uint32_t kTmemCols = 512;
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct Maps {
+  CUtensorMap q, k, ks, v, d_o;
+};
+
+struct Geo {
+  int nch, nck, ncv;    // 64-wide chunks of q.k, of its head-specific part, of d_v
+  int nb;               // 128-row blocks per (b, h)
+  int nt;               // dkv: query tiles per (b, h)
+  int vst;              // dq: value stages
+  int nunit;            // units per (b, h): pairs of blocks when causal
+  uint32_t units;       // below 2^30 (checked on the host)
+  long long sp;         // padded row length of nlse and delta
+  FastDiv div_nunit, div_h;
+};
+
+// Work order as in the forward: causal units are pairs of blocks (u, nb-1-u)
+// of one (b, h), equal in work whatever u is, numbered (b, h)-major so that the
+// CTAs in flight share a few heads in L2.  Returns 1 with an item, 0 for the
+// missing half of an unpaired middle block, -1 at the end.
+__device__ inline int next_item(const AttnBwdParams& p, const Geo& g, uint32_t n, int& b, int& h, int& blk) {
+  const uint32_t u = blockIdx.x + (n >> 1) * gridDim.x;
+  if (u >= g.units) return -1;
+  const uint32_t bh = fastdiv(u, g.div_nunit);
+  const int pu = (int)(u - bh * (uint32_t)g.nunit);
+  b = (int)fastdiv(bh, g.div_h);
+  h = (int)(bh - (uint32_t)b * (uint32_t)p.H);
+  if (!p.causal) {
+    blk = pu;
+    return (n & 1) ? 0 : 1;
+  }
+  if ((n & 1) == 0) { blk = g.nb - 1 - pu; return 1; }
+  blk = pu;
+  return pu < g.nb - 1 - pu ? 1 : 0;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T: A is M rows (lanes) of bf16 pairs, K-major.
+__device__ inline void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                 uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 lanes x 8 columns of 32-bit values into TMEM
+__device__ inline void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+__device__ inline uint32_t pack_bf16(float a, float b) {
+  __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h2);
+}
+
+// All 32 lanes wait; true only if every lane saw the phase complete.
+__device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
+  const bool ok = mbar_wait(bar, parity, abort_flag);
+  return __all_sync(0xffffffffu, ok);
+}
+
+// 16 values v[0..16) of one output row to dst[0 .. n) (n <= 16 of them exist),
+// as bf16; dst is 16-byte aligned.
+__device__ inline void store_row16(__nv_bfloat16* dst, const float (&v)[16], int n) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    if (8 * u + 8 <= n) {
+      *reinterpret_cast<uint4*>(dst + 8 * u) =
+          make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
+                     pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (8 * u + x < n) dst[8 * u + x] = __float2bfloat16_rn(v[8 * u + x]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- rows
+// delta_i = sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
+// in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
+// delta = 0.  16 lanes per (b, i, h), 8 features each.  Streams o and do once.
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const long long sp) {
+  const int sub = threadIdx.x & 15;
+  const long long per = 256 / 16;
+  const long long rows = (long long)p.B * sp * p.H;
+  for (long long r = (long long)blockIdx.x * per + (threadIdx.x >> 4);; r += (long long)gridDim.x * per) {
+    // whole warps leave together: the shuffles below need every lane
+    if (__all_sync(0xffffffffu, r >= rows)) break;
+    const bool in = r < rows;
+    const long long bi = in ? r / p.H : 0;
+    const int h = in ? (int)(r - bi * p.H) : 0;
+    const int b = (int)(bi / sp);
+    const long long i = bi - (long long)b * sp;
+    float s = 0.f;
+    const bool live = in && i < p.S;
+    if (live) {
+      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + i * p.os[1] + h * p.os[2];
+      const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + i * p.dos[1] + h * p.dos[2];
+      const int c0 = sub * 8;
+      if (c0 + 8 <= p.d_v) {
+        const uint4 a = *reinterpret_cast<const uint4*>(o + c0), e = *reinterpret_cast<const uint4*>(d + c0);
+        const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
+        const __nv_bfloat162* e2 = reinterpret_cast<const __nv_bfloat162*>(&e);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 fa = __bfloat1622float2(a2[x]), fe = __bfloat1622float2(e2[x]);
+          s = fmaf(fa.x, fe.x, s);
+          s = fmaf(fa.y, fe.y, s);
+        }
+      } else {
+        for (int c = c0; c < p.d_v; ++c) s = fmaf(__bfloat162float(o[c]), __bfloat162float(d[c]), s);
+      }
+    }
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (in && sub == 0) {
+      const long long at = ((long long)b * p.H + h) * sp + i;
+      p.delta[at] = s;
+      p.nlse[at] = live ? -p.lse[((long long)b * p.H + h) * p.S + i] * kLog2e : -INFINITY;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ dK, dV
+// Tensor memory: dK [0, 64 nch), dV [.., + 64 ncv), then S^T and dP^T of NQ
+// columns each: 128 + 128 + 2 * 128 with q.k lengths up to 128, 192 + 128 +
+// 2 * 96 above, hence the 96-query tile there.  P^T / dS^T (bf16) take the
+// first half of each half of the columns of S^T / dP^T, so no warp overwrites
+// columns that the other warp of its lanes still has to read.
+//
+// The issue order per query tile t is dV(t), S(t+1), dK(t), dP(t+1): while the
+// compute warps turn dP(t) into dS(t) the tensor core runs dV(t) and S(t+1),
+// while they turn S(t+1) into P(t+1) it runs dK(t) and dP(t+1).  The products of
+// one issuing thread execute in order, so S(t+1) follows dV(t)'s reads of P(t)
+// and dP(t+1) follows dK(t)'s reads of dS(t) without a wait.
+template <int NQ>
+__global__ void __launch_bounds__(kThreads, 1)
+    dkv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+  constexpr int NH = NQ / 2;             // queries per compute warp
+  constexpr int CQ = NQ * 128;           // bytes of one chunk of a query tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kbuf = smem;                                    // nch chunks
+  uint8_t* vbuf = kbuf + g.nch * CH;                       // ncv chunks
+  uint8_t* qbuf = vbuf + g.ncv * CH;                       // 2 x nch chunks
+  uint8_t* dobuf = qbuf + 2 * g.nch * CQ;                  // 2 x ncv chunks
+  float* rowv = reinterpret_cast<float*>(dobuf + 2 * g.ncv * CQ);   // [2 stages][nlse, delta][NQ]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rowv + 4 * NQ);
+  uint64_t* kv_full = bars + 0;
+  uint64_t* kv_empty = bars + 1;
+  uint64_t* q_full = bars + 2;      // [2] Q tile with its nlse and delta
+  uint64_t* q_empty = bars + 4;     // [2]
+  uint64_t* do_full = bars + 6;     // [2]
+  uint64_t* do_empty = bars + 8;    // [2]
+  uint64_t* s_full = bars + 10;
+  uint64_t* p_full = bars + 11;
+  uint64_t* dp_full = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* acc_full = bars + 14;
+  uint64_t* acc_empty = bars + 15;
+  uint64_t* drain = bars + 16;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1);
+      mbar_init(&do_full[s], 1); mbar_init(&do_empty[s], 1);
+    }
+    mbar_init(s_full, 1); mbar_init(p_full, 8);
+    mbar_init(dp_full, 1); mbar_init(ds_full, 8);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
+    if (g.nch > g.nck) prefetch_tmap(&mp.ks);
+  }
+  if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * g.nch, t_s = t_dv + 64 * g.ncv, t_dp = t_s + NQ;
+  auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
+  // first query tile that has a query at or behind the block's first key
+  auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t t = 0, li = 0;
+      bool used_kv = false, used_q[2] = {}, used_do[2] = {};
+      uint32_t par_kv = 0, par_q[2] = {}, par_do[2] = {};
+      for (uint32_t n = 0; !abort_flag; ++n) {
+        int b, h, blk;
+        const int st = next_item(p, g, n, b, h, blk);
+        if (st < 0) break;
+        if (st == 0) continue;
+        const int t0 = first_tile(blk);
+        const long long rowbase = ((long long)b * p.H + h) * g.sp;
+        bool ok = true;
+        for (int it = t0; it < g.nt && ok; ++it, ++t) {
+          const int s = t & 1;
+          const uint32_t ph = (t >> 1) & 1;
+          if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          mbar_arrive_expect_tx(&q_full[s], g.nch * CQ + 2 * NQ * 4);
+          for (int c = 0; c < g.nch; ++c)
+            tma_load_4d(qbuf + (s * g.nch + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
+          bulk_load_1d(rowv + s * 2 * NQ, p.nlse + rowbase + it * NQ, NQ * 4, &q_full[s]);
+          bulk_load_1d(rowv + s * 2 * NQ + NQ, p.delta + rowbase + it * NQ, NQ * 4, &q_full[s]);
+          used_q[s] = true; par_q[s] = ph;
+          if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          mbar_arrive_expect_tx(&do_full[s], g.ncv * CQ);
+          for (int c = 0; c < g.ncv; ++c)
+            tma_load_4d(dobuf + (s * g.ncv + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
+          used_do[s] = true; par_do[s] = ph;
+          if (it == t0) {        // the item's keys and values, behind its first query tile
+            if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+            mbar_arrive_expect_tx(kv_full, (g.nch + g.ncv) * CH);
+            for (int c = 0; c < g.nch; ++c) {
+              if (c < g.nck) tma_load_4d(kbuf + c * CH, &mp.k, kv_full, 64 * c, h, blk * BM, b);
+              else tma_load_3d(kbuf + c * CH, &mp.ks, kv_full, 64 * (c - g.nck), blk * BM, b);
+            }
+            for (int c = 0; c < g.ncv; ++c) tma_load_4d(vbuf + c * CH, &mp.v, kv_full, 64 * c, h, blk * BM, b);
+            used_kv = true; par_kv = li & 1;
+          }
+        }
+        if (!ok) break;
+        ++li;
+      }
+      // every issued copy must have landed before the CTA may exit
+      if (used_kv) mbar_wait(kv_full, par_kv, nullptr);
+      for (int s = 0; s < 2; ++s) {
+        if (used_q[s]) mbar_wait(&q_full[s], par_q[s], nullptr);
+        if (used_do[s]) mbar_wait(&do_full[s], par_do[s], nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = make_idesc_bf16(BM, NQ, 0, 0);
+      const uint32_t idesc_dv = make_idesc_bf16(BM, 64 * g.ncv, 0, 1);
+      const uint32_t idesc_dk = make_idesc_bf16(BM, 64 * g.nch, 0, 1);
+      const uint32_t ka = smem_u32(kbuf), va = smem_u32(vbuf);
+      uint32_t t = 0, li = 0;
+      bool issued = false;
+      auto scores = [&](uint32_t tt) {       // S^T = K Q^T
+        const uint32_t qa = smem_u32(qbuf + (tt & 1) * g.nch * CQ);
+        for (int c = 0; c < g.nch; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma(t_s, make_sdesc_sw128(ka + c * CH + kk * 32, 16, 1024),
+                   make_sdesc_sw128(qa + c * CQ + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(s_full);
+      };
+      auto dprobs = [&](uint32_t tt) {       // dP^T = V dO^T
+        const uint32_t da = smem_u32(dobuf + (tt & 1) * g.ncv * CQ);
+        for (int c = 0; c < g.ncv; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma(t_dp, make_sdesc_sw128(va + c * CH + kk * 32, 16, 1024),
+                   make_sdesc_sw128(da + c * CQ + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+        tc_commit(dp_full);
+      };
+      // A (tensor memory): NQ / 16 k-steps of 8 columns; the second half of the
+      // queries starts at column NH.  B: rows of 64 features (MN-major), 16
+      // query rows = 2048 bytes per k-step.
+      auto accumulate = [&](uint32_t d, uint32_t a, uint32_t b0, uint32_t idesc, bool add) {
+#pragma unroll
+        for (int kk = 0; kk < NQ / 16; ++kk) {
+          constexpr int half = NQ / 32;
+          const uint32_t ac = a + (kk < half ? kk * 8 : NH + (kk - half) * 8);
+          tc_mma_ts(d, ac, make_sdesc(b0 + kk * 2048, CQ, 1024, 2), idesc, (add || kk > 0) ? 1u : 0u);
+        }
+      };
+      for (uint32_t n = 0; !abort_flag; ++n) {
+        int b, h, blk;
+        const int st = next_item(p, g, n, b, h, blk);
+        if (st < 0) break;
+        if (st == 0) continue;
+        const int nt = g.nt - first_tile(blk);
+        bool ok = mbar_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && mbar_wait(kv_full, li & 1, &abort_flag);
+        if (!ok) { fail(); break; }
+        tc_fence_after();
+        scores(t);
+        issued = true;
+        if (!mbar_wait(&do_full[t & 1], (t >> 1) & 1, &abort_flag)) { fail(); break; }
+        tc_fence_after();
+        dprobs(t);
+        if (nt == 1) tc_commit(kv_empty);
+        for (int i = 0; i < nt; ++i, ++t) {
+          const int s = t & 1, s1 = s ^ 1;
+          const uint32_t ph1 = ((t + 1) >> 1) & 1;
+          if (!mbar_wait(p_full, t & 1, &abort_flag)) { ok = false; break; }
+          if (i == 0 && !mbar_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          accumulate(t_dv, t_s, smem_u32(dobuf + s * g.ncv * CQ), idesc_dv, i > 0);
+          tc_commit(&do_empty[s]);
+          if (i + 1 < nt) {
+            if (!mbar_wait(&q_full[s1], ph1, &abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            scores(t + 1);
+          }
+          if (!mbar_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          accumulate(t_dk, t_dp, smem_u32(qbuf + s * g.nch * CQ), idesc_dk, i > 0);
+          tc_commit(&q_empty[s]);
+          if (i + 1 < nt) {
+            if (!mbar_wait(&do_full[s1], ph1, &abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            dprobs(t + 1);
+            if (i + 2 == nt) tc_commit(kv_empty);
+          }
+        }
+        if (!ok) { fail(); break; }
+        tc_commit(acc_full);
+        ++li;
+      }
+      if (issued) { tc_commit(drain); mbar_wait(drain, 0, nullptr); }
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS, epilogue
+    // Warp e = warp - 2: keys 32 q .. 32 q + 31 of the block (q = warp & 3, its
+    // TMEM lane quadrant), queries of half e >> 2 of the tile; in the epilogue
+    // that half of the dK and dV columns.
+    const int q = warp & 3, hf = (warp - 2) >> 2;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH;
+    const float c2 = p.scale * kLog2e;
+    uint32_t t = 0, li = 0;
+    bool bad = false;
+    for (uint32_t n = 0;; ++n) {
+      int b, h, blk;
+      const int st = next_item(p, g, n, b, h, blk);
+      if (st < 0) break;
+      if (st == 0) continue;
+      const int j = blk * BM + row;                     // this thread's key
+      bool ok = true;
+      for (int it = first_tile(blk); it < g.nt; ++it, ++t) {
+        const float* nl = rowv + (t & 1) * 2 * NQ + hf * NH;
+        const int i0 = it * NQ + hf * NH;
+        const bool diag = p.causal && i0 < blk * BM + q * 32 + 31;   // some (i, j) of the warp has i < j
+        ok = warp_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && warp_wait(s_full, t & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        float pv[NH];
+        {
+          uint32_t r[NH / 16][16];
+#pragma unroll
+          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(ts + c * 16, r[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
+#pragma unroll
+          for (int x = 0; x < NH; x += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(nl + x);
+            pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, l.x));
+            pv[x + 1] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 1]), c2, l.y));
+            pv[x + 2] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 2]), c2, l.z));
+            pv[x + 3] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 3]), c2, l.w));
+          }
+        }
+        if (diag) {
+#pragma unroll
+          for (int x = 0; x < NH; ++x)
+            if (i0 + x < j) pv[x] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < NH / 16; ++c) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
+          tmem_st_32x32b_x8(ts + c * 8, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full);
+
+        ok = warp_wait(dp_full, t & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          uint32_t r[NH / 16][16];
+#pragma unroll
+          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(tdp + c * 16, r[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
+#pragma unroll
+          for (int x = 0; x < NH; x += 4) {
+            const float4 d = *reinterpret_cast<const float4*>(nl + NQ + x);
+            pv[x] *= __uint_as_float(r[x / 16][x % 16]) - d.x;
+            pv[x + 1] *= __uint_as_float(r[x / 16][x % 16 + 1]) - d.y;
+            pv[x + 2] *= __uint_as_float(r[x / 16][x % 16 + 2]) - d.z;
+            pv[x + 3] *= __uint_as_float(r[x / 16][x % 16 + 3]) - d.w;
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < NH / 16; ++c) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
+          tmem_st_32x32b_x8(tdp + c * 8, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
+      if (!ok) { if (lane == 0) fail(); break; }
+      tc_fence_after();
+      // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
+      // per-head fp32 partial sums
+      const bool live = j < p.S;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + j * p.dvs[1] + h * p.dvs[2];
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + j * p.dks[1] + h * p.dks[2];
+      float* part = p.part + (((long long)b * p.H + h) * p.S + j) * p.d_shared;
+      for (int c = 0; c < 2 * g.ncv + 2 * g.nch; ++c) {
+        const bool is_v = c < 2 * g.ncv;
+        const int col = is_v ? hf * 32 * g.ncv + c * 16 : hf * 32 * g.nch + (c - 2 * g.ncv) * 16;
+        uint32_t r[16];
+        tmem_ld_32x32b_x16_async((is_v ? t_dv : t_dk) + lanes + col, r);
+        tmem_ld_wait();
+        reg_fence16(r);
+        float v[16];
+        const float sc = is_v ? 1.f : p.scale;
+        int width = is_v ? p.d_v - col : col < 64 * g.nck ? p.d_head - col : p.d_head + p.d_shared - col;
+        if (width > 16) width = 16;
+        if (live && width > 0) {
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            v[x] = __uint_as_float(r[x]) * sc;
+            if (x < width) bad |= !finite_f(v[x]);
+          }
+          if (is_v) store_row16(dv + col, v, width);
+          else if (col < 64 * g.nck) store_row16(dk + col, v, width);
+          else {
+#pragma unroll
+            for (int x = 0; x < 16; ++x)
+              if (x < width) part[col - p.d_head + x] = v[x];
+          }
+        }
+        __syncwarp();                    // the next load takes the whole warp
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      ++li;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// --------------------------------------------------------------------- dQ
+// Tensor memory: dQ [0, 192), S, dP (128 columns each), dS (64): dS has columns
+// of its own, so S(t+1) starts as soon as S(t) has been read and dP(t+1) as soon
+// as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1), dQ(t).
+constexpr int BN = 128;
+
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;                                   // nch chunks
+  uint8_t* dobuf = qbuf + g.nch * CH;                     // ncv chunks
+  uint8_t* kbuf = dobuf + g.ncv * CH;                     // 2 x nch chunks
+  uint8_t* vbuf = kbuf + 2 * g.nch * CH;                  // vst x ncv chunks
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + g.vst * g.ncv * CH);
+  uint64_t* q_full = bars + 0;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* k_full = bars + 2;      // [2]
+  uint64_t* k_empty = bars + 4;     // [2]
+  uint64_t* v_full = bars + 6;      // [2]
+  uint64_t* v_empty = bars + 8;     // [2]
+  uint64_t* s_full = bars + 10;
+  uint64_t* s_empty = bars + 11;
+  uint64_t* dp_full = bars + 12;
+  uint64_t* ds_full = bars + 13;
+  uint64_t* ds_empty = bars + 14;
+  uint64_t* acc_full = bars + 15;
+  uint64_t* acc_empty = bars + 16;
+  uint64_t* drain = bars + 17;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  __shared__ volatile int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_init(q_full, 1); mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1);
+    }
+    mbar_init(s_full, 1); mbar_init(s_empty, 8);
+    mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
+    if (g.nch > g.nck) prefetch_tmap(&mp.ks);
+  }
+  if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t t_dq = tmem_base, t_s = tmem_base + 192, t_dp = t_s + BN, t_ds = t_dp + BN;
+  auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
+  auto tiles = [&](int blk) {
+    const int hi = p.causal ? min(p.S, (blk + 1) * BM) : p.S;
+    return (hi + BN - 1) / BN;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      uint32_t t = 0, li = 0, vs = 0, vph = 0;
+      bool used_q = false, used_k[2] = {}, used_v[2] = {};
+      uint32_t par_q = 0, par_k[2] = {}, par_v[2] = {};
+      for (uint32_t n = 0; !abort_flag; ++n) {
+        int b, h, blk;
+        const int st = next_item(p, g, n, b, h, blk);
+        if (st < 0) break;
+        if (st == 0) continue;
+        const int nt = tiles(blk);
+        bool ok = true;
+        for (int it = 0; it < nt && ok; ++it, ++t) {
+          const int s = t & 1;
+          const uint32_t ph = (t >> 1) & 1;
+          if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          mbar_arrive_expect_tx(&k_full[s], g.nch * CH);
+          for (int c = 0; c < g.nch; ++c) {
+            uint8_t* dst = kbuf + (s * g.nch + c) * CH;
+            if (c < g.nck) tma_load_4d(dst, &mp.k, &k_full[s], 64 * c, h, it * BN, b);
+            else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
+          }
+          used_k[s] = true; par_k[s] = ph;
+          if (it == 0) {         // the item's queries, behind its first keys
+            if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+            mbar_arrive_expect_tx(q_full, (g.nch + g.ncv) * CH);
+            for (int c = 0; c < g.nch; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
+            for (int c = 0; c < g.ncv; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
+            used_q = true; par_q = li & 1;
+          }
+          if (!mbar_wait(&v_empty[vs], vph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          mbar_arrive_expect_tx(&v_full[vs], g.ncv * CH);
+          for (int c = 0; c < g.ncv; ++c)
+            tma_load_4d(vbuf + (vs * g.ncv + c) * CH, &mp.v, &v_full[vs], 64 * c, h, it * BN, b);
+          used_v[vs] = true; par_v[vs] = vph;
+          if (++vs == (uint32_t)g.vst) { vs = 0; vph ^= 1; }
+        }
+        if (!ok) break;
+        ++li;
+      }
+      if (used_q) mbar_wait(q_full, par_q, nullptr);
+      for (int s = 0; s < 2; ++s) {
+        if (used_k[s]) mbar_wait(&k_full[s], par_k[s], nullptr);
+        if (used_v[s]) mbar_wait(&v_full[s], par_v[s], nullptr);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = make_idesc_bf16(BM, BN, 0, 0);
+      const uint32_t idesc_dq = make_idesc_bf16(BM, 64 * g.nch, 0, 1);
+      const uint32_t qa = smem_u32(qbuf), da = smem_u32(dobuf);
+      uint32_t t = 0, li = 0, vs = 0, vph = 0;
+      bool issued = false;
+      auto product = [&](uint32_t d, uint32_t a, uint32_t b0, int nc) {
+        for (int c = 0; c < nc; ++c)
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma(d, make_sdesc_sw128(a + c * CH + kk * 32, 16, 1024),
+                   make_sdesc_sw128(b0 + c * CH + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+      };
+      // dP(t) = dO V_t^T; `last`: the item's queries and gradients are free after it
+      auto dprobs = [&](bool last) -> bool {
+        if (!mbar_wait(&v_full[vs], vph, &abort_flag)) return false;
+        tc_fence_after();
+        product(t_dp, da, smem_u32(vbuf + vs * g.ncv * CH), g.ncv);
+        tc_commit(&v_empty[vs]);
+        tc_commit(dp_full);
+        if (last) tc_commit(q_empty);
+        if (++vs == (uint32_t)g.vst) { vs = 0; vph ^= 1; }
+        return true;
+      };
+      for (uint32_t n = 0; !abort_flag; ++n) {
+        int b, h, blk;
+        const int st = next_item(p, g, n, b, h, blk);
+        if (st < 0) break;
+        if (st == 0) continue;
+        const int nt = tiles(blk);
+        // S and dP of the previous item have been read: its last s_empty and
+        // ds_full were waited for below
+        bool ok = mbar_wait(q_full, li & 1, &abort_flag) && mbar_wait(&k_full[t & 1], (t >> 1) & 1, &abort_flag);
+        if (!ok) { fail(); break; }
+        tc_fence_after();
+        product(t_s, qa, smem_u32(kbuf + (t & 1) * g.nch * CH), g.nch);
+        issued = true;
+        tc_commit(s_full);
+        if (!dprobs(nt == 1)) { fail(); break; }
+        for (int i = 0; i < nt; ++i, ++t) {
+          const int s = t & 1, s1 = s ^ 1;
+          if (!mbar_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
+          if (i + 1 < nt) {
+            if (!mbar_wait(&k_full[s1], ((t + 1) >> 1) & 1, &abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            product(t_s, qa, smem_u32(kbuf + s1 * g.nch * CH), g.nch);
+            tc_commit(s_full);
+          }
+          if (!mbar_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
+          if (i == 0 && !mbar_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t kb = smem_u32(kbuf + s * g.nch * CH);
+#pragma unroll
+          for (int kk = 0; kk < BN / 16; ++kk)
+            tc_mma_ts(t_dq, t_ds + kk * 8, make_sdesc(kb + kk * 2048, CH, 1024, 2), idesc_dq, (i > 0 || kk > 0) ? 1u : 0u);
+          tc_commit(&k_empty[s]);
+          tc_commit(ds_empty);
+        }
+        if (!ok) { fail(); break; }
+        tc_commit(acc_full);
+        ++li;
+      }
+      if (issued) { tc_commit(drain); mbar_wait(drain, 0, nullptr); }
+    }
+  } else {
+    // ------------------------------------------------------------ P, dS, epilogue
+    const int q = warp & 3, hf = (warp - 2) >> 2;
+    const int row = q * 32 + lane;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    const uint32_t ts = t_s + lanes + hf * 64, tdp = t_dp + lanes + hf * 64, tds = t_ds + lanes + hf * 32;
+    const float c2 = p.scale * kLog2e;
+    uint32_t t = 0, li = 0;
+    bool bad = false;
+    for (uint32_t n = 0;; ++n) {
+      int b, h, blk;
+      const int st = next_item(p, g, n, b, h, blk);
+      if (st < 0) break;
+      if (st == 0) continue;
+      const int i = blk * BM + row;                      // this thread's query
+      const int nt = tiles(blk);
+      const long long at = ((long long)b * p.H + h) * g.sp + i;   // i < sp: sp is padded to whole blocks
+      const float nl = p.nlse[at], dl = p.delta[at];
+      bool ok = true;
+      for (int it = 0; it < nt; ++it, ++t) {
+        const int j0 = it * BN + hf * 64;
+        const bool full = j0 + 63 < p.S && (!p.causal || j0 + 63 <= blk * BM + q * 32);
+        ok = warp_wait(s_full, t & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        float pv[64];
+        {
+          uint32_t r[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x16_async(ts + c * 16, r[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_empty);
+#pragma unroll
+          for (int x = 0; x < 64; ++x) pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, nl));
+        }
+        ok = warp_wait(dp_full, t & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        {
+          uint32_t r[4][16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x16_async(tdp + c * 16, r[c]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
+#pragma unroll
+          for (int x = 0; x < 64; ++x) pv[x] *= __uint_as_float(r[x / 16][x % 16]) - dl;
+        }
+        if (!full) {
+          const int lim = p.causal ? min(i, p.S - 1) : p.S - 1;   // last key of this row
+#pragma unroll
+          for (int x = 0; x < 64; ++x)
+            if (j0 + x > lim) pv[x] = 0.f;
+        }
+        ok = warp_wait(ds_empty, (t & 1) ^ 1, &abort_flag);      // dQ(t-1) has read dS(t-1)
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
+          tmem_st_32x32b_x8(tds + c * 8, pk);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(ds_full);
+      }
+      if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
+      if (!ok) { if (lane == 0) fail(); break; }
+      tc_fence_after();
+      const int D = p.d_head + p.d_shared;
+      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
+      for (int c = 0; c < 2 * g.nch; ++c) {
+        const int col = hf * 32 * g.nch + c * 16;
+        uint32_t r[16];
+        tmem_ld_32x32b_x16_async(t_dq + lanes + col, r);
+        tmem_ld_wait();
+        reg_fence16(r);
+        const int width = min(D - col, 16);
+        if (i < p.S && width > 0) {
+          float v[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            v[x] = __uint_as_float(r[x]) * p.scale;
+            if (x < width) bad |= !finite_f(v[x]);
+          }
+          store_row16(dq + col, v, width);
+        }
+        __syncwarp();                    // the next load takes the whole warp
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+      ++li;
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------- shared key
+// dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums.
+__global__ void shared_kernel(const __grid_constant__ AttnBwdParams p) {
+  const long long per = (long long)p.S * p.d_shared, total = per * p.B;
+  for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total;
+       x += (long long)gridDim.x * blockDim.x) {
+    const long long b = x / per, r = x - b * per;
+    const float* src = p.part + b * p.H * per + r;
+    float s = 0.f;
+    for (int h = 0; h < p.H; ++h) s += src[h * per];
+    const long long j = r / p.d_shared, c = r - j * p.d_shared;
+    static_cast<__nv_bfloat16*>(p.dksh)[b * p.dkshs[0] + j * p.dkshs[1] + c] = __float2bfloat16_rn(s);
+  }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn get_encode() {
+  static EncodeTiledFn fn = [] {
+    cudaDriverEntryPointQueryResult qr;
+    void* f = nullptr;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &qr) == cudaSuccess &&
+        qr == cudaDriverEntryPointSuccess)
+      return reinterpret_cast<EncodeTiledFn>(f);
+    return static_cast<EncodeTiledFn>(nullptr);
+  }();
+  return fn;
+}
+
+// [B, S, H, width] (or [B, S, width] with H = 0) in boxes of 64 features x `rows`
+bool encode(CUtensorMap* m, const void* base, int width, int H, int S, int B, const long long* st, int rows) {
+  EncodeTiledFn enc = get_encode();
+  if (!enc) return false;
+  const int rank = H ? 4 : 3;
+  cuuint64_t dims[4] = {(cuuint64_t)width, (cuuint64_t)H, (cuuint64_t)S, (cuuint64_t)B};
+  cuuint64_t by[3] = {(cuuint64_t)(H ? st[2] : 0) * 2, (cuuint64_t)st[1] * 2, (cuuint64_t)st[0] * 2};
+  cuuint32_t box[4] = {64, 1, (cuuint32_t)rows, 1}, es[4] = {1, 1, 1, 1};
+  if (!H) {
+    dims[1] = (cuuint64_t)S; dims[2] = (cuuint64_t)B;
+    by[0] = (cuuint64_t)st[1] * 2; by[1] = (cuuint64_t)st[0] * 2;
+    box[1] = (cuuint32_t)rows; box[2] = 1;
+  }
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, by, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int query_tile(const AttnBwdParams& p) { return p.d_head + p.d_shared > 128 ? 96 : 128; }
+
+bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
+  g.nck = (p.d_head + 63) / 64;
+  g.nch = p.d_shared > 0 ? g.nck + (p.d_shared + 63) / 64 : g.nck;
+  g.ncv = (p.d_v + 63) / 64;
+  g.nb = (p.S + BM - 1) / BM;
+  g.nt = (p.S + query_tile(p) - 1) / query_tile(p);
+  g.nunit = p.causal ? (g.nb + 1) / 2 : g.nb;
+  const long long units = (long long)p.B * p.H * g.nunit;
+  if (units >= (1ll << 30)) { snprintf(err, errlen, "%lld work units exceed the kernel's 2^30", units); return false; }
+  g.units = (uint32_t)units;
+  g.sp = attn_bwd_padded_rows(p.S);
+  g.div_nunit = make_fastdiv((uint32_t)g.nunit);
+  g.div_h = make_fastdiv((uint32_t)p.H);
+  const size_t cap = 227 * 1024 - 1024 - 256 - 64;     // alignment, barriers, static
+  g.vst = (size_t)(3 * g.nch + 3 * g.ncv) * CH <= cap ? 2 : 1;
+  return true;
+}
+
+template <int NQ>
+cudaError_t launch_dkv(const AttnBwdParams& p, const Maps& mp, const Geo& g, int grid, cudaStream_t s) {
+  const size_t smem = 1024 + (size_t)(g.nch + g.ncv) * CH + 2 * (size_t)(g.nch + g.ncv) * NQ * 128 + 4 * NQ * 4 + 256;
+  cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  dkv_kernel<NQ><<<grid, kThreads, smem, s>>>(p, mp, g);
+  return cudaGetLastError();
+}
+
+}  // namespace ab
+}  // namespace
+
+// Rows of nlse and delta per (b, h): whole 128-row blocks and whole 96-row
+// tiles both end inside.
+long long attn_bwd_padded_rows(int S) {
+  const long long a = round_up(S, 128), b = round_up(S, 96);
+  return round_up(a > b ? a : b, 32);
+}
+
+bool attn_bwd_supported(const AttnBwdParams& p, char* err, size_t errlen) {
+  const int D = p.d_head + p.d_shared;
+  if (D < 16 || D > 192) { snprintf(err, errlen, "q.k length %d outside [16, 192]", D); return false; }
+  if (p.d_v < 16 || p.d_v > 128) { snprintf(err, errlen, "d_v %d outside [16, 128]", p.d_v); return false; }
+  if (p.d_shared > 0 && (p.d_head % 64) != 0) {
+    snprintf(err, errlen, "with a shared key part d_head must be a multiple of 64 (got %d)", p.d_head);
+    return false;
+  }
+  ab::Geo g;
+  return ab::geometry(p, g, err, errlen);
+}
+
+cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, size_t errlen) {
+  using namespace ab;
+  Geo g;
+  if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
+  const int nq = query_tile(p), D = p.d_head + p.d_shared;
+  Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (128 both)
+  memset(&kv, 0, sizeof kv);
+  bool ok = encode(&kv.q, p.q, D, p.H, p.S, p.B, p.qs, nq) && encode(&kv.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, BM) &&
+            encode(&kv.v, p.v, p.d_v, p.H, p.S, p.B, p.vs, BM) && encode(&kv.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, nq) &&
+            (p.d_shared == 0 || encode(&kv.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, BM));
+  qm = kv;
+  ok = ok && encode(&qm.q, p.q, D, p.H, p.S, p.B, p.qs, BM) && encode(&qm.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, BM);
+  if (!ok) { snprintf(err, errlen, "tensor map encoding failed"); return cudaErrorInvalidValue; }
+  const int sms = sm_count();
+  const long long rows = (long long)p.B * g.sp * p.H;
+  const long long want = cdiv(rows, 16);
+  rows_kernel<<<(int)(want < (long long)sms * 16 ? want : (long long)sms * 16), 256, 0, s>>>(p, g.sp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int grid = (int)(g.units < (uint32_t)sms ? g.units : (uint32_t)sms);
+  e = nq == 96 ? launch_dkv<96>(p, kv, g, grid, s) : launch_dkv<128>(p, kv, g, grid, s);
+  if (e != cudaSuccess) return e;
+  const size_t smem = 1024 + (size_t)(3 * g.nch + (1 + g.vst) * g.ncv) * CH + 256;
+  e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  dq_kernel<<<grid, kThreads, smem, s>>>(p, qm, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || p.d_shared == 0) return e;
+  const long long n = (long long)p.B * p.S * p.d_shared;
+  const long long blocks = cdiv(n, 256);
+  shared_kernel<<<(int)(blocks < (long long)sms * 8 ? blocks : (long long)sms * 8), 256, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace mc

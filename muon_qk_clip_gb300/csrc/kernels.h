@@ -231,6 +231,25 @@ struct AttnFwdParams {
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, cudaStream_t s, char* err, size_t errlen);
 bool attn_fwd_supported(const AttnFwdParams& p, char* err, size_t errlen);
 
+// Attention backward (bf16, tensor cores), recomputing the probabilities.
+struct AttnBwdParams {
+  int B, S, H, d_head, d_shared, d_v;
+  int causal;
+  float scale;
+  const void* q; const void* k; const void* ks; const void* v; const void* o; const void* d_o;
+  const float* lse;        // [B, H, S]
+  void* dq; void* dk; void* dksh; void* dv;
+  long long qs[3], kst[3], kss[2], vs[3], os[3], dos[3];     // element strides (batch, seq, head)
+  long long dqs[3], dks[3], dkshs[2], dvs[3];
+  float* nlse;             // workspace [B, H, sp]: -lse log2(e), -inf past the sequence
+  float* delta;            // workspace [B, H, sp]: do . o
+  float* part;             // workspace [B, H, S, d_shared]: per-head gradients of the shared key
+  int32_t* status;
+};
+long long attn_bwd_padded_rows(int S);                       // sp
+bool attn_bwd_supported(const AttnBwdParams& p, char* err, size_t errlen);
+cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, size_t errlen);
+
 // Bounded-wait self-check (one CTA waits on a phase nothing completes).
 cudaError_t launch_wait_selftest(unsigned long long budget_ns, unsigned long long abort_after_ns,
                                  int32_t* status, unsigned long long* waited_ns, cudaStream_t s);

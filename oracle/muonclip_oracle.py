@@ -248,6 +248,39 @@ def attention_forward(Q: np.ndarray, K: np.ndarray, V: np.ndarray, K_shared=None
     return O, lse, smax
 
 
+def attention_backward(Q, K, V, O, lse, dO, K_shared=None, causal: bool = True, scale=None):
+    """Gradients of attention_forward's output, from its O and log-sum-exp.
+
+    With P = exp(scale Q K^T - lse) (zero above the diagonal when causal) and
+    the row sums delta = sum(dO * O): dV = P^T dO, dS = P * (dO V^T - delta),
+    dQ = scale dS K, dK = scale dS^T Q; the shared key columns of dK summed
+    over the heads.  Shapes as in attention_forward; O and lse are taken as
+    given (they may be rounded).  Returns (dQ, dK, dV, dK_shared or None).
+    """
+    Bsz, S, H, dq = Q.shape
+    dk, dv = K.shape[3], V.shape[3]
+    if scale is None:
+        scale = 1.0 / math.sqrt(dq)
+    dQ, dK, dV = np.zeros((Bsz, S, H, dq)), np.zeros((Bsz, S, H, dk)), np.zeros((Bsz, S, H, dv))
+    dKs = None if K_shared is None else np.zeros((Bsz, S, dq - dk))
+    for b in range(Bsz):
+        for h in range(H):
+            q, v, do = (np.asarray(t[b, :, h], np.float64) for t in (Q, V, dO))
+            k = head_keys(K, K_shared, b, h)
+            P = np.exp(np.minimum(scale * (q @ k.T) - np.asarray(lse[b, h], np.float64)[:, None], 700.0))
+            if causal:
+                P = np.tril(P)
+            delta = np.sum(do * np.asarray(O[b, :, h], np.float64), axis=1)
+            dS = P * (do @ v.T - delta[:, None])
+            dV[b, :, h] = P.T @ do
+            dQ[b, :, h] = scale * (dS @ k)
+            full = scale * (dS.T @ q)
+            dK[b, :, h] = full[:, :dk]
+            if dKs is not None:
+                dKs[b] += full[:, dk:]
+    return dQ, dK, dV, dKs
+
+
 def clip_factors(smax: np.ndarray, tau: float):
     """gamma_h = min(1, tau / S_max^h); a head clips only when S_max^h > tau.
 

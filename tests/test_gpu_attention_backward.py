@@ -1,0 +1,265 @@
+"""GPU parity of qk_attention_backward with the oracle's gradients.
+
+Bounds, from the kernel's arithmetic (u = 2^-8: half a step of bf16, relative;
+w = 2^-24: of fp32), with magnitudes summed over absolute values:
+  * the exponent of p: the fp32 sum of D products, its scaling and the rounded
+    lse give an absolute error of at most
+        a_ij = w (D + 4) scale |q_i|.|k_j| + 4 w |lse_i|;
+    the hardware's base-2 exponential adds 2^-22 relative: p has relative error
+    e = a + 2^-22, and u more as an operand
+  * dv: sum (u + e) p |do| + S w sum p |do|, then u |dv| for the rounding
+  * ds = p (dp - delta): e |ds| + p w (d_v + 4) (|do|.|v| + |do|.|o|), and u |ds|
+    as an operand
+  * dq, dk: the sums of ds's error with |k|, |q|, S w of the sum's magnitude,
+    u of the result; dk_shared sums those of the heads
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from muon_qk_clip_gb300 import abi, build
+from muon_qk_clip_gb300 import binding as mc
+from muon_qk_clip_gb300 import synth
+from tests.gpu_helpers import f64
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+U, W = 2.0 ** -8, 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    abi.load()
+
+
+def inputs(B, S, H, dh, dr, dv, seed, causal=True, head_scale=None):
+    """bf16 q, k, ks, v, do and the oracle's o (bf16) and lse (fp32) for them."""
+    q = synth.normal((B, S, H, dh + dr), 1.0, "bq", seed)
+    if head_scale is not None:
+        q = q * torch.tensor(head_scale)[None, None, :, None]
+    q = q.to(BF16)
+    k = synth.normal((B, S, H, dh), 1.0, "bk", seed).to(BF16)
+    ks = synth.normal((B, S, dr), 1.0, "bks", seed).to(BF16) if dr else None
+    v = synth.normal((B, S, H, dv), 1.0, "bv", seed).to(BF16)
+    do = synth.normal((B, S, H, dv), 0.01, "bdo", seed).to(BF16)
+    o, lse, _ = O.attention_forward(f64(q), f64(k), f64(v), None if ks is None else f64(ks), causal=causal)
+    return q, k, ks, v, do, torch.from_numpy(o).to(BF16), torch.from_numpy(lse).float()
+
+
+def bounds(q, k, ks, v, do, o, lse, causal, scale=None):
+    """(gradients, error bounds) in float64, as the module's docstring derives them."""
+    Q, K, V, dO, Og, L = (f64(t) for t in (q, k, v, do, o, lse))
+    Ks = None if ks is None else f64(ks)
+    B, S, H, D = Q.shape
+    dh, dv = K.shape[3], V.shape[3]
+    scale = 1.0 / np.sqrt(D) if scale is None else scale
+    ref = O.attention_backward(Q, K, V, Og, L, dO, Ks, causal=causal, scale=scale)
+    eq, ek, ev = (np.zeros_like(r) for r in ref[:3])
+    es = None if Ks is None else np.zeros_like(ref[3])
+    for b in range(B):
+        for h in range(H):
+            qq, vv, dd, oo = Q[b, :, h], V[b, :, h], dO[b, :, h], Og[b, :, h]
+            kk = O.head_keys(K, Ks, b, h)
+            p = np.exp(np.minimum(scale * qq @ kk.T - L[b, h][:, None], 700.0))
+            if causal:
+                p = np.tril(p)
+            a = W * (D + 4) * scale * (np.abs(qq) @ np.abs(kk).T) + 4 * W * np.abs(L[b, h])[:, None]
+            e = a + 2.0 ** -22
+            ds = np.abs(p * (dd @ vv.T - np.sum(dd * oo, 1)[:, None]))
+            mags = np.abs(dd) @ np.abs(vv).T + np.sum(np.abs(dd) * np.abs(oo), 1)[:, None]
+            err = (e + U) * ds + p * (1 + e + U) * W * (dv + 4) * mags
+            pd = p.T @ np.abs(dd)
+            ev[b, :, h] = ((U + e) * p).T @ np.abs(dd) + S * W * pd
+            eq[b, :, h] = scale * ((err + S * W * ds) @ np.abs(kk))
+            full = scale * ((err + S * W * ds).T @ np.abs(qq))
+            ek[b, :, h] = full[:, :dh]
+            if es is not None:
+                es[b] += full[:, dh:]
+    errs = [eq, ek, ev, es]
+    return ref, [None if r is None else x * 1.01 + U * np.abs(r) + 1e-30 for r, x in zip(ref, errs)]
+
+
+def check(got, ref, tol):
+    for name, g, r, t in zip(("dq", "dk", "dv", "dk_shared"), got, ref, tol):
+        if r is None:
+            assert g is None
+            continue
+        err = np.abs(f64(g) - r)
+        assert np.all(err <= t), (f"{name}: {int(np.sum(~(err <= t)))} of {err.size} outside, "
+                                  f"worst excess {np.nanmax(err - t):.3g}, max err {np.nanmax(err):.3g}")
+
+
+def dev(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+CASES = [
+    (1, 1, 1, 64, 0, 64, True),           # one token
+    (2, 3, 2, 16, 0, 16, True),           # the narrowest widths
+    (1, 128, 2, 128, 0, 128, True),       # exactly one block
+    (1, 129, 2, 128, 0, 128, True),       # one row into the second
+    (2, 300, 3, 128, 0, 128, True),       # ragged last block
+    (1, 384, 2, 64, 0, 128, False),       # unmasked, whole blocks, values wider than keys
+    (3, 333, 2, 80, 0, 48, False),        # widths off the 64-wide chunks
+    (1, 200, 2, 24, 0, 72, True),
+    (1, 290, 2, 192, 0, 64, True),        # q.k length 192 without a shared part: 96-query tiles
+    (1, 257, 2, 128, 64, 128, True),      # MLA
+    (2, 96, 3, 128, 64, 128, True),       # MLA, exactly one query tile
+    (1, 193, 3, 128, 64, 128, False),     # MLA, no mask
+    (1, 150, 5, 64, 40, 96, True),        # MLA, one chunk each, odd rotary width
+    (1, 700, 1, 128, 8, 16, True),        # several tiles of both sizes
+]
+
+
+@pytest.mark.parametrize("B,S,H,dh,dr,dv,causal", CASES)
+def test_attention_backward_parity(B, S, H, dh, dr, dv, causal):
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, dv, 70 + S, causal)
+    ref, tol = bounds(q, k, ks, v, do, o, lse, causal)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dq_, dk_, dks_, dv_, ddo, do_, dl = dev(q, k, ks, v, do, o, lse)
+    got = mc.qk_attention_backward(dq_, dk_, dv_, do_, dl, ddo, k_shared=dks_, causal=causal, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(got, ref, tol)
+    again = mc.qk_attention_backward(dq_, dk_, dv_, do_, dl, ddo, k_shared=dks_, causal=causal)
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, again))     # no atomics
+
+
+def test_attention_backward_heavy_logits():
+    """Heads with logits far over tau: nearly one-hot rows, where ds is a small
+    difference of large terms, and an explicit scale."""
+    q, k, ks, v, do, o, lse = inputs(1, 400, 3, 128, 0, 128, 91, True, head_scale=[1.0, 12.0, 25.0])
+    ref, tol = bounds(q, k, ks, v, do, o, lse, True)
+    a = dev(q, k, v, o, lse, do)
+    check(mc.qk_attention_backward(*a), ref, tol)
+    q, k, ks, v, do, _, _ = inputs(1, 140, 2, 64, 0, 64, 92)
+    out, lse, _ = O.attention_forward(f64(q), f64(k), f64(v), scale=0.31)
+    o, lse = torch.from_numpy(out).to(BF16), torch.from_numpy(lse).float()
+    ref, tol = bounds(q, k, ks, v, do, o, lse, True, scale=0.31)
+    check(mc.qk_attention_backward(*dev(q, k, v, o, lse, do), scale=0.31), ref, tol)
+
+
+def test_attention_backward_strided_outputs_and_inputs():
+    """k and v interleaved in one buffer, as the MLA projection gives them, their
+    gradients in another; q and its gradient head-major; nothing outside the
+    outputs is touched."""
+    B, S, H, dh, dr, dv = 2, 200, 3, 64, 16, 48
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, dv, 93)
+    ref, tol = bounds(q, k, ks, v, do, o, lse, True)
+    kv = torch.cat([k, v], -1).cuda()
+    dkv = torch.full((B, S + 2, H, dh + dv + 8), 7.0, dtype=BF16, device="cuda")
+    qh = q.permute(0, 2, 1, 3).contiguous().cuda().permute(0, 2, 1, 3)
+    dq = torch.full((B, H, S + 1, dh + dr), 7.0, dtype=BF16, device="cuda").permute(0, 2, 1, 3)
+    got = mc.qk_attention_backward(qh, kv[..., :dh], kv[..., dh:], o.cuda(), lse.cuda(), do.cuda(), k_shared=ks.cuda(),
+                                   dq=dq[:, :S], dk=dkv[:, :S, :, :dh], dv=dkv[:, :S, :, dh:dh + dv])
+    torch.cuda.synchronize()
+    check(got, ref, tol)
+    assert torch.all(dkv[:, S:] == 7.0) and torch.all(dkv[..., dh + dv:] == 7.0) and torch.all(dq[:, S:] == 7.0)
+
+
+def test_attention_backward_of_broadcast_keys():
+    """One key/value head for every query head (stride 0): the gradients come per
+    query head, for the caller to sum."""
+    B, S, H, d = 1, 150, 4, 64
+    q, k, _, v, do, _, _ = inputs(B, S, H, d, 0, d, 94)
+    k, v = k[:, :, :1].expand(B, S, H, d), v[:, :, :1].expand(B, S, H, d)
+    out, lse, _ = O.attention_forward(f64(q), f64(k), f64(v))
+    o, lse = torch.from_numpy(out).to(BF16), torch.from_numpy(lse).float()
+    ref, tol = bounds(q, k, None, v, do, o, lse, True)
+    kd, vd = k[:, :, :1].cuda().expand(B, S, H, d), v[:, :, :1].cuda().expand(B, S, H, d)
+    check(mc.qk_attention_backward(q.cuda(), kd, vd, o.cuda(), lse.cuda(), do.cuda()), ref, tol)
+
+
+def test_attention_backward_differences():
+    """Against central differences of the oracle's forward along random
+    directions: the sum over a whole gradient averages the operand roundings, so
+    4 u relative to the sum of magnitudes / sqrt(n) holds with room."""
+    q, k, ks, v, do, o, lse = inputs(1, 70, 2, 64, 16, 32, 95)
+    got = mc.qk_attention_backward(*dev(q, k, v, o, lse, do), k_shared=ks.cuda())
+    x = [f64(t) for t in (q, k, v, ks)]
+    rng = np.random.default_rng(0)
+    for n in range(4):
+        step = rng.standard_normal(x[n].shape)
+        val = []
+        for eps in (1e-4, -1e-4):
+            y = list(x)
+            y[n] = x[n] + eps * step
+            val.append(float(np.sum(O.attention_forward(y[0], y[1], y[2], y[3])[0] * f64(do))))
+        diff = (val[0] - val[1]) / 2e-4
+        g = f64(got[n])
+        assert abs(np.sum(g * step) - diff) <= 4 * U * np.sqrt(np.sum((g * step) ** 2)) + U * abs(diff)
+
+
+def test_attention_backward_after_the_forward():
+    """The forward's own o and lse feed the backward; a second stream, a given
+    workspace, and rows of the batch done alone give the same bits."""
+    q, k, ks, v, do, _, _ = inputs(3, 260, 2, 128, 64, 128, 96)
+    qd, kd, ksd, vd, dod = dev(q, k, ks, v, do)
+    out, lse, _ = mc.qk_attention_forward(qd, kd, vd, ksd, lse=True)
+    got = mc.qk_attention_backward(qd, kd, vd, out, lse, dod, k_shared=ksd)
+    ref, tol = bounds(q, k, ks, v, do, out.cpu(), lse.cpu(), True)
+    check(got, ref, tol)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    ws = torch.empty(mc.attention_backward_workspace_size(qd, kd, ksd), dtype=torch.uint8, device="cuda")
+    ws.fill_(0xFF)                        # NaN: every value that is read was written in the call
+    side.wait_stream(torch.cuda.current_stream())
+    one = mc.qk_attention_backward(qd, kd, vd, out, lse, dod, k_shared=ksd, workspace=ws, stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, one))
+    for b in range(3):
+        s = slice(b, b + 1)
+        alone = mc.qk_attention_backward(qd[s], kd[s], vd[s], out[s], lse[s], dod[s], k_shared=ksd[s])
+        assert all(torch.equal(x[s], y) for x, y in zip(got, alone))
+
+
+def test_attention_backward_in_cuda_graph():
+    q, k, ks, v, do, o, lse = inputs(2, 140, 2, 128, 0, 128, 97)
+    a = dev(q, k, v, o, lse, do)
+    eager = mc.qk_attention_backward(*a)
+    torch.cuda.synchronize()
+    outs = [torch.full_like(g, 3.0) for g in eager[:3]]
+    ws = torch.empty(mc.attention_backward_workspace_size(a[0], a[1]), dtype=torch.uint8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mc.qk_attention_backward(*a, dq=outs[0], dk=outs[1], dv=outs[2], workspace=ws)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(eager[:3], outs))
+    a[5].mul_(2.0)                        # new inputs in the same buffers
+    graph.replay()
+    fresh = mc.qk_attention_backward(*a)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(fresh[:3], outs))
+
+
+def test_attention_backward_flags_nonfinite():
+    q, k, ks, v, do, o, lse = inputs(1, 64, 2, 64, 0, 64, 98)
+    do[0, 5, 1, 3] = float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_backward(*dev(q, k, v, o, lse, do), status=st)
+    torch.cuda.synchronize()
+    assert st.item() & abi.MC_STATUS_NONFINITE_UPDATE
+    assert all(torch.isfinite(g[:, :, 0]).all() for g in got[:3])       # the other head
+
+
+def test_attention_backward_dense_block_full_size():
+    """The dense_block layer's launch (B 4, S 4096, H 16, d 128): two heads of one
+    batch row against the oracle, every row of them."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    mk = lambda std=1.0: (torch.randn(4, 4096, 16, 128, generator=g, device="cuda") * std).to(BF16)  # noqa: E731
+    q, k, v, do = mk(), mk(), mk(), mk(0.01)
+    q[:, :, 2] *= 8
+    out, lse, _ = mc.qk_attention_forward(q, k, v, lse=True)
+    got = mc.qk_attention_backward(q, k, v, out, lse, do)
+    torch.cuda.synchronize()
+    for b, h in ((0, 2), (3, 15)):
+        s = (slice(b, b + 1), slice(None), slice(h, h + 1))
+        sub = [t[s].cpu() for t in (q, k, v, do, out)]
+        ref, tol = bounds(sub[0], sub[1], None, sub[2], sub[3], sub[4], lse[b:b + 1, h:h + 1].cpu(), True)
+        check([x[s] for x in got[:3]] + [None], ref, tol)
