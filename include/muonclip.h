@@ -58,7 +58,8 @@ typedef enum {
 #define MC_STATUS_NONFINITE_SMAX   4  /* NaN/Inf S_max given to the clip     */
 #define MC_STATUS_TIMEOUT          8  /* a bounded device wait gave up       */
 
-typedef enum { MC_F32 = 0, MC_BF16 = 1 } mc_dtype;
+/* MC_F8E4M3: an output type of mc_add_rms_norm only. */
+typedef enum { MC_F32 = 0, MC_BF16 = 1, MC_F8E4M3 = 2 } mc_dtype;
 
 /* Arithmetic of the Newton-Schulz products.
  *   MC_NS_SPLIT_BF16: tcgen05 tensor cores on 16-bit (hi, lo) planes, fp32
@@ -405,6 +406,57 @@ mc_status mc_rms_norm(const void* x, int64_t ldx, void* y, int64_t ldy, int64_t 
  * on `stream`. */
 mc_status mc_rope(void* x, int32_t B, int32_t S, int32_t nh, int32_t d, int64_t sb, int64_t ss, int64_t sh,
                   int32_t dtype, double theta, mc_stream_t stream);
+
+/* Gradient of mc_rope: (dy0, dy1) of a pair at position s becomes
+ * (dy0 cos + dy1 sin, dy1 cos - dy0 sin), angle s * theta^(-2k/d).  dy and dx
+ * [b, s, h, 0..d) with strides (yb, ys, yh) and (xb, xs, xh) in elements, unit
+ * stride along d; dx == dy with equal strides rotates in place, any other
+ * overlap is refused, as is a dx with shared addresses.  Types, d and theta as
+ * in mc_rope; B or S of 0 returns at once.  Asynchronous on `stream`. */
+mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, void* dx, int64_t xb, int64_t xs,
+                           int64_t xh, int32_t B, int32_t S, int32_t nh, int32_t d, int32_t dtype, double theta,
+                           mc_stream_t stream);
+
+/* ---- Norms of a block, with the residual stream's addition and their gradient ---- */
+
+/* Per row of `cols` values, fp32 arithmetic:
+ *   h = x + residual, the fp32 sum rounded to dtype and stored (h = x without:
+ *       pass residual and h both or neither);
+ *   rstd = 1 / sqrt(mean(h^2) + eps) (stored in rstd [rows] unless NULL);
+ *   y = h rstd weight (weight [cols] of dtype; NULL: ones).
+ * dtype (of x, residual, weight and h): MC_BF16 or MC_F32.  y_dtype: dtype, or
+ * MC_F8E4M3: then every row and 128 columns (the last tile of a row may be
+ * shorter) have one scale, scales[row * lds + col / 128] =
+ * max(max|y| / 448, 2^-100), and y holds e4m3(y / scale), rounded to nearest
+ * even; scales is NULL otherwise.  Pitches in elements, at least the row's
+ * length.  h may be x or residual, y (of dtype) may be x or residual, in place
+ * with the same pitch (not both on one); any other overlap with an output is
+ * refused.  Pointers are aligned to their type; rows of 16-byte aligned
+ * operands run at full width.  rows of 0 returns at once.  A NaN/Inf in a row
+ * reaches that row's outputs only.  Asynchronous on `stream`. */
+mc_status mc_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                          void* h, int64_t ldh, void* y, int64_t ldy, float* scales, int64_t lds, float* rstd,
+                          int64_t rows, int32_t cols, int32_t dtype, int32_t y_dtype, float eps,
+                          mc_stream_t stream);
+
+/* Bytes of workspace that mc_rms_norm_backward needs for a dweight of cols. */
+mc_status mc_rms_norm_backward_workspace_size(int32_t cols, size_t* bytes);
+
+/* Gradient of y = h rstd weight (mc_add_rms_norm before any 8-bit rounding;
+ * mc_rms_norm with weight = NULL), given dy, h and rstd [rows]:
+ *   xhat = h rstd, g = weight dy,
+ *   dx = rstd (g - xhat mean(g xhat)) + dres, rounded to dtype once;
+ *   dweight[c] = sum over the rows of dy xhat (fp32, written; NULL: not wanted).
+ * dres (dtype, or NULL) is the gradient that reaches h past the norm, along the
+ * residual stream.  dx is the gradient of x and of the residual alike.  dx may
+ * be dy, h or dres, in place with the same pitch; other overlaps are refused.
+ * Sums run in a fixed order.  workspace: device, 16-byte aligned, only with a
+ * dweight, for this call alone while it runs.  rows of 0 zeroes dweight.
+ * Asynchronous on `stream`. */
+mc_status mc_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const float* rstd,
+                               const void* weight, const void* dres, int64_t ldr, void* dx, int64_t lddx,
+                               float* dweight, int64_t rows, int32_t cols, int32_t dtype, void* workspace,
+                               size_t workspace_bytes, mc_stream_t stream);
 
 /* Diagnostic: exercises the bounded device wait that every tcgen05 kernel of
  * the library uses for its mbarrier phases.  One CTA waits on a phase that

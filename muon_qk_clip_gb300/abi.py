@@ -24,7 +24,7 @@ MC_STATUS_TIMEOUT = 8
 
 MC_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
-MC_F32, MC_BF16 = 0, 1
+MC_F32, MC_BF16, MC_F8E4M3 = 0, 1, 2
 MC_NS_AUTO, MC_NS_SPLIT_BF16, MC_NS_BF16, MC_NS_FP32 = 0, 1, 2, 3
 MC_SCALE_RMS, MC_SCALE_SPECTRAL = 0, 1
 MC_CLIP_PER_HEAD, MC_CLIP_TOTAL = 0, 1
@@ -106,6 +106,15 @@ SIGNATURES = {
                               c_void_p]),
     "mc_rope": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_int32, c_int64, c_int64, c_int64, c_int32,
                           c_double, c_void_p]),
+    "mc_rope_backward": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                   c_int32, c_int32, c_int32, c_int32, c_int32, c_double, c_void_p]),
+    "mc_add_rms_norm": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int64, c_void_p,
+                                  c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32, c_int32,
+                                  c_float, c_void_p]),
+    "mc_rms_norm_backward_workspace_size": (c_int32, [c_int32, POINTER(c_size_t)]),
+    "mc_rms_norm_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                                       c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32,
+                                       c_void_p, c_size_t, c_void_p]),
     "mc_selftest_bounded_wait": (c_int32, [c_uint64, c_uint64, c_void_p, c_void_p, c_void_p]),
     "mc_profiler_enable": (None, [c_int32]),
     "mc_profiler_read": (c_int32, [POINTER(McKernelTime), c_int32, c_int32]),

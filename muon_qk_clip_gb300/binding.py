@@ -385,6 +385,124 @@ def rope_(x, theta: float = 10000.0, stream=None):
     return x
 
 
+def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
+    """Gradient of rope_: the transposed rotation of dy [B, S, d] or
+    [B, S, heads, d] (unit stride along d), positions 0..S-1.  Returns `out`, a
+    new tensor unless given; out=dy rotates in place."""
+    dev = _same_device(dy=dy, out=out)
+    if out is None:
+        out = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
+    if dy.dim() not in (3, 4) or dy.dtype not in _DT or dy.stride(-1) != 1:
+        raise ValueError("dy: [B, S, d] or [B, S, heads, d] with unit stride along d")
+    if out.shape != dy.shape or out.dtype != dy.dtype or out.stride(-1) != 1:
+        raise ValueError("out must have dy's shape and type and unit stride along d")
+    B, S, d = dy.shape[0], dy.shape[1], dy.shape[-1]
+    nh, yh, xh = (dy.shape[2], dy.stride(2), out.stride(2)) if dy.dim() == 4 else (1, 0, 0)
+    with torch.cuda.device(dev):
+        check(abi.load().mc_rope_backward(_ptr(dy), dy.stride(0), dy.stride(1), yh, _ptr(out), out.stride(0),
+                                          out.stride(1), xh, B, S, nh, d, _DT[dy.dtype], float(theta),
+                                          _stream(stream)), "mc_rope_backward")
+    return out
+
+
+def _matrix(t, name, shape, dtype):
+    """Row pitch of a given 2-D operand: `shape`, `dtype`, unit column stride."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name}: expected unit column stride and rows that do not overlap")
+    return max(t.stride(0), t.shape[1])
+
+
+def _vector(t, name, n, dtype):
+    if t is not None and (tuple(t.shape) != (n,) or t.dtype != dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype}")
+
+
+def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
+                 scales=None, rstd=None, stream=None):
+    """h = x + residual (h = x without one), y = h / sqrt(mean(h^2) + eps) * weight
+    per row of x [rows, cols] (bf16 or fp32; residual of the same shape, weight
+    [cols], both of x's type).  out_dtype=torch.float8_e4m3fn stores y as e4m3
+    with one fp32 scale per row and 128 columns.  Returns (y, scales or None, h,
+    rstd [rows] f32); h is x itself without a residual.  Outputs are allocated
+    unless given; h may be x or residual (in place)."""
+    if x.dim() != 2 or x.dtype not in _DT:
+        raise ValueError("x: expected a 2-D bfloat16 or float32 tensor")
+    dev = _same_device(x=x, residual=residual, weight=weight, h=h, out=out, scales=scales, rstd=rstd)
+    rows, cols = x.shape
+    f8 = out_dtype == torch.float8_e4m3fn
+    if out_dtype not in (None, x.dtype, torch.float8_e4m3fn):
+        raise ValueError(f"out_dtype: {x.dtype} or torch.float8_e4m3fn")
+    ldx = _matrix(x, "x", (rows, cols), x.dtype)
+    _vector(weight, "weight", cols, x.dtype)
+    if residual is None:
+        if h is not None:
+            raise ValueError("h without residual: h is x itself")
+        ldr = ldh = 0
+    else:
+        ldr = _matrix(residual, "residual", (rows, cols), x.dtype)
+        if h is None:
+            h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
+        ldh = _matrix(h, "h", (rows, cols), x.dtype)
+    y_dtype = out_dtype or x.dtype
+    if out is None:
+        out = torch.empty((rows, cols), dtype=y_dtype, device=dev)
+    ldy = _matrix(out, "out", (rows, cols), y_dtype)
+    lds = 0
+    if f8:
+        tiles = -(-cols // 128)
+        if scales is None:
+            scales = torch.empty((rows, tiles), dtype=torch.float32, device=dev)
+        lds = _matrix(scales, "scales", (rows, tiles), torch.float32)
+    elif scales is not None:
+        raise ValueError("scales go with out_dtype=torch.float8_e4m3fn")
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+    _vector(rstd, "rstd", rows, torch.float32)
+    with torch.cuda.device(dev):
+        check(abi.load().mc_add_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(h), ldh, _ptr(out),
+                                         ldy, _ptr(scales), lds, _ptr(rstd), rows, cols, _DT[x.dtype],
+                                         abi.MC_F8E4M3 if f8 else _DT[x.dtype], float(eps), _stream(stream)),
+              "mc_add_rms_norm")
+    return out, scales, (x if residual is None else h), rstd
+
+
+def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None, workspace=None, stream=None):
+    """Gradient of y = h * rstd * weight given dy [rows, cols], h and rstd as
+    add_rms_norm returned them: dx (of the norm's input and of the residual
+    alike; plus dres, the gradient that reaches h past the norm) and dweight
+    [cols] f32.  Returns (dx, dweight); dweight is None without a weight unless
+    one is given to write.  dx may be dy, h or dres (in place)."""
+    if dy.dim() != 2 or dy.dtype not in _DT:
+        raise ValueError("dy: expected a 2-D bfloat16 or float32 tensor")
+    dev = _same_device(dy=dy, h=h, rstd=rstd, weight=weight, dres=dres, dx=dx, dweight=dweight, workspace=workspace)
+    rows, cols = dy.shape
+    lddy = _matrix(dy, "dy", (rows, cols), dy.dtype)
+    ldh = _matrix(h, "h", (rows, cols), dy.dtype)
+    ldr = 0 if dres is None else _matrix(dres, "dres", (rows, cols), dy.dtype)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
+    lddx = _matrix(dx, "dx", (rows, cols), dy.dtype)
+    _vector(rstd, "rstd", rows, torch.float32)
+    _vector(weight, "weight", cols, dy.dtype)
+    if dweight is None and weight is not None:
+        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
+    _vector(dweight, "dweight", cols, torch.float32)
+    lib = abi.load()
+    with torch.cuda.device(dev):
+        if dweight is not None and workspace is None:
+            n = ctypes.c_size_t(0)
+            check(lib.mc_rms_norm_backward_workspace_size(cols, ctypes.byref(n)),
+                  "mc_rms_norm_backward_workspace_size")
+            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
+        check(lib.mc_rms_norm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(rstd), _ptr(weight), _ptr(dres), ldr,
+                                       _ptr(dx), lddx, _ptr(dweight), rows, cols, _DT[dy.dtype], _ptr(workspace),
+                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                       _stream(stream)), "mc_rms_norm_backward")
+    return dx, dweight
+
+
 def profiler_enable(on: bool = True):
     """Bracket every library launch with CUDA events (per kernel class)."""
     abi.load().mc_profiler_enable(1 if on else 0)

@@ -987,23 +987,14 @@ mc_status check_attn_tensor(const char* name, const void* ptr, const int64_t* st
                             int64_t width, bool output, long long* out) {
   if (!ptr) return fail(MC_ERR_INVALID_ARG, "attention backward: %s is null", name);
   if (!aligned16(ptr)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s must be 16-byte aligned", name);
-  int64_t s[3], e[3];
-  int m = 0;
   for (int i = 0; i < n; ++i) {
     out[i] = extent[i] == 1 ? round_up(width, 8) : st[i];
     if (out[i] < 0) return fail(MC_ERR_INVALID_ARG, "attention backward: %s has a negative stride", name);
     if (out[i] % 8) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides must be multiples of 8 elements", name);
     if (out[i] >= (1ll << 38)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides are too large", name);
-    if (extent[i] > 1) { s[m] = st[i]; e[m] = extent[i]; ++m; }
   }
-  if (!output) return MC_OK;
-  for (int i = 1; i < m; ++i)            // by ascending stride
-    for (int j = i; j > 0 && s[j] < s[j - 1]; --j) { std::swap(s[j], s[j - 1]); std::swap(e[j], e[j - 1]); }
-  int64_t span = width;                  // elements that the inner axes reach over
-  for (int i = 0; i < m; ++i) {
-    if (s[i] < span) return fail(MC_ERR_INVALID_ARG, "attention backward: elements of %s share addresses", name);
-    span += s[i] * (e[i] - 1);
-  }
+  if (output && !distinct_addresses(st, extent, n, width))
+    return fail(MC_ERR_INVALID_ARG, "attention backward: elements of %s share addresses", name);
   return MC_OK;
 }
 

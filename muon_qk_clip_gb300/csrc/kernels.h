@@ -12,6 +12,27 @@ namespace mc {
 inline constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline constexpr int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
+// Whether every element of a strided array (n <= 3 axes, `width` contiguous
+// elements under them) has an address of its own.  Axes of one element may have
+// any stride.
+inline bool distinct_addresses(const int64_t* stride, const int64_t* extent, int n, int64_t width) {
+  int64_t s[3], e[3];
+  int m = 0;
+  for (int i = 0; i < n; ++i) {
+    if (extent[i] <= 1) continue;
+    int j = m++;                         // by ascending stride
+    for (; j > 0 && s[j - 1] > stride[i]; --j) { s[j] = s[j - 1]; e[j] = e[j - 1]; }
+    s[j] = stride[i];
+    e[j] = extent[i];
+  }
+  int64_t span = width;                  // elements that the inner axes reach over
+  for (int i = 0; i < m; ++i) {
+    if (s[i] < span) return false;
+    span += s[i] * (e[i] - 1);
+  }
+  return true;
+}
+
 // 16-bit formats of a tensor-core Newton-Schulz launch: operands (A, B, C)
 // and stored output D.
 enum GemmFmt : int {

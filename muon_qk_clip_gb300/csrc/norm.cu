@@ -1,0 +1,616 @@
+// RMS norm with the residual's addition, and the norm's gradient, per row of
+// `cols` values (the norms between an attention block's products; the MLA
+// latents' is the weightless one):
+//
+//   mc_add_rms_norm       h = rn(x + residual), rstd = 1 / sqrt(mean(h^2) + eps),
+//                         y = h rstd w, in the inputs' type or as e4m3 with one
+//                         fp32 scale per row and 128 columns:
+//                         scale = max(max|y| / 448, 2^-100), q = rn(y / scale)
+//   mc_rms_norm_backward  xhat = h rstd, g = w dy,
+//                         dx = rstd (g - xhat mean(g xhat)) + dres,
+//                         dw = sum over the rows of dy xhat
+//
+// Both stream each value once: a row stays in the registers of the warps that
+// share it, between the sum over the row and its use.  A warp takes units of 32
+// lanes x 16 bytes (or, where a pointer, pitch or width is not a multiple of 16
+// bytes, of 128 single values); unit u of a row belongs to warp u mod WPR, each
+// warp holds at most NU units.  Rows too wide for that (NU = 0) are read twice.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "../../include/muonclip.h"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace mc {
+namespace {
+namespace nm {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTile = 128;               // columns per e4m3 scale
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleMin = 7.888609052210118e-31f;   // 2^-100: 1 / scale stays finite
+constexpr int kBackGrid = 304;           // blocks of the backward (two per SM); its workspace's rows
+
+// A lane's share of a unit: E values of the row from column col(unit, lane, 0).
+template <typename T, bool VEC>
+struct Unit;
+template <>
+struct Unit<__nv_bfloat16, true> {
+  static constexpr int E = 8, kCols = 256;
+  uint4 r;
+  __device__ static int col(int unit, int lane, int) { return unit * kCols + lane * E; }
+  __device__ void load(const __nv_bfloat16* p, int unit, int lane, int cols) {
+    const int c = col(unit, lane, 0);
+    r = c < cols ? *reinterpret_cast<const uint4*>(p + c) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ void get(float (&v)[E]) const {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ static void store(__nv_bfloat16* p, int unit, int lane, int cols, const float (&v)[E]) {
+    const int c = col(unit, lane, 0);
+    if (c >= cols) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+template <>
+struct Unit<float, true> {
+  static constexpr int E = 4, kCols = 128;
+  float4 r;
+  __device__ static int col(int unit, int lane, int) { return unit * kCols + lane * E; }
+  __device__ void load(const float* p, int unit, int lane, int cols) {
+    const int c = col(unit, lane, 0);
+    r = c < cols ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ void get(float (&v)[E]) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
+  __device__ static void store(float* p, int unit, int lane, int cols, const float (&v)[E]) {
+    const int c = col(unit, lane, 0);
+    if (c < cols) *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+  }
+};
+template <typename T>
+struct Unit<T, false> {
+  static constexpr int E = 4, kCols = 128;
+  T r[E];
+  __device__ static int col(int unit, int lane, int e) { return unit * kCols + e * 32 + lane; }
+  __device__ void load(const T* p, int unit, int lane, int cols) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = col(unit, lane, e);
+      r[e] = c < cols ? p[c] : T(0.f);
+    }
+  }
+  __device__ void get(float (&v)[E]) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = static_cast<float>(r[e]);
+  }
+  __device__ static void store(T* p, int unit, int lane, int cols, const float (&v)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int c = col(unit, lane, e);
+      if (c < cols) p[c] = T(v[e]);
+    }
+  }
+};
+
+template <typename T>
+__device__ inline float rounded(float v);
+template <>
+__device__ inline float rounded<float>(float v) { return v; }
+template <>
+__device__ inline float rounded<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+
+__device__ inline float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// e4m3 of a unit's values and the tiles' scales.  A 16-byte bf16 unit covers
+// two tiles (a half-warp each), the others one.
+template <typename T, bool VEC>
+__device__ inline void store_e4m3(uint8_t* y, float* scales, int unit, int lane, int cols,
+                                  const float (&v)[Unit<T, VEC>::E]) {
+  using U = Unit<T, VEC>;
+  constexpr int lanes = 32 * kTile / U::kCols;
+  float top = 0.f;
+#pragma unroll
+  for (int e = 0; e < U::E; ++e) top = max_nan(top, fabsf(v[e]));
+#pragma unroll
+  for (int o = lanes / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float scale = max_nan(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
+  const int tile0 = unit * U::kCols + (lane / lanes) * kTile;
+  if (lane % lanes == 0 && tile0 < cols) scales[tile0 / kTile] = scale;
+  uint32_t w[(U::E + 3) / 4] = {};
+#pragma unroll
+  for (int e = 0; e < U::E; e += 2) {
+    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[e] * inv, v[e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    w[e / 4] |= two << (8 * (e % 4));
+  }
+  if (VEC) {
+    const int c = U::col(unit, lane, 0);
+    if (c < cols) {
+      if (U::E == 8) *reinterpret_cast<uint2*>(y + c) = make_uint2(w[0], w[(U::E + 3) / 4 - 1]);
+      else *reinterpret_cast<uint32_t*>(y + c) = w[0];
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < U::E; ++e) {
+      const int c = U::col(unit, lane, e);
+      if (c < cols) y[c] = (uint8_t)(w[0] >> (8 * e));
+    }
+  }
+}
+
+__device__ inline float warp_sum(float s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+struct AddParams {
+  const void* x; const void* r; const void* w;
+  void* h; void* y; float* scales; float* rstd;
+  long long ldx, ldr, ldh, ldy, lds, rows;
+  int cols, wpr, f8;
+  float eps;
+};
+
+// The sum over the row's warps of one value per warp, in a fixed order.  red:
+// one slot per warp; the block's threads all call it.
+__device__ inline float row_sum(float s, float* red, int wpr) {
+  s = warp_sum(s);
+  if (wpr == 1) return s;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = s;
+  __syncthreads();
+  const int first = warp / wpr * wpr;
+  float t = 0.f;
+  for (int i = 0; i < wpr; ++i) t += red[first + i];
+  return t;
+}
+
+template <typename T, bool VEC, int NU>
+__global__ void __launch_bounds__(kThreads) add_norm_kernel(const AddParams p) {
+  using U = Unit<T, VEC>;
+  constexpr int N = NU ? NU : 1;
+  __shared__ float red[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w0 = warp % p.wpr;
+  const long long row = (long long)blockIdx.x * (kWarps / p.wpr) + warp / p.wpr;
+  const bool live = row < p.rows;
+  const long long at = live ? row : 0;
+  const T* x = static_cast<const T*>(p.x) + at * p.ldx;
+  const T* r = p.r ? static_cast<const T*>(p.r) + at * p.ldr : nullptr;
+  T* h = p.r ? static_cast<T*>(p.h) + at * p.ldh : nullptr;
+  const T* w = static_cast<const T*>(p.w);
+  const int cols = live ? p.cols : 0;    // rows past the end read and write nothing
+  const int units = (p.cols + U::kCols - 1) / U::kCols;
+  auto add = [&](int unit, const U& a, const U& b, float (&v)[U::E]) {
+    a.get(v);
+    if (!r) return;
+    float s[U::E];
+    b.get(s);
+#pragma unroll
+    for (int e = 0; e < U::E; ++e) v[e] = rounded<T>(v[e] + s[e]);
+    U::store(h, unit, lane, cols, v);
+  };
+  auto finish = [&](int unit, float rs, float (&v)[U::E]) {
+    if (w) {
+      U uw;
+      uw.load(w, unit, lane, p.cols);
+      float f[U::E];
+      uw.get(f);
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) v[e] = v[e] * rs * f[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) v[e] *= rs;
+    }
+    if (p.f8) store_e4m3<T, VEC>(static_cast<uint8_t*>(p.y) + at * p.ldy, p.scales + at * p.lds, unit, lane, cols, v);
+    else U::store(static_cast<T*>(p.y) + at * p.ldy, unit, lane, cols, v);
+  };
+  float s = 0.f;
+  U ux[N], ur[N];
+  float v[N][U::E];
+  if (NU) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) ux[k].load(x, k * p.wpr + w0, lane, cols);
+    if (r) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) ur[k].load(r, k * p.wpr + w0, lane, cols);
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      add(k * p.wpr + w0, ux[k], ur[k], v[k]);
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) s = fmaf(v[k][e], v[k][e], s);
+    }
+  } else {
+    for (int u = w0; u < units; u += p.wpr) {
+      ux[0].load(x, u, lane, cols);
+      if (r) ur[0].load(r, u, lane, cols);
+      add(u, ux[0], ur[0], v[0]);
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) s = fmaf(v[0][e], v[0][e], s);
+    }
+  }
+  s = row_sum(s, red, p.wpr);
+  const float rs = 1.f / sqrtf(s / (float)p.cols + p.eps);
+  if (live && p.rstd && w0 == 0 && lane == 0) p.rstd[row] = rs;
+  if (NU) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k * p.wpr + w0 < units) finish(k * p.wpr + w0, rs, v[k]);
+  } else {
+    const T* again = r ? h : x;          // each lane reads back its own values
+    for (int u = w0; u < units; u += p.wpr) {
+      ux[0].load(again, u, lane, cols);
+      ux[0].get(v[0]);
+      finish(u, rs, v[0]);
+    }
+  }
+}
+
+struct BackParams {
+  const void* dy; const void* h; const float* rstd; const void* w; const void* dres;
+  void* dx; float* part;                 // [grid][cols] sums of dy xhat, or null
+  long long lddy, ldh, ldr, ldx, rows;
+  int cols, wpr;
+};
+
+// Row groups of wpr warps walk the rows in steps of grid * groups; each lane
+// keeps its columns' sums of dy xhat.  The groups of a block add up in order
+// through shared memory, and the block writes one row of partial sums.
+template <typename T, bool VEC, int NU>
+__global__ void __launch_bounds__(kThreads) norm_back_kernel(const BackParams p) {
+  using U = Unit<T, VEC>;
+  constexpr int N = NU ? NU : 1;
+  __shared__ float red[2][kWarps];
+  extern __shared__ float sums[];        // [cols] when several groups share a block
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = kWarps / p.wpr, w0 = warp % p.wpr, mine = warp / p.wpr;
+  const int units = (p.cols + U::kCols - 1) / U::kCols;
+  const T* w = static_cast<const T*>(p.w);
+  float* part = p.part ? p.part + (long long)blockIdx.x * p.cols : nullptr;
+  float acc[N][U::E] = {};
+  if (!NU && part) {                     // wide rows: the block's own partial sums in global memory
+    for (int c = threadIdx.x; c < p.cols; c += kThreads) part[c] = 0.f;
+    __syncthreads();
+  }
+  int turn = 0;
+  for (long long row0 = (long long)blockIdx.x * groups; row0 < p.rows; row0 += (long long)gridDim.x * groups, turn ^= 1) {
+    const long long row = row0 + mine;
+    const bool live = row < p.rows;
+    const long long at = live ? row : 0;
+    const int cols = live ? p.cols : 0;
+    const T* dy = static_cast<const T*>(p.dy) + at * p.lddy;
+    const T* h = static_cast<const T*>(p.h) + at * p.ldh;
+    const T* dres = p.dres ? static_cast<const T*>(p.dres) + at * p.ldr : nullptr;
+    T* dx = static_cast<T*>(p.dx) + at * p.ldx;
+    const float rs = live ? p.rstd[row] : 0.f;
+    // xhat and g of a unit; its share of sum(g xhat); dy xhat onto a
+    auto take = [&](int unit, const U& uy, const U& uh, float (&xh)[U::E], float (&g)[U::E], float (&a)[U::E]) {
+      uh.get(xh);
+      uy.get(g);
+      float t = 0.f;
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) {
+        xh[e] *= rs;
+        a[e] = fmaf(g[e], xh[e], a[e]);
+      }
+      if (w) {
+        U uw;
+        uw.load(w, unit, lane, p.cols);
+        float f[U::E];
+        uw.get(f);
+#pragma unroll
+        for (int e = 0; e < U::E; ++e) g[e] *= f[e];
+      }
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) t = fmaf(g[e], xh[e], t);
+      return t;
+    };
+    auto put = [&](int unit, float m, const U& ud, const float (&xh)[U::E], float (&g)[U::E]) {
+      float d[U::E] = {};
+      if (dres) ud.get(d);
+#pragma unroll
+      for (int e = 0; e < U::E; ++e) g[e] = fmaf(rs, fmaf(-xh[e], m, g[e]), d[e]);
+      U::store(dx, unit, lane, cols, g);
+    };
+    U uy[N], uh[N], ud[N];
+    float xh[N][U::E], g[N][U::E];
+    float s = 0.f;
+    if (NU) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        uy[k].load(dy, k * p.wpr + w0, lane, cols);
+        uh[k].load(h, k * p.wpr + w0, lane, cols);
+      }
+      if (dres) {
+#pragma unroll
+        for (int k = 0; k < N; ++k) ud[k].load(dres, k * p.wpr + w0, lane, cols);
+      }
+#pragma unroll
+      for (int k = 0; k < N; ++k) s += take(k * p.wpr + w0, uy[k], uh[k], xh[k], g[k], acc[k]);
+    } else {
+      for (int u = w0; u < units; u += p.wpr) {
+        uy[0].load(dy, u, lane, cols);
+        uh[0].load(h, u, lane, cols);
+        float a[U::E] = {};
+        s += take(u, uy[0], uh[0], xh[0], g[0], a);
+        if (part) {
+#pragma unroll
+          for (int e = 0; e < U::E; ++e) {
+            const int c = U::col(u, lane, e) + (VEC ? e : 0);
+            if (c < cols) part[c] += a[e];
+          }
+        }
+      }
+    }
+    const float m = row_sum(s, red[turn], p.wpr) / (float)p.cols;
+    if (NU) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) put(k * p.wpr + w0, m, ud[k], xh[k], g[k]);
+    } else {
+      for (int u = w0; u < units; u += p.wpr) {
+        uy[0].load(dy, u, lane, cols);
+        uh[0].load(h, u, lane, cols);
+        if (dres) ud[0].load(dres, u, lane, cols);
+        float a[U::E] = {};
+        take(u, uy[0], uh[0], xh[0], g[0], a);
+        put(u, m, ud[0], xh[0], g[0]);
+      }
+    }
+  }
+  if (!NU || !part) return;
+  for (int gr = groups - 1; gr >= 0; --gr) {
+    if (gr == mine) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int e = 0; e < U::E; ++e) {
+          const int c = U::col(k * p.wpr + w0, lane, e) + (VEC ? e : 0);
+          if (c >= p.cols) continue;
+          const float t = (gr == groups - 1 ? 0.f : sums[c]) + acc[k][e];
+          if (gr) sums[c] = t;
+          else part[c] = t;
+        }
+    }
+    if (groups > 1) __syncthreads();
+  }
+}
+
+// dw[c] = sum over the partial rows: 32 columns per block, 8 rows at a time,
+// the eight sums added in order.
+__global__ void __launch_bounds__(kThreads) norm_weight_kernel(const float* part, float* dw, int n, int cols) {
+  __shared__ float red[kWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < cols)
+    for (int i = warp; i < n; i += kWarps) s += part[(long long)i * cols + c];
+  red[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) t += red[i][lane];
+    dw[c] = t;
+  }
+}
+
+// Warps per row and units per warp: the fewest warps that hold a row in at most
+// `most` units each; 0 units when eight cannot.
+void split_row(int cols, int unit_cols, int most, int& wpr, int& nu) {
+  const int units = (cols + unit_cols - 1) / unit_cols;
+  for (wpr = 1; wpr < kWarps && (units + wpr - 1) / wpr > most; wpr *= 2) {}
+  nu = (units + wpr - 1) / wpr;
+  if (nu > most) nu = 0;
+  while (nu & (nu - 1)) ++nu;            // 1, 2, 4, 8
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_add(AddParams p, cudaStream_t s) {
+  int nu;
+  split_row(p.cols, Unit<T, VEC>::kCols, 32 / Unit<T, VEC>::E, p.wpr, nu);
+  const unsigned grid = (unsigned)cdiv(p.rows, kWarps / p.wpr);
+  switch (nu) {
+    case 1: add_norm_kernel<T, VEC, 1><<<grid, kThreads, 0, s>>>(p); break;
+    case 2: add_norm_kernel<T, VEC, 2><<<grid, kThreads, 0, s>>>(p); break;
+    case 4: add_norm_kernel<T, VEC, 4><<<grid, kThreads, 0, s>>>(p); break;
+    case 8: add_norm_kernel<T, VEC, VEC && sizeof(T) == 2 ? 4 : 8><<<grid, kThreads, 0, s>>>(p); break;
+    default: add_norm_kernel<T, VEC, 0><<<grid, kThreads, 0, s>>>(p); break;
+  }
+  return cudaGetLastError();
+}
+
+template <typename T, bool VEC>
+cudaError_t launch_back(BackParams p, float* dw, cudaStream_t s) {
+  int nu;
+  split_row(p.cols, Unit<T, VEC>::kCols, 16 / Unit<T, VEC>::E * 2, p.wpr, nu);
+  const int groups = kWarps / p.wpr;
+  const long long want = cdiv(p.rows, groups);
+  const int grid = (int)(want < kBackGrid ? want : kBackGrid);
+  const size_t smem = p.part && groups > 1 && nu ? (size_t)p.cols * 4 : 0;   // at most 4 x 1024 columns: 16 KB
+  switch (nu) {
+    case 1: norm_back_kernel<T, VEC, 1><<<grid, kThreads, smem, s>>>(p); break;
+    case 2: norm_back_kernel<T, VEC, 2><<<grid, kThreads, smem, s>>>(p); break;
+    case 4: norm_back_kernel<T, VEC, 4><<<grid, kThreads, smem, s>>>(p); break;
+    case 8: norm_back_kernel<T, VEC, VEC && sizeof(T) == 2 ? 4 : 8><<<grid, kThreads, smem, s>>>(p); break;
+    default: norm_back_kernel<T, VEC, 0><<<grid, kThreads, smem, s>>>(p); break;
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || !p.part) return e;
+  norm_weight_kernel<<<(unsigned)cdiv(p.cols, 32), kThreads, 0, s>>>(p.part, dw, grid, p.cols);
+  return cudaGetLastError();
+}
+
+mc_status err(mc_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return record_error(s, buf);
+}
+
+// One 2-D operand of a call: rows of `bytes` bytes each `pitch` bytes apart.
+struct Rows {
+  const char* name;
+  const void* p;
+  long long pitch, bytes;
+  bool out;
+};
+uintptr_t at(const Rows& a) { return reinterpret_cast<uintptr_t>(a.p); }
+// Whether two operands of `n` rows share an address.  Equal pitches allow two
+// column ranges of one buffer.
+bool overlap(const Rows& a, const Rows& b, long long n) {
+  const uintptr_t ea = at(a) + (n - 1) * a.pitch + a.bytes, eb = at(b) + (n - 1) * b.pitch + b.bytes;
+  if (at(a) >= eb || at(b) >= ea) return false;
+  if (a.pitch != b.pitch || a.pitch == 0 || n == 1) return true;
+  const Rows &lo = at(a) <= at(b) ? a : b, &hi = at(a) <= at(b) ? b : a;
+  const long long d = (long long)((at(hi) - at(lo)) % (uintptr_t)a.pitch);
+  return d < lo.bytes || d + hi.bytes > a.pitch;
+}
+// Outputs may lie exactly on an operand that `same` allows, and share no
+// address with any other.
+template <typename Same>
+mc_status check_overlaps(const char* call, const Rows* t, int n, long long rows, Same same) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j) {
+      if (i == j || !t[i].out || !t[i].p || !t[j].p || (t[j].out && j < i)) continue;
+      if (same(i, j) && t[i].p == t[j].p && t[i].pitch == t[j].pitch) continue;
+      if (overlap(t[i], t[j], rows)) return err(MC_ERR_INVALID_ARG, "%s: %s overlaps %s", call, t[i].name, t[j].name);
+    }
+  return MC_OK;
+}
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace nm
+}  // namespace
+}  // namespace mc
+
+using namespace mc;
+using namespace mc::nm;
+
+extern "C" {
+
+mc_status mc_add_rms_norm(const void* x, int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                          void* h, int64_t ldh, void* y, int64_t ldy, float* scales, int64_t lds, float* rstd,
+                          int64_t rows, int32_t cols, int32_t dtype, int32_t y_dtype, float eps,
+                          mc_stream_t stream) {
+  const char* me = "mc_add_rms_norm";
+  if (dtype != MC_BF16 && dtype != MC_F32) return err(MC_ERR_INVALID_ARG, "%s: dtype %d", me, dtype);
+  if (y_dtype != dtype && y_dtype != MC_F8E4M3) return err(MC_ERR_INVALID_ARG, "%s: y_dtype %d", me, y_dtype);
+  const bool f8 = y_dtype == MC_F8E4M3;
+  if (rows < 0 || rows > 0x7fffffff || cols < 1 || cols > (1 << 30))
+    return err(MC_ERR_INVALID_ARG, "%s: rows %lld, cols %d", me, (long long)rows, cols);
+  const int tiles = (cols + kTile - 1) / kTile;
+  if (ldx < cols || ldy < cols || (residual && (ldr < cols || ldh < cols)) || (f8 && scales && lds < tiles))
+    return err(MC_ERR_INVALID_ARG, "%s: a pitch is below its row's length", me);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return err(MC_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", me);
+  if (rows == 0) return record_error(MC_OK, "");
+  if ((residual == nullptr) != (h == nullptr)) return err(MC_ERR_INVALID_ARG, "%s: residual and h go together", me);
+  if (f8 != (scales != nullptr)) return err(MC_ERR_INVALID_ARG, "%s: scales go with an e4m3 y", me);
+  if (!x || !y) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  const size_t es = dtype == MC_BF16 ? 2 : 4;
+  for (const void* p : {x, residual, weight, static_cast<const void*>(h), static_cast<const void*>(f8 ? nullptr : y)})
+    if (!aligned(p, es)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  if (!aligned(scales, 4) || !aligned(rstd, 4)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  const long long e = (long long)es;
+  const Rows t[] = {{"x", x, ldx * e, cols * e, false},
+                    {"residual", residual, ldr * e, cols * e, false},
+                    {"weight", weight, 0, cols * e, false},
+                    {"h", h, ldh * e, cols * e, true},
+                    {"y", y, ldy * (f8 ? 1 : e), cols * (f8 ? 1 : e), true},
+                    {"scales", scales, lds * 4, tiles * 4ll, true},
+                    {"rstd", rstd, 4, 4, true}};
+  // a lane writes h and y over values of x and residual that it has read
+  const mc_status st = check_overlaps(me, t, 7, rows, [&](int i, int j) {
+    return (i == 3 && j <= 1) || (i == 4 && j <= 1 && !f8);
+  });
+  if (st != MC_OK) return st;
+  AddParams p{x, residual, weight, h, y, f8 ? scales : nullptr, rstd, ldx, ldr, ldh, ldy, lds, rows, cols, 1, f8, eps};
+  const int per = 16 / (int)es;          // values per 16 bytes
+  const bool vec = cols % per == 0 && ldx % per == 0 && aligned(x, 16) && aligned(weight, 16) &&
+                   (!residual || (ldr % per == 0 && ldh % per == 0 && aligned(residual, 16) && aligned(h, 16))) &&
+                   ldy % per == 0 && aligned(y, f8 ? per : 16);
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t c;
+  if (dtype == MC_BF16) c = vec ? launch_add<__nv_bfloat16, true>(p, s) : launch_add<__nv_bfloat16, false>(p, s);
+  else c = vec ? launch_add<float, true>(p, s) : launch_add<float, false>(p, s);
+  if (c != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(c));
+  return record_error(MC_OK, "");
+}
+
+mc_status mc_rms_norm_backward_workspace_size(int32_t cols, size_t* bytes) {
+  if (cols < 1 || cols > (1 << 30) || !bytes) return err(MC_ERR_INVALID_ARG, "mc_rms_norm_backward: cols %d or null bytes", cols);
+  *bytes = (size_t)kBackGrid * (size_t)cols * 4;
+  return record_error(MC_OK, "");
+}
+
+mc_status mc_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int64_t ldh, const float* rstd,
+                               const void* weight, const void* dres, int64_t ldr, void* dx, int64_t lddx,
+                               float* dweight, int64_t rows, int32_t cols, int32_t dtype, void* workspace,
+                               size_t workspace_bytes, mc_stream_t stream) {
+  const char* me = "mc_rms_norm_backward";
+  if (dtype != MC_BF16 && dtype != MC_F32) return err(MC_ERR_INVALID_ARG, "%s: dtype %d", me, dtype);
+  if (rows < 0 || rows > 0x7fffffff || cols < 1 || cols > (1 << 30))
+    return err(MC_ERR_INVALID_ARG, "%s: rows %lld, cols %d", me, (long long)rows, cols);
+  if (lddy < cols || ldh < cols || lddx < cols || (dres && ldr < cols))
+    return err(MC_ERR_INVALID_ARG, "%s: a pitch is below its row's length", me);
+  if (!aligned(dweight, 4)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (rows == 0) {                       // a sum over no rows
+    const cudaError_t c = dweight ? cudaMemsetAsync(dweight, 0, (size_t)cols * 4, s) : cudaSuccess;
+    if (c != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(c));
+    return record_error(MC_OK, "");
+  }
+  if (!dy || !h || !rstd || !dx) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  const size_t es = dtype == MC_BF16 ? 2 : 4;
+  for (const void* p : {dy, h, weight, dres, static_cast<const void*>(dx)})
+    if (!aligned(p, es)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  if (!aligned(rstd, 4)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  const size_t need = (size_t)kBackGrid * (size_t)cols * 4;
+  if (dweight && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
+    return err(MC_ERR_WORKSPACE, "%s: dweight needs a 16-byte aligned workspace of %zu bytes", me, need);
+  const long long e = (long long)es;
+  const Rows t[] = {{"dy", dy, lddy * e, cols * e, false}, {"h", h, ldh * e, cols * e, false},
+                    {"dres", dres, ldr * e, cols * e, false}, {"rstd", rstd, 4, 4, false},
+                    {"weight", weight, 0, cols * e, false}, {"dx", dx, lddx * e, cols * e, true},
+                    {"dweight", dweight, 0, cols * 4ll, true},
+                    {"workspace", dweight ? workspace : nullptr, 0, (long long)need, true}};
+  // a lane writes dx over values of dy, h and dres that it has read
+  const mc_status st = check_overlaps(me, t, 8, rows, [](int i, int j) { return i == 5 && j <= 2; });
+  if (st != MC_OK) return st;
+  BackParams p{dy, h, rstd, weight, dres, dx, dweight ? static_cast<float*>(workspace) : nullptr,
+               lddy, ldh, ldr, lddx, rows, cols, 1};
+  const int per = 16 / (int)es;
+  const bool vec = cols % per == 0 && lddy % per == 0 && ldh % per == 0 && lddx % per == 0 && aligned(dy, 16) &&
+                   aligned(h, 16) && aligned(dx, 16) && aligned(weight, 16) &&
+                   (!dres || (ldr % per == 0 && aligned(dres, 16)));
+  cudaError_t c;
+  if (dtype == MC_BF16) c = vec ? launch_back<__nv_bfloat16, true>(p, dweight, s) : launch_back<__nv_bfloat16, false>(p, dweight, s);
+  else c = vec ? launch_back<float, true>(p, dweight, s) : launch_back<float, false>(p, dweight, s);
+  if (c != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(c));
+  return record_error(MC_OK, "");
+}
+
+}  // extern "C"

@@ -13,9 +13,11 @@
 //                the latents), fp32 arithmetic.
 //   mc_rope      rotary embedding on interleaved pairs at positions 0..S-1,
 //                angles s * theta^(-2k/d) and their cosines and sines in fp64.
+//   mc_rope_backward  its gradient: the transposed rotation.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -92,6 +94,80 @@ __global__ void rope_kernel(T* x, int B, int S, int nh, int d, long long sb, lon
       stv(p + 1, x0 * sn + x1 * c);
     }
   }
+}
+
+// Gradient of the rotary embedding: the transposed rotation of each pair, from
+// dy to dx (which may be dy).  A block takes `per` consecutive positions of
+// every (b, head): it writes their cosines and sines to shared memory, then
+// moves 16 bytes (V pairs) per thread and step.  The frequency table is fp64
+// (once per block); an angle is reduced in fp64 to at most half a turn, so its
+// fp32 sine and cosine are good to 2^-23 absolute at any position, without
+// fp64 trigonometry for each position.
+struct RopeBack {
+  const void* dy; void* dx;
+  long long yb, ys, yh, xb, xs, xh;
+  int B, S, nh, d, per;
+  double step;                           // log2(theta) * 2 / d
+};
+template <typename T, int V>
+__global__ void __launch_bounds__(256) rope_back_kernel(const RopeBack p) {
+  extern __shared__ double turns[];      // [d/2] turns per position, then [per][d/2] (cos, sin)
+  const int half = p.d / 2, nv = half / V;
+  float2* cs = reinterpret_cast<float2*>(turns + half);
+  for (int k = threadIdx.x; k < half; k += blockDim.x) turns[k] = exp2(-p.step * k) * 0.15915494309189535;
+  const long long blocks = ((long long)p.S + p.per - 1) / p.per;
+  for (long long blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
+    const int s0 = (int)(blk * p.per), n = min(p.per, p.S - s0);
+    __syncthreads();
+    for (int x = threadIdx.x; x < n * half; x += blockDim.x) {
+      const int i = x / half, k = x - i * half;
+      double t = (double)(s0 + i) * turns[k];
+      t -= rint(t);
+      float sn, cn;
+      sincospif((float)(2.0 * t), &sn, &cn);
+      cs[x] = make_float2(cn, sn);
+    }
+    __syncthreads();
+    const long long items = (long long)p.B * n * p.nh * nv;
+    for (long long x = threadIdx.x; x < items; x += blockDim.x) {
+      const long long row = x / nv;
+      const int c = (int)(x - row * nv);
+      const long long bi = row / p.nh;
+      const int h = (int)(row - bi * p.nh);
+      const int b = (int)(bi / n), i = (int)(bi - (long long)b * n);
+      const T* src = static_cast<const T*>(p.dy) + b * p.yb + (s0 + i) * p.ys + h * p.yh + 2 * V * c;
+      T* dst = static_cast<T*>(p.dx) + b * p.xb + (s0 + i) * p.xs + h * p.xh + 2 * V * c;
+      const float2* f = cs + i * half + V * c;
+      alignas(16) T v[2 * V];
+      if (V > 1) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src);
+      else { v[0] = src[0]; v[1] = src[1]; }
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const float a = ldv(v + 2 * k), e = ldv(v + 2 * k + 1);
+        stv(v + 2 * k, fmaf(a, f[k].x, e * f[k].y));
+        stv(v + 2 * k + 1, fmaf(e, f[k].x, -(a * f[k].y)));
+      }
+      if (V > 1) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(v);
+      else { dst[0] = v[0]; dst[1] = v[1]; }
+    }
+  }
+}
+
+template <typename T, int V>
+cudaError_t launch_rope_back(RopeBack p, cudaStream_t s) {
+  // positions per block: about 2048 accesses of a block's 256 threads, fewer
+  // while that leaves SMs without a block; the table stays under 32 KB
+  const long long each = (long long)p.B * p.nh * (p.d / 2 / V);
+  long long per = cdiv(2048, each);
+  const long long spread = cdiv(p.S, 2ll * sm_count());
+  if (per > spread) per = spread;
+  const long long room = 4096 / (p.d / 2);
+  if (per > room) per = room;
+  p.per = (int)(per < 1 ? 1 : per);
+  const size_t smem = (size_t)(p.d / 2) * 8 * (1 + p.per);
+  const long long blocks = cdiv(p.S, p.per), most = (long long)sm_count() * 8;
+  rope_back_kernel<T, V><<<(unsigned)(blocks < most ? blocks : most), 256, smem, s>>>(p);
+  return cudaGetLastError();
 }
 
 mc_status err(mc_status s, const char* fmt, ...) {
@@ -205,6 +281,43 @@ mc_status mc_rope(void* x, int32_t B, int32_t S, int32_t nh, int32_t d, int64_t 
     rope_kernel<float><<<grid, 256, smem, s>>>(static_cast<float*>(x), B, S, nh, d, sb, ss, sh, theta);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return err(MC_ERR_CUDA, "mc_rope: %s", cudaGetErrorString(e));
+  return done();
+}
+
+mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, void* dx, int64_t xb, int64_t xs,
+                           int64_t xh, int32_t B, int32_t S, int32_t nh, int32_t d, int32_t dtype, double theta,
+                           mc_stream_t stream) {
+  const char* me = "mc_rope_backward";
+  if (dtype != MC_BF16 && dtype != MC_F32) return err(MC_ERR_INVALID_ARG, "%s: dtype %d", me, dtype);
+  if (B < 0 || S < 0 || nh < 1 || d < 2 || (d & 1) || d > 4096)
+    return err(MC_ERR_INVALID_ARG, "%s: B %d, S %d, heads %d, d %d (d even, 2..4096)", me, B, S, nh, d);
+  if (!(theta > 0.0) || !std::isfinite(theta)) return err(MC_ERR_INVALID_ARG, "%s: theta must be finite and > 0", me);
+  if ((long long)B * S == 0) return done();
+  if (!dy || !dx) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  const size_t es = esize(dtype);
+  if (reinterpret_cast<uintptr_t>(dy) % es || reinterpret_cast<uintptr_t>(dx) % es)
+    return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  const int64_t ext[3] = {B, S, nh}, sy[3] = {yb, ys, yh}, sx[3] = {xb, xs, xh};
+  int64_t endy = d, endx = d;
+  bool same = dy == dx, vec = d % (16 / es) == 0 && al16(dy) && al16(dx);
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] == 1) continue;
+    if (sy[i] < 0 || sx[i] < 0) return err(MC_ERR_INVALID_ARG, "%s: negative stride", me);
+    endy += (ext[i] - 1) * sy[i];
+    endx += (ext[i] - 1) * sx[i];
+    same = same && sy[i] == sx[i];
+    vec = vec && (sy[i] * es) % 16 == 0 && (sx[i] * es) % 16 == 0;
+  }
+  if (!distinct_addresses(sx, ext, 3, d)) return err(MC_ERR_INVALID_ARG, "%s: elements of dx share addresses", me);
+  const uintptr_t py = reinterpret_cast<uintptr_t>(dy), px = reinterpret_cast<uintptr_t>(dx);
+  if (!same && py < px + endx * es && px < py + endy * es)
+    return err(MC_ERR_INVALID_ARG, "%s: dx overlaps dy without being dy", me);
+  RopeBack p{dy, dx, yb, ys, yh, xb, xs, xh, B, S, nh, d, 1, std::log2(theta) * 2.0 / d};
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (dtype == MC_BF16) e = vec ? launch_rope_back<__nv_bfloat16, 4>(p, s) : launch_rope_back<__nv_bfloat16, 1>(p, s);
+  else e = vec ? launch_rope_back<float, 2>(p, s) : launch_rope_back<float, 1>(p, s);
+  if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
   return done();
 }
 

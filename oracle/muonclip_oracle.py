@@ -423,6 +423,30 @@ def rope(x: np.ndarray, theta: float = 10000.0) -> np.ndarray:
     return out
 
 
+def rms_norm_backward(dy, h, rstd, w=None, dres=None):
+    """Gradients of y = h rstd w with rstd = 1/sqrt(mean(h^2) + eps) per row:
+    dh = rstd (g - xhat mean(g xhat)) (+ dres), dw = sum over rows of dy xhat,
+    xhat = h rstd, g = w dy.  rstd is taken as given (it may be rounded)."""
+    dy, h = np.asarray(dy, np.float64), np.asarray(h, np.float64)
+    xhat = h * np.asarray(rstd, np.float64)[:, None]
+    g = dy if w is None else dy * np.asarray(w, np.float64)
+    dx = np.asarray(rstd, np.float64)[:, None] * (g - xhat * np.mean(g * xhat, axis=1, keepdims=True))
+    if dres is not None:
+        dx = dx + np.asarray(dres, np.float64)
+    return dx, np.sum(dy * xhat, axis=0)
+
+
+def rope_backward(dy: np.ndarray, theta: float = 10000.0) -> np.ndarray:
+    """Gradient of rope: each pair turned back by its angle."""
+    dy = np.asarray(dy, np.float64)
+    S, d = dy.shape[1], dy.shape[-1]
+    turn = np.exp(-1j * np.arange(S)[:, None] * theta ** (-np.arange(0, d, 2) / d)[None, :])
+    z = (dy[..., 0::2] + 1j * dy[..., 1::2]) * turn.reshape([1, S] + [1] * (dy.ndim - 3) + [d // 2])
+    out = np.empty_like(dy)
+    out[..., 0::2], out[..., 1::2] = z.real, z.imag
+    return out
+
+
 def project_mla(X, W_DQ, W_UQ, W_DKV, W_UKV, W_KR, H: int, d_nope: int = 128,
                 d_rope: int = 64, d_v: int = 128):
     """MLA query/key features: returns (Q [B,S,H,d_nope+d_rope] = [q^C||q^R],
@@ -460,6 +484,15 @@ def round_to_bf16(x: np.ndarray) -> np.ndarray:
     r = np.round(m * 256.0)
     out = np.ldexp(r, e - 8)
     return np.where(np.isfinite(x), out, x)
+
+
+def round_to_e4m3(x: np.ndarray) -> np.ndarray:
+    """Round float64 to the nearest e4m3 value (4 significand bits, quantum 2^-9
+    below 2^-6, largest 448, ties to even), saturating, as float64."""
+    x = np.asarray(x, np.float64)
+    _, e = np.frexp(x)
+    q = np.ldexp(1.0, np.maximum(e, -5) - 4)
+    return np.clip(np.round(x / q) * q, -448.0, 448.0)
 
 
 def round_to_f32(x: np.ndarray) -> np.ndarray:

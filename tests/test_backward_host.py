@@ -132,3 +132,130 @@ def test_grad_struct_layout(tmp_path):
     got = subprocess.run([str(tmp_path / "l")], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == [ctypes.sizeof(McAttnGrad), McAttnGrad.lse.offset, McAttnGrad.dk_shared.offset,
                                      McAttnGrad.dv.offset]
+
+
+# ------------------------------------------------------------- norms and the rotary gradient
+X, R, H, Y, SC, RS, WT = (P(FAKE + i * STEP) for i in range(7))
+BF, F32, F8 = abi.MC_BF16, abi.MC_F32, abi.MC_F8E4M3
+
+
+def add(**kw):
+    a = dict(x=X, ldx=256, r=R, ldr=256, w=WT, h=H, ldh=256, y=Y, ldy=256, sc=None, lds=0, rs=RS, rows=4, cols=256,
+             dt=BF, yt=BF, eps=1e-6, stream=None)
+    a.update(kw)
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(dt=5), "dtype 5"),
+    (dict(yt=F32), "y_dtype"),
+    (dict(yt=F8), "scales"),
+    (dict(sc=SC, lds=2), "scales"),
+    (dict(yt=F8, sc=SC, lds=1), "pitch"),
+    (dict(rows=-1), "rows -1"),
+    (dict(cols=0), "cols 0"),
+    (dict(ldx=255), "pitch"),
+    (dict(ldh=100), "pitch"),
+    (dict(eps=-1.0), "eps"),
+    (dict(eps=float("inf")), "eps"),
+    (dict(h=None), "together"),
+    (dict(r=None), "together"),
+    (dict(x=None), "null"),
+    (dict(y=None), "null"),
+    (dict(x=P(FAKE + 1)), "aligned"),
+    (dict(rs=P(FAKE + 5 * STEP + 2)), "aligned"),
+    (dict(y=H), "h overlaps y"),
+    (dict(h=P(FAKE + 512)), "h overlaps x"),                # another row of x
+    (dict(h=X, ldh=512), "h overlaps x"),                   # x's memory at another pitch
+    (dict(y=WT), "y overlaps weight"),
+    (dict(yt=F8, sc=SC, lds=2, y=X), "y overlaps x"),       # 8-bit rows over wider ones
+    (dict(rs=P(FAKE + 4)), "rstd overlaps x"),
+])
+def test_add_rms_norm_refuses(lib, kw, needle):
+    assert lib.mc_add_rms_norm(*add(**kw)) == INV
+    assert needle in lib.mc_last_error().decode()
+
+
+def test_norm_calls_on_no_rows_launch_nothing(lib):
+    assert lib.mc_add_rms_norm(*add(rows=0)) == abi.MC_OK
+    assert lib.mc_rms_norm_backward(*back(rows=0, dw=None)) == abi.MC_OK
+
+
+def back(**kw):
+    a = dict(dy=X, lddy=256, h=R, ldh=256, rs=RS, w=WT, dres=H, ldr=256, dx=Y, lddx=256, dw=SC, rows=4, cols=256, dt=BF,
+             ws=P(FAKE + 8 * STEP), n=1 << 30, stream=None)
+    a.update(kw)
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("kw,code,needle", [
+    (dict(dt=F8), INV, "dtype"),
+    (dict(rows=-2), INV, "rows -2"),
+    (dict(cols=-1), INV, "cols -1"),
+    (dict(lddy=10), INV, "pitch"),
+    (dict(ldr=10), INV, "pitch"),
+    (dict(dy=None), INV, "null"),
+    (dict(rs=None), INV, "null"),
+    (dict(dx=None), INV, "null"),
+    (dict(h=P(FAKE + STEP + 1)), INV, "aligned"),
+    (dict(dw=P(FAKE + 3)), INV, "aligned"),
+    (dict(ws=None), WS, "workspace"),
+    (dict(n=304 * 256 * 4 - 1), WS, "workspace"),
+    (dict(ws=P(FAKE + 8 * STEP + 8)), WS, "workspace"),
+    (dict(dx=P(FAKE + 512)), INV, "dx overlaps dy"),
+    (dict(dx=R, lddx=512), INV, "dx overlaps h"),
+    (dict(dw=RS), INV, "dweight overlaps rstd"),
+    (dict(ws=X), INV, "workspace overlaps dy"),
+])
+def test_rms_norm_backward_refuses(lib, kw, code, needle):
+    assert lib.mc_rms_norm_backward(*back(**kw)) == code
+    assert needle in lib.mc_last_error().decode()
+
+
+def test_rms_norm_backward_workspace_size(lib):
+    n = ctypes.c_size_t(0)
+    assert lib.mc_rms_norm_backward_workspace_size(256, ctypes.byref(n)) == abi.MC_OK and n.value == 304 * 256 * 4
+    assert lib.mc_rms_norm_backward_workspace_size(0, ctypes.byref(n)) == INV
+    assert lib.mc_rms_norm_backward_workspace_size(256, None) == INV
+
+
+def rope(**kw):
+    a = dict(dy=X, yb=8192, ys=1024, yh=64, dx=Y, xb=8192, xs=1024, xh=64, B=2, S=8, nh=16, d=64, dt=BF, theta=1e4,
+             stream=None)
+    a.update(kw)
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("kw,needle", [
+    (dict(dt=F8), "dtype"),
+    (dict(d=63), "d 63"),
+    (dict(d=0), "d 0"),
+    (dict(d=8192), "d 8192"),
+    (dict(nh=0), "heads 0"),
+    (dict(S=-1), "S -1"),
+    (dict(theta=0.0), "theta"),
+    (dict(theta=float("inf")), "theta"),
+    (dict(dy=None), "null"),
+    (dict(dx=None), "null"),
+    (dict(dx=P(FAKE + 3 * STEP + 1)), "aligned"),
+    (dict(ys=-1024), "negative"),
+    (dict(xh=0), "share"),
+    (dict(xs=512), "share"),
+    (dict(dx=P(FAKE + 64)), "overlaps"),
+    (dict(dx=X, xs=2048, xb=16384), "overlaps"),            # in place with other strides
+])
+def test_rope_backward_refuses(lib, kw, needle):
+    assert lib.mc_rope_backward(*rope(**kw)) == INV
+    assert needle in lib.mc_last_error().decode()
+
+
+def test_rope_backward_of_nothing_is_a_no_op(lib):
+    assert lib.mc_rope_backward(*rope(B=0, dy=None, dx=None)) == abi.MC_OK
+
+
+def test_norm_bindings_refuse_host_tensors():
+    x = torch.zeros(2, 8)
+    for call in (lambda: mc.add_rms_norm(x), lambda: mc.rms_norm_backward(x, x, x[:, 0].contiguous()),
+                 lambda: mc.rope_backward(torch.zeros(1, 2, 8))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

@@ -74,3 +74,48 @@ def test_attention_backward_catches_planted_mistakes(mistake):
         "shared_mean": lambda: right[:3] + (right[3] / H,),
     }[mistake]()
     assert max(np.max(np.abs(a - b)) for a, b in zip(right, wrong)) > 1e-2
+
+
+def test_rms_norm_backward_matches_differences():
+    rng = np.random.default_rng(6)
+    h, w, dy = rnd(rng, 3, 7), 1 + 0.3 * rnd(rng, 7), rnd(rng, 3, 7)
+    eps = 0.05
+    rstd = 1 / np.sqrt(np.mean(h * h, 1) + eps)
+    loss = lambda: float(np.sum(O.rms_norm(h, eps) * w * dy))  # noqa: E731
+    dx, dw = O.rms_norm_backward(dy, h, rstd, w)
+    for x, g in ((h, dx), (w, dw)):
+        for idx in np.ndindex(*x.shape):
+            keep = x[idx]
+            x[idx] = keep + 1e-5
+            up = loss()
+            x[idx] = keep - 1e-5
+            down = loss()
+            x[idx] = keep
+            assert abs((up - down) / 2e-5 - g[idx]) < 1e-8
+    assert np.allclose(O.rms_norm_backward(dy, h, rstd, w, dres=h)[0], dx + h)
+    # a missing mean term or weight is far off
+    assert np.max(np.abs(rstd[:, None] * dy * w - dx)) > 1e-2
+    assert np.max(np.abs(O.rms_norm_backward(dy, h, rstd)[0] - dx)) > 1e-2
+
+
+def test_rope_backward_is_the_transpose():
+    """<rope(x), dy> = <x, rope_backward(dy)>, and it undoes the rotation."""
+    rng = np.random.default_rng(7)
+    x, dy = rnd(rng, 2, 9, 3, 6), rnd(rng, 2, 9, 3, 6)
+    assert abs(np.sum(O.rope(x) * dy) - np.sum(x * O.rope_backward(dy))) < 1e-10
+    assert np.allclose(O.rope_backward(O.rope(x, 77.0), 77.0), x)
+    assert np.max(np.abs(O.rope(dy) - O.rope_backward(dy))) > 0.1     # the direction matters
+
+
+def test_e4m3_rounding():
+    """Every e4m3 value is kept, midpoints go to even, small ones to the 2^-9 grid."""
+    vals = sorted({m / 8 * 2.0 ** e for e in range(-6, 9) for m in range(8, 16)} | {m * 2.0 ** -9 for m in range(8)})
+    vals = np.array([v for v in vals if v <= 448.0])
+    assert len(vals) == 127                               # 7 f is NaN
+    assert np.array_equal(O.round_to_e4m3(vals), vals) and np.array_equal(O.round_to_e4m3(-vals), -vals)
+    mid = (vals[1:] + vals[:-1]) / 2
+    got = O.round_to_e4m3(mid)
+    even = np.where(np.arange(len(mid)) % 2 == 0, vals[:-1], vals[1:])
+    assert np.array_equal(got, even)
+    assert np.array_equal(O.round_to_e4m3(mid * (1 + 1e-9)), vals[1:])
+    assert O.round_to_e4m3(1e9) == 448.0
