@@ -134,19 +134,11 @@ def attn_desc(q, k, k_shared=None, causal=True, scale=None) -> McAttnDesc:
         raise ValueError("feature axis must be contiguous")
     if q.dtype not in _DT or k.dtype != q.dtype or (k_shared is not None and k_shared.dtype != q.dtype):
         raise ValueError("q, k, k_shared must share a supported dtype")
-    d = McAttnDesc()
-    d.B, d.S, d.H, d.d_head, d.d_shared = B, S, H, dk, dr
-    d.dtype = _DT[q.dtype]
-    d.causal = 1 if causal else 0
-    d.scale = (1.0 / math.sqrt(dq)) if scale is None else scale
-    d.q, d.k = q.data_ptr(), k.data_ptr()
-    d.k_shared = None if k_shared is None else k_shared.data_ptr()
-    for i in range(3):
-        d.q_strides[i] = q.stride(i)
-        d.k_strides[i] = k.stride(i)
-    if k_shared is not None:
-        d.ks_strides[0], d.ks_strides[1] = k_shared.stride(0), k_shared.stride(1)
-    return d
+    if scale is None:
+        scale = 1.0 / math.sqrt(dq)
+    return McAttnDesc(B, S, H, dk, dr, _DT[q.dtype], 1 if causal else 0, scale, q.data_ptr(), k.data_ptr(),
+                      None if k_shared is None else k_shared.data_ptr(), q.stride()[:3], k.stride()[:3],
+                      (0, 0) if k_shared is None else k_shared.stride()[:2])
 
 
 def qk_max_logit(q, k, k_shared=None, causal=True, scale=None, smax=None, argmax=None,
@@ -195,18 +187,33 @@ def qk_attention_forward(q, k, v, k_shared=None, causal=True, scale=None, out=No
     return out, lse, smax
 
 
-def _same_device(**tensors):
-    """All given tensors on one CUDA device; returns it."""
-    dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.device.type != "cuda":
-            raise ValueError(f"{name}: expected a CUDA tensor")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, not on {dev}")
-        dev = t.device
-    return dev
+def _device_of(first, name, *others):
+    """Index of the CUDA device that every given tensor (or None) is on."""
+    index = first.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on {first.device}; one is on {t.device}")
+    return index
+
+
+def _run(fn, name, index, stream, *args):
+    """fn(*args, stream) on device `index` (its current stream unless given)."""
+    if torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _run(fn, name, index, stream, *args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    code = fn(*args, stream)
+    if code:
+        check(code, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def attention_backward_workspace_size(q, k, k_shared=None) -> int:
@@ -227,54 +234,41 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
     allocated unless given (any strides the features may have).  workspace: a
     uint8 CUDA tensor of attention_backward_workspace_size bytes; without one,
     one is allocated for the call."""
-    B, S, H, D = q.shape
-    dvw = v.shape[-1]
-    dev = _same_device(q=q, k=k, v=v, out=out, lse=lse, dout=dout, k_shared=k_shared, dq=dq, dk=dk, dv=dv,
-                       dk_shared=dk_shared, workspace=workspace, status=status)
-    for name, t, shape in (("k", k, (B, S, H, k.shape[-1])), ("v", v, (B, S, H, dvw)), ("out", out, (B, S, H, dvw)),
-                           ("dout", dout, (B, S, H, dvw))):
-        if tuple(t.shape) != shape or t.stride(3) != 1 or t.dtype != q.dtype:
-            raise ValueError(f"{name} must be {list(shape)} with a contiguous feature axis and q's dtype")
-    if k_shared is not None and tuple(k_shared.shape[:2]) != (B, S):
-        raise ValueError("k_shared must be [B, S, dr]")
-    if tuple(lse.shape) != (B, H, S) or not lse.is_contiguous() or lse.dtype != torch.float32:
-        raise ValueError("lse must be a contiguous [B, H, S] float32 tensor")
+    index = _device_of(q, "q", k, v, out, lse, dout, k_shared, dq, dk, dv, dk_shared, workspace, status)
     d = attn_desc(q, k, k_shared, causal, scale)
-
-    def output(name, t, shape):
-        if t is None:
-            return torch.empty(shape, dtype=q.dtype, device=dev)
-        if tuple(t.shape) != tuple(shape) or t.stride(-1) != 1 or t.dtype != q.dtype:
-            raise ValueError(f"{name} must be {list(shape)} with a contiguous feature axis and q's dtype")
-        return t
-
-    dq = output("dq", dq, (B, S, H, D))
-    dk = output("dk", dk, k.shape)
-    dv = output("dv", dv, v.shape)
-    if k_shared is not None:
-        dk_shared = output("dk_shared", dk_shared, k_shared.shape)
-    elif dk_shared is not None:
+    B, S, H, _ = q_shape = q.shape
+    v_shape, t = v.shape, q.dtype
+    dvw = v_shape[3]
+    if k.shape[:3] != q_shape[:3] or v_shape[:3] != q_shape[:3]:
+        raise ValueError("k and v must have q's batch, sequence and heads")
+    if k_shared is not None and k_shared.shape[:2] != q_shape[:2]:
+        raise ValueError("k_shared must be [B, S, dr]")
+    if lse.shape != (B, H, S) or not lse.is_contiguous() or lse.dtype != torch.float32:
+        raise ValueError("lse must be a contiguous [B, H, S] float32 tensor")
+    for name, x in (("v", v), ("out", out), ("dout", dout)):
+        if x.shape != v_shape or x.stride(3) != 1 or x.dtype != t:
+            raise ValueError(f"{name} must be [B, S, H, d_v] with a contiguous feature axis and q's dtype")
+    if k_shared is None and dk_shared is not None:
         raise ValueError("dk_shared without k_shared")
-    g = McAttnGrad()
-    g.d_v = dvw
-    g.lse = lse.data_ptr()
-    for ptr, st, t in (("v", "v_strides", v), ("o", "o_strides", out), ("d_o", "do_strides", dout),
-                       ("dq", "dq_strides", dq), ("dk", "dk_strides", dk), ("dv", "dv_strides", dv)):
-        setattr(g, ptr, t.data_ptr())
-        getattr(g, st)[:] = t.stride()[:3]
-    if dk_shared is not None:
-        g.dk_shared = dk_shared.data_ptr()
-        g.dks_strides[:] = dk_shared.stride()[:2]
+    grads = []
+    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dk_shared", dk_shared, k_shared)):
+        if g is None and like is not None:
+            g = torch.empty(like.shape, dtype=t, device=q.device)
+        elif g is not None and (g.shape != like.shape or g.stride(-1) != 1 or g.dtype != t):
+            raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
+        grads.append(g)
+    dq, dk, dv, dk_shared = grads
     lib = abi.load()
-    with torch.cuda.device(dev):
-        if workspace is None:
-            n = ctypes.c_size_t(0)
-            check(lib.qk_attention_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)),
-                  "qk_attention_backward_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        check(lib.qk_attention_backward(ctypes.byref(d), ctypes.byref(g), _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _ptr(status),
-                                        _stream(stream)), "qk_attention_backward")
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        check(lib.qk_attention_backward_workspace_size(d, n), "qk_attention_backward_workspace_size")
+        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
+    g = McAttnGrad(v.data_ptr(), dvw, 0, v.stride()[:3], out.data_ptr(), out.stride()[:3], lse.data_ptr(),
+                   dout.data_ptr(), dout.stride()[:3], dq.data_ptr(), dq.stride()[:3], dk.data_ptr(), dk.stride()[:3],
+                   _at(dk_shared), (0, 0) if dk_shared is None else dk_shared.stride()[:2], dv.data_ptr(),
+                   dv.stride()[:3])
+    _run(lib.qk_attention_backward, "qk_attention_backward", index, stream, d, g, workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), _at(status))
     return dq, dk, dv, dk_shared
 
 
@@ -389,33 +383,37 @@ def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
     """Gradient of rope_: the transposed rotation of dy [B, S, d] or
     [B, S, heads, d] (unit stride along d), positions 0..S-1.  Returns `out`, a
     new tensor unless given; out=dy rotates in place."""
-    dev = _same_device(dy=dy, out=out)
-    if out is None:
-        out = torch.empty(dy.shape, dtype=dy.dtype, device=dev)
-    if dy.dim() not in (3, 4) or dy.dtype not in _DT or dy.stride(-1) != 1:
+    index = _device_of(dy, "dy", out)
+    shape, y = dy.shape, dy.stride()
+    dt = _DT.get(dy.dtype)
+    if len(shape) not in (3, 4) or dt is None or y[-1] != 1:
         raise ValueError("dy: [B, S, d] or [B, S, heads, d] with unit stride along d")
-    if out.shape != dy.shape or out.dtype != dy.dtype or out.stride(-1) != 1:
+    if out is None:
+        out = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+    x = out.stride()
+    if out.shape != shape or out.dtype != dy.dtype or x[-1] != 1:
         raise ValueError("out must have dy's shape and type and unit stride along d")
-    B, S, d = dy.shape[0], dy.shape[1], dy.shape[-1]
-    nh, yh, xh = (dy.shape[2], dy.stride(2), out.stride(2)) if dy.dim() == 4 else (1, 0, 0)
-    with torch.cuda.device(dev):
-        check(abi.load().mc_rope_backward(_ptr(dy), dy.stride(0), dy.stride(1), yh, _ptr(out), out.stride(0),
-                                          out.stride(1), xh, B, S, nh, d, _DT[dy.dtype], float(theta),
-                                          _stream(stream)), "mc_rope_backward")
+    nh, yh, xh = (shape[2], y[2], x[2]) if len(shape) == 4 else (1, 0, 0)
+    _run(abi.load().mc_rope_backward, "mc_rope_backward", index, stream, dy.data_ptr(), y[0], y[1], yh,
+         out.data_ptr(), x[0], x[1], xh, shape[0], shape[1], nh, shape[-1], dt, theta)
     return out
 
 
-def _matrix(t, name, shape, dtype):
-    """Row pitch of a given 2-D operand: `shape`, `dtype`, unit column stride."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+def _pitch(t, name, shape, dtype):
+    """Row pitch of a 2-D operand that must have this shape and type, unit
+    column stride and rows that do not overlap."""
+    if t.shape != shape or t.dtype != dtype:
         raise ValueError(f"{name} must be {list(shape)} of {dtype}")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+    ld, inner = t.stride()
+    if t.is_contiguous():
+        return shape[1]
+    if inner != 1 or ld < shape[1]:
         raise ValueError(f"{name}: expected unit column stride and rows that do not overlap")
-    return max(t.stride(0), t.shape[1])
+    return ld
 
 
 def _vector(t, name, n, dtype):
-    if t is not None and (tuple(t.shape) != (n,) or t.dtype != dtype or not t.is_contiguous()):
+    if t.shape != (n,) or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype}")
 
 
@@ -427,44 +425,46 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
     with one fp32 scale per row and 128 columns.  Returns (y, scales or None, h,
     rstd [rows] f32); h is x itself without a residual.  Outputs are allocated
     unless given; h may be x or residual (in place)."""
-    if x.dim() != 2 or x.dtype not in _DT:
+    index = _device_of(x, "x", residual, weight, h, out, scales, rstd)
+    shape, t = x.shape, x.dtype
+    dt = _DT.get(t)
+    if len(shape) != 2 or dt is None:
         raise ValueError("x: expected a 2-D bfloat16 or float32 tensor")
-    dev = _same_device(x=x, residual=residual, weight=weight, h=h, out=out, scales=scales, rstd=rstd)
-    rows, cols = x.shape
+    if out_dtype is None:
+        out_dtype = t
     f8 = out_dtype == torch.float8_e4m3fn
-    if out_dtype not in (None, x.dtype, torch.float8_e4m3fn):
-        raise ValueError(f"out_dtype: {x.dtype} or torch.float8_e4m3fn")
-    ldx = _matrix(x, "x", (rows, cols), x.dtype)
-    _vector(weight, "weight", cols, x.dtype)
-    if residual is None:
-        if h is not None:
-            raise ValueError("h without residual: h is x itself")
-        ldr = ldh = 0
-    else:
-        ldr = _matrix(residual, "residual", (rows, cols), x.dtype)
+    if out_dtype != t and not f8:
+        raise ValueError(f"out_dtype: {t} or torch.float8_e4m3fn")
+    rows, cols = shape
+    dev = x.device
+    ldx = _pitch(x, "x", shape, t)
+    if weight is not None:
+        _vector(weight, "weight", cols, t)
+    ldr = ldh = lds = 0
+    if residual is not None:
+        ldr = _pitch(residual, "residual", shape, t)
         if h is None:
-            h = torch.empty((rows, cols), dtype=x.dtype, device=dev)
-        ldh = _matrix(h, "h", (rows, cols), x.dtype)
-    y_dtype = out_dtype or x.dtype
+            h = torch.empty(shape, dtype=t, device=dev)
+        ldh = _pitch(h, "h", shape, t)
+    elif h is not None:
+        raise ValueError("h without residual: h is x itself")
     if out is None:
-        out = torch.empty((rows, cols), dtype=y_dtype, device=dev)
-    ldy = _matrix(out, "out", (rows, cols), y_dtype)
-    lds = 0
+        out = torch.empty(shape, dtype=out_dtype, device=dev)
+    ldy = _pitch(out, "out", shape, out_dtype)
     if f8:
-        tiles = -(-cols // 128)
+        tiles = (rows, -(-cols // 128))
         if scales is None:
-            scales = torch.empty((rows, tiles), dtype=torch.float32, device=dev)
-        lds = _matrix(scales, "scales", (rows, tiles), torch.float32)
+            scales = torch.empty(tiles, dtype=torch.float32, device=dev)
+        lds = _pitch(scales, "scales", tiles, torch.float32)
     elif scales is not None:
         raise ValueError("scales go with out_dtype=torch.float8_e4m3fn")
     if rstd is None:
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-    _vector(rstd, "rstd", rows, torch.float32)
-    with torch.cuda.device(dev):
-        check(abi.load().mc_add_rms_norm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), _ptr(h), ldh, _ptr(out),
-                                         ldy, _ptr(scales), lds, _ptr(rstd), rows, cols, _DT[x.dtype],
-                                         abi.MC_F8E4M3 if f8 else _DT[x.dtype], float(eps), _stream(stream)),
-              "mc_add_rms_norm")
+    else:
+        _vector(rstd, "rstd", rows, torch.float32)
+    _run(abi.load().mc_add_rms_norm, "mc_add_rms_norm", index, stream, x.data_ptr(), ldx, _at(residual), ldr,
+         _at(weight), _at(h), ldh, out.data_ptr(), ldy, _at(scales), lds, rstd.data_ptr(), rows, cols, dt,
+         abi.MC_F8E4M3 if f8 else dt, eps)
     return out, scales, (x if residual is None else h), rstd
 
 
@@ -473,34 +473,42 @@ def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None
     add_rms_norm returned them: dx (of the norm's input and of the residual
     alike; plus dres, the gradient that reaches h past the norm) and dweight
     [cols] f32.  Returns (dx, dweight); dweight is None without a weight unless
-    one is given to write.  dx may be dy, h or dres (in place)."""
-    if dy.dim() != 2 or dy.dtype not in _DT:
+    one is given to write.  dx may be dy, h or dres (in place).  workspace: a
+    CUDA tensor of rms_norm_backward_workspace_size(cols) bytes, allocated for
+    the call where a dweight needs one and none is given."""
+    index = _device_of(dy, "dy", h, rstd, weight, dres, dx, dweight, workspace)
+    shape, t = dy.shape, dy.dtype
+    dt = _DT.get(t)
+    if len(shape) != 2 or dt is None:
         raise ValueError("dy: expected a 2-D bfloat16 or float32 tensor")
-    dev = _same_device(dy=dy, h=h, rstd=rstd, weight=weight, dres=dres, dx=dx, dweight=dweight, workspace=workspace)
-    rows, cols = dy.shape
-    lddy = _matrix(dy, "dy", (rows, cols), dy.dtype)
-    ldh = _matrix(h, "h", (rows, cols), dy.dtype)
-    ldr = 0 if dres is None else _matrix(dres, "dres", (rows, cols), dy.dtype)
-    if dx is None:
-        dx = torch.empty((rows, cols), dtype=dy.dtype, device=dev)
-    lddx = _matrix(dx, "dx", (rows, cols), dy.dtype)
+    rows, cols = shape
+    lddy, ldh = _pitch(dy, "dy", shape, t), _pitch(h, "h", shape, t)
+    ldr = 0 if dres is None else _pitch(dres, "dres", shape, t)
     _vector(rstd, "rstd", rows, torch.float32)
-    _vector(weight, "weight", cols, dy.dtype)
-    if dweight is None and weight is not None:
-        dweight = torch.empty(cols, dtype=torch.float32, device=dev)
-    _vector(dweight, "dweight", cols, torch.float32)
-    lib = abi.load()
-    with torch.cuda.device(dev):
-        if dweight is not None and workspace is None:
-            n = ctypes.c_size_t(0)
-            check(lib.mc_rms_norm_backward_workspace_size(cols, ctypes.byref(n)),
-                  "mc_rms_norm_backward_workspace_size")
-            workspace = torch.empty(n.value, dtype=torch.uint8, device=dev)
-        check(lib.mc_rms_norm_backward(_ptr(dy), lddy, _ptr(h), ldh, _ptr(rstd), _ptr(weight), _ptr(dres), ldr,
-                                       _ptr(dx), lddx, _ptr(dweight), rows, cols, _DT[dy.dtype], _ptr(workspace),
-                                       0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                       _stream(stream)), "mc_rms_norm_backward")
+    if dx is None:
+        dx = torch.empty(shape, dtype=t, device=dy.device)
+    lddx = _pitch(dx, "dx", shape, t)
+    if weight is not None:
+        _vector(weight, "weight", cols, t)
+        if dweight is None:
+            dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+    nbytes = 0
+    if dweight is not None:
+        _vector(dweight, "dweight", cols, torch.float32)
+        if workspace is None:
+            workspace = torch.empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8, device=dy.device)
+        nbytes = workspace.numel() * workspace.element_size()
+    _run(abi.load().mc_rms_norm_backward, "mc_rms_norm_backward", index, stream, dy.data_ptr(), lddy, h.data_ptr(),
+         ldh, rstd.data_ptr(), _at(weight), _at(dres), ldr, dx.data_ptr(), lddx, _at(dweight), rows, cols, dt,
+         _at(workspace), nbytes)
     return dx, dweight
+
+
+def rms_norm_backward_workspace_size(cols: int) -> int:
+    """Bytes of workspace that rms_norm_backward needs for a dweight."""
+    n = ctypes.c_size_t(0)
+    check(abi.load().mc_rms_norm_backward_workspace_size(cols, n), "mc_rms_norm_backward_workspace_size")
+    return n.value
 
 
 def profiler_enable(on: bool = True):
