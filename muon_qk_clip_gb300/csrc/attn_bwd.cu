@@ -42,6 +42,11 @@ constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
+// Queries per tile of the dK / dV pass, and value stages of the dQ pass, by the
+// 64-wide chunks of q.k and d_v (tensor memory and shared memory decide).
+__host__ __device__ constexpr int query_tile(int nch) { return nch > 2 ? 96 : 128; }
+__host__ __device__ constexpr int value_stages(int nch, int ncv) { return nch + ncv > 4 ? 1 : 2; }
+
 struct Maps {
   CUtensorMap q, k, ks, v, d_o;
 };
@@ -50,7 +55,6 @@ struct Geo {
   int nch, nck, ncv;    // 64-wide chunks of q.k, of its head-specific part, of d_v
   int nb;               // 128-row blocks per (b, h)
   int nt;               // dkv: query tiles per (b, h)
-  int vst;              // dq: value stages
   int nunit;            // units per (b, h): pairs of blocks when causal
   uint32_t units;       // below 2^30 (checked on the host)
   long long sp;         // padded row length of nlse and delta
@@ -86,6 +90,18 @@ __device__ inline void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdes
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// True in one lane of the (whole) warp.  The MMA issuer runs as a whole warp
+// with the products under this predicate, so that descriptors stay in uniform
+// registers.
+__device__ inline bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
 }
 // 32 lanes x 8 columns of 32-bit values into TMEM
 __device__ inline void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
@@ -180,18 +196,19 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
 // while they turn S(t+1) into P(t+1) it runs dK(t) and dP(t+1).  The products of
 // one issuing thread execute in order, so S(t+1) follows dV(t)'s reads of P(t)
 // and dP(t+1) follows dK(t)'s reads of dS(t) without a wait.
-template <int NQ>
+template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+  constexpr int NQ = query_tile(NCH);
   constexpr int NH = NQ / 2;             // queries per compute warp
   constexpr int CQ = NQ * 128;           // bytes of one chunk of a query tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                                    // nch chunks
-  uint8_t* vbuf = kbuf + g.nch * CH;                       // ncv chunks
-  uint8_t* qbuf = vbuf + g.ncv * CH;                       // 2 x nch chunks
-  uint8_t* dobuf = qbuf + 2 * g.nch * CQ;                  // 2 x ncv chunks
-  float* rowv = reinterpret_cast<float*>(dobuf + 2 * g.ncv * CQ);   // [2 stages][nlse, delta][NQ]
+  uint8_t* vbuf = kbuf + NCH * CH;                       // ncv chunks
+  uint8_t* qbuf = vbuf + NCV * CH;                       // 2 x nch chunks
+  uint8_t* dobuf = qbuf + 2 * NCH * CQ;                  // 2 x ncv chunks
+  float* rowv = reinterpret_cast<float*>(dobuf + 2 * NCV * CQ);   // [2 stages][nlse, delta][NQ]
   uint64_t* bars = reinterpret_cast<uint64_t*>(rowv + 4 * NQ);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
@@ -225,14 +242,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
-    if (g.nch > g.nck) prefetch_tmap(&mp.ks);
+    if (NCH > g.nck) prefetch_tmap(&mp.ks);
   }
   if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * g.nch, t_s = t_dv + 64 * g.ncv, t_dp = t_s + NQ;
+  const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * NCH, t_s = t_dv + 64 * NCV, t_dp = t_s + NQ;
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   // first query tile that has a query at or behind the block's first key
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
@@ -255,25 +272,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = t & 1;
           const uint32_t ph = (t >> 1) & 1;
           if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&q_full[s], g.nch * CQ + 2 * NQ * 4);
-          for (int c = 0; c < g.nch; ++c)
-            tma_load_4d(qbuf + (s * g.nch + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
+          mbar_arrive_expect_tx(&q_full[s], NCH * CQ + 2 * NQ * 4);
+          for (int c = 0; c < NCH; ++c)
+            tma_load_4d(qbuf + (s * NCH + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
           bulk_load_1d(rowv + s * 2 * NQ, p.nlse + rowbase + it * NQ, NQ * 4, &q_full[s]);
           bulk_load_1d(rowv + s * 2 * NQ + NQ, p.delta + rowbase + it * NQ, NQ * 4, &q_full[s]);
           used_q[s] = true; par_q[s] = ph;
           if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&do_full[s], g.ncv * CQ);
-          for (int c = 0; c < g.ncv; ++c)
-            tma_load_4d(dobuf + (s * g.ncv + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
+          mbar_arrive_expect_tx(&do_full[s], NCV * CQ);
+          for (int c = 0; c < NCV; ++c)
+            tma_load_4d(dobuf + (s * NCV + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
           used_do[s] = true; par_do[s] = ph;
           if (it == t0) {        // the item's keys and values, behind its first query tile
             if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
-            mbar_arrive_expect_tx(kv_full, (g.nch + g.ncv) * CH);
-            for (int c = 0; c < g.nch; ++c) {
+            mbar_arrive_expect_tx(kv_full, (NCH + NCV) * CH);
+            for (int c = 0; c < NCH; ++c) {
               if (c < g.nck) tma_load_4d(kbuf + c * CH, &mp.k, kv_full, 64 * c, h, blk * BM, b);
               else tma_load_3d(kbuf + c * CH, &mp.ks, kv_full, 64 * (c - g.nck), blk * BM, b);
             }
-            for (int c = 0; c < g.ncv; ++c) tma_load_4d(vbuf + c * CH, &mp.v, kv_full, 64 * c, h, blk * BM, b);
+            for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + c * CH, &mp.v, kv_full, 64 * c, h, blk * BM, b);
             used_kv = true; par_kv = li & 1;
           }
         }
@@ -289,86 +306,98 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc_bf16(BM, NQ, 0, 0);
-      const uint32_t idesc_dv = make_idesc_bf16(BM, 64 * g.ncv, 0, 1);
-      const uint32_t idesc_dk = make_idesc_bf16(BM, 64 * g.nch, 0, 1);
-      const uint32_t ka = smem_u32(kbuf), va = smem_u32(vbuf);
-      uint32_t t = 0, li = 0;
-      bool issued = false;
-      auto scores = [&](uint32_t tt) {       // S^T = K Q^T
-        const uint32_t qa = smem_u32(qbuf + (tt & 1) * g.nch * CQ);
-        for (int c = 0; c < g.nch; ++c)
+    constexpr uint32_t idesc_s = make_idesc_bf16(BM, NQ, 0, 0);
+    constexpr uint32_t idesc_dv = make_idesc_bf16(BM, 64 * NCV, 0, 1);
+    constexpr uint32_t idesc_dk = make_idesc_bf16(BM, 64 * NCH, 0, 1);
+    // operand descriptors: rows of 64 features, K-major for S^T and dP^T,
+    // MN-major (16 query rows = 2048 bytes per k-step) for dV and dK
+    const uint64_t dk_ = make_sdesc_sw128(smem_u32(kbuf), 16, 1024), dv_ = make_sdesc_sw128(smem_u32(vbuf), 16, 1024);
+    const uint64_t dq_ = make_sdesc_sw128(smem_u32(qbuf), 16, 1024), ddo_ = make_sdesc_sw128(smem_u32(dobuf), 16, 1024);
+    const uint64_t mq_ = make_sdesc(smem_u32(qbuf), CQ, 1024, 2), mdo_ = make_sdesc(smem_u32(dobuf), CQ, 1024, 2);
+    uint32_t t = 0, li = 0;
+    bool issued = false;
+    auto scores = [&](uint32_t tt) {       // S^T = K Q^T
+      const uint64_t q0 = dq_ + (tt & 1) * (NCH * CQ / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma(t_s, make_sdesc_sw128(ka + c * CH + kk * 32, 16, 1024),
-                   make_sdesc_sw128(qa + c * CQ + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+            tc_mma(t_s, dk_ + (c * CH + kk * 32) / 16, q0 + (c * CQ + kk * 32) / 16, idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
         tc_commit(s_full);
-      };
-      auto dprobs = [&](uint32_t tt) {       // dP^T = V dO^T
-        const uint32_t da = smem_u32(dobuf + (tt & 1) * g.ncv * CQ);
-        for (int c = 0; c < g.ncv; ++c)
+      }
+      __syncwarp();
+    };
+    auto dprobs = [&](uint32_t tt, bool last) {       // dP^T = V dO^T
+      const uint64_t d0 = ddo_ + (tt & 1) * (NCV * CQ / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < NCV; ++c)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma(t_dp, make_sdesc_sw128(va + c * CH + kk * 32, 16, 1024),
-                   make_sdesc_sw128(da + c * CQ + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+            tc_mma(t_dp, dv_ + (c * CH + kk * 32) / 16, d0 + (c * CQ + kk * 32) / 16, idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
         tc_commit(dp_full);
-      };
-      // A (tensor memory): NQ / 16 k-steps of 8 columns; the second half of the
-      // queries starts at column NH.  B: rows of 64 features (MN-major), 16
-      // query rows = 2048 bytes per k-step.
-      auto accumulate = [&](uint32_t d, uint32_t a, uint32_t b0, uint32_t idesc, bool add) {
+        if (last) tc_commit(kv_empty);
+      }
+      __syncwarp();
+    };
+    // A (tensor memory): NQ / 16 k-steps of 8 columns; the second half of the
+    // queries starts at column NH
+    auto accumulate = [&](uint32_t d, uint32_t a, uint64_t b0, uint32_t idesc, bool add, uint64_t* done) {
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < NQ / 16; ++kk) {
           constexpr int half = NQ / 32;
-          const uint32_t ac = a + (kk < half ? kk * 8 : NH + (kk - half) * 8);
-          tc_mma_ts(d, ac, make_sdesc(b0 + kk * 2048, CQ, 1024, 2), idesc, (add || kk > 0) ? 1u : 0u);
+          tc_mma_ts(d, a + (kk < half ? kk * 8 : NH + (kk - half) * 8), b0 + kk * 128, idesc, (add || kk > 0) ? 1u : 0u);
         }
-      };
-      for (uint32_t n = 0; !abort_flag; ++n) {
-        int b, h, blk;
-        const int st = next_item(p, g, n, b, h, blk);
-        if (st < 0) break;
-        if (st == 0) continue;
-        const int nt = g.nt - first_tile(blk);
-        bool ok = mbar_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && mbar_wait(kv_full, li & 1, &abort_flag);
-        if (!ok) { fail(); break; }
-        tc_fence_after();
-        scores(t);
-        issued = true;
-        if (!mbar_wait(&do_full[t & 1], (t >> 1) & 1, &abort_flag)) { fail(); break; }
-        tc_fence_after();
-        dprobs(t);
-        if (nt == 1) tc_commit(kv_empty);
-        for (int i = 0; i < nt; ++i, ++t) {
-          const int s = t & 1, s1 = s ^ 1;
-          const uint32_t ph1 = ((t + 1) >> 1) & 1;
-          if (!mbar_wait(p_full, t & 1, &abort_flag)) { ok = false; break; }
-          if (i == 0 && !mbar_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          accumulate(t_dv, t_s, smem_u32(dobuf + s * g.ncv * CQ), idesc_dv, i > 0);
-          tc_commit(&do_empty[s]);
-          if (i + 1 < nt) {
-            if (!mbar_wait(&q_full[s1], ph1, &abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            scores(t + 1);
-          }
-          if (!mbar_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          accumulate(t_dk, t_dp, smem_u32(qbuf + s * g.nch * CQ), idesc_dk, i > 0);
-          tc_commit(&q_empty[s]);
-          if (i + 1 < nt) {
-            if (!mbar_wait(&do_full[s1], ph1, &abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            dprobs(t + 1);
-            if (i + 2 == nt) tc_commit(kv_empty);
-          }
-        }
-        if (!ok) { fail(); break; }
-        tc_commit(acc_full);
-        ++li;
+        tc_commit(done);
       }
-      if (issued) { tc_commit(drain); mbar_wait(drain, 0, nullptr); }
+      __syncwarp();
+    };
+    for (uint32_t n = 0;; ++n) {
+      int b, h, blk;
+      const int st = next_item(p, g, n, b, h, blk);
+      if (st < 0) break;
+      if (st == 0) continue;
+      const int nt = g.nt - first_tile(blk);
+      bool ok = warp_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && warp_wait(kv_full, li & 1, &abort_flag);
+      if (!ok) { fail(); break; }
+      tc_fence_after();
+      scores(t);
+      issued = true;
+      if (!warp_wait(&do_full[t & 1], (t >> 1) & 1, &abort_flag)) { fail(); break; }
+      tc_fence_after();
+      dprobs(t, nt == 1);
+      for (int i = 0; i < nt; ++i, ++t) {
+        const int s = t & 1, s1 = s ^ 1;
+        const uint32_t ph1 = ((t + 1) >> 1) & 1;
+        if (!warp_wait(p_full, t & 1, &abort_flag)) { ok = false; break; }
+        if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        accumulate(t_dv, t_s, mdo_ + s * (NCV * CQ / 16), idesc_dv, i > 0, &do_empty[s]);
+        if (i + 1 < nt) {
+          if (!warp_wait(&q_full[s1], ph1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          scores(t + 1);
+        }
+        if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        accumulate(t_dk, t_dp, mq_ + s * (NCH * CQ / 16), idesc_dk, i > 0, &q_empty[s]);
+        if (i + 1 < nt) {
+          if (!warp_wait(&do_full[s1], ph1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          dprobs(t + 1, i + 2 == nt);
+        }
+      }
+      if (!ok) { fail(); break; }
+      if (elect_one()) tc_commit(acc_full);
+      __syncwarp();
+      ++li;
+    }
+    if (issued) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, nullptr);
     }
   } else {
     // ------------------------------------------------------------ P, dS, epilogue
@@ -470,9 +499,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + j * p.dvs[1] + h * p.dvs[2];
       __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + j * p.dks[1] + h * p.dks[2];
       float* part = p.part + (((long long)b * p.H + h) * p.S + j) * p.d_shared;
-      for (int c = 0; c < 2 * g.ncv + 2 * g.nch; ++c) {
-        const bool is_v = c < 2 * g.ncv;
-        const int col = is_v ? hf * 32 * g.ncv + c * 16 : hf * 32 * g.nch + (c - 2 * g.ncv) * 16;
+      for (int c = 0; c < 2 * NCV + 2 * NCH; ++c) {
+        const bool is_v = c < 2 * NCV;
+        const int col = is_v ? hf * 32 * NCV + c * 16 : hf * 32 * NCH + (c - 2 * NCV) * 16;
         uint32_t r[16];
         tmem_ld_32x32b_x16_async((is_v ? t_dv : t_dk) + lanes + col, r);
         tmem_ld_wait();
@@ -519,15 +548,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1), dQ(t).
 constexpr int BN = 128;
 
+template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+  constexpr int VST = value_stages(NCH, NCV);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;                                   // nch chunks
-  uint8_t* dobuf = qbuf + g.nch * CH;                     // ncv chunks
-  uint8_t* kbuf = dobuf + g.ncv * CH;                     // 2 x nch chunks
-  uint8_t* vbuf = kbuf + 2 * g.nch * CH;                  // vst x ncv chunks
-  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + g.vst * g.ncv * CH);
+  uint8_t* dobuf = qbuf + NCH * CH;                     // ncv chunks
+  uint8_t* kbuf = dobuf + NCV * CH;                     // 2 x nch chunks
+  uint8_t* vbuf = kbuf + 2 * NCH * CH;                  // vst x ncv chunks
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + VST * NCV * CH);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [2]
@@ -561,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
-    if (g.nch > g.nck) prefetch_tmap(&mp.ks);
+    if (NCH > g.nck) prefetch_tmap(&mp.ks);
   }
   if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
   tc_fence_before();
@@ -592,26 +623,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int s = t & 1;
           const uint32_t ph = (t >> 1) & 1;
           if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&k_full[s], g.nch * CH);
-          for (int c = 0; c < g.nch; ++c) {
-            uint8_t* dst = kbuf + (s * g.nch + c) * CH;
+          mbar_arrive_expect_tx(&k_full[s], NCH * CH);
+          for (int c = 0; c < NCH; ++c) {
+            uint8_t* dst = kbuf + (s * NCH + c) * CH;
             if (c < g.nck) tma_load_4d(dst, &mp.k, &k_full[s], 64 * c, h, it * BN, b);
             else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
           }
           used_k[s] = true; par_k[s] = ph;
           if (it == 0) {         // the item's queries, behind its first keys
             if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
-            mbar_arrive_expect_tx(q_full, (g.nch + g.ncv) * CH);
-            for (int c = 0; c < g.nch; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
-            for (int c = 0; c < g.ncv; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
+            mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
+            for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
+            for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
             used_q = true; par_q = li & 1;
           }
           if (!mbar_wait(&v_empty[vs], vph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&v_full[vs], g.ncv * CH);
-          for (int c = 0; c < g.ncv; ++c)
-            tma_load_4d(vbuf + (vs * g.ncv + c) * CH, &mp.v, &v_full[vs], 64 * c, h, it * BN, b);
+          mbar_arrive_expect_tx(&v_full[vs], NCV * CH);
+          for (int c = 0; c < NCV; ++c)
+            tma_load_4d(vbuf + (vs * NCV + c) * CH, &mp.v, &v_full[vs], 64 * c, h, it * BN, b);
           used_v[vs] = true; par_v[vs] = vph;
-          if (++vs == (uint32_t)g.vst) { vs = 0; vph ^= 1; }
+          if (++vs == (uint32_t)VST) { vs = 0; vph ^= 1; }
         }
         if (!ok) break;
         ++li;
@@ -624,71 +655,86 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = make_idesc_bf16(BM, BN, 0, 0);
-      const uint32_t idesc_dq = make_idesc_bf16(BM, 64 * g.nch, 0, 1);
-      const uint32_t qa = smem_u32(qbuf), da = smem_u32(dobuf);
-      uint32_t t = 0, li = 0, vs = 0, vph = 0;
-      bool issued = false;
-      auto product = [&](uint32_t d, uint32_t a, uint32_t b0, int nc) {
-        for (int c = 0; c < nc; ++c)
+    constexpr uint32_t idesc_s = make_idesc_bf16(BM, BN, 0, 0);
+    constexpr uint32_t idesc_dq = make_idesc_bf16(BM, 64 * NCH, 0, 1);
+    const uint64_t dq_ = make_sdesc_sw128(smem_u32(qbuf), 16, 1024), ddo_ = make_sdesc_sw128(smem_u32(dobuf), 16, 1024);
+    const uint64_t dk_ = make_sdesc_sw128(smem_u32(kbuf), 16, 1024), dv_ = make_sdesc_sw128(smem_u32(vbuf), 16, 1024);
+    const uint64_t mk_ = make_sdesc(smem_u32(kbuf), CH, 1024, 2);
+    uint32_t t = 0, li = 0, vs = 0, vph = 0;
+    bool issued = false;
+    auto scores = [&](uint32_t tt) {       // S = Q K^T
+      const uint64_t k0 = dk_ + (tt & 1) * (NCH * CH / 16);
+      if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma(d, make_sdesc_sw128(a + c * CH + kk * 32, 16, 1024),
-                   make_sdesc_sw128(b0 + c * CH + kk * 32, 16, 1024), idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
-      };
-      // dP(t) = dO V_t^T; `last`: the item's queries and gradients are free after it
-      auto dprobs = [&](bool last) -> bool {
-        if (!mbar_wait(&v_full[vs], vph, &abort_flag)) return false;
-        tc_fence_after();
-        product(t_dp, da, smem_u32(vbuf + vs * g.ncv * CH), g.ncv);
+        for (int c = 0; c < 4 * NCH; ++c)
+          tc_mma(t_s, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16, k0 + ((c >> 2) * CH + (c & 3) * 32) / 16, idesc_s, c > 0);
+        tc_commit(s_full);
+      }
+      __syncwarp();
+    };
+    // dP = dO V^T; `last`: the item's queries and gradients are free after it
+    auto dprobs = [&](bool last) -> bool {
+      if (!warp_wait(&v_full[vs], vph, &abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t v0 = dv_ + vs * (NCV * CH / 16);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 4 * NCV; ++c)
+          tc_mma(t_dp, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16, v0 + ((c >> 2) * CH + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(&v_empty[vs]);
         tc_commit(dp_full);
         if (last) tc_commit(q_empty);
-        if (++vs == (uint32_t)g.vst) { vs = 0; vph ^= 1; }
-        return true;
-      };
-      for (uint32_t n = 0; !abort_flag; ++n) {
-        int b, h, blk;
-        const int st = next_item(p, g, n, b, h, blk);
-        if (st < 0) break;
-        if (st == 0) continue;
-        const int nt = tiles(blk);
-        // S and dP of the previous item have been read: its last s_empty and
-        // ds_full were waited for below
-        bool ok = mbar_wait(q_full, li & 1, &abort_flag) && mbar_wait(&k_full[t & 1], (t >> 1) & 1, &abort_flag);
-        if (!ok) { fail(); break; }
+      }
+      __syncwarp();
+      if (++vs == (uint32_t)VST) { vs = 0; vph ^= 1; }
+      return true;
+    };
+    for (uint32_t n = 0;; ++n) {
+      int b, h, blk;
+      const int st = next_item(p, g, n, b, h, blk);
+      if (st < 0) break;
+      if (st == 0) continue;
+      const int nt = tiles(blk);
+      // S and dP of the previous item have been read: its last s_empty and
+      // ds_full were waited for below
+      bool ok = warp_wait(q_full, li & 1, &abort_flag) && warp_wait(&k_full[t & 1], (t >> 1) & 1, &abort_flag);
+      if (!ok) { fail(); break; }
+      tc_fence_after();
+      scores(t);
+      issued = true;
+      if (!dprobs(nt == 1)) { fail(); break; }
+      for (int i = 0; i < nt; ++i, ++t) {
+        const int s = t & 1, s1 = s ^ 1;
+        if (!warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
+        if (i + 1 < nt) {
+          if (!warp_wait(&k_full[s1], ((t + 1) >> 1) & 1, &abort_flag)) { ok = false; break; }
+          tc_fence_after();
+          scores(t + 1);
+        }
+        if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        product(t_s, qa, smem_u32(kbuf + (t & 1) * g.nch * CH), g.nch);
-        issued = true;
-        tc_commit(s_full);
-        if (!dprobs(nt == 1)) { fail(); break; }
-        for (int i = 0; i < nt; ++i, ++t) {
-          const int s = t & 1, s1 = s ^ 1;
-          if (!mbar_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
-          if (i + 1 < nt) {
-            if (!mbar_wait(&k_full[s1], ((t + 1) >> 1) & 1, &abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            product(t_s, qa, smem_u32(kbuf + s1 * g.nch * CH), g.nch);
-            tc_commit(s_full);
-          }
-          if (!mbar_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
-          if (i == 0 && !mbar_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t kb = smem_u32(kbuf + s * g.nch * CH);
+        if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
+        if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t k0 = mk_ + s * (NCH * CH / 16);
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
-            tc_mma_ts(t_dq, t_ds + kk * 8, make_sdesc(kb + kk * 2048, CH, 1024, 2), idesc_dq, (i > 0 || kk > 0) ? 1u : 0u);
+            tc_mma_ts(t_dq, t_ds + kk * 8, k0 + kk * 128, idesc_dq, (i > 0 || kk > 0) ? 1u : 0u);
           tc_commit(&k_empty[s]);
           tc_commit(ds_empty);
         }
-        if (!ok) { fail(); break; }
-        tc_commit(acc_full);
-        ++li;
+        __syncwarp();
       }
-      if (issued) { tc_commit(drain); mbar_wait(drain, 0, nullptr); }
+      if (!ok) { fail(); break; }
+      if (elect_one()) tc_commit(acc_full);
+      __syncwarp();
+      ++li;
+    }
+    if (issued) {
+      if (elect_one()) tc_commit(drain);
+      __syncwarp();
+      mbar_wait(drain, 0, nullptr);
     }
   } else {
     // ------------------------------------------------------------ P, dS, epilogue
@@ -768,8 +814,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int D = p.d_head + p.d_shared;
       __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
-      for (int c = 0; c < 2 * g.nch; ++c) {
-        const int col = hf * 32 * g.nch + c * 16;
+      for (int c = 0; c < 2 * NCH; ++c) {
+        const int col = hf * 32 * NCH + c * 16;
         uint32_t r[16];
         tmem_ld_32x32b_x16_async(t_dq + lanes + col, r);
         tmem_ld_wait();
@@ -851,14 +897,12 @@ bool encode(CUtensorMap* m, const void* base, int width, int H, int S, int B, co
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int query_tile(const AttnBwdParams& p) { return p.d_head + p.d_shared > 128 ? 96 : 128; }
-
 bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   g.nck = (p.d_head + 63) / 64;
   g.nch = p.d_shared > 0 ? g.nck + (p.d_shared + 63) / 64 : g.nck;
   g.ncv = (p.d_v + 63) / 64;
   g.nb = (p.S + BM - 1) / BM;
-  g.nt = (p.S + query_tile(p) - 1) / query_tile(p);
+  g.nt = (p.S + query_tile(g.nch) - 1) / query_tile(g.nch);
   g.nunit = p.causal ? (g.nb + 1) / 2 : g.nb;
   const long long units = (long long)p.B * p.H * g.nunit;
   if (units >= (1ll << 30)) { snprintf(err, errlen, "%lld work units exceed the kernel's 2^30", units); return false; }
@@ -866,17 +910,24 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   g.sp = attn_bwd_padded_rows(p.S);
   g.div_nunit = make_fastdiv((uint32_t)g.nunit);
   g.div_h = make_fastdiv((uint32_t)p.H);
-  const size_t cap = 227 * 1024 - 1024 - 256 - 64;     // alignment, barriers, static
-  g.vst = (size_t)(3 * g.nch + 3 * g.ncv) * CH <= cap ? 2 : 1;
   return true;
 }
 
-template <int NQ>
-cudaError_t launch_dkv(const AttnBwdParams& p, const Maps& mp, const Geo& g, int grid, cudaStream_t s) {
-  const size_t smem = 1024 + (size_t)(g.nch + g.ncv) * CH + 2 * (size_t)(g.nch + g.ncv) * NQ * 128 + 4 * NQ * 4 + 256;
-  cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <int NCH, int NCV>
+cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
+  constexpr int NQ = query_tile(NCH);
+  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + 2 * (size_t)(NCH + NCV) * NQ * 128 + 4 * NQ * 4 + 256;
+  constexpr size_t sq = 1024 + (size_t)(3 * NCH + (1 + value_stages(NCH, NCV)) * NCV) * CH + 256;
+  static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
+  static_assert(64 * (NCH + NCV) + 2 * NQ <= 512, "tensor memory");
+  cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
   if (e != cudaSuccess) return e;
-  dkv_kernel<NQ><<<grid, kThreads, smem, s>>>(p, mp, g);
+  dkv_kernel<NCH, NCV><<<grid, kThreads, skv, s>>>(p, kv, g);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(dq_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
+  if (e != cudaSuccess) return e;
+  dq_kernel<NCH, NCV><<<grid, kThreads, sq, s>>>(p, qm, g);
   return cudaGetLastError();
 }
 
@@ -906,7 +957,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   using namespace ab;
   Geo g;
   if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
-  const int nq = query_tile(p), D = p.d_head + p.d_shared;
+  const int nq = query_tile(g.nch), D = p.d_head + p.d_shared;
   Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (128 both)
   memset(&kv, 0, sizeof kv);
   bool ok = encode(&kv.q, p.q, D, p.H, p.S, p.B, p.qs, nq) && encode(&kv.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, BM) &&
@@ -922,13 +973,11 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int grid = (int)(g.units < (uint32_t)sms ? g.units : (uint32_t)sms);
-  e = nq == 96 ? launch_dkv<96>(p, kv, g, grid, s) : launch_dkv<128>(p, kv, g, grid, s);
-  if (e != cudaSuccess) return e;
-  const size_t smem = 1024 + (size_t)(3 * g.nch + (1 + g.vst) * g.ncv) * CH + 256;
-  e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  dq_kernel<<<grid, kThreads, smem, s>>>(p, qm, g);
-  e = cudaGetLastError();
+  using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
+  static const Launch by_chunks[3][2] = {{launch_passes<1, 1>, launch_passes<1, 2>},
+                                         {launch_passes<2, 1>, launch_passes<2, 2>},
+                                         {launch_passes<3, 1>, launch_passes<3, 2>}};
+  e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
   if (e != cudaSuccess || p.d_shared == 0) return e;
   const long long n = (long long)p.B * p.S * p.d_shared;
   const long long blocks = cdiv(n, 256);
