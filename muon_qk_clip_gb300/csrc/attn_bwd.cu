@@ -42,10 +42,11 @@ constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Queries per tile of the dK / dV pass, and value stages of the dQ pass, by the
-// 64-wide chunks of q.k and d_v (tensor memory and shared memory decide).
+// Queries per tile of the dK / dV pass and keys per tile of the dQ pass, by the
+// 64-wide chunks of q.k (tensor memory and shared memory decide).
 __host__ __device__ constexpr int query_tile(int nch) { return nch > 2 ? 96 : 128; }
-__host__ __device__ constexpr int value_stages(int nch, int ncv) { return nch + ncv > 4 ? 1 : 2; }
+__host__ __device__ constexpr int key_tile(int nch) { return nch > 2 ? 96 : 128; }
+constexpr int kKStages = 3;              // of the dQ pass; its values have one
 
 struct Maps {
   CUtensorMap q, k, ks, v, d_o;
@@ -543,28 +544,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------------- dQ
-// Tensor memory: dQ [0, 192), S, dP (128 columns each), dS (64): dS has columns
-// of its own, so S(t+1) starts as soon as S(t) has been read and dP(t+1) as soon
-// as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1), dQ(t).
-constexpr int BN = 128;
-
+// Tensor memory: dQ [0, 192), S, dP (BN columns each), dS (BN / 2): dS has
+// columns of its own, so S(t+1) starts as soon as S(t) has been read and dP(t+1)
+// as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1), dQ(t).
+// A key tile is held from S(t) to dQ(t), two products later than the next one's
+// S wants its own, so keys have three stages; values are held for one product
+// and have one.  96-key tiles leave room for three stages of 192-wide keys.
 template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
-  constexpr int VST = value_stages(NCH, NCV);
+  constexpr int BN = key_tile(NCH), NH = BN / 2;
+  constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* qbuf = smem;                                   // nch chunks
-  uint8_t* dobuf = qbuf + NCH * CH;                     // ncv chunks
-  uint8_t* kbuf = dobuf + NCV * CH;                     // 2 x nch chunks
-  uint8_t* vbuf = kbuf + 2 * NCH * CH;                  // vst x ncv chunks
-  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + VST * NCV * CH);
+  uint8_t* qbuf = smem;                                 // NCH chunks
+  uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
+  uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
+  uint8_t* vbuf = kbuf + kKStages * NCH * CK;           // NCV chunks
+  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + NCV * CK);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
-  uint64_t* k_full = bars + 2;      // [2]
-  uint64_t* k_empty = bars + 4;     // [2]
-  uint64_t* v_full = bars + 6;      // [2]
-  uint64_t* v_empty = bars + 8;     // [2]
+  uint64_t* k_full = bars + 2;      // [3]
+  uint64_t* k_empty = bars + 5;     // [3]
+  uint64_t* v_full = bars + 8;
+  uint64_t* v_empty = bars + 9;
   uint64_t* s_full = bars + 10;
   uint64_t* s_empty = bars + 11;
   uint64_t* dp_full = bars + 12;
@@ -580,10 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
-    for (int s = 0; s < 2; ++s) {
-      mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1);
-    }
+    for (int s = 0; s < kKStages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    mbar_init(v_full, 1); mbar_init(v_empty, 1);
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
     mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
@@ -609,9 +610,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t t = 0, li = 0, vs = 0, vph = 0;
-      bool used_q = false, used_k[2] = {}, used_v[2] = {};
-      uint32_t par_q = 0, par_k[2] = {}, par_v[2] = {};
+      uint32_t t = 0, li = 0, s = 0, ph = 0, loads = 0;
+      bool used_q = false, used_k[kKStages] = {};
+      uint32_t par_q = 0, par_k[kKStages] = {};
       for (uint32_t n = 0; !abort_flag; ++n) {
         int b, h, blk;
         const int st = next_item(p, g, n, b, h, blk);
@@ -620,16 +621,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nt = tiles(blk);
         bool ok = true;
         for (int it = 0; it < nt && ok; ++it, ++t) {
-          const int s = t & 1;
-          const uint32_t ph = (t >> 1) & 1;
           if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&k_full[s], NCH * CH);
+          mbar_arrive_expect_tx(&k_full[s], NCH * CK);
           for (int c = 0; c < NCH; ++c) {
-            uint8_t* dst = kbuf + (s * NCH + c) * CH;
+            uint8_t* dst = kbuf + (s * NCH + c) * CK;
             if (c < g.nck) tma_load_4d(dst, &mp.k, &k_full[s], 64 * c, h, it * BN, b);
             else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
           }
           used_k[s] = true; par_k[s] = ph;
+          if (++s == kKStages) { s = 0; ph ^= 1; }
           if (it == 0) {         // the item's queries, behind its first keys
             if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
             mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
@@ -637,21 +637,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
             used_q = true; par_q = li & 1;
           }
-          if (!mbar_wait(&v_empty[vs], vph ^ 1, &abort_flag)) { fail(); ok = false; break; }
-          mbar_arrive_expect_tx(&v_full[vs], NCV * CH);
-          for (int c = 0; c < NCV; ++c)
-            tma_load_4d(vbuf + (vs * NCV + c) * CH, &mp.v, &v_full[vs], 64 * c, h, it * BN, b);
-          used_v[vs] = true; par_v[vs] = vph;
-          if (++vs == (uint32_t)VST) { vs = 0; vph ^= 1; }
+          if (!mbar_wait(v_empty, (t & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          mbar_arrive_expect_tx(v_full, NCV * CK);
+          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + c * CK, &mp.v, v_full, 64 * c, h, it * BN, b);
+          ++loads;
         }
         if (!ok) break;
         ++li;
       }
       if (used_q) mbar_wait(q_full, par_q, nullptr);
-      for (int s = 0; s < 2; ++s) {
-        if (used_k[s]) mbar_wait(&k_full[s], par_k[s], nullptr);
-        if (used_v[s]) mbar_wait(&v_full[s], par_v[s], nullptr);
-      }
+      for (int i = 0; i < kKStages; ++i) if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
+      if (loads) mbar_wait(v_full, (loads - 1) & 1, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -659,34 +655,37 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t idesc_dq = make_idesc_bf16(BM, 64 * NCH, 0, 1);
     const uint64_t dq_ = make_sdesc_sw128(smem_u32(qbuf), 16, 1024), ddo_ = make_sdesc_sw128(smem_u32(dobuf), 16, 1024);
     const uint64_t dk_ = make_sdesc_sw128(smem_u32(kbuf), 16, 1024), dv_ = make_sdesc_sw128(smem_u32(vbuf), 16, 1024);
-    const uint64_t mk_ = make_sdesc(smem_u32(kbuf), CH, 1024, 2);
-    uint32_t t = 0, li = 0, vs = 0, vph = 0;
+    const uint64_t mk_ = make_sdesc(smem_u32(kbuf), CK, 1024, 2);
+    uint32_t t = 0, tv = 0, li = 0, ks = 0, kph = 0, kd = 0;   // tiles, value tiles, items; key stage of S and of dQ
     bool issued = false;
-    auto scores = [&](uint32_t tt) {       // S = Q K^T
-      const uint64_t k0 = dk_ + (tt & 1) * (NCH * CH / 16);
+    auto scores = [&]() -> bool {          // S = Q K^T
+      if (!warp_wait(&k_full[ks], kph, &abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t k0 = dk_ + ks * (NCH * CK / 16);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCH; ++c)
-          tc_mma(t_s, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16, k0 + ((c >> 2) * CH + (c & 3) * 32) / 16, idesc_s, c > 0);
+          tc_mma(t_s, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(s_full);
       }
       __syncwarp();
+      if (++ks == kKStages) { ks = 0; kph ^= 1; }
+      return true;
     };
     // dP = dO V^T; `last`: the item's queries and gradients are free after it
     auto dprobs = [&](bool last) -> bool {
-      if (!warp_wait(&v_full[vs], vph, &abort_flag)) return false;
+      if (!warp_wait(v_full, tv & 1, &abort_flag)) return false;
       tc_fence_after();
-      const uint64_t v0 = dv_ + vs * (NCV * CH / 16);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCV; ++c)
-          tc_mma(t_dp, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16, v0 + ((c >> 2) * CH + (c & 3) * 32) / 16, idesc_s, c > 0);
-        tc_commit(&v_empty[vs]);
+          tc_mma(t_dp, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16, dv_ + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+        tc_commit(v_empty);
         tc_commit(dp_full);
         if (last) tc_commit(q_empty);
       }
       __syncwarp();
-      if (++vs == (uint32_t)VST) { vs = 0; vph ^= 1; }
+      ++tv;
       return true;
     };
     for (uint32_t n = 0;; ++n) {
@@ -697,34 +696,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nt = tiles(blk);
       // S and dP of the previous item have been read: its last s_empty and
       // ds_full were waited for below
-      bool ok = warp_wait(q_full, li & 1, &abort_flag) && warp_wait(&k_full[t & 1], (t >> 1) & 1, &abort_flag);
+      bool ok = warp_wait(q_full, li & 1, &abort_flag) && scores();
       if (!ok) { fail(); break; }
-      tc_fence_after();
-      scores(t);
       issued = true;
       if (!dprobs(nt == 1)) { fail(); break; }
       for (int i = 0; i < nt; ++i, ++t) {
-        const int s = t & 1, s1 = s ^ 1;
         if (!warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
-        if (i + 1 < nt) {
-          if (!warp_wait(&k_full[s1], ((t + 1) >> 1) & 1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          scores(t + 1);
-        }
+        if (i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
         if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
         if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        const uint64_t k0 = mk_ + s * (NCH * CH / 16);
+        const uint64_t k0 = mk_ + kd * (NCH * CK / 16);
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BN / 16; ++kk)
             tc_mma_ts(t_dq, t_ds + kk * 8, k0 + kk * 128, idesc_dq, (i > 0 || kk > 0) ? 1u : 0u);
-          tc_commit(&k_empty[s]);
+          tc_commit(&k_empty[kd]);
           tc_commit(ds_empty);
         }
         __syncwarp();
+        if (++kd == kKStages) kd = 0;
       }
       if (!ok) { fail(); break; }
       if (elect_one()) tc_commit(acc_full);
@@ -741,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, hf = (warp - 2) >> 2;
     const int row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t ts = t_s + lanes + hf * 64, tdp = t_dp + lanes + hf * 64, tds = t_ds + lanes + hf * 32;
+    const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tds = t_ds + lanes + hf * (NH / 2);
     const float c2 = p.scale * kLog2e;
     uint32_t t = 0, li = 0;
     bool bad = false;
@@ -756,49 +749,49 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float nl = p.nlse[at], dl = p.delta[at];
       bool ok = true;
       for (int it = 0; it < nt; ++it, ++t) {
-        const int j0 = it * BN + hf * 64;
-        const bool full = j0 + 63 < p.S && (!p.causal || j0 + 63 <= blk * BM + q * 32);
+        const int j0 = it * BN + hf * NH;
+        const bool full = j0 + NH <= p.S && (!p.causal || j0 + NH - 1 <= blk * BM + q * 32);
         ok = warp_wait(s_full, t & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        float pv[64];
+        float pv[NH];
         {
-          uint32_t r[4][16];
+          uint32_t r[NH / 16][16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x16_async(ts + c * 16, r[c]);
+          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(ts + c * 16, r[c]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
+          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(s_empty);
 #pragma unroll
-          for (int x = 0; x < 64; ++x) pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, nl));
+          for (int x = 0; x < NH; ++x) pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, nl));
         }
         ok = warp_wait(dp_full, t & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
         {
-          uint32_t r[4][16];
+          uint32_t r[NH / 16][16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x16_async(tdp + c * 16, r[c]);
+          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(tdp + c * 16, r[c]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence16(r[c]);
+          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
 #pragma unroll
-          for (int x = 0; x < 64; ++x) pv[x] *= __uint_as_float(r[x / 16][x % 16]) - dl;
+          for (int x = 0; x < NH; ++x) pv[x] *= __uint_as_float(r[x / 16][x % 16]) - dl;
         }
         if (!full) {
           const int lim = p.causal ? min(i, p.S - 1) : p.S - 1;   // last key of this row
 #pragma unroll
-          for (int x = 0; x < 64; ++x)
+          for (int x = 0; x < NH; ++x)
             if (j0 + x > lim) pv[x] = 0.f;
         }
         ok = warp_wait(ds_empty, (t & 1) ^ 1, &abort_flag);      // dQ(t-1) has read dS(t-1)
         if (!ok) break;
         tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < NH / 16; ++c) {
           uint32_t pk[8];
 #pragma unroll
           for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
@@ -917,9 +910,9 @@ template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr int NQ = query_tile(NCH);
   constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + 2 * (size_t)(NCH + NCV) * NQ * 128 + 4 * NQ * 4 + 256;
-  constexpr size_t sq = 1024 + (size_t)(3 * NCH + (1 + value_stages(NCH, NCV)) * NCV) * CH + 256;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kKStages * NCH + NCV) * key_tile(NCH) * 128 + 256;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
-  static_assert(64 * (NCH + NCV) + 2 * NQ <= 512, "tensor memory");
+  static_assert(64 * (NCH + NCV) + 2 * NQ <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
   if (e != cudaSuccess) return e;
   dkv_kernel<NCH, NCV><<<grid, kThreads, skv, s>>>(p, kv, g);
@@ -958,13 +951,17 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   Geo g;
   if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
   const int nq = query_tile(g.nch), D = p.d_head + p.d_shared;
-  Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (128 both)
+  const int nk = key_tile(g.nch);
+  Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (nk-row keys, 128-row queries)
   memset(&kv, 0, sizeof kv);
   bool ok = encode(&kv.q, p.q, D, p.H, p.S, p.B, p.qs, nq) && encode(&kv.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, BM) &&
             encode(&kv.v, p.v, p.d_v, p.H, p.S, p.B, p.vs, BM) && encode(&kv.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, nq) &&
             (p.d_shared == 0 || encode(&kv.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, BM));
   qm = kv;
   ok = ok && encode(&qm.q, p.q, D, p.H, p.S, p.B, p.qs, BM) && encode(&qm.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, BM);
+  if (nk != BM)
+    ok = ok && encode(&qm.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, nk) && encode(&qm.v, p.v, p.d_v, p.H, p.S, p.B, p.vs, nk) &&
+         (p.d_shared == 0 || encode(&qm.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, nk));
   if (!ok) { snprintf(err, errlen, "tensor map encoding failed"); return cudaErrorInvalidValue; }
   const int sms = sm_count();
   const long long rows = (long long)p.B * g.sp * p.H;
