@@ -42,11 +42,19 @@ constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk 
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Queries per tile of the dK / dV pass and keys per tile of the dQ pass, by the
-// 64-wide chunks of q.k (tensor memory and shared memory decide).
-__host__ __device__ constexpr int query_tile(int nch) { return nch > 2 ? 96 : 128; }
+// Tiles of the dK / dV pass by the 64-wide chunks of q.k and d_v.  Tensor memory
+// has 512 columns: dK and dV take 64 (nch + ncv), S^T and dP^T one per query of
+// the tile, P^T (bf16 pairs) half of one.  Up to three chunks P^T has columns of
+// its own beside 128-query tiles; with more it is written over S^T: 128 queries
+// then still fit four chunks, 96 five.  (With P^T apart and 96 / 64 queries those
+// ran at 470 / 704 us for their pass on dense_block / k2_mla_layer: the smaller
+// the tile, the more often the tensor core re-reads K and V from shared memory.)
+__host__ __device__ constexpr bool p_apart(int nch, int ncv) { return nch + ncv < 4; }
+__host__ __device__ constexpr int query_tile(int nch, int ncv) { return nch + ncv > 4 ? 96 : 128; }
+__host__ __device__ constexpr int query_stages(int nch, int ncv) { return p_apart(nch, ncv) ? 3 : 2; }
+// Keys per tile of the dQ pass: three stages of 192-wide keys fit with 96.
 __host__ __device__ constexpr int key_tile(int nch) { return nch > 2 ? 96 : 128; }
-constexpr int kKStages = 3;              // of the dQ pass; its values have one
+constexpr int kStages = 3;               // key tiles of the dQ pass (its values have one)
 
 struct Maps {
   CUtensorMap q, k, ks, v, d_o;
@@ -103,6 +111,24 @@ __device__ inline bool elect_one() {
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(p));
   return p != 0;
+}
+// 16 lanes x 16 columns: thread t receives, for n = 0, 1, rows t / 4 (r[4n],
+// r[4n + 1]) and t / 4 + 8 (r[4n + 2], r[4n + 3]) of columns 8n + 2 (t % 4) and
+// the next.  Issue only, like tmem_ld_32x32b_x16_async.
+__device__ inline void tmem_ld_16x256b_x2_async(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ inline void reg_fence8(uint32_t (&r)[8]) {
+  asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]));
+}
+// 16 lanes x 8 columns: thread t gives, for n = 0, 1, rows t / 4 (r[2n]) and
+// t / 4 + 8 (r[2n + 1]) of column 4n + t % 4.
+__device__ inline void tmem_st_16x128b_x2(uint32_t taddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r0), "r"(r1), "r"(r2),
+               "r"(r3)
+               : "memory");
 }
 // 32 lanes x 8 columns of 32-bit values into TMEM
 __device__ inline void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
@@ -186,56 +212,68 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
 }
 
 // ------------------------------------------------------------------ dK, dV
-// Tensor memory: dK [0, 64 nch), dV [.., + 64 ncv), then S^T and dP^T of NQ
-// columns each: 128 + 128 + 2 * 128 with q.k lengths up to 128, 192 + 128 +
-// 2 * 96 above, hence the 96-query tile there.  P^T / dS^T (bf16) take the
-// first half of each half of the columns of S^T / dP^T, so no warp overwrites
-// columns that the other warp of its lanes still has to read.
+// dS^T (bf16) is written over dP^T, into the first half of each half of its
+// columns, so no warp overwrites columns that the other warp of its lanes still
+// has to read; P^T lies over S^T in the same way where it has no columns of its
+// own.
 //
-// The issue order per query tile t is dV(t), S(t+1), dK(t), dP(t+1): while the
-// compute warps turn dP(t) into dS(t) the tensor core runs dV(t) and S(t+1),
-// while they turn S(t+1) into P(t+1) it runs dK(t) and dP(t+1).  The products of
-// one issuing thread execute in order, so S(t+1) follows dV(t)'s reads of P(t)
-// and dP(t+1) follows dK(t)'s reads of dS(t) without a wait.
+// Per query tile t the tensor core gets dV(t), S(t+1), dK(t), dP(t+1) (S(t+1)
+// before dV(t) where P^T is apart: then S(t) need only have been read).  It runs
+// the first two while the compute warps turn dP(t) into dS(t), the others while
+// they turn S(t+1) into P(t+1).  The products of one issuing thread execute in
+// order, so S(t+1) follows dV(t)'s reads of P(t), and dP(t+1) dK(t)'s of dS(t),
+// without a wait.
+//
+// The compute warps read S^T and dP^T in the 16 x 256-bit shape (a thread: 4 keys
+// x a quarter of the queries): a row value per query then takes 8 bytes per two
+// queries and thread from shared memory; with a key's whole row per thread every
+// one of these loads was a 16-byte broadcast, 512 bytes of return bandwidth for
+// each four queries of each warp, next to the operand reads of the tensor core.
 template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dkv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
-  constexpr int NQ = query_tile(NCH);
+  constexpr int NQ = query_tile(NCH, NCV);
+  constexpr bool APART = p_apart(NCH, NCV);
+  constexpr int kStages = query_stages(NCH, NCV);
   constexpr int NH = NQ / 2;             // queries per compute warp
+  constexpr int NU = NH / 16;            // in units of 16
   constexpr int CQ = NQ * 128;           // bytes of one chunk of a query tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* kbuf = smem;                                    // nch chunks
-  uint8_t* vbuf = kbuf + NCH * CH;                       // ncv chunks
-  uint8_t* qbuf = vbuf + NCV * CH;                       // 2 x nch chunks
-  uint8_t* dobuf = qbuf + 2 * NCH * CQ;                  // 2 x ncv chunks
-  float* rowv = reinterpret_cast<float*>(dobuf + 2 * NCV * CQ);   // [2 stages][nlse, delta][NQ]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(rowv + 4 * NQ);
+  uint8_t* kbuf = smem;                                    // NCH chunks
+  uint8_t* vbuf = kbuf + NCH * CH;                         // NCV chunks
+  uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
+  uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
+  float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, delta][NQ]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(rowv + kStages * 2 * NQ);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
-  uint64_t* q_full = bars + 2;      // [2] Q tile with its nlse and delta
-  uint64_t* q_empty = bars + 4;     // [2]
-  uint64_t* do_full = bars + 6;     // [2]
-  uint64_t* do_empty = bars + 8;    // [2]
-  uint64_t* s_full = bars + 10;
-  uint64_t* p_full = bars + 11;
-  uint64_t* dp_full = bars + 12;
-  uint64_t* ds_full = bars + 13;
-  uint64_t* acc_full = bars + 14;
-  uint64_t* acc_empty = bars + 15;
-  uint64_t* drain = bars + 16;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 17);
+  uint64_t* q_full = bars + 2;      // [stages <= 3] Q tile with its nlse and delta
+  uint64_t* q_empty = bars + 5;     // [3]
+  uint64_t* do_full = bars + 8;     // [3]
+  uint64_t* do_empty = bars + 11;   // [3]
+  uint64_t* s_full = bars + 14;
+  uint64_t* s_empty = bars + 15;
+  uint64_t* p_full = bars + 16;
+  uint64_t* p_empty = bars + 17;
+  uint64_t* dp_full = bars + 18;
+  uint64_t* ds_full = bars + 19;
+  uint64_t* acc_full = bars + 20;
+  uint64_t* acc_empty = bars + 21;
+  uint64_t* drain = bars + 22;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1);
       mbar_init(&do_full[s], 1); mbar_init(&do_empty[s], 1);
     }
-    mbar_init(s_full, 1); mbar_init(p_full, 8);
+    mbar_init(s_full, 1); mbar_init(s_empty, 8);
+    mbar_init(p_full, 8); mbar_init(p_empty, 1);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8);
     mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
     mbar_init(drain, 1);
@@ -250,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * NCH, t_s = t_dv + 64 * NCV, t_dp = t_s + NQ;
+  const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * NCH, t_s = t_dv + 64 * NCV, t_dp = t_s + NQ, t_p = APART ? t_dp + NQ : t_s;
+  constexpr uint32_t kHalfP = APART ? NH / 2 : NH;       // second half of the queries in P^T
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   // first query tile that has a query at or behind the block's first key
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
@@ -258,9 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t t = 0, li = 0;
-      bool used_kv = false, used_q[2] = {}, used_do[2] = {};
-      uint32_t par_kv = 0, par_q[2] = {}, par_do[2] = {};
+      uint32_t li = 0, s = 0, ph = 0;
+      bool used_kv = false, used_q[kStages] = {}, used_do[kStages] = {};
+      uint32_t par_kv = 0, par_q[kStages] = {}, par_do[kStages] = {};
       for (uint32_t n = 0; !abort_flag; ++n) {
         int b, h, blk;
         const int st = next_item(p, g, n, b, h, blk);
@@ -269,9 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t0 = first_tile(blk);
         const long long rowbase = ((long long)b * p.H + h) * g.sp;
         bool ok = true;
-        for (int it = t0; it < g.nt && ok; ++it, ++t) {
-          const int s = t & 1;
-          const uint32_t ph = (t >> 1) & 1;
+        for (int it = t0; it < g.nt; ++it) {
           if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
           mbar_arrive_expect_tx(&q_full[s], NCH * CQ + 2 * NQ * 4);
           for (int c = 0; c < NCH; ++c)
@@ -284,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < NCV; ++c)
             tma_load_4d(dobuf + (s * NCV + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
           used_do[s] = true; par_do[s] = ph;
+          if (++s == kStages) { s = 0; ph ^= 1; }
           if (it == t0) {        // the item's keys and values, behind its first query tile
             if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
             mbar_arrive_expect_tx(kv_full, (NCH + NCV) * CH);
@@ -300,9 +338,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every issued copy must have landed before the CTA may exit
       if (used_kv) mbar_wait(kv_full, par_kv, nullptr);
-      for (int s = 0; s < 2; ++s) {
-        if (used_q[s]) mbar_wait(&q_full[s], par_q[s], nullptr);
-        if (used_do[s]) mbar_wait(&do_full[s], par_do[s], nullptr);
+      for (int i = 0; i < kStages; ++i) {
+        if (used_q[i]) mbar_wait(&q_full[i], par_q[i], nullptr);
+        if (used_do[i]) mbar_wait(&do_full[i], par_do[i], nullptr);
       }
     }
   } else if (warp == 1) {
@@ -316,42 +354,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq_ = make_sdesc_sw128(smem_u32(qbuf), 16, 1024), ddo_ = make_sdesc_sw128(smem_u32(dobuf), 16, 1024);
     const uint64_t mq_ = make_sdesc(smem_u32(qbuf), CQ, 1024, 2), mdo_ = make_sdesc(smem_u32(dobuf), CQ, 1024, 2);
     uint32_t t = 0, li = 0;
+    // stages: of the next S, the next dP, and the tile whose dV and dK come next
+    uint32_t ss = 0, sph = 0, sp = 0, pph = 0, sd = 0;
     bool issued = false;
-    auto scores = [&](uint32_t tt) {       // S^T = K Q^T
-      const uint64_t q0 = dq_ + (tt & 1) * (NCH * CQ / 16);
+    auto scores = [&]() -> bool {          // S^T = K Q^T
+      if (!warp_wait(&q_full[ss], sph, &abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t q0 = dq_ + ss * (NCH * CQ / 16);
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < NCH; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma(t_s, dk_ + (c * CH + kk * 32) / 16, q0 + (c * CQ + kk * 32) / 16, idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+        for (int c = 0; c < 4 * NCH; ++c)
+          tc_mma(t_s, dk_ + ((c >> 2) * CH + (c & 3) * 32) / 16, q0 + ((c >> 2) * CQ + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(s_full);
       }
       __syncwarp();
+      if (++ss == kStages) { ss = 0; sph ^= 1; }
+      return true;
     };
-    auto dprobs = [&](uint32_t tt, bool last) {       // dP^T = V dO^T
-      const uint64_t d0 = ddo_ + (tt & 1) * (NCV * CQ / 16);
+    auto dprobs = [&](bool last) -> bool { // dP^T = V dO^T; `last`: keys and values are free after it
+      if (!warp_wait(&do_full[sp], pph, &abort_flag)) return false;
+      tc_fence_after();
+      const uint64_t d0 = ddo_ + sp * (NCV * CQ / 16);
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < NCV; ++c)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma(t_dp, dv_ + (c * CH + kk * 32) / 16, d0 + (c * CQ + kk * 32) / 16, idesc_s, (c > 0 || kk > 0) ? 1u : 0u);
+        for (int c = 0; c < 4 * NCV; ++c)
+          tc_mma(t_dp, dv_ + ((c >> 2) * CH + (c & 3) * 32) / 16, d0 + ((c >> 2) * CQ + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(dp_full);
         if (last) tc_commit(kv_empty);
       }
       __syncwarp();
+      if (++sp == kStages) { sp = 0; pph ^= 1; }
+      return true;
     };
     // A (tensor memory): NQ / 16 k-steps of 8 columns; the second half of the
-    // queries starts at column NH
-    auto accumulate = [&](uint32_t d, uint32_t a, uint64_t b0, uint32_t idesc, bool add, uint64_t* done) {
+    // queries starts at column a + `half`
+    auto accumulate = [&](uint32_t d, uint32_t a, int half, uint64_t b0, uint32_t idesc, bool add, uint64_t* done,
+                          uint64_t* done2) {
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < NQ / 16; ++kk) {
-          constexpr int half = NQ / 32;
-          tc_mma_ts(d, a + (kk < half ? kk * 8 : NH + (kk - half) * 8), b0 + kk * 128, idesc, (add || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 0; kk < NQ / 16; ++kk)
+          tc_mma_ts(d, a + (kk < NU ? kk * 8 : half + (kk - NU) * 8), b0 + kk * 128, idesc, (add || kk > 0) ? 1u : 0u);
         tc_commit(done);
+        if (done2) tc_commit(done2);
       }
       __syncwarp();
     };
@@ -361,34 +405,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (st < 0) break;
       if (st == 0) continue;
       const int nt = g.nt - first_tile(blk);
-      bool ok = warp_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && warp_wait(kv_full, li & 1, &abort_flag);
+      // S and dP of the previous item have been read: its last p_full and
+      // ds_full were waited for below
+      bool ok = warp_wait(kv_full, li & 1, &abort_flag) && scores();
       if (!ok) { fail(); break; }
-      tc_fence_after();
-      scores(t);
       issued = true;
-      if (!warp_wait(&do_full[t & 1], (t >> 1) & 1, &abort_flag)) { fail(); break; }
-      tc_fence_after();
-      dprobs(t, nt == 1);
+      if (!dprobs(nt == 1)) { fail(); break; }
       for (int i = 0; i < nt; ++i, ++t) {
-        const int s = t & 1, s1 = s ^ 1;
-        const uint32_t ph1 = ((t + 1) >> 1) & 1;
+        if (APART && !warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
+        if (APART && i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(p_full, t & 1, &abort_flag)) { ok = false; break; }
         if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        accumulate(t_dv, t_s, mdo_ + s * (NCV * CQ / 16), idesc_dv, i > 0, &do_empty[s]);
-        if (i + 1 < nt) {
-          if (!warp_wait(&q_full[s1], ph1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          scores(t + 1);
-        }
+        accumulate(t_dv, t_p, kHalfP, mdo_ + sd * (NCV * CQ / 16), idesc_dv, i > 0, &do_empty[sd], APART ? p_empty : nullptr);
+        if (!APART && i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        accumulate(t_dk, t_dp, mq_ + s * (NCH * CQ / 16), idesc_dk, i > 0, &q_empty[s]);
-        if (i + 1 < nt) {
-          if (!warp_wait(&do_full[s1], ph1, &abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          dprobs(t + 1, i + 2 == nt);
-        }
+        accumulate(t_dk, t_dp, NH, mq_ + sd * (NCH * CQ / 16), idesc_dk, i > 0, &q_empty[sd], nullptr);
+        if (++sd == kStages) sd = 0;
+        if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
       }
       if (!ok) { fail(); break; }
       if (elect_one()) tc_commit(acc_full);
@@ -404,57 +439,85 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ P, dS, epilogue
     // Warp e = warp - 2: keys 32 q .. 32 q + 31 of the block (q = warp & 3, its
     // TMEM lane quadrant), queries of half e >> 2 of the tile; in the epilogue
-    // that half of the dK and dV columns.
+    // that half of the dK and dV columns.  A thread holds keys r0, r0 + 8,
+    // r0 + 16, r0 + 24 and, of each 8 queries, the two from c0.
     const int q = warp & 3, hf = (warp - 2) >> 2;
-    const int row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH;
+    const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tp = t_p + lanes + hf * kHalfP;
+    const int r0 = lane >> 2, c0 = 2 * (lane & 3);
     const float c2 = p.scale * kLog2e;
-    uint32_t t = 0, li = 0;
+    uint32_t t = 0, li = 0, s = 0, sph = 0;
     bool bad = false;
     for (uint32_t n = 0;; ++n) {
       int b, h, blk;
       const int st = next_item(p, g, n, b, h, blk);
       if (st < 0) break;
       if (st == 0) continue;
-      const int j = blk * BM + row;                     // this thread's key
       bool ok = true;
       for (int it = first_tile(blk); it < g.nt; ++it, ++t) {
-        const float* nl = rowv + (t & 1) * 2 * NQ + hf * NH;
+        const float* nl = rowv + s * 2 * NQ + hf * NH + c0;
         const int i0 = it * NQ + hf * NH;
-        const bool diag = p.causal && i0 < blk * BM + q * 32 + 31;   // some (i, j) of the warp has i < j
-        ok = warp_wait(&q_full[t & 1], (t >> 1) & 1, &abort_flag) && warp_wait(s_full, t & 1, &abort_flag);
+        const int key0 = blk * BM + q * 32;
+        const bool diag = p.causal && i0 < key0 + 31;    // some (i, j) of the warp has i < j
+        ok = warp_wait(&q_full[s], sph, &abort_flag) && warp_wait(s_full, t & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        float pv[NH];
+        float pv[NU][2][8];              // [unit][16-key half][register of the 16 x 256-bit shape]
         {
-          uint32_t r[NH / 16][16];
+          uint32_t r[NU][2][8];
 #pragma unroll
-          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(ts + c * 16, r[c]);
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) tmem_ld_16x256b_x2_async(ts + ((uint32_t)(16 * hh) << 16) + u * 16, r[u][hh]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
+          for (int u = 0; u < NU; ++u)
 #pragma unroll
-          for (int x = 0; x < NH; x += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(nl + x);
-            pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, l.x));
-            pv[x + 1] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 1]), c2, l.y));
-            pv[x + 2] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 2]), c2, l.z));
-            pv[x + 3] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16 + 3]), c2, l.w));
+            for (int hh = 0; hh < 2; ++hh) reg_fence8(r[u][hh]);
+          if (APART) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_empty);
           }
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float2 l = *reinterpret_cast<const float2*>(nl + u * 16 + m * 8);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                  pv[u][hh][4 * m + x] = ex2_approx(fmaf(__uint_as_float(r[u][hh][4 * m + x]), c2, l.x));
+                  pv[u][hh][4 * m + x + 1] = ex2_approx(fmaf(__uint_as_float(r[u][hh][4 * m + x + 1]), c2, l.y));
+                }
+            }
         }
         if (diag) {
+          // register x of unit u, half hh: query i0 + 16 u + 8 (x / 4) + c0 + x % 2,
+          // key key0 + 16 hh + 8 (x / 2 % 2) + r0
+          const int d = i0 + c0 - key0 - r0;
 #pragma unroll
-          for (int x = 0; x < NH; ++x)
-            if (i0 + x < j) pv[x] = 0.f;
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                if (d + 16 * u + 8 * (x / 4) + x % 2 - 16 * hh - 8 * (x / 2 % 2) < 0) pv[u][hh][x] = 0.f;
+        }
+        if (APART) {
+          ok = warp_wait(p_empty, (t & 1) ^ 1, &abort_flag);     // dV(t-1) has read P(t-1)
+          if (!ok) break;
+          tc_fence_after();
         }
 #pragma unroll
-        for (int c = 0; c < NH / 16; ++c) {
-          uint32_t pk[8];
+        for (int u = 0; u < NU; ++u)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
-          tmem_st_32x32b_x8(ts + c * 8, pk);
-        }
+          for (int hh = 0; hh < 2; ++hh) {
+            const float* v = pv[u][hh];
+            tmem_st_16x128b_x2(tp + ((uint32_t)(16 * hh) << 16) + u * 8, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+          }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -464,36 +527,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         {
-          uint32_t r[NH / 16][16];
+          uint32_t r[NU][2][8];
 #pragma unroll
-          for (int c = 0; c < NH / 16; ++c) tmem_ld_32x32b_x16_async(tdp + c * 16, r[c]);
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh) tmem_ld_16x256b_x2_async(tdp + ((uint32_t)(16 * hh) << 16) + u * 16, r[u][hh]);
           tmem_ld_wait();
 #pragma unroll
-          for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
+          for (int u = 0; u < NU; ++u)
 #pragma unroll
-          for (int x = 0; x < NH; x += 4) {
-            const float4 d = *reinterpret_cast<const float4*>(nl + NQ + x);
-            pv[x] *= __uint_as_float(r[x / 16][x % 16]) - d.x;
-            pv[x + 1] *= __uint_as_float(r[x / 16][x % 16 + 1]) - d.y;
-            pv[x + 2] *= __uint_as_float(r[x / 16][x % 16 + 2]) - d.z;
-            pv[x + 3] *= __uint_as_float(r[x / 16][x % 16 + 3]) - d.w;
+            for (int hh = 0; hh < 2; ++hh) reg_fence8(r[u][hh]);
+#pragma unroll
+          for (int u = 0; u < NU; ++u)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              const float2 d = *reinterpret_cast<const float2*>(nl + NQ + u * 16 + m * 8);
+#pragma unroll
+              for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int x = 0; x < 4; x += 2) {
+                  pv[u][hh][4 * m + x] *= __uint_as_float(r[u][hh][4 * m + x]) - d.x;
+                  pv[u][hh][4 * m + x + 1] *= __uint_as_float(r[u][hh][4 * m + x + 1]) - d.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int hh = 0; hh < 2; ++hh) {
+            const float* v = pv[u][hh];
+            tmem_st_16x128b_x2(tdp + ((uint32_t)(16 * hh) << 16) + u * 8, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                               pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
           }
-        }
-#pragma unroll
-        for (int c = 0; c < NH / 16; ++c) {
-          uint32_t pk[8];
-#pragma unroll
-          for (int x = 0; x < 8; ++x) pk[x] = pack_bf16(pv[c * 16 + 2 * x], pv[c * 16 + 2 * x + 1]);
-          tmem_st_32x32b_x8(tdp + c * 8, pk);
-        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
+        if (++s == kStages) { s = 0; sph ^= 1; }
       }
       if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
       if (!ok) { if (lane == 0) fail(); break; }
       tc_fence_after();
+      const int j = blk * BM + q * 32 + lane;            // the epilogue's thread: one key
       // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
       // per-head fp32 partial sums
       const bool live = j < p.S;
@@ -560,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qbuf = smem;                                 // NCH chunks
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
-  uint8_t* vbuf = kbuf + kKStages * NCH * CK;           // NCV chunks
+  uint8_t* vbuf = kbuf + kStages * NCH * CK;           // NCV chunks
   uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + NCV * CK);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
@@ -583,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
-    for (int s = 0; s < kKStages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
+    for (int s = 0; s < kStages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
     mbar_init(v_full, 1); mbar_init(v_empty, 1);
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
@@ -611,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t t = 0, li = 0, s = 0, ph = 0, loads = 0;
-      bool used_q = false, used_k[kKStages] = {};
-      uint32_t par_q = 0, par_k[kKStages] = {};
+      bool used_q = false, used_k[kStages] = {};
+      uint32_t par_q = 0, par_k[kStages] = {};
       for (uint32_t n = 0; !abort_flag; ++n) {
         int b, h, blk;
         const int st = next_item(p, g, n, b, h, blk);
@@ -629,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
           }
           used_k[s] = true; par_k[s] = ph;
-          if (++s == kKStages) { s = 0; ph ^= 1; }
+          if (++s == kStages) { s = 0; ph ^= 1; }
           if (it == 0) {         // the item's queries, behind its first keys
             if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
             mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
@@ -646,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++li;
       }
       if (used_q) mbar_wait(q_full, par_q, nullptr);
-      for (int i = 0; i < kKStages; ++i) if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
+      for (int i = 0; i < kStages; ++i) if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
       if (loads) mbar_wait(v_full, (loads - 1) & 1, nullptr);
     }
   } else if (warp == 1) {
@@ -669,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_commit(s_full);
       }
       __syncwarp();
-      if (++ks == kKStages) { ks = 0; kph ^= 1; }
+      if (++ks == kStages) { ks = 0; kph ^= 1; }
       return true;
     };
     // dP = dO V^T; `last`: the item's queries and gradients are free after it
@@ -717,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_commit(ds_empty);
         }
         __syncwarp();
-        if (++kd == kKStages) kd = 0;
+        if (++kd == kStages) kd = 0;
       }
       if (!ok) { fail(); break; }
       if (elect_one()) tc_commit(acc_full);
@@ -895,7 +970,7 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   g.nch = p.d_shared > 0 ? g.nck + (p.d_shared + 63) / 64 : g.nck;
   g.ncv = (p.d_v + 63) / 64;
   g.nb = (p.S + BM - 1) / BM;
-  g.nt = (p.S + query_tile(g.nch) - 1) / query_tile(g.nch);
+  g.nt = (p.S + query_tile(g.nch, g.ncv) - 1) / query_tile(g.nch, g.ncv);
   g.nunit = p.causal ? (g.nb + 1) / 2 : g.nb;
   const long long units = (long long)p.B * p.H * g.nunit;
   if (units >= (1ll << 30)) { snprintf(err, errlen, "%lld work units exceed the kernel's 2^30", units); return false; }
@@ -908,11 +983,11 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
 
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
-  constexpr int NQ = query_tile(NCH);
-  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + 2 * (size_t)(NCH + NCV) * NQ * 128 + 4 * NQ * 4 + 256;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kKStages * NCH + NCV) * key_tile(NCH) * 128 + 256;
+  constexpr int NQ = query_tile(NCH, NCV);
+  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 256;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 256;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
-  static_assert(64 * (NCH + NCV) + 2 * NQ <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
+  static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
   if (e != cudaSuccess) return e;
   dkv_kernel<NCH, NCV><<<grid, kThreads, skv, s>>>(p, kv, g);
@@ -950,7 +1025,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   using namespace ab;
   Geo g;
   if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
-  const int nq = query_tile(g.nch), D = p.d_head + p.d_shared;
+  const int nq = query_tile(g.nch, g.ncv), D = p.d_head + p.d_shared;
   const int nk = key_tile(g.nch);
   Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (nk-row keys, 128-row queries)
   memset(&kv, 0, sizeof kv);
