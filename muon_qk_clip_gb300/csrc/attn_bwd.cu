@@ -148,66 +148,124 @@ __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* a
   return __all_sync(0xffffffffu, ok);
 }
 
-// 16 values v[0..16) of one output row to dst[0 .. n) (n <= 16 of them exist),
-// as bf16; dst is 16-byte aligned.
-__device__ inline void store_row16(__nv_bfloat16* dst, const float (&v)[16], int n) {
+// 32 columns of one accumulator row (r: fp32 bits) times `scale` to dst[0 .. n)
+// (n <= 32 of them exist) as bf16; dst is 16-byte aligned.  True if one of the
+// values is not finite.
+__device__ inline bool store_row(__nv_bfloat16* dst, const uint32_t (&r)[32], float scale, int n) {
+  bool bad = false;
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < 4; ++u) {
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(r[8 * u + x]) * scale;
     if (8 * u + 8 <= n) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) bad |= !finite_f(v[x]);
       *reinterpret_cast<uint4*>(dst + 8 * u) =
-          make_uint4(pack_bf16(v[8 * u], v[8 * u + 1]), pack_bf16(v[8 * u + 2], v[8 * u + 3]),
-                     pack_bf16(v[8 * u + 4], v[8 * u + 5]), pack_bf16(v[8 * u + 6], v[8 * u + 7]));
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     } else {
 #pragma unroll
       for (int x = 0; x < 8; ++x)
-        if (8 * u + x < n) dst[8 * u + x] = __float2bfloat16_rn(v[8 * u + x]);
+        if (8 * u + x < n) {
+          bad |= !finite_f(v[x]);
+          dst[8 * u + x] = __float2bfloat16_rn(v[x]);
+        }
     }
   }
+  return bad;
+}
+// The same in fp32.
+__device__ inline bool store_row(float* dst, const uint32_t (&r)[32], float scale, int n, bool vec) {
+  bool bad = false;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    float v[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) v[x] = __uint_as_float(r[4 * u + x]) * scale;
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+      if (4 * u + x < n) bad |= !finite_f(v[x]);
+    if (vec && 4 * u + 4 <= n) {
+      *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (4 * u + x < n) dst[4 * u + x] = v[x];
+    }
+  }
+  return bad;
+}
+// 32 N columns of this thread's row from tensor memory, every load in flight
+// before the first use.
+template <int N>
+__device__ inline void read_row(uint32_t taddr, uint32_t (&r)[N][32]) {
+#pragma unroll
+  for (int c = 0; c < N; ++c) tmem_ld_32x32b_x32_async(taddr + c * 32, r[c]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < N; ++c) reg_fence32(r[c]);
 }
 
 // ------------------------------------------------------------------- rows
 // delta_i = sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
 // in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
-// delta = 0.  16 lanes per (b, i, h), 8 features each.  Streams o and do once.
-__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const long long sp) {
-  const int sub = threadIdx.x & 15;
-  const long long per = 256 / 16;
-  const long long rows = (long long)p.B * sp * p.H;
-  for (long long r = (long long)blockIdx.x * per + (threadIdx.x >> 4);; r += (long long)gridDim.x * per) {
-    // whole warps leave together: the shuffles below need every lane
-    if (__all_sync(0xffffffffu, r >= rows)) break;
-    const bool in = r < rows;
-    const long long bi = in ? r / p.H : 0;
-    const int h = in ? (int)(r - bi * p.H) : 0;
-    const int b = (int)(bi / sp);
-    const long long i = bi - (long long)b * sp;
-    float s = 0.f;
-    const bool live = in && i < p.S;
-    if (live) {
+// delta = 0.  A block takes 32 positions of 8 heads: 16 lanes per row with 8
+// features each, 16 rows in flight per thread group pass, the results written
+// through shared memory so that a warp stores 32 positions of a head.
+constexpr int kRowPos = 32, kRowHeads = 8;
+__global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
+                                                   const int nh) {
+  __shared__ float sums[kRowHeads][kRowPos + 1];
+  // block: position group fastest, then head group, then batch
+  const int bi = blockIdx.x / ni, i0 = (blockIdx.x - bi * ni) * kRowPos;
+  const int b = bi / nh, h0 = (bi - b * nh) * kRowHeads;
+  const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int c0 = sub * 8;
+  constexpr int N = kRowPos * kRowHeads / 16;            // rows per group
+  uint4 a[N], e[N];
+  bool live[N];
+  // row x: head h0 + x % 8 of position i0 + x / 8 (neighbouring heads are
+  // neighbours in memory)
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int x = n * 16 + group, h = h0 + x % kRowHeads, i = i0 + x / kRowHeads;
+    live[n] = h < p.H && i < p.S;
+    a[n] = e[n] = make_uint4(0, 0, 0, 0);
+    if (live[n] && c0 < p.d_v) {
       const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + i * p.os[1] + h * p.os[2];
       const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + i * p.dos[1] + h * p.dos[2];
-      const int c0 = sub * 8;
       if (c0 + 8 <= p.d_v) {
-        const uint4 a = *reinterpret_cast<const uint4*>(o + c0), e = *reinterpret_cast<const uint4*>(d + c0);
-        const __nv_bfloat162* a2 = reinterpret_cast<const __nv_bfloat162*>(&a);
-        const __nv_bfloat162* e2 = reinterpret_cast<const __nv_bfloat162*>(&e);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float2 fa = __bfloat1622float2(a2[x]), fe = __bfloat1622float2(e2[x]);
-          s = fmaf(fa.x, fe.x, s);
-          s = fmaf(fa.y, fe.y, s);
-        }
+        a[n] = *reinterpret_cast<const uint4*>(o + c0);
+        e[n] = *reinterpret_cast<const uint4*>(d + c0);
       } else {
-        for (int c = c0; c < p.d_v; ++c) s = fmaf(__bfloat162float(o[c]), __bfloat162float(d[c]), s);
+        __nv_bfloat16* ta = reinterpret_cast<__nv_bfloat16*>(&a[n]);
+        __nv_bfloat16* te = reinterpret_cast<__nv_bfloat16*>(&e[n]);
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+          if (c0 + c < p.d_v) { ta[c] = o[c0 + c]; te[c] = d[c0 + c]; }
       }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const uint32_t wa[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, we[4] = {e[n].x, e[n].y, e[n].z, e[n].w};
+    float s = 0.f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      s = fmaf(__uint_as_float(wa[x] << 16), __uint_as_float(we[x] << 16), s);
+      s = fmaf(__uint_as_float(wa[x] & 0xffff0000u), __uint_as_float(we[x] & 0xffff0000u), s);
     }
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (in && sub == 0) {
-      const long long at = ((long long)b * p.H + h) * sp + i;
-      p.delta[at] = s;
-      p.nlse[at] = live ? -p.lse[((long long)b * p.H + h) * p.S + i] * kLog2e : -INFINITY;
-    }
+    const int x = n * 16 + group;
+    if (sub == 0) sums[x % kRowHeads][x / kRowHeads] = s;
+  }
+  __syncthreads();
+  const int h = h0 + threadIdx.x / 32, i = i0 + threadIdx.x % 32;
+  if (h < p.H && i < sp) {
+    const long long bh = (long long)b * p.H + h;
+    p.delta[bh * sp + i] = sums[threadIdx.x / 32][threadIdx.x % 32];
+    p.nlse[bh * sp + i] = i < p.S ? -p.lse[bh * p.S + i] * kLog2e : -INFINITY;
   }
 }
 
@@ -258,10 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* p_empty = bars + 17;
   uint64_t* dp_full = bars + 18;
   uint64_t* ds_full = bars + 19;
-  uint64_t* acc_full = bars + 20;
-  uint64_t* acc_empty = bars + 21;
-  uint64_t* drain = bars + 22;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 23);
+  uint64_t* dv_full = bars + 20;
+  uint64_t* dv_empty = bars + 21;
+  uint64_t* dk_full = bars + 22;
+  uint64_t* dk_empty = bars + 23;
+  uint64_t* drain = bars + 24;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -275,7 +335,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(p_full, 8); mbar_init(p_empty, 1);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8);
-    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(dv_full, 1); mbar_init(dv_empty, 8);
+    mbar_init(dk_full, 1); mbar_init(dk_empty, 8);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
@@ -389,13 +450,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A (tensor memory): NQ / 16 k-steps of 8 columns; the second half of the
     // queries starts at column a + `half`
     auto accumulate = [&](uint32_t d, uint32_t a, int half, uint64_t b0, uint32_t idesc, bool add, uint64_t* done,
-                          uint64_t* done2) {
+                          uint64_t* done2, uint64_t* done3) {
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < NQ / 16; ++kk)
           tc_mma_ts(d, a + (kk < NU ? kk * 8 : half + (kk - NU) * 8), b0 + kk * 128, idesc, (add || kk > 0) ? 1u : 0u);
         tc_commit(done);
         if (done2) tc_commit(done2);
+        if (done3) tc_commit(done3);
       }
       __syncwarp();
     };
@@ -415,19 +477,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (APART && !warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
         if (APART && i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(p_full, t & 1, &abort_flag)) { ok = false; break; }
-        if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+        if (i == 0 && !warp_wait(dv_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        accumulate(t_dv, t_p, kHalfP, mdo_ + sd * (NCV * CQ / 16), idesc_dv, i > 0, &do_empty[sd], APART ? p_empty : nullptr);
+        accumulate(t_dv, t_p, kHalfP, mdo_ + sd * (NCV * CQ / 16), idesc_dv, i > 0, &do_empty[sd],
+                   APART ? p_empty : nullptr, i + 1 == nt ? dv_full : nullptr);
         if (!APART && i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
+        if (i == 0 && !warp_wait(dk_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        accumulate(t_dk, t_dp, NH, mq_ + sd * (NCH * CQ / 16), idesc_dk, i > 0, &q_empty[sd], nullptr);
+        accumulate(t_dk, t_dp, NH, mq_ + sd * (NCH * CQ / 16), idesc_dk, i > 0, &q_empty[sd], nullptr,
+                   i + 1 == nt ? dk_full : nullptr);
         if (++sd == kStages) sd = 0;
         if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
       }
       if (!ok) { fail(); break; }
-      if (elect_one()) tc_commit(acc_full);
-      __syncwarp();
       ++li;
     }
     if (issued) {
@@ -565,46 +628,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ds_full);
         if (++s == kStages) { s = 0; sph ^= 1; }
       }
-      if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
+      // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
+      // per-head fp32 partial sums.  Each half of the warps takes half of the
+      // columns, a thread one key.
+      const int j = blk * BM + q * 32 + lane;
+      if (ok) ok = warp_wait(dv_full, li & 1, &abort_flag);
       if (!ok) { if (lane == 0) fail(); break; }
       tc_fence_after();
-      const int j = blk * BM + q * 32 + lane;            // the epilogue's thread: one key
-      // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
-      // per-head fp32 partial sums
-      const bool live = j < p.S;
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + j * p.dvs[1] + h * p.dvs[2];
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + j * p.dks[1] + h * p.dks[2];
-      float* part = p.part + (((long long)b * p.H + h) * p.S + j) * p.d_shared;
-      for (int c = 0; c < 2 * NCV + 2 * NCH; ++c) {
-        const bool is_v = c < 2 * NCV;
-        const int col = is_v ? hf * 32 * NCV + c * 16 : hf * 32 * NCH + (c - 2 * NCV) * 16;
-        uint32_t r[16];
-        tmem_ld_32x32b_x16_async((is_v ? t_dv : t_dk) + lanes + col, r);
-        tmem_ld_wait();
-        reg_fence16(r);
-        float v[16];
-        const float sc = is_v ? 1.f : p.scale;
-        int width = is_v ? p.d_v - col : col < 64 * g.nck ? p.d_head - col : p.d_head + p.d_shared - col;
-        if (width > 16) width = 16;
-        if (live && width > 0) {
+      {
+        uint32_t r[NCV][32];
+        read_row(t_dv + lanes + hf * 32 * NCV, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dv_empty);
+        if (j < p.S) {
+          __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + j * p.dvs[1] + h * p.dvs[2];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            v[x] = __uint_as_float(r[x]) * sc;
-            if (x < width) bad |= !finite_f(v[x]);
-          }
-          if (is_v) store_row16(dv + col, v, width);
-          else if (col < 64 * g.nck) store_row16(dk + col, v, width);
-          else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x)
-              if (x < width) part[col - p.d_head + x] = v[x];
+          for (int c = 0; c < NCV; ++c) {
+            const int col = hf * 32 * NCV + c * 32;
+            bad |= store_row(dv + col, r[c], 1.f, p.d_v - col);
           }
         }
-        __syncwarp();                    // the next load takes the whole warp
+        __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
+      ok = warp_wait(dk_full, li & 1, &abort_flag);
+      if (!ok) { if (lane == 0) fail(); break; }
+      tc_fence_after();
+      {
+        uint32_t r[NCH][32];
+        read_row(t_dk + lanes + hf * 32 * NCH, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dk_empty);
+        if (j < p.S) {
+          __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + j * p.dks[1] + h * p.dks[2];
+          float* part = p.part + (((long long)b * p.H + h) * p.S + j) * p.d_shared;
+#pragma unroll
+          for (int c = 0; c < NCH; ++c) {
+            const int col = hf * 32 * NCH + c * 32;
+            if (col < 64 * g.nck) bad |= store_row(dk + col, r[c], p.scale, p.d_head - col);
+            else bad |= store_row(part + col - p.d_head, r[c], p.scale, p.d_head + p.d_shared - col, p.d_shared % 4 == 0);
+          }
+        }
+        __syncwarp();
+      }
       ++li;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
@@ -880,29 +947,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
       if (!ok) { if (lane == 0) fail(); break; }
       tc_fence_after();
-      const int D = p.d_head + p.d_shared;
-      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
-      for (int c = 0; c < 2 * NCH; ++c) {
-        const int col = hf * 32 * NCH + c * 16;
-        uint32_t r[16];
-        tmem_ld_32x32b_x16_async(t_dq + lanes + col, r);
-        tmem_ld_wait();
-        reg_fence16(r);
-        const int width = min(D - col, 16);
-        if (i < p.S && width > 0) {
-          float v[16];
+      {
+        uint32_t r[NCH][32];
+        read_row(t_dq + lanes + hf * 32 * NCH, r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty);
+        if (i < p.S) {
+          __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            v[x] = __uint_as_float(r[x]) * p.scale;
-            if (x < width) bad |= !finite_f(v[x]);
+          for (int c = 0; c < NCH; ++c) {
+            const int col = hf * 32 * NCH + c * 32;
+            bad |= store_row(dq + col, r[c], p.scale, p.d_head + p.d_shared - col);
           }
-          store_row16(dq + col, v, width);
         }
-        __syncwarp();                    // the next load takes the whole warp
+        __syncwarp();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(acc_empty);
       ++li;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
@@ -917,15 +977,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- shared key
-// dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums.
-__global__ void shared_kernel(const __grid_constant__ AttnBwdParams p) {
+// dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums:
+// a thread per position and feature, eight heads' loads in flight.
+__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p) {
   const long long per = (long long)p.S * p.d_shared, total = per * p.B;
   for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total;
        x += (long long)gridDim.x * blockDim.x) {
     const long long b = x / per, r = x - b * per;
     const float* src = p.part + b * p.H * per + r;
     float s = 0.f;
-    for (int h = 0; h < p.H; ++h) s += src[h * per];
+    int h = 0;
+    for (; h + 8 <= p.H; h += 8) {
+      float v[8];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) v[y] = src[(h + y) * per];
+#pragma unroll
+      for (int y = 0; y < 8; ++y) s += v[y];
+    }
+    for (; h < p.H; ++h) s += src[h * per];
     const long long j = r / p.d_shared, c = r - j * p.d_shared;
     static_cast<__nv_bfloat16*>(p.dksh)[b * p.dkshs[0] + j * p.dkshs[1] + c] = __float2bfloat16_rn(s);
   }
@@ -1039,9 +1108,9 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
          (p.d_shared == 0 || encode(&qm.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, nk));
   if (!ok) { snprintf(err, errlen, "tensor map encoding failed"); return cudaErrorInvalidValue; }
   const int sms = sm_count();
-  const long long rows = (long long)p.B * g.sp * p.H;
-  const long long want = cdiv(rows, 16);
-  rows_kernel<<<(int)(want < (long long)sms * 16 ? want : (long long)sms * 16), 256, 0, s>>>(p, g.sp);
+  const long long ni = cdiv(g.sp, kRowPos), nh = cdiv(p.H, kRowHeads);
+  if (ni * nh * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
+  rows_kernel<<<(unsigned)(ni * nh * p.B), 256, 0, s>>>(p, (int)g.sp, (int)ni, (int)nh);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const int grid = (int)(g.units < (uint32_t)sms ? g.units : (uint32_t)sms);
