@@ -55,9 +55,12 @@ __host__ __device__ constexpr int query_stages(int nch, int ncv) { return p_apar
 // Keys per tile of the dQ pass: three stages of 192-wide keys fit with 96.
 __host__ __device__ constexpr int key_tile(int nch) { return nch > 2 ? 96 : 128; }
 constexpr int kStages = 3;               // key tiles of the dQ pass (its values have one)
+// Output columns that a warp of the dQ pass stores at a time, by the shared
+// memory that is left.
+__host__ __device__ constexpr int dq_columns(int nch) { return nch > 2 ? 16 : 32; }
 
 struct Maps {
-  CUtensorMap q, k, ks, v, d_o;
+  CUtensorMap q, k, ks, v, d_o;          // inputs: 64-feature chunks of a tile's rows
 };
 
 struct Geo {
@@ -148,62 +151,57 @@ __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* a
   return __all_sync(0xffffffffu, ok);
 }
 
-// 32 columns of one accumulator row (r: fp32 bits) times `scale` to dst[0 .. n)
-// (n <= 32 of them exist) as bf16; dst is 16-byte aligned.  True if one of the
-// values is not finite.
-__device__ inline bool store_row(__nv_bfloat16* dst, const uint32_t (&r)[32], float scale, int n) {
-  bool bad = false;
+// W (16 or 32) columns of an accumulator, from tensor memory at `taddr` (a row
+// per lane), times `scale`, as bf16, to 32 rows of an output that are `pitch`
+// elements apart.  They turn through this warp's 64 W bytes of shared memory so
+// that its stores write whole sectors.  The first `rows` rows and `n` columns
+// exist.  True if one of this lane's row's values is not finite.
+//
+// The epilogue calls this in loops that stay rolled: its code runs once per work
+// item between tiles of other code, and unrolled (a copy per 16 or 32 columns) it
+// took 2200-4700 clocks per 128 columns, most of them fetching instructions.
+template <int W>
+__device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long pitch, uint8_t* buf, float scale, int rows,
+                                  int n) {
+  constexpr int NU = W / 8;              // 16-byte units per row
+  const int lane = threadIdx.x & 31;
+  auto at = [&](int row, int u) { return reinterpret_cast<uint4*>(buf + row * W * 2 + ((u ^ (NU == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4)); };
+  uint32_t r[W / 16][16];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    float v[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] = __uint_as_float(r[8 * u + x]) * scale;
-    if (8 * u + 8 <= n) {
-#pragma unroll
-      for (int x = 0; x < 8; ++x) bad |= !finite_f(v[x]);
-      *reinterpret_cast<uint4*>(dst + 8 * u) =
-          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-#pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (8 * u + x < n) {
-          bad |= !finite_f(v[x]);
-          dst[8 * u + x] = __float2bfloat16_rn(v[x]);
-        }
-    }
-  }
-  return bad;
-}
-// The same in fp32.
-__device__ inline bool store_row(float* dst, const uint32_t (&r)[32], float scale, int n, bool vec) {
-  bool bad = false;
-#pragma unroll
-  for (int u = 0; u < 8; ++u) {
-    float v[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) v[x] = __uint_as_float(r[4 * u + x]) * scale;
-#pragma unroll
-    for (int x = 0; x < 4; ++x)
-      if (4 * u + x < n) bad |= !finite_f(v[x]);
-    if (vec && 4 * u + 4 <= n) {
-      *reinterpret_cast<float4*>(dst + 4 * u) = make_float4(v[0], v[1], v[2], v[3]);
-    } else {
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (4 * u + x < n) dst[4 * u + x] = v[x];
-    }
-  }
-  return bad;
-}
-// 32 N columns of this thread's row from tensor memory, every load in flight
-// before the first use.
-template <int N>
-__device__ inline void read_row(uint32_t taddr, uint32_t (&r)[N][32]) {
-#pragma unroll
-  for (int c = 0; c < N; ++c) tmem_ld_32x32b_x32_async(taddr + c * 32, r[c]);
+  for (int c = 0; c < W / 16; ++c) tmem_ld_32x32b_x16_async(taddr + c * 16, r[c]);
   tmem_ld_wait();
 #pragma unroll
-  for (int c = 0; c < N; ++c) reg_fence32(r[c]);
+  for (int c = 0; c < W / 16; ++c) reg_fence16(r[c]);
+  float z = 0.f;                         // 0, or NaN once a value is not finite
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    float v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      v[x] = __uint_as_float(r[u / 2][8 * (u % 2) + x]) * scale;
+      z = fmaf(v[x], 0.f, z);
+    }
+    *at(lane, u) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  }
+  __syncwarp();
+#pragma unroll
+  for (int x = 0; x < NU; ++x) {
+    const int row = (x * 32 + lane) / NU, u = lane % NU;
+    const uint4 w = *at(row, u);
+    if (row < rows && 8 * u < n) {
+      __nv_bfloat16* to = dst + row * pitch + 8 * u;
+      if (8 * u + 8 <= n) {
+        *reinterpret_cast<uint4*>(to) = w;
+      } else {
+        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int y = 0; y < 7; ++y)
+          if (8 * u + y < n) to[y] = __ushort_as_bfloat16((unsigned short)(e[y / 2] >> (16 * (y % 2))));
+      }
+    }
+  }
+  __syncwarp();
+  return z != z && lane < rows;
 }
 
 // ------------------------------------------------------------------- rows
@@ -303,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
   uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
   float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, delta][NQ]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(rowv + kStages * 2 * NQ);
+  uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [8 warps][2 KB]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 8 * 2048);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
   uint64_t* q_full = bars + 2;      // [stages <= 3] Q tile with its nlse and delta
@@ -509,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tp = t_p + lanes + hf * kHalfP;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
     const float c2 = p.scale * kLog2e;
+    uint8_t* mine = stage + (warp - 2) * 2048;
     uint32_t t = 0, li = 0, s = 0, sph = 0;
     bool bad = false;
     for (uint32_t n = 0;; ++n) {
@@ -589,39 +589,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = warp_wait(dp_full, t & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        {
-          uint32_t r[NU][2][8];
+        // unit by unit, the next one's load under the arithmetic: dS^T of unit u
+        // (8 columns) lies before every column that is still to be read
+        uint32_t r[2][2][8];
+        auto load = [&](int u) {
 #pragma unroll
-          for (int u = 0; u < NU; ++u)
+          for (int hh = 0; hh < 2; ++hh) tmem_ld_16x256b_x2_async(tdp + ((uint32_t)(16 * hh) << 16) + u * 16, r[u & 1][hh]);
+        };
+        load(0);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) tmem_ld_16x256b_x2_async(tdp + ((uint32_t)(16 * hh) << 16) + u * 16, r[u][hh]);
+        for (int u = 0; u < NU; ++u) {
           tmem_ld_wait();
+          reg_fence8(r[u & 1][0]);
+          reg_fence8(r[u & 1][1]);
+          if (u + 1 < NU) load(u + 1);
 #pragma unroll
-          for (int u = 0; u < NU; ++u)
+          for (int m = 0; m < 2; ++m) {
+            const float2 d = *reinterpret_cast<const float2*>(nl + NQ + u * 16 + m * 8);
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh) reg_fence8(r[u][hh]);
+            for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-          for (int u = 0; u < NU; ++u)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              const float2 d = *reinterpret_cast<const float2*>(nl + NQ + u * 16 + m * 8);
-#pragma unroll
-              for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                  pv[u][hh][4 * m + x] *= __uint_as_float(r[u][hh][4 * m + x]) - d.x;
-                  pv[u][hh][4 * m + x + 1] *= __uint_as_float(r[u][hh][4 * m + x + 1]) - d.y;
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < NU; ++u)
+              for (int x = 0; x < 4; x += 2) {
+                pv[u][hh][4 * m + x] *= __uint_as_float(r[u & 1][hh][4 * m + x]) - d.x;
+                pv[u][hh][4 * m + x + 1] *= __uint_as_float(r[u & 1][hh][4 * m + x + 1]) - d.y;
+              }
+          }
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
             const float* v = pv[u][hh];
             tmem_st_16x128b_x2(tdp + ((uint32_t)(16 * hh) << 16) + u * 8, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
                                pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
           }
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -630,48 +629,51 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
       // per-head fp32 partial sums.  Each half of the warps takes half of the
-      // columns, a thread one key.
-      const int j = blk * BM + q * 32 + lane;
-      if (ok) ok = warp_wait(dv_full, li & 1, &abort_flag);
-      if (!ok) { if (lane == 0) fail(); break; }
-      tc_fence_after();
-      {
-        uint32_t r[NCV][32];
-        read_row(t_dv + lanes + hf * 32 * NCV, r);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dv_empty);
-        if (j < p.S) {
-          __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + j * p.dvs[1] + h * p.dvs[2];
+      // columns.
+      const int key0 = blk * BM + q * 32, rows = p.S - key0;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key0 * p.dvs[1] + h * p.dvs[2];
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key0 * p.dks[1] + h * p.dks[2];
+#pragma unroll 1
+      for (int c = 0; ok && c < NCV + NCH; ++c) {
+        const bool is_v = c < NCV;
+        if (c == 0 || c == NCV) {
+          ok = warp_wait(is_v ? dv_full : dk_full, li & 1, &abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const int col = is_v ? hf * 32 * NCV + c * 32 : hf * 32 * NCH + (c - NCV) * 32;
+        const uint32_t from = (is_v ? t_dv : t_dk) + lanes + col;
+        if (is_v || col < 64 * g.nck) {
+          const int n = (is_v ? p.d_v : p.d_head) - col;
+          if (n > 0)
+            bad |= store_rows<32>(from, (is_v ? dv : dk) + col, is_v ? p.dvs[1] : p.dks[1], mine, is_v ? 1.f : p.scale, rows, n);
+        } else {                           // [b][h][feature][position]: 32 keys are 128 bytes
+          const int f0 = col - p.d_head;
+          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key0 + lane;
+#pragma unroll 1
+          for (int y = 0; y < 32; y += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16_async(from + y, r);
+            tmem_ld_wait();
+            reg_fence16(r);
+            float z = 0.f;
 #pragma unroll
-          for (int c = 0; c < NCV; ++c) {
-            const int col = hf * 32 * NCV + c * 32;
-            bad |= store_row(dv + col, r[c], 1.f, p.d_v - col);
+            for (int x = 0; x < 16; ++x) {
+              const float v = __uint_as_float(r[x]) * p.scale;
+              z = fmaf(v, 0.f, z);
+              if (lane < rows && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
+            }
+            bad |= z != z && lane < rows;
+            __syncwarp();
           }
         }
-        __syncwarp();
-      }
-      ok = warp_wait(dk_full, li & 1, &abort_flag);
-      if (!ok) { if (lane == 0) fail(); break; }
-      tc_fence_after();
-      {
-        uint32_t r[NCH][32];
-        read_row(t_dk + lanes + hf * 32 * NCH, r);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(dk_empty);
-        if (j < p.S) {
-          __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + j * p.dks[1] + h * p.dks[2];
-          float* part = p.part + (((long long)b * p.H + h) * p.S + j) * p.d_shared;
-#pragma unroll
-          for (int c = 0; c < NCH; ++c) {
-            const int col = hf * 32 * NCH + c * 32;
-            if (col < 64 * g.nck) bad |= store_row(dk + col, r[c], p.scale, p.d_head - col);
-            else bad |= store_row(part + col - p.d_head, r[c], p.scale, p.d_head + p.d_shared - col, p.d_shared % 4 == 0);
-          }
+        if (c == NCV - 1 || c == NCV + NCH - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(is_v ? dv_empty : dk_empty);
         }
-        __syncwarp();
       }
+      if (!ok) { if (lane == 0) fail(); break; }
       ++li;
     }
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
@@ -696,6 +698,7 @@ template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
   constexpr int BN = key_tile(NCH), NH = BN / 2;
+  constexpr int W = dq_columns(NCH);     // of dQ that a warp stores at a time
   constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -703,7 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
   uint8_t* vbuf = kbuf + kStages * NCH * CK;           // NCV chunks
-  uint64_t* bars = reinterpret_cast<uint64_t*>(vbuf + NCV * CK);
+  uint8_t* stage = vbuf + NCV * CK;                     // [8 warps][64 W bytes]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 8 * 64 * W);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
@@ -878,17 +882,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tds = t_ds + lanes + hf * (NH / 2);
     const float c2 = p.scale * kLog2e;
+    uint8_t* mine = stage + (warp - 2) * 64 * W;
     uint32_t t = 0, li = 0;
     bool bad = false;
-    for (uint32_t n = 0;; ++n) {
-      int b, h, blk;
-      const int st = next_item(p, g, n, b, h, blk);
-      if (st < 0) break;
-      if (st == 0) continue;
+    // this item and the next one, whose row values are loaded an item ahead
+    int b, h, blk, b1, h1, blk1;
+    float nl = 0.f, dl = 0.f, nl1 = 0.f, dl1 = 0.f;
+    uint32_t n = 0;
+    auto fetch = [&]() -> bool {           // the next item: coordinates, nlse and delta of this thread's query
+      int st;
+      while ((st = next_item(p, g, n, b1, h1, blk1)) == 0) ++n;
+      if (st < 0) return false;
+      ++n;
+      const long long at = ((long long)b1 * p.H + h1) * g.sp + blk1 * BM + row;   // inside: sp is padded to whole blocks
+      nl1 = p.nlse[at];
+      dl1 = p.delta[at];
+      return true;
+    };
+    bool more = fetch();
+    while (more) {
+      b = b1; h = h1; blk = blk1; nl = nl1; dl = dl1;
+      more = fetch();
       const int i = blk * BM + row;                      // this thread's query
       const int nt = tiles(blk);
-      const long long at = ((long long)b * p.H + h) * g.sp + i;   // i < sp: sp is padded to whole blocks
-      const float nl = p.nlse[at], dl = p.delta[at];
       bool ok = true;
       for (int it = 0; it < nt; ++it, ++t) {
         const int j0 = it * BN + hf * NH;
@@ -948,20 +964,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) { if (lane == 0) fail(); break; }
       tc_fence_after();
       {
-        uint32_t r[NCH][32];
-        read_row(t_dq + lanes + hf * 32 * NCH, r);
+        const int D = p.d_head + p.d_shared, q0 = blk * BM + q * 32;
+        __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + q0 * p.dqs[1] + h * p.dqs[2];
+#pragma unroll 1
+        for (int c = 0; c < 32 * NCH / W; ++c) {
+          const int col = hf * 32 * NCH + c * W;
+          if (col < D) bad |= store_rows<W>(t_dq + lanes + col, dq + col, p.dqs[1], mine, p.scale, p.S - q0, D - col);
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty);
-        if (i < p.S) {
-          __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
-#pragma unroll
-          for (int c = 0; c < NCH; ++c) {
-            const int col = hf * 32 * NCH + c * 32;
-            bad |= store_row(dq + col, r[c], p.scale, p.d_head + p.d_shared - col);
-          }
-        }
-        __syncwarp();
       }
       ++li;
     }
@@ -977,15 +989,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ------------------------------------------------------------- shared key
-// dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums:
-// a thread per position and feature, eight heads' loads in flight.
-__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p) {
-  const long long per = (long long)p.S * p.d_shared, total = per * p.B;
-  for (long long x = (long long)blockIdx.x * blockDim.x + threadIdx.x; x < total;
-       x += (long long)gridDim.x * blockDim.x) {
-    const long long b = x / per, r = x - b * per;
-    const float* src = p.part + b * p.H * per + r;
-    float s = 0.f;
+// dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums
+// [b][h][c][j].  A block takes 32 positions of 8 features, eight heads' loads in
+// flight per thread, and turns its tile through shared memory.
+__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p, const int nj, const int nc) {
+  __shared__ float tile[32][9];
+  const int bi = blockIdx.x / nj, j0 = (blockIdx.x - bi * nj) * 32;
+  const int b = bi / nc, c0 = (bi - b * nc) * 8;
+  const int lane = threadIdx.x & 31, c = c0 + threadIdx.x / 32, j = j0 + lane;
+  const long long per = (long long)p.d_shared * p.S;
+  float s = 0.f;
+  if (c < p.d_shared && j < p.S) {
+    const float* src = p.part + (long long)b * p.H * per + (long long)c * p.S + j;
     int h = 0;
     for (; h + 8 <= p.H; h += 8) {
       float v[8];
@@ -995,9 +1010,13 @@ __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ Att
       for (int y = 0; y < 8; ++y) s += v[y];
     }
     for (; h < p.H; ++h) s += src[h * per];
-    const long long j = r / p.d_shared, c = r - j * p.d_shared;
-    static_cast<__nv_bfloat16*>(p.dksh)[b * p.dkshs[0] + j * p.dkshs[1] + c] = __float2bfloat16_rn(s);
   }
+  tile[lane][threadIdx.x / 32] = s;
+  __syncthreads();
+  const int jj = j0 + threadIdx.x / 8, cc = c0 + threadIdx.x % 8;
+  if (jj < p.S && cc < p.d_shared)
+    static_cast<__nv_bfloat16*>(p.dksh)[b * p.dkshs[0] + jj * p.dkshs[1] + cc] =
+        __float2bfloat16_rn(tile[threadIdx.x / 8][threadIdx.x % 8]);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1053,8 +1072,8 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr int NQ = query_tile(NCH, NCV);
-  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 256;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 256;
+  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 8 * 2048 + 256;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 8 * 64 * dq_columns(NCH) + 256;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
   static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
@@ -1120,9 +1139,9 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
                                          {launch_passes<3, 1>, launch_passes<3, 2>}};
   e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
   if (e != cudaSuccess || p.d_shared == 0) return e;
-  const long long n = (long long)p.B * p.S * p.d_shared;
-  const long long blocks = cdiv(n, 256);
-  shared_kernel<<<(int)(blocks < (long long)sms * 8 ? blocks : (long long)sms * 8), 256, 0, s>>>(p);
+  const long long nj = cdiv(p.S, 32), nc = cdiv(p.d_shared, 8);
+  if (nj * nc * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
+  shared_kernel<<<(unsigned)(nj * nc * p.B), 256, 0, s>>>(p, (int)nj, (int)nc);
   return cudaGetLastError();
 }
 

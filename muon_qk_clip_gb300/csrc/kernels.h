@@ -264,7 +264,7 @@ struct AttnBwdParams {
   long long dqs[3], dks[3], dkshs[2], dvs[3];
   float* nlse;             // workspace [B, H, sp]: -lse log2(e), -inf past the sequence
   float* delta;            // workspace [B, H, sp]: do . o
-  float* part;             // workspace [B, H, S, d_shared]: per-head gradients of the shared key
+  float* part;             // workspace [B, H, d_shared, S]: per-head gradients of the shared key
   int32_t* status;
 };
 long long attn_bwd_padded_rows(int S);                       // sp
