@@ -954,7 +954,7 @@ namespace {
 
 // Workspace of the attention backward, in 256-byte aligned parts.
 struct AttnBwdPlan {
-  size_t nlse, delta, part, bytes;
+  size_t nlse, delta, part, counter, bytes;
 };
 AttnBwdPlan plan_attn_bwd(int64_t B, int64_t S, int64_t H, int64_t d_shared) {
   const size_t rows = (size_t)round_up(B * H * attn_bwd_padded_rows((int)S) * 4, 256);
@@ -962,7 +962,8 @@ AttnBwdPlan plan_attn_bwd(int64_t B, int64_t S, int64_t H, int64_t d_shared) {
   w.nlse = 0;
   w.delta = rows;
   w.part = 2 * rows;
-  w.bytes = w.part + (size_t)round_up(B * H * S * d_shared * 4, 256);
+  w.counter = w.part + (size_t)round_up(B * H * S * d_shared * 4, 256);
+  w.bytes = w.counter + 256;
   return w;
 }
 
@@ -1072,6 +1073,7 @@ mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, vo
   p.nlse = reinterpret_cast<float*>(base + w.nlse);
   p.delta = reinterpret_cast<float*>(base + w.delta);
   p.part = reinterpret_cast<float*>(base + w.part);
+  p.counter = reinterpret_cast<int*>(base + w.counter);
   cudaError_t e;
   {
     ProfScope ps(kAttnBwd, a->d_shared > 0 ? 4 : 3, (cudaStream_t)stream);

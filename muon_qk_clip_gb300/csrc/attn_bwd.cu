@@ -67,30 +67,49 @@ struct Geo {
   int nch, nck, ncv;    // 64-wide chunks of q.k, of its head-specific part, of d_v
   int nb;               // 128-row blocks per (b, h)
   int nt;               // dkv: query tiles per (b, h)
-  int nunit;            // units per (b, h): pairs of blocks when causal
-  uint32_t units;       // below 2^30 (checked on the host)
+  int items;            // blocks in all, below 2^30 (checked on the host)
+  int heads;            // B H
+  int group;            // (b, h) pairs per group of the work order
+  int full;             // items in whole groups
   long long sp;         // padded row length of nlse and delta
-  FastDiv div_nunit, div_h;
+  FastDiv div_h, div_group_items, div_group, div_last;
 };
 
-// Work order as in the forward: causal units are pairs of blocks (u, nb-1-u)
-// of one (b, h), equal in work whatever u is, numbered (b, h)-major so that the
-// CTAs in flight share a few heads in L2.  Returns 1 with an item, 0 for the
-// missing half of an unpaired middle block, -1 at the end.
-__device__ inline int next_item(const AttnBwdParams& p, const Geo& g, uint32_t n, int& b, int& h, int& blk) {
-  const uint32_t u = blockIdx.x + (n >> 1) * gridDim.x;
-  if (u >= g.units) return -1;
-  const uint32_t bh = fastdiv(u, g.div_nunit);
-  const int pu = (int)(u - bh * (uint32_t)g.nunit);
+// Work order.  Item x is one 128-row block of one (b, h).  Causal blocks differ
+// in work by up to nb to 1, so the CTAs take items from a counter, in groups of
+// about 512 blocks ((b, h) pairs that L2 can hold, more than the CTAs in flight),
+// heaviest block first within a group: the last group's light blocks fill the
+// end.  (Equal pairs of blocks dealt out in advance left CTAs idle for 4 % of the
+// time with 64 heads of 32 blocks, for 19 % with 2 of 256 or 16 of 32.)
+__device__ inline void item_at(const AttnBwdParams& p, const Geo& g, int x, bool heavy_last, int& b, int& h, int& blk) {
+  const uint32_t grp = fastdiv((uint32_t)x, g.div_group_items);
+  const uint32_t rem = (uint32_t)x - grp * (uint32_t)(g.group * g.nb);
+  const bool last = x >= g.full;
+  const uint32_t rank = fastdiv(rem, last ? g.div_last : g.div_group);
+  const uint32_t n = last ? (uint32_t)(g.heads - (int)grp * g.group) : (uint32_t)g.group;
+  const uint32_t bh = grp * (uint32_t)g.group + (rem - rank * n);
   b = (int)fastdiv(bh, g.div_h);
   h = (int)(bh - (uint32_t)b * (uint32_t)p.H);
-  if (!p.causal) {
-    blk = pu;
-    return (n & 1) ? 0 : 1;
-  }
-  if ((n & 1) == 0) { blk = g.nb - 1 - pu; return 1; }
-  blk = pu;
-  return pu < g.nb - 1 - pu ? 1 : 0;
+  blk = heavy_last && p.causal ? g.nb - 1 - (int)rank : (int)rank;
+}
+
+// The items go from the producer, which takes them from the counter, to the
+// other warps through a ring in shared memory.  The producer takes and publishes
+// the next item before it loads the current one's last tile: late, so that no
+// CTA holds an item that another could begin, and early enough that no warp
+// waits for it.
+constexpr int kRing = 4;
+struct Ring {
+  volatile int* slot;   // [kRing]
+  uint64_t* full;       // [kRing] 1 arrival
+  uint64_t* empty;      // [kRing] an arrival from each of the 9 other warps
+};
+__device__ inline bool ring_put(const Ring& r, uint32_t n, int x, volatile int* abort_flag) {
+  const int s = n % kRing;
+  if (!mbar_wait(&r.empty[s], ((n / kRing) & 1) ^ 1, abort_flag)) return false;
+  r.slot[s] = x;
+  mbar_arrive(&r.full[s]);
+  return true;
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: A is M rows (lanes) of bf16 pairs, K-major.
@@ -149,6 +168,15 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
 __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const bool ok = mbar_wait(bar, parity, abort_flag);
   return __all_sync(0xffffffffu, ok);
+}
+// The n-th item for a whole warp; false on a wait that gave up.
+__device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int* abort_flag) {
+  const int s = n % kRing;
+  if (!warp_wait(&r.full[s], (n / kRing) & 1, abort_flag)) return false;
+  x = r.slot[s];
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[s]);
+  return true;
 }
 
 // W (16 or 32) columns of an accumulator, from tensor memory at `taddr` (a row
@@ -214,6 +242,7 @@ constexpr int kRowPos = 32, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
   __shared__ float sums[kRowHeads][kRowPos + 1];
+  if (blockIdx.x == 0 && threadIdx.x < 2) p.counter[threadIdx.x] = 0;   // of the launches behind this one
   // block: position group fastest, then head group, then batch
   const int bi = blockIdx.x / ni, i0 = (blockIdx.x - bi * ni) * kRowPos;
   const int b = bi / nh, h0 = (bi - b * nh) * kRowHeads;
@@ -320,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dk_full = bars + 22;
   uint64_t* dk_empty = bars + 23;
   uint64_t* drain = bars + 24;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 25);
+  const Ring ring = {reinterpret_cast<volatile int*>(bars + 34), bars + 25, bars + 29};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -337,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dv_full, 1); mbar_init(dv_empty, 8);
     mbar_init(dk_full, 1); mbar_init(dk_empty, 8);
     mbar_init(drain, 1);
+    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 9); }
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -360,30 +391,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t li = 0, s = 0, ph = 0;
       bool used_kv = false, used_q[kStages] = {}, used_do[kStages] = {};
       uint32_t par_kv = 0, par_q[kStages] = {}, par_do[kStages] = {};
-      for (uint32_t n = 0; !abort_flag; ++n) {
+      int x = atomicAdd(p.counter, 1), x1 = 0;
+      bool ok = ring_put(ring, 0, x, &abort_flag);
+      for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
         int b, h, blk;
-        const int st = next_item(p, g, n, b, h, blk);
-        if (st < 0) break;
-        if (st == 0) continue;
+        item_at(p, g, x, false, b, h, blk);
         const int t0 = first_tile(blk);
         const long long rowbase = ((long long)b * p.H + h) * g.sp;
-        bool ok = true;
         for (int it = t0; it < g.nt; ++it) {
-          if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          if (it == max(t0, g.nt - 2)) x1 = atomicAdd(p.counter, 1);       // used a tile later: its latency is hidden
+          if (it == g.nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&q_full[s], NCH * CQ + 2 * NQ * 4);
           for (int c = 0; c < NCH; ++c)
             tma_load_4d(qbuf + (s * NCH + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
           bulk_load_1d(rowv + s * 2 * NQ, p.nlse + rowbase + it * NQ, NQ * 4, &q_full[s]);
           bulk_load_1d(rowv + s * 2 * NQ + NQ, p.delta + rowbase + it * NQ, NQ * 4, &q_full[s]);
           used_q[s] = true; par_q[s] = ph;
-          if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&do_full[s], NCV * CQ);
           for (int c = 0; c < NCV; ++c)
             tma_load_4d(dobuf + (s * NCV + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
           used_do[s] = true; par_do[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
           if (it == t0) {        // the item's keys and values, behind its first query tile
-            if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+            if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
             mbar_arrive_expect_tx(kv_full, (NCH + NCV) * CH);
             for (int c = 0; c < NCH; ++c) {
               if (c < g.nck) tma_load_4d(kbuf + c * CH, &mp.k, kv_full, 64 * c, h, blk * BM, b);
@@ -393,9 +425,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             used_kv = true; par_kv = li & 1;
           }
         }
-        if (!ok) break;
         ++li;
       }
+      if (!ok) fail();
       // every issued copy must have landed before the CTA may exit
       if (used_kv) mbar_wait(kv_full, par_kv, nullptr);
       for (int i = 0; i < kStages; ++i) {
@@ -460,11 +492,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     };
-    for (uint32_t n = 0;; ++n) {
-      int b, h, blk;
-      const int st = next_item(p, g, n, b, h, blk);
-      if (st < 0) break;
-      if (st == 0) continue;
+    for (;; ) {
+      int x, b, h, blk;
+      if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
+      if (x >= g.items) break;
+      item_at(p, g, x, false, b, h, blk);
       const int nt = g.nt - first_tile(blk);
       // S and dP of the previous item have been read: its last p_full and
       // ds_full were waited for below
@@ -511,11 +543,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* mine = stage + (warp - 2) * 2048;
     uint32_t t = 0, li = 0, s = 0, sph = 0;
     bool bad = false;
-    for (uint32_t n = 0;; ++n) {
-      int b, h, blk;
-      const int st = next_item(p, g, n, b, h, blk);
-      if (st < 0) break;
-      if (st == 0) continue;
+    for (;; ) {
+      int x, b, h, blk;
+      if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
+      if (x >= g.items) break;
+      item_at(p, g, x, false, b, h, blk);
       bool ok = true;
       for (int it = first_tile(blk); it < g.nt; ++it, ++t) {
         const float* nl = rowv + s * 2 * NQ + hf * NH + c0;
@@ -722,7 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_full = bars + 15;
   uint64_t* acc_empty = bars + 16;
   uint64_t* drain = bars + 17;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  const Ring ring = {reinterpret_cast<volatile int*>(bars + 27), bars + 18, bars + 22};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -735,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
     mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
     mbar_init(drain, 1);
+    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 9); }
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -759,15 +793,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t t = 0, li = 0, s = 0, ph = 0, loads = 0;
       bool used_q = false, used_k[kStages] = {};
       uint32_t par_q = 0, par_k[kStages] = {};
-      for (uint32_t n = 0; !abort_flag; ++n) {
+      int x = atomicAdd(p.counter + 1, 1), x1 = 0;
+      bool ok = ring_put(ring, 0, x, &abort_flag);
+      for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
         int b, h, blk;
-        const int st = next_item(p, g, n, b, h, blk);
-        if (st < 0) break;
-        if (st == 0) continue;
+        item_at(p, g, x, true, b, h, blk);
         const int nt = tiles(blk);
-        bool ok = true;
-        for (int it = 0; it < nt && ok; ++it, ++t) {
-          if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { fail(); ok = false; break; }
+        for (int it = 0; it < nt; ++it, ++t) {
+          if (it == max(0, nt - 2)) x1 = atomicAdd(p.counter + 1, 1);      // used a tile later: its latency is hidden
+          if (it == nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[s], NCH * CK);
           for (int c = 0; c < NCH; ++c) {
             uint8_t* dst = kbuf + (s * NCH + c) * CK;
@@ -777,20 +812,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           used_k[s] = true; par_k[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
           if (it == 0) {         // the item's queries, behind its first keys
-            if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+            if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
             mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
             for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
             for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
             used_q = true; par_q = li & 1;
           }
-          if (!mbar_wait(v_empty, (t & 1) ^ 1, &abort_flag)) { fail(); ok = false; break; }
+          if (!mbar_wait(v_empty, (t & 1) ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(v_full, NCV * CK);
           for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + c * CK, &mp.v, v_full, 64 * c, h, it * BN, b);
           ++loads;
         }
-        if (!ok) break;
         ++li;
       }
+      if (!ok) fail();
       if (used_q) mbar_wait(q_full, par_q, nullptr);
       for (int i = 0; i < kStages; ++i) if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
       if (loads) mbar_wait(v_full, (loads - 1) & 1, nullptr);
@@ -834,11 +869,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++tv;
       return true;
     };
-    for (uint32_t n = 0;; ++n) {
-      int b, h, blk;
-      const int st = next_item(p, g, n, b, h, blk);
-      if (st < 0) break;
-      if (st == 0) continue;
+    for (;; ) {
+      int x, b, h, blk;
+      if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
+      if (x >= g.items) break;
+      item_at(p, g, x, true, b, h, blk);
       const int nt = tiles(blk);
       // S and dP of the previous item have been read: its last s_empty and
       // ds_full were waited for below
@@ -888,27 +923,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this item and the next one, whose row values are loaded an item ahead
     int b, h, blk, b1, h1, blk1;
     float nl = 0.f, dl = 0.f, nl1 = 0.f, dl1 = 0.f;
-    uint32_t n = 0;
-    auto fetch = [&]() -> bool {           // the next item: coordinates, nlse and delta of this thread's query
-      int st;
-      while ((st = next_item(p, g, n, b1, h1, blk1)) == 0) ++n;
-      if (st < 0) return false;
-      ++n;
-      const long long at = ((long long)b1 * p.H + h1) * g.sp + blk1 * BM + row;   // inside: sp is padded to whole blocks
-      nl1 = p.nlse[at];
-      dl1 = p.delta[at];
+    bool more = true;
+    auto fetch = [&](uint32_t n) -> bool {   // item n: coordinates, nlse and delta of this thread's query
+      int x;
+      if (!ring_get(ring, n, x, &abort_flag)) return false;
+      more = x < g.items;
+      if (more) {
+        item_at(p, g, x, true, b1, h1, blk1);
+        const long long at = ((long long)b1 * p.H + h1) * g.sp + blk1 * BM + row;   // inside: sp is padded to whole blocks
+        nl1 = p.nlse[at];
+        dl1 = p.delta[at];
+      }
       return true;
     };
-    bool more = fetch();
-    while (more) {
+    bool ok = fetch(0);
+    while (ok && more) {
       b = b1; h = h1; blk = blk1; nl = nl1; dl = dl1;
-      more = fetch();
       const int i = blk * BM + row;                      // this thread's query
       const int nt = tiles(blk);
-      bool ok = true;
       for (int it = 0; it < nt; ++it, ++t) {
         const int j0 = it * BN + hf * NH;
         const bool full = j0 + NH <= p.S && (!p.causal || j0 + NH - 1 <= blk * BM + q * 32);
+        if (it == nt - 1 && !(ok = fetch(li + 1))) break;
         ok = warp_wait(s_full, t & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
@@ -961,7 +997,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ds_full);
       }
       if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
-      if (!ok) { if (lane == 0) fail(); break; }
+      if (!ok) break;
       tc_fence_after();
       {
         const int D = p.d_head + p.d_shared, q0 = blk * BM + q * 32;
@@ -977,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++li;
     }
+    if (!ok && lane == 0) fail();
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
   }
 
@@ -1059,12 +1096,17 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   g.ncv = (p.d_v + 63) / 64;
   g.nb = (p.S + BM - 1) / BM;
   g.nt = (p.S + query_tile(g.nch, g.ncv) - 1) / query_tile(g.nch, g.ncv);
-  g.nunit = p.causal ? (g.nb + 1) / 2 : g.nb;
-  const long long units = (long long)p.B * p.H * g.nunit;
-  if (units >= (1ll << 30)) { snprintf(err, errlen, "%lld work units exceed the kernel's 2^30", units); return false; }
-  g.units = (uint32_t)units;
+  const long long items = (long long)p.B * p.H * g.nb;
+  if (items >= (1ll << 30)) { snprintf(err, errlen, "%lld work items exceed the kernel's 2^30", items); return false; }
+  g.items = (int)items;
+  g.heads = p.B * p.H;
+  g.group = 512 / g.nb < 1 ? 1 : 512 / g.nb;
+  if (g.group > g.heads) g.group = g.heads;
+  g.full = g.heads / g.group * g.group * g.nb;
   g.sp = attn_bwd_padded_rows(p.S);
-  g.div_nunit = make_fastdiv((uint32_t)g.nunit);
+  g.div_group_items = make_fastdiv((uint32_t)(g.group * g.nb));
+  g.div_group = make_fastdiv((uint32_t)g.group);
+  g.div_last = make_fastdiv((uint32_t)(g.heads % g.group ? g.heads % g.group : 1));
   g.div_h = make_fastdiv((uint32_t)p.H);
   return true;
 }
@@ -1072,8 +1114,8 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr int NQ = query_tile(NCH, NCV);
-  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 8 * 2048 + 256;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 8 * 64 * dq_columns(NCH) + 256;
+  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 8 * 2048 + 320;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 8 * 64 * dq_columns(NCH) + 320;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
   static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
@@ -1132,7 +1174,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   rows_kernel<<<(unsigned)(ni * nh * p.B), 256, 0, s>>>(p, (int)g.sp, (int)ni, (int)nh);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int grid = (int)(g.units < (uint32_t)sms ? g.units : (uint32_t)sms);
+  const int grid = (int)(g.items < sms ? g.items : sms);
   using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
   static const Launch by_chunks[3][2] = {{launch_passes<1, 1>, launch_passes<1, 2>},
                                          {launch_passes<2, 1>, launch_passes<2, 2>},

@@ -265,6 +265,7 @@ struct AttnBwdParams {
   float* nlse;             // workspace [B, H, sp]: -lse log2(e), -inf past the sequence
   float* delta;            // workspace [B, H, sp]: do . o
   float* part;             // workspace [B, H, d_shared, S]: per-head gradients of the shared key
+  int* counter;            // workspace [2]: the next work item of the two passes
   int32_t* status;
 };
 long long attn_bwd_padded_rows(int S);                       // sp
