@@ -52,12 +52,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 __host__ __device__ constexpr bool p_apart(int nch, int ncv) { return nch + ncv < 4; }
 __host__ __device__ constexpr int query_tile(int nch, int ncv) { return nch + ncv > 4 ? 96 : 128; }
 __host__ __device__ constexpr int query_stages(int nch, int ncv) { return p_apart(nch, ncv) ? 3 : 2; }
-// Keys per tile of the dQ pass: three stages of 192-wide keys fit with 96.
-__host__ __device__ constexpr int key_tile(int nch) { return nch > 2 ? 96 : 128; }
-constexpr int kStages = 3;               // key tiles of the dQ pass (its values have one)
-// Output columns that a warp of the dQ pass stores at a time, by the shared
-// memory that is left.
-__host__ __device__ constexpr int dq_columns(int nch) { return nch > 2 ? 16 : 32; }
+// Keys per tile of the dQ pass: tensor memory holds dQ (64 nch columns), Q and dO
+// as operands (32 nch, 32 ncv), S and dP (a column per key) and dS (half of one).
+__host__ __device__ constexpr int key_tile(int nch, int ncv) { return nch > 2 ? 64 : nch > 1 ? 96 : 128; }
+constexpr int kKeyStages = 3;            // key and value tiles of the dQ pass
 
 struct Maps {
   CUtensorMap q, k, ks, v, d_o;          // inputs: 64-feature chunks of a tile's rows
@@ -164,6 +162,12 @@ __device__ inline uint32_t pack_bf16(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h2);
 }
 
+// 128 rows x 32 bytes of a K-major operand in shared memory to 8 columns of
+// tensor memory (a row per lane), in order before later products of this thread.
+__device__ inline void tc_cp_128x256b(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
 // All 32 lanes wait; true only if every lane saw the phase complete.
 __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag) {
   const bool ok = mbar_wait(bar, parity, abort_flag);
@@ -173,7 +177,7 @@ __device__ inline bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* a
 __device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int* abort_flag) {
   const int s = n % kRing;
   if (!warp_wait(&r.full[s], (n / kRing) & 1, abort_flag)) return false;
-  x = r.slot[s];
+  x = (int)__reduce_max_sync(0xffffffffu, (unsigned)r.slot[s]);   // the same in every lane, and uniform to the compiler
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[s]);
   return true;
@@ -720,50 +724,57 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // --------------------------------------------------------------------- dQ
-// Tensor memory: dQ [0, 192), S, dP (BN columns each), dS (BN / 2): dS has
-// columns of its own, so S(t+1) starts as soon as S(t) has been read and dP(t+1)
-// as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1), dQ(t).
-// A key tile is held from S(t) to dQ(t), two products later than the next one's
-// S wants its own, so keys have three stages; values are held for one product
-// and have one.  96-key tiles leave room for three stages of 192-wide keys.
+// Q and dO are the A operands of every product of an item but one, so they move
+// from shared memory to tensor memory once per item (tcgen05.cp, a 16-feature
+// k-step at a time) and only keys and values are read from shared memory for the
+// products: with Q and dO there too, S and dP took 85 clocks per instruction
+// instead of 64, and the pass 300 / 412 us on dense_block / k2_mla_layer.
+//
+// dS has columns of its own, so S(t+1) starts as soon as S(t) has been read and
+// dP(t+1) as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1),
+// dQ(t).  A key tile is held from S(t) to dQ(t), two products later than the next
+// one's S wants its own, so keys and values have three stages.
 template <int NCH, int NCV>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
-  constexpr int BN = key_tile(NCH), NH = BN / 2;
-  constexpr int W = dq_columns(NCH);     // of dQ that a warp stores at a time
+  constexpr int BN = key_tile(NCH, NCV), NH = BN / 2;
+  constexpr int kStages = kKeyStages;
+  constexpr int W = 32;                  // columns of dQ that a warp stores at a time
   constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;                                 // NCH chunks
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
-  uint8_t* vbuf = kbuf + kStages * NCH * CK;           // NCV chunks
-  uint8_t* stage = vbuf + NCV * CK;                     // [8 warps][64 W bytes]
+  uint8_t* vbuf = kbuf + kStages * NCH * CK;           // 3 x NCV chunks
+  uint8_t* stage = vbuf + kStages * NCV * CK;                     // [8 warps][64 W bytes]
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 8 * 64 * W);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
   uint64_t* k_empty = bars + 5;     // [3]
-  uint64_t* v_full = bars + 8;
-  uint64_t* v_empty = bars + 9;
-  uint64_t* s_full = bars + 10;
-  uint64_t* s_empty = bars + 11;
-  uint64_t* dp_full = bars + 12;
-  uint64_t* ds_full = bars + 13;
-  uint64_t* ds_empty = bars + 14;
-  uint64_t* acc_full = bars + 15;
-  uint64_t* acc_empty = bars + 16;
-  uint64_t* drain = bars + 17;
-  const Ring ring = {reinterpret_cast<volatile int*>(bars + 27), bars + 18, bars + 22};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  uint64_t* v_full = bars + 8;      // [3]
+  uint64_t* v_empty = bars + 11;    // [3]
+  uint64_t* s_full = bars + 14;
+  uint64_t* s_empty = bars + 15;
+  uint64_t* dp_full = bars + 16;
+  uint64_t* ds_full = bars + 17;
+  uint64_t* ds_empty = bars + 18;
+  uint64_t* acc_full = bars + 19;
+  uint64_t* acc_empty = bars + 20;
+  uint64_t* drain = bars + 21;
+  const Ring ring = {reinterpret_cast<volatile int*>(bars + 31), bars + 22, bars + 26};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   __shared__ volatile int abort_flag;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
-    for (int s = 0; s < kStages; ++s) { mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1); }
-    mbar_init(v_full, 1); mbar_init(v_empty, 1);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1);
+    }
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
     mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
@@ -780,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const uint32_t t_dq = tmem_base, t_s = tmem_base + 192, t_dp = t_s + BN, t_ds = t_dp + BN;
+  const uint32_t t_dq = tmem_base, t_q = t_dq + 64 * NCH, t_do = t_q + 32 * NCH, t_s = t_do + 32 * NCV, t_dp = t_s + BN, t_ds = t_dp + BN;
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   auto tiles = [&](int blk) {
     const int hi = p.causal ? min(p.S, (blk + 1) * BM) : p.S;
@@ -790,16 +801,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t t = 0, li = 0, s = 0, ph = 0, loads = 0;
-      bool used_q = false, used_k[kStages] = {};
-      uint32_t par_q = 0, par_k[kStages] = {};
+      uint32_t li = 0, s = 0, ph = 0;
+      bool used_q = false, used_k[kStages] = {}, used_v[kStages] = {};
+      uint32_t par_q = 0, par_k[kStages] = {}, par_v[kStages] = {};
       int x = atomicAdd(p.counter + 1, 1), x1 = 0;
       bool ok = ring_put(ring, 0, x, &abort_flag);
       for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
         int b, h, blk;
         item_at(p, g, x, true, b, h, blk);
         const int nt = tiles(blk);
-        for (int it = 0; it < nt; ++it, ++t) {
+        // the queries' buffer is free once the item before has begun
+        if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
+        mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
+        for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
+        for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
+        used_q = true; par_q = li & 1;
+        for (int it = 0; it < nt; ++it) {
           if (it == max(0, nt - 2)) x1 = atomicAdd(p.counter + 1, 1);      // used a tile later: its latency is hidden
           if (it == nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
           if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
@@ -810,25 +827,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
           }
           used_k[s] = true; par_k[s] = ph;
+          if (!mbar_wait(&v_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(&v_full[s], NCV * CK);
+          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + (s * NCV + c) * CK, &mp.v, &v_full[s], 64 * c, h, it * BN, b);
+          used_v[s] = true; par_v[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
-          if (it == 0) {         // the item's queries, behind its first keys
-            if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
-            mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
-            for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
-            for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
-            used_q = true; par_q = li & 1;
-          }
-          if (!mbar_wait(v_empty, (t & 1) ^ 1, &abort_flag)) { ok = false; break; }
-          mbar_arrive_expect_tx(v_full, NCV * CK);
-          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + c * CK, &mp.v, v_full, 64 * c, h, it * BN, b);
-          ++loads;
         }
         ++li;
       }
       if (!ok) fail();
       if (used_q) mbar_wait(q_full, par_q, nullptr);
-      for (int i = 0; i < kStages; ++i) if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
-      if (loads) mbar_wait(v_full, (loads - 1) & 1, nullptr);
+      for (int i = 0; i < kStages; ++i) {
+        if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
+        if (used_v[i]) mbar_wait(&v_full[i], par_v[i], nullptr);
+      }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -837,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint64_t dq_ = make_sdesc_sw128(smem_u32(qbuf), 16, 1024), ddo_ = make_sdesc_sw128(smem_u32(dobuf), 16, 1024);
     const uint64_t dk_ = make_sdesc_sw128(smem_u32(kbuf), 16, 1024), dv_ = make_sdesc_sw128(smem_u32(vbuf), 16, 1024);
     const uint64_t mk_ = make_sdesc(smem_u32(kbuf), CK, 1024, 2);
-    uint32_t t = 0, tv = 0, li = 0, ks = 0, kph = 0, kd = 0;   // tiles, value tiles, items; key stage of S and of dQ
+    uint32_t t = 0, li = 0, ks = 0, kph = 0, vs = 0, vph = 0, kd = 0;   // tiles, items; stages of S, of dP and of dQ
     bool issued = false;
     auto scores = [&]() -> bool {          // S = Q K^T
       if (!warp_wait(&k_full[ks], kph, &abort_flag)) return false;
@@ -846,27 +858,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCH; ++c)
-          tc_mma(t_s, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+          tc_mma_ts(t_s, t_q + c * 8, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(s_full);
       }
       __syncwarp();
       if (++ks == kStages) { ks = 0; kph ^= 1; }
       return true;
     };
-    // dP = dO V^T; `last`: the item's queries and gradients are free after it
-    auto dprobs = [&](bool last) -> bool {
-      if (!warp_wait(v_full, tv & 1, &abort_flag)) return false;
+    auto dprobs = [&]() -> bool {          // dP = dO V^T
+      if (!warp_wait(&v_full[vs], vph, &abort_flag)) return false;
       tc_fence_after();
+      const uint64_t v0 = dv_ + vs * (NCV * CK / 16);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCV; ++c)
-          tc_mma(t_dp, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16, dv_ + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
-        tc_commit(v_empty);
+          tc_mma_ts(t_dp, t_do + c * 8, v0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+        tc_commit(&v_empty[vs]);
         tc_commit(dp_full);
-        if (last) tc_commit(q_empty);
       }
       __syncwarp();
-      ++tv;
+      if (++vs == kStages) { vs = 0; vph ^= 1; }
       return true;
     };
     for (;; ) {
@@ -875,18 +886,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x >= g.items) break;
       item_at(p, g, x, true, b, h, blk);
       const int nt = tiles(blk);
-      // S and dP of the previous item have been read: its last s_empty and
-      // ds_full were waited for below
-      bool ok = warp_wait(q_full, li & 1, &abort_flag) && scores();
+      // The previous item's S and dP are done and have been read: its last
+      // s_empty and ds_full were waited for below.  So its queries may be
+      // overwritten.
+      bool ok = warp_wait(q_full, li & 1, &abort_flag);
       if (!ok) { fail(); break; }
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < 4 * NCH; ++c) tc_cp_128x256b(t_q + c * 8, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
+#pragma unroll
+        for (int c = 0; c < 4 * NCV; ++c) tc_cp_128x256b(t_do + c * 8, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
+        tc_commit(q_empty);
+      }
+      __syncwarp();
       issued = true;
-      if (!dprobs(nt == 1)) { fail(); break; }
+      if (!scores() || !dprobs()) { fail(); break; }
       for (int i = 0; i < nt; ++i, ++t) {
         if (!warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
         if (i + 1 < nt && !scores()) { ok = false; break; }
         if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
+        if (i + 1 < nt && !dprobs()) { ok = false; break; }
         if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint64_t k0 = mk_ + kd * (NCH * CK / 16);
@@ -1115,9 +1136,9 @@ template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr int NQ = query_tile(NCH, NCV);
   constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 8 * 2048 + 320;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)(kStages * NCH + NCV) * key_tile(NCH) * 128 + 8 * 64 * dq_columns(NCH) + 320;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)kKeyStages * (NCH + NCV) * key_tile(NCH, NCV) * 128 + 8 * 2048 + 320;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
-  static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 192 + 5 * key_tile(NCH) / 2 <= 512, "tensor memory");
+  static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 96 * NCH + 32 * NCV + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
   if (e != cudaSuccess) return e;
   dkv_kernel<NCH, NCV><<<grid, kThreads, skv, s>>>(p, kv, g);
@@ -1156,7 +1177,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   Geo g;
   if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
   const int nq = query_tile(g.nch, g.ncv), D = p.d_head + p.d_shared;
-  const int nk = key_tile(g.nch);
+  const int nk = key_tile(g.nch, g.ncv);
   Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (nk-row keys, 128-row queries)
   memset(&kv, 0, sizeof kv);
   bool ok = encode(&kv.q, p.q, D, p.H, p.S, p.B, p.qs, nq) && encode(&kv.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, BM) &&
