@@ -37,7 +37,12 @@ namespace {
 namespace ab {
 
 constexpr int BM = 128;                  // rows of a work item: keys (dkv) or queries (dq)
-constexpr int kThreads = 320;            // producer, MMA issuer, 8 compute warps
+// Warps: 0 producer, 1 MMA issuer, 2 and 3 idle, 4..7 output, 8..15 compute (a
+// warp reads the tensor-memory lanes of its index mod 4).  The launch's 128
+// registers a thread are dealt out again per group of four warps: the sum over
+// the groups, 96 + 80 + 168 + 168, is the launch's 4 x 128.
+constexpr int kThreads = 512;
+constexpr int kRegsIssue = 96, kRegsOutput = 80, kRegsCompute = 168;
 constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk (128-byte swizzle)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -100,7 +105,7 @@ constexpr int kRing = 4;
 struct Ring {
   volatile int* slot;   // [kRing]
   uint64_t* full;       // [kRing] 1 arrival
-  uint64_t* empty;      // [kRing] an arrival from each of the 9 other warps
+  uint64_t* empty;      // [kRing] an arrival from each of the 13 other warps
 };
 __device__ inline bool ring_put(const Ring& r, uint32_t n, int x, volatile int* abort_flag) {
   const int s = n % kRing;
@@ -120,6 +125,11 @@ __device__ inline void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdes
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+template <int N>
+__device__ inline void regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ inline void regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // True in one lane of the (whole) warp.  The MMA issuer runs as a whole warp
 // with the products under this predicate, so that descriptors stay in uniform
 // registers.
@@ -334,8 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
   uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
   float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, delta][NQ]
-  uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [8 warps][2 KB]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 8 * 2048);
+  uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [4 warps][2 KB]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * 2048);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
   uint64_t* q_full = bars + 2;      // [stages <= 3] Q tile with its nlse and delta
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
   __shared__ volatile int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform to the compiler
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
@@ -368,10 +378,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(p_full, 8); mbar_init(p_empty, 1);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8);
-    mbar_init(dv_full, 1); mbar_init(dv_empty, 8);
-    mbar_init(dk_full, 1); mbar_init(dk_empty, 8);
+    mbar_init(dv_full, 1); mbar_init(dv_empty, 4);
+    mbar_init(dk_full, 1); mbar_init(dk_empty, 4);
     mbar_init(drain, 1);
-    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 9); }
+    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 13); }
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -389,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // first query tile that has a query at or behind the block's first key
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
 
+  if (warp < 4) regs_release<kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -533,20 +544,81 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(drain, 0, nullptr);
     }
-  } else {
-    // ------------------------------------------------------------ P, dS, epilogue
-    // Warp e = warp - 2: keys 32 q .. 32 q + 31 of the block (q = warp & 3, its
-    // TMEM lane quadrant), queries of half e >> 2 of the tile; in the epilogue
-    // that half of the dK and dV columns.  A thread holds keys r0, r0 + 8,
-    // r0 + 16, r0 + 24 and, of each 8 queries, the two from c0.
-    const int q = warp & 3, hf = (warp - 2) >> 2;
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ output
+    // Warp w: keys 32 q .. 32 q + 31 of the block, every column: dV as soon as the
+    // item's last dV product is done, then scale * dK (the shared key's columns go
+    // to the per-head fp32 partial sums), while the other warps are at the next
+    // item.
+    regs_release<kRegsOutput>();
+    const int q = warp & 3;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    uint8_t* mine = stage + q * 2048;
+    uint32_t li = 0;
+    bool bad = false, ok = true;
+    for (;; ++li) {
+      int x, b, h, blk;
+      if (!(ok = ring_get(ring, li, x, &abort_flag)) || x >= g.items) break;
+      item_at(p, g, x, false, b, h, blk);
+      const int key0 = blk * BM + q * 32, rows = p.S - key0;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key0 * p.dvs[1] + h * p.dvs[2];
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key0 * p.dks[1] + h * p.dks[2];
+#pragma unroll 1
+      for (int c = 0; c < 2 * (NCV + NCH); ++c) {
+        const bool is_v = c < 2 * NCV;
+        if (c == 0 || c == 2 * NCV) {
+          ok = warp_wait(is_v ? dv_full : dk_full, li & 1, &abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const int col = 32 * (is_v ? c : c - 2 * NCV);
+        const uint32_t from = (is_v ? t_dv : t_dk) + lanes + col;
+        if (is_v || col < 64 * g.nck) {
+          const int n = (is_v ? p.d_v : p.d_head) - col;
+          if (n > 0)
+            bad |= store_rows<32>(from, (is_v ? dv : dk) + col, is_v ? p.dvs[1] : p.dks[1], mine, is_v ? 1.f : p.scale, rows, n);
+        } else {                           // [b][h][feature][position]: 32 keys are 128 bytes
+          const int f0 = col - p.d_head;
+          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key0 + lane;
+#pragma unroll 1
+          for (int y = 0; y < 32; y += 16) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16_async(from + y, r);
+            tmem_ld_wait();
+            reg_fence16(r);
+            float z = 0.f;
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float v = __uint_as_float(r[x]) * p.scale;
+              z = fmaf(v, 0.f, z);
+              if (lane < rows && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
+            }
+            bad |= z != z && lane < rows;
+            __syncwarp();
+          }
+        }
+        if (c == 2 * NCV - 1 || c == 2 * (NCV + NCH) - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(is_v ? dv_empty : dk_empty);
+        }
+      }
+      if (!ok) break;
+    }
+    if (!ok && lane == 0) fail();
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ P, dS
+    regs_acquire<kRegsCompute>();
+    // Warp e = warp - 8: keys 32 q .. 32 q + 31 of the block (q = warp & 3, its
+    // TMEM lane quadrant), queries of half e >> 2 of the tile.  A thread holds
+    // keys r0, r0 + 8, r0 + 16, r0 + 24 and, of each 8 queries, the two from c0.
+    const int q = warp & 3, hf = (warp - 8) >> 2;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tp = t_p + lanes + hf * kHalfP;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
     const float c2 = p.scale * kLog2e;
-    uint8_t* mine = stage + (warp - 2) * 2048;
     uint32_t t = 0, li = 0, s = 0, sph = 0;
-    bool bad = false;
     for (;; ) {
       int x, b, h, blk;
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
@@ -663,56 +735,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(ds_full);
         if (++s == kStages) { s = 0; sph ^= 1; }
       }
-      // ---- epilogue: dV, then scale * dK; the shared key's columns go to the
-      // per-head fp32 partial sums.  Each half of the warps takes half of the
-      // columns.
-      const int key0 = blk * BM + q * 32, rows = p.S - key0;
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key0 * p.dvs[1] + h * p.dvs[2];
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key0 * p.dks[1] + h * p.dks[2];
-#pragma unroll 1
-      for (int c = 0; ok && c < NCV + NCH; ++c) {
-        const bool is_v = c < NCV;
-        if (c == 0 || c == NCV) {
-          ok = warp_wait(is_v ? dv_full : dk_full, li & 1, &abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const int col = is_v ? hf * 32 * NCV + c * 32 : hf * 32 * NCH + (c - NCV) * 32;
-        const uint32_t from = (is_v ? t_dv : t_dk) + lanes + col;
-        if (is_v || col < 64 * g.nck) {
-          const int n = (is_v ? p.d_v : p.d_head) - col;
-          if (n > 0)
-            bad |= store_rows<32>(from, (is_v ? dv : dk) + col, is_v ? p.dvs[1] : p.dks[1], mine, is_v ? 1.f : p.scale, rows, n);
-        } else {                           // [b][h][feature][position]: 32 keys are 128 bytes
-          const int f0 = col - p.d_head;
-          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key0 + lane;
-#pragma unroll 1
-          for (int y = 0; y < 32; y += 16) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16_async(from + y, r);
-            tmem_ld_wait();
-            reg_fence16(r);
-            float z = 0.f;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float v = __uint_as_float(r[x]) * p.scale;
-              z = fmaf(v, 0.f, z);
-              if (lane < rows && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
-            }
-            bad |= z != z && lane < rows;
-            __syncwarp();
-          }
-        }
-        if (c == NCV - 1 || c == NCV + NCH - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(is_v ? dv_empty : dk_empty);
-        }
-      }
       if (!ok) { if (lane == 0) fail(); break; }
       ++li;
     }
-    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
   }
 
   tc_fence_before();
@@ -739,7 +764,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
   constexpr int BN = key_tile(NCH, NCV), NH = BN / 2;
   constexpr int kStages = kKeyStages;
-  constexpr int W = 32;                  // columns of dQ that a warp stores at a time
   constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -747,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
   uint8_t* vbuf = kbuf + kStages * NCH * CK;           // 3 x NCV chunks
-  uint8_t* stage = vbuf + kStages * NCV * CK;                     // [8 warps][64 W bytes]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 8 * 64 * W);
+  uint8_t* stage = vbuf + kStages * NCV * CK;                     // [4 warps][2 KB]
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * 2048);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
@@ -767,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   __shared__ volatile int abort_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform to the compiler
   if (threadIdx.x == 0) {
     abort_flag = 0;
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
@@ -777,9 +801,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
-    mbar_init(acc_full, 1); mbar_init(acc_empty, 8);
+    mbar_init(acc_full, 1); mbar_init(acc_empty, 4);
     mbar_init(drain, 1);
-    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 9); }
+    for (int s = 0; s < kRing; ++s) { mbar_init(&ring.full[s], 1); mbar_init(&ring.empty[s], 13); }
     fence_mbar_init();
   }
   if (warp == 0 && lane == 0) {
@@ -798,6 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (hi + BN - 1) / BN;
   };
 
+  if (warp < 4) regs_release<kRegsIssue>();
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
@@ -931,16 +956,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(drain, 0, nullptr);
     }
-  } else {
-    // ------------------------------------------------------------ P, dS, epilogue
-    const int q = warp & 3, hf = (warp - 2) >> 2;
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------ output
+    // Warp w: queries 32 q .. 32 q + 31 of the block: scale * dQ, while the other
+    // warps are at the next item
+    regs_release<kRegsOutput>();
+    const int q = warp & 3, D = p.d_head + p.d_shared;
+    const uint32_t lanes = (uint32_t)(q * 32) << 16;
+    uint8_t* mine = stage + q * 2048;
+    bool bad = false, ok = true;
+    for (uint32_t li = 0;; ++li) {
+      int x, b, h, blk;
+      if (!(ok = ring_get(ring, li, x, &abort_flag)) || x >= g.items) break;
+      item_at(p, g, x, true, b, h, blk);
+      if (!(ok = warp_wait(acc_full, li & 1, &abort_flag))) break;
+      tc_fence_after();
+      const int q0 = blk * BM + q * 32;
+      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + q0 * p.dqs[1] + h * p.dqs[2];
+#pragma unroll 1
+      for (int col = 0; col < D; col += 32)
+        bad |= store_rows<32>(t_dq + lanes + col, dq + col, p.dqs[1], mine, p.scale, p.S - q0, D - col);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(acc_empty);
+    }
+    if (!ok && lane == 0) fail();
+    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------ P, dS
+    regs_acquire<kRegsCompute>();
+    const int q = warp & 3, hf = (warp - 8) >> 2;
     const int row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tds = t_ds + lanes + hf * (NH / 2);
     const float c2 = p.scale * kLog2e;
-    uint8_t* mine = stage + (warp - 2) * 64 * W;
     uint32_t t = 0, li = 0;
-    bool bad = false;
     // this item and the next one, whose row values are loaded an item ahead
     int b, h, blk, b1, h1, blk1;
     float nl = 0.f, dl = 0.f, nl1 = 0.f, dl1 = 0.f;
@@ -1017,25 +1067,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full);
       }
-      if (ok) ok = warp_wait(acc_full, li & 1, &abort_flag);
       if (!ok) break;
-      tc_fence_after();
-      {
-        const int D = p.d_head + p.d_shared, q0 = blk * BM + q * 32;
-        __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + q0 * p.dqs[1] + h * p.dqs[2];
-#pragma unroll 1
-        for (int c = 0; c < 32 * NCH / W; ++c) {
-          const int col = hf * 32 * NCH + c * W;
-          if (col < D) bad |= store_rows<W>(t_dq + lanes + col, dq + col, p.dqs[1], mine, p.scale, p.S - q0, D - col);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(acc_empty);
-      }
       ++li;
     }
     if (!ok && lane == 0) fail();
-    if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
   }
 
   tc_fence_before();
@@ -1135,8 +1170,8 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr int NQ = query_tile(NCH, NCV);
-  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 8 * 2048 + 320;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)kKeyStages * (NCH + NCV) * key_tile(NCH, NCV) * 128 + 8 * 2048 + 320;
+  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 4 * 2048 + 320;
+  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)kKeyStages * (NCH + NCV) * key_tile(NCH, NCV) * 128 + 4 * 2048 + 320;
   static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
   static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 96 * NCH + 32 * NCV + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
   cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
