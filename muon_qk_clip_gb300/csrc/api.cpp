@@ -1071,7 +1071,7 @@ mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, vo
   p.dq = g->dq; p.dk = g->dk; p.dksh = g->dk_shared; p.dv = g->dv;
   char* base = static_cast<char*>(workspace);
   p.nlse = reinterpret_cast<float*>(base + w.nlse);
-  p.delta = reinterpret_cast<float*>(base + w.delta);
+  p.ndelta = reinterpret_cast<float*>(base + w.delta);
   p.part = reinterpret_cast<float*>(base + w.part);
   p.counter = reinterpret_cast<int*>(base + w.counter);
   cudaError_t e;

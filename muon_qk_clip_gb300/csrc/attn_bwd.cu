@@ -167,6 +167,40 @@ __device__ inline void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
+// Two fp32 operations in one instruction.
+__device__ inline unsigned long long two(float a, float b) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ inline void untwo(unsigned long long v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ inline unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ inline unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ inline unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// p <- 2^(s c2 + n) and p <- p (d + n) for two values given as raw fp32 bits
+__device__ inline void probs2(float& p0, float& p1, uint32_t s0, uint32_t s1, unsigned long long c2, unsigned long long n) {
+  untwo(fma2(two(__uint_as_float(s0), __uint_as_float(s1)), c2, n), p0, p1);
+  p0 = ex2_approx(p0);
+  p1 = ex2_approx(p1);
+}
+__device__ inline void dscores2(float& p0, float& p1, uint32_t d0, uint32_t d1, unsigned long long n) {
+  untwo(mul2(two(p0, p1), add2(two(__uint_as_float(d0), __uint_as_float(d1)), n)), p0, p1);
+}
+
 __device__ inline uint32_t pack_bf16(float a, float b) {
   __nv_bfloat162 h2 = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t*>(&h2);
@@ -247,7 +281,7 @@ __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long 
 }
 
 // ------------------------------------------------------------------- rows
-// delta_i = sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
+// -delta_i = -sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
 // in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
 // delta = 0.  A block takes 32 positions of 8 heads: 16 lanes per row with 8
 // features each, 16 rows in flight per thread group pass, the results written
@@ -305,7 +339,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
   const int h = h0 + threadIdx.x / 32, i = i0 + threadIdx.x % 32;
   if (h < p.H && i < sp) {
     const long long bh = (long long)b * p.H + h;
-    p.delta[bh * sp + i] = sums[threadIdx.x / 32][threadIdx.x % 32];
+    p.ndelta[bh * sp + i] = -sums[threadIdx.x / 32][threadIdx.x % 32];
     p.nlse[bh * sp + i] = i < p.S ? -p.lse[bh * p.S + i] * kLog2e : -INFINITY;
   }
 }
@@ -343,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* vbuf = kbuf + NCH * CH;                         // NCV chunks
   uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
   uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
-  float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, delta][NQ]
+  float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, -delta][NQ]
   uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [4 warps][2 KB]
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * 2048);
   uint64_t* kv_full = bars + 0;
@@ -421,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < NCH; ++c)
             tma_load_4d(qbuf + (s * NCH + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
           bulk_load_1d(rowv + s * 2 * NQ, p.nlse + rowbase + it * NQ, NQ * 4, &q_full[s]);
-          bulk_load_1d(rowv + s * 2 * NQ + NQ, p.delta + rowbase + it * NQ, NQ * 4, &q_full[s]);
+          bulk_load_1d(rowv + s * 2 * NQ + NQ, p.ndelta + rowbase + it * NQ, NQ * 4, &q_full[s]);
           used_q[s] = true; par_q[s] = ph;
           if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&do_full[s], NCV * CQ);
@@ -618,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tp = t_p + lanes + hf * kHalfP;
     const int r0 = lane >> 2, c0 = 2 * (lane & 3);
     const float c2 = p.scale * kLog2e;
+    const unsigned long long c22 = two(c2, c2);
     uint32_t t = 0, li = 0, s = 0, sph = 0;
     for (;; ) {
       int x, b, h, blk;
@@ -654,14 +689,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int u = 0; u < NU; ++u)
 #pragma unroll
             for (int m = 0; m < 2; ++m) {
-              const float2 l = *reinterpret_cast<const float2*>(nl + u * 16 + m * 8);
+              const unsigned long long l = *reinterpret_cast<const unsigned long long*>(nl + u * 16 + m * 8);
 #pragma unroll
               for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-                for (int x = 0; x < 4; x += 2) {
-                  pv[u][hh][4 * m + x] = ex2_approx(fmaf(__uint_as_float(r[u][hh][4 * m + x]), c2, l.x));
-                  pv[u][hh][4 * m + x + 1] = ex2_approx(fmaf(__uint_as_float(r[u][hh][4 * m + x + 1]), c2, l.y));
-                }
+                for (int x = 4 * m; x < 4 * m + 4; x += 2)
+                  probs2(pv[u][hh][x], pv[u][hh][x + 1], r[u][hh][x], r[u][hh][x + 1], c22, l);
             }
         }
         if (diag) {
@@ -713,14 +746,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (u + 1 < NU) load(u + 1);
 #pragma unroll
           for (int m = 0; m < 2; ++m) {
-            const float2 d = *reinterpret_cast<const float2*>(nl + NQ + u * 16 + m * 8);
+            const unsigned long long d = *reinterpret_cast<const unsigned long long*>(nl + NQ + u * 16 + m * 8);
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-              for (int x = 0; x < 4; x += 2) {
-                pv[u][hh][4 * m + x] *= __uint_as_float(r[u & 1][hh][4 * m + x]) - d.x;
-                pv[u][hh][4 * m + x + 1] *= __uint_as_float(r[u & 1][hh][4 * m + x + 1]) - d.y;
-              }
+              for (int x = 4 * m; x < 4 * m + 4; x += 2)
+                dscores2(pv[u][hh][x], pv[u][hh][x + 1], r[u & 1][hh][x], r[u & 1][hh][x + 1], d);
           }
 #pragma unroll
           for (int hh = 0; hh < 2; ++hh) {
@@ -990,6 +1021,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     const uint32_t ts = t_s + lanes + hf * NH, tdp = t_dp + lanes + hf * NH, tds = t_ds + lanes + hf * (NH / 2);
     const float c2 = p.scale * kLog2e;
+    const unsigned long long c22 = two(c2, c2);
     uint32_t t = 0, li = 0;
     // this item and the next one, whose row values are loaded an item ahead
     int b, h, blk, b1, h1, blk1;
@@ -1003,13 +1035,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         item_at(p, g, x, true, b1, h1, blk1);
         const long long at = ((long long)b1 * p.H + h1) * g.sp + blk1 * BM + row;   // inside: sp is padded to whole blocks
         nl1 = p.nlse[at];
-        dl1 = p.delta[at];
+        dl1 = p.ndelta[at];
       }
       return true;
     };
     bool ok = fetch(0);
     while (ok && more) {
       b = b1; h = h1; blk = blk1; nl = nl1; dl = dl1;
+      const unsigned long long nl2 = two(nl, nl), dl2 = two(dl, dl);
       const int i = blk * BM + row;                      // this thread's query
       const int nt = tiles(blk);
       for (int it = 0; it < nt; ++it, ++t) {
@@ -1031,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(s_empty);
 #pragma unroll
-          for (int x = 0; x < NH; ++x) pv[x] = ex2_approx(fmaf(__uint_as_float(r[x / 16][x % 16]), c2, nl));
+          for (int x = 0; x < NH; x += 2) probs2(pv[x], pv[x + 1], r[x / 16][x % 16], r[x / 16][x % 16 + 1], c22, nl2);
         }
         ok = warp_wait(dp_full, t & 1, &abort_flag);
         if (!ok) break;
@@ -1044,7 +1077,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < NH / 16; ++c) reg_fence16(r[c]);
 #pragma unroll
-          for (int x = 0; x < NH; ++x) pv[x] *= __uint_as_float(r[x / 16][x % 16]) - dl;
+          for (int x = 0; x < NH; x += 2) dscores2(pv[x], pv[x + 1], r[x / 16][x % 16], r[x / 16][x % 16 + 1], dl2);
         }
         if (!full) {
           const int lim = p.causal ? min(i, p.S - 1) : p.S - 1;   // last key of this row

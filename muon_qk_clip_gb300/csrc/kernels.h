@@ -263,7 +263,7 @@ struct AttnBwdParams {
   long long qs[3], kst[3], kss[2], vs[3], os[3], dos[3];     // element strides (batch, seq, head)
   long long dqs[3], dks[3], dkshs[2], dvs[3];
   float* nlse;             // workspace [B, H, sp]: -lse log2(e), -inf past the sequence
-  float* delta;            // workspace [B, H, sp]: do . o
+  float* ndelta;           // workspace [B, H, sp]: -do . o
   float* part;             // workspace [B, H, d_shared, S]: per-head gradients of the shared key
   int* counter;            // workspace [2]: the next work item of the two passes
   int32_t* status;
