@@ -40,9 +40,9 @@ constexpr int BM = 128;                  // rows of a work item: keys (dkv) or q
 // Warps: 0 producer, 1 MMA issuer, 2 and 3 idle, 4..7 output, 8..15 compute (a
 // warp reads the tensor-memory lanes of its index mod 4).  The launch's 128
 // registers a thread are dealt out again per group of four warps: the sum over
-// the groups, 96 + 80 + 168 + 168, is the launch's 4 x 128.
+// the groups, 88 + 72 + 176 + 176, is the launch's 4 x 128.
 constexpr int kThreads = 512;
-constexpr int kRegsIssue = 96, kRegsOutput = 80, kRegsCompute = 168;
+constexpr int kRegsIssue = 88, kRegsOutput = 72, kRegsCompute = 176;
 constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk (128-byte swizzle)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -284,8 +284,8 @@ __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long 
 // -delta_i = -sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
 // in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
 // delta = 0.  A block takes 32 positions of 8 heads: 16 lanes per row with 8
-// features each, 16 rows in flight per thread group pass, the results written
-// through shared memory so that a warp stores 32 positions of a head.
+// features each, the results written through shared memory so that a warp stores
+// 32 positions of a head.
 constexpr int kRowPos = 32, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
@@ -296,44 +296,48 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
   const int b = bi / nh, h0 = (bi - b * nh) * kRowHeads;
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int c0 = sub * 8;
-  constexpr int N = kRowPos * kRowHeads / 16;            // rows per group
-  uint4 a[N], e[N];
-  bool live[N];
   // row x: head h0 + x % 8 of position i0 + x / 8 (neighbouring heads are
-  // neighbours in memory)
+  // neighbours in memory); four rows of a group in flight
+#pragma unroll 1
+  for (int x0 = group; x0 < kRowPos * kRowHeads; x0 += 64) {
+    uint4 a[4], e[4];
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int x = n * 16 + group, h = h0 + x % kRowHeads, i = i0 + x / kRowHeads;
-    live[n] = h < p.H && i < p.S;
-    a[n] = e[n] = make_uint4(0, 0, 0, 0);
-    if (live[n] && c0 < p.d_v) {
-      const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + i * p.os[1] + h * p.os[2];
-      const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + i * p.dos[1] + h * p.dos[2];
-      if (c0 + 8 <= p.d_v) {
-        a[n] = *reinterpret_cast<const uint4*>(o + c0);
-        e[n] = *reinterpret_cast<const uint4*>(d + c0);
-      } else {
-        __nv_bfloat16* ta = reinterpret_cast<__nv_bfloat16*>(&a[n]);
-        __nv_bfloat16* te = reinterpret_cast<__nv_bfloat16*>(&e[n]);
+    for (int n = 0; n < 4; ++n) {
+      const int x = x0 + 16 * n, h = h0 + x % kRowHeads, i = i0 + x / kRowHeads;
+      a[n] = e[n] = make_uint4(0, 0, 0, 0);
+      if (h < p.H && i < p.S && c0 < p.d_v) {
+        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + i * p.os[1] + h * p.os[2];
+        const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + i * p.dos[1] + h * p.dos[2];
+        if (c0 + 8 <= p.d_v) {
+          a[n] = *reinterpret_cast<const uint4*>(o + c0);
+          e[n] = *reinterpret_cast<const uint4*>(d + c0);
+        } else {
+          uint32_t wa[4] = {}, we[4] = {};
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          if (c0 + c < p.d_v) { ta[c] = o[c0 + c]; te[c] = d[c0 + c]; }
+          for (int c = 0; c < 7; ++c)
+            if (c0 + c < p.d_v) {
+              wa[c / 2] |= (uint32_t)__bfloat16_as_ushort(o[c0 + c]) << (16 * (c % 2));
+              we[c / 2] |= (uint32_t)__bfloat16_as_ushort(d[c0 + c]) << (16 * (c % 2));
+            }
+          a[n] = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+          e[n] = make_uint4(we[0], we[1], we[2], we[3]);
+        }
       }
     }
-  }
 #pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const uint32_t wa[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, we[4] = {e[n].x, e[n].y, e[n].z, e[n].w};
-    float s = 0.f;
+    for (int n = 0; n < 4; ++n) {
+      const uint32_t wa[4] = {a[n].x, a[n].y, a[n].z, a[n].w}, we[4] = {e[n].x, e[n].y, e[n].z, e[n].w};
+      float s = 0.f;
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      s = fmaf(__uint_as_float(wa[x] << 16), __uint_as_float(we[x] << 16), s);
-      s = fmaf(__uint_as_float(wa[x] & 0xffff0000u), __uint_as_float(we[x] & 0xffff0000u), s);
+      for (int x = 0; x < 4; ++x) {
+        s = fmaf(__uint_as_float(wa[x] << 16), __uint_as_float(we[x] << 16), s);
+        s = fmaf(__uint_as_float(wa[x] & 0xffff0000u), __uint_as_float(we[x] & 0xffff0000u), s);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const int x = x0 + 16 * n;
+      if (sub == 0) sums[x % kRowHeads][x / kRowHeads] = s;
     }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int x = n * 16 + group;
-    if (sub == 0) sums[x % kRowHeads][x / kRowHeads] = s;
   }
   __syncthreads();
   const int h = h0 + threadIdx.x / 32, i = i0 + threadIdx.x % 32;
