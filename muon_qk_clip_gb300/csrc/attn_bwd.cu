@@ -167,30 +167,6 @@ __device__ inline void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-// Two fp32 operations in one instruction.
-__device__ inline unsigned long long two(float a, float b) {
-  unsigned long long r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ inline void untwo(unsigned long long v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ inline unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-  unsigned long long r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ inline unsigned long long add2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ inline unsigned long long mul2(unsigned long long a, unsigned long long b) {
-  unsigned long long r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 // p <- 2^(s c2 + n) and p <- p (d + n) for two values given as raw fp32 bits
 __device__ inline void probs2(float& p0, float& p1, uint32_t s0, uint32_t s1, unsigned long long c2, unsigned long long n) {
   untwo(fma2(two(__uint_as_float(s0), __uint_as_float(s1)), c2, n), p0, p1);

@@ -57,16 +57,18 @@ struct Unit<__nv_bfloat16, true> {
       v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
-  __device__ static void store(__nv_bfloat16* p, int unit, int lane, int cols, const float (&v)[E]) {
-    const int c = col(unit, lane, 0);
-    if (c >= cols) return;
+  __device__ void set(const float (&v)[E]) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
       w[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ void store(__nv_bfloat16* p, int unit, int lane, int cols) const {
+    const int c = col(unit, lane, 0);
+    if (c < cols) *reinterpret_cast<uint4*>(p + c) = r;
   }
 };
 template <>
@@ -79,9 +81,10 @@ struct Unit<float, true> {
     r = c < cols ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __device__ void get(float (&v)[E]) const { v[0] = r.x; v[1] = r.y; v[2] = r.z; v[3] = r.w; }
-  __device__ static void store(float* p, int unit, int lane, int cols, const float (&v)[E]) {
+  __device__ void set(const float (&v)[E]) { r = make_float4(v[0], v[1], v[2], v[3]); }
+  __device__ void store(float* p, int unit, int lane, int cols) const {
     const int c = col(unit, lane, 0);
-    if (c < cols) *reinterpret_cast<float4*>(p + c) = make_float4(v[0], v[1], v[2], v[3]);
+    if (c < cols) *reinterpret_cast<float4*>(p + c) = r;
   }
 };
 template <typename T>
@@ -100,21 +103,24 @@ struct Unit<T, false> {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = static_cast<float>(r[e]);
   }
-  __device__ static void store(T* p, int unit, int lane, int cols, const float (&v)[E]) {
+  __device__ void set(const float (&v)[E]) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) r[e] = T(v[e]);
+  }
+  __device__ void store(T* p, int unit, int lane, int cols) const {
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int c = col(unit, lane, e);
-      if (c < cols) p[c] = T(v[e]);
+      if (c < cols) p[c] = r[e];
     }
   }
 };
 
-template <typename T>
-__device__ inline float rounded(float v);
-template <>
-__device__ inline float rounded<float>(float v) { return v; }
-template <>
-__device__ inline float rounded<__nv_bfloat16>(float v) { return __bfloat162float(__float2bfloat16_rn(v)); }
+// Most units of a row per warp.
+template <typename T, bool VEC>
+constexpr int kAddUnits = VEC && sizeof(T) == 2 ? 4 : 4;
+template <typename T, bool VEC>
+constexpr int kBackUnits = VEC && sizeof(T) == 2 ? 2 : 4;
 
 __device__ inline float max_nan(float a, float b) {
   float r;
@@ -122,11 +128,24 @@ __device__ inline float max_nan(float a, float b) {
   return r;
 }
 
+// Packed pairs of a unit's values.
+template <int E>
+__device__ inline void mul_all(float (&v)[E], const float (&f)[E]) {
+#pragma unroll
+  for (int e = 0; e < E; e += 2) untwo(mul2(two(v[e], v[e + 1]), two(f[e], f[e + 1])), v[e], v[e + 1]);
+}
+template <int E>
+__device__ inline void mul_all(float (&v)[E], float f) {
+  const unsigned long long f2 = two(f, f);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) untwo(mul2(two(v[e], v[e + 1]), f2), v[e], v[e + 1]);
+}
+
 // e4m3 of a unit's values and the tiles' scales.  A 16-byte bf16 unit covers
 // two tiles (a half-warp each), the others one.
 template <typename T, bool VEC>
 __device__ inline void store_e4m3(uint8_t* y, float* scales, int unit, int lane, int cols,
-                                  const float (&v)[Unit<T, VEC>::E]) {
+                                  float (&v)[Unit<T, VEC>::E]) {
   using U = Unit<T, VEC>;
   constexpr int lanes = 32 * kTile / U::kCols;
   float top = 0.f;
@@ -134,14 +153,15 @@ __device__ inline void store_e4m3(uint8_t* y, float* scales, int unit, int lane,
   for (int e = 0; e < U::E; ++e) top = max_nan(top, fabsf(v[e]));
 #pragma unroll
   for (int o = lanes / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float scale = max_nan(top / kE4m3Max, kScaleMin), inv = 1.f / scale;
+  const float scale = max_nan(top * (1.f / kE4m3Max), kScaleMin);
   const int tile0 = unit * U::kCols + (lane / lanes) * kTile;
   if (lane % lanes == 0 && tile0 < cols) scales[tile0 / kTile] = scale;
+  mul_all(v, __frcp_rn(scale));
   uint32_t w[(U::E + 3) / 4] = {};
 #pragma unroll
   for (int e = 0; e < U::E; e += 2) {
-    const uint32_t two = __nv_cvt_float2_to_fp8x2(make_float2(v[e] * inv, v[e + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-    w[e / 4] |= two << (8 * (e % 4));
+    const uint32_t pair = __nv_cvt_float2_to_fp8x2(make_float2(v[e], v[e + 1]), __NV_SATFINITE, __NV_E4M3);
+    w[e / 4] = e % 4 ? __byte_perm(w[e / 4], pair, 0x5410) : pair;
   }
   if (VEC) {
     const int c = U::col(unit, lane, 0);
@@ -168,32 +188,38 @@ struct AddParams {
   const void* x; const void* r; const void* w;
   void* h; void* y; float* scales; float* rstd;
   long long ldx, ldr, ldh, ldy, lds, rows;
-  int cols, wpr, f8;
+  int cols, f8;
   float eps;
 };
 
-// The sum over the row's warps of one value per warp, in a fixed order.  red:
-// one slot per warp; the block's threads all call it.
-__device__ inline float row_sum(float s, float* red, int wpr) {
+// The sum over the row's WPR warps of one value per lane, in a fixed order.
+// red: one slot per warp; the block's threads all call it.
+template <int WPR>
+__device__ inline float row_sum(float s, float* red) {
   s = warp_sum(s);
-  if (wpr == 1) return s;
+  if (WPR == 1) return s;
   const int warp = threadIdx.x >> 5;
   if ((threadIdx.x & 31) == 0) red[warp] = s;
   __syncthreads();
-  const int first = warp / wpr * wpr;
+  const int first = warp / WPR * WPR;
   float t = 0.f;
-  for (int i = 0; i < wpr; ++i) t += red[first + i];
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) t += red[first + i];
   return t;
 }
 
-template <typename T, bool VEC, int NU>
-__global__ void __launch_bounds__(kThreads) add_norm_kernel(const AddParams p) {
+// A row per WPR warps, NU units of it per warp (0: a row of any width, read
+// twice).  Widths and shares are template parameters because these kernels spend
+// their time on instructions as much as on memory (a run-time WPR: 39 us for
+// 4096 x 7168 with e4m3 output, 68 % of the issue slots).
+template <typename T, bool VEC, int WPR, int NU>
+__global__ void __launch_bounds__(kThreads) add_norm_kernel(const __grid_constant__ AddParams p) {
   using U = Unit<T, VEC>;
   constexpr int N = NU ? NU : 1;
   __shared__ float red[kWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w0 = warp % p.wpr;
-  const long long row = (long long)blockIdx.x * (kWarps / p.wpr) + warp / p.wpr;
+  const int w0 = warp % WPR;
+  const long long row = (long long)blockIdx.x * (kWarps / WPR) + warp / WPR;
   const bool live = row < p.rows;
   const long long at = live ? row : 0;
   const T* x = static_cast<const T*>(p.x) + at * p.ldx;
@@ -202,68 +228,76 @@ __global__ void __launch_bounds__(kThreads) add_norm_kernel(const AddParams p) {
   const T* w = static_cast<const T*>(p.w);
   const int cols = live ? p.cols : 0;    // rows past the end read and write nothing
   const int units = (p.cols + U::kCols - 1) / U::kCols;
-  auto add = [&](int unit, const U& a, const U& b, float (&v)[U::E]) {
+  // a <- h of the unit (stored where there is a residual); its squares onto s
+  unsigned long long s2 = 0;
+  auto add = [&](int unit, U& a, const U& b) {
+    float v[U::E];
     a.get(v);
-    if (!r) return;
-    float s[U::E];
-    b.get(s);
+    if (r) {
+      float t[U::E];
+      b.get(t);
 #pragma unroll
-    for (int e = 0; e < U::E; ++e) v[e] = rounded<T>(v[e] + s[e]);
-    U::store(h, unit, lane, cols, v);
+      for (int e = 0; e < U::E; e += 2) untwo(add2(two(v[e], v[e + 1]), two(t[e], t[e + 1])), v[e], v[e + 1]);
+      a.set(v);
+      a.store(h, unit, lane, cols);
+      a.get(v);
+    }
+#pragma unroll
+    for (int e = 0; e < U::E; e += 2) s2 = fma2(two(v[e], v[e + 1]), two(v[e], v[e + 1]), s2);
   };
-  auto finish = [&](int unit, float rs, float (&v)[U::E]) {
+  auto finish = [&](int unit, float rs, U& a, const U& uw) {
+    float v[U::E];
+    a.get(v);
+    mul_all(v, rs);
     if (w) {
-      U uw;
-      uw.load(w, unit, lane, p.cols);
       float f[U::E];
       uw.get(f);
-#pragma unroll
-      for (int e = 0; e < U::E; ++e) v[e] = v[e] * rs * f[e];
-    } else {
-#pragma unroll
-      for (int e = 0; e < U::E; ++e) v[e] *= rs;
+      mul_all(v, f);
     }
-    if (p.f8) store_e4m3<T, VEC>(static_cast<uint8_t*>(p.y) + at * p.ldy, p.scales + at * p.lds, unit, lane, cols, v);
-    else U::store(static_cast<T*>(p.y) + at * p.ldy, unit, lane, cols, v);
+    if (p.f8) {
+      store_e4m3<T, VEC>(static_cast<uint8_t*>(p.y) + at * p.ldy, p.scales + at * p.lds, unit, lane, cols, v);
+    } else {
+      a.set(v);
+      a.store(static_cast<T*>(p.y) + at * p.ldy, unit, lane, cols);
+    }
   };
-  float s = 0.f;
+  // the row stays packed in its own type between the two uses of it
   U ux[N], ur[N];
-  float v[N][U::E];
   if (NU) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) ux[k].load(x, k * p.wpr + w0, lane, cols);
+    for (int k = 0; k < N; ++k) ux[k].load(x, k * WPR + w0, lane, cols);
     if (r) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) ur[k].load(r, k * p.wpr + w0, lane, cols);
+      for (int k = 0; k < N; ++k) ur[k].load(r, k * WPR + w0, lane, cols);
     }
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      add(k * p.wpr + w0, ux[k], ur[k], v[k]);
+    for (int k = 0; k < N; ++k) add(k * WPR + w0, ux[k], ur[k]);
+    if (w) {                             // into the residual's registers, under the sum
 #pragma unroll
-      for (int e = 0; e < U::E; ++e) s = fmaf(v[k][e], v[k][e], s);
+      for (int k = 0; k < N; ++k) ur[k].load(w, k * WPR + w0, lane, p.cols);
     }
   } else {
-    for (int u = w0; u < units; u += p.wpr) {
+    for (int u = w0; u < units; u += WPR) {
       ux[0].load(x, u, lane, cols);
       if (r) ur[0].load(r, u, lane, cols);
-      add(u, ux[0], ur[0], v[0]);
-#pragma unroll
-      for (int e = 0; e < U::E; ++e) s = fmaf(v[0][e], v[0][e], s);
+      add(u, ux[0], ur[0]);
     }
   }
-  s = row_sum(s, red, p.wpr);
+  float sa, sb;
+  untwo(s2, sa, sb);
+  const float s = row_sum<WPR>(sa + sb, red);
   const float rs = 1.f / sqrtf(s / (float)p.cols + p.eps);
   if (live && p.rstd && w0 == 0 && lane == 0) p.rstd[row] = rs;
   if (NU) {
 #pragma unroll
     for (int k = 0; k < N; ++k)
-      if (k * p.wpr + w0 < units) finish(k * p.wpr + w0, rs, v[k]);
+      if (k * WPR + w0 < units) finish(k * WPR + w0, rs, ux[k], ur[k]);
   } else {
     const T* again = r ? h : x;          // each lane reads back its own values
-    for (int u = w0; u < units; u += p.wpr) {
+    for (int u = w0; u < units; u += WPR) {
       ux[0].load(again, u, lane, cols);
-      ux[0].get(v[0]);
-      finish(u, rs, v[0]);
+      if (w) ur[0].load(w, u, lane, p.cols);
+      finish(u, rs, ux[0], ur[0]);
     }
   }
 }
@@ -272,112 +306,154 @@ struct BackParams {
   const void* dy; const void* h; const float* rstd; const void* w; const void* dres;
   void* dx; float* part;                 // [grid][cols] sums of dy xhat, or null
   long long lddy, ldh, ldr, ldx, rows;
-  int cols, wpr;
+  int cols;
 };
 
-// Row groups of wpr warps walk the rows in steps of grid * groups; each lane
-// keeps its columns' sums of dy xhat.  The groups of a block add up in order
-// through shared memory, and the block writes one row of partial sums.
-template <typename T, bool VEC, int NU>
-__global__ void __launch_bounds__(kThreads) norm_back_kernel(const BackParams p) {
+// dx = rstd g - (rstd mean(g xhat)) xhat + dres and dw += dy xhat, with xhat formed
+// from h both before and after the row's sum (h itself may be far from 1, so rstd
+// stays with it).
+// Row groups of WPR warps walk the rows in steps of grid * groups; the next row
+// is loaded while the current one is worked on, both packed in their own type,
+// and each lane keeps its columns' weights and sums.  The groups of a block add
+// up in order through shared memory, and the block writes one row of partial
+// sums.  (Loading a row at a time, with xhat and g as fp32 arrays: 80 us for
+// 16384 x 2048 with a weight and dres.)
+template <typename T, bool VEC, int WPR, int NU>
+__global__ void __launch_bounds__(kThreads) norm_back_kernel(const __grid_constant__ BackParams p) {
   using U = Unit<T, VEC>;
-  constexpr int N = NU ? NU : 1;
+  constexpr int N = NU ? NU : 1, groups = kWarps / WPR;
   __shared__ float red[2][kWarps];
   extern __shared__ float sums[];        // [cols] when several groups share a block
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = kWarps / p.wpr, w0 = warp % p.wpr, mine = warp / p.wpr;
+  const int w0 = warp % WPR, mine = warp / WPR;
   const int units = (p.cols + U::kCols - 1) / U::kCols;
   const T* w = static_cast<const T*>(p.w);
   float* part = p.part ? p.part + (long long)blockIdx.x * p.cols : nullptr;
   float acc[N][U::E] = {};
-  if (!NU && part) {                     // wide rows: the block's own partial sums in global memory
+  U uw[N];
+  if (NU) {
+    if (w) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) uw[k].load(w, k * WPR + w0, lane, p.cols);
+    }
+  } else if (part) {                     // wide rows: the block's own partial sums in global memory
     for (int c = threadIdx.x; c < p.cols; c += kThreads) part[c] = 0.f;
     __syncthreads();
   }
-  int turn = 0;
-  for (long long row0 = (long long)blockIdx.x * groups; row0 < p.rows; row0 += (long long)gridDim.x * groups, turn ^= 1) {
+  // t2 += sum of w dy xhat over a unit; a += dy xhat
+  auto before = [&](float rs, const U& uy, const U& uh, const U& wt, float (&a)[U::E], unsigned long long& t2) {
+    float y[U::E], f[U::E];
+    uh.get(y);
+    mul_all(y, rs);
+    uy.get(f);
+    mul_all(y, f);
+#pragma unroll
+    for (int e = 0; e < U::E; e += 2) untwo(add2(two(y[e], y[e + 1]), two(a[e], a[e + 1])), a[e], a[e + 1]);
+    if (w) {
+      wt.get(f);
+#pragma unroll
+      for (int e = 0; e < U::E; e += 2) t2 = fma2(two(y[e], y[e + 1]), two(f[e], f[e + 1]), t2);
+    } else {
+#pragma unroll
+      for (int e = 0; e < U::E; e += 2) t2 = add2(two(y[e], y[e + 1]), t2);
+    }
+  };
+  // dx of a unit, given c = -rstd mean(g xhat)
+  auto after = [&](T* dx, int unit, int cols, float rs, float c, const U& uy, const U& uh, const U& wt, const U& ud) {
+    float v[U::E], f[U::E];
+    uh.get(v);
+    mul_all(v, rs);
+    const unsigned long long c2 = two(c, c), r2 = two(rs, rs);
+    if (p.dres) {
+      ud.get(f);
+#pragma unroll
+      for (int e = 0; e < U::E; e += 2) untwo(fma2(two(v[e], v[e + 1]), c2, two(f[e], f[e + 1])), v[e], v[e + 1]);
+    } else {
+      mul_all(v, c);
+    }
+    float y[U::E];
+    uy.get(y);
+    if (w) {
+      wt.get(f);
+      mul_all(y, f);
+    }
+#pragma unroll
+    for (int e = 0; e < U::E; e += 2) untwo(fma2(two(y[e], y[e + 1]), r2, two(v[e], v[e + 1])), v[e], v[e + 1]);
+    U o;
+    o.set(v);
+    o.store(dx, unit, lane, cols);
+  };
+  struct Row {
+    U y[N], h[N], d[N];
+    float rs;
+    long long at;
+    int cols;
+  };
+  // a row past the end reads nothing and counts as zeros
+  auto fetch = [&](long long row0, Row& q) {
     const long long row = row0 + mine;
     const bool live = row < p.rows;
-    const long long at = live ? row : 0;
-    const int cols = live ? p.cols : 0;
-    const T* dy = static_cast<const T*>(p.dy) + at * p.lddy;
-    const T* h = static_cast<const T*>(p.h) + at * p.ldh;
-    const T* dres = p.dres ? static_cast<const T*>(p.dres) + at * p.ldr : nullptr;
-    T* dx = static_cast<T*>(p.dx) + at * p.ldx;
-    const float rs = live ? p.rstd[row] : 0.f;
-    // xhat and g of a unit; its share of sum(g xhat); dy xhat onto a
-    auto take = [&](int unit, const U& uy, const U& uh, float (&xh)[U::E], float (&g)[U::E], float (&a)[U::E]) {
-      uh.get(xh);
-      uy.get(g);
-      float t = 0.f;
+    q.at = live ? row : 0;
+    q.cols = live ? p.cols : 0;
+    q.rs = live ? p.rstd[row] : 0.f;
+    if (!NU) return;
+    const T* dy = static_cast<const T*>(p.dy) + q.at * p.lddy;
+    const T* h = static_cast<const T*>(p.h) + q.at * p.ldh;
 #pragma unroll
-      for (int e = 0; e < U::E; ++e) {
-        xh[e] *= rs;
-        a[e] = fmaf(g[e], xh[e], a[e]);
-      }
-      if (w) {
-        U uw;
-        uw.load(w, unit, lane, p.cols);
-        float f[U::E];
-        uw.get(f);
+    for (int k = 0; k < N; ++k) {
+      q.y[k].load(dy, k * WPR + w0, lane, q.cols);
+      q.h[k].load(h, k * WPR + w0, lane, q.cols);
+    }
+    if (p.dres) {
+      const T* dres = static_cast<const T*>(p.dres) + q.at * p.ldr;
 #pragma unroll
-        for (int e = 0; e < U::E; ++e) g[e] *= f[e];
-      }
-#pragma unroll
-      for (int e = 0; e < U::E; ++e) t = fmaf(g[e], xh[e], t);
-      return t;
-    };
-    auto put = [&](int unit, float m, const U& ud, const float (&xh)[U::E], float (&g)[U::E]) {
-      float d[U::E] = {};
-      if (dres) ud.get(d);
-#pragma unroll
-      for (int e = 0; e < U::E; ++e) g[e] = fmaf(rs, fmaf(-xh[e], m, g[e]), d[e]);
-      U::store(dx, unit, lane, cols, g);
-    };
-    U uy[N], uh[N], ud[N];
-    float xh[N][U::E], g[N][U::E];
-    float s = 0.f;
+      for (int k = 0; k < N; ++k) q.d[k].load(dres, k * WPR + w0, lane, q.cols);
+    }
+  };
+  const long long step = (long long)gridDim.x * groups;
+  const float inv_n = 1.f / (float)p.cols;
+  int turn = 0;
+  Row now, next;
+  fetch((long long)blockIdx.x * groups, now);
+  for (long long row0 = (long long)blockIdx.x * groups; row0 < p.rows; row0 += step, turn ^= 1) {
+    fetch(row0 + step, next);
+    T* dx = static_cast<T*>(p.dx) + now.at * p.ldx;
+    const float rs = now.rs;
+    unsigned long long t2 = 0;
+    float ta, tb;
     if (NU) {
 #pragma unroll
-      for (int k = 0; k < N; ++k) {
-        uy[k].load(dy, k * p.wpr + w0, lane, cols);
-        uh[k].load(h, k * p.wpr + w0, lane, cols);
-      }
-      if (dres) {
+      for (int k = 0; k < N; ++k) before(rs, now.y[k], now.h[k], uw[k], acc[k], t2);
+      untwo(t2, ta, tb);
+      const float c = -rs * (row_sum<WPR>(ta + tb, red[turn]) * inv_n);
 #pragma unroll
-        for (int k = 0; k < N; ++k) ud[k].load(dres, k * p.wpr + w0, lane, cols);
-      }
-#pragma unroll
-      for (int k = 0; k < N; ++k) s += take(k * p.wpr + w0, uy[k], uh[k], xh[k], g[k], acc[k]);
+      for (int k = 0; k < N; ++k) after(dx, k * WPR + w0, now.cols, rs, c, now.y[k], now.h[k], uw[k], now.d[k]);
     } else {
-      for (int u = w0; u < units; u += p.wpr) {
-        uy[0].load(dy, u, lane, cols);
-        uh[0].load(h, u, lane, cols);
+      const T* dy = static_cast<const T*>(p.dy) + now.at * p.lddy;
+      const T* h = static_cast<const T*>(p.h) + now.at * p.ldh;
+      for (int u = w0; u < units; u += WPR) {
+        now.y[0].load(dy, u, lane, now.cols);
+        now.h[0].load(h, u, lane, now.cols);
+        if (w) uw[0].load(w, u, lane, p.cols);
         float a[U::E] = {};
-        s += take(u, uy[0], uh[0], xh[0], g[0], a);
-        if (part) {
+        before(rs, now.y[0], now.h[0], uw[0], a, t2);
 #pragma unroll
-          for (int e = 0; e < U::E; ++e) {
-            const int c = U::col(u, lane, e) + (VEC ? e : 0);
-            if (c < cols) part[c] += a[e];
-          }
+        for (int e = 0; e < U::E; ++e) {
+          const int c = U::col(u, lane, e) + (VEC ? e : 0);
+          if (part && c < now.cols) part[c] += a[e];
         }
       }
-    }
-    const float m = row_sum(s, red[turn], p.wpr) / (float)p.cols;
-    if (NU) {
-#pragma unroll
-      for (int k = 0; k < N; ++k) put(k * p.wpr + w0, m, ud[k], xh[k], g[k]);
-    } else {
-      for (int u = w0; u < units; u += p.wpr) {
-        uy[0].load(dy, u, lane, cols);
-        uh[0].load(h, u, lane, cols);
-        if (dres) ud[0].load(dres, u, lane, cols);
-        float a[U::E] = {};
-        take(u, uy[0], uh[0], xh[0], g[0], a);
-        put(u, m, ud[0], xh[0], g[0]);
+      untwo(t2, ta, tb);
+      const float c = -rs * (row_sum<WPR>(ta + tb, red[turn]) * inv_n);
+      for (int u = w0; u < units; u += WPR) {
+        now.y[0].load(dy, u, lane, now.cols);
+        now.h[0].load(h, u, lane, now.cols);
+        if (w) uw[0].load(w, u, lane, p.cols);
+        if (p.dres) now.d[0].load(static_cast<const T*>(p.dres) + now.at * p.ldr, u, lane, now.cols);
+        after(dx, u, now.cols, rs, c, now.y[0], now.h[0], uw[0], now.d[0]);
       }
     }
+    now = next;
   }
   if (!NU || !part) return;
   for (int gr = groups - 1; gr >= 0; --gr) {
@@ -386,7 +462,7 @@ __global__ void __launch_bounds__(kThreads) norm_back_kernel(const BackParams p)
       for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int e = 0; e < U::E; ++e) {
-          const int c = U::col(k * p.wpr + w0, lane, e) + (VEC ? e : 0);
+          const int c = U::col(k * WPR + w0, lane, e) + (VEC ? e : 0);
           if (c >= p.cols) continue;
           const float t = (gr == groups - 1 ? 0.f : sums[c]) + acc[k][e];
           if (gr) sums[c] = t;
@@ -397,68 +473,77 @@ __global__ void __launch_bounds__(kThreads) norm_back_kernel(const BackParams p)
   }
 }
 
-// dw[c] = sum over the partial rows: 32 columns per block, 8 rows at a time,
-// the eight sums added in order.
-__global__ void __launch_bounds__(kThreads) norm_weight_kernel(const float* part, float* dw, int n, int cols) {
-  __shared__ float red[kWarps][32];
+// dw[c] = sum over the partial rows: 32 columns per block, a warp per 32nd row,
+// the 32 sums added in a fixed tree.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, float* dw, int n, int cols) {
+  __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < cols)
-    for (int i = warp; i < n; i += kWarps) s += part[(long long)i * cols + c];
+  if (c < cols) {
+#pragma unroll 4
+    for (int i = warp; i < n; i += 32) s += part[(long long)i * cols + c];
+  }
   red[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    float t = 0.f;
+  s = red[lane][warp];                   // a warp per column now
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) t += red[i][lane];
-    dw[c] = t;
-  }
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const int d = blockIdx.x * 32 + warp;
+  if (lane == 0 && d < cols) dw[d] = s;
 }
 
-// Warps per row and units per warp: the fewest warps that hold a row in at most
-// `most` units each; 0 units when eight cannot.
-void split_row(int cols, int unit_cols, int most, int& wpr, int& nu) {
+// The fewest warps that hold a row of `cols` in at most MOST units each, as
+// f(WPR, NU); NU = 0 when eight cannot.
+template <int W, int N>
+struct Share {};
+template <int MOST, typename F>
+cudaError_t by_share(int cols, int unit_cols, F f) {
   const int units = (cols + unit_cols - 1) / unit_cols;
-  for (wpr = 1; wpr < kWarps && (units + wpr - 1) / wpr > most; wpr *= 2) {}
-  nu = (units + wpr - 1) / wpr;
-  if (nu > most) nu = 0;
-  while (nu & (nu - 1)) ++nu;            // 1, 2, 4, 8
+  if (units <= 1) return f(Share<1, 1>());
+  if (units <= MOST) return f(Share<1, MOST>());
+  if (units <= 2 * MOST) return f(Share<2, MOST>());
+  if (units <= 4 * MOST) return f(Share<4, MOST>());
+  if (units <= 8 * MOST) return f(Share<8, MOST>());
+  return f(Share<8, 0>());
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_add(AddParams p, cudaStream_t s) {
-  int nu;
-  split_row(p.cols, Unit<T, VEC>::kCols, 32 / Unit<T, VEC>::E, p.wpr, nu);
-  const unsigned grid = (unsigned)cdiv(p.rows, kWarps / p.wpr);
-  switch (nu) {
-    case 1: add_norm_kernel<T, VEC, 1><<<grid, kThreads, 0, s>>>(p); break;
-    case 2: add_norm_kernel<T, VEC, 2><<<grid, kThreads, 0, s>>>(p); break;
-    case 4: add_norm_kernel<T, VEC, 4><<<grid, kThreads, 0, s>>>(p); break;
-    case 8: add_norm_kernel<T, VEC, VEC && sizeof(T) == 2 ? 4 : 8><<<grid, kThreads, 0, s>>>(p); break;
-    default: add_norm_kernel<T, VEC, 0><<<grid, kThreads, 0, s>>>(p); break;
+struct AddLaunch {
+  const AddParams& p;
+  cudaStream_t s;
+  template <int WPR, int NU>
+  cudaError_t operator()(Share<WPR, NU>) const {
+    add_norm_kernel<T, VEC, WPR, NU><<<(unsigned)cdiv(p.rows, kWarps / WPR), kThreads, 0, s>>>(p);
+    return cudaGetLastError();
   }
-  return cudaGetLastError();
+};
+template <typename T, bool VEC>
+cudaError_t launch_add(const AddParams& p, cudaStream_t s) {
+  return by_share<kAddUnits<T, VEC>>(p.cols, Unit<T, VEC>::kCols, AddLaunch<T, VEC>{p, s});
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_back(BackParams p, float* dw, cudaStream_t s) {
-  int nu;
-  split_row(p.cols, Unit<T, VEC>::kCols, 16 / Unit<T, VEC>::E * 2, p.wpr, nu);
-  const int groups = kWarps / p.wpr;
-  const long long want = cdiv(p.rows, groups);
-  const int grid = (int)(want < kBackGrid ? want : kBackGrid);
-  const size_t smem = p.part && groups > 1 && nu ? (size_t)p.cols * 4 : 0;   // at most 4 x 1024 columns: 16 KB
-  switch (nu) {
-    case 1: norm_back_kernel<T, VEC, 1><<<grid, kThreads, smem, s>>>(p); break;
-    case 2: norm_back_kernel<T, VEC, 2><<<grid, kThreads, smem, s>>>(p); break;
-    case 4: norm_back_kernel<T, VEC, 4><<<grid, kThreads, smem, s>>>(p); break;
-    case 8: norm_back_kernel<T, VEC, VEC && sizeof(T) == 2 ? 4 : 8><<<grid, kThreads, smem, s>>>(p); break;
-    default: norm_back_kernel<T, VEC, 0><<<grid, kThreads, smem, s>>>(p); break;
+struct BackLaunch {
+  const BackParams& p;
+  int& grid;
+  cudaStream_t s;
+  template <int WPR, int NU>
+  cudaError_t operator()(Share<WPR, NU>) const {
+    constexpr int groups = kWarps / WPR;
+    const long long want = cdiv(p.rows, groups);
+    grid = (int)(want < kBackGrid ? want : kBackGrid);
+    const size_t smem = p.part && groups > 1 && NU ? (size_t)p.cols * 4 : 0;   // at most 4096 columns: 16 KB
+    norm_back_kernel<T, VEC, WPR, NU><<<grid, kThreads, smem, s>>>(p);
+    return cudaGetLastError();
   }
-  cudaError_t e = cudaGetLastError();
+};
+template <typename T, bool VEC>
+cudaError_t launch_back(const BackParams& p, float* dw, cudaStream_t s) {
+  int grid = 0;
+  const cudaError_t e = by_share<kBackUnits<T, VEC>>(p.cols, Unit<T, VEC>::kCols, BackLaunch<T, VEC>{p, grid, s});
   if (e != cudaSuccess || !p.part) return e;
-  norm_weight_kernel<<<(unsigned)cdiv(p.cols, 32), kThreads, 0, s>>>(p.part, dw, grid, p.cols);
+  norm_weight_kernel<<<(unsigned)cdiv(p.cols, 32), 1024, 0, s>>>(p.part, dw, grid, p.cols);
   return cudaGetLastError();
 }
 
@@ -547,7 +632,7 @@ mc_status mc_add_rms_norm(const void* x, int64_t ldx, const void* residual, int6
     return (i == 3 && j <= 1) || (i == 4 && j <= 1 && !f8);
   });
   if (st != MC_OK) return st;
-  AddParams p{x, residual, weight, h, y, f8 ? scales : nullptr, rstd, ldx, ldr, ldh, ldy, lds, rows, cols, 1, f8, eps};
+  AddParams p{x, residual, weight, h, y, f8 ? scales : nullptr, rstd, ldx, ldr, ldh, ldy, lds, rows, cols, f8, eps};
   const int per = 16 / (int)es;          // values per 16 bytes
   const bool vec = cols % per == 0 && ldx % per == 0 && aligned(x, 16) && aligned(weight, 16) &&
                    (!residual || (ldr % per == 0 && ldh % per == 0 && aligned(residual, 16) && aligned(h, 16))) &&
@@ -601,7 +686,7 @@ mc_status mc_rms_norm_backward(const void* dy, int64_t lddy, const void* h, int6
   const mc_status st = check_overlaps(me, t, 8, rows, [](int i, int j) { return i == 5 && j <= 2; });
   if (st != MC_OK) return st;
   BackParams p{dy, h, rstd, weight, dres, dx, dweight ? static_cast<float*>(workspace) : nullptr,
-               lddy, ldh, ldr, lddx, rows, cols, 1};
+               lddy, ldh, ldr, lddx, rows, cols};
   const int per = 16 / (int)es;
   const bool vec = cols % per == 0 && lddy % per == 0 && ldh % per == 0 && lddx % per == 0 && aligned(dy, 16) &&
                    aligned(h, 16) && aligned(dx, 16) && aligned(weight, 16) &&

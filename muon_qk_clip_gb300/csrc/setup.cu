@@ -24,6 +24,7 @@
 
 #include "../../include/muonclip.h"
 #include "common.cuh"
+#include "fastdiv.cuh"
 #include "kernels.h"
 
 namespace mc {
@@ -97,76 +98,92 @@ __global__ void rope_kernel(T* x, int B, int S, int nh, int d, long long sb, lon
 }
 
 // Gradient of the rotary embedding: the transposed rotation of each pair, from
-// dy to dx (which may be dy).  A block takes `per` consecutive positions of
-// every (b, head): it writes their cosines and sines to shared memory, then
-// moves 16 bytes (V pairs) per thread and step.  The frequency table is fp64
-// (once per block); an angle is reduced in fp64 to at most half a turn, so its
-// fp32 sine and cosine are good to 2^-23 absolute at any position, without
-// fp64 trigonometry for each position.
+// dy to dx (which may be dy).  A block takes `per` consecutive positions of one
+// batch row at a time: it writes their cosines and sines to shared memory, then
+// moves 16 bytes (V pairs) per thread and step.  A pair's turns per position are
+// a sum of two fp32 (from fp64, once per block), and the turns at a position are
+// reduced to at most half a turn exactly: s hi and its rounding error, plus s lo.
+// So the fp32 sine and cosine are good to 2^-23 absolute at any position without
+// fp64 arithmetic per position (this part runs it at a fraction of fp32's rate).
 struct RopeBack {
   const void* dy; void* dx;
   long long yb, ys, yh, xb, xs, xh;
-  int B, S, nh, d, per;
+  int S, nh, d, per, chunks;             // chunks of `per` positions in a batch row
+  long long blocks;                      // chunks * B
   double step;                           // log2(theta) * 2 / d
+  FastDiv div_half, div_nv, div_nh;
 };
 template <typename T, int V>
-__global__ void __launch_bounds__(256) rope_back_kernel(const RopeBack p) {
-  extern __shared__ double turns[];      // [d/2] turns per position, then [per][d/2] (cos, sin)
+__global__ void __launch_bounds__(256) rope_back_kernel(const __grid_constant__ RopeBack p) {
+  extern __shared__ float2 turns[];      // [d/2] (hi, lo) turns per position, then [per][d/2] (cos, sin)
   const int half = p.d / 2, nv = half / V;
-  float2* cs = reinterpret_cast<float2*>(turns + half);
-  for (int k = threadIdx.x; k < half; k += blockDim.x) turns[k] = exp2(-p.step * k) * 0.15915494309189535;
-  const long long blocks = ((long long)p.S + p.per - 1) / p.per;
-  for (long long blk = blockIdx.x; blk < blocks; blk += gridDim.x) {
-    const int s0 = (int)(blk * p.per), n = min(p.per, p.S - s0);
+  float2* cs = turns + half;
+  for (int k = threadIdx.x; k < half; k += blockDim.x) {
+    const double t = exp2(-p.step * k) * 0.15915494309189535;
+    const float hi = (float)t;
+    turns[k] = make_float2(hi, (float)(t - hi));
+  }
+  for (long long blk = blockIdx.x; blk < p.blocks; blk += gridDim.x) {
+    const int b = (int)(blk / p.chunks), s0 = (int)(blk - (long long)b * p.chunks) * p.per, n = min(p.per, p.S - s0);
     __syncthreads();
     for (int x = threadIdx.x; x < n * half; x += blockDim.x) {
-      const int i = x / half, k = x - i * half;
-      double t = (double)(s0 + i) * turns[k];
-      t -= rint(t);
+      const int i = (int)fastdiv(x, p.div_half);
+      const float2 f = turns[x - i * half];
+      const float s = (float)(s0 + i), t = s * f.x, e = fmaf(s, f.x, -t);
       float sn, cn;
-      sincospif((float)(2.0 * t), &sn, &cn);
+      sincospif(2.f * ((t - rintf(t)) + fmaf(s, f.y, e)), &sn, &cn);
       cs[x] = make_float2(cn, sn);
     }
     __syncthreads();
-    const long long items = (long long)p.B * n * p.nh * nv;
-    for (long long x = threadIdx.x; x < items; x += blockDim.x) {
-      const long long row = x / nv;
-      const int c = (int)(x - row * nv);
-      const long long bi = row / p.nh;
-      const int h = (int)(row - bi * p.nh);
-      const int b = (int)(bi / n), i = (int)(bi - (long long)b * n);
-      const T* src = static_cast<const T*>(p.dy) + b * p.yb + (s0 + i) * p.ys + h * p.yh + 2 * V * c;
-      T* dst = static_cast<T*>(p.dx) + b * p.xb + (s0 + i) * p.xs + h * p.xh + 2 * V * c;
-      const float2* f = cs + i * half + V * c;
+    const T* src = static_cast<const T*>(p.dy) + b * p.yb + s0 * p.ys;
+    T* dst = static_cast<T*>(p.dx) + b * p.xb + s0 * p.xs;
+    const int items = n * p.nh * nv;
+#pragma unroll 4
+    for (int x = threadIdx.x; x < items; x += blockDim.x) {
+      const int row = (int)fastdiv(x, p.div_nv), c = x - row * nv;
+      const int i = (int)fastdiv(row, p.div_nh), h = row - i * p.nh;
+      const T* from = src + i * p.ys + h * p.yh + 2 * V * c;
+      T* to = dst + i * p.xs + h * p.xh + 2 * V * c;
       alignas(16) T v[2 * V];
-      if (V > 1) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src);
-      else { v[0] = src[0]; v[1] = src[1]; }
+      if (V > 1) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(from);
+      else { v[0] = from[0]; v[1] = from[1]; }
+      alignas(16) float2 f[V];
+      if (V > 1) {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) *reinterpret_cast<float4*>(f + k) = *reinterpret_cast<const float4*>(cs + i * half + V * c + k);
+      } else {
+        f[0] = cs[i * half + c];
+      }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const float a = ldv(v + 2 * k), e = ldv(v + 2 * k + 1);
         stv(v + 2 * k, fmaf(a, f[k].x, e * f[k].y));
         stv(v + 2 * k + 1, fmaf(e, f[k].x, -(a * f[k].y)));
       }
-      if (V > 1) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(v);
-      else { dst[0] = v[0]; dst[1] = v[1]; }
+      if (V > 1) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(v);
+      else { to[0] = v[0]; to[1] = v[1]; }
     }
   }
 }
 
 template <typename T, int V>
-cudaError_t launch_rope_back(RopeBack p, cudaStream_t s) {
-  // positions per block: about 2048 accesses of a block's 256 threads, fewer
-  // while that leaves SMs without a block; the table stays under 32 KB
-  const long long each = (long long)p.B * p.nh * (p.d / 2 / V);
-  long long per = cdiv(2048, each);
-  const long long spread = cdiv(p.S, 2ll * sm_count());
+cudaError_t launch_rope_back(RopeBack p, int B, cudaStream_t s) {
+  // positions per block: about 2048 accesses of its 256 threads, fewer while that
+  // leaves SMs without a block; the table stays within 48 KB
+  const int half = p.d / 2;
+  long long per = cdiv(2048, (long long)p.nh * (half / V));
+  const long long spread = cdiv((long long)p.S * B, 4ll * sm_count());
   if (per > spread) per = spread;
-  const long long room = 4096 / (p.d / 2);
+  const long long room = 48 * 1024 / 8 / half - 1;
   if (per > room) per = room;
   p.per = (int)(per < 1 ? 1 : per);
-  const size_t smem = (size_t)(p.d / 2) * 8 * (1 + p.per);
-  const long long blocks = cdiv(p.S, p.per), most = (long long)sm_count() * 8;
-  rope_back_kernel<T, V><<<(unsigned)(blocks < most ? blocks : most), 256, smem, s>>>(p);
+  p.chunks = (int)cdiv(p.S, p.per);
+  p.blocks = (long long)p.chunks * B;
+  p.div_half = make_fastdiv((uint32_t)half);
+  p.div_nv = make_fastdiv((uint32_t)(half / V));
+  p.div_nh = make_fastdiv((uint32_t)p.nh);
+  const long long most = (long long)sm_count() * 8;
+  rope_back_kernel<T, V><<<(unsigned)(p.blocks < most ? p.blocks : most), 256, (size_t)half * 8 * (1 + p.per), s>>>(p);
   return cudaGetLastError();
 }
 
@@ -312,11 +329,18 @@ mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, v
   const uintptr_t py = reinterpret_cast<uintptr_t>(dy), px = reinterpret_cast<uintptr_t>(dx);
   if (!same && py < px + endx * es && px < py + endy * es)
     return err(MC_ERR_INVALID_ARG, "%s: dx overlaps dy without being dy", me);
-  RopeBack p{dy, dx, yb, ys, yh, xb, xs, xh, B, S, nh, d, 1, std::log2(theta) * 2.0 / d};
+  if ((long long)nh * (d / 2) >= (1 << 28)) return err(MC_ERR_UNSUPPORTED, "%s: %d heads of %d in one position", me, nh, d);
+  RopeBack p;
+  memset(&p, 0, sizeof p);
+  p.dy = dy; p.dx = dx;
+  p.yb = yb; p.ys = ys; p.yh = yh;
+  p.xb = xb; p.xs = xs; p.xh = xh;
+  p.S = S; p.nh = nh; p.d = d;
+  p.step = std::log2(theta) * 2.0 / d;
   const cudaStream_t s = (cudaStream_t)stream;
   cudaError_t e;
-  if (dtype == MC_BF16) e = vec ? launch_rope_back<__nv_bfloat16, 4>(p, s) : launch_rope_back<__nv_bfloat16, 1>(p, s);
-  else e = vec ? launch_rope_back<float, 2>(p, s) : launch_rope_back<float, 1>(p, s);
+  if (dtype == MC_BF16) e = vec ? launch_rope_back<__nv_bfloat16, 4>(p, B, s) : launch_rope_back<__nv_bfloat16, 1>(p, B, s);
+  else e = vec ? launch_rope_back<float, 2>(p, B, s) : launch_rope_back<float, 1>(p, B, s);
   if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
   return done();
 }
