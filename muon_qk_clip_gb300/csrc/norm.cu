@@ -118,9 +118,9 @@ struct Unit<T, false> {
 
 // Most units of a row per warp.
 template <typename T, bool VEC>
-constexpr int kAddUnits = VEC && sizeof(T) == 2 ? 4 : 4;
+constexpr int kAddUnits = 4;
 template <typename T, bool VEC>
-constexpr int kBackUnits = VEC && sizeof(T) == 2 ? 2 : 4;
+constexpr int kBackUnits = 2;
 
 __device__ inline float max_nan(float a, float b) {
   float r;
@@ -319,7 +319,7 @@ struct BackParams {
 // sums.  (Loading a row at a time, with xhat and g as fp32 arrays: 80 us for
 // 16384 x 2048 with a weight and dres.)
 template <typename T, bool VEC, int WPR, int NU>
-__global__ void __launch_bounds__(kThreads) norm_back_kernel(const __grid_constant__ BackParams p) {
+__global__ void __launch_bounds__(kThreads, 2) norm_back_kernel(const __grid_constant__ BackParams p) {
   using U = Unit<T, VEC>;
   constexpr int N = NU ? NU : 1, groups = kWarps / WPR;
   __shared__ float red[2][kWarps];
@@ -480,10 +480,15 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, fl
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < cols) {
-#pragma unroll 4
-    for (int i = warp; i < n; i += 32) s += part[(long long)i * cols + c];
+  constexpr int flight = (kBackGrid + 31) / 32;        // every load at once
+  float v[flight];
+#pragma unroll
+  for (int k = 0; k < flight; ++k) {
+    const int i = warp + 32 * k;
+    v[k] = c < cols && i < n ? part[(long long)i * cols + c] : 0.f;
   }
+#pragma unroll
+  for (int k = 0; k < flight; ++k) s += v[k];
   red[warp][lane] = s;
   __syncthreads();
   s = red[lane][warp];                   // a warp per column now

@@ -98,92 +98,134 @@ __global__ void rope_kernel(T* x, int B, int S, int nh, int d, long long sb, lon
 }
 
 // Gradient of the rotary embedding: the transposed rotation of each pair, from
-// dy to dx (which may be dy).  A block takes `per` consecutive positions of one
-// batch row at a time: it writes their cosines and sines to shared memory, then
-// moves 16 bytes (V pairs) per thread and step.  A pair's turns per position are
-// a sum of two fp32 (from fp64, once per block), and the turns at a position are
-// reduced to at most half a turn exactly: s hi and its rounding error, plus s lo.
-// So the fp32 sine and cosine are good to 2^-23 absolute at any position without
-// fp64 arithmetic per position (this part runs it at a fraction of fp32's rate).
+// dy to dx (which may be dy).  A thread owns V pairs (16 bytes) of one position
+// and walks over a group of heads, eight loads in flight, so it needs its sines
+// and cosines once.  A pair's turns per position are a sum of two fp32 (from fp64,
+// once per block, under the first loads), and the turns at a position are reduced
+// to at most half a turn exactly: s hi and its rounding error, plus s lo.  So the
+// fp32 sine and cosine are good to 2^-23 absolute at any position without fp64
+// arithmetic per position (this part runs it at a fraction of fp32's rate).  Bound
+// by memory and its latency; a table of sines per block in shared memory, as in
+// the forward, cost two barriers per few positions (18 us for [1, 4096, 64, 64]
+// bf16 against a floor of 10).
 struct RopeBack {
   const void* dy; void* dx;
   long long yb, ys, yh, xb, xs, xh;
-  int S, nh, d, per, chunks;             // chunks of `per` positions in a batch row
-  long long blocks;                      // chunks * B
+  int S, nh, d;
+  int heads;                             // per thread
+  int total;                             // threads that have work
   double step;                           // log2(theta) * 2 / d
-  FastDiv div_half, div_nv, div_nh;
+  FastDiv div_nv, div_s, div_groups;
 };
+constexpr int kRopeFlight = 8;
+// (a, b) -> (a c + b s, b c - a s)
+__device__ inline void turn_back(float& a, float& b, float c, float s) {
+  untwo(fma2(two(b, a), two(s, -s), mul2(two(a, b), two(c, c))), a, b);
+}
+// V pairs of one head and position: one 16-byte access, or two single values.
 template <typename T, int V>
-__global__ void __launch_bounds__(256) rope_back_kernel(const __grid_constant__ RopeBack p) {
-  extern __shared__ float2 turns[];      // [d/2] (hi, lo) turns per position, then [per][d/2] (cos, sin)
-  const int half = p.d / 2, nv = half / V;
-  float2* cs = turns + half;
-  for (int k = threadIdx.x; k < half; k += blockDim.x) {
-    const double t = exp2(-p.step * k) * 0.15915494309189535;
-    const float hi = (float)t;
-    turns[k] = make_float2(hi, (float)(t - hi));
+struct PairsOf;
+template <>
+struct PairsOf<__nv_bfloat16, 4> {
+  uint32_t w[4];
+  __device__ void load(const __nv_bfloat16* p) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
   }
-  for (long long blk = blockIdx.x; blk < p.blocks; blk += gridDim.x) {
-    const int b = (int)(blk / p.chunks), s0 = (int)(blk - (long long)b * p.chunks) * p.per, n = min(p.per, p.S - s0);
-    __syncthreads();
-    for (int x = threadIdx.x; x < n * half; x += blockDim.x) {
-      const int i = (int)fastdiv(x, p.div_half);
-      const float2 f = turns[x - i * half];
-      const float s = (float)(s0 + i), t = s * f.x, e = fmaf(s, f.x, -t);
-      float sn, cn;
-      sincospif(2.f * ((t - rintf(t)) + fmaf(s, f.y, e)), &sn, &cn);
-      cs[x] = make_float2(cn, sn);
-    }
-    __syncthreads();
-    const T* src = static_cast<const T*>(p.dy) + b * p.yb + s0 * p.ys;
-    T* dst = static_cast<T*>(p.dx) + b * p.xb + s0 * p.xs;
-    const int items = n * p.nh * nv;
-#pragma unroll 4
-    for (int x = threadIdx.x; x < items; x += blockDim.x) {
-      const int row = (int)fastdiv(x, p.div_nv), c = x - row * nv;
-      const int i = (int)fastdiv(row, p.div_nh), h = row - i * p.nh;
-      const T* from = src + i * p.ys + h * p.yh + 2 * V * c;
-      T* to = dst + i * p.xs + h * p.xh + 2 * V * c;
-      alignas(16) T v[2 * V];
-      if (V > 1) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(from);
-      else { v[0] = from[0]; v[1] = from[1]; }
-      alignas(16) float2 f[V];
-      if (V > 1) {
+  __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
+  __device__ void turn_back(const float (&c)[4], const float (&s)[4]) {
 #pragma unroll
-        for (int k = 0; k < V; k += 2) *reinterpret_cast<float4*>(f + k) = *reinterpret_cast<const float4*>(cs + i * half + V * c + k);
-      } else {
-        f[0] = cs[i * half + c];
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const float a = ldv(v + 2 * k), e = ldv(v + 2 * k + 1);
-        stv(v + 2 * k, fmaf(a, f[k].x, e * f[k].y));
-        stv(v + 2 * k + 1, fmaf(e, f[k].x, -(a * f[k].y)));
-      }
-      if (V > 1) *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(v);
-      else { to[0] = v[0]; to[1] = v[1]; }
+    for (int k = 0; k < 4; ++k) {
+      float a = __uint_as_float(w[k] << 16), b = __uint_as_float(w[k] & 0xffff0000u);
+      mc::turn_back(a, b, c[k], s[k]);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+      w[k] = *reinterpret_cast<const uint32_t*>(&r);
     }
+  }
+};
+template <>
+struct PairsOf<float, 2> {
+  float4 w;
+  __device__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
+  __device__ void store(float* p) const { *reinterpret_cast<float4*>(p) = w; }
+  __device__ void turn_back(const float (&c)[2], const float (&s)[2]) {
+    mc::turn_back(w.x, w.y, c[0], s[0]);
+    mc::turn_back(w.z, w.w, c[1], s[1]);
+  }
+};
+template <typename T>
+struct PairsOf<T, 1> {
+  T a, b;
+  __device__ void load(const T* p) { a = p[0]; b = p[1]; }
+  __device__ void store(T* p) const { p[0] = a; p[1] = b; }
+  __device__ void turn_back(const float (&c)[1], const float (&s)[1]) {
+    float x = ldv(&a), y = ldv(&b);
+    mc::turn_back(x, y, c[0], s[0]);
+    stv(&a, x);
+    stv(&b, y);
+  }
+};
+
+template <typename T, int V>
+__global__ void __launch_bounds__(256, 4) rope_back_kernel(const __grid_constant__ RopeBack p) {
+  extern __shared__ float2 turns[];      // [d/2] (hi, lo) turns per position
+  const int half = p.d / 2, nv = half / V;
+  const int t = (int)(blockIdx.x * 256 + threadIdx.x);
+  const int r0 = (int)fastdiv(t, p.div_nv), c = t - r0 * nv;
+  const int r1 = (int)fastdiv(r0, p.div_s), s = r0 - r1 * p.S;
+  const int b = (int)fastdiv(r1, p.div_groups);
+  const int groups = (p.nh + p.heads - 1) / p.heads;
+  const int h0 = (r1 - b * groups) * p.heads, h1 = t < p.total ? min(p.nh, h0 + p.heads) : h0;
+  const T* src = static_cast<const T*>(p.dy) + b * p.yb + s * p.ys + 2 * V * c;
+  T* dst = static_cast<T*>(p.dx) + b * p.xb + s * p.xs + 2 * V * c;
+  PairsOf<T, V> q[kRopeFlight];
+  // heads h .. h + 7 of the group (those that it has)
+  auto load = [&](int h) {
+    const T* from = src + h * p.yh;
+#pragma unroll
+    for (int n = 0; n < kRopeFlight; ++n, from += p.yh)
+      if (h + n < h1) q[n].load(from);
+  };
+  load(h0);
+  for (int k = threadIdx.x; k < half; k += 256) {
+    const double x = exp2(-p.step * k) * 0.15915494309189535;
+    const float hi = (float)x;
+    turns[k] = make_float2(hi, (float)(x - hi));
+  }
+  __syncthreads();
+  float cn[V], sn[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) {
+    const float2 f = turns[V * c + k];
+    const float at = (float)s, x = at * f.x, e = fmaf(at, f.x, -x);
+    sincospif(2.f * ((x - rintf(x)) + fmaf(at, f.y, e)), &sn[k], &cn[k]);
+  }
+  for (int h = h0; h < h1; h += kRopeFlight) {
+    if (h > h0) load(h);
+    T* to = dst + h * p.xh;
+#pragma unroll
+    for (int n = 0; n < kRopeFlight; ++n, to += p.xh)
+      if (h + n < h1) {
+        q[n].turn_back(cn, sn);
+        q[n].store(to);
+      }
   }
 }
 
 template <typename T, int V>
 cudaError_t launch_rope_back(RopeBack p, int B, cudaStream_t s) {
-  // positions per block: about 2048 accesses of its 256 threads, fewer while that
-  // leaves SMs without a block; the table stays within 48 KB
-  const int half = p.d / 2;
-  long long per = cdiv(2048, (long long)p.nh * (half / V));
-  const long long spread = cdiv((long long)p.S * B, 4ll * sm_count());
-  if (per > spread) per = spread;
-  const long long room = 48 * 1024 / 8 / half - 1;
-  if (per > room) per = room;
-  p.per = (int)(per < 1 ? 1 : per);
-  p.chunks = (int)cdiv(p.S, p.per);
-  p.blocks = (long long)p.chunks * B;
-  p.div_half = make_fastdiv((uint32_t)half);
-  p.div_nv = make_fastdiv((uint32_t)(half / V));
-  p.div_nh = make_fastdiv((uint32_t)p.nh);
-  const long long most = (long long)sm_count() * 8;
-  rope_back_kernel<T, V><<<(unsigned)(p.blocks < most ? p.blocks : most), 256, (size_t)half * 8 * (1 + p.per), s>>>(p);
+  // heads are split over threads as long as four blocks per SM, which are
+  // resident at once, take them
+  const int nv = p.d / 2 / V;
+  const long long at = (long long)B * p.S * nv, most = 4ll * 256 * sm_count() / at;
+  const int ways = (int)(most < 1 ? 1 : most > p.nh ? p.nh : most);
+  p.heads = (p.nh + ways - 1) / ways;
+  const int groups = (p.nh + p.heads - 1) / p.heads;
+  p.total = (int)(at * groups);          // below 2^31: at is checked, and groups > 1 stays within four blocks per SM
+  p.div_nv = make_fastdiv((uint32_t)nv);
+  p.div_s = make_fastdiv((uint32_t)p.S);
+  p.div_groups = make_fastdiv((uint32_t)groups);
+  rope_back_kernel<T, V><<<(unsigned)cdiv(at * groups, 256), 256, (size_t)(p.d / 2) * 8, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -329,7 +371,7 @@ mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, v
   const uintptr_t py = reinterpret_cast<uintptr_t>(dy), px = reinterpret_cast<uintptr_t>(dx);
   if (!same && py < px + endx * es && px < py + endy * es)
     return err(MC_ERR_INVALID_ARG, "%s: dx overlaps dy without being dy", me);
-  if ((long long)nh * (d / 2) >= (1 << 28)) return err(MC_ERR_UNSUPPORTED, "%s: %d heads of %d in one position", me, nh, d);
+  if ((long long)B * S > (1ll << 31) / (d / 2) / 2) return err(MC_ERR_UNSUPPORTED, "%s: B %d, S %d, d %d are too large", me, B, S, d);
   RopeBack p;
   memset(&p, 0, sizeof p);
   p.dy = dy; p.dx = dx;
