@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -17,6 +18,11 @@ from . import abi
 from .abi import McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat, check
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
+
+# McAttnDesc and McAttnGrad as packed values (a fraction of the time that ctypes
+# takes to convert their fields one by one)
+_ATTN_DESC = struct.Struct("@7if3P8q")
+_ATTN_GRAD = struct.Struct("@P2i3qP3qPP3qP3qP3qP2qP3q")
 
 
 def _ptr(t):
@@ -136,9 +142,10 @@ def attn_desc(q, k, k_shared=None, causal=True, scale=None) -> McAttnDesc:
         raise ValueError("q, k, k_shared must share a supported dtype")
     if scale is None:
         scale = 1.0 / math.sqrt(dq)
-    return McAttnDesc(B, S, H, dk, dr, _DT[q.dtype], 1 if causal else 0, scale, q.data_ptr(), k.data_ptr(),
-                      None if k_shared is None else k_shared.data_ptr(), q.stride()[:3], k.stride()[:3],
-                      (0, 0) if k_shared is None else k_shared.stride()[:2])
+    at, ks = (0, (0, 0)) if k_shared is None else (k_shared.data_ptr(), k_shared.stride())
+    return McAttnDesc.from_buffer_copy(_ATTN_DESC.pack(
+        B, S, H, dk, dr, _DT[q.dtype], 1 if causal else 0, scale, q.data_ptr(), k.data_ptr(), at,
+        *q.stride()[:3], *k.stride()[:3], ks[0], ks[1]))
 
 
 def qk_max_logit(q, k, k_shared=None, causal=True, scale=None, smax=None, argmax=None,
@@ -236,40 +243,51 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
     one is allocated for the call."""
     index = _device_of(q, "q", k, v, out, lse, dout, k_shared, dq, dk, dv, dk_shared, workspace, status)
     d = attn_desc(q, k, k_shared, causal, scale)
-    B, S, H, _ = q_shape = q.shape
-    v_shape, t = v.shape, q.dtype
-    dvw = v_shape[3]
-    if k.shape[:3] != q_shape[:3] or v_shape[:3] != q_shape[:3]:
-        raise ValueError("k and v must have q's batch, sequence and heads")
-    if k_shared is not None and k_shared.shape[:2] != q_shape[:2]:
-        raise ValueError("k_shared must be [B, S, dr]")
-    if lse.shape != (B, H, S) or not lse.is_contiguous() or lse.dtype != torch.float32:
+    B, S, H, _ = q.shape
+    t, dvw = q.dtype, v.shape[-1]
+    v_shape = (B, S, H, dvw)
+    if k.shape != (B, S, H, d.d_head):
+        raise ValueError("k must have q's batch, sequence and heads")
+    if lse.shape != (B, H, S) or lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous [B, H, S] float32 tensor")
-    for name, x in (("v", v), ("out", out), ("dout", dout)):
-        if x.shape != v_shape or x.stride(3) != 1 or x.dtype != t:
-            raise ValueError(f"{name} must be [B, S, H, d_v] with a contiguous feature axis and q's dtype")
-    if k_shared is None and dk_shared is not None:
+    vs, os, ds = v.stride(), out.stride(), dout.stride()
+    if (v.shape != v_shape or out.shape != v_shape or dout.shape != v_shape or v.dtype != t or out.dtype != t
+            or dout.dtype != t or vs[3] != 1 or os[3] != 1 or ds[3] != 1):
+        raise ValueError("v, out and dout must be [B, S, H, d_v] with contiguous feature axes and q's dtype")
+    dq = _grad_like("dq", dq, q)
+    dk = _grad_like("dk", dk, k)
+    dv = _grad_like("dv", dv, v)
+    dks_at, dks_strides = 0, (0, 0)
+    if k_shared is not None:
+        if k_shared.shape != (B, S, d.d_shared):
+            raise ValueError("k_shared must be [B, S, dr]")
+        dk_shared = _grad_like("dk_shared", dk_shared, k_shared)
+        dks_at, dks_strides = dk_shared.data_ptr(), dk_shared.stride()[:2]
+    elif dk_shared is not None:
         raise ValueError("dk_shared without k_shared")
-    grads = []
-    for name, g, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v), ("dk_shared", dk_shared, k_shared)):
-        if g is None and like is not None:
-            g = torch.empty(like.shape, dtype=t, device=q.device)
-        elif g is not None and (g.shape != like.shape or g.stride(-1) != 1 or g.dtype != t):
-            raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
-        grads.append(g)
-    dq, dk, dv, dk_shared = grads
     lib = abi.load()
     if workspace is None:
         n = ctypes.c_size_t(0)
         check(lib.qk_attention_backward_workspace_size(d, n), "qk_attention_backward_workspace_size")
-        workspace = torch.empty(n.value, dtype=torch.uint8, device=q.device)
-    g = McAttnGrad(v.data_ptr(), dvw, 0, v.stride()[:3], out.data_ptr(), out.stride()[:3], lse.data_ptr(),
-                   dout.data_ptr(), dout.stride()[:3], dq.data_ptr(), dq.stride()[:3], dk.data_ptr(), dk.stride()[:3],
-                   _at(dk_shared), (0, 0) if dk_shared is None else dk_shared.stride()[:2], dv.data_ptr(),
-                   dv.stride()[:3])
-    _run(lib.qk_attention_backward, "qk_attention_backward", index, stream, d, g, workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), _at(status))
+        workspace, nbytes = q.new_empty(n.value, dtype=torch.uint8), n.value
+    else:
+        nbytes = workspace.numel() * workspace.element_size()
+    g = McAttnGrad.from_buffer_copy(_ATTN_GRAD.pack(
+        v.data_ptr(), dvw, 0, *vs[:3], out.data_ptr(), *os[:3], lse.data_ptr(), dout.data_ptr(), *ds[:3],
+        dq.data_ptr(), *dq.stride()[:3], dk.data_ptr(), *dk.stride()[:3], dks_at, *dks_strides,
+        dv.data_ptr(), *dv.stride()[:3]))
+    _run(lib.qk_attention_backward, "qk_attention_backward", index, stream, d, g, workspace.data_ptr(), nbytes,
+         _at(status))
     return dq, dk, dv, dk_shared
+
+
+def _grad_like(name, g, like):
+    """The given gradient tensor, checked, or a new one of `like`'s shape."""
+    if g is None:
+        return like.new_empty(like.shape)
+    if g.shape != like.shape or g.stride(-1) != 1 or g.dtype != like.dtype:
+        raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
+    return g
 
 
 @dataclass
@@ -389,7 +407,7 @@ def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
     if len(shape) not in (3, 4) or dt is None or y[-1] != 1:
         raise ValueError("dy: [B, S, d] or [B, S, heads, d] with unit stride along d")
     if out is None:
-        out = torch.empty(shape, dtype=dy.dtype, device=dy.device)
+        out = dy.new_empty(shape)
     x = out.stride()
     if out.shape != shape or out.dtype != dy.dtype or x[-1] != 1:
         raise ValueError("out must have dy's shape and type and unit stride along d")
@@ -436,7 +454,6 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
     if out_dtype != t and not f8:
         raise ValueError(f"out_dtype: {t} or torch.float8_e4m3fn")
     rows, cols = shape
-    dev = x.device
     ldx = _pitch(x, "x", shape, t)
     if weight is not None:
         _vector(weight, "weight", cols, t)
@@ -444,22 +461,25 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
     if residual is not None:
         ldr = _pitch(residual, "residual", shape, t)
         if h is None:
-            h = torch.empty(shape, dtype=t, device=dev)
-        ldh = _pitch(h, "h", shape, t)
+            h, ldh = x.new_empty(shape), cols
+        else:
+            ldh = _pitch(h, "h", shape, t)
     elif h is not None:
         raise ValueError("h without residual: h is x itself")
     if out is None:
-        out = torch.empty(shape, dtype=out_dtype, device=dev)
-    ldy = _pitch(out, "out", shape, out_dtype)
+        out, ldy = x.new_empty(shape, dtype=out_dtype), cols
+    else:
+        ldy = _pitch(out, "out", shape, out_dtype)
     if f8:
         tiles = (rows, -(-cols // 128))
         if scales is None:
-            scales = torch.empty(tiles, dtype=torch.float32, device=dev)
-        lds = _pitch(scales, "scales", tiles, torch.float32)
+            scales, lds = x.new_empty(tiles, dtype=torch.float32), tiles[1]
+        else:
+            lds = _pitch(scales, "scales", tiles, torch.float32)
     elif scales is not None:
         raise ValueError("scales go with out_dtype=torch.float8_e4m3fn")
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        rstd = x.new_empty(rows, dtype=torch.float32)
     else:
         _vector(rstd, "rstd", rows, torch.float32)
     _run(abi.load().mc_add_rms_norm, "mc_add_rms_norm", index, stream, x.data_ptr(), ldx, _at(residual), ldr,
@@ -486,17 +506,18 @@ def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None
     ldr = 0 if dres is None else _pitch(dres, "dres", shape, t)
     _vector(rstd, "rstd", rows, torch.float32)
     if dx is None:
-        dx = torch.empty(shape, dtype=t, device=dy.device)
-    lddx = _pitch(dx, "dx", shape, t)
+        dx, lddx = dy.new_empty(shape), cols
+    else:
+        lddx = _pitch(dx, "dx", shape, t)
     if weight is not None:
         _vector(weight, "weight", cols, t)
         if dweight is None:
-            dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
+            dweight = dy.new_empty(cols, dtype=torch.float32)
     nbytes = 0
     if dweight is not None:
         _vector(dweight, "dweight", cols, torch.float32)
         if workspace is None:
-            workspace = torch.empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8, device=dy.device)
+            workspace = dy.new_empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8)
         nbytes = workspace.numel() * workspace.element_size()
     _run(abi.load().mc_rms_norm_backward, "mc_rms_norm_backward", index, stream, dy.data_ptr(), lddy, h.data_ptr(),
          ldh, rstd.data_ptr(), _at(weight), _at(dres), ldr, dx.data_ptr(), lddx, _at(dweight), rows, cols, dt,

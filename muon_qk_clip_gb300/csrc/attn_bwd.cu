@@ -1232,7 +1232,8 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
             encode(&kv.v, p.v, p.d_v, p.H, p.S, p.B, p.vs, BM) && encode(&kv.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, nq) &&
             (p.d_shared == 0 || encode(&kv.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, BM));
   qm = kv;
-  ok = ok && encode(&qm.q, p.q, D, p.H, p.S, p.B, p.qs, BM) && encode(&qm.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, BM);
+  if (nq != BM)
+    ok = ok && encode(&qm.q, p.q, D, p.H, p.S, p.B, p.qs, BM) && encode(&qm.d_o, p.d_o, p.d_v, p.H, p.S, p.B, p.dos, BM);
   if (nk != BM)
     ok = ok && encode(&qm.k, p.k, p.d_head, p.H, p.S, p.B, p.kst, nk) && encode(&qm.v, p.v, p.d_v, p.H, p.S, p.B, p.vs, nk) &&
          (p.d_shared == 0 || encode(&qm.ks, p.ks, p.d_shared, 0, p.S, p.B, p.kss, nk));

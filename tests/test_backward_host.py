@@ -259,3 +259,18 @@ def test_norm_bindings_refuse_host_tensors():
                  lambda: mc.rope_backward(torch.zeros(1, 2, 8))):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_packed_descriptors_match_the_structures():
+    """The binding packs the attention descriptors by format: every field arrives."""
+    assert mc._ATTN_DESC.size == ctypes.sizeof(McAttnDesc) and mc._ATTN_GRAD.size == ctypes.sizeof(McAttnGrad)
+    d = McAttnDesc.from_buffer_copy(mc._ATTN_DESC.pack(*range(1, 8), 0.5, *range(9, 20)))
+    assert [d.B, d.S, d.H, d.d_head, d.d_shared, d.dtype, d.causal, d.scale] == [1, 2, 3, 4, 5, 6, 7, 0.5]
+    assert [d.q, d.k, d.k_shared, *d.q_strides, *d.k_strides, *d.ks_strides] == list(range(9, 20))
+    n = len(mc._ATTN_GRAD.unpack(bytes(mc._ATTN_GRAD.size)))
+    g = McAttnGrad.from_buffer_copy(mc._ATTN_GRAD.pack(*range(1, n + 1)))
+    flat = []
+    for name, _ in McAttnGrad._fields_:
+        x = getattr(g, name)
+        flat += list(x) if hasattr(x, "__len__") else [x]
+    assert flat == list(range(1, n + 1))
