@@ -8,12 +8,12 @@
 //   dq_i  = scale sum_j ds_ij k_j
 //   dk_j  = scale sum_i ds_ij q_i             (its shared rotary columns summed over the heads)
 //
-// Four launches on the caller's stream, no atomics, so equal inputs give equal
-// bits:
+// Three launches on the caller's stream (two without a shared key), no atomics
+// on results, so equal inputs give equal bits:
 //   rows_kernel     delta and -lse log2(e) of every row, padded to whole tiles
-//   dkv_kernel      one CTA per 128 keys, loop over query tiles: S^T = K Q^T,
-//                   dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
-//   dq_kernel       one CTA per 128 queries, loop over key tiles: S = Q K^T,
+//   bwd_kernel      dkv_pass: an item is 128 keys, loop over query tiles:
+//                   S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
+//                   then dq_pass: 128 queries, loop over key tiles: S = Q K^T,
 //                   dP = dO V^T, dQ += dS K
 //   shared_kernel   the shared key's gradient, summed over the heads in order
 // Two passes recompute S and dP (7 products for the 5 that the formulas need),
@@ -129,6 +129,10 @@ template <int N>
 __device__ inline void regs_release() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ inline void regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
+enum Role { kIssue, kOutput, kCompute };
+// All threads of the block, whichever role's code they are in.
+__device__ inline void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 // True in one lane of the (whole) warp.  The MMA issuer runs as a whole warp
 // with the products under this predicate, so that descriptors stay in uniform
@@ -342,24 +346,21 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
 // queries and thread from shared memory; with a key's whole row per thread every
 // one of these loads was a 16-byte broadcast, 512 bytes of return bandwidth for
 // each four queries of each warp, next to the operand reads of the tensor core.
-template <int NCH, int NCV>
-__global__ void __launch_bounds__(kThreads, 1)
-    dkv_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+template <int NCH, int NCV, int ROLE>
+__device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp, const Geo& g, uint8_t* smem, uint64_t* bars,
+                                         uint32_t tmem_base, volatile int& abort_flag, int warp, int lane) {
   constexpr int NQ = query_tile(NCH, NCV);
   constexpr bool APART = p_apart(NCH, NCV);
   constexpr int kStages = query_stages(NCH, NCV);
   constexpr int NH = NQ / 2;             // queries per compute warp
   constexpr int NU = NH / 16;            // in units of 16
   constexpr int CQ = NQ * 128;           // bytes of one chunk of a query tile
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* kbuf = smem;                                    // NCH chunks
   uint8_t* vbuf = kbuf + NCH * CH;                         // NCV chunks
   uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
   uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
   float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, -delta][NQ]
   uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [4 warps][2 KB]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * 2048);
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
   uint64_t* q_full = bars + 2;      // [stages <= 3] Q tile with its nlse and delta
@@ -378,12 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* dk_empty = bars + 23;
   uint64_t* drain = bars + 24;
   const Ring ring = {reinterpret_cast<volatile int*>(bars + 34), bars + 25, bars + 29};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 33);
-  __shared__ volatile int abort_flag;
-
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform to the compiler
   if (threadIdx.x == 0) {
-    abort_flag = 0;
     mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&q_full[s], 1); mbar_init(&q_empty[s], 1);
@@ -402,19 +398,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
     if (NCH > g.nck) prefetch_tmap(&mp.ks);
   }
-  if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  block_sync();
   const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * NCH, t_s = t_dv + 64 * NCV, t_dp = t_s + NQ, t_p = APART ? t_dp + NQ : t_s;
   constexpr uint32_t kHalfP = APART ? NH / 2 : NH;       // second half of the queries in P^T
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   // first query tile that has a query at or behind the block's first key
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
 
-  if (warp < 4) regs_release<kRegsIssue>();
-  if (warp == 0) {
+  if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t li = 0, s = 0, ph = 0;
@@ -464,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (used_do[i]) mbar_wait(&do_full[i], par_do[i], nullptr);
       }
     }
-  } else if (warp == 1) {
+  } else if (ROLE == kIssue && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_s = make_idesc_bf16(BM, NQ, 0, 0);
     constexpr uint32_t idesc_dv = make_idesc_bf16(BM, 64 * NCV, 0, 1);
@@ -558,13 +549,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(drain, 0, nullptr);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (ROLE == kOutput) {
     // ------------------------------------------------------------ output
     // Warp w: keys 32 q .. 32 q + 31 of the block, every column: dV as soon as the
     // item's last dV product is done, then scale * dK (the shared key's columns go
     // to the per-head fp32 partial sums), while the other warps are at the next
     // item.
-    regs_release<kRegsOutput>();
     const int q = warp & 3;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     uint8_t* mine = stage + q * 2048;
@@ -621,9 +611,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) fail();
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
-  } else if (warp >= 8) {
+  } else if (ROLE == kCompute) {
     // ------------------------------------------------------------ P, dS
-    regs_acquire<kRegsCompute>();
     // Warp e = warp - 8: keys 32 q .. 32 q + 31 of the block (q = warp & 3, its
     // TMEM lane quadrant), queries of half e >> 2 of the tile.  A thread holds
     // keys r0, r0 + 8, r0 + 16, r0 + 24 and, of each 8 queries, the two from c0.
@@ -751,12 +740,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  // everything in flight has landed and been read: the next pass may reuse tensor
+  // memory and shared memory (its barriers have memory of their own)
+  fence_async_smem();
   tc_fence_before();
-  __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
-  }
+  block_sync();
+  tc_fence_after();
 }
 
 // --------------------------------------------------------------------- dQ
@@ -770,20 +759,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 // dP(t+1) as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1),
 // dQ(t).  A key tile is held from S(t) to dQ(t), two products later than the next
 // one's S wants its own, so keys and values have three stages.
-template <int NCH, int NCV>
-__global__ void __launch_bounds__(kThreads, 1)
-    dq_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps mp, const Geo g) {
+template <int NCH, int NCV, int ROLE>
+__device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, const Geo& g, uint8_t* smem, uint64_t* bars,
+                                         uint32_t tmem_base, volatile int& abort_flag, int warp, int lane) {
   constexpr int BN = key_tile(NCH, NCV), NH = BN / 2;
   constexpr int kStages = kKeyStages;
   constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;                                 // NCH chunks
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
   uint8_t* vbuf = kbuf + kStages * NCH * CK;           // 3 x NCV chunks
   uint8_t* stage = vbuf + kStages * NCV * CK;                     // [4 warps][2 KB]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * 2048);
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
@@ -799,12 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_empty = bars + 20;
   uint64_t* drain = bars + 21;
   const Ring ring = {reinterpret_cast<volatile int*>(bars + 31), bars + 22, bars + 26};
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
-  __shared__ volatile int abort_flag;
-
-  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform to the compiler
   if (threadIdx.x == 0) {
-    abort_flag = 0;
     mbar_init(q_full, 1); mbar_init(q_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1);
@@ -821,11 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&mp.q); prefetch_tmap(&mp.k); prefetch_tmap(&mp.v); prefetch_tmap(&mp.d_o);
     if (NCH > g.nck) prefetch_tmap(&mp.ks);
   }
-  if (warp == 1) { tmem_alloc(tmem_slot, kTmemCols); tmem_relinquish(); }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  block_sync();
   const uint32_t t_dq = tmem_base, t_q = t_dq + 64 * NCH, t_do = t_q + 32 * NCH, t_s = t_do + 32 * NCV, t_dp = t_s + BN, t_ds = t_dp + BN;
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   auto tiles = [&](int blk) {
@@ -833,8 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     return (hi + BN - 1) / BN;
   };
 
-  if (warp < 4) regs_release<kRegsIssue>();
-  if (warp == 0) {
+  if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
       uint32_t li = 0, s = 0, ph = 0;
@@ -878,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (used_v[i]) mbar_wait(&v_full[i], par_v[i], nullptr);
       }
     }
-  } else if (warp == 1) {
+  } else if (ROLE == kIssue && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc_s = make_idesc_bf16(BM, BN, 0, 0);
     constexpr uint32_t idesc_dq = make_idesc_bf16(BM, 64 * NCH, 0, 1);
@@ -967,11 +943,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       mbar_wait(drain, 0, nullptr);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (ROLE == kOutput) {
     // ------------------------------------------------------------ output
     // Warp w: queries 32 q .. 32 q + 31 of the block: scale * dQ, while the other
     // warps are at the next item
-    regs_release<kRegsOutput>();
     const int q = warp & 3, D = p.d_head + p.d_shared;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
     uint8_t* mine = stage + q * 2048;
@@ -993,9 +968,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok && lane == 0) fail();
     if (__any_sync(0xffffffffu, bad) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
-  } else if (warp >= 8) {
+  } else if (ROLE == kCompute) {
     // ------------------------------------------------------------ P, dS
-    regs_acquire<kRegsCompute>();
     const int q = warp & 3, hf = (warp - 8) >> 2;
     const int row = q * 32 + lane;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
@@ -1086,11 +1060,64 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!ok && lane == 0) fail();
   }
 
+  // everything in flight has landed and been read: the next pass may reuse tensor
+  // memory and shared memory (its barriers have memory of their own)
+  fence_async_smem();
+  tc_fence_before();
+  block_sync();
+  tc_fence_after();
+}
+
+// ---------------------------------------------------------------- both passes
+// One persistent CTA per SM takes dK / dV items until there are none, then dQ
+// items: the second pass starts wherever the first one has run out, with no
+// launch in between, and a small batch runs both at once on different SMs.
+constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
+
+template <int NCH, int NCV>
+constexpr size_t smem_bytes() {
+  const size_t nq = query_tile(NCH, NCV), nk = key_tile(NCH, NCV), own = (size_t)(NCH + NCV);
+  const size_t kv = own * CH + query_stages(NCH, NCV) * (own * nq * 128 + 2 * nq * 4) + 4 * 2048;
+  const size_t q = own * CH + kKeyStages * own * nk * 128 + 4 * 2048;
+  return 1024 + 2 * kBarBytes + (kv > q ? kv : q);      // 1024: alignment
+}
+
+template <int NCH, int NCV>
+__global__ void __launch_bounds__(kThreads, 1)
+    bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps kv, const __grid_constant__ Maps qm,
+               const __grid_constant__ Geo g) {
+  static_assert(smem_bytes<NCH, NCV>() + 64 <= 227 * 1024, "shared memory");
+  static_assert(64 * (NCH + NCV) + 2 * query_tile(NCH, NCV) + (p_apart(NCH, NCV) ? query_tile(NCH, NCV) / 2 : 0) <= 512 &&
+                96 * NCH + 32 * NCV + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ volatile int abort_flag;
+  __shared__ uint32_t tmem_slot;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;   // uniform to the compiler
+  if (threadIdx.x == 0) abort_flag = 0;
+  if (warp == 1) { tmem_alloc(&tmem_slot, kTmemCols); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
-    tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_slot;
+  uint64_t *bars = reinterpret_cast<uint64_t*>(smem), *bars2 = bars + kBarBytes / 8;
+  uint8_t* data = smem + 2 * kBarBytes;
+  // one branch per role, its register share at the head of it: the compiler
+  // allocates the code behind a setmaxnreg by that.  (A pass that gave up waiting
+  // leaves the flag up: the second one ends at its first wait.)
+  if (warp < 4) {
+    regs_release<kRegsIssue>();
+    dkv_pass<NCH, NCV, kIssue>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, kIssue>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
+    if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
+  } else if (warp < 8) {
+    regs_release<kRegsOutput>();
+    dkv_pass<NCH, NCV, kOutput>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, kOutput>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
+  } else {
+    regs_acquire<kRegsCompute>();
+    dkv_pass<NCH, NCV, kCompute>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, kCompute>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
   }
 }
 
@@ -1182,19 +1209,10 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
 
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
-  constexpr int NQ = query_tile(NCH, NCV);
-  constexpr size_t skv = 1024 + (size_t)(NCH + NCV) * CH + query_stages(NCH, NCV) * ((size_t)(NCH + NCV) * NQ * 128 + 2 * NQ * 4) + 4 * 2048 + 320;
-  constexpr size_t sq = 1024 + (size_t)(NCH + NCV) * CH + (size_t)kKeyStages * (NCH + NCV) * key_tile(NCH, NCV) * 128 + 4 * 2048 + 320;
-  static_assert(skv + 64 <= 227 * 1024 && sq + 64 <= 227 * 1024, "shared memory");
-  static_assert(64 * (NCH + NCV) + 2 * NQ + (p_apart(NCH, NCV) ? NQ / 2 : 0) <= 512 && 96 * NCH + 32 * NCV + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
-  cudaError_t e = cudaFuncSetAttribute(dkv_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)skv);
+  constexpr size_t smem = smem_bytes<NCH, NCV>();
+  const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  dkv_kernel<NCH, NCV><<<grid, kThreads, skv, s>>>(p, kv, g);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(dq_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sq);
-  if (e != cudaSuccess) return e;
-  dq_kernel<NCH, NCV><<<grid, kThreads, sq, s>>>(p, qm, g);
+  bwd_kernel<NCH, NCV><<<grid, kThreads, smem, s>>>(p, kv, qm, g);
   return cudaGetLastError();
 }
 
@@ -1244,7 +1262,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   rows_kernel<<<(unsigned)(ni * nh * p.B), 256, 0, s>>>(p, (int)g.sp, (int)ni, (int)nh);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int grid = (int)(g.items < sms ? g.items : sms);
+  const int grid = 2 * g.items < sms ? 2 * g.items : sms;
   using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
   static const Launch by_chunks[3][2] = {{launch_passes<1, 1>, launch_passes<1, 2>},
                                          {launch_passes<2, 1>, launch_passes<2, 2>},
