@@ -263,10 +263,10 @@ __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long 
 // ------------------------------------------------------------------- rows
 // -delta_i = -sum_c do_ic o_ic (fp32) and nlse_i = -lse_i log2(e) per (b, h, i),
 // in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
-// delta = 0.  A block takes 32 positions of 8 heads: 16 lanes per row with 8
+// delta = 0.  A block takes 16 positions of 8 heads: 16 lanes per row with 8
 // features each, the results written through shared memory so that a warp stores
-// 32 positions of a head.
-constexpr int kRowPos = 32, kRowHeads = 8;
+// 16 positions of a head.
+constexpr int kRowPos = 16, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
   __shared__ float sums[kRowHeads][kRowPos + 1];
@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
     }
   }
   __syncthreads();
-  const int h = h0 + threadIdx.x / 32, i = i0 + threadIdx.x % 32;
-  if (h < p.H && i < sp) {
+  const int h = h0 + threadIdx.x / kRowPos, i = i0 + threadIdx.x % kRowPos;
+  if (threadIdx.x < kRowPos * kRowHeads && h < p.H && i < sp) {
     const long long bh = (long long)b * p.H + h;
-    p.ndelta[bh * sp + i] = -sums[threadIdx.x / 32][threadIdx.x % 32];
+    p.ndelta[bh * sp + i] = -sums[threadIdx.x / kRowPos][threadIdx.x % kRowPos];
     p.nlse[bh * sp + i] = i < p.S ? -p.lse[bh * p.S + i] * kLog2e : -INFINITY;
   }
 }
