@@ -269,7 +269,7 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
     if workspace is None:
         n = ctypes.c_size_t(0)
         check(lib.qk_attention_backward_workspace_size(d, n), "qk_attention_backward_workspace_size")
-        workspace, nbytes = q.new_empty(n.value, dtype=torch.uint8), n.value
+        workspace, nbytes = torch.empty(n.value, dtype=torch.uint8, device=q.device), n.value
     else:
         nbytes = workspace.numel() * workspace.element_size()
     g = McAttnGrad.from_buffer_copy(_ATTN_GRAD.pack(
@@ -284,7 +284,7 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
 def _grad_like(name, g, like):
     """The given gradient tensor, checked, or a new one of `like`'s shape."""
     if g is None:
-        return like.new_empty(like.shape)
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     if g.shape != like.shape or g.stride(-1) != 1 or g.dtype != like.dtype:
         raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
     return g
@@ -407,7 +407,7 @@ def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
     if len(shape) not in (3, 4) or dt is None or y[-1] != 1:
         raise ValueError("dy: [B, S, d] or [B, S, heads, d] with unit stride along d")
     if out is None:
-        out = dy.new_empty(shape)
+        out = torch.empty(shape, dtype=dy.dtype, device=dy.device)
     x = out.stride()
     if out.shape != shape or out.dtype != dy.dtype or x[-1] != 1:
         raise ValueError("out must have dy's shape and type and unit stride along d")
@@ -454,6 +454,7 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
     if out_dtype != t and not f8:
         raise ValueError(f"out_dtype: {t} or torch.float8_e4m3fn")
     rows, cols = shape
+    dev = x.device
     ldx = _pitch(x, "x", shape, t)
     if weight is not None:
         _vector(weight, "weight", cols, t)
@@ -461,25 +462,25 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
     if residual is not None:
         ldr = _pitch(residual, "residual", shape, t)
         if h is None:
-            h, ldh = x.new_empty(shape), cols
+            h, ldh = torch.empty(shape, dtype=t, device=dev), cols
         else:
             ldh = _pitch(h, "h", shape, t)
     elif h is not None:
         raise ValueError("h without residual: h is x itself")
     if out is None:
-        out, ldy = x.new_empty(shape, dtype=out_dtype), cols
+        out, ldy = torch.empty(shape, dtype=out_dtype, device=dev), cols
     else:
         ldy = _pitch(out, "out", shape, out_dtype)
     if f8:
         tiles = (rows, -(-cols // 128))
         if scales is None:
-            scales, lds = x.new_empty(tiles, dtype=torch.float32), tiles[1]
+            scales, lds = torch.empty(tiles, dtype=torch.float32, device=dev), tiles[1]
         else:
             lds = _pitch(scales, "scales", tiles, torch.float32)
     elif scales is not None:
         raise ValueError("scales go with out_dtype=torch.float8_e4m3fn")
     if rstd is None:
-        rstd = x.new_empty(rows, dtype=torch.float32)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _vector(rstd, "rstd", rows, torch.float32)
     _run(abi.load().mc_add_rms_norm, "mc_add_rms_norm", index, stream, x.data_ptr(), ldx, _at(residual), ldr,
@@ -506,18 +507,18 @@ def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None
     ldr = 0 if dres is None else _pitch(dres, "dres", shape, t)
     _vector(rstd, "rstd", rows, torch.float32)
     if dx is None:
-        dx, lddx = dy.new_empty(shape), cols
+        dx, lddx = torch.empty(shape, dtype=t, device=dy.device), cols
     else:
         lddx = _pitch(dx, "dx", shape, t)
     if weight is not None:
         _vector(weight, "weight", cols, t)
         if dweight is None:
-            dweight = dy.new_empty(cols, dtype=torch.float32)
+            dweight = torch.empty(cols, dtype=torch.float32, device=dy.device)
     nbytes = 0
     if dweight is not None:
         _vector(dweight, "dweight", cols, torch.float32)
         if workspace is None:
-            workspace = dy.new_empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8)
+            workspace = torch.empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8, device=dy.device)
         nbytes = workspace.numel() * workspace.element_size()
     _run(abi.load().mc_rms_norm_backward, "mc_rms_norm_backward", index, stream, dy.data_ptr(), lddy, h.data_ptr(),
          ldh, rstd.data_ptr(), _at(weight), _at(dres), ldr, dx.data_ptr(), lddx, _at(dweight), rows, cols, dt,
