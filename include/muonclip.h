@@ -412,7 +412,8 @@ mc_status mc_rope(void* x, int32_t B, int32_t S, int32_t nh, int32_t d, int64_t 
  * [b, s, h, 0..d) with strides (yb, ys, yh) and (xb, xs, xh) in elements, unit
  * stride along d; dx == dy with equal strides rotates in place, any other
  * overlap is refused, as is a dx with shared addresses.  Types, d and theta as
- * in mc_rope; B or S of 0 returns at once.  Asynchronous on `stream`. */
+ * in mc_rope, for angles up to 2^24: S max(1, 1/theta) <= 2^24 (else
+ * MC_ERR_UNSUPPORTED); B or S of 0 returns at once.  Asynchronous on `stream`. */
 mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, void* dx, int64_t xb, int64_t xs,
                            int64_t xh, int32_t B, int32_t S, int32_t nh, int32_t d, int32_t dtype, double theta,
                            mc_stream_t stream);

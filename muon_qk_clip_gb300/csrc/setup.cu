@@ -103,7 +103,8 @@ __global__ void rope_kernel(T* x, int B, int S, int nh, int d, long long sb, lon
 // and cosines once.  A pair's turns per position are a sum of two fp32 (from fp64,
 // once per block, under the first loads), and the turns at a position are reduced
 // to at most half a turn exactly: s hi and its rounding error, plus s lo.  So the
-// fp32 sine and cosine are good to 2^-23 absolute at any position without fp64
+// fp32 sine and cosine are good to 2^-22 absolute at any angle up to 2^24 (two
+// fp32 hold 2^-48 of the turn per position; larger ones are refused) without fp64
 // arithmetic per position (this part runs it at a fraction of fp32's rate).  Bound
 // by memory and its latency; a table of sines per block in shared memory, as in
 // the forward, cost two barriers per few positions (18 us for [1, 4096, 64, 64]
@@ -352,6 +353,9 @@ mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, v
     return err(MC_ERR_INVALID_ARG, "%s: B %d, S %d, heads %d, d %d (d even, 2..4096)", me, B, S, nh, d);
   if (!(theta > 0.0) || !std::isfinite(theta)) return err(MC_ERR_INVALID_ARG, "%s: theta must be finite and > 0", me);
   if ((long long)B * S == 0) return done();
+  // positions are exact as fp32, and angles keep the accuracy of their two-fp32 turns
+  if (S * (theta < 1.0 ? 1.0 / theta : 1.0) > 0x1p24)
+    return err(MC_ERR_UNSUPPORTED, "%s: S %d, theta %g: angles beyond 2^24 are too large", me, S, theta);
   if (!dy || !dx) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
   const size_t es = esize(dtype);
   if (reinterpret_cast<uintptr_t>(dy) % es || reinterpret_cast<uintptr_t>(dx) % es)

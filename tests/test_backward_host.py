@@ -249,6 +249,15 @@ def test_rope_backward_refuses(lib, kw, needle):
     assert needle in lib.mc_last_error().decode()
 
 
+@pytest.mark.parametrize("kw", [
+    dict(B=1, S=(1 << 24) + 1, nh=1, d=2, ys=2, xs=2),      # a position that fp32 does not hold
+    dict(theta=1e-7),                                       # 8 positions of up to 1e7 radians each
+    dict(theta=1e-300)])
+def test_rope_backward_refuses_angles_that_it_cannot_hold(lib, kw):
+    assert lib.mc_rope_backward(*rope(**kw)) == UNS
+    assert "angles" in lib.mc_last_error().decode()
+
+
 def test_rope_backward_of_nothing_is_a_no_op(lib):
     assert lib.mc_rope_backward(*rope(B=0, dy=None, dx=None)) == abi.MC_OK
 

@@ -227,10 +227,11 @@ def check_rope(dy, out, theta):
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("B,S,nh,d,skip,theta", [
     (1, 1, 1, 2, 0, 10000.0), (2, 700, 3, 64, 128, 10000.0), (1, 5000, 1, 64, 0, 10000.0), (3, 17, 5, 6, 1, 500.0),
-    (1, 33, 2, 4096, 0, 1e6), (2, 9, 70, 30, 2, 10000.0), (1, 40000, 1, 16, 0, 10000.0)])
+    (1, 33, 2, 4096, 0, 1e6), (2, 9, 70, 30, 2, 10000.0), (1, 40000, 1, 16, 0, 10000.0),
+    (1, 1 << 20, 1, 4, 0, 0.25), (1, 200, 3, 8, 0, 1e-4)])
 def test_rope_backward_parity(B, S, nh, d, skip, theta, dtype):
     """Out of place and in place, on the rotary columns of wider heads, at
-    positions up to 39999; aligned and unaligned slices."""
+    positions up to 2^20 and angles up to 2^22; aligned and unaligned slices."""
     full = normal((B, S, nh, skip + d), 0.5, "rd", dtype)
     keep = full.clone()
     dy = full[..., skip:]
