@@ -289,8 +289,9 @@ mc_status qk_attention_forward(const mc_attn_desc* attn, const mc_attn_out* out,
  * Everything is bf16 but lse; features have unit stride; the other strides are
  * in elements, multiples of 8 (axes of one element: any), and pointers are
  * 16-byte aligned.  Inputs may broadcast (stride 0); an output gives every
- * element an address of its own and overlaps no input, no other output and not
- * the workspace (outputs may interleave, as dk and dv in one buffer). */
+ * element an address of its own and overlaps no input, not lse, status or the
+ * workspace, and no other output (two outputs may interleave, as dk and dv of
+ * one buffer: equal strides on the axes around the blocks that alternate). */
 typedef struct {
   const void* v;           /* device values [B, S, H, d_v]                          */
   int32_t d_v;             /* value width, 16..128                                  */

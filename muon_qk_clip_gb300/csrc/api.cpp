@@ -992,11 +992,50 @@ mc_status check_attn_tensor(const char* name, const void* ptr, const int64_t* st
     out[i] = extent[i] == 1 ? round_up(width, 8) : st[i];
     if (out[i] < 0) return fail(MC_ERR_INVALID_ARG, "attention backward: %s has a negative stride", name);
     if (out[i] % 8) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides must be multiples of 8 elements", name);
-    if (out[i] >= (1ll << 38)) return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides are too large", name);
+    if (out[i] >= (1ll << 38) || (extent[i] > 1 && out[i] > (1ll << 46) / (extent[i] - 1)))
+      return fail(MC_ERR_UNSUPPORTED, "attention backward: %s strides are too large", name);
   }
   if (output && !distinct_addresses(st, extent, n, width))
     return fail(MC_ERR_INVALID_ARG, "attention backward: elements of %s share addresses", name);
   return MC_OK;
+}
+
+// Addresses that an operand lies within.
+struct Span { uintptr_t lo, hi; };
+Span span_of(const void* p, int64_t bytes) {
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+  return {lo, lo + (uintptr_t)bytes};
+}
+bool meet(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+// Whether two outputs (each with addresses of its own), the second one `apart`
+// elements behind the first, share no address although their spans meet: their
+// outer axes agree, the blocks under these axes lie beside each other, and
+// blocks as wide as both together still have addresses of their own.
+bool interleave(const int64_t* sa, int na, int64_t wa, const int64_t* sb, int nb, int64_t wb, const int64_t* extent,
+                int64_t apart) {
+  struct Axes { int64_t s[3], e[3]; int n; } a{{}, {}, 0}, b{{}, {}, 0};
+  auto sort = [&](Axes& x, const int64_t* s, int n) {    // by descending stride
+    for (int i = 0; i < n; ++i) {
+      if (extent[i] <= 1) continue;
+      int j = x.n++;
+      for (; j > 0 && x.s[j - 1] < s[i]; --j) { x.s[j] = x.s[j - 1]; x.e[j] = x.e[j - 1]; }
+      x.s[j] = s[i];
+      x.e[j] = extent[i];
+    }
+  };
+  sort(a, sa, na);
+  sort(b, sb, nb);
+  for (int k = 0; k <= a.n && k <= b.n; ++k) {           // k outer axes in common
+    if (k > 0 && (a.s[k - 1] != b.s[k - 1] || a.e[k - 1] != b.e[k - 1])) return false;
+    int64_t la = wa, lb = wb;
+    for (int i = k; i < a.n; ++i) la += a.s[i] * (a.e[i] - 1);
+    for (int i = k; i < b.n; ++i) lb += b.s[i] * (b.e[i] - 1);
+    if (apart < la && apart + lb > 0) continue;
+    const int64_t from = apart < 0 ? apart : 0, to = la > apart + lb ? la : apart + lb;
+    if (distinct_addresses(a.s, a.e, k, to - from)) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -1040,30 +1079,43 @@ mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, vo
       {"dk_shared", g->dk_shared, g->dks_strides, 2, a->d_shared, true, p.dkshs},
   };
   const int nt = a->d_shared > 0 ? 10 : 8;
-  uintptr_t lo[10], hi[10];
+  Span at[10];
   for (int i = 0; i < nt; ++i) {
     st = check_attn_tensor(ts[i].name, ts[i].ptr, ts[i].st, ts[i].n, ext, ts[i].width, ts[i].out, ts[i].to);
     if (st != MC_OK) return st;
     int64_t last = ts[i].width;
     for (int d = 0; d < ts[i].n; ++d) last += (ext[d] - 1) * ts[i].to[d];
-    lo[i] = reinterpret_cast<uintptr_t>(ts[i].ptr);
-    hi[i] = lo[i] + (uintptr_t)last * 2;
+    at[i] = span_of(ts[i].ptr, last * 2);
   }
-  // a launch reads its inputs while others' outputs are written: no output may
-  // lie among the inputs (two outputs may interleave, as dk and dv of one buffer)
-  for (int i = 0; i < nt; ++i)
-    for (int j = 0; j < nt; ++j)
-      if (ts[i].out && i != j) {
-        if (!ts[j].out && lo[i] < hi[j] && lo[j] < hi[i])
-          return fail(MC_ERR_INVALID_ARG, "attention backward: %s overlaps %s", ts[i].name, ts[j].name);
-        if (ts[j].out && lo[i] == lo[j])
-          return fail(MC_ERR_INVALID_ARG, "attention backward: %s and %s are the same memory", ts[i].name, ts[j].name);
-      }
   if (!g->lse || (reinterpret_cast<uintptr_t>(g->lse) & 3u) != 0)
     return fail(MC_ERR_INVALID_ARG, "attention backward: lse must be given, 4-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(status) & 3u) != 0)
+    return fail(MC_ERR_INVALID_ARG, "attention backward: status must be 4-byte aligned");
   const AttnBwdPlan w = plan_attn_bwd(a->B, a->S, a->H, a->d_shared);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return fail(MC_ERR_WORKSPACE, "attention backward: workspace must be given, 256-byte aligned");
+  // a launch reads its inputs while others' outputs are written: no output may
+  // lie among the inputs, nor anything in the workspace (two outputs may
+  // interleave, as dk and dv of one buffer)
+  const Span lse = span_of(g->lse, (int64_t)a->B * a->H * a->S * 4), ws = span_of(workspace, (int64_t)w.bytes),
+             flag = span_of(status, status ? 4 : 0);
+  if (meet(lse, ws) || meet(flag, ws) || meet(flag, lse))
+    return fail(MC_ERR_INVALID_ARG, "attention backward: lse, status and workspace overlap");
+  for (int i = 0; i < nt; ++i) {
+    if (meet(at[i], ws)) return fail(MC_ERR_INVALID_ARG, "attention backward: the workspace overlaps %s", ts[i].name);
+    if (meet(at[i], flag)) return fail(MC_ERR_INVALID_ARG, "attention backward: status overlaps %s", ts[i].name);
+    if (!ts[i].out) continue;
+    if (meet(at[i], lse)) return fail(MC_ERR_INVALID_ARG, "attention backward: %s overlaps lse", ts[i].name);
+    for (int j = 0; j < nt; ++j) {
+      if (i == j || !meet(at[i], at[j])) continue;
+      if (!ts[j].out) return fail(MC_ERR_INVALID_ARG, "attention backward: %s overlaps %s", ts[i].name, ts[j].name);
+      if (at[i].lo == at[j].lo)
+        return fail(MC_ERR_INVALID_ARG, "attention backward: %s and %s are the same memory", ts[i].name, ts[j].name);
+      const int64_t apart = ((int64_t)at[j].lo - (int64_t)at[i].lo) / 2;
+      if (!interleave(ts[i].st, ts[i].n, ts[i].width, ts[j].st, ts[j].n, ts[j].width, ext, apart))
+        return fail(MC_ERR_INVALID_ARG, "attention backward: %s and %s share memory", ts[i].name, ts[j].name);
+    }
+  }
   if (workspace_bytes < w.bytes)
     return fail(MC_ERR_WORKSPACE, "attention backward: workspace of %zu bytes, %zu needed", workspace_bytes, w.bytes);
   p.q = a->q; p.k = a->k; p.ks = a->k_shared; p.v = g->v; p.o = g->o; p.d_o = g->d_o;

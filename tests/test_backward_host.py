@@ -99,6 +99,50 @@ def test_attention_backward_refuses(lib, dkw, gkw, code, needle):
     assert needle in lib.mc_last_error().decode()
 
 
+DQ, DK, DV, LSE, WSP = (FAKE + n * STEP for n in (5, 6, 7, 10, 20))
+KV = [16 * 2 * 128, 2 * 128, 128]          # [B, S, H, 64 + 64]
+BHSD = [2 * 16 * 64, 64, 16 * 64]          # heads outside the sequence
+
+
+@pytest.mark.parametrize("gkw,needle", [
+    (dict(dv=DK + 16), "dk and dv share"),                           # an overlap that does not begin together
+    (dict(dv=DK + 64, dk_strides=KV, dv_strides=KV), "dk and dv share"),
+    (dict(dv=DK + 128, dk_strides=KV, dv_strides=[16 * 2 * 128, 2 * 128, 64]), "dk and dv share"),
+    (dict(dv=DK + 128, dk_strides=KV, dv_strides=[16 * 2 * 128, 128, 16 * 128]), "dk and dv share"),
+    (dict(dv=DK + 256 - 32, dk_strides=KV, dv_strides=KV), "dk and dv share"),        # into the next head's dk
+    (dict(dk=LSE + 64), "dk overlaps lse"),
+    (dict(lse=WSP + 64), "lse, status and workspace"),
+    (dict(dv=WSP - 16), "workspace overlaps dv"),
+    (dict(v=WSP + 256), "workspace overlaps v"),
+    (dict(q_strides=[1 << 36, 1 << 36, 64], S=1 << 20), "too large"),
+])
+def test_attention_backward_refuses_shared_memory(lib, gkw, needle):
+    d = attn(**{k: gkw.pop(k) for k in ("q_strides", "S") if k in gkw})
+    assert call(lib, d, grad(**gkw)) in (INV, UNS)
+    assert needle in lib.mc_last_error().decode()
+
+
+@pytest.mark.parametrize("gkw", [
+    dict(dv=DK + 128, dk_strides=KV, dv_strides=KV),                                  # [B, S, H, dk | dv]
+    dict(dk=DV + 128, dk_strides=KV, dv_strides=KV),
+    dict(dv=DK + 2 * 64 * 2, dk_strides=[16 * 256, 256, 64], dv_strides=[16 * 256, 256, 64]),   # [B, S, 2, H, 64]
+    dict(dv=DK + 16 * 64 * 2, dk_strides=[4096, 64, 2048], dv_strides=[4096, 64, 2048]),        # [B, H, 2, S, 64]
+    dict(dv=DK + 2 * 2048 * 2, dk_strides=BHSD, dv_strides=BHSD),                     # one after the other
+])
+def test_attention_backward_takes_outputs_that_interleave(lib, gkw):
+    """These pass the checks of memory: the next refusal, of the workspace's size, is the one that is met."""
+    assert call(lib, attn(), grad(**gkw), nbytes=0) == WS
+
+
+@pytest.mark.parametrize("status,needle", [
+    (FAKE + 20 * STEP + 64, "lse, status and workspace"), (LSE + 8, "lse, status and workspace"),
+    (FAKE + 4 * STEP + 4, "status overlaps d_o"), (DQ + 4, "status overlaps dq"), (FAKE + 30 * STEP + 2, "4-byte")])
+def test_attention_backward_refuses_a_status_among_its_operands(lib, status, needle):
+    d, g = attn(), grad()
+    assert lib.qk_attention_backward(ctypes.byref(d), ctypes.byref(g), P(WSP), 1 << 40, P(status), None) == INV
+    assert needle in lib.mc_last_error().decode()
+
+
 def test_attention_backward_workspace(lib):
     n, d = ctypes.c_size_t(0), attn()
     assert lib.qk_attention_backward_workspace_size(ctypes.byref(d), ctypes.byref(n)) == abi.MC_OK
