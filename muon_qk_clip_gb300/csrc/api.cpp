@@ -1044,6 +1044,8 @@ mc_status qk_attention_backward_workspace_size(const mc_attn_desc* a, size_t* by
   mc_status st = check_attn_shape(a);
   if (st != MC_OK) return st;
   if (!bytes) return fail(MC_ERR_INVALID_ARG, "bytes: null");
+  const int64_t D = (int64_t)a->d_head + a->d_shared;
+  if (D < 16 || D > 192) return fail(MC_ERR_UNSUPPORTED, "attention backward: q.k length %lld outside [16, 192]", (long long)D);
   *bytes = plan_attn_bwd(a->B, a->S, a->H, a->d_shared).bytes;
   return ok();
 }

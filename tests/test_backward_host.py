@@ -158,6 +158,14 @@ def test_attention_backward_workspace(lib):
     assert lib.qk_attention_backward_workspace_size(ctypes.byref(d), None) == INV
 
 
+@pytest.mark.parametrize("kw", [dict(d_head=8), dict(d_head=200), dict(d_shared=192),
+                                dict(B=1 << 10, S=1 << 20, H=1 << 10, d_shared=(1 << 31) - 1)])   # would overflow
+def test_attention_backward_workspace_of_unsupported_widths(lib, kw):
+    n = ctypes.c_size_t(0)
+    assert lib.qk_attention_backward_workspace_size(ctypes.byref(attn(**kw)), ctypes.byref(n)) == UNS
+    assert n.value == 0 and "q.k length" in lib.mc_last_error().decode()
+
+
 def test_binding_refuses_host_tensors_and_shapes():
     x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
