@@ -8,6 +8,7 @@ here.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import struct
 from dataclasses import dataclass
@@ -205,18 +206,42 @@ def _device_of(first, name, *others):
     return index
 
 
-def _run(fn, name, index, stream, *args):
-    """fn(*args, stream) on device `index` (its current stream unless given)."""
+def _run(fn, name, index, *args):
+    """fn(*args, stream) on device `index` and its current stream."""
     if torch.cuda.current_device() != index:
         with torch.cuda.device(index):
-            return _run(fn, name, index, stream, *args)
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
-    code = fn(*args, stream)
+            return _run(fn, name, index, *args)
+    code = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if code:
         check(code, name)
+
+
+def _on_stream(fn):
+    """fn with a stream (torch's or a raw handle) that it runs under as the
+    current one: what it allocates then belongs to that stream, so memory that it
+    drops is not given to another stream's work while its own still runs."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        index = next((t.get_device() for t in (*args, *kw.values()) if isinstance(t, torch.Tensor)), -1)
+        if index < 0:                      # refused by fn
+            return fn(*args, **kw)
+        if not isinstance(stream, torch.cuda.Stream):
+            at = stream if isinstance(stream, int) else stream.cuda_stream
+            stream = torch.cuda.ExternalStream(at, device=index) if at else torch.cuda.default_stream(index)
+        elif stream.device.index != index:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{index}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _nbytes(workspace):
+    """Bytes of a workspace tensor, all of them in its storage."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
 
 
 def _at(t):
@@ -232,15 +257,17 @@ def attention_backward_workspace_size(q, k, k_shared=None) -> int:
     return n.value
 
 
+@_on_stream
 def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, scale=None, dq=None,
-                          dk=None, dv=None, dk_shared=None, workspace=None, status=None, stream=None):
+                          dk=None, dv=None, dk_shared=None, workspace=None, status=None, *, stream=None):
     """Gradients of qk_attention_forward's output: q [B,S,H,dq], k [B,S,H,dk],
     k_shared [B,S,dr] or None, v, out and dout [B,S,H,dv] (bf16, contiguous
     feature axes), lse [B,H,S] f32 as the forward returned it; causal and scale
     as in the forward.  Returns (dq, dk, dv, dk_shared or None); outputs are
     allocated unless given (any strides the features may have).  workspace: a
-    uint8 CUDA tensor of attention_backward_workspace_size bytes; without one,
-    one is allocated for the call."""
+    contiguous CUDA tensor of attention_backward_workspace_size bytes; without one,
+    one is allocated for the call.  stream: what is allocated here belongs to it;
+    other tensors used on it are the caller's to order and keep."""
     index = _device_of(q, "q", k, v, out, lse, dout, k_shared, dq, dk, dv, dk_shared, workspace, status)
     d = attn_desc(q, k, k_shared, causal, scale)
     B, S, H, _ = q.shape
@@ -271,12 +298,12 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
         check(lib.qk_attention_backward_workspace_size(d, n), "qk_attention_backward_workspace_size")
         workspace, nbytes = torch.empty(n.value, dtype=torch.uint8, device=q.device), n.value
     else:
-        nbytes = workspace.numel() * workspace.element_size()
+        nbytes = _nbytes(workspace)
     g = McAttnGrad.from_buffer_copy(_ATTN_GRAD.pack(
         v.data_ptr(), dvw, 0, *vs[:3], out.data_ptr(), *os[:3], lse.data_ptr(), dout.data_ptr(), *ds[:3],
         dq.data_ptr(), *dq.stride()[:3], dk.data_ptr(), *dk.stride()[:3], dks_at, *dks_strides,
         dv.data_ptr(), *dv.stride()[:3]))
-    _run(lib.qk_attention_backward, "qk_attention_backward", index, stream, d, g, workspace.data_ptr(), nbytes,
+    _run(lib.qk_attention_backward, "qk_attention_backward", index, d, g, workspace.data_ptr(), nbytes,
          _at(status))
     return dq, dk, dv, dk_shared
 
@@ -397,7 +424,8 @@ def rope_(x, theta: float = 10000.0, stream=None):
     return x
 
 
-def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
+@_on_stream
+def rope_backward(dy, theta: float = 10000.0, out=None, *, stream=None):
     """Gradient of rope_: the transposed rotation of dy [B, S, d] or
     [B, S, heads, d] (unit stride along d), positions 0..S-1.  Returns `out`, a
     new tensor unless given; out=dy rotates in place."""
@@ -412,7 +440,7 @@ def rope_backward(dy, theta: float = 10000.0, out=None, stream=None):
     if out.shape != shape or out.dtype != dy.dtype or x[-1] != 1:
         raise ValueError("out must have dy's shape and type and unit stride along d")
     nh, yh, xh = (shape[2], y[2], x[2]) if len(shape) == 4 else (1, 0, 0)
-    _run(abi.load().mc_rope_backward, "mc_rope_backward", index, stream, dy.data_ptr(), y[0], y[1], yh,
+    _run(abi.load().mc_rope_backward, "mc_rope_backward", index, dy.data_ptr(), y[0], y[1], yh,
          out.data_ptr(), x[0], x[1], xh, shape[0], shape[1], nh, shape[-1], dt, theta)
     return out
 
@@ -435,8 +463,9 @@ def _vector(t, name, n, dtype):
         raise ValueError(f"{name} must be a contiguous [{n}] tensor of {dtype}")
 
 
+@_on_stream
 def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=None, h=None, out=None,
-                 scales=None, rstd=None, stream=None):
+                 scales=None, rstd=None, *, stream=None):
     """h = x + residual (h = x without one), y = h / sqrt(mean(h^2) + eps) * weight
     per row of x [rows, cols] (bf16 or fp32; residual of the same shape, weight
     [cols], both of x's type).  out_dtype=torch.float8_e4m3fn stores y as e4m3
@@ -483,13 +512,14 @@ def add_rms_norm(x, residual=None, weight=None, eps: float = 1e-6, out_dtype=Non
         rstd = torch.empty(rows, dtype=torch.float32, device=dev)
     else:
         _vector(rstd, "rstd", rows, torch.float32)
-    _run(abi.load().mc_add_rms_norm, "mc_add_rms_norm", index, stream, x.data_ptr(), ldx, _at(residual), ldr,
+    _run(abi.load().mc_add_rms_norm, "mc_add_rms_norm", index, x.data_ptr(), ldx, _at(residual), ldr,
          _at(weight), _at(h), ldh, out.data_ptr(), ldy, _at(scales), lds, rstd.data_ptr(), rows, cols, dt,
          abi.MC_F8E4M3 if f8 else dt, eps)
     return out, scales, (x if residual is None else h), rstd
 
 
-def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None, workspace=None, stream=None):
+@_on_stream
+def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None, workspace=None, *, stream=None):
     """Gradient of y = h * rstd * weight given dy [rows, cols], h and rstd as
     add_rms_norm returned them: dx (of the norm's input and of the residual
     alike; plus dres, the gradient that reaches h past the norm) and dweight
@@ -519,8 +549,8 @@ def rms_norm_backward(dy, h, rstd, weight=None, dres=None, dx=None, dweight=None
         _vector(dweight, "dweight", cols, torch.float32)
         if workspace is None:
             workspace = torch.empty(rms_norm_backward_workspace_size(cols), dtype=torch.uint8, device=dy.device)
-        nbytes = workspace.numel() * workspace.element_size()
-    _run(abi.load().mc_rms_norm_backward, "mc_rms_norm_backward", index, stream, dy.data_ptr(), lddy, h.data_ptr(),
+        nbytes = _nbytes(workspace)
+    _run(abi.load().mc_rms_norm_backward, "mc_rms_norm_backward", index, dy.data_ptr(), lddy, h.data_ptr(),
          ldh, rstd.data_ptr(), _at(weight), _at(dres), ldr, dx.data_ptr(), lddx, _at(dweight), rows, cols, dt,
          _at(workspace), nbytes)
     return dx, dweight

@@ -263,3 +263,24 @@ def test_attention_backward_dense_block_full_size():
         sub = [t[s].cpu() for t in (q, k, v, do, out)]
         ref, tol = bounds(sub[0], sub[1], None, sub[2], sub[3], sub[4], lse[b:b + 1, h:h + 1].cpu(), True)
         check([x[s] for x in got[:3]] + [None], ref, tol)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_attention_backward_on_another_stream_keeps_its_memory(raw):
+    """The workspace that a call allocates for itself on a given stream is not
+    handed to the current stream's next allocations while the call still runs."""
+    q, k, ks, v, do, o, lse = inputs(2, 140, 2, 128, 32, 64, 99)
+    a, ksd = dev(q, k, v, o, lse, do), ks.cuda()
+    want = mc.qk_attention_backward(*a, k_shared=ksd)
+    n = mc.attention_backward_workspace_size(a[0], a[1], ksd)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)      # about 10 ms
+    got = mc.qk_attention_backward(*a, k_shared=ksd, stream=side.cuda_stream if raw else side)
+    taken = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    taken += [torch.full_like(g, float("nan")) for g in got]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    assert mc.qk_attention_backward(*a, k_shared=ksd, stream=0)[0].shape == q.shape

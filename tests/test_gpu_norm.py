@@ -281,3 +281,23 @@ def test_norm_and_rope_calls_in_a_cuda_graph_and_on_a_stream():
     calls(side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, (o["out"].view(torch.uint8), o["scales"], o["h"], dx, dw, rx)))
+
+
+def test_norm_gradient_on_another_stream_keeps_its_memory():
+    """As for the attention's gradient: the partial weight sums of a call on a
+    given stream are not handed out while it runs."""
+    dy, h = normal((96, 640), 0.01, "gd", BF16), normal((96, 640), 1.0, "gx", BF16)
+    w = (1 + normal((640,), 0.2, "gw", F32)).to(BF16)
+    rstd = mc.add_rms_norm(h)[3]
+    want = mc.rms_norm_backward(dy, h, rstd, weight=w)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)      # about 10 ms
+    got = mc.rms_norm_backward(dy, h, rstd, weight=w, stream=side)
+    taken = [torch.full((mc.rms_norm_backward_workspace_size(640) // 4,), float("nan"), device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert len(taken) == 4 and all(torch.equal(a, b) for a, b in zip(want, got))
+    with pytest.raises(ValueError, match="contiguous"):
+        mc.rms_norm_backward(dy, h, rstd, weight=w, workspace=torch.empty(1, device="cuda").expand(304 * 640))
