@@ -29,9 +29,10 @@ def _turned(t):
 
 
 def _pitched(t):
-    """t with rows of 16-byte pitch: t itself if it has them, or a copy."""
+    """t with rows of 16-byte pitch: t itself if it has them, or a copy (of
+    broadcast rows too)."""
     per = 16 // t.element_size()
-    if t.stride(1) == 1 and t.stride(0) % per == 0 and t.data_ptr() % 16 == 0:
+    if t.stride(1) == 1 and t.stride(0) % per == 0 and t.stride(0) >= t.shape[1] and t.data_ptr() % 16 == 0:
         return t
     out = t.new_empty((t.shape[0], (t.shape[1] + per - 1) // per * per))[:, :t.shape[1]]
     return out.copy_(t)
@@ -68,7 +69,7 @@ def project_mla_backward(X, W, H: int, dq, dk, dkr, dv=None, d_nope=128, d_rope=
     qk_attention_backward gives it) and dv [B,S,H,d_v] (None: zero) to
     ({name: dW}, dX) for W_DQ, W_UQ, W_DKV, W_UKV and W_KR.  The latents are
     recomputed from X.  No gradient is overwritten."""
-    _on_device(X, dq, dk, dkr, *W.values())
+    _on_device(X, dq, dk, dkr, *W.values(), *(() if dv is None else (dv,)))
     B, S, D = X.shape
     T = B * S
     x2 = X.reshape(T, D)

@@ -381,6 +381,8 @@ def _rows(t, name):
         raise ValueError(f"{name}: expected a 2-D tensor with unit column stride")
     if t.dtype not in _DT:
         raise ValueError(f"{name}: unsupported dtype {t.dtype}")
+    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name}: rows that share memory")
     return max(t.stride(0), t.shape[1])
 
 

@@ -335,3 +335,11 @@ def test_packed_descriptors_match_the_structures():
         x = getattr(g, name)
         flat += list(x) if hasattr(x, "__len__") else [x]
     assert flat == list(range(1, n + 1))
+
+
+def test_products_refuse_rows_that_share_memory():
+    """Broadcast rows would be read past their storage."""
+    x, w = torch.zeros(1, 8).expand(4, 8), torch.zeros(3, 8)
+    for call in (lambda: mc.matmul(x, w), lambda: mc.matmul(w, x), lambda: mc.rms_norm(x)):
+        with pytest.raises(ValueError, match="share memory"):
+            call()

@@ -84,6 +84,19 @@ def test_project_mha_backward(B, S, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+def test_project_backward_of_broadcast_tensors(dtype):
+    """Rows that share memory (one token's X, or one gradient for all tokens) are
+    read as the rows that they stand for."""
+    B, D, H, d = 5, 64, 2, 32
+    Wq, Wk = mk((H * d, D), 0.1, "wq", dtype), mk((H * d, D), 0.1, "wk", dtype)
+    X, dq, dk = (mk((1, 1, *s), 1.0, n, dtype).expand(B, 1, *s) for n, s in (("x", (D,)), ("gq", (H, d)), ("gk", (H, d))))
+    got = backward.project_mha_backward(X, Wq, Wk, dq, dk)
+    want = backward.project_mha_backward(X.contiguous(), Wq, Wk, dq.contiguous(), dk.contiguous())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("with_v", [True, False])
 def test_project_mla_backward(dtype, with_v):
     B, S, D, H, ql, kl, dn, dr, dv = 2, 75, 192, 3, 96, 64, 16, 8, 24
