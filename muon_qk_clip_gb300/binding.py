@@ -143,6 +143,8 @@ def attn_desc(q, k, k_shared=None, causal=True, scale=None) -> McAttnDesc:
         raise ValueError("q, k, k_shared must share a supported dtype")
     if scale is None:
         scale = 1.0 / math.sqrt(dq)
+    else:
+        scale = ctypes.c_float(scale).value           # beyond fp32: inf, which the library refuses
     at, ks = (0, (0, 0)) if k_shared is None else (k_shared.data_ptr(), k_shared.stride())
     return McAttnDesc.from_buffer_copy(_ATTN_DESC.pack(
         B, S, H, dk, dr, _DT[q.dtype], 1 if causal else 0, scale, q.data_ptr(), k.data_ptr(), at,
@@ -292,6 +294,8 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
         dks_at, dks_strides = dk_shared.data_ptr(), dk_shared.stride()[:2]
     elif dk_shared is not None:
         raise ValueError("dk_shared without k_shared")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
     lib = abi.load()
     if workspace is None:
         n = ctypes.c_size_t(0)

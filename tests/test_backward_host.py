@@ -343,3 +343,11 @@ def test_products_refuse_rows_that_share_memory():
     for call in (lambda: mc.matmul(x, w), lambda: mc.matmul(w, x), lambda: mc.rms_norm(x)):
         with pytest.raises(ValueError, match="share memory"):
             call()
+
+
+def test_descriptor_scale_beyond_fp32_is_left_to_the_library(lib):
+    x = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16)
+    d = mc.attn_desc(x, x, scale=1e300)
+    assert d.scale == float("inf")
+    d.q, d.k = FAKE, FAKE + STEP
+    assert call(lib, d, grad()) == INV and "scale" in lib.mc_last_error().decode()
