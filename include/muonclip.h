@@ -325,8 +325,8 @@ mc_status qk_attention_backward_workspace_size(const mc_attn_desc* attn, size_t*
  *   dk_j = scale sum_i ds_ij q_i.
  * Same shapes, types and limits as the forward (bf16; MC_ERR_UNSUPPORTED
  * otherwise).  p and ds are rounded to bf16 as operands, sums are fp32, each
- * gradient is rounded to bf16 once; no atomics, so equal inputs give equal
- * bits.  workspace: device, 256-byte aligned, for this call alone while it
+ * gradient is rounded to bf16 once; every sum runs in a fixed order, so equal
+ * inputs give equal bits.  workspace: device, 256-byte aligned, for this call alone while it
  * runs.  S_max is a maximum for the clip, not part of the loss: it has no
  * gradient.  A NaN/Inf gradient sets MC_STATUS_NONFINITE_UPDATE; NaN/Inf
  * inputs may reach every gradient of their (batch, head). */
@@ -360,7 +360,7 @@ mc_status muonclip_step(mc_mat* W, const mc_mat* G, mc_mat* M, int32_t count,
 /* Optional launch timing (observability).  While enabled, every kernel
  * launch of the library is bracketed by CUDA events recorded on the launch's
  * stream, accumulated per kernel class ("prep", "norms", "ns_gemm", "apply",
- * "clip", "max_logit").  mc_profiler_read synchronises on the recorded
+ * "clip", "max_logit", "attn_fwd", "attn_bwd").  mc_profiler_read synchronises on the recorded
  * events, writes up to `max` entries (class name, launches, total
  * milliseconds) and returns the number written; reset = 1 clears the totals.
  * Process-wide; not meant for use while several threads launch. */

@@ -51,9 +51,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 // has 512 columns: dK and dV take 64 (nch + ncv), S^T and dP^T one per query of
 // the tile, P^T (bf16 pairs) half of one.  Up to three chunks P^T has columns of
 // its own beside 128-query tiles; with more it is written over S^T: 128 queries
-// then still fit four chunks, 96 five.  (With P^T apart and 96 / 64 queries those
-// ran at 470 / 704 us for their pass on dense_block / k2_mla_layer: the smaller
-// the tile, the more often the tensor core re-reads K and V from shared memory.)
+// then still fit four chunks, 96 five.  (With P^T apart and 96 queries four chunks'
+// pass took 385 us on dense_block, against 358: the smaller the tile, the more
+// often the tensor core re-reads K and V from shared memory.)
 __host__ __device__ constexpr bool p_apart(int nch, int ncv) { return nch + ncv < 4; }
 __host__ __device__ constexpr int query_tile(int nch, int ncv) { return nch + ncv > 4 ? 96 : 128; }
 __host__ __device__ constexpr int query_stages(int nch, int ncv) { return p_apart(nch, ncv) ? 3 : 2; }
@@ -265,7 +265,8 @@ __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long 
 // in rows of `sp` values; rows past the sequence get nlse = -inf (p = 0) and
 // delta = 0.  A block takes 16 positions of 8 heads: 16 lanes per row with 8
 // features each, the results written through shared memory so that a warp stores
-// 16 positions of a head.
+// 16 positions of a head.  Bound by memory: 26.7 us for dense_block's 134 MB (5.0
+// TB/s).
 constexpr int kRowPos = 16, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
@@ -752,8 +753,9 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
 // Q and dO are the A operands of every product of an item but one, so they move
 // from shared memory to tensor memory once per item (tcgen05.cp, a 16-feature
 // k-step at a time) and only keys and values are read from shared memory for the
-// products: with Q and dO there too, S and dP took 85 clocks per instruction
-// instead of 64, and the pass 300 / 412 us on dense_block / k2_mla_layer.
+// products: with Q and dO there too, a product of 64 keys took 48 clocks instead of
+// 32, and the whole call 734 / 1030 us instead of 715 / 997 on dense_block /
+// k2_mla_layer (as both passes then were).
 //
 // dS has columns of its own, so S(t+1) starts as soon as S(t) has been read and
 // dP(t+1) as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1),
@@ -1071,7 +1073,18 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
 // ---------------------------------------------------------------- both passes
 // One persistent CTA per SM takes dK / dV items until there are none, then dQ
 // items: the second pass starts wherever the first one has run out, with no
-// launch in between, and a small batch runs both at once on different SMs.
+// launch in between, and a small batch runs both at once on different SMs.  (As
+// two launches: 623 us instead of 614 on dense_block, 45 instead of 39 on
+// [3, 1021, 5, 80 / 48].)
+//
+// Measured, whole call: 616 us for [4, 4096, 16, 128] causal (1115 TFLOP/s of the
+// formulas' five products, 1561 of the seven executed), 896 us for [1, 4096, 64,
+// 192 / 128] with a shared key, 1462 us for [1, 32768, 2, 192 / 128].  The tensor
+// pipe is active 72 % / 63 % of bwd_kernel on the first two: what bounds it is the
+// chain of a tile (product, barrier, S or dP from tensor memory, exponential,
+// P or dS back, barrier, product), which takes 2540 clocks per 128-query tile of
+// the dK / dV pass where the products alone need 2048, and 1400 per 96-key tile of
+// the dQ pass (products 1152).  DRAM moves 545 + 186 MB in 589 us (dense_block).
 constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
 
 template <int NCH, int NCV>
@@ -1124,7 +1137,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------- shared key
 // dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums
 // [b][h][c][j].  A block takes 32 positions of 8 features, eight heads' loads in
-// flight per thread, and turns its tile through shared memory.
+// flight per thread, and turns its tile through shared memory.  14.8 us for the 67
+// MB of k2_mla_layer, most of them still in L2.
 __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p, const int nj, const int nc) {
   __shared__ float tile[32][9];
   const int bi = blockIdx.x / nj, j0 = (blockIdx.x - bi * nj) * 32;

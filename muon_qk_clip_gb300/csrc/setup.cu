@@ -106,9 +106,9 @@ __global__ void rope_kernel(T* x, int B, int S, int nh, int d, long long sb, lon
 // fp32 sine and cosine are good to 2^-22 absolute at any angle up to 2^24 (two
 // fp32 hold 2^-48 of the turn per position; larger ones are refused) without fp64
 // arithmetic per position (this part runs it at a fraction of fp32's rate).  Bound
-// by memory and its latency; a table of sines per block in shared memory, as in
-// the forward, cost two barriers per few positions (18 us for [1, 4096, 64, 64]
-// bf16 against a floor of 10).
+// by memory and its latency: [1, 4096, 64, 64] bf16, 67 MB, takes 11.6 us (5.8
+// TB/s); a table of sines per block in shared memory, as in the forward, cost two
+// barriers per few positions (18 us).
 struct RopeBack {
   const void* dy; void* dx;
   long long yb, ys, yh, xb, xs, xh;
