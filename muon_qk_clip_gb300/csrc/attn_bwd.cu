@@ -207,57 +207,61 @@ __device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int*
   return true;
 }
 
-// W (16 or 32) columns of an accumulator, from tensor memory at `taddr` (a row
-// per lane), times `scale`, as bf16, to 32 rows of an output that are `pitch`
-// elements apart.  They turn through this warp's 64 W bytes of shared memory so
-// that its stores write whole sectors.  The first `rows` rows and `n` columns
-// exist.  True if one of this lane's row's values is not finite.
+// 32 columns of an accumulator, from tensor memory at `taddr` (a row per lane),
+// times `scale`, as bf16, to this lane's row of an output at `dst`.  The row
+// exists if `row`, and `n` of its columns.  Rows on 32-byte boundaries (`wide`) are
+// stored a whole sector per lane and instruction.  True if a value of the row is
+// not finite.
 //
-// The epilogue calls this in loops that stay rolled: its code runs once per work
-// item between tiles of other code, and unrolled (a copy per 16 or 32 columns) it
-// took 2200-4700 clocks per 128 columns, most of them fetching instructions.
-template <int W>
-__device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, long long pitch, uint8_t* buf, float scale, int rows,
-                                  int n) {
-  constexpr int NU = W / 8;              // 16-byte units per row
-  const int lane = threadIdx.x & 31;
-  auto at = [&](int row, int u) { return reinterpret_cast<uint4*>(buf + row * W * 2 + ((u ^ (NU == 4 ? (row >> 1) & 3 : (row >> 2) & 1)) << 4)); };
-  uint32_t r[W / 16][16];
+// The next item's products wait for the accumulators, so they leave tensor memory
+// by the shortest way.  (Turned through shared memory, so that neighbouring lanes
+// write neighbouring addresses, 32 columns took 900 clocks, most of them waiting
+// for shared memory behind the tensor core's operand reads.)  The epilogue calls
+// this in loops that stay rolled: its code runs once per work item between tiles
+// of other code, and unrolled it spent most of its time fetching instructions.
+__device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, float scale, bool row, bool wide, int n) {
+  uint32_t r[2][16];
 #pragma unroll
-  for (int c = 0; c < W / 16; ++c) tmem_ld_32x32b_x16_async(taddr + c * 16, r[c]);
+  for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x16_async(taddr + c * 16, r[c]);
   tmem_ld_wait();
 #pragma unroll
-  for (int c = 0; c < W / 16; ++c) reg_fence16(r[c]);
+  for (int c = 0; c < 2; ++c) reg_fence16(r[c]);
   float z = 0.f;                         // 0, or NaN once a value is not finite
+  uint32_t w[16];
 #pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    float v[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      v[x] = __uint_as_float(r[u / 2][8 * (u % 2) + x]) * scale;
-      z = fmaf(v[x], 0.f, z);
-    }
-    *at(lane, u) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+  for (int x = 0; x < 16; ++x) {
+    const float v0 = __uint_as_float(r[x / 8][2 * (x % 8)]) * scale, v1 = __uint_as_float(r[x / 8][2 * (x % 8) + 1]) * scale;
+    z = fmaf(v0, 0.f, fmaf(v1, 0.f, z));
+    w[x] = pack_bf16(v0, v1);
   }
-  __syncwarp();
+  if (row) {
+    if (wide && n >= 32) {
 #pragma unroll
-  for (int x = 0; x < NU; ++x) {
-    const int row = (x * 32 + lane) / NU, u = lane % NU;
-    const uint4 w = *at(row, u);
-    if (row < rows && 8 * u < n) {
-      __nv_bfloat16* to = dst + row * pitch + 8 * u;
-      if (8 * u + 8 <= n) {
-        *reinterpret_cast<uint4*>(to) = w;
-      } else {
-        const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+      for (int u = 0; u < 2; ++u)
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * u), "r"(w[8 * u]), "r"(w[8 * u + 1]),
+                     "r"(w[8 * u + 2]), "r"(w[8 * u + 3]), "r"(w[8 * u + 4]), "r"(w[8 * u + 5]), "r"(w[8 * u + 6]),
+                     "r"(w[8 * u + 7])
+                     : "memory");
+    } else {
 #pragma unroll
-        for (int y = 0; y < 7; ++y)
-          if (8 * u + y < n) to[y] = __ushort_as_bfloat16((unsigned short)(e[y / 2] >> (16 * (y % 2))));
+      for (int u = 0; u < 4; ++u) {
+        if (8 * u + 8 <= n) {
+          *reinterpret_cast<uint4*>(dst + 8 * u) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+        } else {
+#pragma unroll
+          for (int y = 0; y < 7; ++y)
+            if (8 * u + y < n) dst[8 * u + y] = __ushort_as_bfloat16((unsigned short)(w[4 * u + y / 2] >> (16 * (y % 2))));
+        }
       }
     }
   }
   __syncwarp();
-  return z != z && lane < rows;
+  return z != z && row;
+}
+// Whether every row of an output begins on a 32-byte boundary (its blocks of 32
+// columns then do too).
+__device__ inline bool rows_wide(const void* base, const long long* st) {
+  return ((reinterpret_cast<uintptr_t>(base) >> 1 | (uintptr_t)st[0] | (uintptr_t)st[1] | (uintptr_t)st[2]) & 15) == 0;
 }
 
 // ------------------------------------------------------------------- rows
@@ -361,7 +365,6 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
   uint8_t* qbuf = vbuf + NCV * CH;                         // stages x NCH chunks of a query tile
   uint8_t* dobuf = qbuf + kStages * NCH * CQ;              // stages x NCV chunks
   float* rowv = reinterpret_cast<float*>(dobuf + kStages * NCV * CQ);   // [stage][nlse, -delta][NQ]
-  uint8_t* stage = reinterpret_cast<uint8_t*>(rowv + kStages * 2 * NQ);   // [4 warps][2 KB]
   uint64_t* kv_full = bars + 0;
   uint64_t* kv_empty = bars + 1;
   uint64_t* q_full = bars + 2;      // [stages <= 3] Q tile with its nlse and delta
@@ -558,16 +561,17 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
     // item.
     const int q = warp & 3;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    uint8_t* mine = stage + q * 2048;
+    const bool wide_v = rows_wide(p.dv, p.dvs), wide_k = rows_wide(p.dk, p.dks);
     uint32_t li = 0;
     bool bad = false, ok = true;
     for (;; ++li) {
       int x, b, h, blk;
       if (!(ok = ring_get(ring, li, x, &abort_flag)) || x >= g.items) break;
       item_at(p, g, x, false, b, h, blk);
-      const int key0 = blk * BM + q * 32, rows = p.S - key0;
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key0 * p.dvs[1] + h * p.dvs[2];
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key0 * p.dks[1] + h * p.dks[2];
+      const int key = blk * BM + q * 32 + lane;
+      const bool row = key < p.S;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key * p.dvs[1] + h * p.dvs[2];
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key * p.dks[1] + h * p.dks[2];
 #pragma unroll 1
       for (int c = 0; c < 2 * (NCV + NCH); ++c) {
         const bool is_v = c < 2 * NCV;
@@ -581,10 +585,10 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
         if (is_v || col < 64 * g.nck) {
           const int n = (is_v ? p.d_v : p.d_head) - col;
           if (n > 0)
-            bad |= store_rows<32>(from, (is_v ? dv : dk) + col, is_v ? p.dvs[1] : p.dks[1], mine, is_v ? 1.f : p.scale, rows, n);
+            bad |= store_rows(from, (is_v ? dv : dk) + col, is_v ? 1.f : p.scale, row, is_v ? wide_v : wide_k, n);
         } else {                           // [b][h][feature][position]: 32 keys are 128 bytes
           const int f0 = col - p.d_head;
-          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key0 + lane;
+          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key;
 #pragma unroll 1
           for (int y = 0; y < 32; y += 16) {
             uint32_t r[16];
@@ -596,9 +600,9 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
             for (int x = 0; x < 16; ++x) {
               const float v = __uint_as_float(r[x]) * p.scale;
               z = fmaf(v, 0.f, z);
-              if (lane < rows && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
+              if (row && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
             }
-            bad |= z != z && lane < rows;
+            bad |= z != z && row;
             __syncwarp();
           }
         }
@@ -771,7 +775,6 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
   uint8_t* vbuf = kbuf + kStages * NCH * CK;           // 3 x NCV chunks
-  uint8_t* stage = vbuf + kStages * NCV * CK;                     // [4 warps][2 KB]
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
@@ -951,7 +954,7 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     // warps are at the next item
     const int q = warp & 3, D = p.d_head + p.d_shared;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    uint8_t* mine = stage + q * 2048;
+    const bool wide = rows_wide(p.dq, p.dqs);
     bool bad = false, ok = true;
     for (uint32_t li = 0;; ++li) {
       int x, b, h, blk;
@@ -959,11 +962,11 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
       item_at(p, g, x, true, b, h, blk);
       if (!(ok = warp_wait(acc_full, li & 1, &abort_flag))) break;
       tc_fence_after();
-      const int q0 = blk * BM + q * 32;
-      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + q0 * p.dqs[1] + h * p.dqs[2];
+      const int i = blk * BM + q * 32 + lane;
+      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
 #pragma unroll 1
       for (int col = 0; col < D; col += 32)
-        bad |= store_rows<32>(t_dq + lanes + col, dq + col, p.dqs[1], mine, p.scale, p.S - q0, D - col);
+        bad |= store_rows(t_dq + lanes + col, dq + col, p.scale, i < p.S, wide, D - col);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
@@ -1090,8 +1093,8 @@ constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
 template <int NCH, int NCV>
 constexpr size_t smem_bytes() {
   const size_t nq = query_tile(NCH, NCV), nk = key_tile(NCH, NCV), own = (size_t)(NCH + NCV);
-  const size_t kv = own * CH + query_stages(NCH, NCV) * (own * nq * 128 + 2 * nq * 4) + 4 * 2048;
-  const size_t q = own * CH + kKeyStages * own * nk * 128 + 4 * 2048;
+  const size_t kv = own * CH + query_stages(NCH, NCV) * (own * nq * 128 + 2 * nq * 4);
+  const size_t q = own * CH + kKeyStages * own * nk * 128;
   return 1024 + 2 * kBarBytes + (kv > q ? kv : q);      // 1024: alignment
 }
 
