@@ -962,7 +962,7 @@ AttnBwdPlan plan_attn_bwd(int64_t B, int64_t S, int64_t H, int64_t d_shared) {
   w.nlse = 0;
   w.delta = rows;
   w.part = 2 * rows;
-  w.counter = w.part + (size_t)round_up(B * H * S * d_shared * 4, 256);
+  w.counter = w.part + (size_t)round_up(B * H * S * part_pitch((int)d_shared) * 4, 256);
   w.bytes = w.counter + 256;
   return w;
 }

@@ -207,6 +207,21 @@ __device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int*
   return true;
 }
 
+// 32 columns of 32 lanes, waited for.
+__device__ inline void load_32(uint32_t taddr, uint32_t (&r)[2][16]) {
+#pragma unroll
+  for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x16_async(taddr + c * 16, r[c]);
+  tmem_ld_wait();
+#pragma unroll
+  for (int c = 0; c < 2; ++c) reg_fence16(r[c]);
+}
+// One 32-byte sector (aligned)
+__device__ inline void store_32b(void* to, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 32 columns of an accumulator, from tensor memory at `taddr` (a row per lane),
 // times `scale`, as bf16, to this lane's row of an output at `dst`.  The row
 // exists if `row`, and `n` of its columns.  Rows on 32-byte boundaries (`wide`) are
@@ -220,28 +235,23 @@ __device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int*
 // this in loops that stay rolled: its code runs once per work item between tiles
 // of other code, and unrolled it spent most of its time fetching instructions.
 __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, float scale, bool row, bool wide, int n) {
-  uint32_t r[2][16];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) tmem_ld_32x32b_x16_async(taddr + c * 16, r[c]);
-  tmem_ld_wait();
-#pragma unroll
-  for (int c = 0; c < 2; ++c) reg_fence16(r[c]);
-  float z = 0.f;                         // 0, or NaN once a value is not finite
-  uint32_t w[16];
+  uint32_t r[2][16], w[16];
+  load_32(taddr, r);
+  const unsigned long long s2 = two(scale, scale);
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 z = zero;               // zeros, or NaN once a value is not finite
 #pragma unroll
   for (int x = 0; x < 16; ++x) {
-    const float v0 = __uint_as_float(r[x / 8][2 * (x % 8)]) * scale, v1 = __uint_as_float(r[x / 8][2 * (x % 8) + 1]) * scale;
-    z = fmaf(v0, 0.f, fmaf(v1, 0.f, z));
-    w[x] = pack_bf16(v0, v1);
+    float v0, v1;
+    untwo(mul2(two(__uint_as_float(r[x / 8][2 * (x % 8)]), __uint_as_float(r[x / 8][2 * (x % 8) + 1])), s2), v0, v1);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(v0, v1);
+    z = __hfma2(v, zero, z);
+    w[x] = *reinterpret_cast<const uint32_t*>(&v);
   }
   if (row) {
     if (wide && n >= 32) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
-        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 16 * u), "r"(w[8 * u]), "r"(w[8 * u + 1]),
-                     "r"(w[8 * u + 2]), "r"(w[8 * u + 3]), "r"(w[8 * u + 4]), "r"(w[8 * u + 5]), "r"(w[8 * u + 6]),
-                     "r"(w[8 * u + 7])
-                     : "memory");
+      for (int u = 0; u < 2; ++u) store_32b(dst + 16 * u, w + 8 * u);
     } else {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -256,7 +266,31 @@ __device__ inline bool store_rows(uint32_t taddr, __nv_bfloat16* dst, float scal
     }
   }
   __syncwarp();
-  return z != z && row;
+  return row && (__low2float(z) != 0.f || __high2float(z) != 0.f);   // NaN differs from 0
+}
+// The same in fp32, to this lane's row of the shared key's partial sums; `n`, a
+// multiple of 8, of its columns exist.
+__device__ inline bool store_part(uint32_t taddr, float* dst, float scale, bool row, int n) {
+  uint32_t r[2][16], w[32];
+  load_32(taddr, r);
+  const unsigned long long s2 = two(scale, scale);
+  unsigned long long z = 0;
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const unsigned long long v = mul2(two(__uint_as_float(r[x / 8][2 * (x % 8)]), __uint_as_float(r[x / 8][2 * (x % 8) + 1])), s2);
+    z = fma2(v, 0, z);
+    float v0, v1;
+    untwo(v, v0, v1);
+    w[2 * x] = __float_as_uint(v0);
+    w[2 * x + 1] = __float_as_uint(v1);
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (row && 8 * u < n) store_32b(dst + 8 * u, w + 8 * u);
+  __syncwarp();
+  float z0, z1;
+  untwo(z, z0, z1);
+  return row && (z0 != 0.f || z1 != 0.f);
 }
 // Whether every row of an output begins on a 32-byte boundary (its blocks of 32
 // columns then do too).
@@ -586,25 +620,10 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
           const int n = (is_v ? p.d_v : p.d_head) - col;
           if (n > 0)
             bad |= store_rows(from, (is_v ? dv : dk) + col, is_v ? 1.f : p.scale, row, is_v ? wide_v : wide_k, n);
-        } else {                           // [b][h][feature][position]: 32 keys are 128 bytes
-          const int f0 = col - p.d_head;
-          float* part = p.part + (((long long)b * p.H + h) * p.d_shared + f0) * p.S + key;
-#pragma unroll 1
-          for (int y = 0; y < 32; y += 16) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16_async(from + y, r);
-            tmem_ld_wait();
-            reg_fence16(r);
-            float z = 0.f;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float v = __uint_as_float(r[x]) * p.scale;
-              z = fmaf(v, 0.f, z);
-              if (row && f0 + y + x < p.d_shared) part[(long long)(y + x) * p.S] = v;
-            }
-            bad |= z != z && row;
-            __syncwarp();
-          }
+        } else {
+          const int f0 = col - p.d_head, n = part_pitch(p.d_shared) - f0;
+          if (n > 0)
+            bad |= store_part(from, p.part + (((long long)b * p.H + h) * p.S + key) * part_pitch(p.d_shared) + f0, p.scale, row, n);
         }
         if (c == 2 * NCV - 1 || c == 2 * (NCV + NCH) - 1) {
           tc_fence_before();
@@ -1139,34 +1158,32 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------- shared key
 // dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums
-// [b][h][c][j].  A block takes 32 positions of 8 features, eight heads' loads in
-// flight per thread, and turns its tile through shared memory.  14.8 us for the 67
-// MB of k2_mla_layer, most of them still in L2.
-__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p, const int nj, const int nc) {
-  __shared__ float tile[32][9];
-  const int bi = blockIdx.x / nj, j0 = (blockIdx.x - bi * nj) * 32;
-  const int b = bi / nc, c0 = (bi - b * nc) * 8;
-  const int lane = threadIdx.x & 31, c = c0 + threadIdx.x / 32, j = j0 + lane;
-  const long long per = (long long)p.d_shared * p.S;
-  float s = 0.f;
-  if (c < p.d_shared && j < p.S) {
-    const float* src = p.part + (long long)b * p.H * per + (long long)c * p.S + j;
-    int h = 0;
-    for (; h + 8 <= p.H; h += 8) {
-      float v[8];
+// [b][h][j][c] (rows of part_pitch values).  A thread takes four features of a
+// position, eight heads' loads in flight.
+__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p, const int blocks) {
+  const int quads = part_pitch(p.d_shared) / 4, b = blockIdx.x / blocks;
+  const long long per = (long long)p.S * quads, e = (long long)(blockIdx.x - b * blocks) * 256 + threadIdx.x;
+  if (e >= per) return;
+  const float4* src = reinterpret_cast<const float4*>(p.part) + (long long)b * p.H * per + e;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v) { s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w; };
+  int h = 0;
+  for (; h + 8 <= p.H; h += 8) {
+    float4 v[8];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) v[y] = src[(h + y) * per];
+    for (int y = 0; y < 8; ++y) v[y] = src[(h + y) * per];
 #pragma unroll
-      for (int y = 0; y < 8; ++y) s += v[y];
-    }
-    for (; h < p.H; ++h) s += src[h * per];
+    for (int y = 0; y < 8; ++y) add(v[y]);
   }
-  tile[lane][threadIdx.x / 32] = s;
-  __syncthreads();
-  const int jj = j0 + threadIdx.x / 8, cc = c0 + threadIdx.x % 8;
-  if (jj < p.S && cc < p.d_shared)
-    static_cast<__nv_bfloat16*>(p.dksh)[b * p.dkshs[0] + jj * p.dkshs[1] + cc] =
-        __float2bfloat16_rn(tile[threadIdx.x / 8][threadIdx.x % 8]);
+  for (; h < p.H; ++h) add(src[h * per]);
+  const int j = (int)(e / quads), c = 4 * (int)(e - (long long)j * quads);
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.dksh) + b * p.dkshs[0] + j * p.dkshs[1] + c;
+  if (c + 4 <= p.d_shared) {
+    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+  } else {
+    const float v[3] = {s.x, s.y, s.z};
+    for (int y = 0; c + y < p.d_shared; ++y) to[y] = __float2bfloat16_rn(v[y]);
+  }
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
@@ -1286,9 +1303,9 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
                                          {launch_passes<3, 1>, launch_passes<3, 2>}};
   e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
   if (e != cudaSuccess || p.d_shared == 0) return e;
-  const long long nj = cdiv(p.S, 32), nc = cdiv(p.d_shared, 8);
-  if (nj * nc * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-  shared_kernel<<<(unsigned)(nj * nc * p.B), 256, 0, s>>>(p, (int)nj, (int)nc);
+  const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), 256);
+  if (blocks * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
+  shared_kernel<<<(unsigned)(blocks * p.B), 256, 0, s>>>(p, (int)blocks);
   return cudaGetLastError();
 }
 

@@ -252,6 +252,9 @@ struct AttnFwdParams {
 cudaError_t launch_attn_fwd(const AttnFwdParams& p, cudaStream_t s, char* err, size_t errlen);
 bool attn_fwd_supported(const AttnFwdParams& p, char* err, size_t errlen);
 
+// Row length of the shared key's partial sums: whole 32-byte sectors.
+__host__ __device__ inline constexpr int part_pitch(int d_shared) { return (d_shared + 7) / 8 * 8; }
+
 // Attention backward (bf16, tensor cores), recomputing the probabilities.
 struct AttnBwdParams {
   int B, S, H, d_head, d_shared, d_v;
@@ -264,7 +267,7 @@ struct AttnBwdParams {
   long long dqs[3], dks[3], dkshs[2], dvs[3];
   float* nlse;             // workspace [B, H, sp]: -lse log2(e), -inf past the sequence
   float* ndelta;           // workspace [B, H, sp]: -do . o
-  float* part;             // workspace [B, H, d_shared, S]: per-head gradients of the shared key
+  float* part;             // workspace [B, H, S, part_pitch(d_shared)]: per-head gradients of the shared key
   int* counter;            // workspace [2]: the next work item of the two passes
   int32_t* status;
 };
