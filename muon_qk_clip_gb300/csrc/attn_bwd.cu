@@ -1099,14 +1099,15 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
 // two launches: 623 us instead of 614 on dense_block, 45 instead of 39 on
 // [3, 1021, 5, 80 / 48].)
 //
-// Measured, whole call: 616 us for [4, 4096, 16, 128] causal (1115 TFLOP/s of the
-// formulas' five products, 1561 of the seven executed), 896 us for [1, 4096, 64,
-// 192 / 128] with a shared key, 1462 us for [1, 32768, 2, 192 / 128].  The tensor
-// pipe is active 72 % / 63 % of bwd_kernel on the first two: what bounds it is the
+// Measured, whole call: 598 us for [4, 4096, 16, 128] causal (1150 TFLOP/s of the
+// formulas' five products, 1610 of the seven executed), 838 us for [1, 4096, 64,
+// 192 / 128] with a shared key, 1425 us for [1, 32768, 2, 192 / 128].  The tensor
+// pipe is active 76 % / 69 % of bwd_kernel on the first two: what bounds it is the
 // chain of a tile (product, barrier, S or dP from tensor memory, exponential,
 // P or dS back, barrier, product), which takes 2540 clocks per 128-query tile of
 // the dK / dV pass where the products alone need 2048, and 1400 per 96-key tile of
-// the dQ pass (products 1152).  DRAM moves 545 + 186 MB in 589 us (dense_block).
+// the dQ pass (products 1152), and at the change of items about 2900 clocks more.
+// DRAM moves 545 + 184 MB in 568 us (dense_block).
 constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
 
 template <int NCH, int NCV>
@@ -1159,10 +1160,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ------------------------------------------------------------- shared key
 // dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums
 // [b][h][j][c] (rows of part_pitch values).  A thread takes four features of a
-// position, eight heads' loads in flight.
-__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ AttnBwdParams p, const int blocks) {
+// position, eight heads' loads in flight.  15.2 us for the 67 MB of k2_mla_layer
+// (16.4 in blocks of 256 threads, one or two per SM).
+constexpr int kSharedThreads = 64;
+__global__ void __launch_bounds__(kSharedThreads) shared_kernel(const __grid_constant__ AttnBwdParams p, const int blocks) {
   const int quads = part_pitch(p.d_shared) / 4, b = blockIdx.x / blocks;
-  const long long per = (long long)p.S * quads, e = (long long)(blockIdx.x - b * blocks) * 256 + threadIdx.x;
+  const long long per = (long long)p.S * quads, e = (long long)(blockIdx.x - b * blocks) * kSharedThreads + threadIdx.x;
   if (e >= per) return;
   const float4* src = reinterpret_cast<const float4*>(p.part) + (long long)b * p.H * per + e;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1303,9 +1306,9 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
                                          {launch_passes<3, 1>, launch_passes<3, 2>}};
   e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
   if (e != cudaSuccess || p.d_shared == 0) return e;
-  const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), 256);
+  const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), kSharedThreads);
   if (blocks * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-  shared_kernel<<<(unsigned)(blocks * p.B), 256, 0, s>>>(p, (int)blocks);
+  shared_kernel<<<(unsigned)(blocks * p.B), kSharedThreads, 0, s>>>(p, (int)blocks);
   return cudaGetLastError();
 }
 
