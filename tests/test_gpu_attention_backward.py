@@ -160,6 +160,40 @@ def test_attention_backward_strided_outputs_and_inputs():
     assert torch.all(dkv[:, S:] == 7.0) and torch.all(dkv[..., dh + dv:] == 7.0) and torch.all(dq[:, S:] == 7.0)
 
 
+@pytest.mark.parametrize("B,S,H,dh,dr,dv,off", [(2, 131, 3, 20, 0, 50, 0), (1, 150, 2, 64, 12, 33, 0), (1, 140, 3, 128, 61, 127, 8),
+                                                (2, 33, 2, 191, 0, 17, 8), (1, 1, 1, 64, 1, 16, 8)])
+def test_attention_backward_odd_widths(B, S, H, dh, dr, dv, off):
+    """Widths that are no multiple of eight, in rows padded to one, on 16-byte
+    addresses that are and are not 32-byte ones: what lies between the rows is
+    neither read (it is NaN in the inputs) nor written."""
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, dv, 101)
+    ref, tol = bounds(q, k, ks, v, do, o, lse, True)
+
+    def padded(shape, fill):
+        w = (shape[-1] + 7) // 8 * 8 + off
+        return torch.full((*shape[:-1], w + off), fill, dtype=BF16, device="cuda")
+
+    def within(t):
+        if t is None:
+            return None
+        big = padded(t.shape, float("nan"))
+        big[..., off:off + t.shape[-1]] = t.cuda()
+        return big[..., off:off + t.shape[-1]]
+
+    bigs = [None if t is None else padded(t.shape, 7.0) for t in (q, k, v, ks)]
+    outs = [None if b is None else b[..., off:off + t.shape[-1]] for b, t in zip(bigs, (q, k, v, ks))]
+    a = [within(t) for t in (q, k, v, o)]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_backward(*a, lse.cuda(), within(do), k_shared=within(ks), dq=outs[0], dk=outs[1], dv=outs[2],
+                                   dk_shared=outs[3], status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(got, ref, tol)
+    for big, t in zip(bigs, (q, k, v, ks)):
+        if big is not None:
+            assert torch.all(big[..., :off] == 7.0) and torch.all(big[..., off + t.shape[-1]:] == 7.0)
+
+
 def test_attention_backward_of_broadcast_keys():
     """One key/value head for every query head (stride 0): the gradients come per
     query head, for the caller to sum."""
