@@ -1130,7 +1130,7 @@ mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, vo
   p.counter = reinterpret_cast<int*>(base + w.counter);
   cudaError_t e;
   {
-    ProfScope ps(kAttnBwd, a->d_shared > 0 ? 3 : 2, (cudaStream_t)stream);
+    ProfScope ps(kAttnBwd, (a->S <= kAttnBwdShort ? 1 : 2) + (a->d_shared > 0 ? 1 : 0), (cudaStream_t)stream);
     e = launch_attn_bwd(p, (cudaStream_t)stream, err, sizeof err);
   }
   if (e != cudaSuccess) {

@@ -1157,6 +1157,178 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// -------------------------------------------------------- short sequences
+// Sequences of at most kAttnBwdShort positions: one block per (b, h) with q, k, v, do and
+// o in shared memory as fp32 and fp32 arithmetic throughout (P and dS are not
+// rounded).  A warp takes four queries, a lane a key of two of them, for P and dS;
+// then a warp takes four rows of an output, a lane four of its columns.  The difference
+// do . v - do . o is summed as do . (v - o), which is exact where a row has one key
+// and o is its value: dq and dk of one-position sequences are exactly 0.
+constexpr int kShortPitch = 20;          // of P and dS: rows of 16-byte alignment
+// Row pitch of `width` columns: whole 16 bytes, an odd number of them, so that 8
+// lanes that read 16 bytes of 8 rows meet no bank twice.
+__host__ __device__ inline int short_pitch(int width) { return 4 * (((width + 3) / 4) | 1); }
+
+// S rows of `width` bf16 columns to fp32 rows of `pitch`, zeros up to a multiple
+// of four columns.
+__device__ inline void short_load(float* to, int pitch, const __nv_bfloat16* from, long long stride, int S, int width) {
+  const int n = (width + 7) / 8, cols = (width + 3) / 4 * 4;
+  for (int x = threadIdx.x; x < S * n; x += blockDim.x) {
+    const int r = x / n, c = 8 * (x - r * n);
+    const __nv_bfloat16* src = from + r * stride + c;
+    float* dst = to + r * pitch + c;
+    if (c + 8 <= width) {
+      const uint4 w = *reinterpret_cast<const uint4*>(src);
+      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+        *reinterpret_cast<float4*>(dst + 4 * y) =
+            make_float4(__uint_as_float(e[2 * y] << 16), __uint_as_float(e[2 * y] & 0xffff0000u),
+                        __uint_as_float(e[2 * y + 1] << 16), __uint_as_float(e[2 * y + 1] & 0xffff0000u));
+    } else {
+      for (int y = 0; c + y < cols; ++y) dst[y] = c + y < width ? __bfloat162float(src[y]) : 0.f;
+    }
+  }
+}
+// a += x b for four columns
+__device__ inline void short_add(float4& a, float x, const float4& b) {
+  a.x = fmaf(x, b.x, a.x);
+  a.y = fmaf(x, b.y, a.y);
+  a.z = fmaf(x, b.z, a.z);
+  a.w = fmaf(x, b.w, a.w);
+}
+// Columns c .. c + 3 of a row of `width`, times `scale`, as bf16; true if one is
+// not finite.
+__device__ inline bool short_store(__nv_bfloat16* row, int c, int width, const float4& v, float scale) {
+  const float e[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
+  float z = 0.f;
+  if (c + 4 <= width) {
+    *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]));
+  } else {
+#pragma unroll
+    for (int y = 0; y < 3; ++y)
+      if (c + y < width) row[c + y] = __float2bfloat16_rn(e[y]);
+  }
+#pragma unroll
+  for (int y = 0; y < 4; ++y)
+    if (c + y < width) z = fmaf(e[y], 0.f, z);
+  return z != z;
+}
+
+__global__ void __launch_bounds__(128, 4) short_kernel(const __grid_constant__ AttnBwdParams p) {
+  extern __shared__ float4 short_smem[];
+  const int S = p.S, D = p.d_head + p.d_shared, pd = short_pitch(D), pv = short_pitch(p.d_v);
+  float* q = reinterpret_cast<float*>(short_smem);
+  float *k = q + S * pd, *v = k + S * pd, *dO = v + S * pv, *o = dO + S * pv, *P = o + S * pv, *dS = P + S * kShortPitch;
+  const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto at = [&](const void* base, const long long* st) {
+    return static_cast<const __nv_bfloat16*>(base) + b * st[0] + h * st[2];
+  };
+  short_load(q, pd, at(p.q, p.qs), p.qs[1], S, D);
+  short_load(k, pd, at(p.k, p.kst), p.kst[1], S, p.d_head);
+  if (p.d_shared)
+    short_load(k + p.d_head, pd, static_cast<const __nv_bfloat16*>(p.ks) + b * p.kss[0], p.kss[1], S, p.d_shared);
+  short_load(v, pv, at(p.v, p.vs), p.vs[1], S, p.d_v);
+  short_load(dO, pv, at(p.d_o, p.dos), p.dos[1], S, p.d_v);
+  short_load(o, pv, at(p.o, p.os), p.os[1], S, p.d_v);
+  __syncthreads();
+  const int r0 = 4 * warp;               // this warp's four queries, then its four rows of each output
+  int row[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) row[r] = min(r0 + r, S - 1);
+  {
+    static_assert(kAttnBwdShort <= 16, "a half-warp holds the keys");
+    const int j = lane & 15, key = min(j, S - 1), i0 = r0 + 2 * (lane >> 4);
+    const int query[2] = {min(i0, S - 1), min(i0 + 1, S - 1)};
+    float s[2] = {}, x[2] = {};
+#pragma unroll 4
+    for (int c = 0; c < D; c += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(k + key * pd + c);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float4 e = *reinterpret_cast<const float4*>(q + query[r] * pd + c);
+        s[r] = fmaf(e.x, a.x, fmaf(e.y, a.y, fmaf(e.z, a.z, fmaf(e.w, a.w, s[r]))));
+      }
+    }
+#pragma unroll 4
+    for (int c = 0; c < p.d_v; c += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(v + key * pv + c);
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const float4 e = *reinterpret_cast<const float4*>(dO + query[r] * pv + c);
+        const float4 m = *reinterpret_cast<const float4*>(o + query[r] * pv + c);
+        x[r] = fmaf(e.x, a.x - m.x, fmaf(e.y, a.y - m.y, fmaf(e.z, a.z - m.z, fmaf(e.w, a.w - m.w, x[r]))));
+      }
+    }
+    const float* lse = p.lse + (long long)blockIdx.x * S;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = i0 + r;
+      if (i >= S) continue;
+      const bool seen = j < S && (!p.causal || j <= i);
+      const float e = expf(fmaf(p.scale, s[r], -lse[i]));
+      P[i * kShortPitch + j] = seen ? e : 0.f;
+      dS[i * kShortPitch + j] = seen ? e * x[r] : 0.f;
+    }
+  }
+  __syncthreads();
+  bool bad = false;
+  const int from = p.causal ? r0 : 0, to = p.causal ? min(S, r0 + 4) : S;   // queries of these keys, keys of these queries
+  // rows r0 .. of M^T A (M: P or dS, A: rows of `pitch`), columns c .. c + 3
+  auto keys = [&](const float* M, const float* A, int pitch, int c, float4 (&sum)[4]) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = from; i < S; ++i) {
+      const float4 a = *reinterpret_cast<const float4*>(A + i * pitch + c), m = *reinterpret_cast<const float4*>(M + i * kShortPitch + r0);
+      short_add(sum[0], m.x, a);
+      short_add(sum[1], m.y, a);
+      short_add(sum[2], m.z, a);
+      short_add(sum[3], m.w, a);
+    }
+  };
+  auto out = [&](void* base, const long long* st, int r) {
+    return static_cast<__nv_bfloat16*>(base) + b * st[0] + (r0 + r) * st[1] + h * st[2];
+  };
+  for (int c = 4 * lane; c < p.d_v; c += 128) {
+    float4 sum[4];
+    keys(P, dO, pv, c, sum);
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r0 + r < S) bad |= short_store(out(p.dv, p.dvs, r), c, p.d_v, sum[r], 1.f);
+  }
+  const int pitch = part_pitch(p.d_shared);
+  for (int c = 4 * lane; c < D; c += 128) {
+    float4 sum[4];
+    keys(dS, q, pd, c, sum);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      if (r0 + r >= S) continue;
+      if (c < p.d_head) {
+        bad |= short_store(out(p.dk, p.dks, r), c, p.d_head, sum[r], p.scale);
+      } else {
+        const float4 w = make_float4(sum[r].x * p.scale, sum[r].y * p.scale, sum[r].z * p.scale, sum[r].w * p.scale);
+        const float z = fmaf(w.x, 0.f, fmaf(w.y, 0.f, fmaf(w.z, 0.f, w.w * 0.f)));
+        *reinterpret_cast<float4*>(p.part + ((long long)blockIdx.x * S + r0 + r) * pitch + c - p.d_head) = w;
+        bad |= z != z;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) sum[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < to; ++j) {
+      const float4 a = *reinterpret_cast<const float4*>(k + j * pd + c);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) short_add(sum[r], dS[row[r] * kShortPitch + j], a);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      if (r0 + r < S) bad |= short_store(out(p.dq, p.dqs, r), c, D, sum[r], p.scale);
+  }
+  if (bad) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+}
+
 // ------------------------------------------------------------- shared key
 // dk_shared[b, j, c] = sum over the heads, in order, of the fp32 partial sums
 // [b][h][j][c] (rows of part_pitch values).  A thread takes four features of a
@@ -1279,6 +1451,22 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   using namespace ab;
   Geo g;
   if (!geometry(p, g, err, errlen)) return cudaErrorInvalidValue;
+  auto sum_heads = [&]() -> cudaError_t {
+    if (p.d_shared == 0) return cudaSuccess;
+    const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), kSharedThreads);
+    if (blocks * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
+    shared_kernel<<<(unsigned)(blocks * p.B), kSharedThreads, 0, s>>>(p, (int)blocks);
+    return cudaGetLastError();
+  };
+  if (p.S <= kAttnBwdShort) {
+    const int pd = short_pitch(p.d_head + p.d_shared), pv = short_pitch(p.d_v);
+    const size_t smem = (size_t)p.S * (2 * pd + 3 * pv + 2 * kShortPitch) * 4;
+    cudaError_t e = cudaFuncSetAttribute(short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    short_kernel<<<(unsigned)g.heads, 32 * (unsigned)cdiv(p.S, 4), smem, s>>>(p);
+    e = cudaGetLastError();
+    return e != cudaSuccess ? e : sum_heads();
+  }
   const int nq = query_tile(g.nch, g.ncv), D = p.d_head + p.d_shared;
   const int nk = key_tile(g.nch, g.ncv);
   Maps kv, qm;                            // for dkv (128-row keys, nq-row queries) and dq (nk-row keys, 128-row queries)
@@ -1305,11 +1493,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
                                          {launch_passes<2, 1>, launch_passes<2, 2>},
                                          {launch_passes<3, 1>, launch_passes<3, 2>}};
   e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
-  if (e != cudaSuccess || p.d_shared == 0) return e;
-  const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), kSharedThreads);
-  if (blocks * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-  shared_kernel<<<(unsigned)(blocks * p.B), kSharedThreads, 0, s>>>(p, (int)blocks);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : sum_heads();
 }
 
 }  // namespace mc

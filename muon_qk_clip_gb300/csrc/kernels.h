@@ -255,6 +255,9 @@ bool attn_fwd_supported(const AttnFwdParams& p, char* err, size_t errlen);
 // Row length of the shared key's partial sums: whole 32-byte sectors.
 __host__ __device__ inline constexpr int part_pitch(int d_shared) { return (d_shared + 7) / 8 * 8; }
 
+// Sequences up to this length take the attention backward's fp32 kernel.
+inline constexpr int kAttnBwdShort = 16;
+
 // Attention backward (bf16, tensor cores), recomputing the probabilities.
 struct AttnBwdParams {
   int B, S, H, d_head, d_shared, d_v;

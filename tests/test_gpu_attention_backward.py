@@ -49,8 +49,9 @@ def inputs(B, S, H, dh, dr, dv, seed, causal=True, head_scale=None):
     return q, k, ks, v, do, torch.from_numpy(o).to(BF16), torch.from_numpy(lse).float()
 
 
-def bounds(q, k, ks, v, do, o, lse, causal, scale=None):
-    """(gradients, error bounds) in float64, as the module's docstring derives them."""
+def bounds(q, k, ks, v, do, o, lse, causal, scale=None, operand=U):
+    """(gradients, error bounds) in float64, as the module's docstring derives them;
+    operand: the rounding of p and ds as operands."""
     Q, K, V, dO, Og, L = (f64(t) for t in (q, k, v, do, o, lse))
     Ks = None if ks is None else f64(ks)
     B, S, H, D = Q.shape
@@ -70,9 +71,9 @@ def bounds(q, k, ks, v, do, o, lse, causal, scale=None):
             e = a + 2.0 ** -22
             ds = np.abs(p * (dd @ vv.T - np.sum(dd * oo, 1)[:, None]))
             mags = np.abs(dd) @ np.abs(vv).T + np.sum(np.abs(dd) * np.abs(oo), 1)[:, None]
-            err = (e + U) * ds + p * (1 + e + U) * W * (dv + 4) * mags
+            err = (e + operand) * ds + p * (1 + e + operand) * W * (dv + 4) * mags
             pd = p.T @ np.abs(dd)
-            ev[b, :, h] = ((U + e) * p).T @ np.abs(dd) + S * W * pd
+            ev[b, :, h] = ((operand + e) * p).T @ np.abs(dd) + S * W * pd
             eq[b, :, h] = scale * ((err + S * W * ds) @ np.abs(kk))
             full = scale * ((err + S * W * ds).T @ np.abs(qq))
             ek[b, :, h] = full[:, :dh]
@@ -161,7 +162,8 @@ def test_attention_backward_strided_outputs_and_inputs():
 
 
 @pytest.mark.parametrize("B,S,H,dh,dr,dv,off", [(2, 131, 3, 20, 0, 50, 0), (1, 150, 2, 64, 12, 33, 0), (1, 140, 3, 128, 61, 127, 8),
-                                                (2, 33, 2, 191, 0, 17, 8), (1, 1, 1, 64, 1, 16, 8)])
+                                                (2, 33, 2, 191, 0, 17, 8), (1, 1, 1, 64, 1, 16, 8),
+                                                (1, 8, 7, 64, 61, 33, 8), (2, 30, 2, 45, 0, 19, 0)])
 def test_attention_backward_odd_widths(B, S, H, dh, dr, dv, off):
     """Widths that are no multiple of eight, in rows padded to one, on 16-byte
     addresses that are and are not 32-byte ones: what lies between the rows is
@@ -318,3 +320,43 @@ def test_attention_backward_on_another_stream_keeps_its_memory(raw):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, got))
     assert mc.qk_attention_backward(*a, k_shared=ksd, stream=0)[0].shape == q.shape
+
+
+@pytest.mark.parametrize("B,S,H,dh,dr,dv,causal", [
+    (1, 1, 3, 128, 0, 128, True), (2, 2, 2, 64, 0, 64, True), (3, 5, 4, 24, 0, 40, False), (1, 8, 7, 64, 56, 40, True),
+    (2, 15, 2, 128, 64, 128, True), (1, 16, 3, 192, 0, 128, False), (40, 16, 9, 64, 8, 128, True),
+    (2, 17, 3, 80, 0, 48, True), (2, 31, 2, 128, 64, 128, True)])
+def test_attention_backward_of_short_sequences(B, S, H, dh, dr, dv, causal):
+    """Up to 16 positions in fp32: p and ds are not rounded, so the bounds hold
+    without their operands' rounding; 17 positions take the tensor cores.  Heads
+    with heavy logits among them."""
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, dv, 110 + S, causal, head_scale=[1.0 + 11.0 * (h % 4 == 1) for h in range(H)])
+    ref, tol = bounds(q, k, ks, v, do, o, lse, causal, operand=0.0 if S <= 16 else U)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, ks, v, do, o, lse = dev(q, k, ks, v, do, o, lse)
+    got = mc.qk_attention_backward(q, k, v, o, lse, do, k_shared=ks, causal=causal, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(got, ref, tol)
+
+
+def test_attention_backward_of_single_positions_is_exact():
+    """One key, and o its value: ds = do . (v - o) = 0, so dq, dk and dk_shared are 0, and dv is do."""
+    mk = lambda *s: torch.randn(*s, device="cuda").to(BF16)  # noqa: E731
+    q, k, ks, v, do = mk(3, 1, 5, 192), mk(3, 1, 5, 128), mk(3, 1, 64), mk(3, 1, 5, 128), mk(3, 1, 5, 128)
+    lse = (torch.cat([k, ks[:, :, None].expand(3, 1, 5, 64)], -1).float() * q.float()).sum(-1).permute(0, 2, 1) / 192 ** 0.5
+    dq, dk, dv, dks = mc.qk_attention_backward(q, k, v, v, lse.contiguous(), do, k_shared=ks)
+    torch.cuda.synchronize()
+    assert not dq.any() and not dk.any() and not dks.any()
+    assert torch.equal(dv, do)
+
+
+def test_attention_backward_of_short_sequences_flags_nonfinite():
+    q, k, ks, v, do, o, lse = inputs(2, 9, 2, 64, 16, 64, 130)
+    do[1, 5, 0, 3] = float("inf")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, ks, v, do, o, lse = dev(q, k, ks, v, do, o, lse)
+    got = mc.qk_attention_backward(q, k, v, o, lse, do, k_shared=ks, status=st)
+    torch.cuda.synchronize()
+    assert st.item() & abi.MC_STATUS_NONFINITE_UPDATE
+    assert all(torch.isfinite(g[0]).all() for g in got) and all(torch.isfinite(g[1, :, 1]).all() for g in got[:3])
