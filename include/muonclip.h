@@ -324,7 +324,8 @@ mc_status qk_attention_backward_workspace_size(const mc_attn_desc* attn, size_t*
  *   dv_j = sum_i p_ij do_i, dq_i = scale sum_j ds_ij k_j,
  *   dk_j = scale sum_i ds_ij q_i.
  * Same shapes, types and limits as the forward (bf16; MC_ERR_UNSUPPORTED
- * otherwise).  p and ds are rounded to bf16 as operands, sums are fp32, each
+ * otherwise).  p and ds are rounded to bf16 as operands (not in sequences of at
+ * most 16 positions, which are computed in fp32), sums are fp32, each
  * gradient is rounded to bf16 once; every sum runs in a fixed order, so equal
  * inputs give equal bits.  workspace: device, 256-byte aligned, for this call alone while it
  * runs.  S_max is a maximum for the clip, not part of the loss: it has no

@@ -8,8 +8,9 @@
 //   dq_i  = scale sum_j ds_ij k_j
 //   dk_j  = scale sum_i ds_ij q_i             (its shared rotary columns summed over the heads)
 //
-// Three launches on the caller's stream (two without a shared key), no atomics
-// on results, so equal inputs give equal bits:
+// Three launches on the caller's stream (two without a shared key; sequences of at
+// most 16 positions have one kernel for the first two), no atomics on results, so
+// equal inputs give equal bits:
 //   rows_kernel     delta and -lse log2(e) of every row, padded to whole tiles
 //   bwd_kernel      dkv_pass: an item is 128 keys, loop over query tiles:
 //                   S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q;
@@ -1164,31 +1165,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 // then a warp takes four rows of an output, a lane four of its columns.  The difference
 // do . v - do . o is summed as do . (v - o), which is exact where a row has one key
 // and o is its value: dq and dk of one-position sequences are exactly 0.
+//
+// Up to 16 positions this beats the tensor cores' 128-row tiles with few sequences
+// and with many (us, against the kernels above; H = 16 or 4, d = 128): 8 of 4
+// positions 8.2 (16.4), 8 of 16 10.2 (18.4), 8192 of 2 33 (309), of 8 94 (313), of
+// 16 145 (315).  With 32 positions, eight warps and the same layout it lost with
+// many: 545 (313).  Bound by the loads' latency with few, by shared-memory reads
+// with many.
+constexpr int kShortThreads = 128;       // at most: a warp per four rows, a thread per load while there are so many
 constexpr int kShortPitch = 20;          // of P and dS: rows of 16-byte alignment
 // Row pitch of `width` columns: whole 16 bytes, an odd number of them, so that 8
 // lanes that read 16 bytes of 8 rows meet no bank twice.
 __host__ __device__ inline int short_pitch(int width) { return 4 * (((width + 3) / 4) | 1); }
 
-// S rows of `width` bf16 columns to fp32 rows of `pitch`, zeros up to a multiple
-// of four columns.
-__device__ inline void short_load(float* to, int pitch, const __nv_bfloat16* from, long long stride, int S, int width) {
-  const int n = (width + 7) / 8, cols = (width + 3) / 4 * 4;
-  for (int x = threadIdx.x; x < S * n; x += blockDim.x) {
-    const int r = x / n, c = 8 * (x - r * n);
-    const __nv_bfloat16* src = from + r * stride + c;
-    float* dst = to + r * pitch + c;
-    if (c + 8 <= width) {
-      const uint4 w = *reinterpret_cast<const uint4*>(src);
-      const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+// Columns c .. c + 7 of a row of `width`, zeros behind it; and these as fp32 in
+// shared memory, up to a multiple of four columns.
+__device__ inline uint4 short_fetch(const __nv_bfloat16* row, int c, int width) {
+  if (c + 8 <= width) return *reinterpret_cast<const uint4*>(row + c);
+  uint32_t w[4] = {};
 #pragma unroll
-      for (int y = 0; y < 2; ++y)
-        *reinterpret_cast<float4*>(dst + 4 * y) =
-            make_float4(__uint_as_float(e[2 * y] << 16), __uint_as_float(e[2 * y] & 0xffff0000u),
-                        __uint_as_float(e[2 * y + 1] << 16), __uint_as_float(e[2 * y + 1] & 0xffff0000u));
-    } else {
-      for (int y = 0; c + y < cols; ++y) dst[y] = c + y < width ? __bfloat162float(src[y]) : 0.f;
-    }
-  }
+  for (int y = 0; y < 7; ++y)
+    if (c + y < width) w[y / 2] |= (uint32_t)__bfloat16_as_ushort(row[c + y]) << (16 * (y % 2));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ inline void short_put(float* row, int c, int width, const uint4& w) {
+  const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int y = 0; y < 2; ++y)
+    if (c + 4 * y < width)
+      *reinterpret_cast<float4*>(row + c + 4 * y) =
+          make_float4(__uint_as_float(e[2 * y] << 16), __uint_as_float(e[2 * y] & 0xffff0000u),
+                      __uint_as_float(e[2 * y + 1] << 16), __uint_as_float(e[2 * y + 1] & 0xffff0000u));
 }
 // a += x b for four columns
 __device__ inline void short_add(float4& a, float x, const float4& b) {
@@ -1215,30 +1222,45 @@ __device__ inline bool short_store(__nv_bfloat16* row, int c, int width, const f
   return z != z;
 }
 
-__global__ void __launch_bounds__(128, 4) short_kernel(const __grid_constant__ AttnBwdParams p) {
+__global__ void __launch_bounds__(kShortThreads, 4) short_kernel(const __grid_constant__ AttnBwdParams p) {
   extern __shared__ float4 short_smem[];
   const int S = p.S, D = p.d_head + p.d_shared, pd = short_pitch(D), pv = short_pitch(p.d_v);
   float* q = reinterpret_cast<float*>(short_smem);
   float *k = q + S * pd, *v = k + S * pd, *dO = v + S * pv, *o = dO + S * pv, *P = o + S * pv, *dS = P + S * kShortPitch;
   const int b = blockIdx.x / p.H, h = blockIdx.x - b * p.H;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto at = [&](const void* base, const long long* st) {
-    return static_cast<const __nv_bfloat16*>(base) + b * st[0] + h * st[2];
+  auto at = [&](const void* base, const long long* st, int r) {
+    return static_cast<const __nv_bfloat16*>(base) + b * st[0] + r * st[1] + h * st[2];
   };
-  short_load(q, pd, at(p.q, p.qs), p.qs[1], S, D);
-  short_load(k, pd, at(p.k, p.kst), p.kst[1], S, p.d_head);
-  if (p.d_shared)
-    short_load(k + p.d_head, pd, static_cast<const __nv_bfloat16*>(p.ks) + b * p.kss[0], p.kss[1], S, p.d_shared);
-  short_load(v, pv, at(p.v, p.vs), p.vs[1], S, p.d_v);
-  short_load(dO, pv, at(p.d_o, p.dos), p.dos[1], S, p.d_v);
-  short_load(o, pv, at(p.o, p.os), p.os[1], S, p.d_v);
+  // every tensor's eight columns in flight before the first is stored
+  const int n = (max(D, p.d_v) + 7) / 8;
+  for (int x = threadIdx.x; x < S * n; x += blockDim.x) {
+    const int r = x / n, c = 8 * (x - r * n);
+    const bool own = c < p.d_head;
+    uint4 wq = {}, wk = {}, wv = {}, wd = {}, wo = {};
+    if (c < D) {
+      wq = short_fetch(at(p.q, p.qs, r), c, D);
+      wk = own ? short_fetch(at(p.k, p.kst, r), c, p.d_head)
+               : short_fetch(static_cast<const __nv_bfloat16*>(p.ks) + b * p.kss[0] + r * p.kss[1], c - p.d_head, p.d_shared);
+    }
+    if (c < p.d_v) {
+      wv = short_fetch(at(p.v, p.vs, r), c, p.d_v);
+      wd = short_fetch(at(p.d_o, p.dos, r), c, p.d_v);
+      wo = short_fetch(at(p.o, p.os, r), c, p.d_v);
+    }
+    short_put(q + r * pd, c, D, wq);
+    short_put(k + r * pd, c, D, wk);
+    short_put(v + r * pv, c, p.d_v, wv);
+    short_put(dO + r * pv, c, p.d_v, wd);
+    short_put(o + r * pv, c, p.d_v, wo);
+  }
   __syncthreads();
   const int r0 = 4 * warp;               // this warp's four queries, then its four rows of each output
   int row[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) row[r] = min(r0 + r, S - 1);
-  {
-    static_assert(kAttnBwdShort <= 16, "a half-warp holds the keys");
+  if (r0 < S) {
+    static_assert(kAttnBwdShort <= 16 && kAttnBwdShort <= kShortThreads / 8, "a half-warp holds the keys, the warps all rows");
     const int j = lane & 15, key = min(j, S - 1), i0 = r0 + 2 * (lane >> 4);
     const int query[2] = {min(i0, S - 1), min(i0 + 1, S - 1)};
     float s[2] = {}, x[2] = {};
@@ -1273,6 +1295,7 @@ __global__ void __launch_bounds__(128, 4) short_kernel(const __grid_constant__ A
     }
   }
   __syncthreads();
+  if (r0 >= S) return;
   bool bad = false;
   const int from = p.causal ? r0 : 0, to = p.causal ? min(S, r0 + 4) : S;   // queries of these keys, keys of these queries
   // rows r0 .. of M^T A (M: P or dS, A: rows of `pitch`), columns c .. c + 3
@@ -1463,7 +1486,10 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
     const size_t smem = (size_t)p.S * (2 * pd + 3 * pv + 2 * kShortPitch) * 4;
     cudaError_t e = cudaFuncSetAttribute(short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    short_kernel<<<(unsigned)g.heads, 32 * (unsigned)cdiv(p.S, 4), smem, s>>>(p);
+    const int width = p.d_head + p.d_shared > p.d_v ? p.d_head + p.d_shared : p.d_v;
+    const int want = p.S * (width > 64 ? (width + 7) / 8 : 8);       // 8 S: a warp per four rows
+    const int threads = want < kShortThreads ? (want + 31) / 32 * 32 : kShortThreads;
+    short_kernel<<<(unsigned)g.heads, threads, smem, s>>>(p);
     e = cudaGetLastError();
     return e != cudaSuccess ? e : sum_heads();
   }
