@@ -131,6 +131,13 @@ __device__ inline void regs_release() { asm volatile("setmaxnreg.dec.sync.aligne
 template <int N>
 __device__ inline void regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// Programmatic dependent launch: a kernel's blocks may start before the one behind
+// it in the stream has ended, and wait for its end (and its writes) here.  2 us
+// less on small batches (16.4 instead of 18.4 for [2, 128, 4, 64], 34.8 instead of
+// 36.9 for [3, 1021, 5, 80 / 48]).
+__device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ inline void release_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 enum Role { kIssue, kOutput, kCompute };
 // All threads of the block, whichever role's code they are in.
 __device__ inline void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
@@ -310,6 +317,7 @@ constexpr int kRowPos = 16, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
   __shared__ float sums[kRowHeads][kRowPos + 1];
+  release_next();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.counter[threadIdx.x] = 0;   // of the launches behind this one
   // block: position group fastest, then head group, then batch
   const int bi = blockIdx.x / ni, i0 = (blockIdx.x - bi * ni) * kRowPos;
@@ -1137,6 +1145,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = tmem_slot;
+  await_previous();
   uint64_t *bars = reinterpret_cast<uint64_t*>(smem), *bars2 = bars + kBarBytes / 8;
   uint8_t* data = smem + 2 * kBarBytes;
   // one branch per role, its register share at the head of it: the compiler
@@ -1360,6 +1369,7 @@ __global__ void __launch_bounds__(kShortThreads, 4) short_kernel(const __grid_co
 constexpr int kSharedThreads = 64;
 __global__ void __launch_bounds__(kSharedThreads) shared_kernel(const __grid_constant__ AttnBwdParams p, const int blocks) {
   const int quads = part_pitch(p.d_shared) / 4, b = blockIdx.x / blocks;
+  await_previous();
   const long long per = (long long)p.S * quads, e = (long long)(blockIdx.x - b * blocks) * kSharedThreads + threadIdx.x;
   if (e >= per) return;
   const float4* src = reinterpret_cast<const float4*>(p.part) + (long long)b * p.H * per + e;
@@ -1439,13 +1449,28 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   return true;
 }
 
+// Launches a kernel that calls await_previous().
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 template <int NCH, int NCV>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr size_t smem = smem_bytes<NCH, NCV>();
   const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  bwd_kernel<NCH, NCV><<<grid, kThreads, smem, s>>>(p, kv, qm, g);
-  return cudaGetLastError();
+  return launch_behind(bwd_kernel<NCH, NCV>, (unsigned)grid, kThreads, smem, s, p, kv, qm, g);
 }
 
 }  // namespace ab
@@ -1478,8 +1503,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
     if (p.d_shared == 0) return cudaSuccess;
     const long long blocks = cdiv((long long)p.S * (part_pitch(p.d_shared) / 4), kSharedThreads);
     if (blocks * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-    shared_kernel<<<(unsigned)(blocks * p.B), kSharedThreads, 0, s>>>(p, (int)blocks);
-    return cudaGetLastError();
+    return launch_behind(shared_kernel, (unsigned)(blocks * p.B), kSharedThreads, 0, s, p, (int)blocks);
   };
   if (p.S <= kAttnBwdShort) {
     const int pd = short_pitch(p.d_head + p.d_shared), pv = short_pitch(p.d_v);
