@@ -131,13 +131,6 @@ __device__ inline void regs_release() { asm volatile("setmaxnreg.dec.sync.aligne
 template <int N>
 __device__ inline void regs_acquire() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// Programmatic dependent launch: a kernel's blocks may start before the one behind
-// it in the stream has ended, and wait for its end (and its writes) here.  2 us
-// less on small batches (16.4 instead of 18.4 for [2, 128, 4, 64], 34.8 instead of
-// 36.9 for [3, 1021, 5, 80 / 48]).
-__device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ inline void release_next() { asm volatile("griddepcontrol.launch_dependents;"); }
-
 enum Role { kIssue, kOutput, kCompute };
 // All threads of the block, whichever role's code they are in.
 __device__ inline void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
@@ -1447,22 +1440,6 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   g.div_last = make_fastdiv((uint32_t)(g.heads % g.group ? g.heads % g.group : 1));
   g.div_h = make_fastdiv((uint32_t)p.H);
   return true;
-}
-
-// Launches a kernel that calls await_previous().
-template <typename... P, typename... A>
-cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(grid);
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = at;
-  c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 
 template <int NCH, int NCV>

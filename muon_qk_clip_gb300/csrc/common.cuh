@@ -65,6 +65,29 @@ __device__ inline uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// Programmatic dependent launch: a kernel's blocks may start before the one behind
+// it in the stream has ended, and wait for its end (and its writes) here.  Attention
+// backward: 16.4 us instead of 18.4 for [2, 128, 4, 64], 34.8 instead of 36.9 for
+// [3, 1021, 5, 80 / 48].
+__device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ inline void release_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+// Launches a kernel that calls await_previous().
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3(grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+}
+
 // Two fp32 operations in one instruction.
 __device__ inline unsigned long long two(float a, float b) {
   unsigned long long r;

@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_back_kernel(const __grid_con
   constexpr int N = NU ? NU : 1, groups = kWarps / WPR;
   __shared__ float red[2][kWarps];
   extern __shared__ float sums[];        // [cols] when several groups share a block
+  release_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = warp % WPR, mine = warp / WPR;
   const int units = (p.cols + U::kCols - 1) / U::kCols;
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(1024) norm_weight_kernel(const float* part, fl
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  await_previous();
   constexpr int flight = (kBackGrid + 31) / 32;        // every load at once
   float v[flight];
 #pragma unroll
@@ -551,8 +553,7 @@ cudaError_t launch_back(const BackParams& p, float* dw, cudaStream_t s) {
   int grid = 0;
   const cudaError_t e = by_share<kBackUnits<T, VEC>>(p.cols, Unit<T, VEC>::kCols, BackLaunch<T, VEC>{p, grid, s});
   if (e != cudaSuccess || !p.part) return e;
-  norm_weight_kernel<<<(unsigned)cdiv(p.cols, 32), 1024, 0, s>>>(p.part, dw, grid, p.cols);
-  return cudaGetLastError();
+  return launch_behind(norm_weight_kernel, (unsigned)cdiv(p.cols, 32), 1024, 0, s, p.part, dw, grid, p.cols);
 }
 
 mc_status err(mc_status s, const char* fmt, ...) {
