@@ -310,6 +310,7 @@ constexpr int kRowPos = 16, kRowHeads = 8;
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
                                                    const int nh) {
   __shared__ float sums[kRowHeads][kRowPos + 1];
+  await_previous();
   release_next();
   if (blockIdx.x == 0 && threadIdx.x < 2) p.counter[threadIdx.x] = 0;   // of the launches behind this one
   // block: position group fastest, then head group, then batch
@@ -1226,6 +1227,7 @@ __device__ inline bool short_store(__nv_bfloat16* row, int c, int width, const f
 
 __global__ void __launch_bounds__(kShortThreads, 4) short_kernel(const __grid_constant__ AttnBwdParams p) {
   extern __shared__ float4 short_smem[];
+  await_previous();
   const int S = p.S, D = p.d_head + p.d_shared, pd = short_pitch(D), pv = short_pitch(p.d_v);
   float* q = reinterpret_cast<float*>(short_smem);
   float *k = q + S * pd, *v = k + S * pd, *dO = v + S * pv, *o = dO + S * pv, *P = o + S * pv, *dS = P + S * kShortPitch;
@@ -1490,8 +1492,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
     const int width = p.d_head + p.d_shared > p.d_v ? p.d_head + p.d_shared : p.d_v;
     const int want = p.S * (width > 64 ? (width + 7) / 8 : 8);       // 8 S: a warp per four rows
     const int threads = want < kShortThreads ? (want + 31) / 32 * 32 : kShortThreads;
-    short_kernel<<<(unsigned)g.heads, threads, smem, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_behind(short_kernel, (unsigned)g.heads, (unsigned)threads, smem, s, p);
     return e != cudaSuccess ? e : sum_heads();
   }
   const int nq = query_tile(g.nch, g.ncv), D = p.d_head + p.d_shared;
@@ -1511,8 +1512,7 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   const int sms = sm_count();
   const long long ni = cdiv(g.sp, kRowPos), nh = cdiv(p.H, kRowHeads);
   if (ni * nh * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-  rows_kernel<<<(unsigned)(ni * nh * p.B), 256, 0, s>>>(p, (int)g.sp, (int)ni, (int)nh);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_behind(rows_kernel, (unsigned)(ni * nh * p.B), 256, 0, s, p, (int)g.sp, (int)ni, (int)nh);
   if (e != cudaSuccess) return e;
   const int grid = 2 * g.items < sms ? 2 * g.items : sms;
   using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);

@@ -66,9 +66,11 @@ __device__ inline uint32_t smem_u32(const void* p) {
 }
 
 // Programmatic dependent launch: a kernel's blocks may start before the one behind
-// it in the stream has ended, and wait for its end (and its writes) here.  Attention
+// it in the stream has ended, and wait for its end (and its writes) here: every
+// thread, before it reads or writes anything that another kernel may.  Attention
 // backward: 16.4 us instead of 18.4 for [2, 128, 4, 64], 34.8 instead of 36.9 for
-// [3, 1021, 5, 80 / 48].
+// [3, 1021, 5, 80 / 48]; calls in a row: add_norm of 4096 x 7168 to e4m3 33.9 us
+// each instead of 36.1, the rotary gradient of [1, 4096, 64, 64] 12.2 instead of 14.5.
 __device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ inline void release_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 

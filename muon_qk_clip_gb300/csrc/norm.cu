@@ -219,6 +219,8 @@ __global__ void __launch_bounds__(kThreads) add_norm_kernel(const __grid_constan
   using U = Unit<T, VEC>;
   constexpr int N = NU ? NU : 1;
   __shared__ float red[kWarps];
+  await_previous();
+  release_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = warp % WPR;
   const long long row = (long long)blockIdx.x * (kWarps / WPR) + warp / WPR;
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kThreads, 2) norm_back_kernel(const __grid_con
   constexpr int N = NU ? NU : 1, groups = kWarps / WPR;
   __shared__ float red[2][kWarps];
   extern __shared__ float sums[];        // [cols] when several groups share a block
+  await_previous();
   release_next();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w0 = warp % WPR, mine = warp / WPR;
@@ -524,8 +527,7 @@ struct AddLaunch {
   cudaStream_t s;
   template <int WPR, int NU>
   cudaError_t operator()(Share<WPR, NU>) const {
-    add_norm_kernel<T, VEC, WPR, NU><<<(unsigned)cdiv(p.rows, kWarps / WPR), kThreads, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch_behind(add_norm_kernel<T, VEC, WPR, NU>, (unsigned)cdiv(p.rows, kWarps / WPR), kThreads, 0, s, p);
   }
 };
 template <typename T, bool VEC>
@@ -544,8 +546,7 @@ struct BackLaunch {
     const long long want = cdiv(p.rows, groups);
     grid = (int)(want < kBackGrid ? want : kBackGrid);
     const size_t smem = p.part && groups > 1 && NU ? (size_t)p.cols * 4 : 0;   // at most 4096 columns: 16 KB
-    norm_back_kernel<T, VEC, WPR, NU><<<grid, kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_behind(norm_back_kernel<T, VEC, WPR, NU>, (unsigned)grid, kThreads, smem, s, p);
   }
 };
 template <typename T, bool VEC>

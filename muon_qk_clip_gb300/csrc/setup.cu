@@ -170,6 +170,8 @@ struct PairsOf<T, 1> {
 template <typename T, int V>
 __global__ void __launch_bounds__(256, 4) rope_back_kernel(const __grid_constant__ RopeBack p) {
   extern __shared__ float2 turns[];      // [d/2] (hi, lo) turns per position
+  await_previous();
+  release_next();
   const int half = p.d / 2, nv = half / V;
   const int t = (int)(blockIdx.x * 256 + threadIdx.x);
   const int r0 = (int)fastdiv(t, p.div_nv), c = t - r0 * nv;
@@ -226,8 +228,7 @@ cudaError_t launch_rope_back(RopeBack p, int B, cudaStream_t s) {
   p.div_nv = make_fastdiv((uint32_t)nv);
   p.div_s = make_fastdiv((uint32_t)p.S);
   p.div_groups = make_fastdiv((uint32_t)groups);
-  rope_back_kernel<T, V><<<(unsigned)cdiv(at * groups, 256), 256, (size_t)(p.d / 2) * 8, s>>>(p);
-  return cudaGetLastError();
+  return launch_behind(rope_back_kernel<T, V>, (unsigned)cdiv(at * groups, 256), 256, (size_t)(p.d / 2) * 8, s, p);
 }
 
 mc_status err(mc_status s, const char* fmt, ...) {

@@ -187,3 +187,40 @@ def test_projection_backward_rejects_host_tensors():
     X, W = torch.zeros(1, 4, 8), torch.zeros(8, 8)
     with pytest.raises(ValueError, match="device tensors"):
         backward.project_mha_backward(X, W, W, X.view(1, 4, 1, 8), X.view(1, 4, 1, 8))
+
+
+def test_chained_layer_calls_match_calls_one_by_one():
+    """Forward, attention's gradient (long and short sequences), rotary gradient:
+    queued behind each other, eagerly and captured, with the bits of calls that each
+    wait for the one before."""
+    for B, S in ((2, 300), (40, 12)):
+        q, k, v, do = (mk((B, S, 4, d), 1.0, n, BF16) for n, d in (("cq", 192), ("ck", 128), ("cv", 128), ("cd", 128)))
+        ks, big = mk((B, S, 64), 1.0, "cks", BF16), torch.empty(64 << 20, device="cuda")
+
+        def chain(wait):
+            done = torch.cuda.synchronize if wait else (lambda: None)
+            big.fill_(1.0)
+            done()
+            o, lse, _ = mc.qk_attention_forward(q, k, v, ks, lse=True)
+            done()
+            dq, dk, dv, dks = mc.qk_attention_backward(q, k, v, o, lse, do, k_shared=ks)
+            done()
+            mc.rope_backward(dq[..., 128:], out=dq[..., 128:])
+            done()
+            dks = mc.rope_backward(dks)
+            done()
+            return dq, dk, dv, dks
+
+        want = chain(True)
+        runs = [chain(False) for _ in range(4)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for got in runs for a, b in zip(want, got))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = [chain(False), chain(False)]
+        for _ in range(2):
+            for t in (*got[0], *got[1]):
+                t.fill_(7.0)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for g in got for a, b in zip(want, g))

@@ -301,3 +301,61 @@ def test_norm_gradient_on_another_stream_keeps_its_memory():
     assert len(taken) == 4 and all(torch.equal(a, b) for a, b in zip(want, got))
     with pytest.raises(ValueError, match="contiguous"):
         mc.rms_norm_backward(dy, h, rstd, weight=w, workspace=torch.empty(1, device="cuda").expand(304 * 640))
+
+
+def test_calls_wait_for_what_their_inputs_come_from():
+    """The kernels may be scheduled before the work in front of them has ended, and
+    wait for it: behind a long kernel, a copy, a fill, another stream's work and
+    each other, eagerly and captured, they see its results."""
+    src, w = normal((3000, 1024), 1.0, "dx", BF16), (1 + normal((1024,), 0.2, "dw", F32)).to(BF16)
+    host = src.cpu().pin_memory()
+    x, r, dy = torch.empty_like(src), torch.empty_like(src), torch.empty_like(src)
+    side = torch.cuda.Stream()
+    big = torch.empty(64 << 20, device="cuda")
+
+    def chain(seed):
+        big.fill_(seed)                                    # a kernel that outlasts the launches behind it
+        x.copy_(src)
+        y, _, h, rstd = mc.add_rms_norm(x, weight=w)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            big.fill_(seed + 1)
+            dy.copy_(y)
+        torch.cuda.current_stream().wait_stream(side)
+        dx, dw = mc.rms_norm_backward(dy, h, rstd, weight=w)
+        r.zero_()
+        r.add_(dx)
+        y2, s2, h2, _ = mc.add_rms_norm(y, r, w, out_dtype=F8)
+        out = mc.rope_backward(h2.view(1, 3000, 16, 64))
+        big.fill_(seed + 2)
+        x.copy_(host, non_blocking=True)
+        z = mc.add_rms_norm(x, out.view(3000, 1024), w)[0]
+        return dx, dw, y2.view(torch.uint8), s2, out, z
+
+    torch.cuda.synchronize()
+    steps = []
+    real = mc._run
+
+    def one_by_one(*a):
+        torch.cuda.synchronize()
+        real(*a)
+        torch.cuda.synchronize()
+    mc._run = one_by_one
+    try:
+        want = [t.clone() for t in chain(1.0)]
+    finally:
+        mc._run = real
+    for _ in range(3):
+        steps.append(chain(2.0))
+    torch.cuda.synchronize()
+    for got in steps:
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = chain(3.0)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
