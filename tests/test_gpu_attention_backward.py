@@ -126,7 +126,7 @@ def test_attention_backward_parity(B, S, H, dh, dr, dv, causal):
     assert st.item() == 0
     check(got, ref, tol)
     again = mc.qk_attention_backward(dq_, dk_, dv_, do_, dl, ddo, k_shared=dks_, causal=causal)
-    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, again))     # no atomics
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, again))     # equal bits
 
 
 def test_attention_backward_heavy_logits():
