@@ -289,8 +289,9 @@ mc_status qk_attention_forward(const mc_attn_desc* attn, const mc_attn_out* out,
  * Everything is bf16 but lse; features have unit stride; the other strides are
  * in elements, multiples of 8 (axes of one element: any), and pointers are
  * 16-byte aligned.  Inputs may broadcast (stride 0); an output gives every
- * element an address of its own and overlaps no input, not lse, status or the
- * workspace, and no other output (two outputs may interleave, as dk and dv of
+ * element an address of its own and overlaps no memory that an input, lse,
+ * status or the
+ * workspace spans, and no other output (two outputs may interleave, as dk and dv of
  * one buffer: equal strides on the axes around the blocks that alternate). */
 typedef struct {
   const void* v;           /* device values [B, S, H, d_v]                          */
@@ -413,7 +414,7 @@ mc_status mc_rope(void* x, int32_t B, int32_t S, int32_t nh, int32_t d, int64_t 
  * (dy0 cos + dy1 sin, dy1 cos - dy0 sin), angle s * theta^(-2k/d).  dy and dx
  * [b, s, h, 0..d) with strides (yb, ys, yh) and (xb, xs, xh) in elements, unit
  * stride along d; dx == dy with equal strides rotates in place, any other
- * overlap is refused, as is a dx with shared addresses.  Types, d and theta as
+ * overlap of the memory that they span is refused, as is a dx with shared addresses.  Types, d and theta as
  * in mc_rope, for angles up to 2^24: S max(1, 1/theta) <= 2^24 (else
  * MC_ERR_UNSUPPORTED); B or S of 0 returns at once.  Asynchronous on `stream`. */
 mc_status mc_rope_backward(const void* dy, int64_t yb, int64_t ys, int64_t yh, void* dx, int64_t xb, int64_t xs,

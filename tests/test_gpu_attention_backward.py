@@ -360,3 +360,42 @@ def test_attention_backward_of_short_sequences_flags_nonfinite():
     torch.cuda.synchronize()
     assert st.item() & abi.MC_STATUS_NONFINITE_UPDATE
     assert all(torch.isfinite(g[0]).all() for g in got) and all(torch.isfinite(g[1, :, 1]).all() for g in got[:3])
+
+
+@pytest.mark.parametrize("S,stride", [(3, (1 << 31) + 8), (20, (1 << 28) + 8)])
+def test_attention_backward_offsets_past_32_bits(S, stride):
+    """Positions so far apart that element offsets pass 2^31 and byte offsets 2^32,
+    in inputs and outputs, by the short sequences' kernel and the tensor cores."""
+    q, k, ks, v, do, o, lse = inputs(1, S, 2, 64, 16, 48, 140 + S)
+    a = dev(q, k, v, o, lse, do)
+    ksd = ks.cuda()
+    want = mc.qk_attention_backward(*a, k_shared=ksd)
+    far = torch.empty((S - 1) * stride + 1024, dtype=BF16, device="cuda")
+
+    def spread(t, at):                     # [1, S, H, w] or [1, S, w] at `at` of each position's place
+        st = (0, stride, t.shape[-1], 1) if t.dim() == 4 else (0, stride, 1)
+        return far.as_strided(t.shape, st, at)
+    places = [spread(t, at) for t, at in ((a[0], 0), (a[1], 160), (a[2], 288), (a[3], 384), (a[5], 480), (ksd, 576))]
+    for p, t in zip(places, (a[0], a[1], a[2], a[3], a[5], ksd)):
+        p.copy_(t)
+    got = mc.qk_attention_backward(*places[:4], a[4], places[4], k_shared=places[5])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    room = torch.empty_like(far)
+    outs = [room.as_strided(g.shape, (0, stride, g.shape[-1], 1) if g.dim() == 4 else (0, stride, 1), at)
+            for g, at in zip(want, (0, 160, 288, 384))]
+    got = mc.qk_attention_backward(*a, k_shared=ksd, dq=outs[0], dk=outs[1], dv=outs[2], dk_shared=outs[3])
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+
+
+def test_attention_backward_on_two_streams_at_once():
+    sets = [dev(*(inputs(2, S, 3, 64, 0, 64, 150 + S)[i] for i in (0, 1, 3, 5, 6, 4))) for S in (16, 200, 520, 330)]
+    want = [mc.qk_attention_backward(*a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        got = [mc.qk_attention_backward(*a, stream=s) for a, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for w, g in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(w[:3], g[:3]))

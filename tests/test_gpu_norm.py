@@ -359,3 +359,28 @@ def test_calls_wait_for_what_their_inputs_come_from():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+def test_norm_and_rope_offsets_past_32_bits():
+    """Rows and positions so far apart that element offsets pass 2^31."""
+    rows, cols, ld = 3, 384, (1 << 31) + 8
+    far = torch.empty((rows - 1) * ld + 4 * cols, dtype=BF16, device="cuda")
+    x, r, dy = (normal((rows, cols), 1.0, n, BF16) for n in ("fx", "fr", "fd"))
+    w = (1 + normal((cols,), 0.2, "fw", F32)).to(BF16)
+    place = [far.as_strided((rows, cols), (ld, 1), i * cols) for i in range(4)]
+    y, _, h, rstd = mc.add_rms_norm(x, r, w)
+    dx, dw = mc.rms_norm_backward(dy, h, rstd, weight=w)
+    place[0].copy_(x)
+    place[1].copy_(r)
+    y2, _, h2, rstd2 = mc.add_rms_norm(place[0], place[1], w, h=place[2], out=place[3])
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(h, h2) and torch.equal(rstd, rstd2)
+    place[0].copy_(dy)
+    dx2, dw2 = mc.rms_norm_backward(place[0], h2, rstd, weight=w, dx=place[1])
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    want = mc.rope_backward(dy.view(1, rows, 3, 128))
+    got = mc.rope_backward(place[0].as_strided((1, rows, 3, 128), (0, ld, 128, 1), 0),
+                           out=torch.empty_like(far).as_strided((1, rows, 3, 128), (0, ld, 128, 1), 0))
+    torch.cuda.synchronize()
+    assert torch.equal(want, got)
