@@ -290,9 +290,9 @@ mc_status qk_attention_forward(const mc_attn_desc* attn, const mc_attn_out* out,
  * in elements, multiples of 8 (axes of one element: any), and pointers are
  * 16-byte aligned.  Inputs may broadcast (stride 0); an output gives every
  * element an address of its own and overlaps no memory that an input, lse,
- * status or the
- * workspace spans, and no other output (two outputs may interleave, as dk and dv of
- * one buffer: equal strides on the axes around the blocks that alternate). */
+ * status or the workspace spans, and no other output (two outputs may
+ * interleave, as dk and dv of one buffer: equal strides on the axes around the
+ * blocks that alternate). */
 typedef struct {
   const void* v;           /* device values [B, S, H, d_v]                          */
   int32_t d_v;             /* value width, 16..128                                  */

@@ -59,9 +59,17 @@ __host__ __device__ constexpr bool p_apart(int nch, int ncv) { return nch + ncv 
 __host__ __device__ constexpr int query_tile(int nch, int ncv) { return nch + ncv > 4 ? 96 : 128; }
 __host__ __device__ constexpr int query_stages(int nch, int ncv) { return p_apart(nch, ncv) ? 3 : 2; }
 // Keys per tile of the dQ pass: tensor memory holds dQ (64 nch columns), Q and dO
-// as operands (32 nch, 32 ncv), S and dP (a column per key) and dS (half of one).
-__host__ __device__ constexpr int key_tile(int nch, int ncv) { return nch > 2 ? 64 : nch > 1 ? 96 : 128; }
-constexpr int kKeyStages = 3;            // key and value tiles of the dQ pass
+// as operands (32 each per chunk), S and dP (a column per key) and dS (half of
+// one).  With three chunks of q.k 96 keys fit when only two chunks of Q are there
+// and dO is not: the rest is read from shared memory, and values have one stage.
+// (64 keys with all of Q and dO in tensor memory: 1439 us for 32768 tokens instead
+// of 1404, 841 for k2_mla_layer instead of 835; 96 keys with dS over dP, so that
+// dP waits for dQ: 1414 and 842.)
+__host__ __device__ constexpr int key_tile(int nch, int ncv) { return nch > 1 ? 96 : 128; }
+__host__ __device__ constexpr int q_in_tmem(int nch) { return nch < 3 ? nch : 2; }
+__host__ __device__ constexpr bool do_in_tmem(int nch) { return nch < 3; }
+constexpr int kKeyStages = 3;            // key tiles of the dQ pass, and value tiles where they fit
+__host__ __device__ constexpr int value_stages(int nch, int ncv) { return nch < 3 ? 3 : ncv < 2 ? 2 : 1; }
 
 struct Maps {
   CUtensorMap q, k, ks, v, d_o;          // inputs: 64-feature chunks of a tile's rows
@@ -786,17 +794,19 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
 // dS has columns of its own, so S(t+1) starts as soon as S(t) has been read and
 // dP(t+1) as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1),
 // dQ(t).  A key tile is held from S(t) to dQ(t), two products later than the next
-// one's S wants its own, so keys and values have three stages.
+// one's S wants its own, so keys have three stages, and values where they fit.
 template <int NCH, int NCV, int ROLE>
 __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, const Geo& g, uint8_t* smem, uint64_t* bars,
                                          uint32_t tmem_base, volatile int& abort_flag, int warp, int lane) {
   constexpr int BN = key_tile(NCH, NCV), NH = BN / 2;
-  constexpr int kStages = kKeyStages;
+  constexpr int kStages = kKeyStages, VS = value_stages(NCH, NCV);
+  constexpr int QT = q_in_tmem(NCH);     // chunks of Q that are operands in tensor memory
+  constexpr bool DOT = do_in_tmem(NCH);  // dO is one too
   constexpr int CK = BN * 128;           // bytes of one chunk of a key tile
   uint8_t* qbuf = smem;                                 // NCH chunks
   uint8_t* dobuf = qbuf + NCH * CH;                     // NCV chunks
   uint8_t* kbuf = dobuf + NCV * CH;                     // 3 x NCH chunks of a key tile
-  uint8_t* vbuf = kbuf + kStages * NCH * CK;           // 3 x NCV chunks
+  uint8_t* vbuf = kbuf + kStages * NCH * CK;            // VS x NCV chunks
   uint64_t* q_full = bars + 0;
   uint64_t* q_empty = bars + 1;
   uint64_t* k_full = bars + 2;      // [3]
@@ -811,12 +821,14 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
   uint64_t* acc_full = bars + 19;
   uint64_t* acc_empty = bars + 20;
   uint64_t* drain = bars + 21;
+  uint64_t* do_full = bars + 33;
+  uint64_t* do_empty = bars + 34;
   const Ring ring = {reinterpret_cast<volatile int*>(bars + 31), bars + 22, bars + 26};
   if (threadIdx.x == 0) {
-    mbar_init(q_full, 1); mbar_init(q_empty, 1);
+    mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&k_full[s], 1); mbar_init(&k_empty[s], 1);
-      mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1);
+      mbar_init(&v_full[s], 1); mbar_init(&v_empty[s], 1);     // VS of them are used
     }
     mbar_init(s_full, 1); mbar_init(s_empty, 8);
     mbar_init(dp_full, 1); mbar_init(ds_full, 8); mbar_init(ds_empty, 1);
@@ -830,7 +842,8 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     if (NCH > g.nck) prefetch_tmap(&mp.ks);
   }
   block_sync();
-  const uint32_t t_dq = tmem_base, t_q = t_dq + 64 * NCH, t_do = t_q + 32 * NCH, t_s = t_do + 32 * NCV, t_dp = t_s + BN, t_ds = t_dp + BN;
+  const uint32_t t_dq = tmem_base, t_q = t_dq + 64 * NCH, t_do = t_q + 32 * QT, t_s = t_do + (DOT ? 32 * NCV : 0), t_dp = t_s + BN,
+                 t_ds = t_dp + BN;
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
   auto tiles = [&](int blk) {
     const int hi = p.causal ? min(p.S, (blk + 1) * BM) : p.S;
@@ -840,9 +853,9 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
   if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      uint32_t li = 0, s = 0, ph = 0;
-      bool used_q = false, used_k[kStages] = {}, used_v[kStages] = {};
-      uint32_t par_q = 0, par_k[kStages] = {}, par_v[kStages] = {};
+      uint32_t li = 0, s = 0, ph = 0, sv = 0, phv = 0;
+      bool used_q = false, used_do = false, used_k[kStages] = {}, used_v[VS] = {};
+      uint32_t par_q = 0, par_do = 0, par_k[kStages] = {}, par_v[VS] = {};
       int x = atomicAdd(p.counter + 1, 1), x1 = 0;
       bool ok = ring_put(ring, 0, x, &abort_flag);
       for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
@@ -851,10 +864,17 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
         const int nt = tiles(blk);
         // the queries' buffer is free once the item before has begun
         if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
-        mbar_arrive_expect_tx(q_full, (NCH + NCV) * CH);
+        mbar_arrive_expect_tx(q_full, NCH * CH);
         for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
-        for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, q_full, 64 * c, h, blk * BM, b);
         used_q = true; par_q = li & 1;
+        auto load_do = [&]() -> bool {
+          if (!mbar_wait(do_empty, (li & 1) ^ 1, &abort_flag)) return false;
+          mbar_arrive_expect_tx(do_full, NCV * CH);
+          for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, do_full, 64 * c, h, blk * BM, b);
+          used_do = true; par_do = li & 1;
+          return true;
+        };
+        if (DOT && !load_do()) { ok = false; break; }
         for (int it = 0; it < nt; ++it) {
           if (it == max(0, nt - 2)) x1 = atomicAdd(p.counter + 1, 1);      // used a tile later: its latency is hidden
           if (it == nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
@@ -866,20 +886,23 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
             else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
           }
           used_k[s] = true; par_k[s] = ph;
-          if (!mbar_wait(&v_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
-          mbar_arrive_expect_tx(&v_full[s], NCV * CK);
-          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + (s * NCV + c) * CK, &mp.v, &v_full[s], 64 * c, h, it * BN, b);
-          used_v[s] = true; par_v[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
+          if (!DOT && it == 0 && !load_do()) { ok = false; break; }        // not needed before the first S
+          if (!mbar_wait(&v_empty[sv], phv ^ 1, &abort_flag)) { ok = false; break; }
+          mbar_arrive_expect_tx(&v_full[sv], NCV * CK);
+          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + (sv * NCV + c) * CK, &mp.v, &v_full[sv], 64 * c, h, it * BN, b);
+          used_v[sv] = true; par_v[sv] = phv;
+          if (++sv == VS) { sv = 0; phv ^= 1; }
         }
         ++li;
       }
       if (!ok) fail();
       if (used_q) mbar_wait(q_full, par_q, nullptr);
-      for (int i = 0; i < kStages; ++i) {
+      if (used_do) mbar_wait(do_full, par_do, nullptr);
+      for (int i = 0; i < kStages; ++i)
         if (used_k[i]) mbar_wait(&k_full[i], par_k[i], nullptr);
+      for (int i = 0; i < VS; ++i)
         if (used_v[i]) mbar_wait(&v_full[i], par_v[i], nullptr);
-      }
     }
   } else if (ROLE == kIssue && warp == 1) {
     // ------------------------------------------------------------ MMA issuer
@@ -890,33 +913,37 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     const uint64_t mk_ = make_sdesc(smem_u32(kbuf), CK, 1024, 2);
     uint32_t t = 0, li = 0, ks = 0, kph = 0, vs = 0, vph = 0, kd = 0;   // tiles, items; stages of S, of dP and of dQ
     bool issued = false;
-    auto scores = [&]() -> bool {          // S = Q K^T
+    auto scores = [&](bool last) -> bool { // S = Q K^T; `last`: Q is free after it
       if (!warp_wait(&k_full[ks], kph, &abort_flag)) return false;
       tc_fence_after();
       const uint64_t k0 = dk_ + ks * (NCH * CK / 16);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCH; ++c)
-          tc_mma_ts(t_s, t_q + c * 8, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+          if (c < 4 * QT) tc_mma_ts(t_s, t_q + c * 8, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+          else tc_mma(t_s, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16, k0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, 1);
         tc_commit(s_full);
+        if (QT < NCH && last) tc_commit(q_empty);
       }
       __syncwarp();
       if (++ks == kStages) { ks = 0; kph ^= 1; }
       return true;
     };
-    auto dprobs = [&]() -> bool {          // dP = dO V^T
+    auto dprobs = [&](bool last) -> bool { // dP = dO V^T; `last`: dO is free after it
       if (!warp_wait(&v_full[vs], vph, &abort_flag)) return false;
       tc_fence_after();
       const uint64_t v0 = dv_ + vs * (NCV * CK / 16);
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 4 * NCV; ++c)
-          tc_mma_ts(t_dp, t_do + c * 8, v0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+          if (DOT) tc_mma_ts(t_dp, t_do + c * 8, v0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
+          else tc_mma(t_dp, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16, v0 + ((c >> 2) * CK + (c & 3) * 32) / 16, idesc_s, c > 0);
         tc_commit(&v_empty[vs]);
         tc_commit(dp_full);
+        if (!DOT && last) tc_commit(do_empty);
       }
       __syncwarp();
-      if (++vs == kStages) { vs = 0; vph ^= 1; }
+      if (++vs == VS) { vs = 0; vph ^= 1; }
       return true;
     };
     for (;; ) {
@@ -928,25 +955,27 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
       // The previous item's S and dP are done and have been read: its last
       // s_empty and ds_full were waited for below.  So its queries may be
       // overwritten.
-      bool ok = warp_wait(q_full, li & 1, &abort_flag);
+      bool ok = warp_wait(q_full, li & 1, &abort_flag) && (!DOT || warp_wait(do_full, li & 1, &abort_flag));
       if (!ok) { fail(); break; }
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 4 * NCH; ++c) tc_cp_128x256b(t_q + c * 8, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
+        for (int c = 0; c < 4 * QT; ++c) tc_cp_128x256b(t_q + c * 8, dq_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
 #pragma unroll
-        for (int c = 0; c < 4 * NCV; ++c) tc_cp_128x256b(t_do + c * 8, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
-        tc_commit(q_empty);
+        for (int c = 0; c < 4 * NCV; ++c)
+          if (DOT) tc_cp_128x256b(t_do + c * 8, ddo_ + ((c >> 2) * CH + (c & 3) * 32) / 16);
+        if (QT == NCH) tc_commit(q_empty);
+        if (DOT) tc_commit(do_empty);
       }
       __syncwarp();
       issued = true;
-      if (!scores() || !dprobs()) { fail(); break; }
+      if (!scores(nt == 1) || !(DOT || warp_wait(do_full, li & 1, &abort_flag)) || !dprobs(nt == 1)) { fail(); break; }
       for (int i = 0; i < nt; ++i, ++t) {
         if (!warp_wait(s_empty, t & 1, &abort_flag)) { ok = false; break; }
-        if (i + 1 < nt && !scores()) { ok = false; break; }
+        if (i + 1 < nt && !scores(i + 2 == nt)) { ok = false; break; }
         if (!warp_wait(ds_full, t & 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (i + 1 < nt && !dprobs()) { ok = false; break; }
+        if (i + 1 < nt && !dprobs(i + 2 == nt)) { ok = false; break; }
         if (i == 0 && !warp_wait(acc_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint64_t k0 = mk_ + kd * (NCH * CK / 16);
@@ -1103,8 +1132,8 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
 // [3, 1021, 5, 80 / 48].)
 //
 // Measured, whole call: 598 us for [4, 4096, 16, 128] causal (1150 TFLOP/s of the
-// formulas' five products, 1610 of the seven executed), 838 us for [1, 4096, 64,
-// 192 / 128] with a shared key, 1425 us for [1, 32768, 2, 192 / 128].  The tensor
+// formulas' five products, 1610 of the seven executed), 835 us for [1, 4096, 64,
+// 192 / 128] with a shared key, 1404 us for [1, 32768, 2, 192 / 128].  The tensor
 // pipe is active 76 % / 69 % of bwd_kernel on the first two: what bounds it is the
 // chain of a tile (product, barrier, S or dP from tensor memory, exponential,
 // P or dS back, barrier, product), which takes 2540 clocks per 128-query tile of
@@ -1117,7 +1146,7 @@ template <int NCH, int NCV>
 constexpr size_t smem_bytes() {
   const size_t nq = query_tile(NCH, NCV), nk = key_tile(NCH, NCV), own = (size_t)(NCH + NCV);
   const size_t kv = own * CH + query_stages(NCH, NCV) * (own * nq * 128 + 2 * nq * 4);
-  const size_t q = own * CH + kKeyStages * own * nk * 128;
+  const size_t q = own * CH + (kKeyStages * NCH + value_stages(NCH, NCV) * NCV) * nk * 128;
   return 1024 + 2 * kBarBytes + (kv > q ? kv : q);      // 1024: alignment
 }
 
@@ -1127,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                const __grid_constant__ Geo g) {
   static_assert(smem_bytes<NCH, NCV>() + 64 <= 227 * 1024, "shared memory");
   static_assert(64 * (NCH + NCV) + 2 * query_tile(NCH, NCV) + (p_apart(NCH, NCV) ? query_tile(NCH, NCV) / 2 : 0) <= 512 &&
-                96 * NCH + 32 * NCV + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
+                64 * NCH + 32 * q_in_tmem(NCH) + (do_in_tmem(NCH) ? 32 * NCV : 0) + 5 * key_tile(NCH, NCV) / 2 <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ volatile int abort_flag;
