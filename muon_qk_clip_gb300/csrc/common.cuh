@@ -87,7 +87,8 @@ cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads,
   c.stream = s;
   c.attrs = at;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kernel, P(args)...);
+  cudaLaunchKernelEx(&c, kernel, P(args)...);
+  return cudaGetLastError();              // and no error left behind for the next caller
 }
 
 // Two fp32 operations in one instruction.
