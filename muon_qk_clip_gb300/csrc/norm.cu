@@ -141,6 +141,29 @@ __device__ inline void mul_all(float (&v)[E], float f) {
   for (int e = 0; e < E; e += 2) untwo(mul2(two(v[e], v[e + 1]), f2), v[e], v[e + 1]);
 }
 
+// v / f for f > 0 (or NaN): with r the rounded reciprocal, v r is at most 1.5 units
+// in the last place off; adding r times the remainder v - (v r) f, which one fused
+// step gives exactly, leaves the quotient's own rounding (Markstein, IBM Journal of
+// Research and Development 34, 1990).  Two more packed steps per pair; the division
+// operator instead takes 40.8 us for 4096 x 7168, this 34.6, the product without the
+// remainder, which gives values next to a tie the neighbouring code, 33.8.
+template <int E>
+__device__ inline void div_all(float (&v)[E], float f) {
+  const float r = __frcp_rn(f), g = -fminf(f, 3.402823466e38f);      // f = inf: v 0, not inf 0
+  const unsigned long long r2 = two(r, r), g2 = two(g, g);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const unsigned long long a = two(v[e], v[e + 1]), q = mul2(a, r2);
+    untwo(fma2(fma2(q, g2, a), r2, q), v[e], v[e + 1]);
+  }
+}
+
+// v / f in the same way for one value and a constant; NaN and infinity stay.
+__device__ inline float div_one(float v, float f) {
+  const float r = 1.f / f, q = v * r;
+  return v <= 3.402823466e38f ? fmaf(fmaf(q, -f, v), r, q) : v;
+}
+
 // e4m3 of a unit's values and the tiles' scales.  A 16-byte bf16 unit covers
 // two tiles (a half-warp each), the others one.
 template <typename T, bool VEC>
@@ -153,10 +176,10 @@ __device__ inline void store_e4m3(uint8_t* y, float* scales, int unit, int lane,
   for (int e = 0; e < U::E; ++e) top = max_nan(top, fabsf(v[e]));
 #pragma unroll
   for (int o = lanes / 2; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float scale = max_nan(top * (1.f / kE4m3Max), kScaleMin);
+  const float scale = max_nan(div_one(top, kE4m3Max), kScaleMin);
   const int tile0 = unit * U::kCols + (lane / lanes) * kTile;
   if (lane % lanes == 0 && tile0 < cols) scales[tile0 / kTile] = scale;
-  mul_all(v, __frcp_rn(scale));
+  div_all(v, scale);
   uint32_t w[(U::E + 3) / 4] = {};
 #pragma unroll
   for (int e = 0; e < U::E; e += 2) {

@@ -384,3 +384,31 @@ def test_norm_and_rope_offsets_past_32_bits():
                            out=torch.empty_like(far).as_strided((1, rows, 3, 128), (0, ld, 128, 1), 0))
     torch.cuda.synchronize()
     assert torch.equal(want, got)
+
+
+@pytest.mark.parametrize("shift,extra", [(0, 24), (3, 5)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_add_rms_norm_e4m3_is_the_rounded_quotient(dtype, shift, extra):
+    """Rows of +-1 with eps = 0 have rstd = 1, so y is +-w exactly: the scale has the
+    bits of the fp32 quotient max|w| / 448 and the codes those of e4m3(w / scale),
+    on weights next to the values where e4m3 changes its code."""
+    tiles, cols = 41, 40 * 128 + 40
+    g = np.random.default_rng(5)
+    top = g.integers(128, 256, tiles) * 2.0 ** g.integers(-110, 3, tiles)
+    tie = (2 * g.integers(8, 16, (tiles, 128)) + 1) * 2.0 ** g.integers(-11, 4, (tiles, 128))
+    w = np.minimum(tie / 448, 1.0) * top[:, None]
+    w[:, 5] = top
+    w[7] = 0
+    w = torch.from_numpy(w.reshape(-1)[:cols]).to(dtype).cuda()
+    x = torch.where(torch.rand(3, cols, device="cuda") < 0.5, -1.0, 1.0).to(dtype)
+    _, vx = pitched(x, extra, shift)
+    y, s, _, rstd = mc.add_rms_norm(vx, weight=w, eps=0.0, out_dtype=F8)
+    torch.cuda.synchronize()
+    assert torch.all(rstd == 1)
+    v = np.zeros(tiles * 128, np.float32)
+    v[:cols] = w.float().cpu().numpy()
+    v = v.reshape(tiles, 128)
+    scale = np.maximum(np.abs(v).max(1) / np.float32(448), np.float32(2.0 ** -100))
+    code = O.round_to_e4m3((v / scale[:, None]).astype(np.float64)).reshape(-1)[:cols]
+    assert scale.dtype == np.float32 and np.array_equal(s.cpu().numpy(), np.broadcast_to(scale, (3, tiles)))
+    assert np.array_equal(y.float().double().cpu().numpy(), f64(x) * code)
