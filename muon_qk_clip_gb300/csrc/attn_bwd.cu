@@ -1237,21 +1237,21 @@ __device__ inline void short_add(float4& a, float x, const float4& b) {
   a.w = fmaf(x, b.w, a.w);
 }
 // Columns c .. c + 3 of a row of `width`, times `scale`, as bf16; true if one is
-// not finite.
+// not finite as stored (the rounding to bf16 may take the largest to infinity).
 __device__ inline bool short_store(__nv_bfloat16* row, int c, int width, const float4& v, float scale) {
-  const float e[4] = {v.x * scale, v.y * scale, v.z * scale, v.w * scale};
-  float z = 0.f;
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 lo = __floats2bfloat162_rn(v.x * scale, v.y * scale), hi = __floats2bfloat162_rn(v.z * scale, v.w * scale);
   if (c + 4 <= width) {
-    *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]));
-  } else {
-#pragma unroll
-    for (int y = 0; y < 3; ++y)
-      if (c + y < width) row[c + y] = __float2bfloat16_rn(e[y]);
+    *reinterpret_cast<uint2*>(row + c) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {                               // columns behind the row do not count
+    if (c < width) row[c] = lo.x; else lo.x = zero.x;
+    if (c + 1 < width) row[c + 1] = lo.y; else lo.y = zero.x;
+    if (c + 2 < width) row[c + 2] = hi.x; else hi.x = zero.x;
+    hi.y = zero.x;
   }
-#pragma unroll
-  for (int y = 0; y < 4; ++y)
-    if (c + y < width) z = fmaf(e[y], 0.f, z);
-  return z != z;
+  const __nv_bfloat162 z = __hfma2(hi, zero, __hmul2(lo, zero));    // zeros, or NaN where a value is not finite
+  return __low2float(z) != 0.f || __high2float(z) != 0.f;
 }
 
 __global__ void __launch_bounds__(kShortThreads, 4) short_kernel(const __grid_constant__ AttnBwdParams p) {
@@ -1409,13 +1409,9 @@ __global__ void __launch_bounds__(kSharedThreads) shared_kernel(const __grid_con
   }
   for (; h < p.H; ++h) add(src[h * per]);
   const int j = (int)(e / quads), c = 4 * (int)(e - (long long)j * quads);
-  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.dksh) + b * p.dkshs[0] + j * p.dkshs[1] + c;
-  if (c + 4 <= p.d_shared) {
-    *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
-  } else {
-    const float v[3] = {s.x, s.y, s.z};
-    for (int y = 0; c + y < p.d_shared; ++y) to[y] = __float2bfloat16_rn(v[y]);
-  }
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.dksh) + b * p.dkshs[0] + j * p.dkshs[1];
+  // finite parts may have a sum that is not
+  if (short_store(to, c, p.d_shared, s, 1.f)) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,

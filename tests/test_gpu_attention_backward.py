@@ -399,3 +399,45 @@ def test_attention_backward_on_two_streams_at_once():
         torch.cuda.synchronize()
         for w, g in zip(want, got):
             assert all(torch.equal(x, y) for x, y in zip(w[:3], g[:3]))
+
+
+def lone_query(S, q_shared, do, v, lse):
+    """[1, S, 2, 64 + 16 / 64] where only query 0 and key 0 meet values: logits are 0,
+    p_00 = exp(-lse), ds_00 = p do v, dv_0 = p do and, per head, the shared key's
+    gradient (scale 1) is ds_00 q_shared in its first column; the rest is 0."""
+    q, do_ = torch.zeros(1, S, 2, 80), torch.zeros(1, S, 2, 64)
+    v_, zero = torch.zeros(1, S, 2, 64), torch.zeros(1, S, 2, 64)
+    q[0, 0, :, 64] = torch.tensor(q_shared)
+    do_[0, 0, :, 3] = do
+    v_[0, 0, :, 3] = v
+    q, do_, v_, zero = (t.to(BF16).cuda() for t in (q, do_, v_, zero))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ks, lse = torch.zeros(1, S, 16, dtype=BF16, device="cuda"), torch.full((1, 2, S), lse, device="cuda")
+    got = mc.qk_attention_backward(q, zero, v_, zero, lse, do_, k_shared=ks, scale=1.0, status=st)
+    torch.cuda.synchronize()
+    return got, st.item()
+
+
+BIG = 2.0 ** 64
+
+
+@pytest.mark.parametrize("S", [1, 3, 40])
+@pytest.mark.parametrize("q_shared", [[BIG, BIG], [BIG, BIG * (1 - 2.0 ** -8)]])
+def test_attention_backward_flags_a_shared_key_sum_that_overflows(S, q_shared):
+    """Heads whose parts are finite (up to 2^127) with a sum beyond fp32, or beyond
+    what rounds to a finite bf16: dk_shared is infinite and the status says so."""
+    (dq, dk, dv, dks), st = lone_query(S, q_shared, 2.0 ** 33, 2.0 ** 30, 0.0)
+    assert torch.isinf(dks[0, 0, 0]) and torch.isfinite(dks[0, :, 1:]).all()
+    assert all(torch.isfinite(t).all() for t in (dq, dk, dv))
+    assert st & abi.MC_STATUS_NONFINITE_UPDATE
+    (_, _, _, dks), st = lone_query(S, [BIG, -BIG], 2.0 ** 33, 2.0 ** 30, 0.0)
+    assert st == 0 and not dks.any()                   # parts that cancel
+
+
+@pytest.mark.parametrize("S", [1, 16])
+def test_attention_backward_flags_values_that_round_to_infinity(S):
+    """dv_0 = 1.003 times bf16's largest value: finite in fp32, infinite as stored."""
+    (dq, dk, dv, dks), st = lone_query(S, [1.0, 1.0], torch.finfo(BF16).max, 0.0, -0.003)
+    assert torch.isinf(dv[0, 0, :, 3]).all() and st & abi.MC_STATUS_NONFINITE_UPDATE
+    (_, _, dv, _), st = lone_query(S, [1.0, 1.0], torch.finfo(BF16).max, 0.0, 0.01)
+    assert torch.isfinite(dv).all() and st == 0
