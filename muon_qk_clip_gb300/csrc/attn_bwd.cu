@@ -1208,7 +1208,7 @@ constexpr int kShortThreads = 128;       // at most: a warp per four rows, a thr
 constexpr int kShortPitch = 20;          // of P and dS: rows of 16-byte alignment
 // Row pitch of `width` columns: whole 16 bytes, an odd number of them, so that 8
 // lanes that read 16 bytes of 8 rows meet no bank twice.
-__host__ __device__ inline int short_pitch(int width) { return 4 * (((width + 3) / 4) | 1); }
+__host__ __device__ constexpr int short_pitch(int width) { return 4 * (((width + 3) / 4) | 1); }
 
 // Columns c .. c + 7 of a row of `width`, zeros behind it; and these as fp32 in
 // shared memory, up to a multiple of four columns.
@@ -1512,7 +1512,10 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   if (p.S <= kAttnBwdShort) {
     const int pd = short_pitch(p.d_head + p.d_shared), pv = short_pitch(p.d_v);
     const size_t smem = (size_t)p.S * (2 * pd + 3 * pv + 2 * kShortPitch) * 4;
-    cudaError_t e = cudaFuncSetAttribute(short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit belongs to the kernel, not to this call: always that of the largest,
+    // so that another thread's call cannot lower it before this launch
+    constexpr int most = kAttnBwdShort * (2 * short_pitch(192) + 3 * short_pitch(128) + 2 * kShortPitch) * 4;
+    cudaError_t e = cudaFuncSetAttribute(short_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     const int width = p.d_head + p.d_shared > p.d_v ? p.d_head + p.d_shared : p.d_v;
     const int want = p.S * (width > 64 ? (width + 7) / 8 : 8);       // 8 S: a warp per four rows

@@ -1,0 +1,88 @@
+"""Calls from several host threads at once, each on a stream of its own: the C
+entries keep nothing of a call that another one could change, so every call
+succeeds and has the bits of the call alone.
+
+A pair of threads runs shapes that need different amounts of shared memory, as
+prepared C calls (ctypes leaves the interpreter's lock during them).
+"""
+import ctypes
+import threading
+
+import pytest
+import torch
+
+from muon_qk_clip_gb300 import abi, build
+from muon_qk_clip_gb300 import binding as mc
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+CALLS = 3000                               # per thread
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    abi.load()
+
+
+def mk(*shape, dtype=BF16):
+    return torch.randn(*shape, device="cuda").to(dtype)
+
+
+def attention(S, dh, dv):
+    """q, k, v, out, lse, do of 2 x S positions and 3 heads."""
+    q, k, v, do = mk(2, S, 3, dh), mk(2, S, 3, dh), mk(2, S, 3, dv), mk(2, S, 3, dv)
+    out, lse, _ = mc.qk_attention_forward(q, k, v, lse=True)
+    return q, k, v, out, lse, do
+
+
+def backward_call(S, dh, dv):
+    a = attention(S, dh, dv)
+    outs = [torch.empty_like(t) for t in a[:3]]
+    ws = torch.empty(mc.attention_backward_workspace_size(a[0], a[1]), dtype=torch.uint8, device="cuda")
+    got, real = [], mc._run
+    mc._run = lambda fn, name, index, *args: got.append((fn, args))
+    try:
+        mc.qk_attention_backward(*a, dq=outs[0], dk=outs[1], dv=outs[2], workspace=ws)
+    finally:
+        mc._run = real
+    fn, args = got[0]
+    return (lambda stream: fn(*args, stream)), outs, (a, ws)
+
+
+def run_at_once(*calls):
+    """Every call CALLS times from its own thread; their codes that are not MC_OK."""
+    want, codes = [], []
+    for call, outs, _ in calls:
+        assert call(torch.cuda.current_stream().cuda_stream) == abi.MC_OK
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in outs])
+        for t in outs:
+            t.fill_(7)
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(calls))
+
+    def work(call, stream):
+        start.wait()
+        for n in range(CALLS):
+            code = call(stream.cuda_stream)
+            if code != abi.MC_OK:
+                codes.append((code, abi.load().mc_last_error().decode()))
+            if n % 100 == 99:
+                stream.synchronize()
+
+    streams = [torch.cuda.Stream() for _ in calls]
+    threads = [threading.Thread(target=work, args=(c[0], s)) for c, s in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not codes, (len(codes), codes[0])
+    for (_, outs, _), w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(outs, w))
+
+
+def test_short_attention_backward_from_two_threads():
+    run_at_once(backward_call(16, 192, 128), backward_call(2, 16, 16))
