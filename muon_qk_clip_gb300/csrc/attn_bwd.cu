@@ -1443,9 +1443,11 @@ bool encode(CUtensorMap* m, const void* base, int width, int H, int S, int B, co
     by[0] = (cuuint64_t)st[1] * 2; by[1] = (cuuint64_t)st[0] * 2;
     box[1] = (cuuint32_t)rows; box[2] = 1;
   }
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, by, box, es,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encode_bound([&] {
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, by, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  });
 }
 
 bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {

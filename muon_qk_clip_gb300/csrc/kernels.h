@@ -12,6 +12,16 @@ namespace mc {
 inline constexpr int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline constexpr int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
+// The driver encodes a tensor map in the calling thread's context, and a host thread
+// whose first use of CUDA this is has none until a call of the runtime binds one.
+// Encodes once more after binding it: `encode` returns a CUresult.
+template <typename F>
+bool encode_bound(F encode) {
+  if (encode() == CUDA_SUCCESS) return true;
+  int device;
+  return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && encode() == CUDA_SUCCESS;
+}
+
 // Whether every element of a strided array (n <= 3 axes, `width` contiguous
 // elements under them) has an address of its own.  Axes of one element may have
 // any stride.

@@ -51,6 +51,16 @@ def backward_call(S, dh, dv):
     return (lambda stream: fn(*args, stream)), outs, (a, ws)
 
 
+def forward_call(S, dh, dv):
+    q, k, v, out, lse, _ = attention(S, dh, dv)
+    smax, o, d = torch.empty(3, device="cuda"), abi.McAttnOut(), mc.attn_desc(q, k)
+    o.v, o.d_v, o.o, o.lse = v.data_ptr(), dv, out.data_ptr(), lse.data_ptr()
+    o.v_strides[:], o.o_strides[:] = v.stride()[:3], out.stride()[:3]
+    fn = abi.load().qk_attention_forward
+    call = lambda stream: fn(ctypes.byref(d), ctypes.byref(o), smax.data_ptr(), 0, None, stream)  # noqa: E731
+    return call, [out, lse, smax], (q, k, v)
+
+
 def run_at_once(*calls):
     """Every call CALLS times from its own thread; their codes that are not MC_OK."""
     want, codes = [], []
@@ -86,3 +96,39 @@ def run_at_once(*calls):
 
 def test_short_attention_backward_from_two_threads():
     run_at_once(backward_call(16, 192, 128), backward_call(2, 16, 16))
+
+
+def test_attention_backward_of_all_lengths_from_threads():
+    run_at_once(backward_call(40, 192, 128), backward_call(16, 128, 128), backward_call(40, 64, 64))
+
+
+def first_of_a_thread(call):
+    """The code of a prepared call that is the first use of CUDA in its thread."""
+    codes, stream = [], torch.cuda.current_stream().cuda_stream
+    t = threading.Thread(target=lambda: codes.append((call(stream), abi.load().mc_last_error().decode())))
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    return codes[0]
+
+
+@pytest.mark.parametrize("S", [40, 16])
+def test_attention_calls_as_the_first_of_a_thread(S):
+    """A thread that has not used CUDA yet has no context until a call binds one."""
+    for call, outs, _ in (backward_call(S, 64, 64), forward_call(S, 64, 64)):
+        assert call(torch.cuda.current_stream().cuda_stream) == abi.MC_OK
+        want = [t.clone() for t in outs]
+        for t in outs:
+            t.fill_(7)
+        torch.cuda.synchronize()
+        assert first_of_a_thread(call) == (abi.MC_OK, "")
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+def test_an_accumulating_max_logit_as_the_first_call_of_a_thread():
+    q, k = mk(2, 40, 3, 64), mk(2, 40, 3, 64)
+    want, smax, d = mc.qk_max_logit(q, k)[0], torch.full((3,), -1e30, device="cuda"), mc.attn_desc(q, k)
+    torch.cuda.synchronize()
+    fn = abi.load().qk_max_logit
+    assert first_of_a_thread(lambda s: fn(ctypes.byref(d), smax.data_ptr(), None, 1, None, s)) == (abi.MC_OK, "")
+    assert torch.equal(smax, want)
