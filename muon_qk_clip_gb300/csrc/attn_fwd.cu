@@ -47,6 +47,7 @@ constexpr int CH = 128 * 64 * 2;         // one 128-row x 64-feature bf16 chunk 
 constexpr uint32_t kTmemCols = 512;      // S x 2 (cols 0, 128), O (cols 256 ..)
 constexpr uint32_t kOCol = 256;
 constexpr int kMaxStages = 2;
+constexpr int kMaxSmem = 227 * 1024 - 2 * 2 * BM * 4 - 64;   // beside the static red and abort flag
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.f;             // rescale O when the max grows by more than 2^8
@@ -543,7 +544,7 @@ bool geometry(const AttnFwdParams& p, Geo& g, size_t& smem, char* err, size_t er
   g.units = (uint32_t)units;
   g.div_nunit = make_fastdiv((uint32_t)g.nunit);
   g.div_h = make_fastdiv((uint32_t)p.H);
-  const size_t cap = 227 * 1024 - 1024 - 256 - 2 * 2 * BM * 4 - 64;   // static: red, abort flag
+  const size_t cap = kMaxSmem - 1024 - 256;
   const size_t fixed = (size_t)(g.nch + 2) * CH;      // Q, P
   g.kst = g.vst = 0;
   for (int ks = kMaxStages; ks >= 1 && !g.kst; --ks)
@@ -633,7 +634,9 @@ cudaError_t launch_attn_fwd(const AttnFwdParams& p, cudaStream_t s, char* err, s
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  e = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit belongs to the kernel, not to this call: always the largest, so that
+  // another thread's call cannot lower it before this launch
+  e = cudaFuncSetAttribute(attn_fwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
   if (e != cudaSuccess) return e;
   const int grid = (int)(g.units < (uint32_t)sm_count() ? g.units : (uint32_t)sm_count());
   attn_fwd_kernel<<<grid, kThreads, smem, s>>>(p, mp, g);

@@ -102,6 +102,10 @@ def test_attention_backward_of_all_lengths_from_threads():
     run_at_once(backward_call(40, 192, 128), backward_call(16, 128, 128), backward_call(40, 64, 64))
 
 
+def test_attention_forward_from_two_threads():
+    run_at_once(forward_call(40, 128, 128), forward_call(40, 64, 32))
+
+
 def first_of_a_thread(call):
     """The code of a prepared call that is the first use of CUDA in its thread."""
     codes, stream = [], torch.cuda.current_stream().cuda_stream
