@@ -616,15 +616,12 @@ cudaError_t launch_max_logit(const MaxLogitParams& p, cudaStream_t s, char* err,
   const int nib = (p.S + kT - 1) / kT;
   const long long items = (long long)p.B * p.H * nib;
   const int grid = (int)(items < (long long)sm_count() * 4 ? items : sm_count() * 4);
-  if (p.dtype == MC_BF16) {
-    cudaFuncSetAttribute(ml_simt_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem);
-    ml_simt_kernel<__nv_bfloat16><<<grid, 256, smem, s>>>(p);
-  } else {
-    cudaFuncSetAttribute(ml_simt_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                         (int)smem);
-    ml_simt_kernel<float><<<grid, 256, smem, s>>>(p);
-  }
+  const auto kernel = p.dtype == MC_BF16 ? ml_simt_kernel<__nv_bfloat16> : ml_simt_kernel<float>;
+  // the limit belongs to the kernel, not to this call: always that of 256 features
+  // (the most), so that another thread's call cannot lower it before this launch
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * 256 * (kT + 1) * (int)sizeof(float));
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 256, smem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (p.argmax) ml_final_kernel<<<hb, 128, 0, s>>>(p);

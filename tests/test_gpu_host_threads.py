@@ -61,6 +61,15 @@ def forward_call(S, dh, dv):
     return call, [out, lse, smax], (q, k, v)
 
 
+def max_logit_call(S, dh, dtype, argmax):
+    q, k = mk(2, S, 3, dh, dtype=dtype), mk(2, S, 3, dh, dtype=dtype)
+    smax, d = torch.empty(3, device="cuda"), mc.attn_desc(q, k)
+    where = torch.empty(3, dtype=torch.int64, device="cuda") if argmax else None
+    fn = abi.load().qk_max_logit
+    call = lambda stream: fn(ctypes.byref(d), smax.data_ptr(), mc._at(where), 0, None, stream)  # noqa: E731
+    return call, [smax] + ([where] if argmax else []), (q, k)
+
+
 def run_at_once(*calls):
     """Every call CALLS times from its own thread; their codes that are not MC_OK."""
     want, codes = [], []
@@ -104,6 +113,18 @@ def test_attention_backward_of_all_lengths_from_threads():
 
 def test_attention_forward_from_two_threads():
     run_at_once(forward_call(40, 128, 128), forward_call(40, 64, 32))
+
+
+def test_max_logit_from_two_threads():
+    run_at_once(max_logit_call(40, 192, BF16, True), max_logit_call(40, 64, BF16, True))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_max_logit_on_cuda_cores_from_two_threads(dtype):
+    """Lengths of q.k that the tensor cores do not take (bf16: 12 features, or a
+    narrow view of wider rows)."""
+    wide = 250 if dtype == BF16 else 256
+    run_at_once(max_logit_call(40, wide, dtype, False), max_logit_call(40, 12, dtype, False))
 
 
 def first_of_a_thread(call):
