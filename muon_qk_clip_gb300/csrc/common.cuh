@@ -74,7 +74,9 @@ __device__ inline uint32_t smem_u32(const void* p) {
 __device__ inline void await_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ inline void release_next() { asm volatile("griddepcontrol.launch_dependents;"); }
 
-// Launches a kernel that calls await_previous().
+// Launches a kernel that calls await_previous().  The code is the launch's own: an
+// error that an earlier call of the program left in the runtime stays for it to
+// fetch, one of the launch's does not stay for the next caller.
 template <typename... P, typename... A>
 cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s, A... args) {
   cudaLaunchAttribute at[1];
@@ -87,8 +89,9 @@ cudaError_t launch_behind(void (*kernel)(P...), unsigned grid, unsigned threads,
   c.stream = s;
   c.attrs = at;
   c.numAttrs = 1;
-  cudaLaunchKernelEx(&c, kernel, P(args)...);
-  return cudaGetLastError();              // and no error left behind for the next caller
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, P(args)...);
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
 }
 
 // Two fp32 operations in one instruction.

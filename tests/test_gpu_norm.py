@@ -16,6 +16,8 @@ Bounds (w = 2^-24, u = half a step of the stored type relative: 2^-24 fp32,
   * rotary gradient: angles within half a turn rounded to fp32 (pi w), sines to
     2 ulp, one product and one fma: 8 w (|a| + |b|), u of the result
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -412,3 +414,26 @@ def test_add_rms_norm_e4m3_is_the_rounded_quotient(dtype, shift, extra):
     code = O.round_to_e4m3((v / scale[:, None]).astype(np.float64)).reshape(-1)[:cols]
     assert scale.dtype == np.float32 and np.array_equal(s.cpu().numpy(), np.broadcast_to(scale, (3, tiles)))
     assert np.array_equal(y.float().double().cpu().numpy(), f64(x) * code)
+
+
+def test_an_older_error_of_the_runtime_is_not_the_calls_own():
+    """A runtime call of the program's own has failed and left its error to be
+    fetched: a launch that succeeds says so, and leaves that error where it was."""
+    cudart = ctypes.CDLL("libcudart.so.13")
+    x, dy = normal((5, 640), 1.0, "er", F32), normal((5, 640), 0.1, "ed", F32)
+    y, _, _, rstd = mc.add_rms_norm(x)
+    dx = mc.rms_norm_backward(dy, x, rstd)[0]
+    out, r2, dx2, rx = torch.empty_like(x), torch.empty_like(rstd), torch.empty_like(x), torch.empty_like(x)
+    torch.cuda.synchronize()
+    assert cudart.cudaSetDevice(1 << 20) != 0
+    try:
+        pending = cudart.cudaPeekAtLastError()
+        mc.add_rms_norm(x, out=out, rstd=r2)
+        mc.rms_norm_backward(dy, x, rstd, dx=dx2)
+        mc.rope_backward(dy.view(1, 5, 10, 64), out=rx.view(1, 5, 10, 64))
+        assert pending != 0 and cudart.cudaPeekAtLastError() == pending
+    finally:
+        cudart.cudaGetLastError()
+    torch.cuda.synchronize()
+    assert torch.equal(out, y) and torch.equal(r2, rstd) and torch.equal(dx2, dx)
+    assert torch.equal(rx.view(1, 5, 10, 64), mc.rope_backward(dy.view(1, 5, 10, 64)))
