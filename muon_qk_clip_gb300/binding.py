@@ -266,7 +266,8 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
     k_shared [B,S,dr] or None, v, out and dout [B,S,H,dv] (bf16, contiguous
     feature axes), lse [B,H,S] f32 as the forward returned it; causal and scale
     as in the forward.  Returns (dq, dk, dv, dk_shared or None); outputs are
-    allocated unless given (any strides the features may have).  workspace: a
+    allocated unless given (any strides the features may have): contiguous, or,
+    of a width that is no multiple of eight, in rows padded to one.  workspace: a
     contiguous CUDA tensor of attention_backward_workspace_size bytes; without one,
     one is allocated for the call.  stream: what is allocated here belongs to it;
     other tensors used on it are the caller's to order and keep."""
@@ -313,9 +314,13 @@ def qk_attention_backward(q, k, v, out, lse, dout, k_shared=None, causal=True, s
 
 
 def _grad_like(name, g, like):
-    """The given gradient tensor, checked, or a new one of `like`'s shape."""
+    """The given gradient tensor, checked, or a new one of `like`'s shape, its rows
+    padded to a multiple of eight features (which the library's strides must be)."""
     if g is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        shape = like.shape
+        if shape[-1] % 8:
+            return torch.empty(*shape[:-1], -shape[-1] // 8 * -8, dtype=like.dtype, device=like.device)[..., :shape[-1]]
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
     if g.shape != like.shape or g.stride(-1) != 1 or g.dtype != like.dtype:
         raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
     return g

@@ -441,3 +441,22 @@ def test_attention_backward_flags_values_that_round_to_infinity(S):
     assert torch.isinf(dv[0, 0, :, 3]).all() and st & abi.MC_STATUS_NONFINITE_UPDATE
     (_, _, dv, _), st = lone_query(S, [1.0, 1.0], torch.finfo(BF16).max, 0.0, 0.01)
     assert torch.isfinite(dv).all() and st == 0
+
+
+@pytest.mark.parametrize("B,S,H,dh,dr,dv", [(2, 131, 3, 20, 0, 50), (1, 150, 2, 64, 12, 33), (2, 9, 3, 64, 5, 17)])
+def test_attention_backward_allocates_odd_widths(B, S, H, dh, dr, dv):
+    """Widths that are no multiple of eight, in inputs whose rows are padded to one:
+    the outputs that the call allocates itself are as good as given ones."""
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, dv, 102)
+    ref, tol = bounds(q, k, ks, v, do, o, lse, True)
+
+    def wide(t):
+        if t is None:
+            return None
+        big = torch.full((*t.shape[:-1], (t.shape[-1] + 7) // 8 * 8), float("nan"), dtype=BF16, device="cuda")
+        big[..., :t.shape[-1]] = t.cuda()
+        return big[..., :t.shape[-1]]
+    got = mc.qk_attention_backward(*(wide(t) for t in (q, k, v, o)), lse.cuda(), wide(do), k_shared=wide(ks))
+    torch.cuda.synchronize()
+    assert all(g is None or g.shape == t.shape for g, t in zip(got, (q, k, v, ks)))
+    check(got, ref, tol)
