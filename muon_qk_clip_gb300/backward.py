@@ -53,7 +53,11 @@ def _weight(dy, x, status):
 
 def project_mha_backward(X, Wq, Wk, dq, dk, status=None):
     """Of project_mha: dq, dk [B, S, H, d] to (dWq, dWk, dX)."""
-    _on_device(X, Wq, Wk, dq, dk)
+    with _on_device(X, Wq, Wk, dq, dk):
+        return _mha(X, Wq, Wk, dq, dk, status)
+
+
+def _mha(X, Wq, Wk, dq, dk, status):
     B, S, D = X.shape
     x2 = X.reshape(B * S, D)
     dq2, dk2 = dq.reshape(B * S, -1), dk.reshape(B * S, -1)
@@ -69,7 +73,11 @@ def project_mla_backward(X, W, H: int, dq, dk, dkr, dv=None, d_nope=128, d_rope=
     qk_attention_backward gives it) and dv [B,S,H,d_v] (None: zero) to
     ({name: dW}, dX) for W_DQ, W_UQ, W_DKV, W_UKV and W_KR.  The latents are
     recomputed from X.  No gradient is overwritten."""
-    _on_device(X, dq, dk, dkr, *W.values(), *(() if dv is None else (dv,)))
+    with _on_device(X, dq, dk, dkr, *W.values(), *(() if dv is None else (dv,))):
+        return _mla(X, W, H, dq, dk, dkr, dv, d_nope, d_rope, d_v, eps, theta, status)
+
+
+def _mla(X, W, H, dq, dk, dkr, dv, d_nope, d_rope, d_v, eps, theta, status):
     B, S, D = X.shape
     T = B * S
     x2 = X.reshape(T, D)

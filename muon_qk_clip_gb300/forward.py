@@ -9,18 +9,29 @@ training, S_max comes from the forward pass.  Device tensors only.
 """
 from __future__ import annotations
 
+import torch
+
 from . import binding as mc
 
 
 def _on_device(*ts):
+    """The context of the one device that the tensors are on, which need not be the
+    current one."""
     for t in ts:
         if t.device.type != "cuda":
             raise ValueError("the projection runs on the library's CUDA kernels: pass device tensors")
+        if t.device != ts[0].device:
+            raise ValueError(f"every tensor must be on one device; these are on {ts[0].device} and {t.device}")
+    return torch.cuda.device(ts[0].device)
 
 
 def project_mha(X, Wq, Wk, H: int):
     """Q = X Wq^T, K = X Wk^T as [B, S, H, d] views (fp32 accumulate, X dtype out)."""
-    _on_device(X, Wq, Wk)
+    with _on_device(X, Wq, Wk):
+        return _mha(X, Wq, Wk, H)
+
+
+def _mha(X, Wq, Wk, H):
     B, S, D = X.shape
     x2 = X.reshape(B * S, D)
     q = mc.matmul(x2, Wq.contiguous())
@@ -35,7 +46,11 @@ def project_mla(X, W, H: int, d_nope=128, d_rope=64, d_v=128, with_v=False):
     with_v adds the values V, the other strided view [B,S,H,d_v] of that
     projection.  The latents c_Q = RMSNorm(X W_DQ^T) and c_KV =
     RMSNorm(X W_DKV^T) are rounded to X's dtype before their up-projections."""
-    _on_device(X, *W.values())
+    with _on_device(X, *W.values()):
+        return _mla(X, W, H, d_nope, d_rope, d_v, with_v)
+
+
+def _mla(X, W, H, d_nope, d_rope, d_v, with_v):
     B, S, D = X.shape
     x2 = X.reshape(B * S, D)
     cq = mc.rms_norm(mc.matmul(x2, W["W_DQ"].contiguous()))

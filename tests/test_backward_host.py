@@ -351,3 +351,17 @@ def test_descriptor_scale_beyond_fp32_is_left_to_the_library(lib):
     assert d.scale == float("inf")
     d.q, d.k = FAKE, FAKE + STEP
     assert call(lib, d, grad()) == INV and "scale" in lib.mc_last_error().decode()
+
+
+def test_projections_run_on_their_tensors_device():
+    """The projections and their gradients launch on the device that their tensors
+    are on, whichever is current, and refuse tensors of several devices."""
+    from types import SimpleNamespace
+
+    from muon_qk_clip_gb300 import forward
+    on = lambda name: SimpleNamespace(device=torch.device(name))  # noqa: E731
+    assert forward._on_device(on("cuda:1"), on("cuda:1")).idx == 1
+    with pytest.raises(ValueError, match="one device"):
+        forward._on_device(on("cuda:0"), on("cuda:1"))
+    with pytest.raises(ValueError, match="device tensors"):
+        forward._on_device(on("cuda:0"), on("cpu"))
