@@ -460,3 +460,19 @@ def test_attention_backward_allocates_odd_widths(B, S, H, dh, dr, dv):
     torch.cuda.synchronize()
     assert all(g is None or g.shape == t.shape for g, t in zip(got, (q, k, v, ks)))
     check(got, ref, tol)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("B,S,H,dr", [(1, 129, 257, 0), (3, 140, 100, 0), (3, 600, 35, 8)])
+def test_attention_backward_with_a_ragged_last_group_of_items(B, S, H, dr, causal):
+    """More (batch, head) pairs than a group of the work order takes (512 / blocks),
+    and not a multiple of it: 256 + 1, 256 + 44 and 102 + 3."""
+    dh = 64 if dr else 16
+    q, k, ks, v, do, o, lse = inputs(B, S, H, dh, dr, 16, 160 + S, causal)
+    ref, tol = bounds(q, k, ks, v, do, o, lse, causal)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, ks, v, do, o, lse = dev(q, k, ks, v, do, o, lse)
+    got = mc.qk_attention_backward(q, k, v, o, lse, do, k_shared=ks, causal=causal, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check(got, ref, tol)

@@ -437,3 +437,19 @@ def test_an_older_error_of_the_runtime_is_not_the_calls_own():
     torch.cuda.synchronize()
     assert torch.equal(out, y) and torch.equal(r2, rstd) and torch.equal(dx2, dx)
     assert torch.equal(rx.view(1, 5, 10, 64), mc.rope_backward(dy.view(1, 5, 10, 64)))
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(700, 7168, BF16), (613, 8200, BF16), (650, 7167, BF16), (613, 2100, F32),
+                                             (700, 7168, F32)])
+def test_rms_norm_backward_of_wide_rows_over_many_rows(rows, cols, dtype):
+    """Rows wider than a block's registers hold, several to every block: the
+    weight's sums are carried from row to row."""
+    h, dy = normal((rows, cols), 3.0, "wh", dtype), normal((rows, cols), 0.01, "wd", dtype)
+    dres = normal((rows, cols), 0.01, "wr", dtype)
+    w = (1 + normal((cols,), 0.2, "ww", F32)).to(dtype)
+    rstd = torch.rsqrt(h.float().square().mean(1) + EPS)
+    dx, dw = mc.rms_norm_backward(dy, h, rstd, weight=w, dres=dres)
+    torch.cuda.synchronize()
+    check_back(dy, h, rstd, w, dres, dx, dw)
+    again = mc.rms_norm_backward(dy, h, rstd, weight=w, dres=dres, dx=dres)      # in place
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
