@@ -14,11 +14,13 @@ inline constexpr int64_t round_up(int64_t a, int64_t b) { return cdiv(a, b) * b;
 
 // The driver encodes a tensor map in the calling thread's context, and a host thread
 // whose first use of CUDA this is has none until a call of the runtime binds one.
-// Encodes once more after binding it: `encode` returns a CUresult.
+// Encodes once more after binding it, if that is what was missing: `encode` returns
+// a CUresult.
 template <typename F>
 bool encode_bound(F encode) {
-  if (encode() == CUDA_SUCCESS) return true;
+  const CUresult r = encode();
   int device;
+  if (r != CUDA_ERROR_INVALID_CONTEXT && r != CUDA_ERROR_NOT_INITIALIZED) return r == CUDA_SUCCESS;
   return cudaGetDevice(&device) == cudaSuccess && cudaSetDevice(device) == cudaSuccess && encode() == CUDA_SUCCESS;
 }
 
