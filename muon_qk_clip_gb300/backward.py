@@ -72,7 +72,9 @@ def project_mla_backward(X, W, H: int, dq, dk, dkr, dv=None, d_nope=128, d_rope=
     [B,S,d_rope] (of the shared rotary key, summed over the heads as
     qk_attention_backward gives it) and dv [B,S,H,d_v] (None: zero) to
     ({name: dW}, dX) for W_DQ, W_UQ, W_DKV, W_UKV and W_KR.  The latents are
-    recomputed from X.  No gradient is overwritten."""
+    recomputed from X; their norm's sums run in another order than project_mla's,
+    so a value next to a rounding border may differ from the forward's in its last
+    bit.  No gradient is overwritten."""
     with _on_device(X, dq, dk, dkr, *W.values(), *(() if dv is None else (dv,))):
         return _mla(X, W, H, dq, dk, dkr, dv, d_nope, d_rope, d_v, eps, theta, status)
 

@@ -19,8 +19,7 @@
 //   shared_kernel   the shared key's gradient, summed over the heads in order
 // Two passes recompute S and dP (7 products for the 5 that the formulas need),
 // but dQ never leaves the chip as partial sums: one pass would add a 128 x D
-// fp32 tile to global memory per tile pair and hold dQ, dK, dV, S and dP in
-// tensor memory at once (640 or more of its 512 columns).
+// fp32 tile to global memory per tile pair, in an order that changes the bits.
 //
 // P and dS go from the compute warps to the tensor core through tensor memory
 // (the A operand of dV, dK and dQ), written over the columns of the S / dP that
@@ -387,9 +386,12 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
 // Per query tile t the tensor core gets dV(t), S(t+1), dK(t), dP(t+1) (S(t+1)
 // before dV(t) where P^T is apart: then S(t) need only have been read).  It runs
 // the first two while the compute warps turn dP(t) into dS(t), the others while
-// they turn S(t+1) into P(t+1).  The products of one issuing thread execute in
-// order, so S(t+1) follows dV(t)'s reads of P(t), and dP(t+1) dK(t)'s of dS(t),
-// without a wait.
+// they turn S(t+1) into P(t+1).  S(t+1) overwrites P(t) behind dV(t)'s reads of it,
+// and dP(t+1) dS(t) behind dK(t)'s, without a wait: the tensor core executes the
+// products that one thread issues in their order.  That is how this hardware is
+// seen to behave (equal bits on every run, gradients within bounds that a read of
+// an overwritten P would break), not what PTX promises: its ordered pairs of
+// tcgen05.mma have one accumulator and one shape.  The dQ pass does not rest on it.
 //
 // The compute warps read S^T and dP^T in the 16 x 256-bit shape (a thread: 4 keys
 // x a quarter of the queries): a row value per query then takes 8 bytes per two
@@ -1131,8 +1133,8 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
 // two launches: 623 us instead of 614 on dense_block, 45 instead of 39 on
 // [3, 1021, 5, 80 / 48].)
 //
-// Measured, whole call: 598 us for [4, 4096, 16, 128] causal (1150 TFLOP/s of the
-// formulas' five products, 1610 of the seven executed), 835 us for [1, 4096, 64,
+// Measured, whole call: 594 us for [4, 4096, 16, 128] causal (1157 TFLOP/s of the
+// formulas' five products, 1620 of the seven executed), 835 us for [1, 4096, 64,
 // 192 / 128] with a shared key, 1404 us for [1, 32768, 2, 192 / 128].  The tensor
 // pipe is active 76 % / 69 % of bwd_kernel on the first two: what bounds it is the
 // chain of a tile (product, barrier, S or dP from tensor memory, exponential,
@@ -1200,8 +1202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 //
 // Up to 16 positions this beats the tensor cores' 128-row tiles with few sequences
 // and with many (us, against the kernels above; H = 16 or 4, d = 128): 8 of 4
-// positions 8.2 (16.4), 8 of 16 10.2 (18.4), 8192 of 2 33 (309), of 8 94 (313), of
-// 16 145 (315).  With 32 positions, eight warps and the same layout it lost with
+// positions 8.2 (16.4), 8 of 16 10.2 (18.4), 8192 of 2 35 (309), of 8 94 (313), of
+// 16 147 (315).  With 32 positions, eight warps and the same layout it lost with
 // many: 545 (313).  Bound by the loads' latency with few, by shared-memory reads
 // with many.
 constexpr int kShortThreads = 128;       // at most: a warp per four rows, a thread per load while there are so many

@@ -15,6 +15,8 @@
 // lanes x 16 bytes (or, where a pointer, pitch or width is not a multiple of 16
 // bytes, of 128 single values); unit u of a row belongs to warp u mod WPR, each
 // warp holds at most NU units.  Rows too wide for that (NU = 0) are read twice.
+// Eight warps hold 8192 bf16 columns of the norm and 4096 of its gradient (half of
+// that of fp32 or unaligned rows).
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -235,7 +237,7 @@ __device__ inline float row_sum(float s, float* red) {
 // twice).  Widths and shares are template parameters because these kernels spend
 // their time on instructions as much as on memory (a run-time WPR: 39 us for
 // 4096 x 7168 with e4m3 output, 68 % of the issue slots).  Bound by memory where
-// there are rows enough: that case's 206 MB in 33.0 us (6.26 TB/s); one row of it
+// there are rows enough: that case's 206 MB in 33.8 us (6.1 TB/s); one row of it
 // in 5.4 us, the latency of a load, the row's sum and two stores.
 template <typename T, bool VEC, int WPR, int NU>
 __global__ void __launch_bounds__(kThreads) add_norm_kernel(const __grid_constant__ AddParams p) {
@@ -345,7 +347,9 @@ struct BackParams {
 // up in order through shared memory, and the block writes one row of partial
 // sums.  16384 x 2048 with a weight and dres, 268 MB: 43.3 us (6.2 TB/s), plus 4.3
 // for the weight's sums below.  (Loading a row at a time, with xhat and g as fp32
-// arrays: 80 us.)
+// arrays: 80 us.)  Rows with NU = 0 load nothing ahead, read dy and h twice and
+// carry the weight's sums in global memory: 177 us for 4096 x 7168 bf16, whose 235
+// MB need 35.
 template <typename T, bool VEC, int WPR, int NU>
 __global__ void __launch_bounds__(kThreads, 2) norm_back_kernel(const __grid_constant__ BackParams p) {
   using U = Unit<T, VEC>;
@@ -568,7 +572,7 @@ struct BackLaunch {
     constexpr int groups = kWarps / WPR;
     const long long want = cdiv(p.rows, groups);
     grid = (int)(want < kBackGrid ? want : kBackGrid);
-    const size_t smem = p.part && groups > 1 && NU ? (size_t)p.cols * 4 : 0;   // at most 4096 columns: 16 KB
+    const size_t smem = p.part && groups > 1 && NU ? (size_t)p.cols * 4 : 0;   // at most 2048 columns: 8 KB
     return launch_behind(norm_back_kernel<T, VEC, WPR, NU>, (unsigned)grid, kThreads, smem, s, p);
   }
 };
