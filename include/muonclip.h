@@ -58,7 +58,7 @@ typedef enum {
 #define MC_STATUS_NONFINITE_SMAX   4  /* NaN/Inf S_max given to the clip     */
 #define MC_STATUS_TIMEOUT          8  /* a bounded device wait gave up       */
 
-/* MC_F8E4M3: an output type of mc_add_rms_norm only. */
+/* MC_F8E4M3: an output type of mc_add_rms_norm and a state type of mc_adamw_step only. */
 typedef enum { MC_F32 = 0, MC_BF16 = 1, MC_F8E4M3 = 2 } mc_dtype;
 
 /* Arithmetic of the Newton-Schulz products.
@@ -373,6 +373,56 @@ typedef struct {
 } mc_kernel_time;
 void mc_profiler_enable(int32_t on);
 int32_t mc_profiler_read(mc_kernel_time* out, int32_t max, int32_t reset);
+
+/* ---- AdamW, for the parameters that Muon leaves out ---- */
+
+/* Values of a tensor per scale of an 8-bit state. */
+#define MC_ADAMW_BLOCK 128
+
+/* One parameter tensor of n contiguous values (n = 0: skipped) and its state.
+ * p: MC_BF16 or MC_F32, updated in place; g: MC_BF16 or MC_F32, its gradient;
+ * m and v: first and second moment, updated in place (zeros before the first
+ * step), both MC_F32 (m_scale = v_scale = NULL) or both MC_F8E4M3.  8-bit states
+ * hold m and sqrt(v), one scale per MC_ADAMW_BLOCK values (the last block may be
+ * shorter): m_scale and v_scale [ceil(n / 128)], value = code * scale, scale =
+ * max(max|x| * (1 / 448), 2^-100) over the block, code = e4m3(x * (1 / scale)),
+ * rounded to nearest even; a root above zero takes at least the code 2^-9. */
+typedef struct {
+  void* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  int32_t p_dtype, g_dtype, state_dtype;
+  int32_t _pad;
+} mc_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2;       /* betas in [0, 1)                             */
+  double eps;                    /* >= 0                                        */
+  double weight_decay;           /* decoupled                                   */
+  int64_t step;                  /* t, 1 for the first step                     */
+  const int64_t* step_device;    /* device, or NULL: t is read from here when the
+                                    kernel runs (a captured step that is replayed);
+                                    values below 1 count as 1                   */
+} mc_adamw_hparams;
+
+/* One AdamW step of `count` tensors, fp32 arithmetic:
+ *   g' = *grad_scale g (grad_scale: device float, or NULL for 1)
+ *   m = beta1 m + (1 - beta1) g';  v = beta2 v + (1 - beta2) g'^2
+ *   p -= lr (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay p)
+ * p is rounded to its type once; the step uses m and v before an 8-bit state
+ * rounds them.  Tensors of any sizes and types share launches (one per set of
+ * types and 504 tensors).  Pointers are aligned to their types; tensors whose
+ * operands are aligned to four of their values run at full width.  What is
+ * written overlaps nothing else; gradients may overlap each other.  A NaN/Inf
+ * reaches its own value, of an 8-bit state every value of its block; one in a
+ * new p sets MC_STATUS_NONFINITE_UPDATE.  `t` is read during the call only.
+ * Asynchronous on `stream`. */
+mc_status mc_adamw_step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* hp, const float* grad_scale,
+                        int32_t* status, mc_stream_t stream);
 
 /* ---- Setup (untimed): the attention layer's query/key features on the
  * library's own kernels ([K2-internals] "MLA 的特殊处理": q^C and the rotary

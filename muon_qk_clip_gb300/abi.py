@@ -75,6 +75,17 @@ class McAttnGrad(ctypes.Structure):
                 ("dv", c_void_p), ("dv_strides", c_int64 * 3)]
 
 
+class McAdamTensor(ctypes.Structure):
+    _fields_ = [("p", c_void_p), ("g", c_void_p), ("m", c_void_p), ("v", c_void_p), ("m_scale", c_void_p),
+                ("v_scale", c_void_p), ("n", c_int64), ("p_dtype", c_int32), ("g_dtype", c_int32),
+                ("state_dtype", c_int32), ("_pad", c_int32)]
+
+
+class McAdamHparams(ctypes.Structure):
+    _fields_ = [("lr", c_double), ("beta1", c_double), ("beta2", c_double), ("eps", c_double),
+                ("weight_decay", c_double), ("step", c_int64), ("step_device", c_void_p)]
+
+
 class McKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 24), ("launches", c_int32), ("ms", c_float)]
 
@@ -115,6 +126,7 @@ SIGNATURES = {
     "mc_rms_norm_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                        c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32,
                                        c_void_p, c_size_t, c_void_p]),
+    "mc_adamw_step": (c_int32, [c_void_p, c_int32, POINTER(McAdamHparams), c_void_p, c_void_p, c_void_p]),
     "mc_selftest_bounded_wait": (c_int32, [c_uint64, c_uint64, c_void_p, c_void_p, c_void_p]),
     "mc_profiler_enable": (None, [c_int32]),
     "mc_profiler_read": (c_int32, [POINTER(McKernelTime), c_int32, c_int32]),

@@ -16,7 +16,8 @@ from dataclasses import dataclass
 import torch
 
 from . import abi
-from .abi import McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat, check
+from .abi import (McAdamHparams, McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat,
+                  check)
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 
@@ -572,6 +573,99 @@ def rms_norm_backward_workspace_size(cols: int) -> int:
     n = ctypes.c_size_t(0)
     check(abi.load().mc_rms_norm_backward_workspace_size(cols, n), "mc_rms_norm_backward_workspace_size")
     return n.value
+
+
+@dataclass
+class AdamHparams:
+    """Mirror of mc_adamw_hparams but for the step."""
+    lr: float = 2e-4
+    beta1: float = 0.9
+    beta2: float = 0.95
+    eps: float = 1e-8
+    weight_decay: float = 0.1
+
+
+_ADAM_TENSOR = struct.Struct("@6Pq4i")
+_ADAM_BLOCK = 128                                      # MC_ADAMW_BLOCK
+_ADAM_DT = {**_DT, torch.float8_e4m3fn: abi.MC_F8E4M3}
+_data_ptr, _numel, _is_contiguous, _get_device = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous,
+                                                  torch.Tensor.get_device)
+
+
+def adamw_state(P, bits: int = 32):
+    """Zero states of the parameters P for adamw_step: dict(M, V, m_scales, v_scales)
+    of lists, the scales None with 32 bits."""
+    if bits not in (8, 32):
+        raise ValueError("bits: 8 or 32")
+    dtype = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    zeros = lambda: [torch.zeros(p.shape, dtype=dtype, device=p.device) for p in P]  # noqa: E731
+    scales = lambda: None if bits == 32 else [torch.zeros(-(-p.numel() // _ADAM_BLOCK), device=p.device) for p in P]  # noqa: E731
+    return dict(M=zeros(), V=zeros(), m_scales=scales(), v_scales=scales())
+
+
+@_on_stream
+def _adamw(first, packed, count, hp, grad_scale, status):
+    """The call under its stream; first, a parameter, names the device."""
+    _run(abi.load().mc_adamw_step, "mc_adamw_step", first.get_device(), packed, count, hp, _at(grad_scale), _at(status))
+
+
+def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None, v_scales=None, grad_scale=None,
+               status=None, stream=None):
+    """One AdamW step (decoupled weight decay) of the parameters P, in place, for
+    what muonclip_step does not take: embeddings, output tables, norm weights.
+    P, G: lists of contiguous bf16 or fp32 tensors of any shape, pair by pair of one
+    size; M, V: their moments, fp32, or e4m3 (M and the root of V) with m_scales and
+    v_scales, as adamw_state makes them; all updated in place.  step: 1 for the first
+    one, or a device int64 tensor of one value that is read when the step runs (for a
+    captured step).  grad_scale: a device fp32 tensor of one value that multiplies
+    every gradient (clipping by the global norm).  Tensors of one set of types share
+    launches."""
+    hp = hp or AdamHparams()
+    n = len(P)
+    if len(G) != n or len(M) != n or len(V) != n:
+        raise ValueError("P, G, M and V must have one length")
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales go together")
+    if n == 0:
+        return
+    every = [*P, *G, *M, *V]
+    if m_scales is not None:
+        if len(m_scales) != n or len(v_scales) != n:
+            raise ValueError("m_scales and v_scales must have P's length")
+        every += [*m_scales, *v_scales]
+    device = {*map(_get_device, every)}
+    device.update([t.get_device() for t in (grad_scale, status, step) if isinstance(t, torch.Tensor)])
+    if len(device) > 1 or min(device) < 0:
+        raise ValueError("every tensor must be on one CUDA device")
+    if not all(map(_is_contiguous, every)):
+        raise ValueError("every tensor must be contiguous")
+    size = [*map(_numel, every)]
+    if size[:n] != size[n:2 * n] or size[:n] != size[2 * n:3 * n] or size[:n] != size[3 * n:4 * n]:
+        raise ValueError("P, G, M and V must agree in size, tensor by tensor")
+    types = [_ADAM_DT.get(t.dtype) for t in every]
+    if not {*types[:2 * n]} <= {abi.MC_F32, abi.MC_BF16}:
+        raise ValueError("P and G must be bfloat16 or float32")
+    if {*types[2 * n:4 * n]} != {abi.MC_F32 if m_scales is None else abi.MC_F8E4M3}:
+        raise ValueError("M and V must be float32, or float8_e4m3fn with m_scales and v_scales")
+    if m_scales is not None:
+        blocks = [-(-x // _ADAM_BLOCK) for x in size[:n]]
+        if size[4 * n:] != blocks + blocks or {*types[4 * n:]} != {abi.MC_F32}:
+            raise ValueError(f"scales must be float32, one per {_ADAM_BLOCK} values of their tensor")
+    if grad_scale is not None and (grad_scale.numel() != 1 or grad_scale.dtype != torch.float32):
+        raise ValueError("grad_scale must be one float32 value")
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
+    on_device = isinstance(step, torch.Tensor)
+    if on_device and (step.numel() != 1 or step.dtype != torch.int64):
+        raise ValueError("step must be an integer or one int64 value on the device")
+    at = [*map(_data_ptr, every)]
+    if m_scales is None:
+        at += 2 * n * [0]
+    packed = b"".join(map(_ADAM_TENSOR.pack, at[:n], at[n:2 * n], at[2 * n:3 * n], at[3 * n:4 * n], at[4 * n:5 * n],
+                          at[5 * n:], size, types, types[n:], types[2 * n:], n * [0]))
+    h = McAdamHparams(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, 0 if on_device else step,
+                      step.data_ptr() if on_device else None)
+    _adamw(P[0], packed, n, h, grad_scale, status, stream=stream)
 
 
 def profiler_enable(on: bool = True):

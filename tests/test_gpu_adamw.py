@@ -1,0 +1,270 @@
+"""GPU parity of mc_adamw_step with a 64-bit reference.
+
+Bounds (w = 2^-24; A = |beta1 m| + |(1 - beta1) g|, the magnitudes of the new m):
+  * m: both factors rounded once, a product, the sum, and before them grad_scale's
+    product and an 8-bit state's code * scale: 6 w A
+  * v: as many roundings, the gradient's twice, the stored root's twice, all terms
+    positive: 10 w v
+  * the update u = m i1 / (sqrt(v) i2 + eps): m's, half of v's, a rounding each for
+    the root, i1, i2 and the fma, and 2 ulp (4 w) for the quotient:
+    (8 w A i1 + 16 w |m| i1) / denominator
+  * p: lr (u's + 4 w (|u| + decay |p|)), then one rounding to its type
+  * 8-bit states: the scale within the largest value's relative error and 2 w; the
+    code a rounding of a value within that and 4 w of x / scale (rounding is monotone)
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from muon_qk_clip_gb300 import abi, build
+from muon_qk_clip_gb300 import binding as mc
+from muon_qk_clip_gb300 import synth
+from tests.gpu_helpers import assert_rounded_within, f64
+
+pytestmark = pytest.mark.gpu
+BF16, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+W = 2.0 ** -24
+LEAST, SCALE_MIN = 2.0 ** -9, 2.0 ** -100
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    abi.load()
+
+
+def normal(shape, std, key):
+    return synth.normal(shape, std, key, 11)
+
+
+def copy_of(state):
+    return {k: v and [t.clone() for t in v] for k, v in state.items()}
+
+
+def make(sizes, p_dtype, g_dtype, bits, steps_before=3):
+    """Parameters, gradients and a state that has seen a few steps; some gradients are exactly zero."""
+    P = [normal((n,), 0.02, f"p{i}").to(p_dtype).cuda() for i, n in enumerate(sizes)]
+    G = [(normal((n,), 1e-3, f"g{i}") * torch.exp(normal((n,), 1.0, f"l{i}"))).to(g_dtype).cuda() for i, n in enumerate(sizes)]
+    for g in G:
+        g[::7] = 0.0
+    s = mc.adamw_state(P, bits)
+    for t in range(steps_before):
+        mc.adamw_step([p.clone() for p in P], [g * (1.0 - 0.3 * t) for g in G], hp=mc.AdamHparams(), step=t + 1, **s)
+    return P, G, s
+
+
+def values(code, scale):
+    """The values that codes stand for, in 64 bits."""
+    n = code.numel()
+    return code.float().double().cpu().numpy().ravel() * np.repeat(f64(scale), 128)[:n]
+
+
+def reference(p, g, m, r_or_v, hp, step, bits, gs=1.0):
+    """(p, m, v and the bounds of p and m) of one tensor, from 64-bit copies of what the state holds."""
+    p, g = f64(p).ravel(), f64(g).ravel() * gs
+    v = r_or_v ** 2 if bits == 8 else r_or_v
+    A = np.abs(hp.beta1 * m) + np.abs((1 - hp.beta1) * g)
+    m = hp.beta1 * m + (1 - hp.beta1) * g
+    v = hp.beta2 * v + (1 - hp.beta2) * g * g
+    i1 = 1 / (1 - hp.beta1 ** step)
+    den = np.sqrt(v / (1 - hp.beta2 ** step)) + hp.eps
+    u = m * i1 / den
+    tu = (8 * W * A * i1 + 16 * W * np.abs(m) * i1) / den
+    tp = abs(hp.lr) * (tu + 4 * W * (np.abs(u) + hp.weight_decay * np.abs(p)))
+    return p - hp.lr * (u + hp.weight_decay * p), m, v, tp, 6 * W * A
+
+
+def check_codes(code, scale, x, tol, root):
+    n = x.size
+    pad = lambda t: np.pad(t, (0, -n % 128)).reshape(-1, 128)  # noqa: E731
+    X, T = pad(x), pad(tol)
+    top = np.abs(X).max(1)
+    ref = np.maximum(top / 448.0, SCALE_MIN)
+    ts = T.max(1) / 448.0 + 2 * W * ref
+    s = f64(scale)
+    assert np.all(np.abs(s - ref) <= ts)
+    y = X / ref[:, None]
+    ty = T / ref[:, None] + np.abs(y) * ((ts / ref)[:, None] + 4 * W)
+    lo, hi = O.round_to_e4m3(y - ty), O.round_to_e4m3(y + ty)
+    if root:                              # a root that is not zero has at least the least code
+        some = y > 0
+        lo, hi = np.where(some, np.maximum(lo, LEAST), 0.0), np.where(some, np.maximum(hi, LEAST), 0.0)
+    got = pad(code.float().double().cpu().numpy().ravel())
+    assert np.all((got >= lo) & (got <= hi))
+
+
+def check(P, before, G, s, hp, step, bits, gs=1.0):
+    for i, p in enumerate(P):
+        if p.numel() == 0:
+            continue
+        p0, m0, v0 = before[i]
+        ref, m, v, tp, tm = reference(p0, G[i], m0, v0, hp, step, bits, gs)
+        assert_rounded_within(p.flatten(), ref, tp, f"p[{i}]")
+        if bits == 32:
+            assert np.all(np.abs(f64(s["M"][i]).ravel() - m) <= tm + 1e-44)
+            assert np.all(np.abs(f64(s["V"][i]).ravel() - v) <= 10 * W * v + 1e-44)
+        else:
+            check_codes(s["M"][i], s["m_scales"][i], m, tm, False)
+            r = np.sqrt(v)
+            check_codes(s["V"][i], s["v_scales"][i], r, 6 * W * r, True)
+
+
+def snapshot(P, s, bits):
+    if bits == 32:
+        return [(p.clone(), f64(m).ravel(), f64(v).ravel()) for p, m, v in zip(P, s["M"], s["V"])]
+    return [(p.clone(), values(m, ms), values(v, vs))
+            for p, m, v, ms, vs in zip(P, s["M"], s["V"], s["m_scales"], s["v_scales"])]
+
+
+SIZES = [1, 2, 127, 128, 129, 4095, 4096, 4097, 8200, 0, 5]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p_dtype", [BF16, F32])
+@pytest.mark.parametrize("g_dtype", [BF16, F32])
+def test_parity(p_dtype, g_dtype, bits):
+    P, G, s = make(SIZES, p_dtype, g_dtype, bits)
+    before = snapshot(P, s, bits)
+    hp = mc.AdamHparams(lr=1e-3)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mc.adamw_step(P, G, hp=hp, step=4, status=status, **s)
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    check(P, before, G, s, hp, 4, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_first_step_moves_by_lr(bits):
+    """From zero states m / (1 - beta1) is g and the root of v / (1 - beta2) its magnitude: a step
+    of lr against its sign, and of nothing where g is 0 (0 / eps, no 0 / 0)."""
+    P, G, s = make([1000], F32, F32, bits, steps_before=0)
+    p0 = P[0].clone()
+    mc.adamw_step(P, G, hp=mc.AdamHparams(lr=0.5, weight_decay=0.0, eps=1e-30), step=1, **s)
+    torch.cuda.synchronize()
+    assert torch.allclose(P[0] - p0, -0.5 * torch.sign(G[0]), rtol=1e-5, atol=1e-7)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("count", [16, 17, 128, 129, 504, 600])
+def test_many_tensors(count, bits):
+    """Every size of the launch's table, and more tensors than one launch takes."""
+    sizes = [(i * 37) % 300 + 1 for i in range(count)]
+    flat = normal((sum(sizes),), 0.02, "flat").cuda()
+    grad = normal((sum(sizes),), 1e-3, "gradient").cuda()
+    P, G = list(flat.split(sizes)), list(grad.split(sizes))      # views at any multiple of four bytes
+    s = mc.adamw_state(P, bits)
+    before = snapshot(P, s, bits)
+    hp = mc.AdamHparams()
+    mc.adamw_step(P, G, hp=hp, step=1, **s)
+    torch.cuda.synchronize()
+    check(P, before, G, s, hp, 1, bits)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_nothing_beside_the_tensors_is_written(bits):
+    for lead in (0, 1, 2, 3, 5, 8):
+        n = 300
+        base = {k: torch.full((n + 32,), 7.0, device="cuda") for k in "pg"}
+        state_type = F32 if bits == 32 else F8
+        base |= {k: torch.full((n + 32,), 2.0, device="cuda").to(state_type) for k in "mv"}
+        cut = lambda t: t[lead:lead + n]  # noqa: E731
+        s = dict(M=[cut(base["m"])], V=[cut(base["v"])], m_scales=None, v_scales=None)
+        scales = torch.full((2, 5), 3.0, device="cuda")
+        if bits == 8:
+            s.update(m_scales=[scales[0, 1:4]], v_scales=[scales[1, 1:4]])
+        mc.adamw_step([cut(base["p"])], [cut(base["g"])], hp=mc.AdamHparams(lr=0.1), step=2, **s)
+        torch.cuda.synchronize()
+        for k, t in base.items():
+            outside = torch.cat([t.float()[:lead], t.float()[lead + n:]])
+            assert torch.all(outside == (7.0 if k in "pg" else 2.0)), (lead, k)
+        assert torch.all(base["g"] == 7.0) and torch.all(cut(base["p"]) != 7.0)
+        assert torch.all(scales[:, 0] == 3.0) and torch.all(scales[:, 4] == 3.0)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_grad_scale_and_shapes(bits):
+    P = [normal((33, 5), 0.02, "sp").cuda(), normal((4, 3, 2), 0.02, "sq").to(BF16).cuda()]
+    G = [normal((33, 5), 1.0, "sg").cuda(), normal((4, 3, 2), 1.0, "sh").cuda()]
+    s = mc.adamw_state(P, bits)
+    before = snapshot(P, s, bits)
+    scale = torch.tensor([0.125], device="cuda")
+    hp = mc.AdamHparams()
+    mc.adamw_step(P, G, hp=hp, step=1, grad_scale=scale, **s)
+    torch.cuda.synchronize()
+    check(P, before, G, s, hp, 1, bits, gs=0.125)
+
+
+def test_nonfinite_gradient_stays_in_its_place():
+    for bits in (32, 8):
+        P, G, s = make([700], F32, F32, bits)
+        Q, H, z = make([700], F32, F32, bits)
+        G[0][300] = float("nan")
+        G[0][10] = float("inf")
+        H[0][300], H[0][10] = 0.0, 0.0
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        mc.adamw_step(P, G, hp=mc.AdamHparams(), step=4, status=status, **s)
+        mc.adamw_step(Q, H, hp=mc.AdamHparams(), step=4, **z)
+        torch.cuda.synchronize()
+        assert status.item() == abi.MC_STATUS_NONFINITE_UPDATE
+        keep = torch.ones(700, dtype=torch.bool, device="cuda")
+        keep[[10, 300]] = False
+        assert torch.equal(P[0][keep], Q[0][keep]) and not torch.isfinite(P[0][300])
+        if bits == 8:                    # of the state, its block of 128
+            keep[:128] = False
+            keep[256:384] = False
+            assert torch.isnan(s["m_scales"][0][2]) and torch.isfinite(s["m_scales"][0][1])
+        for k in "MV":
+            assert torch.equal(s[k][0].float()[keep], z[k][0].float()[keep])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_step_counts_on(bits):
+    """A captured step that reads its number from the device, replayed, equals steps one by one."""
+    P, G, s = make([5000, 33], BF16, F32, bits, steps_before=0)
+    Q, z = [p.clone() for p in P], copy_of(s)
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    hp = mc.AdamHparams(lr=1e-2)
+    mc.adamw_step([p.clone() for p in P], G, hp=hp, step=step, **copy_of(s))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.add_(1)
+        mc.adamw_step(P, G, hp=hp, step=step, **s)
+    step.zero_()
+    for _ in range(3):
+        graph.replay()
+    for t in range(3):
+        mc.adamw_step(Q, G, hp=hp, step=t + 1, **z)
+    torch.cuda.synchronize()
+    assert step.item() == 3
+    for a, b in zip(P, Q):               # the factors of t come from two libraries' expm1: an ulp of the update at most
+        assert torch.all((a.float() - b.float()).abs() <= 2.0 ** -8 * b.float().abs() + 1e-12)
+    for a, b in zip(s["M"] + s["V"], z["M"] + z["V"]):
+        assert torch.equal(a.float(), b.float())
+
+
+def test_equal_inputs_give_equal_bits_on_any_stream():
+    P, G, s = make([40000, 777], BF16, BF16, 8)
+    Q, z = [p.clone() for p in P], copy_of(s)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    mc.adamw_step(P, G, hp=mc.AdamHparams(), step=4, **s)
+    mc.adamw_step(Q, G, hp=mc.AdamHparams(), step=4, stream=side, **z)
+    torch.cuda.synchronize()
+    for a, b in zip(P + s["M"] + s["V"], Q + z["M"] + z["V"]):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_tensor_of_more_than_2_to_31_values():
+    n = (1 << 31) + 4099
+    p = torch.zeros(n, dtype=BF16, device="cuda")
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    at = torch.tensor([0, (1 << 31) - 1, 1 << 31, n - 1], device="cuda")
+    p[at] = 1.0
+    g[at] = 0.5
+    s = mc.adamw_state([p], 8)
+    mc.adamw_step([p], [g], hp=mc.AdamHparams(lr=0.25, weight_decay=0.0), step=1, **s)
+    torch.cuda.synchronize()
+    assert torch.all(p[at] == 0.75) and int((p != 0).sum()) == 4 and int((s["M"][0].view(torch.uint8) != 0).sum()) == 4
