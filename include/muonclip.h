@@ -374,6 +374,57 @@ typedef struct {
 void mc_profiler_enable(int32_t on);
 int32_t mc_profiler_read(mc_kernel_time* out, int32_t max, int32_t reset);
 
+/* ---- Norms of query and key heads, with the rotary embedding in the same pass ---- */
+
+/* Most features of a head. */
+#define MC_HEAD_MAX 256
+
+/* Queries [T, heads_q, d] and keys [T, heads_k, d] of T tokens, features with
+ * unit stride; the other strides (token, head) are in elements. */
+typedef struct {
+  int64_t T;                     /* tokens; 0 returns at once                    */
+  int32_t heads_q, heads_k;      /* >= 1; >= 0 (0: k's pointers are not looked at) */
+  int32_t d;                     /* features per head: even, 2..MC_HEAD_MAX      */
+  int32_t rot;                   /* the last `rot` of them are rotated: even, 0..d */
+  int32_t dtype;                 /* MC_BF16 or MC_F32, of everything but rstd and weight gradients */
+  float eps;                     /* >= 0                                         */
+  double theta;                  /* >= 1e-6                                      */
+  const int32_t* positions;      /* device [T], any values; NULL: token t is at t */
+} mc_heads;
+
+/* Per token and head, fp32 arithmetic:
+ *   rstd = 1 / sqrt(mean(x^2) + eps)  (stored: rstd [T, heads_q + heads_k], queries first)
+ *   z = x rstd w   (wq, wk: [d] of dtype, NULL: ones)
+ *   y = z with each pair (z[2k], z[2k+1]) of its last `rot` features rotated by the
+ *       angle position * theta^(-2k/rot): (z0 cos - z1 sin, z0 sin + z1 cos)
+ * rounded to dtype once.  yq may be q and yk may be k, in place with the same
+ * strides; other overlaps with an output are refused, but for head ranges side by
+ * side in one buffer.  Pointers are aligned to their type; 16-byte aligned rows of
+ * whole 16 bytes run at full width.  A NaN/Inf in a head reaches that head's
+ * outputs only.  Asynchronous on `stream`. */
+mc_status mc_head_norm_rope(const mc_heads* h, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                            int64_t k_token, int64_t k_head, const void* wq, const void* wk, void* yq, int64_t yq_token,
+                            int64_t yq_head, void* yk, int64_t yk_token, int64_t yk_head, float* rstd,
+                            mc_stream_t stream);
+
+/* Bytes of workspace that mc_head_norm_rope_backward needs for weight gradients. */
+mc_status mc_head_norm_rope_backward_workspace_size(int32_t d, size_t* bytes);
+
+/* Gradient of mc_head_norm_rope, given its inputs, rstd and the outputs' gradients:
+ *   dz = dy rotated back, xhat = x rstd, g = w dz,
+ *   dx = rstd (g - xhat mean(g xhat)), rounded to dtype once;
+ *   dwq, dwk [d] (fp32, written; NULL: not wanted) = sums over tokens and heads of dz xhat,
+ * in a fixed order.  dq may be dyq or q and dk may be dyk or k, in place with the
+ * same strides; other overlaps as above.  workspace: device, 16-byte aligned, only
+ * with a weight gradient, for this call alone while it runs.  T of 0 zeroes the
+ * weight gradients.  Asynchronous on `stream`. */
+mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t dyq_token, int64_t dyq_head,
+                                     const void* dyk, int64_t dyk_token, int64_t dyk_head, const void* q, int64_t q_token,
+                                     int64_t q_head, const void* k, int64_t k_token, int64_t k_head, const float* rstd,
+                                     const void* wq, const void* wk, void* dq, int64_t dq_token, int64_t dq_head, void* dk,
+                                     int64_t dk_token, int64_t dk_head, float* dwq, float* dwk, void* workspace,
+                                     size_t workspace_bytes, mc_stream_t stream);
+
 /* ---- AdamW, for the parameters that Muon leaves out ---- */
 
 /* Values of a tensor per scale of an 8-bit state. */

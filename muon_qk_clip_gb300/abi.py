@@ -75,6 +75,11 @@ class McAttnGrad(ctypes.Structure):
                 ("dv", c_void_p), ("dv_strides", c_int64 * 3)]
 
 
+class McHeads(ctypes.Structure):
+    _fields_ = [("T", c_int64), ("heads_q", c_int32), ("heads_k", c_int32), ("d", c_int32), ("rot", c_int32),
+                ("dtype", c_int32), ("eps", c_float), ("theta", c_double), ("positions", c_void_p)]
+
+
 class McAdamTensor(ctypes.Structure):
     _fields_ = [("p", c_void_p), ("g", c_void_p), ("m", c_void_p), ("v", c_void_p), ("m_scale", c_void_p),
                 ("v_scale", c_void_p), ("n", c_int64), ("p_dtype", c_int32), ("g_dtype", c_int32),
@@ -126,6 +131,13 @@ SIGNATURES = {
     "mc_rms_norm_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                        c_int64, c_void_p, c_int64, c_void_p, c_int64, c_int32, c_int32,
                                        c_void_p, c_size_t, c_void_p]),
+    "mc_head_norm_rope": (c_int32, [POINTER(McHeads), c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+                                    c_void_p, c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+                                    c_void_p]),
+    "mc_head_norm_rope_backward_workspace_size": (c_int32, [c_int32, POINTER(c_size_t)]),
+    "mc_head_norm_rope_backward": (c_int32, [POINTER(McHeads)] + 4 * [c_void_p, c_int64, c_int64]
+                                   + [c_void_p, c_void_p, c_void_p] + 2 * [c_void_p, c_int64, c_int64]
+                                   + [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "mc_adamw_step": (c_int32, [c_void_p, c_int32, POINTER(McAdamHparams), c_void_p, c_void_p, c_void_p]),
     "mc_selftest_bounded_wait": (c_int32, [c_uint64, c_uint64, c_void_p, c_void_p, c_void_p]),
     "mc_profiler_enable": (None, [c_int32]),

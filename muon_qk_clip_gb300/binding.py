@@ -16,7 +16,7 @@ from dataclasses import dataclass
 import torch
 
 from . import abi
-from .abi import (McAdamHparams, McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat,
+from .abi import (McAdamHparams, McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHeads, McHparams, McMat,
                   check)
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
@@ -573,6 +573,121 @@ def rms_norm_backward_workspace_size(cols: int) -> int:
     n = ctypes.c_size_t(0)
     check(abi.load().mc_rms_norm_backward_workspace_size(cols, n), "mc_rms_norm_backward_workspace_size")
     return n.value
+
+
+def _head_rows(t, name, shape, dtype):
+    """(address, token stride, head stride) of a [T, heads, d] operand of this shape and type."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError(f"{name} must be {list(shape)} of {dtype}")
+    token, head, inner = t.stride()
+    if inner != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: expected unit stride along the features")
+    return t.data_ptr(), token, head
+
+
+def _heads(q, k, positions, theta, rot, eps, *others):
+    """(descriptor, device index, q's and k's shapes and their type)"""
+    index = _device_of(q, "q", k, positions, *others)
+    shape, t = q.shape, q.dtype
+    if len(shape) != 3 or t not in _DT:
+        raise ValueError("q: expected [T, heads, d] of bfloat16 or float32")
+    T, heads, d = shape
+    k_shape = (T, 0, d)
+    if k is not None:
+        k_shape = k.shape
+        if len(k_shape) != 3 or k_shape[0] != T or k_shape[2] != d or k.dtype != t:
+            raise ValueError(f"keys must be [{T}, heads, {d}] of {t}")
+    if positions is not None:
+        _vector(positions, "positions", T, torch.int32)
+    h = McHeads(T, heads, k_shape[1], d, d if rot is None else rot, _DT[t], eps, theta, _at(positions))
+    return h, index, shape, k_shape, t
+
+
+_NO_ROWS = (None, 0, 0)
+
+
+@_on_stream
+def qk_norm_rope(q, k=None, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None, eps: float = 1e-6,
+                 out_q=None, out_k=None, rstd=None, *, stream=None):
+    """RMS norm of every head of q [T, heads, d] and k [T, key heads, d] (bf16 or
+    fp32, features with unit stride, other strides free: views of one projection),
+    times wq, wk [d] if given, then the rotary embedding of the last `rot` features
+    (all by default, interleaved pairs as in rope_) at `positions` [T] int32 (the
+    token's number without).  Returns (yq, yk or None, rstd [T, heads + key heads]
+    f32); out_q=q and out_k=k run in place."""
+    h, index, shape, k_shape, t = _heads(q, k, positions, theta, rot, eps, wq, wk, out_q, out_k, rstd)
+    d = shape[2]
+    for w, name in ((wq, "wq"), (wk, "wk")):
+        if w is not None:
+            _vector(w, name, d, t)
+    if k is None and (wk is not None or out_k is not None):
+        raise ValueError("wk and out_k go with k")
+    if out_q is None:
+        out_q = torch.empty(shape, dtype=t, device=q.device)
+    if k is not None and out_k is None:
+        out_k = torch.empty(k_shape, dtype=t, device=q.device)
+    total = (shape[0], shape[1] + k_shape[1])
+    if rstd is None:
+        rstd = torch.empty(total, dtype=torch.float32, device=q.device)
+    elif rstd.shape != total or rstd.dtype != torch.float32 or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be a contiguous {list(total)} tensor of float32")
+    _run(abi.load().mc_head_norm_rope, "mc_head_norm_rope", index, h, *_head_rows(q, "q", shape, t),
+         *(_NO_ROWS if k is None else _head_rows(k, "k", k_shape, t)), _at(wq), _at(wk),
+         *_head_rows(out_q, "out_q", shape, t), *(_NO_ROWS if k is None else _head_rows(out_k, "out_k", k_shape, t)),
+         rstd.data_ptr())
+    return out_q, out_k, rstd
+
+
+def head_norm_backward_workspace_size(d: int) -> int:
+    """Bytes of workspace that qk_norm_rope_backward needs for weight gradients."""
+    n = ctypes.c_size_t(0)
+    check(abi.load().mc_head_norm_rope_backward_workspace_size(d, n), "mc_head_norm_rope_backward_workspace_size")
+    return n.value
+
+
+@_on_stream
+def qk_norm_rope_backward(dyq, dyk, q, k, rstd, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None,
+                          dq=None, dk=None, dwq=None, dwk=None, workspace=None, *, stream=None):
+    """Gradient of qk_norm_rope given its inputs, the rstd that it returned and the
+    outputs' gradients (dyk and k None without keys): (dq, dk or None, dwq, dwk), the
+    weights' [d] f32, None without a weight unless one is given to write.  dq may be
+    dyq or q and dk may be dyk or k (in place).  workspace: a CUDA tensor of
+    head_norm_backward_workspace_size(d) bytes, allocated for the call where a weight
+    gradient needs one and none is given."""
+    h, index, shape, k_shape, t = _heads(q, k, positions, theta, rot, 0.0, dyq, dyk, rstd, wq, wk, dq, dk, dwq, dwk, workspace)
+    d = shape[2]
+    if (k is None) != (dyk is None) or (k is None and any(x is not None for x in (wk, dk, dwk))):
+        raise ValueError("k, dyk, wk, dk and dwk go together")
+    total = (shape[0], shape[1] + k_shape[1])
+    if rstd.shape != total or rstd.dtype != torch.float32 or not rstd.is_contiguous():
+        raise ValueError(f"rstd must be a contiguous {list(total)} tensor of float32")
+    if dq is None:
+        dq = torch.empty(shape, dtype=t, device=q.device)
+    if k is not None and dk is None:
+        dk = torch.empty(k_shape, dtype=t, device=q.device)
+    if wq is not None:
+        _vector(wq, "wq", d, t)
+        if dwq is None:
+            dwq = torch.empty(d, dtype=torch.float32, device=q.device)
+    if wk is not None:
+        _vector(wk, "wk", d, t)
+        if dwk is None:
+            dwk = torch.empty(d, dtype=torch.float32, device=q.device)
+    nbytes = 0
+    if dwq is not None or dwk is not None:
+        for w, name in ((dwq, "dwq"), (dwk, "dwk")):
+            if w is not None:
+                _vector(w, name, d, torch.float32)
+        if workspace is None:
+            workspace = torch.empty(head_norm_backward_workspace_size(d), dtype=torch.uint8, device=q.device)
+        nbytes = _nbytes(workspace)
+    none = k is None
+    _run(abi.load().mc_head_norm_rope_backward, "mc_head_norm_rope_backward", index, h, *_head_rows(dyq, "dyq", shape, t),
+         *(_NO_ROWS if none else _head_rows(dyk, "dyk", k_shape, t)), *_head_rows(q, "q", shape, t),
+         *(_NO_ROWS if none else _head_rows(k, "k", k_shape, t)), rstd.data_ptr(), _at(wq), _at(wk),
+         *_head_rows(dq, "dq", shape, t), *(_NO_ROWS if none else _head_rows(dk, "dk", k_shape, t)), _at(dwq), _at(dwk),
+         _at(workspace), nbytes)
+    return dq, dk, dwq, dwk
 
 
 @dataclass

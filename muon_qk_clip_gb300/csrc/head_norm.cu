@@ -1,0 +1,579 @@
+// RMS norm of every query and key head with the rotary embedding in the same
+// pass, and its gradient.  Per token t and head h, over the d features of the
+// head, with the rotation R of the token's position on the last `rot` of them
+// (interleaved pairs, angle position * theta^(-2 k / rot)):
+//
+//   rstd = 1 / sqrt(mean(x^2) + eps),   y = R (x rstd w)
+//   dz = R^T dy,   xhat = x rstd,   g = w dz,
+//   dx = rstd (g - xhat mean(g xhat)),   dw = sum over tokens and heads of dz xhat
+//
+// Queries and keys share one launch: a warp takes a token and a range of its
+// heads, so it needs the token's sines and cosines once.  A head's row lies over
+// the fewest lanes that hold it 16 bytes each (16 lanes for 128 bf16 features, two
+// heads per warp), its sums over these lanes' shuffles, several rows' loads in
+// flight.  Bound by memory.
+//
+// Turns: a pair's frequency in turns per position is kept as a 64-bit fraction
+// of a turn (from fp64 on the host), and its product with the position, taken
+// modulo 2^64, is the turn at the position: exact for every 32-bit position
+// (negative ones too) but for the frequency's own rounding, a few 2^-53 of it.
+// Its top 32 bits become an fp32 number of half turns for sincospif.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+#include <cstring>
+
+#include "../../include/muonclip.h"
+#include "common.cuh"
+#include "fastdiv.cuh"
+#include "kernels.h"
+
+namespace mc {
+namespace {
+namespace hn {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxPairs = MC_HEAD_MAX / 2;
+constexpr int kFlight = 4;                        // rows of a lane in flight (the gradient: pairs of rows, half as many)
+constexpr int kBackGrid = 152 * 4;                // blocks (rows of weight sums) of the gradient, at most
+
+struct Side {                                     // queries or keys
+  const void* x;                                  // the norm's input
+  const void* dy;                                 // gradient only
+  void* out;                                      // y, or dx
+  const void* w;
+  long long xt, xh, gt, gh, ot, oh;               // strides: token, head
+  int heads;
+};
+struct Params {
+  Side side[2];
+  unsigned long long turn[kMaxPairs];             // of pair k, in 2^-64 turns per position
+  const int* positions;                           // or null: the token's number
+  float* rstd;                                    // [T, heads of both]
+  float* part;                                    // gradient: [blocks][2][d] weight sums, or null
+  int T, d, rot, heads;
+  int lanes;                                      // per row: a power of two
+  int span, pieces;                               // heads per warp (whole rows of it), warps per token
+  float eps, inv_d;
+  FastDiv div_pieces;
+  long long units;                                // T * pieces, below 2^31
+};
+
+// V neighbouring features of a row.
+template <typename T, int V>
+struct Feat;
+template <>
+struct Feat<__nv_bfloat16, 8> {
+  uint4 w;
+  __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t e[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) { x[2 * i] = __uint_as_float(e[i] << 16); x[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u); }
+  }
+  __device__ static void store(__nv_bfloat16* p, const float (&x)[8]) {
+    uint32_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      e[i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
+  }
+};
+template <>
+struct Feat<float, 4> {
+  float4 w;
+  __device__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
+  __device__ void zero() { w = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ void get(float (&x)[4]) const { x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w; }
+  __device__ static void store(float* p, const float (&x)[4]) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+};
+template <typename T>
+struct Feat<T, 2> {                               // a pair, whatever its alignment
+  float a, b;
+  __device__ static float in(float v) { return v; }
+  __device__ static float in(__nv_bfloat16 v) { return __bfloat162float(v); }
+  __device__ static void to(float* p, float v) { *p = v; }
+  __device__ static void to(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+  __device__ void load(const T* p) { a = in(p[0]); b = in(p[1]); }
+  __device__ void zero() { a = b = 0.f; }
+  __device__ void get(float (&x)[2]) const { x[0] = a; x[1] = b; }
+  __device__ static void store(T* p, const float (&x)[2]) { to(p, x[0]); to(p + 1, x[1]); }
+};
+
+// A lane's features are V from column V * (its lane of the row + lanes * u), u <
+// NU, as long as they are below d.  Sine and cosine per pair; those below the
+// rotated part turn by nothing.
+template <int V, int NU>
+struct Turn {
+  float c[NU][V / 2], s[NU][V / 2];
+  __device__ void at(const Params& p, int pos, int sub) {
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const int col = V * (sub + p.lanes * u) + 2 * k, pair = (col - (p.d - p.rot)) / 2;
+        c[u][k] = 1.f;
+        s[u][k] = 0.f;
+        if (col < p.d && col >= p.d - p.rot) {
+          const long long turn = (long long)(p.turn[pair] * (unsigned long long)(long long)pos);
+          sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s[u][k], &c[u][k]);
+        }
+      }
+  }
+};
+// (a, b) -> (a c - b s, b c + a s)
+__device__ inline void rotate(float& a, float& b, float c, float s) {
+  untwo(fma2(two(b, a), two(-s, s), mul2(two(a, b), two(c, c))), a, b);
+}
+
+__device__ inline float row_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <typename T, int V, int NU>
+__device__ inline void load_weight(const Params& p, const void* w, int sub, float (&x)[NU][V]) {
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int col = V * (sub + p.lanes * u);
+    Feat<T, V> f;
+    f.zero();
+    if (w && col < p.d) f.load(static_cast<const T*>(w) + col);
+    f.get(x[u]);
+    if (!w)
+#pragma unroll
+      for (int k = 0; k < V; ++k) x[u][k] = 1.f;
+  }
+}
+
+template <typename T, int V, int NU>
+__global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_constant__ Params p) {
+  await_previous();
+  release_next();
+  const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
+  float w[2][NU][V];
+  load_weight<T, V, NU>(p, p.side[0].w, sub, w[0]);
+  load_weight<T, V, NU>(p, p.side[1].w, sub, w[1]);
+  const long long warps = (long long)gridDim.x * kWarps;
+  for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.units; unit += warps) {
+    const int t = (int)fastdiv((uint32_t)unit, p.div_pieces), piece = (int)unit - t * p.pieces;
+    const int from = piece * p.span, to = min(p.heads, from + p.span);
+    Turn<V, NU> turn;
+    bool turned = false;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const Side& S = p.side[side];
+      const int base = side ? p.side[0].heads : 0;         // this side's first head among both
+      const int h1 = min(to, base + S.heads) - base;
+      const T* x = static_cast<const T*>(S.x) + t * S.xt;
+      T* y = static_cast<T*>(S.out) + t * S.ot;
+      for (int h0 = max(from - base, 0); h0 < h1; h0 += kFlight * rows) {
+        Feat<T, V> f[kFlight][NU];
+#pragma unroll
+        for (int n = 0; n < kFlight; ++n) {
+          const int h = h0 + n * rows + group;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const int col = V * (sub + p.lanes * u);
+            if (h < h1 && col < p.d) f[n][u].load(x + h * S.xh + col); else f[n][u].zero();
+          }
+        }
+        if (!turned) {                                       // under the first loads
+          turn.at(p, p.positions ? p.positions[t] : t, sub);
+          turned = true;
+        }
+#pragma unroll
+        for (int n = 0; n < kFlight; ++n) {
+          if (h0 + n * rows >= h1) break;                   // the whole warp
+          const int h = h0 + n * rows + group;
+          float v[NU][V], sum = 0.f;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            f[n][u].get(v[u]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) sum = fmaf(v[u][k], v[u][k], sum);
+          }
+          const float rstd = 1.f / sqrtf(fmaf(row_sum(sum, p.lanes), p.inv_d, p.eps));
+          if (h >= h1) continue;
+          if (sub == 0) p.rstd[(long long)t * p.heads + base + h] = rstd;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const int col = V * (sub + p.lanes * u);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) {
+              v[u][k] *= rstd * w[side][u][k];
+              v[u][k + 1] *= rstd * w[side][u][k + 1];
+              rotate(v[u][k], v[u][k + 1], turn.c[u][k / 2], turn.s[u][k / 2]);
+            }
+            if (col < p.d) Feat<T, V>::store(y + h * S.oh + col, v[u]);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, int NU>
+__global__ void __launch_bounds__(kThreads) head_norm_back_kernel(const __grid_constant__ Params p) {
+  extern __shared__ float sums[];                 // [2][rows of all warps][d] weight sums
+  await_previous();
+  release_next();
+  const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
+  float w[2][NU][V], dw[2][NU][V];
+  load_weight<T, V, NU>(p, p.side[0].w, sub, w[0]);
+  load_weight<T, V, NU>(p, p.side[1].w, sub, w[1]);
+#pragma unroll
+  for (int i = 0; i < 2 * NU * V; ++i) dw[i / (NU * V)][i / V % NU][i % V] = 0.f;
+  const long long warps = (long long)gridDim.x * kWarps;
+  for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.units; unit += warps) {
+    const int t = (int)fastdiv((uint32_t)unit, p.div_pieces), piece = (int)unit - t * p.pieces;
+    const int from = piece * p.span, to = min(p.heads, from + p.span);
+    Turn<V, NU> turn;
+    bool turned = false;
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const Side& S = p.side[side];
+      const int base = side ? p.side[0].heads : 0;
+      const int h1 = min(to, base + S.heads) - base;
+      const T* x = static_cast<const T*>(S.x) + t * S.xt;
+      const T* g = static_cast<const T*>(S.dy) + t * S.gt;
+      T* o = static_cast<T*>(S.out) + t * S.ot;
+      const float* rs = p.rstd + (long long)t * p.heads + base;
+      constexpr int F = kFlight / 2;
+      for (int h0 = max(from - base, 0); h0 < h1; h0 += F * rows) {
+        Feat<T, V> fx[F][NU], fg[F][NU];
+        float r[F];
+#pragma unroll
+        for (int n = 0; n < F; ++n) {
+          const int h = h0 + n * rows + group;
+          r[n] = h < h1 ? rs[h] : 0.f;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const int col = V * (sub + p.lanes * u);
+            if (h < h1 && col < p.d) { fx[n][u].load(x + h * S.xh + col); fg[n][u].load(g + h * S.gh + col); }
+            else { fx[n][u].zero(); fg[n][u].zero(); }
+          }
+        }
+        if (!turned) {
+          turn.at(p, p.positions ? p.positions[t] : t, sub);
+          turned = true;
+        }
+#pragma unroll
+        for (int n = 0; n < F; ++n) {
+          if (h0 + n * rows >= h1) break;                   // the whole warp
+          const int h = h0 + n * rows + group;
+          float a[NU][V], b[NU][V], dot = 0.f;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            fx[n][u].get(a[u]);
+            fg[n][u].get(b[u]);
+#pragma unroll
+            for (int k = 0; k < V; k += 2) rotate(b[u][k], b[u][k + 1], turn.c[u][k / 2], -turn.s[u][k / 2]);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+              a[u][k] *= r[n];                               // xhat
+              dw[side][u][k] = fmaf(b[u][k], a[u][k], dw[side][u][k]);
+              b[u][k] *= w[side][u][k];
+              dot = fmaf(b[u][k], a[u][k], dot);
+            }
+          }
+          const float mean = row_sum(dot, p.lanes) * p.inv_d;
+          if (h >= h1) continue;
+#pragma unroll
+          for (int u = 0; u < NU; ++u) {
+            const int col = V * (sub + p.lanes * u);
+#pragma unroll
+            for (int k = 0; k < V; ++k) a[u][k] = r[n] * fmaf(-a[u][k], mean, b[u][k]);
+            if (col < p.d) Feat<T, V>::store(o + h * S.oh + col, a[u]);
+          }
+        }
+      }
+    }
+  }
+  if (!p.part) return;
+  const int all = kWarps * rows;
+#pragma unroll
+  for (int side = 0; side < 2; ++side)
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+      const int col = V * (sub + p.lanes * u);
+      if (col < p.d)
+#pragma unroll
+        for (int k = 0; k < V; ++k) sums[(side * all + (threadIdx.x >> 5) * rows + group) * p.d + col + k] = dw[side][u][k];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
+    const int side = i >= p.d, col = i - side * p.d;
+    float v = 0.f;
+    for (int n = 0; n < all; ++n) v += sums[(side * all + n) * p.d + col];
+    p.part[(long long)blockIdx.x * 2 * p.d + i] = v;
+  }
+}
+
+// dw[side][c] = sum over the blocks, in order: a block takes 32 columns, 32 threads
+// every 32nd row of partial sums each.
+__global__ void __launch_bounds__(1024) head_weight_kernel(const float* part, float* dwq, float* dwk, int blocks, int d) {
+  __shared__ float s[32][33];
+  await_previous();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+  float v = 0.f;
+  if (c < 2 * d)
+#pragma unroll 4
+    for (int b = y; b < blocks; b += 32) v += part[(long long)b * 2 * d + c];
+  s[y][x] = v;
+  __syncthreads();
+  if (y == 0 && c < 2 * d) {
+    float t = 0.f;
+#pragma unroll
+    for (int n = 0; n < 32; ++n) t += s[n][x];
+    float* to = c < d ? dwq : dwk;
+    if (to) to[c < d ? c : c - d] = t;
+  }
+}
+
+mc_status err(mc_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return record_error(s, buf);
+}
+uintptr_t at(const void* p) { return reinterpret_cast<uintptr_t>(p); }
+
+// One operand of a call: [T, heads, d] (elements of the call's type), or `bytes` in
+// one piece, aligned to `align`.
+struct Operand {
+  const char* name;
+  const void* p;
+  int64_t st, sh, heads;                          // strides in elements; 0 heads: one piece
+  int64_t align, bytes;
+  bool out;
+  const void *in0, *in1;                          // the inputs that an output may lie on exactly
+};
+Operand rows_of(const char* name, const void* p, int64_t st, int64_t sh, int64_t heads, bool out = false, const void* in0 = nullptr,
+                const void* in1 = nullptr) {
+  return {name, heads ? p : nullptr, st, sh, heads, 0, 0, out, in0, in1};
+}
+Operand piece(const char* name, const void* p, int64_t align, int64_t bytes, bool out = false) {
+  return {name, p, 0, 0, 0, align, bytes, out, nullptr, nullptr};
+}
+
+// Fills p with what both directions share; checks strides, alignment and overlaps
+// of the operands.  `vec`: rows can be read 16 bytes at a time.
+mc_status fill(const char* me, const mc_heads* h, Operand* ops, int n, Params& p, bool& vec) {
+  const int64_t es = h->dtype == MC_BF16 ? 2 : 4, per = 16 / es;
+  vec = h->d % per == 0;
+  for (int i = 0; i < n; ++i) {
+    Operand& o = ops[i];
+    if (!o.p) continue;
+    if (at(o.p) % (o.heads ? es : o.align)) return err(MC_ERR_INVALID_ARG, "%s: %s is not aligned to its type", me, o.name);
+    if (!o.heads) continue;
+    if (h->T == 1) o.st = o.heads * h->d;
+    if (o.heads == 1) o.sh = h->d;
+    if (o.st < 0 || o.sh < 0) return err(MC_ERR_INVALID_ARG, "%s: %s has a negative stride", me, o.name);
+    if (o.st >= (1ll << 40) / (h->T + 1) || o.sh >= (1ll << 40) / (o.heads + 1))
+      return err(MC_ERR_UNSUPPORTED, "%s: %s has strides that are too large", me, o.name);
+    vec = vec && at(o.p) % 16 == 0 && o.st % per == 0 && o.sh % per == 0;
+    const int64_t st[2] = {o.st, o.sh}, ext[2] = {h->T, o.heads};
+    if (o.out && !distinct_addresses(st, ext, 2, h->d))
+      return err(MC_ERR_INVALID_ARG, "%s: elements of %s share addresses", me, o.name);
+    o.bytes = ((h->T - 1) * o.st + (o.heads - 1) * o.sh + h->d) * es;
+  }
+  // an output shares memory with nothing, but for head ranges side by side in one
+  // buffer (q and k of one projection: equal token strides) and the inputs of its own
+  // side that it may replace
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < n; ++j) {
+      const Operand &a = ops[i], &b = ops[j];
+      if (i == j || !a.out || !a.p || !b.p || (b.out && j < i)) continue;
+      if (at(a.p) >= at(b.p) + b.bytes || at(b.p) >= at(a.p) + a.bytes) continue;
+      bool fine = false;
+      if (a.heads && b.heads) {
+        fine = !b.out && a.p == b.p && a.st == b.st && a.sh == b.sh && a.heads == b.heads && (b.p == a.in0 || b.p == a.in1) &&
+               (i ^ j) % 2 == 0;         // operands of queries and keys alternate
+        if (!fine && a.st == b.st && a.st > 0) {
+          const Operand &lo = at(a.p) <= at(b.p) ? a : b, &hi = at(a.p) <= at(b.p) ? b : a;
+          const int64_t apart = (int64_t)((at(hi.p) - at(lo.p)) / es) % a.st;
+          const int64_t wide_lo = (lo.heads - 1) * lo.sh + h->d, wide_hi = (hi.heads - 1) * hi.sh + h->d;
+          fine = apart >= wide_lo && apart + wide_hi <= a.st;
+        }
+      }
+      if (!fine) return err(MC_ERR_INVALID_ARG, "%s: %s overlaps %s", me, a.name, b.name);
+    }
+  p.T = (int)h->T;
+  p.d = h->d;
+  p.rot = h->rot;
+  p.heads = h->heads_q + h->heads_k;
+  p.positions = h->positions;
+  p.eps = h->eps;
+  p.inv_d = 1.f / (float)h->d;
+  for (int k = 0; k < h->rot / 2; ++k) {
+    const double turns = std::exp2(-std::log2(h->theta) * 2.0 * k / h->rot) * 0.15915494309189535;
+    p.turn[k] = (unsigned long long)std::ldexp(turns - std::floor(turns), 64);
+  }
+  return MC_OK;
+}
+
+mc_status check_shape(const char* me, const mc_heads* h) {
+  if (!h) return err(MC_ERR_INVALID_ARG, "%s: null descriptor", me);
+  if (h->dtype != MC_BF16 && h->dtype != MC_F32) return err(MC_ERR_INVALID_ARG, "%s: dtype %d", me, h->dtype);
+  if (h->T < 0 || h->heads_q < 1 || h->heads_k < 0 || h->d < 2 || h->d % 2 || h->d > MC_HEAD_MAX)
+    return err(MC_ERR_INVALID_ARG, "%s: T %lld, heads %d and %d, d %d (even, 2..%d)", me, (long long)h->T, h->heads_q, h->heads_k,
+               h->d, MC_HEAD_MAX);
+  if (h->rot < 0 || h->rot % 2 || h->rot > h->d) return err(MC_ERR_INVALID_ARG, "%s: rot %d (even, 0..d)", me, h->rot);
+  if (!(h->theta > 0.0) || !std::isfinite(h->theta)) return err(MC_ERR_INVALID_ARG, "%s: theta must be finite and > 0", me);
+  if (!(h->eps >= 0.f) || !std::isfinite(h->eps)) return err(MC_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", me);
+  if (h->heads_q > (1 << 16) || h->heads_k > (1 << 16) || h->T > 0x7fffffffll ||
+      h->T * ((int64_t)h->heads_q + h->heads_k) > (1ll << 36))
+    return err(MC_ERR_UNSUPPORTED, "%s: T %lld with %d and %d heads is too large", me, (long long)h->T, h->heads_q, h->heads_k);
+  // theta^(-2k/rot) in turns is kept as a fraction of one: finite, and exact enough
+  if (h->theta < 1e-6) return err(MC_ERR_UNSUPPORTED, "%s: theta %g below 1e-6", me, h->theta);
+  return MC_OK;
+}
+
+// Lanes per row and heads per warp.  A warp takes all heads of a token as long as
+// that makes `most` warps; else they are split, down to one step of its loop.
+void split(Params& p, int units, int flight, int most) {
+  p.lanes = 1;
+  while (p.lanes < 32 && p.lanes < units) p.lanes *= 2;
+  const int step = 32 / p.lanes * flight;
+  const int steps = (p.heads + step - 1) / step;
+  const long long want = p.T >= most ? 1 : (most + p.T - 1) / p.T;
+  const int ways = (int)(want < steps ? want : steps);
+  p.span = (steps + ways - 1) / ways * step;
+  p.pieces = (p.heads + p.span - 1) / p.span;
+  p.units = (long long)p.T * p.pieces;
+  p.div_pieces = make_fastdiv((uint32_t)p.pieces);
+}
+
+template <typename T, int V, int NU>
+cudaError_t run_forward(Params& p, cudaStream_t s) {
+  const int sms = sm_count();
+  split(p, p.d / V, kFlight, sms * 32);
+  const long long blocks = cdiv(p.units, kWarps);
+  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)(blocks < sms * 16ll ? blocks : sms * 16ll), kThreads, 0, s, p);
+}
+template <typename T, int V, int NU>
+cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
+  split(p, p.d / V, kFlight / 2, kBackGrid * kWarps);
+  const long long blocks = cdiv(p.units, kWarps);
+  const int grid = (int)(blocks < kBackGrid ? blocks : kBackGrid);
+  const size_t smem = p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0;   // a warp's rows have at most 256 features: 16 KB
+  const cudaError_t e = launch_behind(head_norm_back_kernel<T, V, NU>, (unsigned)grid, kThreads, smem, s, p);
+  if (e != cudaSuccess || !p.part) return e;
+  return launch_behind(head_weight_kernel, (unsigned)cdiv(2 * p.d, 32), 1024, 0, s, p.part, dwq, dwk, grid, p.d);
+}
+
+}  // namespace hn
+}  // namespace
+}  // namespace mc
+
+using namespace mc;
+using namespace mc::hn;
+
+extern "C" {
+
+mc_status mc_head_norm_rope(const mc_heads* h, const void* q, int64_t q_token, int64_t q_head, const void* k, int64_t k_token,
+                            int64_t k_head, const void* wq, const void* wk, void* yq, int64_t yq_token, int64_t yq_head,
+                            void* yk, int64_t yk_token, int64_t yk_head, float* rstd, mc_stream_t stream) {
+  const char* me = "mc_head_norm_rope";
+  mc_status st = check_shape(me, h);
+  if (st != MC_OK) return st;
+  if (h->T == 0) return record_error(MC_OK, "");
+  const int64_t es = h->dtype == MC_BF16 ? 2 : 4, H = h->heads_q, G = h->heads_k;
+  if (!q || !yq || !rstd || (G && (!k || !yk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  Operand ops[] = {rows_of("q", q, q_token, q_head, H),
+                   rows_of("k", k, k_token, k_head, G),
+                   rows_of("yq", yq, yq_token, yq_head, H, true, q, q),
+                   rows_of("yk", yk, yk_token, yk_head, G, true, k, k),
+                   piece("wq", wq, es, h->d * es),
+                   piece("wk", G ? wk : nullptr, es, h->d * es),
+                   piece("positions", h->positions, 4, h->T * 4),
+                   piece("rstd", rstd, 4, h->T * (H + G) * 4, true)};
+  Params p;
+  memset(&p, 0, sizeof p);
+  bool vec;
+  if ((st = fill(me, h, ops, 8, p, vec)) != MC_OK) return st;
+  vec = vec && at(wq) % 16 == 0 && (!G || at(wk) % 16 == 0);
+  p.side[0] = {q, nullptr, yq, wq, ops[0].st, ops[0].sh, 0, 0, ops[2].st, ops[2].sh, h->heads_q};
+  p.side[1] = {k, nullptr, yk, wk, ops[1].st, ops[1].sh, 0, 0, ops[3].st, ops[3].sh, h->heads_k};
+  p.rstd = rstd;
+  const cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (h->dtype == MC_BF16) e = vec ? run_forward<__nv_bfloat16, 8, 1>(p, s) : run_forward<__nv_bfloat16, 2, 4>(p, s);
+  else if (vec) e = h->d <= 128 ? run_forward<float, 4, 1>(p, s) : run_forward<float, 4, 2>(p, s);
+  else e = run_forward<float, 2, 4>(p, s);
+  if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
+  return record_error(MC_OK, "");
+}
+
+mc_status mc_head_norm_rope_backward_workspace_size(int32_t d, size_t* bytes) {
+  if (d < 2 || d % 2 || d > MC_HEAD_MAX || !bytes)
+    return err(MC_ERR_INVALID_ARG, "mc_head_norm_rope_backward: d %d (even, 2..%d) or null bytes", d, MC_HEAD_MAX);
+  *bytes = (size_t)kBackGrid * 2 * d * 4;
+  return record_error(MC_OK, "");
+}
+
+mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t dyq_token, int64_t dyq_head, const void* dyk,
+                                     int64_t dyk_token, int64_t dyk_head, const void* q, int64_t q_token, int64_t q_head,
+                                     const void* k, int64_t k_token, int64_t k_head, const float* rstd, const void* wq,
+                                     const void* wk, void* dq, int64_t dq_token, int64_t dq_head, void* dk, int64_t dk_token,
+                                     int64_t dk_head, float* dwq, float* dwk, void* workspace, size_t workspace_bytes,
+                                     mc_stream_t stream) {
+  const char* me = "mc_head_norm_rope_backward";
+  mc_status st = check_shape(me, h);
+  if (st != MC_OK) return st;
+  const cudaStream_t s = (cudaStream_t)stream;
+  const int64_t es = h->dtype == MC_BF16 ? 2 : 4, H = h->heads_q, G = h->heads_k;
+  if (at(dwq) % 4 || at(dwk) % 4) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  if (h->T == 0) {                                // sums over nothing
+    for (float* w : {dwq, G ? dwk : nullptr}) {
+      const cudaError_t e = w ? cudaMemsetAsync(w, 0, (size_t)h->d * 4, s) : cudaSuccess;
+      if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
+    }
+    return record_error(MC_OK, "");
+  }
+  if (!dyq || !q || !rstd || !dq || (G && (!dyk || !k || !dk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  const bool weights = dwq || (G && dwk);
+  const size_t need = (size_t)kBackGrid * 2 * h->d * 4;
+  if (weights && (!workspace || at(workspace) % 16 || workspace_bytes < need))
+    return err(MC_ERR_WORKSPACE, "%s: weight gradients need a 16-byte aligned workspace of %zu bytes", me, need);
+  Operand ops[] = {rows_of("dyq", dyq, dyq_token, dyq_head, H),
+                   rows_of("dyk", dyk, dyk_token, dyk_head, G),
+                   rows_of("q", q, q_token, q_head, H),
+                   rows_of("k", k, k_token, k_head, G),
+                   rows_of("dq", dq, dq_token, dq_head, H, true, dyq, q),
+                   rows_of("dk", dk, dk_token, dk_head, G, true, dyk, k),
+                   piece("wq", wq, es, h->d * es),
+                   piece("wk", G ? wk : nullptr, es, h->d * es),
+                   piece("positions", h->positions, 4, h->T * 4),
+                   piece("rstd", rstd, 4, h->T * (H + G) * 4),
+                   piece("dwq", dwq, 4, h->d * 4ll, true),
+                   piece("dwk", G ? dwk : nullptr, 4, h->d * 4ll, true),
+                   piece("workspace", weights ? workspace : nullptr, 16, (int64_t)need, true)};
+  Params p;
+  memset(&p, 0, sizeof p);
+  bool vec;
+  if ((st = fill(me, h, ops, 13, p, vec)) != MC_OK) return st;
+  vec = vec && at(wq) % 16 == 0 && (!G || at(wk) % 16 == 0);
+  p.side[0] = {q, dyq, dq, wq, ops[2].st, ops[2].sh, ops[0].st, ops[0].sh, ops[4].st, ops[4].sh, h->heads_q};
+  p.side[1] = {k, dyk, dk, wk, ops[3].st, ops[3].sh, ops[1].st, ops[1].sh, ops[5].st, ops[5].sh, h->heads_k};
+  p.rstd = const_cast<float*>(rstd);              // read only
+  p.part = weights ? static_cast<float*>(workspace) : nullptr;
+  cudaError_t e;
+  float* dw = G ? dwk : nullptr;
+  if (h->dtype == MC_BF16) e = vec ? run_backward<__nv_bfloat16, 8, 1>(p, dwq, dw, s) : run_backward<__nv_bfloat16, 2, 4>(p, dwq, dw, s);
+  else if (vec) e = h->d <= 128 ? run_backward<float, 4, 1>(p, dwq, dw, s) : run_backward<float, 4, 2>(p, dwq, dw, s);
+  else e = run_backward<float, 2, 4>(p, dwq, dw, s);
+  if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
+  return record_error(MC_OK, "");
+}
+
+}  // extern "C"
