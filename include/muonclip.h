@@ -57,6 +57,7 @@ typedef enum {
 #define MC_STATUS_NONFINITE_LOGIT  2  /* NaN/Inf among the attention logits */
 #define MC_STATUS_NONFINITE_SMAX   4  /* NaN/Inf S_max given to the clip     */
 #define MC_STATUS_TIMEOUT          8  /* a bounded device wait gave up       */
+#define MC_STATUS_BAD_OFFSETS     16  /* packed offsets that decrease or leave [0, T] */
 
 /* MC_F8E4M3: an output type of mc_add_rms_norm and a state type of mc_adamw_step only. */
 typedef enum { MC_F32 = 0, MC_BF16 = 1, MC_F8E4M3 = 2 } mc_dtype;
@@ -335,6 +336,77 @@ mc_status qk_attention_backward_workspace_size(const mc_attn_desc* attn, size_t*
 mc_status qk_attention_backward(const mc_attn_desc* attn, const mc_attn_grad* grad, void* workspace,
                                 size_t workspace_bytes, int32_t* status, mc_stream_t stream);
 
+/* ---- Causal attention over packed sequences, with grouped heads ---- */
+
+/* T tokens that hold nseq sequences one behind the other: sequence s has the tokens
+ * offsets[s] .. offsets[s + 1] - 1 (equal offsets: an empty one; tokens before the
+ * first offset or behind the last belong to none).  Query head h reads key and value
+ * head h / (H / H_kv); a token sees its own sequence up to itself.  The offsets are
+ * read on the device when the call runs, so a captured call takes new ones; one
+ * that is below its predecessor or outside [0, T] is taken as its predecessor or
+ * the bound, and sets MC_STATUS_BAD_OFFSETS.  bf16; features have unit stride, the
+ * other strides (token, head) are in elements, multiples of 8 (axes of one element:
+ * any), pointers 16-byte aligned. */
+typedef struct {
+  int32_t T, nseq;
+  int32_t H, H_kv;         /* H a multiple of H_kv                              */
+  int32_t d, d_v;          /* q.k and value widths, 16..128                     */
+  int32_t dtype;           /* MC_BF16                                           */
+  float scale;             /* logit scale, > 0                                  */
+  const int32_t* offsets;  /* device [nseq + 1]                                 */
+  const void* q;           /* device [T, H, d]                                  */
+  const void* k;           /* device [T, H_kv, d]                               */
+  const void* v;           /* device [T, H_kv, d_v]                             */
+  int64_t q_strides[2];    /* token, head                                       */
+  int64_t k_strides[2];
+  int64_t v_strides[2];
+} mc_packed_desc;
+
+/* Bytes of workspace that the packed forward (backward = 0) or backward needs (T,
+ * nseq, H, H_kv of *a; its pointers are not looked at). */
+mc_status qk_attention_packed_workspace_size(const mc_packed_desc* a, int32_t backward, size_t* bytes);
+
+/* O^h = softmax(scale Q^h K^h^T) V^h within each sequence ([K2-internals] "核心数学"), with
+ * the per-head max logit S_max^h over all of them on the way (smax [H], written, or
+ * max-combined when accumulate = 1; -inf without any token).  o: device [T, H, d_v],
+ * strides as above, must not overlap an input; lse: device [H, T] (natural log of
+ * the softmax's denominator) or NULL.  Rows that belong to no sequence are left as
+ * they were, in o and lse.  Arithmetic as in qk_attention_forward.  A NaN/Inf logit
+ * sets MC_STATUS_NONFINITE_LOGIT; NaN/Inf inputs may reach every output of their
+ * sequence, and none of another's.  workspace: device, 256-byte aligned, for this
+ * call alone while it runs.  T of 0 only sets smax. */
+mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const int64_t o_strides[2], float* lse, float* smax,
+                                      int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* status,
+                                      mc_stream_t stream);
+
+/* Inputs beside those of mc_packed_desc, and outputs, of the packed backward; limits
+ * as there.  Every output element has an address of its own and none overlaps an
+ * input, lse, status or the workspace, or another output (two outputs may
+ * interleave, as dk and dv of one buffer). */
+typedef struct {
+  const void* o;           /* device [T, H, d_v]: the forward's output          */
+  int64_t o_strides[2];    /* token, head                                       */
+  const float* lse;        /* device [H, T]: the forward's                      */
+  const void* d_o;         /* device [T, H, d_v]: gradient of o                 */
+  int64_t do_strides[2];
+  void* dq;                /* device [T, H, d] (written)                        */
+  int64_t dq_strides[2];
+  void* dk;                /* device [T, H_kv, d] (written): summed over the group */
+  int64_t dk_strides[2];
+  void* dv;                /* device [T, H_kv, d_v] (written): summed over the group */
+  int64_t dv_strides[2];
+} mc_packed_grad;
+
+/* Gradients of qk_attention_packed_forward's O with respect to q, k and v.  As in
+ * qk_attention_backward: probabilities recomputed from lse, p and ds rounded to bf16
+ * as operands, fp32 sums (over a group's heads too) in a fixed order, each gradient
+ * rounded once; ds is exactly 0 where a token sees only itself.  Rows that belong to
+ * no sequence are left as they were.  A NaN/Inf gradient sets
+ * MC_STATUS_NONFINITE_UPDATE; NaN/Inf inputs may reach every gradient of their
+ * sequence and head group, and none of another's. */
+mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_grad* g, void* workspace,
+                                       size_t workspace_bytes, int32_t* status, mc_stream_t stream);
+
 /* QK-Clip for one attention layer.  MC_CLIP_PER_HEAD: for every head with
  * smax[h] > tau, gamma_h = tau / smax[h] and every segment's rows of head h are
  * multiplied by gamma_h^exponent; heads with smax[h] <= tau are untouched bit
@@ -362,7 +434,7 @@ mc_status muonclip_step(mc_mat* W, const mc_mat* G, mc_mat* M, int32_t count,
 /* Optional launch timing (observability).  While enabled, every kernel
  * launch of the library is bracketed by CUDA events recorded on the launch's
  * stream, accumulated per kernel class ("prep", "norms", "ns_gemm", "apply",
- * "clip", "max_logit", "attn_fwd", "attn_bwd").  mc_profiler_read synchronises on the recorded
+ * "clip", "max_logit", "attn_fwd", "attn_bwd"; the packed calls count as attn_fwd and attn_bwd).  mc_profiler_read synchronises on the recorded
  * events, writes up to `max` entries (class name, launches, total
  * milliseconds) and returns the number written; reset = 1 clears the totals.
  * Process-wide; not meant for use while several threads launch. */

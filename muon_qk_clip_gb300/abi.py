@@ -21,6 +21,7 @@ MC_STATUS_NONFINITE_UPDATE = 1
 MC_STATUS_NONFINITE_LOGIT = 2
 MC_STATUS_NONFINITE_SMAX = 4
 MC_STATUS_TIMEOUT = 8
+MC_STATUS_BAD_OFFSETS = 16
 
 MC_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
@@ -75,6 +76,18 @@ class McAttnGrad(ctypes.Structure):
                 ("dv", c_void_p), ("dv_strides", c_int64 * 3)]
 
 
+class McPackedDesc(ctypes.Structure):
+    _fields_ = [("T", c_int32), ("nseq", c_int32), ("H", c_int32), ("H_kv", c_int32), ("d", c_int32), ("d_v", c_int32),
+                ("dtype", c_int32), ("scale", c_float), ("offsets", c_void_p), ("q", c_void_p), ("k", c_void_p),
+                ("v", c_void_p), ("q_strides", c_int64 * 2), ("k_strides", c_int64 * 2), ("v_strides", c_int64 * 2)]
+
+
+class McPackedGrad(ctypes.Structure):
+    _fields_ = [("o", c_void_p), ("o_strides", c_int64 * 2), ("lse", c_void_p), ("d_o", c_void_p),
+                ("do_strides", c_int64 * 2), ("dq", c_void_p), ("dq_strides", c_int64 * 2), ("dk", c_void_p),
+                ("dk_strides", c_int64 * 2), ("dv", c_void_p), ("dv_strides", c_int64 * 2)]
+
+
 class McHeads(ctypes.Structure):
     _fields_ = [("T", c_int64), ("heads_q", c_int32), ("heads_k", c_int32), ("d", c_int32), ("rot", c_int32),
                 ("dtype", c_int32), ("eps", c_float), ("theta", c_double), ("positions", c_void_p)]
@@ -111,6 +124,11 @@ SIGNATURES = {
     "qk_attention_backward_workspace_size": (c_int32, [POINTER(McAttnDesc), POINTER(c_size_t)]),
     "qk_attention_backward": (c_int32, [POINTER(McAttnDesc), POINTER(McAttnGrad), c_void_p, c_size_t,
                                         c_void_p, c_void_p]),
+    "qk_attention_packed_workspace_size": (c_int32, [POINTER(McPackedDesc), c_int32, POINTER(c_size_t)]),
+    "qk_attention_packed_forward": (c_int32, [POINTER(McPackedDesc), c_void_p, c_int64 * 2, c_void_p, c_void_p, c_int32,
+                                              c_void_p, c_size_t, c_void_p, c_void_p]),
+    "qk_attention_packed_backward": (c_int32, [POINTER(McPackedDesc), POINTER(McPackedGrad), c_void_p, c_size_t,
+                                               c_void_p, c_void_p]),
     "qk_clip_apply": (c_int32, [c_void_p, c_int32, c_float, c_int32, POINTER(McClipSeg), c_int32,
                                 c_void_p, c_void_p, c_void_p, c_void_p]),
     "muonclip_step": (c_int32, [POINTER(McMat), POINTER(McMat), POINTER(McMat), c_int32,

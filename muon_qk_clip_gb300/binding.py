@@ -17,7 +17,7 @@ import torch
 
 from . import abi
 from .abi import (McAdamHparams, McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHeads, McHparams, McMat,
-                  check)
+                  McPackedDesc, McPackedGrad, check)
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 
@@ -25,6 +25,9 @@ _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 # takes to convert their fields one by one)
 _ATTN_DESC = struct.Struct("@7if3P8q")
 _ATTN_GRAD = struct.Struct("@P2i3qP3qPP3qP3qP3qP2qP3q")
+_PACKED_DESC = struct.Struct("@7if4P6q")
+_PACKED_GRAD = struct.Struct("@P2qPP2qP2qP2qP2q")
+_TWO = ctypes.c_int64 * 2
 
 
 def _ptr(t):
@@ -325,6 +328,112 @@ def _grad_like(name, g, like):
     if g.shape != like.shape or g.stride(-1) != 1 or g.dtype != like.dtype:
         raise ValueError(f"{name} must have its input's shape and type and a contiguous feature axis")
     return g
+
+
+def _packed_desc(q, k, v, offsets, scale):
+    """Descriptor of packed attention: q [T,H,d], k [T,H_kv,d], v [T,H_kv,dv], offsets [n+1]."""
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [T, heads, features]")
+    T, H, d = q.shape
+    G, dv = v.shape[1:]
+    if k.shape != (T, G, d) or v.shape[0] != T:
+        raise ValueError("k must be [T, H_kv, d] and v [T, H_kv, d_v] with q's tokens and width")
+    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must share a supported dtype")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
+        raise ValueError("feature axes must be contiguous")
+    if offsets.dim() != 1 or offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.numel() < 2:
+        raise ValueError("offsets must be a contiguous int32 tensor of one value more than there are sequences")
+    scale = 1.0 / math.sqrt(d) if scale is None else ctypes.c_float(scale).value   # beyond fp32: inf, which the library refuses
+    return McPackedDesc.from_buffer_copy(_PACKED_DESC.pack(
+        T, offsets.numel() - 1, H, G, d, dv, _DT[q.dtype], scale, offsets.data_ptr(), q.data_ptr(), k.data_ptr(),
+        v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]))
+
+
+def _packed_workspace(d, backward, workspace, device):
+    """(address, bytes, tensor) of the given workspace, or of a new one."""
+    if workspace is None:
+        n = ctypes.c_size_t(0)
+        check(abi.load().qk_attention_packed_workspace_size(d, int(backward), n), "qk_attention_packed_workspace_size")
+        workspace, nbytes = torch.empty(n.value, dtype=torch.uint8, device=device), n.value
+    else:
+        nbytes = _nbytes(workspace)
+    return workspace.data_ptr(), nbytes, workspace
+
+
+def packed_workspace_size(q, k, v, offsets, backward=False) -> int:
+    """Bytes of workspace that the packed attention's forward (or backward) needs."""
+    n = ctypes.c_size_t(0)
+    check(abi.load().qk_attention_packed_workspace_size(_packed_desc(q, k, v, offsets, None), int(bool(backward)), n),
+          "qk_attention_packed_workspace_size")
+    return n.value
+
+
+@_on_stream
+def qk_attention_packed_forward(q, k, v, offsets, scale=None, out=None, lse=None, smax=None, accumulate=False,
+                                workspace=None, status=None, *, stream=None):
+    """Causal attention over packed sequences with grouped heads, with the per-head
+    max logit fused in.  q [T,H,d], k [T,H_kv,d], v [T,H_kv,dv] (bf16, contiguous
+    features; query head h reads key head h // (H / H_kv)); offsets [n+1] int32 on
+    the device: sequence s has the tokens offsets[s]:offsets[s+1].  Returns (out
+    [T,H,dv], lse [H,T] f32 or None, smax [H] f32); pass lse=True to allocate it.
+    Rows of no sequence are not written.  workspace: a CUDA tensor of
+    packed_workspace_size bytes; without one, one is allocated for the call."""
+    index = _device_of(q, "q", k, v, offsets, out, None if lse is True else lse, smax, workspace, status)
+    desc = _packed_desc(q, k, v, offsets, scale)
+    T, H, _ = q.shape
+    shape = (T, H, v.shape[2])
+    if out is None:
+        out = torch.empty(shape if shape[2] % 8 == 0 else (T, H, -shape[2] // 8 * -8), dtype=q.dtype, device=q.device)[..., :shape[2]]
+    elif out.shape != shape or out.stride(2) != 1 or out.dtype != q.dtype:
+        raise ValueError("out must be [T, H, d_v] with a contiguous feature axis and q's dtype")
+    if lse is True:
+        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
+    elif lse is not None and (lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous [H, T] float32 tensor")
+    if smax is None:
+        if accumulate:
+            raise ValueError("accumulate goes with a smax to combine")
+        smax = torch.empty(H, dtype=torch.float32, device=q.device)
+    else:
+        _vector(smax, "smax", H, torch.float32)
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
+    at, nbytes, _keep = _packed_workspace(desc, False, workspace, q.device)
+    os = out.stride()
+    _run(abi.load().qk_attention_packed_forward, "qk_attention_packed_forward", index, desc, out.data_ptr(),
+         _TWO(os[0], os[1]), _at(lse), smax.data_ptr(), int(bool(accumulate)), at, nbytes, _at(status))
+    return out, lse, smax
+
+
+@_on_stream
+def qk_attention_packed_backward(q, k, v, out, lse, dout, offsets, scale=None, dq=None, dk=None, dv=None,
+                                 workspace=None, status=None, *, stream=None):
+    """Gradients of qk_attention_packed_forward's output: out, lse as it returned
+    them, dout [T,H,dv]; the other arguments as there.  Returns (dq, dk, dv), dk and
+    dv summed over the query heads of a group; rows of no sequence are not written.
+    Outputs are allocated unless given: contiguous, or, of a width that is no
+    multiple of eight, in rows padded to one.  workspace: a CUDA tensor of
+    packed_workspace_size(..., backward=True) bytes; without one, one is allocated."""
+    index = _device_of(q, "q", k, v, out, lse, dout, offsets, dq, dk, dv, workspace, status)
+    desc = _packed_desc(q, k, v, offsets, scale)
+    T, H, _ = q.shape
+    shape, t = (T, H, v.shape[2]), q.dtype
+    if lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous [H, T] float32 tensor")
+    os, ds = out.stride(), dout.stride()
+    if out.shape != shape or dout.shape != shape or out.dtype != t or dout.dtype != t or os[2] != 1 or ds[2] != 1:
+        raise ValueError("out and dout must be [T, H, d_v] with contiguous feature axes and q's dtype")
+    dq, dk, dv = _grad_like("dq", dq, q), _grad_like("dk", dk, k), _grad_like("dv", dv, v)
+    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
+        raise ValueError("status must be an int32 tensor")
+    at, nbytes, _keep = _packed_workspace(desc, True, workspace, q.device)
+    g = McPackedGrad.from_buffer_copy(_PACKED_GRAD.pack(
+        out.data_ptr(), os[0], os[1], lse.data_ptr(), dout.data_ptr(), ds[0], ds[1],
+        dq.data_ptr(), *dq.stride()[:2], dk.data_ptr(), *dk.stride()[:2], dv.data_ptr(), *dv.stride()[:2]))
+    _run(abi.load().qk_attention_packed_backward, "qk_attention_packed_backward", index, desc, g, at, nbytes, _at(status))
+    return dq, dk, dv
 
 
 @dataclass

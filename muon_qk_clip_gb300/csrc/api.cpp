@@ -1140,6 +1140,238 @@ mc_status qk_attention_backward(const mc_attn_desc* a, const mc_attn_grad* g, vo
   return ok();
 }
 
+namespace {
+
+// Workspace of the packed attention, in 256-byte aligned parts.
+struct PackedWorkspace {
+  size_t bounds, first, place, blocks, count, nlse, delta, bytes;
+  int64_t capacity, padded;
+};
+PackedWorkspace plan_packed(const mc_packed_desc* a, bool backward, int rows) {
+  PackedWorkspace w;
+  size_t at = 0;
+  auto part = [&](int64_t bytes) {
+    const size_t from = at;
+    at += (size_t)round_up(bytes, 256);
+    return from;
+  };
+  w.capacity = (int64_t)a->T / rows + a->nseq;
+  w.padded = packed_padded_rows(a->T, a->nseq);
+  w.count = part(64);
+  w.bounds = part(((int64_t)a->nseq + 1) * 4);
+  w.first = part((int64_t)a->nseq * 4);
+  w.place = part((w.capacity + 1) * 4);
+  w.blocks = part(w.capacity * 16);
+  w.nlse = part(backward ? a->H * w.padded * 4 : 0);
+  w.delta = part(backward ? a->H * w.padded * 4 : 0);
+  w.bytes = at;
+  return w;
+}
+
+// Rows per block of the forward's plan: two tiles share their keys and values, of
+// two heads if a group has them in pairs, else of two blocks of one head.
+int packed_rows(const mc_packed_desc* a) { return a->H / a->H_kv % 2 == 0 ? 128 : 256; }
+
+mc_status check_packed_shape(const mc_packed_desc* a) {
+  if (!a) return fail(MC_ERR_INVALID_ARG, "packed attention: null descriptor");
+  if (a->T < 0 || a->nseq < 1 || a->H < 1 || a->H_kv < 1 || a->H % a->H_kv)
+    return fail(MC_ERR_INVALID_ARG, "packed attention: T %d, nseq %d, H %d, H_kv %d (T >= 0, the others >= 1, H a multiple of H_kv)", a->T,
+                a->nseq, a->H, a->H_kv);
+  if (a->dtype != MC_F32 && a->dtype != MC_BF16) return fail(MC_ERR_INVALID_ARG, "packed attention: unknown dtype %d", a->dtype);
+  if (a->dtype != MC_BF16) return fail(MC_ERR_UNSUPPORTED, "packed attention: bf16 only");
+  if (a->d < 16 || a->d > 128 || a->d_v < 16 || a->d_v > 128)
+    return fail(MC_ERR_UNSUPPORTED, "packed attention: widths d %d, d_v %d outside [16, 128]", a->d, a->d_v);
+  // places among padded rows are 32-bit, work items below 2^30
+  if (a->T > (1 << 30) || a->nseq > (1 << 22) || a->H > (1 << 16) || ((int64_t)a->T / 128 + a->nseq) * a->H >= (1ll << 30))
+    return fail(MC_ERR_UNSUPPORTED, "packed attention: T %d, nseq %d, H %d are too large", a->T, a->nseq, a->H);
+  return MC_OK;
+}
+
+struct PackedTensor {
+  const char* name;
+  const void* ptr;
+  const int64_t* st;
+  int64_t heads, width;
+  bool out;
+  long long* to;
+};
+
+// Checks the tensors, offsets, lse, status and workspace of a packed call: their
+// layout, and that nothing that the call writes lies among anything else.
+mc_status check_packed(const mc_packed_desc* a, PackedTensor* ts, int nt, const float* lse, bool lse_out, const float* smax,
+                       void* workspace, size_t need, size_t have, int32_t* status) {
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return fail(MC_ERR_INVALID_ARG, "packed attention: scale must be finite and > 0");
+  auto addr = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  if (!a->offsets || addr(a->offsets) % 4) return fail(MC_ERR_INVALID_ARG, "packed attention: offsets must be given, 4-byte aligned");
+  if (addr(lse) % 4 || addr(smax) % 4 || addr(status) % 4)
+    return fail(MC_ERR_INVALID_ARG, "packed attention: lse, smax and status must be 4-byte aligned");
+  if (!workspace || addr(workspace) % 256)
+    return fail(MC_ERR_WORKSPACE, "packed attention: workspace must be given, 256-byte aligned");
+  struct Named { const char* name; Span at; bool out; int tensor; };
+  Named all[16];
+  int n = 0;
+  for (int i = 0; i < nt && a->T > 0; ++i) {
+    const int64_t ext[2] = {a->T, ts[i].heads};
+    const mc_status st = check_attn_tensor(ts[i].name, ts[i].ptr, ts[i].st, 2, ext, ts[i].width, ts[i].out, ts[i].to);
+    if (st != MC_OK) return st;
+    // the tiles' maps have a stride of 2^34 elements less the tokens'
+    if (ts[i].to[0] > (1ll << 33))
+      return fail(MC_ERR_UNSUPPORTED, "packed attention: %s strides are too large", ts[i].name);
+    const int64_t last = ts[i].width + (ext[0] - 1) * ts[i].to[0] + (ext[1] - 1) * ts[i].to[1];
+    all[n++] = {ts[i].name, span_of(ts[i].ptr, last * 2), ts[i].out, i};
+  }
+  all[n++] = {"offsets", span_of(a->offsets, ((int64_t)a->nseq + 1) * 4), false, -1};
+  if (lse && a->T > 0) all[n++] = {"lse", span_of(lse, (int64_t)a->H * a->T * 4), lse_out, -1};
+  if (smax) all[n++] = {"smax", span_of(smax, (int64_t)a->H * 4), true, -1};
+  if (status) all[n++] = {"status", span_of(status, 4), true, -1};
+  all[n++] = {"the workspace", span_of(workspace, (int64_t)need), true, -1};
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j) {
+      if ((!all[i].out && !all[j].out) || !meet(all[i].at, all[j].at)) continue;
+      const int x = all[i].tensor, y = all[j].tensor;
+      if (all[i].out && all[j].out && x >= 0 && y >= 0 && all[i].at.lo != all[j].at.lo) {
+        // axes: token, head; with different numbers of heads, their blocks under a
+        // token must lie side by side
+        const int64_t apart = ((int64_t)all[j].at.lo - (int64_t)all[i].at.lo) / 2;
+        const int64_t ei[2] = {a->T, ts[x].heads}, ej[2] = {a->T, ts[y].heads};
+        if (ei[1] == ej[1] && interleave(ts[x].st, 2, ts[x].width, ts[y].st, 2, ts[y].width, ei, apart)) continue;
+        const int64_t sx = ts[x].to[0], wx = (ei[1] - 1) * ts[x].to[1] + ts[x].width, wy = (ej[1] - 1) * ts[y].to[1] + ts[y].width;
+        if (sx == ts[y].to[0] && sx > 0) {
+          const int64_t r = ((apart % sx) + sx) % sx;
+          if (r >= wx && r + wy <= sx) continue;
+        }
+      }
+      return fail(MC_ERR_INVALID_ARG, "packed attention: %s overlaps %s", all[all[i].out ? i : j].name, all[all[i].out ? j : i].name);
+    }
+  if (have < need) return fail(MC_ERR_WORKSPACE, "packed attention: workspace of %zu bytes, %zu needed", have, need);
+  return MC_OK;
+}
+
+PackedPlan packed_plan(const mc_packed_desc* a, const PackedWorkspace& w, void* workspace, int rows, float* smax, int32_t* status) {
+  char* base = static_cast<char*>(workspace);
+  PackedPlan p;
+  memset(&p, 0, sizeof p);
+  p.offsets = a->offsets;
+  p.T = a->T; p.nseq = a->nseq; p.H = a->H;
+  p.rows = rows;
+  p.capacity = (int)w.capacity;
+  p.bounds = reinterpret_cast<int*>(base + w.bounds);
+  p.first = reinterpret_cast<int*>(base + w.first);
+  p.place = reinterpret_cast<int*>(base + w.place);
+  p.blocks = reinterpret_cast<int4*>(base + w.blocks);
+  p.count = reinterpret_cast<int*>(base + w.count);
+  p.counter = p.count + 4;
+  p.smax = smax;
+  p.status = status;
+  return p;
+}
+
+// Heads of a work order's group: `per` for each key head whose keys and values fit
+// half of L2 together.
+packed::Order packed_order(const mc_packed_desc* a, int per) {
+  const int64_t bytes = (int64_t)a->T * (a->d + a->d_v) * 2, fit = std::max<int64_t>(1, (64ll << 20) / std::max<int64_t>(1, bytes));
+  return {a->H_kv * per, (int)std::min<int64_t>(fit, a->H_kv) * per};
+}
+
+}  // namespace
+
+mc_status qk_attention_packed_workspace_size(const mc_packed_desc* a, int32_t backward, size_t* bytes) {
+  mc_status st = check_packed_shape(a);
+  if (st != MC_OK) return st;
+  if (!bytes) return fail(MC_ERR_INVALID_ARG, "bytes: null");
+  *bytes = plan_packed(a, backward != 0, backward ? 128 : packed_rows(a)).bytes;
+  return ok();
+}
+
+mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const int64_t o_strides[2], float* lse, float* smax,
+                                      int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* status,
+                                      mc_stream_t stream) {
+  mc_status st = check_packed_shape(a);
+  if (st != MC_OK) return st;
+  if (!smax || !o_strides) return fail(MC_ERR_INVALID_ARG, "packed attention: need smax and o's strides");
+  PackedFwdParams p;
+  memset(&p, 0, sizeof p);
+  p.T = a->T; p.H = a->H; p.group = a->H / a->H_kv; p.d = a->d; p.d_v = a->d_v;
+  const int rows = packed_rows(a);
+  p.pair = rows == 128;
+  p.scale = a->scale;
+  PackedTensor ts[] = {{"q", a->q, a->q_strides, a->H, a->d, false, p.qs},
+                       {"k", a->k, a->k_strides, a->H_kv, a->d, false, p.ks},
+                       {"v", a->v, a->v_strides, a->H_kv, a->d_v, false, p.vs},
+                       {"o", o, o_strides, a->H, a->d_v, true, p.os}};
+  const PackedWorkspace w = plan_packed(a, false, rows);
+  if ((st = check_packed(a, ts, 4, lse, true, smax, workspace, w.bytes, workspace_bytes, status)) != MC_OK) return st;
+  const PackedPlan plan = packed_plan(a, w, workspace, rows, accumulate ? nullptr : smax, status);
+  p.q = a->q; p.k = a->k; p.v = a->v; p.o = o;
+  p.lse = lse;
+  p.smax = smax;
+  p.order = packed_order(a, p.pair ? p.group / 2 : p.group);
+  p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
+  p.count = plan.count;
+  p.counter = plan.counter;
+  p.status = status;
+  char err[256] = {0};
+  cudaError_t e;
+  {
+    ProfScope ps(kAttnFwd, a->T > 0 ? 2 : 1, (cudaStream_t)stream);
+    e = launch_packed_plan(plan, (cudaStream_t)stream);
+    if (e == cudaSuccess && a->T > 0) e = launch_packed_fwd(p, plan.capacity, (cudaStream_t)stream, err, sizeof err);
+  }
+  if (e != cudaSuccess) {
+    if (err[0]) return fail(MC_ERR_CUDA, "packed attention: %s", err);
+    return cuda_fail(e, "packed attention launch");
+  }
+  return ok();
+}
+
+mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_grad* g, void* workspace,
+                                       size_t workspace_bytes, int32_t* status, mc_stream_t stream) {
+  mc_status st = check_packed_shape(a);
+  if (st != MC_OK) return st;
+  if (!g) return fail(MC_ERR_INVALID_ARG, "packed attention: null gradient descriptor");
+  if (!g->lse && a->T > 0) return fail(MC_ERR_INVALID_ARG, "packed attention: lse must be given");
+  PackedBwdParams p;
+  memset(&p, 0, sizeof p);
+  p.T = a->T; p.H = a->H; p.group = a->H / a->H_kv; p.d = a->d; p.d_v = a->d_v;
+  p.scale = a->scale;
+  PackedTensor ts[] = {{"q", a->q, a->q_strides, a->H, a->d, false, p.qs},
+                       {"k", a->k, a->k_strides, a->H_kv, a->d, false, p.ks},
+                       {"v", a->v, a->v_strides, a->H_kv, a->d_v, false, p.vs},
+                       {"o", g->o, g->o_strides, a->H, a->d_v, false, p.os},
+                       {"d_o", g->d_o, g->do_strides, a->H, a->d_v, false, p.dos},
+                       {"dq", g->dq, g->dq_strides, a->H, a->d, true, p.dqs},
+                       {"dk", g->dk, g->dk_strides, a->H_kv, a->d, true, p.dks},
+                       {"dv", g->dv, g->dv_strides, a->H_kv, a->d_v, true, p.dvs}};
+  const PackedWorkspace w = plan_packed(a, true, 128);
+  if ((st = check_packed(a, ts, 8, g->lse, false, nullptr, workspace, w.bytes, workspace_bytes, status)) != MC_OK) return st;
+  if (a->T == 0) return ok();
+  const PackedPlan plan = packed_plan(a, w, workspace, 128, nullptr, status);
+  p.q = a->q; p.k = a->k; p.v = a->v; p.o = g->o; p.d_o = g->d_o;
+  p.lse = g->lse;
+  p.dq = g->dq; p.dk = g->dk; p.dv = g->dv;
+  p.nlse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.nlse);
+  p.ndelta = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.delta);
+  p.padded = w.padded;
+  p.by_key_head = packed_order(a, 1);
+  p.by_head = packed_order(a, p.group);
+  p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
+  p.count = plan.count;
+  p.counter = plan.counter;
+  p.status = status;
+  char err[256] = {0};
+  cudaError_t e;
+  {
+    ProfScope ps(kAttnBwd, 3, (cudaStream_t)stream);
+    e = launch_packed_plan(plan, (cudaStream_t)stream);
+    if (e == cudaSuccess) e = launch_packed_bwd(p, plan.capacity, (cudaStream_t)stream, err, sizeof err);
+  }
+  if (e != cudaSuccess) {
+    if (err[0]) return fail(MC_ERR_CUDA, "packed attention: %s", err);
+    return cuda_fail(e, "packed attention launch");
+  }
+  return ok();
+}
+
 mc_status qk_clip_apply(const float* smax, int32_t H, float tau, int32_t mode,
                         const mc_clip_seg* segs, int32_t nsegs, float* gamma_out,
                         int32_t* nclipped, int32_t* status, mc_stream_t stream) {

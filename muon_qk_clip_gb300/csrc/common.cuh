@@ -185,6 +185,14 @@ __device__ inline void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint6
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
       : "memory");
 }
+__device__ inline void tma_load_5d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t x,
+                                   int32_t y, int32_t z, int32_t w, int32_t u) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(u)
+      : "memory");
+}
 // Bring the line holding `p` into L2 (no registers, no completion to wait for).
 __device__ inline void prefetch_l2(const void* p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));

@@ -290,6 +290,72 @@ long long attn_bwd_padded_rows(int S);                       // sp
 bool attn_bwd_supported(const AttnBwdParams& p, char* err, size_t errlen);
 cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, size_t errlen);
 
+// ------------------------------------------------ attention over packed sequences
+// Place of a sequence's first row among rows padded to whole 128-row blocks:
+// sequences begin on multiples of four (16-byte copies of fp32) and leave at least
+// 128 places behind their last row.
+__host__ __device__ inline constexpr int packed_pad(int start, int sequence) { return start / 4 * 4 + 132 * sequence; }
+inline constexpr int64_t packed_padded_rows(int64_t T, int64_t nseq) { return round_up(T + 132 * (nseq + 1), 32); }
+
+// The list of a call's row blocks, made on the device from the offsets.
+struct PackedPlan {
+  const int* offsets;      // [nseq + 1]
+  int T, nseq, H;
+  int rows;                // per block: 128, or 256 (pairs of them)
+  int capacity;            // T / rows + nseq: more blocks there cannot be
+  int* bounds;             // workspace [nseq + 1]
+  int* first;              // workspace [nseq]
+  int* place;              // workspace [capacity + 1]
+  int4* blocks;            // workspace [capacity]: start, length, index in the sequence, padded start
+  int* count;              // workspace: blocks
+  int* counter;            // workspace [2]: the next work items, zeroed
+  float* smax;             // [H], set to -inf, or null
+  int32_t* status;
+};
+cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t s);
+
+namespace packed {
+struct Block;
+struct Order {
+  int heads, group;        // of an item's heads: in all, and next to each other (their keys and values fit L2)
+};
+}  // namespace packed
+
+struct PackedFwdParams {
+  int T, H, group, d, d_v; // group: query heads per key head
+  int pair;                // an item is two heads of a group (else two blocks of rows)
+  float scale;
+  const void* q; const void* k; const void* v; void* o;
+  long long qs[2], ks[2], vs[2], os[2];            // element strides (token, head)
+  float* lse;              // [H, T] or null
+  float* smax;             // [H], max-combined in place
+  packed::Order order;
+  const packed::Block* blocks;
+  const int* count;
+  int* counter;
+  int32_t* status;
+};
+// `blocks`: as many as there may be
+cudaError_t launch_packed_fwd(const PackedFwdParams& p, int blocks, cudaStream_t s, char* err, size_t errlen);
+
+struct PackedBwdParams {
+  int T, H, group, d, d_v;
+  float scale;
+  const void* q; const void* k; const void* v; const void* o; const void* d_o;
+  const float* lse;        // [H, T]
+  void* dq; void* dk; void* dv;
+  long long qs[2], ks[2], vs[2], os[2], dos[2], dqs[2], dks[2], dvs[2];
+  float* nlse;             // workspace [H, padded rows]: -lse log2(e), -inf past a sequence
+  float* ndelta;           // workspace [H, padded rows]: -do . o
+  long long padded;
+  packed::Order by_key_head, by_head;              // of the two passes
+  const packed::Block* blocks;
+  const int* count;
+  int* counter;            // [2]
+  int32_t* status;
+};
+cudaError_t launch_packed_bwd(const PackedBwdParams& p, int blocks, cudaStream_t s, char* err, size_t errlen);
+
 // Bounded-wait self-check (one CTA waits on a phase nothing completes).
 cudaError_t launch_wait_selftest(unsigned long long budget_ns, unsigned long long abort_after_ns,
                                  int32_t* status, unsigned long long* waited_ns, cudaStream_t s);

@@ -1,0 +1,274 @@
+"""GPU parity of the packed attention (qk_attention_packed_forward, _backward) with
+64-bit references, sequence by sequence and head group by head group.
+
+Bounds (u = 2^-8: half a step of bf16, relative; w = 2^-24: of fp32), magnitudes
+summed over absolute values:
+  * a logit: the fp32 sum of d products and its scaling, absolute
+        a_ij = w (d + 4) scale |q_i|.|k_j|
+  * numerators: e = a + 2^-22 relative (the hardware's base-2 exponential), u more
+    as an operand; the row sum e too, and n w for its additions
+        o: sum p |v| (u + 2 e + n w), then u |o|
+  * lse: the largest a of the row, 2^-21, 4 w |lse|; S_max: the largest a of the head
+  * the backward's as in the dense one, with the gradients of a group's heads and their
+    bounds added up: the exponent's error a + 4 w |lse|, ds = p (dp - delta): e |ds| +
+    p w (d_v + 4) (|do|.|v| + |do|.|o|) and u |ds| as an operand; dq, dk: the sums of
+    that with |k|, |q|, n w of the sum's magnitude, u of the result
+"""
+import numpy as np
+import pytest
+import torch
+
+from muon_qk_clip_gb300 import abi, build
+from muon_qk_clip_gb300 import binding as mc
+from muon_qk_clip_gb300 import synth
+from tests.gpu_helpers import f64
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+U, W = 2.0 ** -8, 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    abi.load()
+
+
+def features(lens, H, G, d, dv, seed=0, sharp=1.0, tail=0):
+    """bf16 q, k, v, do of sum(lens) + tail tokens, and the offsets."""
+    T = sum(lens) + tail
+    q = synth.normal((T, H, d), 1.0, "pq", seed)
+    q[:, 1::4] *= sharp
+    k, v = synth.normal((T, G, d), 1.0, "pk", seed), synth.normal((T, G, dv), 1.0, "pv", seed)
+    do = synth.normal((T, H, dv), 0.01, "pd", seed)
+    offsets = torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32)
+    return [t.to(BF16).cuda() for t in (q, k, v, do)] + [offsets.cuda()]
+
+
+def pieces(offsets):
+    o = offsets.cpu().tolist()
+    return [(a, b) for a, b in zip(o, o[1:]) if b > a]
+
+
+def reference_forward(q, k, v, offsets, scale=None):
+    """(o, lse, smax) and their bounds, in 64 bits."""
+    Q, K, V = f64(q), f64(k), f64(v)
+    T, H, d = Q.shape
+    g = H // K.shape[1]
+    scale = 1 / np.sqrt(d) if scale is None else scale
+    o, to = np.zeros((T, H, V.shape[2])), np.zeros((T, H, V.shape[2]))
+    lse, tl = np.zeros((H, T)), np.zeros((H, T))
+    smax, ts = np.full(H, -np.inf), np.zeros(H)
+    for a, b in pieces(offsets):
+        n = b - a
+        mask = np.tril(np.ones((n, n), bool))
+        for h in range(H):
+            qq, kk, vv = Q[a:b, h], K[a:b, h // g], V[a:b, h // g]
+            s = np.where(mask, scale * qq @ kk.T, -np.inf)
+            err = np.where(mask, W * (d + 4) * scale * (np.abs(qq) @ np.abs(kk).T), 0.0)
+            top = s.max(1, keepdims=True)
+            p = np.exp(s - top)
+            total = p.sum(1, keepdims=True)
+            p /= total
+            o[a:b, h] = p @ vv
+            e = err + err.max(1, keepdims=True) + 2 * 2.0 ** -22
+            to[a:b, h] = (p * (U + e + n * W)) @ np.abs(vv) * 1.01 + U * np.abs(o[a:b, h]) + 1e-30
+            lse[h, a:b] = (top + np.log(total))[:, 0]
+            tl[h, a:b] = err.max(1) + 2.0 ** -21 + 4 * W * np.abs(lse[h, a:b])
+            smax[h] = max(smax[h], s.max())
+            ts[h] = max(ts[h], err.max())
+    return (o, lse, smax), (to, tl, ts + 1e-12)
+
+
+def check_forward(got, q, k, v, offsets, scale=None):
+    ref, tol = reference_forward(q, k, v, offsets, scale)
+    rows = np.zeros(q.shape[0], bool)
+    for a, b in pieces(offsets):
+        rows[a:b] = True
+    for name, x, r, t, keep in zip(("o", "lse", "smax"), got, ref, tol, (rows, (slice(None), rows), slice(None))):
+        err, t = np.abs(f64(x)[keep] - r[keep]), t[keep]
+        assert np.all(err <= t), f"{name}: {int(np.sum(~(err <= t)))} of {err.size} outside, max err {np.nanmax(err):.3g}"
+
+
+# lengths, query heads, key heads, d, d_v
+CASES = [
+    ([1], 1, 1, 64, 64),
+    ([1], 2, 1, 16, 16),
+    ([128], 2, 2, 128, 128),
+    ([129], 4, 1, 128, 128),
+    ([127, 1, 130], 3, 1, 128, 64),
+    ([256, 257, 255], 1, 1, 64, 128),
+    ([1, 1, 1, 1, 5], 6, 3, 80, 48),
+    ([0, 300, 0, 0, 7, 0], 8, 2, 24, 72),
+    ([385], 5, 5, 40, 120),
+    ([700, 3, 511], 6, 2, 128, 128),
+    ([64, 700], 8, 1, 112, 96),
+]
+
+
+@pytest.mark.parametrize("lens,H,G,d,dv", CASES)
+def test_forward_parity(lens, H, G, d, dv):
+    q, k, v, _, offsets = features(lens, H, G, d, dv, seed=sum(lens), sharp=8.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check_forward(got, q, k, v, offsets)
+    again = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_forward_many_sequences_against_one_by_one():
+    """More sequences than one step of the plan's scans takes, most of them short: equal bits with
+    each sequence alone."""
+    rng = np.random.RandomState(3)
+    lens = [int(x) for x in rng.randint(0, 9, 2500)]
+    lens[7], lens[1400] = 200, 333
+    q, k, v, _, offsets = features(lens, 2, 1, 32, 32)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    torch.cuda.synchronize()
+    at = offsets.cpu().tolist()
+    best = torch.full((2,), -np.inf, device="cuda")
+    for s in [7, 1400, *range(0, 2500, 97)]:
+        a, b = at[s], at[s + 1]
+        if a == b:
+            continue
+        one = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        x, y, z = mc.qk_attention_packed_forward(q[a:b], k[a:b], v[a:b], one, lse=True)
+        assert torch.equal(x, o[a:b]) and torch.equal(y, lse[:, a:b])
+        best = torch.maximum(best, z)
+    assert torch.all(best <= smax)
+
+
+def test_forward_equals_the_dense_one():
+    """Sequences of one length without groups: the dense call's problem."""
+    B, S, H, d = 3, 300, 4, 128
+    q, k, v, _, offsets = features([S] * B, H, H, d, d, sharp=8.0)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    dense = [t.view(B, S, H, d) for t in (q, k, v)]
+    od, ld, sd = mc.qk_attention_forward(*dense, lse=True)
+    torch.cuda.synchronize()
+    assert torch.equal(smax, sd)
+    assert torch.all((o.view(B, S, H, d).float() - od.float()).abs() <= 4 * U * od.float().abs() + 1e-2)
+    assert torch.all((lse - ld.permute(1, 0, 2).reshape(H, -1)).abs() <= 1e-5)
+
+
+def test_rows_of_no_sequence_stay(tail=37):
+    """Tokens before the first offset and behind the last belong to no sequence: whatever they hold
+    (NaN here) reaches nothing, and the outputs' rows stay as they were."""
+    lens, H, G, d = [130, 40], 4, 2, 64
+    q, k, v, _, offsets = features(lens, H, G, d, d, tail=tail)
+    q2, k2, v2 = (torch.cat([t[-tail:], t[:-tail]]) for t in (q, k, v))      # the strangers first
+    n = sum(lens)
+    want = mc.qk_attention_packed_forward(q[:n], k[:n], v[:n], offsets, lse=True)
+    for a, b, c, off, own in ((q, k, v, offsets, slice(0, n)), (q2, k2, v2, offsets + tail, slice(tail, n + tail))):
+        for t in (a, b, c):
+            keep = t[own].clone()
+            t.fill_(float("nan"))
+            t[own] = keep
+        out = torch.full_like(a, 7.0)
+        lse = torch.full((H, n + tail), 7.0, device="cuda")
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = mc.qk_attention_packed_forward(a, b, c, off, out=out, lse=lse, status=st)
+        torch.cuda.synchronize()
+        assert st.item() == 0
+        other = torch.ones(n + tail, dtype=torch.bool, device="cuda")
+        other[own] = False
+        assert torch.all(out[other] == 7.0) and torch.all(lse[:, other] == 7.0)
+        assert torch.equal(out[own], want[0]) and torch.equal(lse[:, own], want[1]) and torch.equal(got[2], want[2])
+
+
+def test_nonfinite_sequences_keep_to_themselves():
+    lens, H, G, d = [100, 150, 60, 90], 4, 1, 128
+    q, k, v, _, offsets = features(lens, H, G, d, d)
+    want = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    k[120, 0, 3], v[200, 0, 5], q[255, 2, 1] = float("inf"), float("nan"), float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == abi.MC_STATUS_NONFINITE_LOGIT
+    keep = torch.ones(400, dtype=torch.bool, device="cuda")
+    keep[100:310] = False
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][:, keep], want[1][:, keep])
+    assert not torch.isfinite(got[0][240]).all()
+
+
+def test_bad_offsets_are_clamped():
+    """Offsets that decrease or leave [0, T]: the status says so, the sequences are those of the
+    offsets made monotone, and nothing lies outside."""
+    q, k, v, _, _ = features([300], 2, 1, 64, 64)
+    bad = torch.tensor([-5, 100, 60, 900, 900], dtype=torch.int32, device="cuda")
+    good = torch.tensor([0, 100, 100, 300, 300], dtype=torch.int32, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_forward(q, k, v, bad, lse=True, status=st)
+    want = mc.qk_attention_packed_forward(q, k, v, good, lse=True)
+    torch.cuda.synchronize()
+    assert st.item() == abi.MC_STATUS_BAD_OFFSETS
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_accumulate_and_no_tokens():
+    q, k, v, _, offsets = features([50, 70], 4, 2, 64, 64)
+    _, _, s = mc.qk_attention_packed_forward(q, k, v, offsets)
+    high = torch.tensor([1e3, -1e3, 1e3, -1e3], device="cuda")
+    _, _, t = mc.qk_attention_packed_forward(q, k, v, offsets, smax=high.clone(), accumulate=True)
+    empty = torch.zeros(3, dtype=torch.int32, device="cuda")
+    _, _, none = mc.qk_attention_packed_forward(q, k, v, empty)
+    _, _, gone = mc.qk_attention_packed_forward(q[:0], k[:0], v[:0], empty)
+    torch.cuda.synchronize()
+    assert torch.equal(t, torch.maximum(high, s))
+    assert torch.all(none == -float("inf")) and torch.all(gone == -float("inf"))
+
+
+def test_views_streams_and_scale():
+    """q, k and v as views of one projection, out in a wider buffer, another stream, an explicit scale."""
+    T, H, G, d = 260, 4, 2, 64
+    both = synth.normal((T, H + 2 * G, d), 1.0, "views", 1).to(BF16).cuda()
+    q, k, v = both[:, :H], both[:, H:H + G], both[:, H + G:]
+    offsets = torch.tensor([0, 200, 260], dtype=torch.int32, device="cuda")
+    wide = torch.full((T, H, d + 24), 7.0, dtype=BF16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = mc.qk_attention_packed_forward(q, k, v, offsets, scale=0.3, out=wide[..., 8:8 + d], lse=True, stream=side)
+    torch.cuda.synchronize()
+    check_forward(got, q, k, v, offsets, 0.3)
+    assert torch.all(wide[..., :8] == 7.0) and torch.all(wide[..., 8 + d:] == 7.0)
+    # heads outside the tokens
+    head_major = [t.transpose(0, 1).contiguous().transpose(0, 1) for t in (q, k, v)]
+    again = mc.qk_attention_packed_forward(*head_major, offsets, scale=0.3, lse=True)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_forward_captured_with_new_offsets():
+    q, k, v, _, offsets = features([100, 156], 4, 2, 64, 64)
+    other = torch.tensor([0, 30, 256], dtype=torch.int32, device="cuda")
+    want = [mc.qk_attention_packed_forward(q, k, v, o, lse=True) for o in (offsets, other)]
+    torch.cuda.synchronize()
+    held = offsets.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mc.qk_attention_packed_forward(q, k, v, held, lse=True)
+    for o, w in zip((offsets, other), want):
+        held.copy_(o)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+def test_long_sequence_against_a_plain_form():
+    """A length off every tile over many key blocks, by a plain fp64 form on the device: o within u
+    of the operands and u of the result, with a tenth for the fp32 errors."""
+    n, H, G, d = 5003, 4, 2, 128
+    q, k, v, _, offsets = features([n], H, G, d, d, sharp=8.0)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    mask = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    for h in range(H):
+        s = (q[:, h].double() @ k[:, h // 2].double().t()) / d ** 0.5
+        s = s.masked_fill(~mask, -float("inf"))
+        p = torch.softmax(s, -1)
+        ref, mag = p @ v[:, h // 2].double(), p @ v[:, h // 2].double().abs()
+        assert torch.all((o[:, h].double() - ref).abs() <= 1.1 * U * mag + U * ref.abs())
+        assert torch.all((lse[h].double() - torch.logsumexp(s, -1)).abs() <= 1e-4)
+        assert abs(float(smax[h]) - float(s.max())) <= 1e-4
