@@ -21,6 +21,11 @@
 // but dQ never leaves the chip as partial sums: one pass would add a 128 x D
 // fp32 tile to global memory per tile pair, in an order that changes the bits.
 //
+// Packed sequences with grouped heads (attn_packed.cu) take the same passes: an item
+// is then a block of one sequence, from the plan's list, the dK / dV pass goes over
+// the query tiles of every head of the key head's group, and every tile is bounded by
+// its sequence.
+//
 // P and dS go from the compute warps to the tensor core through tensor memory
 // (the A operand of dV, dK and dQ), written over the columns of the S / dP that
 // they came from, rounded to bf16 like every operand; sums are fp32.
@@ -32,6 +37,7 @@
 #include "common.cuh"
 #include "fastdiv.cuh"
 #include "kernels.h"
+#include "packed.cuh"
 
 namespace mc {
 namespace {
@@ -47,6 +53,7 @@ constexpr int kThreads = 512;
 constexpr int kRegsIssue = 88, kRegsOutput = 72, kRegsCompute = 176;
 constexpr int CH = BM * 128;             // one 128-row x 64-feature bf16 chunk (128-byte swizzle)
 constexpr uint32_t kTmemCols = 512;
+constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Tiles of the dK / dV pass by the 64-wide chunks of q.k and d_v.  Tensor memory
@@ -86,6 +93,11 @@ struct Geo {
   int full;             // items in whole groups
   long long sp;         // padded row length of nlse and delta
   FastDiv div_h, div_group_items, div_group, div_last;
+  // packed sequences only
+  int q_heads;          // per key head
+  packed::Order order[2];          // of the dK / dV and the dQ pass
+  const packed::Block* blocks;     // the plan's list, heaviest first, and its length
+  const int* count;
 };
 
 // Work order.  Item x is one 128-row block of one (b, h).  Causal blocks differ
@@ -129,6 +141,68 @@ enum Role { kIssue, kOutput, kCompute };
 // All threads of the block, whichever role's code they are in.
 __device__ inline void block_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
+// The n-th item for a whole warp; false on a wait that gave up.
+__device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int* abort_flag) {
+  const int s = n % kRing;
+  if (!warp_wait(&r.full[s], (n / kRing) & 1, abort_flag)) return false;
+  x = (int)__reduce_max_sync(0xffffffffu, (unsigned)r.slot[s]);   // the same in every lane, and uniform to the compiler
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[s]);
+  return true;
+}
+
+// A work item as it is handed out, and where it lies: block `blk` of a sequence of S
+// positions whose first is row `row0` of the tensors and place `at` among a head's
+// padded rows; head h (of the keys in the dK / dV pass, of the queries in the dQ
+// pass).
+struct Where {
+  int b, h, blk, S, row0;
+  long long at;
+};
+template <bool PACKED>
+struct Hand;
+template <>
+struct Hand<false> {
+  using Work = int;
+  using Ring = ab::Ring;
+  static __device__ inline int draw(const AttnBwdParams&, const Geo&, int, int n) { return n; }
+  static __device__ inline bool more(const Geo& g, int x) { return x < g.items; }
+  static __device__ inline Where where(const AttnBwdParams& p, const Geo& g, int x, int pass) {
+    Where w;
+    item_at(p, g, x, pass == 1, w.b, w.h, w.blk);
+    w.S = p.S;
+    w.row0 = 0;
+    w.at = ((long long)w.b * p.H + w.h) * g.sp;
+    return w;
+  }
+};
+template <>
+struct Hand<true> {
+  using Work = packed::Item;
+  using Ring = packed::Ring;
+  static __device__ inline Work draw(const AttnBwdParams& p, const Geo& g, int pass, int n) {
+    return packed::item_at(g.blocks, *g.count, g.order[pass], p.S, BM, n);
+  }
+  static __device__ inline bool more(const Geo&, const Work& x) { return x.head >= 0; }
+  static __device__ inline Where where(const AttnBwdParams&, const Geo& g, const Work& x, int pass) {
+    Where w;
+    w.b = 0;
+    w.h = x.head;
+    w.S = x.b.len;
+    w.row0 = x.b.start;
+    // the last keys of a sequence have the fewest queries: heaviest first from the other end
+    w.blk = pass == 0 ? (x.b.len + BM - 1) / BM - 1 - x.b.index : x.b.index;
+    w.at = (pass == 0 ? 0 : x.head * g.sp) + x.b.pad;
+    return w;
+  }
+};
+// Rows first .. first + R - 1 of the item's sequence, chunk c of head h.
+template <bool PACKED, int R>
+__device__ inline void load_tile(void* dst, const CUtensorMap* map, uint64_t* bar, int c, int h, const Where& w, int first) {
+  if (PACKED) packed::load_rows<R>(dst, map, bar, c, h, packed::Block{w.row0, w.S, 0, 0}, first);
+  else tma_load_4d(dst, map, bar, 64 * c, h, first, w.b);
+}
+
 // 16 lanes x 16 columns: thread t receives, for n = 0, 1, rows t / 4 (r[4n],
 // r[4n + 1]) and t / 4 + 8 (r[4n + 2], r[4n + 3]) of columns 8n + 2 (t % 4) and
 // the next.  Issue only, like tmem_ld_32x32b_x16_async.
@@ -163,15 +237,6 @@ __device__ inline void tc_cp_128x256b(uint32_t taddr, uint64_t sdesc) {
   asm volatile("tcgen05.cp.cta_group::1.128x256b [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
-// The n-th item for a whole warp; false on a wait that gave up.
-__device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int* abort_flag) {
-  const int s = n % kRing;
-  if (!warp_wait(&r.full[s], (n / kRing) & 1, abort_flag)) return false;
-  x = (int)__reduce_max_sync(0xffffffffu, (unsigned)r.slot[s]);   // the same in every lane, and uniform to the compiler
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[s]);
-  return true;
-}
 
 // The same in fp32, to this lane's row of the shared key's partial sums; `n`, a
 // multiple of 8, of its columns exist.
@@ -205,15 +270,27 @@ __device__ inline bool store_part(uint32_t taddr, float* dst, float scale, bool 
 // 16 positions of a head.  Bound by memory: 26.7 us for dense_block's 134 MB (5.0
 // TB/s).
 constexpr int kRowPos = 16, kRowHeads = 8;
+template <bool PACKED>
 __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnBwdParams p, const int sp, const int ni,
-                                                   const int nh) {
+                                                   const int nh, const packed::Block* blocks, const int* count) {
   __shared__ float sums[kRowHeads][kRowPos + 1];
   await_previous();
   release_next();
-  if (blockIdx.x == 0 && threadIdx.x < 2) p.counter[threadIdx.x] = 0;   // of the launches behind this one
-  // block: position group fastest, then head group, then batch
-  const int bi = blockIdx.x / ni, i0 = (blockIdx.x - bi * ni) * kRowPos;
-  const int b = bi / nh, h0 = (bi - b * nh) * kRowHeads;
+  if (!PACKED && blockIdx.x == 0 && threadIdx.x < 2) p.counter[threadIdx.x] = 0;   // of the launches behind this one
+  // block: position group fastest, then head group, then batch; packed: position group
+  // of a listed block of 128 rows, then head group
+  const int bi = blockIdx.x / ni;
+  int i0 = (blockIdx.x - bi * ni) * kRowPos, S = p.S, row0 = 0, pad = 0;
+  const int b = PACKED ? 0 : bi / nh, h0 = (bi - b * nh) * kRowHeads;
+  if (PACKED) {
+    const int e = i0 / BM;
+    if (e >= *count) return;
+    const int4 at = *reinterpret_cast<const int4*>(blocks + e);
+    i0 += (at.z - e) * BM;
+    S = at.y;
+    row0 = at.x;
+    pad = at.w;
+  }
   const int sub = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int c0 = sub * 8;
   // row x: head h0 + x % 8 of position i0 + x / 8 (neighbouring heads are
@@ -225,9 +302,9 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
     for (int n = 0; n < 4; ++n) {
       const int x = x0 + 16 * n, h = h0 + x % kRowHeads, i = i0 + x / kRowHeads;
       a[n] = e[n] = make_uint4(0, 0, 0, 0);
-      if (h < p.H && i < p.S && c0 < p.d_v) {
-        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + i * p.os[1] + h * p.os[2];
-        const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + i * p.dos[1] + h * p.dos[2];
+      if (h < p.H && i < S && c0 < p.d_v) {
+        const __nv_bfloat16* o = static_cast<const __nv_bfloat16*>(p.o) + b * p.os[0] + (row0 + i) * p.os[1] + h * p.os[2];
+        const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(p.d_o) + b * p.dos[0] + (row0 + i) * p.dos[1] + h * p.dos[2];
         if (c0 + 8 <= p.d_v) {
           a[n] = *reinterpret_cast<const uint4*>(o + c0);
           e[n] = *reinterpret_cast<const uint4*>(d + c0);
@@ -261,10 +338,10 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
   }
   __syncthreads();
   const int h = h0 + threadIdx.x / kRowPos, i = i0 + threadIdx.x % kRowPos;
-  if (threadIdx.x < kRowPos * kRowHeads && h < p.H && i < sp) {
-    const long long bh = (long long)b * p.H + h;
-    p.ndelta[bh * sp + i] = -sums[threadIdx.x / kRowPos][threadIdx.x % kRowPos];
-    p.nlse[bh * sp + i] = i < p.S ? -p.lse[bh * p.S + i] * kLog2e : -INFINITY;
+  if (threadIdx.x < kRowPos * kRowHeads && h < p.H && (PACKED || i < sp)) {
+    const long long bh = (long long)b * p.H + h, to = bh * sp + pad + i;
+    p.ndelta[to] = -sums[threadIdx.x / kRowPos][threadIdx.x % kRowPos];
+    p.nlse[to] = i < S ? -p.lse[bh * p.S + row0 + i] * kLog2e : -INFINITY;
   }
 }
 
@@ -289,7 +366,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const __grid_constant__ AttnB
 // queries and thread from shared memory; with a key's whole row per thread every
 // one of these loads was a 16-byte broadcast, 512 bytes of return bandwidth for
 // each four queries of each warp, next to the operand reads of the tensor core.
-template <int NCH, int NCV, int ROLE>
+template <int NCH, int NCV, bool PACKED, int ROLE>
 __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp, const Geo& g, uint8_t* smem, uint64_t* bars,
                                          uint32_t tmem_base, volatile int& abort_flag, int warp, int lane) {
   constexpr int NQ = query_tile(NCH, NCV);
@@ -320,7 +397,8 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
   uint64_t* dk_full = bars + 22;
   uint64_t* dk_empty = bars + 23;
   uint64_t* drain = bars + 24;
-  const Ring ring = {reinterpret_cast<volatile int*>(bars + 34), bars + 25, bars + 29};
+  using H = Hand<PACKED>;
+  const typename H::Ring ring = {reinterpret_cast<volatile int*>(bars + 34), bars + 25, bars + 29};
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1); mbar_init(kv_empty, 1);
     for (int s = 0; s < kStages; ++s) {
@@ -344,8 +422,11 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
   const uint32_t t_dk = tmem_base, t_dv = t_dk + 64 * NCH, t_s = t_dv + 64 * NCV, t_dp = t_s + NQ, t_p = APART ? t_dp + NQ : t_s;
   constexpr uint32_t kHalfP = APART ? NH / 2 : NH;       // second half of the queries in P^T
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
-  // first query tile that has a query at or behind the block's first key
+  // first query tile that has a query at or behind the block's first key, and the
+  // number of the sequence's tiles
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
+  auto end_tile = [&](const Where& w) { return PACKED ? (w.S + NQ - 1) / NQ : g.nt; };
+  const int heads = PACKED ? g.q_heads : 1;                // of the queries, per item
 
   if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
@@ -353,37 +434,41 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       uint32_t li = 0, s = 0, ph = 0;
       bool used_kv = false, used_q[kStages] = {}, used_do[kStages] = {};
       uint32_t par_kv = 0, par_q[kStages] = {}, par_do[kStages] = {};
-      int x = atomicAdd(p.counter, 1), x1 = 0;
+      int next = atomicAdd(p.counter, 1);
+      typename H::Work x = H::draw(p, g, 0, next), x1 = x;
       bool ok = ring_put(ring, 0, x, &abort_flag);
-      for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
-        int b, h, blk;
-        item_at(p, g, x, false, b, h, blk);
-        const int t0 = first_tile(blk);
-        const long long rowbase = ((long long)b * p.H + h) * g.sp;
-        for (int it = t0; it < g.nt; ++it) {
-          if (it == max(t0, g.nt - 2)) x1 = atomicAdd(p.counter, 1);       // used a tile later: its latency is hidden
-          if (it == g.nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+      for (uint32_t n = 1; ok && H::more(g, x); x = x1, ++n) {
+        const Where w = H::where(p, g, x, 0);
+        const int t0 = first_tile(w.blk), end = end_tile(w);
+        int left = (end - t0) * heads;   // tiles of the item
+        for (int it = t0, hh = 0; left > 0; --left, it = it + 1 < end ? it + 1 : (++hh, t0)) {
+          const int h = PACKED ? w.h * heads + hh : w.h;
+          const long long rowbase = PACKED ? h * g.sp + w.at : w.at;
+          const bool first = it == t0 && hh == 0;
+          if (left == 2 || (left == 1 && first)) next = atomicAdd(p.counter, 1);       // used a tile later: its latency is hidden
+          if (left == 1) {
+            x1 = H::draw(p, g, 0, next);
+            if (!ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+          }
           if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&q_full[s], NCH * CQ + 2 * NQ * 4);
-          for (int c = 0; c < NCH; ++c)
-            tma_load_4d(qbuf + (s * NCH + c) * CQ, &mp.q, &q_full[s], 64 * c, h, it * NQ, b);
+          for (int c = 0; c < NCH; ++c) load_tile<PACKED, NQ>(qbuf + (s * NCH + c) * CQ, &mp.q, &q_full[s], c, h, w, it * NQ);
           bulk_load_1d(rowv + s * 2 * NQ, p.nlse + rowbase + it * NQ, NQ * 4, &q_full[s]);
           bulk_load_1d(rowv + s * 2 * NQ + NQ, p.ndelta + rowbase + it * NQ, NQ * 4, &q_full[s]);
           used_q[s] = true; par_q[s] = ph;
           if (!mbar_wait(&do_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&do_full[s], NCV * CQ);
-          for (int c = 0; c < NCV; ++c)
-            tma_load_4d(dobuf + (s * NCV + c) * CQ, &mp.d_o, &do_full[s], 64 * c, h, it * NQ, b);
+          for (int c = 0; c < NCV; ++c) load_tile<PACKED, NQ>(dobuf + (s * NCV + c) * CQ, &mp.d_o, &do_full[s], c, h, w, it * NQ);
           used_do[s] = true; par_do[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
-          if (it == t0) {        // the item's keys and values, behind its first query tile
+          if (first) {           // the item's keys and values, behind its first query tile
             if (!mbar_wait(kv_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
             mbar_arrive_expect_tx(kv_full, (NCH + NCV) * CH);
             for (int c = 0; c < NCH; ++c) {
-              if (c < g.nck) tma_load_4d(kbuf + c * CH, &mp.k, kv_full, 64 * c, h, blk * BM, b);
-              else tma_load_3d(kbuf + c * CH, &mp.ks, kv_full, 64 * (c - g.nck), blk * BM, b);
+              if (PACKED || c < g.nck) load_tile<PACKED, BM>(kbuf + c * CH, &mp.k, kv_full, c, w.h, w, w.blk * BM);
+              else tma_load_3d(kbuf + c * CH, &mp.ks, kv_full, 64 * (c - g.nck), w.blk * BM, w.b);
             }
-            for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + c * CH, &mp.v, kv_full, 64 * c, h, blk * BM, b);
+            for (int c = 0; c < NCV; ++c) load_tile<PACKED, BM>(vbuf + c * CH, &mp.v, kv_full, c, w.h, w, w.blk * BM);
             used_kv = true; par_kv = li & 1;
           }
         }
@@ -455,11 +540,11 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       __syncwarp();
     };
     for (;; ) {
-      int x, b, h, blk;
+      typename H::Work x;
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
-      if (x >= g.items) break;
-      item_at(p, g, x, false, b, h, blk);
-      const int nt = g.nt - first_tile(blk);
+      if (!H::more(g, x)) break;
+      const Where w = H::where(p, g, x, 0);
+      const int nt = (end_tile(w) - first_tile(w.blk)) * heads;
       // S and dP of the previous item have been read: its last p_full and
       // ds_full were waited for below
       bool ok = warp_wait(kv_full, li & 1, &abort_flag) && scores();
@@ -503,13 +588,13 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
     uint32_t li = 0;
     bool bad = false, ok = true;
     for (;; ++li) {
-      int x, b, h, blk;
-      if (!(ok = ring_get(ring, li, x, &abort_flag)) || x >= g.items) break;
-      item_at(p, g, x, false, b, h, blk);
-      const int key = blk * BM + q * 32 + lane;
-      const bool row = key < p.S;
-      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + key * p.dvs[1] + h * p.dvs[2];
-      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + key * p.dks[1] + h * p.dks[2];
+      typename H::Work x;
+      if (!(ok = ring_get(ring, li, x, &abort_flag)) || !H::more(g, x)) break;
+      const Where w = H::where(p, g, x, 0);
+      const int b = w.b, h = w.h, key = w.blk * BM + q * 32 + lane;
+      const bool row = key < w.S;
+      __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + (w.row0 + key) * p.dvs[1] + h * p.dvs[2];
+      __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + (w.row0 + key) * p.dks[1] + h * p.dks[2];
 #pragma unroll 1
       for (int c = 0; c < 2 * (NCV + NCH); ++c) {
         const bool is_v = c < 2 * NCV;
@@ -520,7 +605,7 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
         }
         const int col = 32 * (is_v ? c : c - 2 * NCV);
         const uint32_t from = (is_v ? t_dv : t_dk) + lanes + col;
-        if (is_v || col < 64 * g.nck) {
+        if (is_v || PACKED || col < 64 * g.nck) {
           const int n = (is_v ? p.d_v : p.d_head) - col;
           if (n > 0)
             bad |= store_rows(from, (is_v ? dv : dk) + col, is_v ? 1.f : p.scale, row, is_v ? wide_v : wide_k, n);
@@ -552,15 +637,17 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
     const unsigned long long c22 = two(c2, c2);
     uint32_t t = 0, li = 0, s = 0, sph = 0;
     for (;; ) {
-      int x, b, h, blk;
+      typename H::Work x;
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
-      if (x >= g.items) break;
-      item_at(p, g, x, false, b, h, blk);
+      if (!H::more(g, x)) break;
+      const Where w = H::where(p, g, x, 0);
+      const int t0 = first_tile(w.blk), end = end_tile(w);
       bool ok = true;
-      for (int it = first_tile(blk); it < g.nt; ++it, ++t) {
+      int left = (end - t0) * heads;
+      for (int it = t0; left > 0; --left, it = it + 1 < end ? it + 1 : t0, ++t) {
         const float* nl = rowv + s * 2 * NQ + hf * NH + c0;
         const int i0 = it * NQ + hf * NH;
-        const int key0 = blk * BM + q * 32;
+        const int key0 = w.blk * BM + q * 32;
         const bool diag = p.causal && i0 < key0 + 31;    // some (i, j) of the warp has i < j
         ok = warp_wait(&q_full[s], sph, &abort_flag) && warp_wait(s_full, t & 1, &abort_flag);
         if (!ok) break;
@@ -623,6 +710,9 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full);
+        // a query that sees one key: its softmax is 1 whatever the logit, and ds is 0 (the
+        // dense sequences short enough to notice take a kernel of their own)
+        if (PACKED && i0 + c0 == 0) pv[0][0][0] = pv[0][0][2] = pv[0][1][0] = pv[0][1][2] = 0.f;
 
         ok = warp_wait(dp_full, t & 1, &abort_flag);
         if (!ok) break;
@@ -688,7 +778,7 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
 // dP(t+1) as soon as dP(t) has.  Issue order per key tile t: S(t+1) | dP(t+1),
 // dQ(t).  A key tile is held from S(t) to dQ(t), two products later than the next
 // one's S wants its own, so keys have three stages, and values where they fit.
-template <int NCH, int NCV, int ROLE>
+template <int NCH, int NCV, bool PACKED, int ROLE>
 __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, const Geo& g, uint8_t* smem, uint64_t* bars,
                                          uint32_t tmem_base, volatile int& abort_flag, int warp, int lane) {
   constexpr int BN = key_tile(NCH, NCV), NH = BN / 2;
@@ -716,7 +806,9 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
   uint64_t* drain = bars + 21;
   uint64_t* do_full = bars + 33;
   uint64_t* do_empty = bars + 34;
-  const Ring ring = {reinterpret_cast<volatile int*>(bars + 31), bars + 22, bars + 26};
+  using H = Hand<PACKED>;
+  const typename H::Ring ring = {reinterpret_cast<volatile int*>(bars + (PACKED ? 36 : 31)), bars + 22, bars + 26};
+  static_assert(36 * 8 + packed::kRing * packed::kSlot * 4 <= kBarBytes, "barriers");
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1); mbar_init(q_empty, 1); mbar_init(do_full, 1); mbar_init(do_empty, 1);
     for (int s = 0; s < kStages; ++s) {
@@ -738,8 +830,8 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
   const uint32_t t_dq = tmem_base, t_q = t_dq + 64 * NCH, t_do = t_q + 32 * QT, t_s = t_do + (DOT ? 32 * NCV : 0), t_dp = t_s + BN,
                  t_ds = t_dp + BN;
   auto fail = [&]() { abort_flag = 1; set_status(p.status, MC_STATUS_TIMEOUT); };
-  auto tiles = [&](int blk) {
-    const int hi = p.causal ? min(p.S, (blk + 1) * BM) : p.S;
+  auto tiles = [&](const Where& w) {
+    const int hi = p.causal ? min(w.S, (w.blk + 1) * BM) : w.S;
     return (hi + BN - 1) / BN;
   };
 
@@ -749,41 +841,44 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
       uint32_t li = 0, s = 0, ph = 0, sv = 0, phv = 0;
       bool used_q = false, used_do = false, used_k[kStages] = {}, used_v[VS] = {};
       uint32_t par_q = 0, par_do = 0, par_k[kStages] = {}, par_v[VS] = {};
-      int x = atomicAdd(p.counter + 1, 1), x1 = 0;
+      int next = atomicAdd(p.counter + 1, 1);
+      typename H::Work x = H::draw(p, g, 1, next), x1 = x;
       bool ok = ring_put(ring, 0, x, &abort_flag);
-      for (uint32_t n = 1; ok && x < g.items; x = x1, ++n) {
-        int b, h, blk;
-        item_at(p, g, x, true, b, h, blk);
-        const int nt = tiles(blk);
+      for (uint32_t n = 1; ok && H::more(g, x); x = x1, ++n) {
+        const Where w = H::where(p, g, x, 1);
+        const int nt = tiles(w), kh = PACKED ? w.h / g.q_heads : w.h;      // the head of its keys
         // the queries' buffer is free once the item before has begun
         if (!mbar_wait(q_empty, (li & 1) ^ 1, &abort_flag)) { ok = false; break; }
         mbar_arrive_expect_tx(q_full, NCH * CH);
-        for (int c = 0; c < NCH; ++c) tma_load_4d(qbuf + c * CH, &mp.q, q_full, 64 * c, h, blk * BM, b);
+        for (int c = 0; c < NCH; ++c) load_tile<PACKED, BM>(qbuf + c * CH, &mp.q, q_full, c, w.h, w, w.blk * BM);
         used_q = true; par_q = li & 1;
         auto load_do = [&]() -> bool {
           if (!mbar_wait(do_empty, (li & 1) ^ 1, &abort_flag)) return false;
           mbar_arrive_expect_tx(do_full, NCV * CH);
-          for (int c = 0; c < NCV; ++c) tma_load_4d(dobuf + c * CH, &mp.d_o, do_full, 64 * c, h, blk * BM, b);
+          for (int c = 0; c < NCV; ++c) load_tile<PACKED, BM>(dobuf + c * CH, &mp.d_o, do_full, c, w.h, w, w.blk * BM);
           used_do = true; par_do = li & 1;
           return true;
         };
         if (DOT && !load_do()) { ok = false; break; }
         for (int it = 0; it < nt; ++it) {
-          if (it == max(0, nt - 2)) x1 = atomicAdd(p.counter + 1, 1);      // used a tile later: its latency is hidden
-          if (it == nt - 1 && !ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+          if (it == max(0, nt - 2)) next = atomicAdd(p.counter + 1, 1);    // used a tile later: its latency is hidden
+          if (it == nt - 1) {
+            x1 = H::draw(p, g, 1, next);
+            if (!ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
+          }
           if (!mbar_wait(&k_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&k_full[s], NCH * CK);
           for (int c = 0; c < NCH; ++c) {
             uint8_t* dst = kbuf + (s * NCH + c) * CK;
-            if (c < g.nck) tma_load_4d(dst, &mp.k, &k_full[s], 64 * c, h, it * BN, b);
-            else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, b);
+            if (PACKED || c < g.nck) load_tile<PACKED, BN>(dst, &mp.k, &k_full[s], c, kh, w, it * BN);
+            else tma_load_3d(dst, &mp.ks, &k_full[s], 64 * (c - g.nck), it * BN, w.b);
           }
           used_k[s] = true; par_k[s] = ph;
           if (++s == kStages) { s = 0; ph ^= 1; }
           if (!DOT && it == 0 && !load_do()) { ok = false; break; }        // not needed before the first S
           if (!mbar_wait(&v_empty[sv], phv ^ 1, &abort_flag)) { ok = false; break; }
           mbar_arrive_expect_tx(&v_full[sv], NCV * CK);
-          for (int c = 0; c < NCV; ++c) tma_load_4d(vbuf + (sv * NCV + c) * CK, &mp.v, &v_full[sv], 64 * c, h, it * BN, b);
+          for (int c = 0; c < NCV; ++c) load_tile<PACKED, BN>(vbuf + (sv * NCV + c) * CK, &mp.v, &v_full[sv], c, kh, w, it * BN);
           used_v[sv] = true; par_v[sv] = phv;
           if (++sv == VS) { sv = 0; phv ^= 1; }
         }
@@ -840,11 +935,10 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
       return true;
     };
     for (;; ) {
-      int x, b, h, blk;
+      typename H::Work x;
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
-      if (x >= g.items) break;
-      item_at(p, g, x, true, b, h, blk);
-      const int nt = tiles(blk);
+      if (!H::more(g, x)) break;
+      const int nt = tiles(H::where(p, g, x, 1));
       // The previous item's S and dP are done and have been read: its last
       // s_empty and ds_full were waited for below.  So its queries may be
       // overwritten.
@@ -901,16 +995,16 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     const bool wide = rows_wide(p.dq, p.dqs);
     bool bad = false, ok = true;
     for (uint32_t li = 0;; ++li) {
-      int x, b, h, blk;
-      if (!(ok = ring_get(ring, li, x, &abort_flag)) || x >= g.items) break;
-      item_at(p, g, x, true, b, h, blk);
+      typename H::Work x;
+      if (!(ok = ring_get(ring, li, x, &abort_flag)) || !H::more(g, x)) break;
+      const Where w = H::where(p, g, x, 1);
       if (!(ok = warp_wait(acc_full, li & 1, &abort_flag))) break;
       tc_fence_after();
-      const int i = blk * BM + q * 32 + lane;
-      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + b * p.dqs[0] + i * p.dqs[1] + h * p.dqs[2];
+      const int i = w.blk * BM + q * 32 + lane;
+      __nv_bfloat16* dq = static_cast<__nv_bfloat16*>(p.dq) + w.b * p.dqs[0] + (w.row0 + i) * p.dqs[1] + w.h * p.dqs[2];
 #pragma unroll 1
       for (int col = 0; col < D; col += 32)
-        bad |= store_rows(t_dq + lanes + col, dq + col, p.scale, i < p.S, wide, D - col);
+        bad |= store_rows(t_dq + lanes + col, dq + col, p.scale, i < w.S, wide, D - col);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);
@@ -927,16 +1021,16 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     const unsigned long long c22 = two(c2, c2);
     uint32_t t = 0, li = 0;
     // this item and the next one, whose row values are loaded an item ahead
-    int b, h, blk, b1, h1, blk1;
+    Where w, w1 = {};
     float nl = 0.f, dl = 0.f, nl1 = 0.f, dl1 = 0.f;
     bool more = true;
     auto fetch = [&](uint32_t n) -> bool {   // item n: coordinates, nlse and delta of this thread's query
-      int x;
+      typename H::Work x;
       if (!ring_get(ring, n, x, &abort_flag)) return false;
-      more = x < g.items;
+      more = H::more(g, x);
       if (more) {
-        item_at(p, g, x, true, b1, h1, blk1);
-        const long long at = ((long long)b1 * p.H + h1) * g.sp + blk1 * BM + row;   // inside: sp is padded to whole blocks
+        w1 = H::where(p, g, x, 1);
+        const long long at = w1.at + w1.blk * BM + row;   // inside: places are padded to whole blocks
         nl1 = p.nlse[at];
         dl1 = p.ndelta[at];
       }
@@ -944,13 +1038,13 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
     };
     bool ok = fetch(0);
     while (ok && more) {
-      b = b1; h = h1; blk = blk1; nl = nl1; dl = dl1;
+      w = w1; nl = nl1; dl = dl1;
       const unsigned long long nl2 = two(nl, nl), dl2 = two(dl, dl);
-      const int i = blk * BM + row;                      // this thread's query
-      const int nt = tiles(blk);
+      const int blk = w.blk, i = blk * BM + row;         // this thread's query
+      const int nt = tiles(w);
       for (int it = 0; it < nt; ++it, ++t) {
         const int j0 = it * BN + hf * NH;
-        const bool full = j0 + NH <= p.S && (!p.causal || j0 + NH - 1 <= blk * BM + q * 32);
+        const bool full = j0 + NH <= w.S && (!p.causal || j0 + NH - 1 <= blk * BM + q * 32);
         if (it == nt - 1 && !(ok = fetch(li + 1))) break;
         ok = warp_wait(s_full, t & 1, &abort_flag);
         if (!ok) break;
@@ -983,7 +1077,8 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
           for (int x = 0; x < NH; x += 2) dscores2(pv[x], pv[x + 1], r[x / 16][x % 16], r[x / 16][x % 16 + 1], dl2);
         }
         if (!full) {
-          const int lim = p.causal ? min(i, p.S - 1) : p.S - 1;   // last key of this row
+          // last key of this row; where there is only one, none: as in the dK / dV pass
+          const int lim = PACKED && i == 0 ? -1 : p.causal ? min(i, w.S - 1) : w.S - 1;
 #pragma unroll
           for (int x = 0; x < NH; ++x)
             if (j0 + x > lim) pv[x] = 0.f;
@@ -1033,8 +1128,6 @@ __device__ __forceinline__ void dq_pass(const AttnBwdParams& p, const Maps& mp, 
 // the dK / dV pass where the products alone need 2048, and 1400 per 96-key tile of
 // the dQ pass (products 1152), and at the change of items about 2900 clocks more.
 // DRAM moves 545 + 184 MB in 568 us (dense_block).
-constexpr int kBarBytes = 512;           // mbarriers and item ring of one pass
-
 template <int NCH, int NCV>
 constexpr size_t smem_bytes() {
   const size_t nq = query_tile(NCH, NCV), nk = key_tile(NCH, NCV), own = (size_t)(NCH + NCV);
@@ -1043,7 +1136,7 @@ constexpr size_t smem_bytes() {
   return 1024 + 2 * kBarBytes + (kv > q ? kv : q);      // 1024: alignment
 }
 
-template <int NCH, int NCV>
+template <int NCH, int NCV, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Maps kv, const __grid_constant__ Maps qm,
                const __grid_constant__ Geo g) {
@@ -1069,17 +1162,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // leaves the flag up: the second one ends at its first wait.)
   if (warp < 4) {
     regs_release<kRegsIssue>();
-    dkv_pass<NCH, NCV, kIssue>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
-    dq_pass<NCH, NCV, kIssue>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
+    dkv_pass<NCH, NCV, PACKED, kIssue>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, PACKED, kIssue>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
     if (warp == 1) tmem_dealloc(tmem_base, kTmemCols);
   } else if (warp < 8) {
     regs_release<kRegsOutput>();
-    dkv_pass<NCH, NCV, kOutput>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
-    dq_pass<NCH, NCV, kOutput>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
+    dkv_pass<NCH, NCV, PACKED, kOutput>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, PACKED, kOutput>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
   } else {
     regs_acquire<kRegsCompute>();
-    dkv_pass<NCH, NCV, kCompute>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
-    dq_pass<NCH, NCV, kCompute>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
+    dkv_pass<NCH, NCV, PACKED, kCompute>(p, kv, g, data, bars, tmem_base, abort_flag, warp, lane);
+    dq_pass<NCH, NCV, PACKED, kCompute>(p, qm, g, data, bars2, tmem_base, abort_flag, warp, lane);
   }
 }
 
@@ -1364,12 +1457,12 @@ bool geometry(const AttnBwdParams& p, Geo& g, char* err, size_t errlen) {
   return true;
 }
 
-template <int NCH, int NCV>
+template <int NCH, int NCV, bool PACKED>
 cudaError_t launch_passes(const AttnBwdParams& p, const Maps& kv, const Maps& qm, const Geo& g, int grid, cudaStream_t s) {
   constexpr size_t smem = smem_bytes<NCH, NCV>();
-  const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<NCH, NCV>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const cudaError_t e = cudaFuncSetAttribute(bwd_kernel<NCH, NCV, PACKED>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_behind(bwd_kernel<NCH, NCV>, (unsigned)grid, kThreads, smem, s, p, kv, qm, g);
+  return launch_behind(bwd_kernel<NCH, NCV, PACKED>, (unsigned)grid, kThreads, smem, s, p, kv, qm, g);
 }
 
 }  // namespace ab
@@ -1435,15 +1528,68 @@ cudaError_t launch_attn_bwd(const AttnBwdParams& p, cudaStream_t s, char* err, s
   const int sms = sm_count();
   const long long ni = cdiv(g.sp, kRowPos), nh = cdiv(p.H, kRowHeads);
   if (ni * nh * p.B > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
-  cudaError_t e = launch_behind(rows_kernel, (unsigned)(ni * nh * p.B), 256, 0, s, p, (int)g.sp, (int)ni, (int)nh);
+  cudaError_t e = launch_behind(rows_kernel<false>, (unsigned)(ni * nh * p.B), 256, 0, s, p, (int)g.sp, (int)ni, (int)nh, nullptr, nullptr);
   if (e != cudaSuccess) return e;
   const int grid = 2 * g.items < sms ? 2 * g.items : sms;
   using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
-  static const Launch by_chunks[3][2] = {{launch_passes<1, 1>, launch_passes<1, 2>},
-                                         {launch_passes<2, 1>, launch_passes<2, 2>},
-                                         {launch_passes<3, 1>, launch_passes<3, 2>}};
+  static const Launch by_chunks[3][2] = {{launch_passes<1, 1, false>, launch_passes<1, 2, false>},
+                                         {launch_passes<2, 1, false>, launch_passes<2, 2, false>},
+                                         {launch_passes<3, 1, false>, launch_passes<3, 2, false>}};
   e = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
   return e != cudaSuccess ? e : sum_heads();
+}
+
+// Packed sequences: the dense passes' parameters with one batch, token strides, and
+// the plan's list in the place of the order of blocks.
+cudaError_t launch_packed_bwd(const PackedBwdParams& a, int blocks, cudaStream_t s, char* err, size_t errlen) {
+  using namespace ab;
+  AttnBwdParams p;
+  Geo g;
+  memset(&p, 0, sizeof p);
+  memset(&g, 0, sizeof g);
+  p.B = 1; p.S = a.T; p.H = a.H; p.d_head = a.d; p.d_v = a.d_v;
+  p.causal = 1;
+  p.scale = a.scale;
+  p.q = a.q; p.k = a.k; p.v = a.v; p.o = a.o; p.d_o = a.d_o;
+  p.lse = a.lse;
+  p.dq = a.dq; p.dk = a.dk; p.dv = a.dv;
+  for (int i = 0; i < 2; ++i) {
+    p.os[i + 1] = a.os[i]; p.dos[i + 1] = a.dos[i];
+    p.dqs[i + 1] = a.dqs[i]; p.dks[i + 1] = a.dks[i]; p.dvs[i + 1] = a.dvs[i];
+  }
+  p.nlse = a.nlse; p.ndelta = a.ndelta;
+  p.counter = a.counter;
+  p.status = a.status;
+  g.nch = g.nck = (a.d + 63) / 64;
+  g.ncv = (a.d_v + 63) / 64;
+  g.sp = a.padded;
+  g.q_heads = a.group;
+  g.order[0] = a.by_key_head;
+  g.order[1] = a.by_head;
+  g.blocks = a.blocks;
+  g.count = a.count;
+  const int nq = query_tile(g.nch, g.ncv), nk = key_tile(g.nch, g.ncv), Hkv = a.H / a.group;
+  static_assert(query_tile(2, 2) == BM, "the padded rows end with whole blocks of 128");
+  Maps kv, qm;
+  memset(&kv, 0, sizeof kv);
+  auto encode = [&](CUtensorMap* m, const void* base, int width, int heads, const long long* st, int rows) {
+    return packed::encode_rows(m, base, width, heads, a.T, st, rows);
+  };
+  bool ok = encode(&kv.q, a.q, a.d, a.H, a.qs, nq) && encode(&kv.d_o, a.d_o, a.d_v, a.H, a.dos, nq) &&
+            encode(&kv.k, a.k, a.d, Hkv, a.ks, BM) && encode(&kv.v, a.v, a.d_v, Hkv, a.vs, BM);
+  qm = kv;
+  if (nk != BM) ok = ok && encode(&qm.k, a.k, a.d, Hkv, a.ks, nk) && encode(&qm.v, a.v, a.d_v, Hkv, a.vs, nk);
+  if (!ok) { snprintf(err, errlen, "tensor map encoding failed"); return cudaErrorInvalidValue; }
+  const long long ni = (long long)blocks * (BM / kRowPos), nh = cdiv(a.H, kRowHeads);
+  if (ni * nh > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
+  const cudaError_t e = launch_behind(rows_kernel<true>, (unsigned)(ni * nh), 256, 0, s, p, (int)g.sp, (int)ni, (int)nh, a.blocks, a.count);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)blocks * (a.H + Hkv);
+  const int grid = items < sm_count() ? (int)items : sm_count();
+  using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
+  static const Launch by_chunks[2][2] = {{launch_passes<1, 1, true>, launch_passes<1, 2, true>},
+                                         {launch_passes<2, 1, true>, launch_passes<2, 2, true>}};
+  return by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
 }
 
 }  // namespace mc

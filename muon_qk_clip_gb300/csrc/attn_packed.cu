@@ -584,9 +584,3 @@ cudaError_t launch_packed_fwd(const PackedFwdParams& p, int blocks, cudaStream_t
 }
 
 }  // namespace mc
-namespace mc {
-cudaError_t launch_packed_bwd(const PackedBwdParams&, int, cudaStream_t, char* err, size_t errlen) {
-  snprintf(err, errlen, "not there yet");
-  return cudaErrorInvalidValue;
-}
-}  // namespace mc

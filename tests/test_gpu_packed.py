@@ -272,3 +272,210 @@ def test_long_sequence_against_a_plain_form():
         assert torch.all((o[:, h].double() - ref).abs() <= 1.1 * U * mag + U * ref.abs())
         assert torch.all((lse[h].double() - torch.logsumexp(s, -1)).abs() <= 1e-4)
         assert abs(float(smax[h]) - float(s.max())) <= 1e-4
+
+
+# --------------------------------------------------------------------------------------- backward
+def reference_backward(q, k, v, o, lse, do, offsets, scale=None, of_o=0.0):
+    """(dq, dk, dv) and their bounds, in 64 bits; of_o: relative error of o that delta takes on."""
+    Q, K, V, OG, L, DO = (f64(t) for t in (q, k, v, o, lse, do))
+    T, H, d = Q.shape
+    dvw = V.shape[2]
+    g = H // K.shape[1]
+    scale = 1 / np.sqrt(d) if scale is None else scale
+    out = [np.zeros_like(x) for x in (Q, K, V)]
+    tol = [np.zeros_like(x) for x in (Q, K, V)]
+    for a, b in pieces(offsets):
+        n = b - a
+        mask = np.tril(np.ones((n, n), bool))
+        for h in range(H):
+            qq, kk, vv, oo, dd = Q[a:b, h], K[a:b, h // g], V[a:b, h // g], OG[a:b, h], DO[a:b, h]
+            p = np.where(mask, np.exp(np.minimum(scale * qq @ kk.T - L[h, a:b][:, None], 700.0)), 0.0)
+            e = W * (d + 4) * scale * (np.abs(qq) @ np.abs(kk).T) + 4 * W * np.abs(L[h, a:b])[:, None] + 2.0 ** -22
+            ds = p * (dd @ vv.T - np.sum(dd * oo, 1)[:, None])
+            mags = np.abs(dd) @ np.abs(vv).T + np.sum(np.abs(dd) * np.abs(oo), 1)[:, None]
+            err = (e + U) * np.abs(ds) + p * (1 + e + U) * W * (dvw + 4) * mags
+            err += p * of_o * np.sum(np.abs(dd) * np.abs(oo), 1)[:, None]
+            ds[0], err[0] = 0.0, 0.0                     # one key
+            out[0][a:b, h] = scale * ds @ kk
+            out[1][a:b, h // g] += scale * ds.T @ qq
+            out[2][a:b, h // g] += p.T @ dd
+            tol[0][a:b, h] = scale * (err + n * W * np.abs(ds)) @ np.abs(kk)
+            tol[1][a:b, h // g] += scale * (err + g * n * W * np.abs(ds)).T @ np.abs(qq)
+            tol[2][a:b, h // g] += ((U + e + g * n * W) * p).T @ np.abs(dd)
+    return out, [x * 1.01 + U * np.abs(r) + 1e-30 for r, x in zip(out, tol)]
+
+
+def check_backward(got, *args):
+    ref, tol = reference_backward(*args)
+    rows = np.zeros(ref[0].shape[0], bool)
+    for a, b in pieces(args[6]):
+        rows[a:b] = True
+    for name, x, r, t in zip(("dq", "dk", "dv"), got, ref, tol):
+        err = np.abs(f64(x) - r)[rows]
+        assert np.all(err <= t[rows]), f"{name}: {int(np.sum(~(err <= t[rows])))} of {err.size} outside, max err {np.nanmax(err):.3g}"
+
+
+def with_forward(lens, H, G, d, dv, **kw):
+    q, k, v, do, offsets = features(lens, H, G, d, dv, **kw)
+    o, lse, _ = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    return q, k, v, o, lse, do, offsets
+
+
+@pytest.mark.parametrize("lens,H,G,d,dv", CASES)
+def test_backward_parity(lens, H, G, d, dv):
+    args = with_forward(lens, H, G, d, dv, seed=sum(lens), sharp=8.0)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_backward(*args, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check_backward(got, *args)
+    again = mc.qk_attention_packed_backward(*args)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_backward_of_single_tokens_is_zero():
+    """Sequences of one token: dq and dk are exactly 0, dv is the group's sum of do."""
+    args = with_forward([1] * 70, 6, 2, 64, 64)
+    dq, dk, dv = mc.qk_attention_packed_backward(*args)
+    torch.cuda.synchronize()
+    assert torch.all(dq == 0) and torch.all(dk == 0)
+    want = args[5].double().view(70, 2, 3, 64).sum(2)
+    assert torch.all((dv.double() - want).abs() <= U * want.abs() + 1e-7)
+
+
+def test_backward_many_sequences_against_one_by_one():
+    rng = np.random.RandomState(4)
+    lens = [int(x) for x in rng.randint(0, 9, 1500)]
+    lens[3], lens[1100] = 200, 333
+    q, k, v, o, lse, do, offsets = with_forward(lens, 4, 2, 32, 32)
+    got = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    torch.cuda.synchronize()
+    at = offsets.cpu().tolist()
+    for s in [3, 1100, *range(0, 1500, 131)]:
+        a, b = at[s], at[s + 1]
+        if a == b:
+            continue
+        one = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        alone = mc.qk_attention_packed_backward(q[a:b], k[a:b], v[a:b], o[a:b], lse[:, a:b].contiguous(), do[a:b], one)
+        assert all(torch.equal(x, y[a:b]) for x, y in zip(alone, got))
+
+
+def test_backward_rows_of_no_sequence_stay_and_outputs_interleave():
+    """Strangers' rows hold NaN and reach nothing; the gradients are views of one buffer, as those
+    of a joint projection."""
+    lens, H, G, d, tail = [130, 40], 4, 2, 64, 50
+    q, k, v, do, offsets = features(lens, H, G, d, d, tail=tail)
+    n = sum(lens)
+    o, lse, _ = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    want = mc.qk_attention_packed_backward(q[:n], k[:n], v[:n], o[:n], lse[:, :n].contiguous(), do[:n], offsets)
+    for t in (q, k, v, o, do):
+        t[n:] = float("nan")
+    lse[:, n:] = float("nan")
+    both = torch.full((n + tail, H + 2 * G, d + 8), 7.0, dtype=BF16, device="cuda")
+    dq, dk, dv = both[:, :H, :d], both[:, H:H + G, :d], both[:, H + G:, :d]
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets, dq=dq, dk=dk, dv=dv, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    assert all(torch.equal(x[:n], y) for x, y in zip((dq, dk, dv), want))
+    assert torch.all(both[n:] == 7.0) and torch.all(both[..., d:] == 7.0)
+
+
+def test_backward_nonfinite_sequences_keep_to_themselves():
+    lens, H, G, d = [100, 150, 60, 90], 4, 1, 128
+    q, k, v, o, lse, do, offsets = with_forward(lens, H, G, d, d)
+    want = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    k[120, 0, 3], v[200, 0, 5], do[255, 2, 1] = float("inf"), float("nan"), float("nan")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == abi.MC_STATUS_NONFINITE_UPDATE
+    keep = torch.ones(400, dtype=torch.bool, device="cuda")
+    keep[100:310] = False
+    assert all(torch.equal(x[keep], y[keep]) for x, y in zip(got, want))
+
+
+def test_backward_equals_the_dense_one():
+    """Sequences of one length without groups: the dense call's problem, tile by tile the same
+    products but for the first query, whose ds is zero here and rounding noise there."""
+    B, S, H, d = 2, 400, 3, 128
+    q, k, v, o, lse, do, offsets = with_forward([S] * B, H, H, d, d)
+    got = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    D = [t.view(B, S, H, d) for t in (q, k, v, o)]
+    ld = lse.view(H, B, S).permute(1, 0, 2).contiguous()
+    dense = mc.qk_attention_backward(*D, ld, do.view(B, S, H, d))
+    torch.cuda.synchronize()
+    for x, y in zip(got, dense):
+        y = y.reshape(B * S, H, d).float()
+        assert torch.all((x.float() - y).abs() <= 2 * U * y.abs() + 1e-6)
+
+
+def test_backward_captured_with_new_offsets():
+    q, k, v, do, offsets = features([100, 156], 4, 2, 64, 64)
+    other = torch.tensor([0, 30, 256], dtype=torch.int32, device="cuda")
+    want = []
+    for o in (offsets, other):
+        out, lse, _ = mc.qk_attention_packed_forward(q, k, v, o, lse=True)
+        want.append(mc.qk_attention_packed_backward(q, k, v, out, lse, do, o))
+    torch.cuda.synchronize()
+    held = offsets.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse, _ = mc.qk_attention_packed_forward(q, k, v, held, lse=True)
+        got = mc.qk_attention_packed_backward(q, k, v, out, lse, do, held)
+    for o, w in zip((offsets, other), want):
+        held.copy_(o)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+def test_gradient_against_differences():
+    """sum(do * o) differentiated numerically in 64 bits, at a few elements, within the bounds with
+    the rounding of o (u) added; the differences are good to 1e-8."""
+    lens, H, G, d = [9, 14], 4, 2, 16
+    q, k, v, o, lse, do, offsets = with_forward(lens, H, G, d, d)
+    got = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    torch.cuda.synchronize()
+    _, tol = reference_backward(q, k, v, o, lse, do, offsets, of_o=1.01 * U)
+    X = [f64(t) for t in (q, k, v)]
+    DO = f64(do)
+
+    def f(Q, K, V):
+        total = 0.0
+        for a, b in pieces(offsets):
+            m = np.tril(np.ones((b - a, b - a), bool))
+            for h in range(H):
+                s = np.where(m, Q[a:b, h] @ K[a:b, h // 2].T / np.sqrt(d), -np.inf)
+                p = np.exp(s - s.max(1, keepdims=True))
+                total += ((p / p.sum(1, keepdims=True) @ V[a:b, h // 2]) * DO[a:b, h]).sum()
+        return total
+
+    rng = np.random.RandomState(0)
+    for n in range(3):
+        for _ in range(25):
+            i = tuple(rng.randint(0, x) for x in X[n].shape)
+            up, down = [x.copy() for x in X], [x.copy() for x in X]
+            up[n][i] += 1e-5
+            down[n][i] -= 1e-5
+            slope = (f(*up) - f(*down)) / 2e-5
+            assert abs(slope - f64(got[n])[i]) <= tol[n][i] + 1e-8
+
+
+def test_backward_long_group_against_a_plain_form():
+    """Several tiles of several heads per key head at a long odd length; the sums in fp64 on the
+    device, errors in the 2-norm: p and ds as bf16 operands 2^-9 each at random, results 2^-9."""
+    n, H, G, d = 3001, 6, 2, 128
+    q, k, v, o, lse, do, offsets = with_forward([n], H, G, d, d, sharp=4.0)
+    dq, dk, dv = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    mask = torch.ones(n, n, dtype=torch.bool, device="cuda").tril()
+    rk, rv = torch.zeros_like(dk, dtype=torch.float64), torch.zeros_like(dv, dtype=torch.float64)
+    for h in range(H):
+        Q, K, V, DO = q[:, h].double(), k[:, h // 3].double(), v[:, h // 3].double(), do[:, h].double()
+        p = torch.exp((Q @ K.t()) / d ** 0.5 - lse[h].double()[:, None]).masked_fill(~mask, 0.0)
+        ds = p * (DO @ V.t() - (DO * o[:, h].double()).sum(-1, keepdim=True))
+        rq = ds @ K / d ** 0.5
+        assert (dq[:, h].double() - rq).norm() <= 0.004 * rq.norm()
+        rk[:, h // 3] += ds.t() @ Q / d ** 0.5
+        rv[:, h // 3] += p.t() @ DO
+    assert (dk.double() - rk).norm() <= 0.004 * rk.norm() and (dv.double() - rv).norm() <= 0.004 * rv.norm()
