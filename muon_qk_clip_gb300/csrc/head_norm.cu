@@ -8,10 +8,10 @@
 //   dx = rstd (g - xhat mean(g xhat)),   dw = sum over tokens and heads of dz xhat
 //
 // Queries and keys share one launch: a warp takes a token and a range of its
-// heads, so it needs the token's sines and cosines once.  A head's row lies over
-// the fewest lanes that hold it 16 bytes each (16 lanes for 128 bf16 features, two
-// heads per warp), its sums over these lanes' shuffles, several rows' loads in
-// flight.  Bound by memory.
+// query or key heads, and needs the token's sines and cosines once for them.  A
+// head's row lies over the fewest lanes that hold it 16 bytes each (16 lanes for 128
+// bf16 features, two heads per warp), its sums over these lanes' shuffles, several
+// rows' loads in flight.  Bound by memory.
 //
 // Turns: a pair's frequency in turns per position is kept as a 64-bit fraction
 // of a turn (from fp64 on the host), and its product with the position, taken
@@ -38,7 +38,10 @@ namespace hn {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxPairs = MC_HEAD_MAX / 2;
 constexpr int kFlight = 4;                        // rows of a lane in flight (the gradient: pairs of rows, half as many)
-constexpr int kBackGrid = 152 * 4;                // blocks (rows of weight sums) of the gradient, at most
+// Blocks of the gradient that an SM holds at once, and blocks (rows of weight sums)
+// at most: one wave.
+__host__ __device__ constexpr int back_blocks(int nu) { return nu == 1 ? 3 : 1; }
+constexpr int kBackGrid = 152 * 3;
 
 struct Side {                                     // queries or keys
   const void* x;                                  // the norm's input
@@ -56,10 +59,10 @@ struct Params {
   float* part;                                    // gradient: [blocks][2][d] weight sums, or null
   int T, d, rot, heads;
   int lanes;                                      // per row: a power of two
-  int span, pieces;                               // heads per warp (whole rows of it), warps per token
+  int span;                                       // heads per unit of work, whole steps of a warp's loop
+  int pieces[2];                                  // units per token and side
   float eps, inv_d;
-  FastDiv div_pieces;
-  long long units;                                // T * pieces, below 2^31
+  FastDiv div_pieces[3];                          // by the units of a token: of queries, of keys, of both
 };
 
 // V neighbouring features of a row.
@@ -109,7 +112,7 @@ struct Feat<T, 2> {                               // a pair, whatever its alignm
 // A lane's features are V from column V * (its lane of the row + lanes * u), u <
 // NU, as long as they are below d.  Sine and cosine per pair; those below the
 // rotated part turn by nothing.
-template <int V, int NU>
+template <int V, int NU, bool FAST>
 struct Turn {
   float c[NU][V / 2], s[NU][V / 2];
   __device__ void at(const Params& p, int pos, int sub) {
@@ -122,7 +125,11 @@ struct Turn {
         s[u][k] = 0.f;
         if (col < p.d && col >= p.d - p.rot) {
           const long long turn = (long long)(p.turn[pair] * (unsigned long long)(long long)pos);
-          sincospif((float)(int)(turn >> 32) * 0x1p-31f, &s[u][k], &c[u][k]);
+          const float half = (float)(int)(turn >> 32) * 0x1p-31f;             // of a turn, within +-1
+          // bf16 rounds to 2^-9: the hardware's sine and cosine, good to 2^-21 absolute
+          // within +-pi, do; fp32 takes the exact ones
+          if (FAST) __sincosf(half * 3.14159265358979f, &s[u][k], &c[u][k]);
+          else sincospif(half, &s[u][k], &c[u][k]);
         }
       }
   }
@@ -137,136 +144,140 @@ __device__ inline float row_sum(float v, int lanes) {
   return v;
 }
 
+// A side's weights as they lie in memory (of a lane's columns).
 template <typename T, int V, int NU>
-__device__ inline void load_weight(const Params& p, const void* w, int sub, float (&x)[NU][V]) {
+struct Weight {
+  Feat<T, V> f[NU];
+  bool given;
+  __device__ void load(const Params& p, const void* w, int sub) {
+    given = w != nullptr;
 #pragma unroll
-  for (int u = 0; u < NU; ++u) {
-    const int col = V * (sub + p.lanes * u);
-    Feat<T, V> f;
-    f.zero();
-    if (w && col < p.d) f.load(static_cast<const T*>(w) + col);
-    f.get(x[u]);
-    if (!w)
-#pragma unroll
-      for (int k = 0; k < V; ++k) x[u][k] = 1.f;
+    for (int u = 0; u < NU; ++u) {
+      const int col = V * (sub + p.lanes * u);
+      f[u].zero();
+      if (w && col < p.d) f[u].load(static_cast<const T*>(w) + col);
+    }
   }
-}
+  __device__ void get(int u, float (&x)[V]) const {
+    f[u].get(x);
+#pragma unroll
+    for (int k = 0; k < V; ++k) x[k] = given ? x[k] : 1.f;
+  }
+};
 
 template <typename T, int V, int NU>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 4 : 2) head_norm_kernel(const __grid_constant__ Params p) {
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
-  float w[2][NU][V];
-  load_weight<T, V, NU>(p, p.side[0].w, sub, w[0]);
-  load_weight<T, V, NU>(p, p.side[1].w, sub, w[1]);
-  const long long warps = (long long)gridDim.x * kWarps;
-  for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.units; unit += warps) {
-    const int t = (int)fastdiv((uint32_t)unit, p.div_pieces), piece = (int)unit - t * p.pieces;
-    const int from = piece * p.span, to = min(p.heads, from + p.span);
-    Turn<V, NU> turn;
-    bool turned = false;
+  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int pieces = p.pieces[0] + p.pieces[1];
+  if (unit >= (long long)p.T * pieces) return;
+  const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[2]), r = (int)unit - t * pieces, side = r >= p.pieces[0];
+  const Side& S = p.side[side];
+  const int from = (r - side * p.pieces[0]) * p.span, to = min(S.heads, from + p.span), base = side ? p.side[0].heads : 0;
+  const T* x = static_cast<const T*>(S.x) + t * S.xt;
+  T* y = static_cast<T*>(S.out) + t * S.ot;
+  Feat<T, V> f[kFlight][NU];
+  // rows h0 + n * (rows of the warp) + this lane's
+  auto load = [&](int h0) {
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const Side& S = p.side[side];
-      const int base = side ? p.side[0].heads : 0;         // this side's first head among both
-      const int h1 = min(to, base + S.heads) - base;
-      const T* x = static_cast<const T*>(S.x) + t * S.xt;
-      T* y = static_cast<T*>(S.out) + t * S.ot;
-      for (int h0 = max(from - base, 0); h0 < h1; h0 += kFlight * rows) {
-        Feat<T, V> f[kFlight][NU];
+    for (int n = 0; n < kFlight; ++n) {
+      const int h = h0 + n * rows + group;
 #pragma unroll
-        for (int n = 0; n < kFlight; ++n) {
-          const int h = h0 + n * rows + group;
+      for (int u = 0; u < NU; ++u) {
+        const int col = V * (sub + p.lanes * u);
+        if (h < to && col < p.d) f[n][u].load(x + h * S.xh + col); else f[n][u].zero();
+      }
+    }
+  };
+  load(from);
+  Weight<T, V, NU> w;
+  w.load(p, S.w, sub);
+  Turn<V, NU, sizeof(T) == 2> turn;
+  turn.at(p, p.positions ? p.positions[t] : t, sub);
+  for (int h0 = from; h0 < to; h0 += kFlight * rows) {
+    if (h0 > from) load(h0);
 #pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const int col = V * (sub + p.lanes * u);
-            if (h < h1 && col < p.d) f[n][u].load(x + h * S.xh + col); else f[n][u].zero();
-          }
+    for (int n = 0; n < kFlight; ++n) {
+      if (h0 + n * rows >= to) break;                       // the whole warp
+      const int h = h0 + n * rows + group;
+      float v[NU][V], sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        f[n][u].get(v[u]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) sum = fmaf(v[u][k], v[u][k], sum);
+      }
+      const float rstd = 1.f / sqrtf(fmaf(row_sum(sum, p.lanes), p.inv_d, p.eps));
+      if (h >= to) continue;
+      if (sub == 0) p.rstd[(long long)t * p.heads + base + h] = rstd;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int col = V * (sub + p.lanes * u);
+        float wt[V];
+        w.get(u, wt);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          v[u][k] *= rstd * wt[k];
+          v[u][k + 1] *= rstd * wt[k + 1];
+          rotate(v[u][k], v[u][k + 1], turn.c[u][k / 2], turn.s[u][k / 2]);
         }
-        if (!turned) {                                       // under the first loads
-          turn.at(p, p.positions ? p.positions[t] : t, sub);
-          turned = true;
-        }
-#pragma unroll
-        for (int n = 0; n < kFlight; ++n) {
-          if (h0 + n * rows >= h1) break;                   // the whole warp
-          const int h = h0 + n * rows + group;
-          float v[NU][V], sum = 0.f;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            f[n][u].get(v[u]);
-#pragma unroll
-            for (int k = 0; k < V; ++k) sum = fmaf(v[u][k], v[u][k], sum);
-          }
-          const float rstd = 1.f / sqrtf(fmaf(row_sum(sum, p.lanes), p.inv_d, p.eps));
-          if (h >= h1) continue;
-          if (sub == 0) p.rstd[(long long)t * p.heads + base + h] = rstd;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const int col = V * (sub + p.lanes * u);
-#pragma unroll
-            for (int k = 0; k < V; k += 2) {
-              v[u][k] *= rstd * w[side][u][k];
-              v[u][k + 1] *= rstd * w[side][u][k + 1];
-              rotate(v[u][k], v[u][k + 1], turn.c[u][k / 2], turn.s[u][k / 2]);
-            }
-            if (col < p.d) Feat<T, V>::store(y + h * S.oh + col, v[u]);
-          }
-        }
+        if (col < p.d) Feat<T, V>::store(y + h * S.oh + col, v[u]);
       }
     }
   }
 }
 
 template <typename T, int V, int NU>
-__global__ void __launch_bounds__(kThreads) head_norm_back_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kernel(const __grid_constant__ Params p) {
   extern __shared__ float sums[];                 // [2][rows of all warps][d] weight sums
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
-  float w[2][NU][V], dw[2][NU][V];
-  load_weight<T, V, NU>(p, p.side[0].w, sub, w[0]);
-  load_weight<T, V, NU>(p, p.side[1].w, sub, w[1]);
+  const int warps = (int)gridDim.x * kWarps, all = kWarps * rows;
+  // queries, then keys: one side's weight and its sums at a time in registers
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const Side& S = p.side[side];
+    const int base = side ? p.side[0].heads : 0, pieces = p.pieces[side];
+    Weight<T, V, NU> w;
+    w.load(p, S.w, sub);
+    float dw[NU][V];
 #pragma unroll
-  for (int i = 0; i < 2 * NU * V; ++i) dw[i / (NU * V)][i / V % NU][i % V] = 0.f;
-  const long long warps = (long long)gridDim.x * kWarps;
-  for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < p.units; unit += warps) {
-    const int t = (int)fastdiv((uint32_t)unit, p.div_pieces), piece = (int)unit - t * p.pieces;
-    const int from = piece * p.span, to = min(p.heads, from + p.span);
-    Turn<V, NU> turn;
-    bool turned = false;
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const Side& S = p.side[side];
-      const int base = side ? p.side[0].heads : 0;
-      const int h1 = min(to, base + S.heads) - base;
+    for (int i = 0; i < NU * V; ++i) dw[i / V][i % V] = 0.f;
+    const long long units = (long long)p.T * pieces;
+    for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < units; unit += warps) {
+      const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[side]);
+      const int from = ((int)unit - t * pieces) * p.span, to = min(S.heads, from + p.span);
       const T* x = static_cast<const T*>(S.x) + t * S.xt;
       const T* g = static_cast<const T*>(S.dy) + t * S.gt;
       T* o = static_cast<T*>(S.out) + t * S.ot;
       const float* rs = p.rstd + (long long)t * p.heads + base;
       constexpr int F = kFlight / 2;
-      for (int h0 = max(from - base, 0); h0 < h1; h0 += F * rows) {
-        Feat<T, V> fx[F][NU], fg[F][NU];
-        float r[F];
+      Feat<T, V> fx[F][NU], fg[F][NU];
+      float r[F];
+      auto load = [&](int h0) {
 #pragma unroll
         for (int n = 0; n < F; ++n) {
           const int h = h0 + n * rows + group;
-          r[n] = h < h1 ? rs[h] : 0.f;
+          r[n] = h < to ? rs[h] : 0.f;
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             const int col = V * (sub + p.lanes * u);
-            if (h < h1 && col < p.d) { fx[n][u].load(x + h * S.xh + col); fg[n][u].load(g + h * S.gh + col); }
+            if (h < to && col < p.d) { fx[n][u].load(x + h * S.xh + col); fg[n][u].load(g + h * S.gh + col); }
             else { fx[n][u].zero(); fg[n][u].zero(); }
           }
         }
-        if (!turned) {
-          turn.at(p, p.positions ? p.positions[t] : t, sub);
-          turned = true;
-        }
+      };
+      load(from);
+      Turn<V, NU, sizeof(T) == 2> turn;
+      turn.at(p, p.positions ? p.positions[t] : t, sub);
+      for (int h0 = from; h0 < to; h0 += F * rows) {
+        if (h0 > from) load(h0);
 #pragma unroll
         for (int n = 0; n < F; ++n) {
-          if (h0 + n * rows >= h1) break;                   // the whole warp
+          if (h0 + n * rows >= to) break;                   // the whole warp
           const int h = h0 + n * rows + group;
           float a[NU][V], b[NU][V], dot = 0.f;
 #pragma unroll
@@ -275,16 +286,18 @@ __global__ void __launch_bounds__(kThreads) head_norm_back_kernel(const __grid_c
             fg[n][u].get(b[u]);
 #pragma unroll
             for (int k = 0; k < V; k += 2) rotate(b[u][k], b[u][k + 1], turn.c[u][k / 2], -turn.s[u][k / 2]);
+            float wt[V];
+            w.get(u, wt);
 #pragma unroll
             for (int k = 0; k < V; ++k) {
               a[u][k] *= r[n];                               // xhat
-              dw[side][u][k] = fmaf(b[u][k], a[u][k], dw[side][u][k]);
-              b[u][k] *= w[side][u][k];
+              dw[u][k] = fmaf(b[u][k], a[u][k], dw[u][k]);
+              b[u][k] *= wt[k];
               dot = fmaf(b[u][k], a[u][k], dot);
             }
           }
           const float mean = row_sum(dot, p.lanes) * p.inv_d;
-          if (h >= h1) continue;
+          if (h >= to) continue;
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
             const int col = V * (sub + p.lanes * u);
@@ -295,18 +308,16 @@ __global__ void __launch_bounds__(kThreads) head_norm_back_kernel(const __grid_c
         }
       }
     }
+    if (p.part)
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int col = V * (sub + p.lanes * u);
+        if (col < p.d)
+#pragma unroll
+          for (int k = 0; k < V; ++k) sums[(side * all + (threadIdx.x >> 5) * rows + group) * p.d + col + k] = dw[u][k];
+      }
   }
   if (!p.part) return;
-  const int all = kWarps * rows;
-#pragma unroll
-  for (int side = 0; side < 2; ++side)
-#pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int col = V * (sub + p.lanes * u);
-      if (col < p.d)
-#pragma unroll
-        for (int k = 0; k < V; ++k) sums[(side * all + (threadIdx.x >> 5) * rows + group) * p.d + col + k] = dw[side][u][k];
-    }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * p.d; i += kThreads) {
     const int side = i >= p.d, col = i - side * p.d;
@@ -430,41 +441,42 @@ mc_status check_shape(const char* me, const mc_heads* h) {
   if (h->rot < 0 || h->rot % 2 || h->rot > h->d) return err(MC_ERR_INVALID_ARG, "%s: rot %d (even, 0..d)", me, h->rot);
   if (!(h->theta > 0.0) || !std::isfinite(h->theta)) return err(MC_ERR_INVALID_ARG, "%s: theta must be finite and > 0", me);
   if (!(h->eps >= 0.f) || !std::isfinite(h->eps)) return err(MC_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", me);
-  if (h->heads_q > (1 << 16) || h->heads_k > (1 << 16) || h->T > 0x7fffffffll ||
-      h->T * ((int64_t)h->heads_q + h->heads_k) > (1ll << 36))
+  if (h->heads_q > (1 << 16) || h->heads_k > (1 << 16) || h->T > (1ll << 29) ||
+      h->T * ((int64_t)h->heads_q + h->heads_k) > (1ll << 34))
     return err(MC_ERR_UNSUPPORTED, "%s: T %lld with %d and %d heads is too large", me, (long long)h->T, h->heads_q, h->heads_k);
   // theta^(-2k/rot) in turns is kept as a fraction of one: finite, and exact enough
   if (h->theta < 1e-6) return err(MC_ERR_UNSUPPORTED, "%s: theta %g below 1e-6", me, h->theta);
   return MC_OK;
 }
 
-// Lanes per row and heads per warp.  A warp takes all heads of a token as long as
-// that makes `most` warps; else they are split, down to one step of its loop.
-void split(Params& p, int units, int flight, int most) {
+// Lanes per row, and heads per unit of work: as many as leave `most` units or more,
+// but 16 steps of the loop at most (a token's sines cost one or two).
+void split(Params& p, int parts, int flight, long long most) {
   p.lanes = 1;
-  while (p.lanes < 32 && p.lanes < units) p.lanes *= 2;
+  while (p.lanes < 32 && p.lanes < parts) p.lanes *= 2;
   const int step = 32 / p.lanes * flight;
-  const int steps = (p.heads + step - 1) / step;
-  const long long want = p.T >= most ? 1 : (most + p.T - 1) / p.T;
-  const int ways = (int)(want < steps ? want : steps);
-  p.span = (steps + ways - 1) / ways * step;
-  p.pieces = (p.heads + p.span - 1) / p.span;
-  p.units = (long long)p.T * p.pieces;
-  p.div_pieces = make_fastdiv((uint32_t)p.pieces);
+  int steps = 16;
+  while (steps > 1 && p.T * cdiv(p.heads, steps * step) < most) steps /= 2;
+  p.span = steps * step;
+  for (int i = 0; i < 2; ++i) p.pieces[i] = (p.side[i].heads + p.span - 1) / p.span;
+  for (int i = 0; i < 3; ++i) {
+    const int n = i < 2 ? p.pieces[i] : p.pieces[0] + p.pieces[1];
+    p.div_pieces[i] = make_fastdiv((uint32_t)(n > 0 ? n : 1));
+  }
 }
 
 template <typename T, int V, int NU>
 cudaError_t run_forward(Params& p, cudaStream_t s) {
-  const int sms = sm_count();
-  split(p, p.d / V, kFlight, sms * 32);
-  const long long blocks = cdiv(p.units, kWarps);
-  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)(blocks < sms * 16ll ? blocks : sms * 16ll), kThreads, 0, s, p);
+  split(p, p.d / V, kFlight, sm_count() * 32);
+  const long long units = (long long)p.T * (p.pieces[0] + p.pieces[1]);
+  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)cdiv(units, kWarps), kThreads, 0, s, p);
 }
 template <typename T, int V, int NU>
 cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
-  split(p, p.d / V, kFlight / 2, kBackGrid * kWarps);
-  const long long blocks = cdiv(p.units, kWarps);
-  const int grid = (int)(blocks < kBackGrid ? blocks : kBackGrid);
+  const int wave = sm_count() * back_blocks(NU), most = wave < kBackGrid ? wave : kBackGrid;
+  split(p, p.d / V, kFlight / 2, 8ll * most * kWarps);      // some units per warp, that the last ones leave few idle
+  const long long blocks = cdiv((long long)p.T * (p.pieces[0] > p.pieces[1] ? p.pieces[0] : p.pieces[1]), kWarps);
+  const int grid = (int)(blocks < most ? blocks : most);
   const size_t smem = p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0;   // a warp's rows have at most 256 features: 16 KB
   const cudaError_t e = launch_behind(head_norm_back_kernel<T, V, NU>, (unsigned)grid, kThreads, smem, s, p);
   if (e != cudaSuccess || !p.part) return e;
