@@ -371,9 +371,10 @@ mc_status qk_attention_packed_workspace_size(const mc_packed_desc* a, int32_t ba
  * max-combined when accumulate = 1; -inf without any token).  o: device [T, H, d_v],
  * strides as above, must not overlap an input; lse: device [H, T] (natural log of
  * the softmax's denominator) or NULL.  Rows that belong to no sequence are left as
- * they were, in o and lse.  Arithmetic as in qk_attention_forward.  A NaN/Inf logit
- * sets MC_STATUS_NONFINITE_LOGIT; NaN/Inf inputs may reach every output of their
- * sequence, and none of another's.  workspace: device, 256-byte aligned, for this
+ * they were, in o and lse.  Arithmetic as in qk_attention_forward.  A NaN/Inf in
+ * a token's q or k, or a logit that overflows to +Inf or NaN, sets
+ * MC_STATUS_NONFINITE_LOGIT (one that overflows to -Inf has weight 0 and need not);
+ * NaN/Inf inputs may reach every output of their sequence, and none of another's.  workspace: device, 256-byte aligned, for this
  * call alone while it runs.  T of 0 only sets smax. */
 mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const int64_t o_strides[2], float* lse, float* smax,
                                       int32_t accumulate, void* workspace, size_t workspace_bytes, int32_t* status,

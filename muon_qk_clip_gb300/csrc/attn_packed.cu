@@ -198,19 +198,20 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
   uint64_t* q_full = bars + 0;       // [2] tiles
   uint64_t* q_empty = bars + 2;      // [2]
   uint64_t* s_full = bars + 4;       // [2]
-  uint64_t* p_full = bars + 6;       // [2] 4 warps
+  uint64_t* p_full = bars + 6;       // [2] 4 warps: all of P
   uint64_t* o_full = bars + 8;       // [2]
   uint64_t* o_empty = bars + 10;     // [2] 4 warps: O and the row sums have been read
   uint64_t* l_full = bars + 12;      // [2] 4 warps: row sums
   uint64_t* drain = bars + 14;
   uint64_t* kv_full = bars + 15;     // [stages <= 6]
   uint64_t* kv_empty = bars + 21;    // [6]
-  const Ring ring = {reinterpret_cast<volatile int*>(bars + 36), bars + 27, bars + 31};
-  static_assert(36 * 8 + kRing * kSlot * 4 <= kBarBytes, "barriers");
+  uint64_t* p_half = bars + 35;      // [2] 4 warps: the first 64 keys of P
+  const Ring ring = {reinterpret_cast<volatile int*>(bars + 38), bars + 27, bars + 31};
+  static_assert(38 * 8 + kRing * kSlot * 4 <= kBarBytes, "barriers");
   if (threadIdx.x == 0) {
     for (int t = 0; t < 2; ++t) {
       mbar_init(&q_full[t], 1); mbar_init(&q_empty[t], 1);
-      mbar_init(&s_full[t], 1); mbar_init(&p_full[t], 4);
+      mbar_init(&s_full[t], 1); mbar_init(&p_full[t], 4); mbar_init(&p_half[t], 4);
       mbar_init(&o_full[t], 1); mbar_init(&o_empty[t], 4);
       mbar_init(&l_full[t], 4);
     }
@@ -293,51 +294,72 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
       if (elect_one()) tc_commit(bar);
       __syncwarp();
     };
-    for (uint32_t li = 0;; ++li) {
-      Item x;
-      if (!ring_get(ring, li, x, &abort_flag)) { ok = false; break; }
-      if (x.head < 0) break;
-      const int n[2] = {tile_of(x, p.pair, 0).nkv, tile_of(x, p.pair, 1).nkv}, nkv = max(n[0], n[1]);
-      if (!(ok = warp_wait(&kv_full[s], ph, &abort_flag))) break;
+    auto weighted = [&](int t, uint32_t stage, int half, bool add) {     // O of tile t (+)= P V for 64 keys
+      if (elect_one()) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (ok && n[t] > 0) {
-          if (!(ok = warp_wait(&q_full[t], nq[t]++ & 1, &abort_flag))) break;
-          tc_fence_after();
-          scores(t, s, n[t] == 1);
-          issued = true;
-        }
-      if (!ok) break;
+        for (int kk = 0; kk < BM / 32; ++kk)
+          tc_mma_ts(tmem + kO + t * BM, tmem + t * BM + (half * BM / 32 + kk) * 8,
+                    dv_ + (stage * kStageBytes) / 16 + (half * BM / 32 + kk) * 128, idesc_o, (add || kk > 0) ? 1u : 0u);
+      }
+      __syncwarp();
+    };
+    // first scores of an item's tile t from the keys in `stage`
+    auto begin = [&](int t, uint32_t stage, int blocks) -> bool {
+      if (!warp_wait(&q_full[t], nq[t]++ & 1, &abort_flag)) return false;
+      tc_fence_after();
+      scores(t, stage, blocks == 1);
+      return true;
+    };
+    Item x;
+    int n[2] = {0, 0};                   // key blocks of the item's tiles
+    auto next_item = [&](uint32_t li) -> bool {
+      if (!ring_get(ring, li, x, &abort_flag)) return false;
+      n[0] = x.head < 0 ? 0 : tile_of(x, p.pair, 0).nkv;
+      n[1] = x.head < 0 ? 0 : tile_of(x, p.pair, 1).nkv;
+      return true;
+    };
+    ok = next_item(0);
+    if (ok && n[0] > 0) {
+      ok = warp_wait(&kv_full[s], ph, &abort_flag) && begin(0, s, n[0]) && (n[1] == 0 || begin(1, s, n[1]));
+      issued = true;
       done(&kv_empty[s]);
       if (++s == kStages) { s = 0; ph ^= 1; }
+    }
+    for (uint32_t li = 1; ok && n[0] > 0; ++li) {
+      const int cur[2] = {n[0], n[1]}, nkv = max(n[0], n[1]);
       for (int j = 0; j < nkv && ok; ++j) {
         const uint32_t sv = s;
         if (!(ok = warp_wait(&kv_full[sv], ph, &abort_flag))) break;
         if (++s == kStages) { s = 0; ph ^= 1; }
-        if (j + 1 < nkv && !(ok = warp_wait(&kv_full[s], ph, &abort_flag))) break;
+        // behind an item's last products come the next item's first scores, tile by tile,
+        // so that the two tiles' softmax stay half a period apart
+        const bool last = j + 1 == nkv;
+        if (last && !(ok = next_item(li))) break;
+        const bool more = !last || n[0] > 0;
+        if (more && !(ok = warp_wait(&kv_full[s], ph, &abort_flag))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          if (j >= n[t]) continue;
-          if (!(ok = warp_wait(&p_full[t], np[t]++ & 1, &abort_flag))) break;
-          if (j == 0 && !(ok = warp_wait(&o_empty[t], (no[t]++ & 1) ^ 1, &abort_flag))) break;
-          tc_fence_after();
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < BM / 16; ++kk)
-              tc_mma_ts(tmem + kO + t * BM, tmem + t * BM + kk * 8, dv_ + (sv * kStageBytes) / 16 + kk * 128, idesc_o, (j > 0 || kk > 0) ? 1u : 0u);
-            if (j + 1 == n[t]) tc_commit(&o_full[t]);
+          if (j < cur[t]) {
+            // the first half of P's keys is multiplied while the second is in the making
+            if (!(ok = warp_wait(&p_half[t], np[t] & 1, &abort_flag))) break;
+            if (j == 0 && !(ok = warp_wait(&o_empty[t], (no[t]++ & 1) ^ 1, &abort_flag))) break;
+            tc_fence_after();
+            weighted(t, sv, 0, j > 0);
+            if (!(ok = warp_wait(&p_full[t], np[t]++ & 1, &abort_flag))) break;
+            tc_fence_after();
+            weighted(t, sv, 1, true);
+            if (j + 1 == cur[t]) done(&o_full[t]);
+            if (j + 1 < cur[t]) scores(t, s, j + 2 == cur[t]);
           }
-          __syncwarp();
-          if (j + 1 < n[t]) scores(t, s, j + 2 == n[t]);
+          if (last && n[t] > 0 && !(ok = begin(t, s, n[t]))) break;
         }
         if (!ok) break;
         done(&kv_empty[sv]);
-        if (j + 1 < nkv) {
+        if (more) {
           done(&kv_empty[s]);
           if (++s == kStages) { s = 0; ph ^= 1; }
         }
       }
-      if (!ok) break;
     }
     if (!ok && lane == 0) fail();
     if (issued) {
@@ -383,7 +405,8 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
     const unsigned long long c22 = two(c2, c2);
     uint32_t ns = 0, no = 0;
     bool ok = true;
-    unsigned long long z = 0;            // zeros, or NaN once a logit is not finite
+    unsigned long long z = 0;            // zeros, or NaN once a logit of the diagonal blocks is not finite
+    bool bad = false;
     for (uint32_t li = 0;; ++li) {
       Item x;
       if (!(ok = ring_get(ring, li, x, &abort_flag)) || x.head < 0) break;
@@ -400,22 +423,33 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < 4; ++c) reg_fence32(r[c]);
-        if (j == tl.nkv - 1) {           // the diagonal: keys up to the row's own
+        // the diagonal block: keys up to the row's own.  Of its four groups of 32 columns a
+        // warp (rows 32 q ..) sees those before q whole, of q those up to the row, and none
+        // behind.  Every token's own logit is here, so a NaN/Inf in its q or k shows here
+        const bool diagonal = j == tl.nkv - 1;
+        const int groups = diagonal ? q + 1 : 4;
+        if (diagonal) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c) {
-            const bool seen = c <= row;
-            if (c % 2 == 0)
-              z = fma2(two(seen ? __uint_as_float(r[c / 32][c % 32]) : 0.f, c < row ? __uint_as_float(r[c / 32][c % 32 + 1]) : 0.f), 0, z);
-            if (!seen) r[c / 32][c % 32] = 0xff800000u;
+          for (int g = 0; g < 4; ++g) {
+            if (g == q) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) {
+                z = fma2(two(c <= lane ? __uint_as_float(r[g][c]) : 0.f, 0.f), 0, z);
+                if (c > lane) r[g][c] = 0xff800000u;
+              }
+            } else if (g < q) {
+#pragma unroll
+              for (int c = 0; c < 32; c += 2) z = fma2(two(__uint_as_float(r[g][c]), __uint_as_float(r[g][c + 1])), 0, z);
+            }
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 128; c += 2) z = fma2(two(__uint_as_float(r[c / 32][c % 32]), __uint_as_float(r[c / 32][c % 32 + 1])), 0, z);
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 128; c += 2)
-          mx[c / 2 % 4] = max3f(mx[c / 2 % 4], __uint_as_float(r[c / 32][c % 32]), __uint_as_float(r[c / 32][c % 32 + 1]));
+        for (int g = 0; g < 4; ++g) {
+          if (g >= groups) break;
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) mx[c / 2 % 4] = max3f(mx[c / 2 % 4], __uint_as_float(r[g][c]), __uint_as_float(r[g][c + 1]));
+        }
         const float mj = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         top = fmaxf(top, mj);
         const bool grow = mj * c2 > m + kLazy;      // always in the first block
@@ -439,19 +473,30 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
         }
         const unsigned long long nm = two(-m, -m);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint32_t w[8];
+        for (int g = 0; g < 4; ++g) {
+          uint32_t w[16];
+          if (g < groups) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int e = 16 * c + 2 * k;
-            float p0, p1;
-            untwo(fma2(two(__uint_as_float(r[e / 32][e % 32]), __uint_as_float(r[e / 32][e % 32 + 1])), c22, nm), p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            l2 = add2(l2, two(p0, p1));
-            w[k] = pack_bf16(p0, p1);
+            for (int k = 0; k < 16; ++k) {
+              float p0, p1;
+              untwo(fma2(two(__uint_as_float(r[g][2 * k]), __uint_as_float(r[g][2 * k + 1])), c22, nm), p0, p1);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              l2 = add2(l2, two(p0, p1));
+              w[k] = pack_bf16(p0, p1);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) w[k] = 0u;
           }
-          tmem_st_32x32b_x8(ts + 8 * c, w);
+          tmem_st_32x32b_x8(ts + 16 * g, w);
+          tmem_st_32x32b_x8(ts + 16 * g + 8, w + 8);
+          if (g == 1) {
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_half[t]);
+          }
         }
         tmem_st_wait();
         tc_fence_before();
@@ -464,6 +509,7 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
       l += l1;
       const int i = tl.row0 + row;
       const bool there = i < x.b.len;
+      bad |= there && !(l <= 3.4e38f);   // NaN or +Inf among the logits
       // the output warps have read the previous item's row sums
       if (!(ok = warp_wait(&o_empty[t], (no++ & 1) ^ 1, &abort_flag))) break;
       inv[t * BM + row] = 1.f / l;
@@ -483,7 +529,7 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
     if (!ok && lane == 0) fail();
     float z0, z1;
     untwo(z, z0, z1);
-    if (__any_sync(0xffffffffu, z0 != 0.f || z1 != 0.f) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_LOGIT);   // NaN differs from 0
+    if (__any_sync(0xffffffffu, bad || z0 != 0.f || z1 != 0.f) && lane == 0) set_status(p.status, MC_STATUS_NONFINITE_LOGIT);   // NaN differs from 0
   }
   tc_fence_before();
   block_sync();
