@@ -540,7 +540,7 @@ typedef struct {
  * p is rounded to its type once; the step uses m and v before an 8-bit state
  * rounds them.  Tensors of any sizes and types share launches (one per set of
  * types and 504 tensors).  Pointers are aligned to their types; tensors whose
- * operands are aligned to four of their values run at full width.  What is
+ * operands are aligned to 32 bytes run at full width.  What is
  * written overlaps nothing else; gradients may overlap each other.  A NaN/Inf
  * reaches its own value, of an 8-bit state every value of its block; one in a
  * new p sets MC_STATUS_NONFINITE_UPDATE.  `t` is read during the call only.

@@ -26,7 +26,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <type_traits>
 #include <vector>
 
 #include "../../include/muonclip.h"
@@ -38,11 +37,16 @@ namespace {
 namespace aw {
 
 constexpr int kThreads = 256;
-constexpr int kSets = 4;                          // groups of four values per thread and chunk
-constexpr int kAhead = 2;                         // sets in flight
-constexpr int kChunk = kThreads * 4 * kSets;      // values per block
-constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale: a warp's 32 x 4
-static_assert(kBlock == 128 && kChunk % kBlock == 0, "a warp holds whole blocks");
+constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale of an 8-bit state
+// Values of a thread's step: four with fp32 states; 16 with 8-bit ones, so that a
+// thread's codes are 16 bytes, and eight threads hold a block.
+constexpr int kWide = 4, kWide8 = 16;
+static_assert(kBlock == 8 * kWide8, "eight threads hold a block");
+// Steps per thread block (together a chunk of a tensor): many where that still leaves
+// every SM some thread blocks, so that few loads stand at a block's start with
+// nothing before them.
+constexpr int kLongSteps = 4, kShortSteps = 2, kLongSteps8 = 8, kShortSteps8 = 1;
+constexpr int kAhead = 2;                         // steps in flight with fp32 states
 constexpr float kLeast = 0x1p-9f;                 // least positive e4m3
 constexpr float kScaleMin = 0x1p-100f;
 
@@ -55,7 +59,7 @@ struct Tensor {
   float* vs;
   long long n;
   uint32_t begin;                                 // its first chunk
-  uint32_t vec;                                   // every operand aligned to four of its values
+  uint32_t vec;                                   // every operand aligned to its accesses
 };
 struct Coef {
   float b1, c1, b2, c2;                           // beta1, 1 - beta1, beta2, 1 - beta2
@@ -71,8 +75,10 @@ struct Launch {
   Tensor t[N];
   Coef c;
   int count;
+  int steps;                                      // per chunk
 };
 
+using Two = unsigned long long;                   // two fp32, for one instruction on both
 // Four neighbouring values.
 template <typename T>
 struct Four;
@@ -83,8 +89,11 @@ struct Four<float> {
   __device__ void part(const float* p, int n) {
     w = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, n > 3 ? p[3] : 0.f);
   }
-  __device__ void get(float (&x)[4]) const { x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w; }
-  __device__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
+  __device__ void get(Two (&x)[2]) const { x[0] = two(w.x, w.y); x[1] = two(w.z, w.w); }
+  __device__ void set(const Two (&x)[2]) {
+    untwo(x[0], w.x, w.y);
+    untwo(x[1], w.z, w.w);
+  }
   __device__ void store(float* p) const { *reinterpret_cast<float4*>(p) = w; }
   __device__ void put(float* p, int n) const {
     if (n > 0) p[0] = w.x;
@@ -103,12 +112,15 @@ struct Four<__nv_bfloat16> {
     for (int i = 0; i < 4; ++i) e[i] = i < n ? __bfloat16_as_ushort(p[i]) : 0u;
     w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
   }
-  __device__ void get(float (&x)[4]) const {
-    x[0] = __uint_as_float(w.x << 16); x[1] = __uint_as_float(w.x & 0xffff0000u);
-    x[2] = __uint_as_float(w.y << 16); x[3] = __uint_as_float(w.y & 0xffff0000u);
+  __device__ void get(Two (&x)[2]) const {
+    x[0] = two(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u));
+    x[1] = two(__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
   }
-  __device__ void set(const float (&x)[4]) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  __device__ void set(const Two (&x)[2]) {
+    float e[4];
+    untwo(x[0], e[0], e[1]);
+    untwo(x[1], e[2], e[3]);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(e[0], e[1]), b = __floats2bfloat162_rn(e[2], e[3]);
     w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   }
   __device__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = w; }
@@ -118,96 +130,226 @@ struct Four<__nv_bfloat16> {
       if (i < n) p[i] = __ushort_as_bfloat16((unsigned short)((i < 2 ? w.x : w.y) >> (16 * (i & 1))));
   }
 };
-// Four e4m3 codes.
-struct Codes {
-  uint32_t w;
-  __device__ void load(const uint8_t* p) { w = *reinterpret_cast<const uint32_t*>(p); }
-  __device__ void part(const uint8_t* p, int n) {
-    w = 0;
+// Four e4m3 codes to and from fp32.
+__device__ inline void decode(uint32_t w, Two (&x)[2]) {
+  const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
+  const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
+  const float2 u = __half22float2(__half2(a)), v = __half22float2(__half2(b));
+  x[0] = two(u.x, u.y);
+  x[1] = two(v.x, v.y);
+}
+__device__ inline uint32_t encode(const float (&x)[4]) {
+  return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
+         (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+}
+// 32 bytes at a time (aligned so).
+__device__ inline void load_32b(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ inline void store_32b(void* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+               "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+// 16 neighbouring values, as they lie in memory.
+template <typename T>
+struct Row;
+template <>
+struct Row<float> {
+  uint32_t w[16];
+  __device__ void load(const float* p) { load_32b(p, w); load_32b(p + 8, w + 8); }
+  __device__ void part(const float* p, int n) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) w |= (uint32_t)p[i] << (8 * i);
+    for (int i = 0; i < 16; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
   }
-  __device__ void get(float (&x)[4]) const {
-    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffffu), __NV_E4M3);
-    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 u = __half22float2(__half2(a)), v = __half22float2(__half2(b));
-    x[0] = u.x; x[1] = u.y; x[2] = v.x; x[3] = v.y;
+  __device__ void get(int u, Two (&x)[2]) const {        // values 4 u .. 4 u + 3
+    x[0] = two(__uint_as_float(w[4 * u]), __uint_as_float(w[4 * u + 1]));
+    x[1] = two(__uint_as_float(w[4 * u + 2]), __uint_as_float(w[4 * u + 3]));
   }
-  __device__ void set(const float (&x)[4]) {
-    w = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3) |
-        (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+  __device__ void set(int u, const Two (&x)[2]) {
+    float e[4];
+    untwo(x[0], e[0], e[1]);
+    untwo(x[1], e[2], e[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[4 * u + i] = __float_as_uint(e[i]);
   }
-  __device__ void store(uint8_t* p) const { *reinterpret_cast<uint32_t*>(p) = w; }
+  __device__ void store(float* p) const { store_32b(p, w); store_32b(p + 8, w + 8); }
+  __device__ void put(float* p, int n) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = __uint_as_float(w[i]);
+  }
+};
+template <>
+struct Row<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ void load(const __nv_bfloat16* p) { load_32b(p, w); }
+  __device__ void part(const __nv_bfloat16* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (2 * i < n ? (uint32_t)__bfloat16_as_ushort(p[2 * i]) : 0u) |
+             (2 * i + 1 < n ? (uint32_t)__bfloat16_as_ushort(p[2 * i + 1]) << 16 : 0u);
+  }
+  __device__ void get(int u, Two (&x)[2]) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x[i] = two(__uint_as_float(w[2 * u + i] << 16), __uint_as_float(w[2 * u + i] & 0xffff0000u));
+  }
+  __device__ void set(int u, const Two (&x)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float a, b;
+      untwo(x[i], a, b);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+      w[2 * u + i] = *reinterpret_cast<const uint32_t*>(&r);
+    }
+  }
+  __device__ void store(__nv_bfloat16* p) const { store_32b(p, w); }
+  __device__ void put(__nv_bfloat16* p, int n) const {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = __ushort_as_bfloat16((unsigned short)(w[i / 2] >> (16 * (i & 1))));
+  }
+};
+struct CodeRow {
+  uint32_t w[4];
+  __device__ void load(const uint8_t* p) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    w[0] = r.x; w[1] = r.y; w[2] = r.z; w[3] = r.w;
+  }
+  __device__ void part(const uint8_t* p, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 0u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < n) w[i / 4] |= (uint32_t)p[i] << (8 * (i & 3));
+  }
+  __device__ void store(uint8_t* p) const { *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]); }
   __device__ void put(uint8_t* p, int n) const {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = (uint8_t)(w >> (8 * i));
+    for (int i = 0; i < 16; ++i)
+      if (i < n) p[i] = (uint8_t)(w[i / 4] >> (8 * (i & 3)));
   }
 };
-
-// max|x| over the warp, NaN if one is (as unsigned integers, non-negative values
-// keep their order and every NaN lies above them).
-__device__ inline float warp_max(const float (&x)[4]) {
-  uint32_t a = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a = max(a, __float_as_uint(fabsf(x[i])));
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, a));
-}
-// Codes of 128 values of a warp, and their scale.  Every operation is one rounding
-// of its operands' (no contraction), so equal states give equal codes wherever
-// they are computed so.
+// Codes of the 128 values that eight neighbouring threads hold, and their scale.
+// Every operation is one rounding of its operands' (no contraction), so equal states
+// give equal codes wherever they are computed so.
 template <bool ROOT>
-__device__ inline void encode(float (&x)[4], Codes& code, float& scale) {
-  const float q = __fmul_rn(warp_max(x), 1.f / 448.f);
-  scale = q < kScaleMin ? kScaleMin : q;          // NaN stays NaN, as fmaxf would not let it
-  const float inv = __frcp_rn(scale);
+__device__ inline void encode(const Two (&v)[8], CodeRow& code, float& scale) {
+  auto max_nan = [](float a, float b) {            // NaN if one is
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+  };
+  float top = 0.f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = __fmul_rn(x[i], inv);
-    x[i] = ROOT && y > 0.f && y < kLeast ? kLeast : y;
+  for (int i = 0; i < 8; ++i) {
+    float a, b;
+    untwo(v[i], a, b);
+    top = max_nan(top, max_nan(fabsf(a), fabsf(b)));
   }
-  code.set(x);
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float q = __fmul_rn(top, 1.f / 448.f);
+  scale = q < kScaleMin ? kScaleMin : q;           // NaN stays NaN, as fmaxf would not let it
+  const float inv = __frcp_rn(scale);
+  const Two i2 = two(inv, inv);
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    float x[4];
+    untwo(mul2(v[2 * u], i2), x[0], x[1]);
+    untwo(mul2(v[2 * u + 1], i2), x[2], x[3]);
+    if (ROOT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = x[i] > 0.f ? fmaxf(x[i], kLeast) : x[i];
+    }
+    code.w[u] = encode(x);
+  }
 }
 
-// A thread's four values of one set, as they lie in memory.
-template <typename P, typename G, bool EIGHT>
-struct Raw {
-  Four<P> p;
-  Four<G> g;
-  typename std::conditional<EIGHT, Codes, Four<float>>::type m, v;
-  float ms, vs;
+// What a thread block does: its chunk of one tensor, and the step's factors.
+struct Chunk {
+  long long first;                                 // the chunk's first value
+  int n;                                           // its values
+  float i1, i2, gs;
 };
-
-template <typename P, typename G, bool EIGHT, int N>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Launch<N> a) {
-  await_previous();
-  release_next();
+template <int N>
+__device__ inline const Tensor& chunk_of(const Launch<N>& a, int step_values, Chunk& c) {
   // the last tensor whose first chunk is at or before this block
   int lo = 0;
 #pragma unroll
   for (int step = N > 256 ? 256 : N / 2; step > 0; step >>= 1)      // N is 504 or a power of two
     if (lo + step < a.count && a.t[lo + step].begin <= blockIdx.x) lo += step;
   const Tensor& t = a.t[lo];
-  const long long first = (long long)(blockIdx.x - t.begin) * kChunk;
-  using S = typename std::conditional<EIGHT, uint8_t, float>::type;
-  P* p = static_cast<P*>(t.p) + first;
-  const G* g = static_cast<const G*>(t.g) + first;
-  S *m = static_cast<S*>(t.m) + first, *v = static_cast<S*>(t.v) + first;
-  float *ms = EIGHT ? t.ms + first / kBlock : nullptr, *vs = EIGHT ? t.vs + first / kBlock : nullptr;
-  const int n = (int)min(t.n - first, (long long)kChunk);             // values of this chunk
-  const bool vec = t.vec;
-  float i1 = a.c.i1, i2 = a.c.i2;
+  const int chunk = a.steps * step_values;
+  c.first = (long long)(blockIdx.x - t.begin) * chunk;
+  c.n = (int)min(t.n - c.first, (long long)chunk);
+  c.i1 = a.c.i1;
+  c.i2 = a.c.i2;
   if (a.c.step) {
     const double at = (double)max(*a.c.step, 1ll);
-    i1 = (float)(-1.0 / expm1(at * a.c.l1));
-    i2 = (float)(1.0 / sqrt(-expm1(at * a.c.l2)));
+    c.i1 = (float)(-1.0 / expm1(at * a.c.l1));
+    c.i2 = (float)(1.0 / sqrt(-expm1(at * a.c.l2)));
   }
-  const float gs = a.c.grad_scale ? *a.c.grad_scale : 1.f;
-  float z = 0.f;                                   // zero, or NaN once a new p is not finite
-  Raw<P, G, EIGHT> raw[kAhead];
-  auto load = [&](int s, Raw<P, G, EIGHT>& r) {
-    const int i = s * (kThreads * 4) + threadIdx.x * 4;
+  c.gs = a.c.grad_scale ? *a.c.grad_scale : 1.f;
+  return t;
+}
+__device__ inline Two dup(float x) { return two(x, x); }
+// Two values' step: p, m and v become the new ones, r the root of v.  m and v by
+// operations of one rounding each, as encode.
+__device__ inline void update(const Coef& c, const Chunk& k, Two g, Two& p, Two& m, Two& v, Two& r) {
+  g = mul2(g, dup(k.gs));
+  m = add2(mul2(m, dup(c.b1)), mul2(g, dup(c.c1)));
+  v = add2(mul2(v, dup(c.b2)), mul2(mul2(g, g), dup(c.c2)));
+  float v0, v1, d0, d1, m0, m1;
+  untwo(v, v0, v1);
+  r = two(__fsqrt_rn(v0), __fsqrt_rn(v1));
+  // the quotient is of the order of 1 and moves p by lr of itself: an ulp or two of it
+  // are nothing beside p's own rounding
+  untwo(fma2(r, dup(k.i2), dup(c.eps)), d0, d1);
+  untwo(mul2(m, dup(k.i1)), m0, m1);
+  const Two u = two(__fdividef(m0, d0), __fdividef(m1, d1));
+  p = fma2(dup(-c.lr), fma2(dup(c.wd), p, u), p);
+}
+// z <- NaN where one of the first n of four values is not finite.
+__device__ inline void note(const Two (&x)[2], int n, Two& z) {
+  if (n >= 4) {
+    z = fma2(x[0], 0, fma2(x[1], 0, z));
+    return;
+  }
+  float e[4];
+  untwo(x[0], e[0], e[1]);
+  untwo(x[1], e[2], e[3]);
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i < n) z = fma2(dup(e[i]), 0, z);
+}
+__device__ inline void report(Two z, int32_t* status) {
+  float a, b;
+  untwo(z, a, b);
+  if (a != 0.f || b != 0.f) set_status(status, MC_STATUS_NONFINITE_UPDATE);       // NaN differs from 0
+}
+
+template <typename P, typename G, int N>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Launch<N> a) {
+  await_previous();
+  release_next();
+  Chunk k;
+  constexpr int kSet = kThreads * kWide;
+  const Tensor& t = chunk_of(a, kSet, k);
+  P* p = static_cast<P*>(t.p) + k.first;
+  const G* g = static_cast<const G*>(t.g) + k.first;
+  float *m = static_cast<float*>(t.m) + k.first, *v = static_cast<float*>(t.v) + k.first;
+  const int n = k.n;
+  const bool vec = t.vec;
+  Two z = 0;                                       // zeros, or NaN once a new p is not finite
+  struct Raw {
+    Four<P> p;
+    Four<G> g;
+    Four<float> m, v;
+  } raw[kAhead];
+  auto load = [&](int i, Raw& r) {
     if (vec && i + 4 <= n) {
       r.p.load(p + i);
       r.g.load(g + i);
@@ -219,87 +361,145 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       r.m.part(m + i, n - i);
       r.v.part(v + i, n - i);
     }
-    if (EIGHT && (i & ~(kBlock - 1)) < n) {
-      r.ms = ms[i / kBlock];
-      r.vs = vs[i / kBlock];
-    }
   };
 #pragma unroll
-  for (int s = 0; s < kAhead; ++s) load(s, raw[s]);
+  for (int s = 0; s < kAhead; ++s) load((s * kThreads + threadIdx.x) * kWide, raw[s]);
+  for (int s0 = 0; s0 < a.steps; s0 += kAhead) {
 #pragma unroll
-  for (int s = 0; s < kSets; ++s) {
-    const int i = s * (kThreads * 4) + threadIdx.x * 4;
-    if ((i & ~(kBlock - 1)) >= n) break;           // the whole warp is behind the end
-    const Raw<P, G, EIGHT> now = raw[s % kAhead];
-    if (s + kAhead < kSets) load(s + kAhead, raw[s % kAhead]);
-    float pv[4], gv[4], mv[4], vv[4], r[4];
-    now.p.get(pv);
-    now.g.get(gv);
-    now.m.get(mv);
-    now.v.get(vv);
+    for (int s = 0; s < kAhead; ++s) {
+      const int i = ((s0 + s) * kThreads + threadIdx.x) * kWide;
+      if (i >= n) break;
+      const Raw now = raw[s];
+      if (s0 + s + kAhead < a.steps) load(i + kAhead * kSet, raw[s]);
+      Two pv[2], gv[2], mv[2], vv[2], rv;
+      now.p.get(pv);
+      now.g.get(gv);
+      now.m.get(mv);
+      now.v.get(vv);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      if (EIGHT) {
-        mv[x] = __fmul_rn(mv[x], now.ms);
-        vv[x] = __fmul_rn(vv[x], now.vs);
-        vv[x] = __fmul_rn(vv[x], vv[x]);
+      for (int x = 0; x < 2; ++x) update(a.c, k, gv[x], pv[x], mv[x], vv[x], rv);
+      note(pv, n - i, z);
+      Four<P> np;
+      Four<float> nm, nv;
+      np.set(pv);
+      nm.set(mv);
+      nv.set(vv);
+      if (vec && i + 4 <= n) {
+        np.store(p + i);
+        nm.store(m + i);
+        nv.store(v + i);
+      } else {
+        np.put(p + i, n - i);
+        nm.put(m + i, n - i);
+        nv.put(v + i, n - i);
       }
-      const float gr = gv[x] * gs;
-      mv[x] = __fadd_rn(__fmul_rn(mv[x], a.c.b1), __fmul_rn(gr, a.c.c1));
-      vv[x] = __fadd_rn(__fmul_rn(vv[x], a.c.b2), __fmul_rn(__fmul_rn(gr, gr), a.c.c2));
-      r[x] = __fsqrt_rn(vv[x]);
-      // the quotient is of the order of 1 and moves p by lr of itself: an ulp or two of
-      // it are nothing beside p's own rounding
-      const float u = __fdividef(mv[x] * i1, fmaf(r[x], i2, a.c.eps));
-      pv[x] = fmaf(-a.c.lr, fmaf(a.c.wd, pv[x], u), pv[x]);
-    }
-    Four<P> out;
-    out.set(pv);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) z = i + x < n ? fmaf(pv[x], 0.f, z) : z;
-    if (vec && i + 4 <= n) out.store(p + i); else out.put(p + i, n - i);
-    // lanes behind the end hold zeros: they neither raise a scale nor are stored
-    typename std::conditional<EIGHT, Codes, Four<float>>::type cm, cv;
-    if constexpr (EIGHT) {
-      float sm, sv;
-      encode<false>(mv, cm, sm);
-      encode<true>(r, cv, sv);
-      if ((threadIdx.x & 31) == 0) {
-        ms[i / kBlock] = sm;
-        vs[i / kBlock] = sv;
-      }
-    } else {
-      cm.set(mv);
-      cv.set(vv);
-    }
-    if (vec && i + 4 <= n) {
-      cm.store(m + i);
-      cv.store(v + i);
-    } else {
-      cm.put(m + i, n - i);
-      cv.put(v + i, n - i);
     }
   }
-  if (z != 0.f) set_status(a.c.status, MC_STATUS_NONFINITE_UPDATE);
+  report(z, a.c.status);
+}
+
+// The same with 8-bit states.
+template <typename P, typename G, int N>
+__global__ void __launch_bounds__(kThreads, 2) adamw8_kernel(const __grid_constant__ Launch<N> a) {
+  await_previous();
+  release_next();
+  Chunk k;
+  constexpr int kSet = kThreads * kWide8;
+  const Tensor& t = chunk_of(a, kSet, k);
+  P* p = static_cast<P*>(t.p) + k.first;
+  const G* g = static_cast<const G*>(t.g) + k.first;
+  uint8_t *m = static_cast<uint8_t*>(t.m) + k.first, *v = static_cast<uint8_t*>(t.v) + k.first;
+  float *ms = t.ms + k.first / kBlock, *vs = t.vs + k.first / kBlock;
+  const int n = k.n;
+  const bool vec = t.vec;
+  Two z = 0;
+  struct Raw {
+    Row<P> p;
+    Row<G> g;
+    CodeRow m, v;
+    float ms, vs;
+  } raw;
+  auto load = [&](int i) {
+    if (vec && i + kWide8 <= n) {
+      raw.p.load(p + i);
+      raw.g.load(g + i);
+      raw.m.load(m + i);
+      raw.v.load(v + i);
+    } else {
+      raw.p.part(p + i, n - i);
+      raw.g.part(g + i, n - i);
+      raw.m.part(m + i, n - i);
+      raw.v.part(v + i, n - i);
+    }
+    raw.ms = raw.vs = 0.f;
+    if ((i & ~(kBlock - 1)) < n) {
+      raw.ms = ms[i / kBlock];
+      raw.vs = vs[i / kBlock];
+    }
+  };
+  load(threadIdx.x * kWide8);
+  for (int s = 0; s < a.steps; ++s) {
+    const int i = (s * kThreads + threadIdx.x) * kWide8;
+    if ((s * kThreads + (threadIdx.x & ~31)) * kWide8 >= n) break;    // the whole warp is behind the end
+    Raw now = raw;
+    if (s + 1 < a.steps) load(i + kSet);
+    Two mv[8], rv[8];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      Two pv[2], gv[2], m2[2], r2[2];
+      now.p.get(u, pv);
+      now.g.get(u, gv);
+      decode(now.m.w[u], m2);
+      decode(now.v.w[u], r2);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        mv[2 * u + x] = mul2(m2[x], dup(now.ms));
+        Two r = mul2(r2[x], dup(now.vs)), v2 = mul2(r, r);
+        update(a.c, k, gv[x], pv[x], mv[2 * u + x], v2, rv[2 * u + x]);
+      }
+      note(pv, n - i - 4 * u, z);
+      now.p.set(u, pv);
+    }
+    // values behind the end are zeros: they neither raise a scale nor are stored
+    float sm, sv;
+    encode<false>(mv, now.m, sm);
+    encode<true>(rv, now.v, sv);
+    if (vec && i + kWide8 <= n) {
+      now.p.store(p + i);
+      now.m.store(m + i);
+      now.v.store(v + i);
+    } else {
+      now.p.put(p + i, n - i);
+      now.m.put(m + i, n - i);
+      now.v.put(v + i, n - i);
+    }
+    if (threadIdx.x % 8 == 0 && i < n) {
+      ms[i / kBlock] = sm;
+      vs[i / kBlock] = sv;
+    }
+  }
+  report(z, a.c.status);
 }
 
 template <typename P, typename G, bool EIGHT, int N>
-cudaError_t launch(const Tensor* t, int count, uint32_t chunks, const Coef& c, cudaStream_t s) {
+cudaError_t launch(const Tensor* t, int count, int steps, uint32_t chunks, const Coef& c, cudaStream_t s) {
   Launch<N> a;
   memcpy(a.t, t, (size_t)count * sizeof(Tensor));
   a.c = c;
   a.count = count;
-  return launch_behind(adamw_kernel<P, G, EIGHT, N>, chunks, kThreads, 0, s, a);
+  a.steps = steps;
+  if constexpr (EIGHT) return launch_behind(adamw8_kernel<P, G, N>, chunks, kThreads, 0, s, a);
+  else return launch_behind(adamw_kernel<P, G, N>, chunks, kThreads, 0, s, a);
 }
 // A launch's tensors travel among its parameters, at most 32,764 bytes of them:
 // few where few do, since the driver copies them all.
 constexpr int kFew = 16, kSome = 128, kMany = 504;
 static_assert(sizeof(Launch<kMany>) <= 32764, "kernel parameters");
 template <typename P, typename G, bool EIGHT>
-cudaError_t launch_any(const Tensor* t, int count, uint32_t chunks, const Coef& c, cudaStream_t s) {
-  if (count <= kFew) return launch<P, G, EIGHT, kFew>(t, count, chunks, c, s);
-  if (count <= kSome) return launch<P, G, EIGHT, kSome>(t, count, chunks, c, s);
-  return launch<P, G, EIGHT, kMany>(t, count, chunks, c, s);
+cudaError_t launch_any(const Tensor* t, int count, int steps, uint32_t chunks, const Coef& c, cudaStream_t s) {
+  if (count <= kFew) return launch<P, G, EIGHT, kFew>(t, count, steps, chunks, c, s);
+  if (count <= kSome) return launch<P, G, EIGHT, kSome>(t, count, steps, chunks, c, s);
+  return launch<P, G, EIGHT, kMany>(t, count, steps, chunks, c, s);
 }
 
 mc_status err(mc_status s, const char* fmt, ...) {
@@ -358,7 +558,8 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
     span("v", i, a.v, a.n * ss, true);
     span("m_scale", i, a.m_scale, scales, true);
     span("v_scale", i, a.v_scale, scales, true);
-    const bool vec = at(a.p) % (4 * ps) == 0 && at(a.g) % (4 * gs) == 0 && at(a.m) % (4 * ss) == 0 && at(a.v) % (4 * ss) == 0;
+    const bool vec = eight ? at(a.p) % 32 == 0 && at(a.g) % 32 == 0 && at(a.m) % 16 == 0 && at(a.v) % 16 == 0
+                           : at(a.p) % (4 * ps) == 0 && at(a.g) % (4 * gs) == 0 && at(a.m) % 16 == 0 && at(a.v) % 16 == 0;
     sorted[(a.p_dtype == MC_BF16) + 2 * (a.g_dtype == MC_BF16) + 4 * eight].push_back(
         {a.p, a.g, a.m, a.v, a.m_scale, a.v_scale, a.n, 0u, vec ? 1u : 0u});
   }
@@ -393,23 +594,27 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
   }
   c.grad_scale = grad_scale;
   c.status = status;
-  using Any = cudaError_t (*)(const Tensor*, int, uint32_t, const Coef&, cudaStream_t);
+  using Any = cudaError_t (*)(const Tensor*, int, int, uint32_t, const Coef&, cudaStream_t);
   using B = __nv_bfloat16;
   static const Any by_types[8] = {launch_any<float, float, false>, launch_any<B, float, false>, launch_any<float, B, false>,
                                   launch_any<B, B, false>,         launch_any<float, float, true>, launch_any<B, float, true>,
                                   launch_any<float, B, true>,      launch_any<B, B, true>};
   for (int k = 0; k < 8; ++k) {
     std::vector<Tensor>& own = sorted[k];
+    long long values = 0;
+    for (const Tensor& x : own) values += x.n;
+    const int set = kThreads * (k < 4 ? kWide : kWide8), most = k < 4 ? kLongSteps : kLongSteps8;
+    const int steps = values >= (long long)sm_count() * 16 * most * set ? most : k < 4 ? kShortSteps : kShortSteps8;
     for (size_t i = 0; i < own.size();) {
       uint32_t chunks = 0;
       size_t j = i;
       for (; j < own.size() && j - i < kMany; ++j) {
-        const long long more = cdiv(own[j].n, kChunk);
-        if (chunks + more > 0x7fffffffll) break;        // 2^40 values are 2^28 chunks: the first always fits
+        const long long more = cdiv(own[j].n, steps * set);
+        if (chunks + more > 0x7fffffffll) break;        // 2^40 values are at most 2^28 chunks: the first always fits
         own[j].begin = chunks;
         chunks += (uint32_t)more;
       }
-      const cudaError_t e = by_types[k](own.data() + i, (int)(j - i), chunks, c, stream);
+      const cudaError_t e = by_types[k](own.data() + i, (int)(j - i), steps, chunks, c, stream);
       if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
       i = j;
     }
