@@ -37,11 +37,11 @@ namespace hn {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxPairs = MC_HEAD_MAX / 2;
-constexpr int kFlight = 4;                        // rows of a lane in flight (the gradient: pairs of rows, half as many)
+constexpr int kFlight = 2;                        // rows of a lane per step of the loop
 // Blocks of the gradient that an SM holds at once, and blocks (rows of weight sums)
 // at most: one wave.
-__host__ __device__ constexpr int back_blocks(int nu) { return nu == 1 ? 3 : 1; }
-constexpr int kBackGrid = 152 * 3;
+__host__ __device__ constexpr int back_blocks(int nu) { return nu == 1 ? 2 : 1; }
+constexpr int kBackGrid = 152 * 2;
 
 struct Side {                                     // queries or keys
   const void* x;                                  // the norm's input
@@ -65,24 +65,29 @@ struct Params {
   FastDiv div_pieces[3];                          // by the units of a token: of queries, of keys, of both
 };
 
-// V neighbouring features of a row.
+using Two = unsigned long long;                   // two fp32
+// V neighbouring features of a row, in registers as they lie in memory.
 template <typename T, int V>
 struct Feat;
 template <>
 struct Feat<__nv_bfloat16, 8> {
   uint4 w;
   __device__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
-  __device__ void zero() { w = make_uint4(0, 0, 0, 0); }
-  __device__ void get(float (&x)[8]) const {
+  __device__ void fill(uint32_t x) { w = make_uint4(x, x, x, x); }
+  __device__ void zero() { fill(0u); }
+  __device__ void ones() { fill(0x3f803f80u); }
+  __device__ void get(Two (&x)[4]) const {
     const uint32_t e[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) { x[2 * i] = __uint_as_float(e[i] << 16); x[2 * i + 1] = __uint_as_float(e[i] & 0xffff0000u); }
+    for (int i = 0; i < 4; ++i) x[i] = two(__uint_as_float(e[i] << 16), __uint_as_float(e[i] & 0xffff0000u));
   }
-  __device__ static void store(__nv_bfloat16* p, const float (&x)[8]) {
+  __device__ static void store(__nv_bfloat16* p, const Two (&x)[4]) {
     uint32_t e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+      float a, b;
+      untwo(x[i], a, b);
+      const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
       e[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
     *reinterpret_cast<uint4*>(p) = make_uint4(e[0], e[1], e[2], e[3]);
@@ -92,9 +97,16 @@ template <>
 struct Feat<float, 4> {
   float4 w;
   __device__ void load(const float* p) { w = *reinterpret_cast<const float4*>(p); }
-  __device__ void zero() { w = make_float4(0.f, 0.f, 0.f, 0.f); }
-  __device__ void get(float (&x)[4]) const { x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w; }
-  __device__ static void store(float* p, const float (&x)[4]) { *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]); }
+  __device__ void fill(float x) { w = make_float4(x, x, x, x); }
+  __device__ void zero() { fill(0.f); }
+  __device__ void ones() { fill(1.f); }
+  __device__ void get(Two (&x)[2]) const { x[0] = two(w.x, w.y); x[1] = two(w.z, w.w); }
+  __device__ static void store(float* p, const Two (&x)[2]) {
+    float4 w;
+    untwo(x[0], w.x, w.y);
+    untwo(x[1], w.z, w.w);
+    *reinterpret_cast<float4*>(p) = w;
+  }
 };
 template <typename T>
 struct Feat<T, 2> {                               // a pair, whatever its alignment
@@ -105,8 +117,14 @@ struct Feat<T, 2> {                               // a pair, whatever its alignm
   __device__ static void to(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
   __device__ void load(const T* p) { a = in(p[0]); b = in(p[1]); }
   __device__ void zero() { a = b = 0.f; }
-  __device__ void get(float (&x)[2]) const { x[0] = a; x[1] = b; }
-  __device__ static void store(T* p, const float (&x)[2]) { to(p, x[0]); to(p + 1, x[1]); }
+  __device__ void ones() { a = b = 1.f; }
+  __device__ void get(Two (&x)[1]) const { x[0] = two(a, b); }
+  __device__ static void store(T* p, const Two (&x)[1]) {
+    float a, b;
+    untwo(x[0], a, b);
+    to(p, a);
+    to(p + 1, b);
+  }
 };
 
 // A lane's features are V from column V * (its lane of the row + lanes * u), u <
@@ -134,39 +152,87 @@ struct Turn {
       }
   }
 };
-// (a, b) -> (a c - b s, b c + a s)
-__device__ inline void rotate(float& a, float& b, float c, float s) {
-  untwo(fma2(two(b, a), two(-s, s), mul2(two(a, b), two(c, c))), a, b);
-}
-
-__device__ inline float row_sum(float v, int lanes) {
-  for (int o = lanes >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// A side's weights as they lie in memory (of a lane's columns).
-template <typename T, int V, int NU>
-struct Weight {
-  Feat<T, V> f[NU];
-  bool given;
-  __device__ void load(const Params& p, const void* w, int sub) {
-    given = w != nullptr;
+// Sums over the lanes of a row, of N rows at once (a chain of shuffles has their
+// latency: several rows' chains side by side).
+template <int N>
+__device__ inline void row_sums(float (&v)[N], int lanes) {
 #pragma unroll
-    for (int u = 0; u < NU; ++u) {
-      const int col = V * (sub + p.lanes * u);
-      f[u].zero();
-      if (w && col < p.d) f[u].load(static_cast<const T*>(w) + col);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes)
+#pragma unroll
+      for (int n = 0; n < N; ++n) v[n] += __shfl_xor_sync(0xffffffffu, v[n], o);
+}
+
+// A lane's weights of one side.
+template <typename T, int V, int NU>
+__device__ inline void load_weight(const Params& p, const void* w, int sub, Two (&x)[NU][V / 2]) {
+#pragma unroll
+  for (int u = 0; u < NU; ++u) {
+    const int col = V * (sub + p.lanes * u);
+    Feat<T, V> f;
+    f.ones();
+    if (w && col < p.d) f.load(static_cast<const T*>(w) + col);
+    f.get(x[u]);
+  }
+}
+__device__ inline float both(Two v) {
+  float a, b;
+  untwo(v, a, b);
+  return a + b;
+}
+
+// A thread's rows on their way: their 16-byte parts are copied asynchronously to
+// places in shared memory that only this thread reads, kDepth steps of F rows ahead,
+// so that loads in flight take no registers.  (With two steps of them in registers the
+// forward took 69 us instead of 65 for 16384 tokens of 32 / 8 heads of 128, the gradient
+// 103 instead of 84.)  Pairs (V = 2, rows of any alignment) are loaded where they are used.
+constexpr int kDepth = 3;
+template <typename T, int V>
+constexpr bool kAsync = V * sizeof(T) == 16;
+__device__ inline void copy_16b(uint4* to, const void* from, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+}
+__device__ inline void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ inline void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+template <typename T, int V, int NU, int F>
+struct Rows {
+  uint4* fifo;                                    // this thread's first place
+  const T* base;                                  // the lane's first column of its first row (there if left and cols are positive)
+  const T* any;                                   // an address of the operand, for copies of nothing
+  long long pitch;                                // of rows that this lane meets in turn
+  int left;                                       // rows that it meets
+  int cols;                                       // columns from base's to the row's end
+  int lanes;
+  __device__ void issue(int step) {
+    if constexpr (kAsync<T, V>) {
+#pragma unroll
+      for (int n = 0; n < F; ++n)
+#pragma unroll
+        for (int u = 0; u < NU; ++u) {
+          const int i = step * F + n, col = V * lanes * u;
+          const bool there = i < left && col < cols;
+          copy_16b(fifo + ((step % kDepth) * F + n) * NU * kThreads + u * kThreads, there ? base + i * pitch + col : any, there);
+        }
     }
   }
-  __device__ void get(int u, float (&x)[V]) const {
-    f[u].get(x);
-#pragma unroll
-    for (int k = 0; k < V; ++k) x[k] = given ? x[k] : 1.f;
+  __device__ void get(int step, int n, int u, Two (&x)[V / 2]) const {
+    Feat<T, V> f;
+    if constexpr (kAsync<T, V>) {
+      f.load(reinterpret_cast<const T*>(fifo + ((step % kDepth) * F + n) * NU * kThreads + u * kThreads));
+    } else {
+      const int i = step * F + n, col = V * lanes * u;
+      f.zero();
+      if (i < left && col < cols) f.load(base + i * pitch + col);
+    }
+    f.get(x);
   }
 };
 
 template <typename T, int V, int NU>
-__global__ void __launch_bounds__(kThreads, NU == 1 ? 4 : 2) head_norm_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) head_norm_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint4 fifo[];
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
@@ -176,134 +242,181 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 4 : 2) head_norm_kernel(co
   const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[2]), r = (int)unit - t * pieces, side = r >= p.pieces[0];
   const Side& S = p.side[side];
   const int from = (r - side * p.pieces[0]) * p.span, to = min(S.heads, from + p.span), base = side ? p.side[0].heads : 0;
-  const T* x = static_cast<const T*>(S.x) + t * S.xt;
-  T* y = static_cast<T*>(S.out) + t * S.ot;
-  Feat<T, V> f[kFlight][NU];
-  // rows h0 + n * (rows of the warp) + this lane's
-  auto load = [&](int h0) {
+  const int steps = (to - from + kFlight * rows - 1) / (kFlight * rows);
+  Rows<T, V, NU, kFlight> x;
+  x.fifo = fifo + threadIdx.x;
+  x.any = static_cast<const T*>(S.x);
+  x.base = x.any + t * S.xt + (from + group) * S.xh + V * sub;
+  x.pitch = rows * S.xh;
+  x.left = (to - from - group + rows - 1) / rows;
+  x.cols = p.d - V * sub;
+  x.lanes = p.lanes;
+  T* y = static_cast<T*>(S.out) + t * S.ot + (from + group) * S.oh + V * sub;
+#pragma unroll
+  for (int i = 0; i < kDepth; ++i) {
+    if (i < steps) x.issue(i);
+    copies_end();
+  }
+  // the weight goes into the rotation: (a, b) -> (a w0 c - b w1 s, a w0 s + b w1 c)
+  float ac[NU][V / 2], bs[NU][V / 2], as[NU][V / 2], bc[NU][V / 2];
+  {
+    Two w[NU][V / 2];
+    load_weight<T, V, NU>(p, S.w, sub, w);
+    Turn<V, NU, sizeof(T) == 2> turn;
+    turn.at(p, p.positions ? p.positions[t] : t, sub);
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        float w0, w1;
+        untwo(w[u][k], w0, w1);
+        ac[u][k] = w0 * turn.c[u][k];
+        as[u][k] = w0 * turn.s[u][k];
+        bc[u][k] = w1 * turn.c[u][k];
+        bs[u][k] = w1 * turn.s[u][k];
+      }
+  }
+  float* rstds = p.rstd + (long long)t * p.heads + base + from + group;
+  for (int i = 0; i < steps; ++i) {
+    copies_wait<kDepth - 1>();
+    float sums[kFlight];
 #pragma unroll
     for (int n = 0; n < kFlight; ++n) {
-      const int h = h0 + n * rows + group;
+      Two sum = 0;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        const int col = V * (sub + p.lanes * u);
-        if (h < to && col < p.d) f[n][u].load(x + h * S.xh + col); else f[n][u].zero();
+        Two v[V / 2];
+        x.get(i, n, u, v);
+#pragma unroll
+        for (int k = 0; k < V / 2; ++k) sum = fma2(v[k], v[k], sum);
       }
+      sums[n] = both(sum);
     }
-  };
-  load(from);
-  Weight<T, V, NU> w;
-  w.load(p, S.w, sub);
-  Turn<V, NU, sizeof(T) == 2> turn;
-  turn.at(p, p.positions ? p.positions[t] : t, sub);
-  for (int h0 = from; h0 < to; h0 += kFlight * rows) {
-    if (h0 > from) load(h0);
+    row_sums(sums, p.lanes);
 #pragma unroll
     for (int n = 0; n < kFlight; ++n) {
-      if (h0 + n * rows >= to) break;                       // the whole warp
-      const int h = h0 + n * rows + group;
-      float v[NU][V], sum = 0.f;
+      const int h = i * kFlight + n;               // of this lane's rows
+      if (h >= x.left) continue;
+      const float rstd = rsqrtf(fmaf(sums[n], p.inv_d, p.eps));
+      if (sub == 0) rstds[h * rows] = rstd;
+      const Two r2 = two(rstd, rstd);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        f[n][u].get(v[u]);
+        Two v[V / 2];
+        x.get(i, n, u, v);
 #pragma unroll
-        for (int k = 0; k < V; ++k) sum = fmaf(v[u][k], v[u][k], sum);
-      }
-      const float rstd = 1.f / sqrtf(fmaf(row_sum(sum, p.lanes), p.inv_d, p.eps));
-      if (h >= to) continue;
-      if (sub == 0) p.rstd[(long long)t * p.heads + base + h] = rstd;
-#pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        const int col = V * (sub + p.lanes * u);
-        float wt[V];
-        w.get(u, wt);
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          v[u][k] *= rstd * wt[k];
-          v[u][k + 1] *= rstd * wt[k + 1];
-          rotate(v[u][k], v[u][k + 1], turn.c[u][k / 2], turn.s[u][k / 2]);
+        for (int k = 0; k < V / 2; ++k) {
+          float a, b;
+          untwo(mul2(v[k], r2), a, b);
+          v[k] = two(fmaf(-b, bs[u][k], a * ac[u][k]), fmaf(b, bc[u][k], a * as[u][k]));
         }
-        if (col < p.d) Feat<T, V>::store(y + h * S.oh + col, v[u]);
+        if (V * p.lanes * u < x.cols) Feat<T, V>::store(y + h * (rows * S.oh) + V * p.lanes * u, v);
       }
     }
+    if (i + kDepth < steps) x.issue(i + kDepth);
+    copies_end();
   }
 }
 
 template <typename T, int V, int NU>
 __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kernel(const __grid_constant__ Params p) {
-  extern __shared__ float sums[];                 // [2][rows of all warps][d] weight sums
+  extern __shared__ uint4 fifo[];                 // rows on their way; then [2][rows of all warps][d] weight sums
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
   const int warps = (int)gridDim.x * kWarps, all = kWarps * rows;
+  constexpr int F = kFlight;
+  float* sums = reinterpret_cast<float*>(fifo + (kAsync<T, V> ? 2 * kDepth * F * NU * kThreads : 0));
   // queries, then keys: one side's weight and its sums at a time in registers
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
     const Side& S = p.side[side];
     const int base = side ? p.side[0].heads : 0, pieces = p.pieces[side];
-    Weight<T, V, NU> w;
-    w.load(p, S.w, sub);
-    float dw[NU][V];
+    Two w[NU][V / 2], dw[NU][V / 2];
+    load_weight<T, V, NU>(p, S.w, sub, w);
 #pragma unroll
-    for (int i = 0; i < NU * V; ++i) dw[i / V][i % V] = 0.f;
+    for (int i = 0; i < NU * V / 2; ++i) dw[i / (V / 2)][i % (V / 2)] = 0;
     const long long units = (long long)p.T * pieces;
     for (long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); unit < units; unit += warps) {
       const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[side]);
       const int from = ((int)unit - t * pieces) * p.span, to = min(S.heads, from + p.span);
-      const T* x = static_cast<const T*>(S.x) + t * S.xt;
-      const T* g = static_cast<const T*>(S.dy) + t * S.gt;
-      T* o = static_cast<T*>(S.out) + t * S.ot;
-      const float* rs = p.rstd + (long long)t * p.heads + base;
-      constexpr int F = kFlight / 2;
-      Feat<T, V> fx[F][NU], fg[F][NU];
-      float r[F];
-      auto load = [&](int h0) {
+      const int steps = (to - from + F * rows - 1) / (F * rows);
+      Rows<T, V, NU, F> x, g;
+      x.fifo = fifo + threadIdx.x;
+      g.fifo = x.fifo + kDepth * F * NU * kThreads;
+      x.any = static_cast<const T*>(S.x);
+      g.any = static_cast<const T*>(S.dy);
+      x.base = x.any + t * S.xt + (from + group) * S.xh + V * sub;
+      g.base = g.any + t * S.gt + (from + group) * S.gh + V * sub;
+      x.pitch = rows * S.xh;
+      g.pitch = rows * S.gh;
+      x.left = g.left = (to - from - group + rows - 1) / rows;
+      x.cols = g.cols = p.d - V * sub;
+      x.lanes = g.lanes = p.lanes;
+      T* o = static_cast<T*>(S.out) + t * S.ot + (from + group) * S.oh + V * sub;
+      const float* rs = p.rstd + (long long)t * p.heads + base + from + group;
 #pragma unroll
-        for (int n = 0; n < F; ++n) {
-          const int h = h0 + n * rows + group;
-          r[n] = h < to ? rs[h] : 0.f;
-#pragma unroll
-          for (int u = 0; u < NU; ++u) {
-            const int col = V * (sub + p.lanes * u);
-            if (h < to && col < p.d) { fx[n][u].load(x + h * S.xh + col); fg[n][u].load(g + h * S.gh + col); }
-            else { fx[n][u].zero(); fg[n][u].zero(); }
-          }
+      for (int i = 0; i < kDepth; ++i) {
+        if (i < steps) {
+          x.issue(i);
+          g.issue(i);
         }
+        copies_end();
+      }
+      float r[F], r1[F];                          // rstd of this step's rows, and of the next one's
+      auto load_r = [&](int i) {
+#pragma unroll
+        for (int n = 0; n < F; ++n) r1[n] = i * F + n < x.left ? rs[(i * F + n) * rows] : 0.f;
       };
-      load(from);
+      load_r(0);
       Turn<V, NU, sizeof(T) == 2> turn;
       turn.at(p, p.positions ? p.positions[t] : t, sub);
-      for (int h0 = from; h0 < to; h0 += F * rows) {
-        if (h0 > from) load(h0);
+      for (int i = 0; i < steps; ++i) {
+#pragma unroll
+        for (int n = 0; n < F; ++n) r[n] = r1[n];
+        load_r(i + 1);
+        copies_wait<kDepth - 1>();
+        Two a[F][NU][V / 2], b[F][NU][V / 2];
+        float dots[F];
 #pragma unroll
         for (int n = 0; n < F; ++n) {
-          if (h0 + n * rows >= to) break;                   // the whole warp
-          const int h = h0 + n * rows + group;
-          float a[NU][V], b[NU][V], dot = 0.f;
+          Two dot = 0;
+          const Two r2 = two(r[n], r[n]);
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
-            fx[n][u].get(a[u]);
-            fg[n][u].get(b[u]);
+            x.get(i, n, u, a[n][u]);
+            g.get(i, n, u, b[n][u]);
 #pragma unroll
-            for (int k = 0; k < V; k += 2) rotate(b[u][k], b[u][k + 1], turn.c[u][k / 2], -turn.s[u][k / 2]);
-            float wt[V];
-            w.get(u, wt);
-#pragma unroll
-            for (int k = 0; k < V; ++k) {
-              a[u][k] *= r[n];                               // xhat
-              dw[u][k] = fmaf(b[u][k], a[u][k], dw[u][k]);
-              b[u][k] *= wt[k];
-              dot = fmaf(b[u][k], a[u][k], dot);
+            for (int k = 0; k < V / 2; ++k) {
+              float g0, g1;                                  // rotated back
+              untwo(b[n][u][k], g0, g1);
+              const Two dz = two(fmaf(g1, turn.s[u][k], g0 * turn.c[u][k]), fmaf(-g0, turn.s[u][k], g1 * turn.c[u][k]));
+              a[n][u][k] = mul2(a[n][u][k], r2);             // xhat
+              dw[u][k] = fma2(dz, a[n][u][k], dw[u][k]);
+              b[n][u][k] = mul2(dz, w[u][k]);
+              dot = fma2(b[n][u][k], a[n][u][k], dot);
             }
           }
-          const float mean = row_sum(dot, p.lanes) * p.inv_d;
-          if (h >= to) continue;
+          dots[n] = both(dot);
+        }
+        // the step's rows are in registers: their places take the next ones
+        if (i + kDepth < steps) {
+          x.issue(i + kDepth);
+          g.issue(i + kDepth);
+        }
+        copies_end();
+        row_sums(dots, p.lanes);
+#pragma unroll
+        for (int n = 0; n < F; ++n) {
+          const int h = i * F + n;
+          if (h >= x.left) continue;
+          const float mean = -dots[n] * p.inv_d;
+          const Two m2 = two(mean, mean), r2 = two(r[n], r[n]);
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
-            const int col = V * (sub + p.lanes * u);
 #pragma unroll
-            for (int k = 0; k < V; ++k) a[u][k] = r[n] * fmaf(-a[u][k], mean, b[u][k]);
-            if (col < p.d) Feat<T, V>::store(o + h * S.oh + col, a[u]);
+            for (int k = 0; k < V / 2; ++k) a[n][u][k] = mul2(r2, fma2(a[n][u][k], m2, b[n][u][k]));
+            if (V * p.lanes * u < x.cols) Feat<T, V>::store(o + h * (rows * S.oh) + V * p.lanes * u, a[n][u]);
           }
         }
       }
@@ -314,7 +427,10 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
         const int col = V * (sub + p.lanes * u);
         if (col < p.d)
 #pragma unroll
-          for (int k = 0; k < V; ++k) sums[(side * all + (threadIdx.x >> 5) * rows + group) * p.d + col + k] = dw[u][k];
+          for (int k = 0; k < V / 2; ++k) {
+            float* to = sums + (side * all + (threadIdx.x >> 5) * rows + group) * p.d + col + 2 * k;
+            untwo(dw[u][k], to[0], to[1]);
+          }
       }
   }
   if (!p.part) return;
@@ -469,16 +585,23 @@ template <typename T, int V, int NU>
 cudaError_t run_forward(Params& p, cudaStream_t s) {
   split(p, p.d / V, kFlight, sm_count() * 32);
   const long long units = (long long)p.T * (p.pieces[0] + p.pieces[1]);
-  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)cdiv(units, kWarps), kThreads, 0, s, p);
+  constexpr size_t smem = kAsync<T, V> ? (size_t)kDepth * kFlight * NU * kThreads * 16 : 0;
+  const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<T, V, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)cdiv(units, kWarps), kThreads, smem, s, p);
 }
 template <typename T, int V, int NU>
 cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
   const int wave = sm_count() * back_blocks(NU), most = wave < kBackGrid ? wave : kBackGrid;
-  split(p, p.d / V, kFlight / 2, 8ll * most * kWarps);      // some units per warp, that the last ones leave few idle
+  split(p, p.d / V, kFlight, 8ll * most * kWarps);      // some units per warp, that the last ones leave few idle
   const long long blocks = cdiv((long long)p.T * (p.pieces[0] > p.pieces[1] ? p.pieces[0] : p.pieces[1]), kWarps);
   const int grid = (int)(blocks < most ? blocks : most);
-  const size_t smem = p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0;   // a warp's rows have at most 256 features: 16 KB
-  const cudaError_t e = launch_behind(head_norm_back_kernel<T, V, NU>, (unsigned)grid, kThreads, smem, s, p);
+  constexpr size_t fifo = kAsync<T, V> ? (size_t)2 * kDepth * kFlight * NU * kThreads * 16 : 0, most_sums = 2 * kWarps * MC_HEAD_MAX * 4;
+  const size_t smem = fifo + (p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0);   // a warp's rows have at most 256 features
+  // the limit belongs to the kernel, not to this call: always that of the largest
+  cudaError_t e = cudaFuncSetAttribute(head_norm_back_kernel<T, V, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fifo + most_sums));
+  if (e != cudaSuccess) return e;
+  e = launch_behind(head_norm_back_kernel<T, V, NU>, (unsigned)grid, kThreads, smem, s, p);
   if (e != cudaSuccess || !p.part) return e;
   return launch_behind(head_weight_kernel, (unsigned)cdiv(2 * p.d, 32), 1024, 0, s, p.part, dwq, dwk, grid, p.d);
 }
