@@ -7,6 +7,7 @@ implementation to fall back to.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_size_t, c_uint64, c_void_p
 
@@ -182,6 +183,25 @@ def load():
             fn.argtypes = args
         _lib = lib
     return _lib
+
+
+_host = None
+
+
+def host():
+    """The helper module _host.so (the binding's native part); raises if absent."""
+    global _host
+    if _host is None:
+        path = os.path.join(os.path.dirname(LIB_PATH), "_host.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built: run `python -m muon_qk_clip_gb300.build`")
+        import torch  # noqa: F401  (its libraries are loaded first)
+        load()
+        spec = importlib.util.spec_from_file_location("_host", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _host = module
+    return _host
 
 
 class MuonClipError(RuntimeError):

@@ -16,8 +16,7 @@ from dataclasses import dataclass
 import torch
 
 from . import abi
-from .abi import (McAdamHparams, McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHeads, McHparams, McMat,
-                  McPackedDesc, McPackedGrad, check)
+from .abi import McAttnDesc, McAttnGrad, McAttnOut, McClipLayer, McClipSeg, McHparams, McMat, check
 
 _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 
@@ -25,9 +24,6 @@ _DT = {torch.float32: abi.MC_F32, torch.bfloat16: abi.MC_BF16}
 # takes to convert their fields one by one)
 _ATTN_DESC = struct.Struct("@7if3P8q")
 _ATTN_GRAD = struct.Struct("@P2i3qP3qPP3qP3qP3qP2qP3q")
-_PACKED_DESC = struct.Struct("@7if4P6q")
-_PACKED_GRAD = struct.Struct("@P2qPP2qP2qP2qP2q")
-_TWO = ctypes.c_int64 * 2
 
 
 def _ptr(t):
@@ -222,6 +218,24 @@ def _run(fn, name, index, *args):
         check(code, name)
 
 
+def _native(entry, name, *args, on=None):
+    """What the native helper's entry returns for args, on the device of args[0] (or of
+    on) and its current stream.  It checks the tensors, allocates what is not given,
+    and calls the library's `name`."""
+    on = args[0] if on is None else on
+    index = on.get_device() if isinstance(on, torch.Tensor) else -1
+    if index < 0:                                      # refused, or without work
+        code, *out = getattr(abi.host(), entry)(*args, 0)
+    elif torch.cuda.current_device() != index:
+        with torch.cuda.device(index):
+            return _native(entry, name, *args, on=on)
+    else:
+        code, *out = getattr(abi.host(), entry)(*args, torch._C._cuda_getCurrentRawStream(index))
+    if code:
+        check(code, name)
+    return tuple(out)
+
+
 def _on_stream(fn):
     """fn with a stream (torch's or a raw handle) that it runs under as the
     current one: what it allocates then belongs to that stream, so memory that it
@@ -330,44 +344,11 @@ def _grad_like(name, g, like):
     return g
 
 
-def _packed_desc(q, k, v, offsets, scale):
-    """Descriptor of packed attention: q [T,H,d], k [T,H_kv,d], v [T,H_kv,dv], offsets [n+1]."""
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("q, k and v must be [T, heads, features]")
-    T, H, d = q.shape
-    G, dv = v.shape[1:]
-    if k.shape != (T, G, d) or v.shape[0] != T:
-        raise ValueError("k must be [T, H_kv, d] and v [T, H_kv, d_v] with q's tokens and width")
-    if q.dtype not in _DT or k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k and v must share a supported dtype")
-    qs, ks, vs = q.stride(), k.stride(), v.stride()
-    if qs[2] != 1 or ks[2] != 1 or vs[2] != 1:
-        raise ValueError("feature axes must be contiguous")
-    if offsets.dim() != 1 or offsets.dtype != torch.int32 or not offsets.is_contiguous() or offsets.numel() < 2:
-        raise ValueError("offsets must be a contiguous int32 tensor of one value more than there are sequences")
-    scale = 1.0 / math.sqrt(d) if scale is None else ctypes.c_float(scale).value   # beyond fp32: inf, which the library refuses
-    return McPackedDesc.from_buffer_copy(_PACKED_DESC.pack(
-        T, offsets.numel() - 1, H, G, d, dv, _DT[q.dtype], scale, offsets.data_ptr(), q.data_ptr(), k.data_ptr(),
-        v.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1]))
-
-
-def _packed_workspace(d, backward, workspace, device):
-    """(address, bytes, tensor) of the given workspace, or of a new one."""
-    if workspace is None:
-        n = ctypes.c_size_t(0)
-        check(abi.load().qk_attention_packed_workspace_size(d, int(backward), n), "qk_attention_packed_workspace_size")
-        workspace, nbytes = torch.empty(n.value, dtype=torch.uint8, device=device), n.value
-    else:
-        nbytes = _nbytes(workspace)
-    return workspace.data_ptr(), nbytes, workspace
-
-
 def packed_workspace_size(q, k, v, offsets, backward=False) -> int:
     """Bytes of workspace that the packed attention's forward (or backward) needs."""
-    n = ctypes.c_size_t(0)
-    check(abi.load().qk_attention_packed_workspace_size(_packed_desc(q, k, v, offsets, None), int(bool(backward)), n),
-          "qk_attention_packed_workspace_size")
-    return n.value
+    code, n = abi.host().packed_size(q, k, v, offsets, bool(backward))
+    check(code, "qk_attention_packed_workspace_size")
+    return n
 
 
 @_on_stream
@@ -380,31 +361,8 @@ def qk_attention_packed_forward(q, k, v, offsets, scale=None, out=None, lse=None
     [T,H,dv], lse [H,T] f32 or None, smax [H] f32); pass lse=True to allocate it.
     Rows of no sequence are not written.  workspace: a CUDA tensor of
     packed_workspace_size bytes; without one, one is allocated for the call."""
-    index = _device_of(q, "q", k, v, offsets, out, None if lse is True else lse, smax, workspace, status)
-    desc = _packed_desc(q, k, v, offsets, scale)
-    T, H, _ = q.shape
-    shape = (T, H, v.shape[2])
-    if out is None:
-        out = torch.empty(shape if shape[2] % 8 == 0 else (T, H, -shape[2] // 8 * -8), dtype=q.dtype, device=q.device)[..., :shape[2]]
-    elif out.shape != shape or out.stride(2) != 1 or out.dtype != q.dtype:
-        raise ValueError("out must be [T, H, d_v] with a contiguous feature axis and q's dtype")
-    if lse is True:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    elif lse is not None and (lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous [H, T] float32 tensor")
-    if smax is None:
-        if accumulate:
-            raise ValueError("accumulate goes with a smax to combine")
-        smax = torch.empty(H, dtype=torch.float32, device=q.device)
-    else:
-        _vector(smax, "smax", H, torch.float32)
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise ValueError("status must be an int32 tensor")
-    at, nbytes, _keep = _packed_workspace(desc, False, workspace, q.device)
-    os = out.stride()
-    _run(abi.load().qk_attention_packed_forward, "qk_attention_packed_forward", index, desc, out.data_ptr(),
-         _TWO(os[0], os[1]), _at(lse), smax.data_ptr(), int(bool(accumulate)), at, nbytes, _at(status))
-    return out, lse, smax
+    return _native("packed_forward", "qk_attention_packed_forward", q, k, v, offsets, scale, out, lse, smax, bool(accumulate),
+                   workspace, status)
 
 
 @_on_stream
@@ -416,24 +374,8 @@ def qk_attention_packed_backward(q, k, v, out, lse, dout, offsets, scale=None, d
     Outputs are allocated unless given: contiguous, or, of a width that is no
     multiple of eight, in rows padded to one.  workspace: a CUDA tensor of
     packed_workspace_size(..., backward=True) bytes; without one, one is allocated."""
-    index = _device_of(q, "q", k, v, out, lse, dout, offsets, dq, dk, dv, workspace, status)
-    desc = _packed_desc(q, k, v, offsets, scale)
-    T, H, _ = q.shape
-    shape, t = (T, H, v.shape[2]), q.dtype
-    if lse.shape != (H, T) or lse.dtype != torch.float32 or not lse.is_contiguous():
-        raise ValueError("lse must be a contiguous [H, T] float32 tensor")
-    os, ds = out.stride(), dout.stride()
-    if out.shape != shape or dout.shape != shape or out.dtype != t or dout.dtype != t or os[2] != 1 or ds[2] != 1:
-        raise ValueError("out and dout must be [T, H, d_v] with contiguous feature axes and q's dtype")
-    dq, dk, dv = _grad_like("dq", dq, q), _grad_like("dk", dk, k), _grad_like("dv", dv, v)
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise ValueError("status must be an int32 tensor")
-    at, nbytes, _keep = _packed_workspace(desc, True, workspace, q.device)
-    g = McPackedGrad.from_buffer_copy(_PACKED_GRAD.pack(
-        out.data_ptr(), os[0], os[1], lse.data_ptr(), dout.data_ptr(), ds[0], ds[1],
-        dq.data_ptr(), *dq.stride()[:2], dk.data_ptr(), *dk.stride()[:2], dv.data_ptr(), *dv.stride()[:2]))
-    _run(abi.load().qk_attention_packed_backward, "qk_attention_packed_backward", index, desc, g, at, nbytes, _at(status))
-    return dq, dk, dv
+    return _native("packed_backward", "qk_attention_packed_backward", q, k, v, out, lse, dout, offsets, scale, dq, dk, dv,
+                   workspace, status)
 
 
 @dataclass
@@ -684,37 +626,6 @@ def rms_norm_backward_workspace_size(cols: int) -> int:
     return n.value
 
 
-def _head_rows(t, name, shape, dtype):
-    """(address, token stride, head stride) of a [T, heads, d] operand of this shape and type."""
-    if t.shape != shape or t.dtype != dtype:
-        raise ValueError(f"{name} must be {list(shape)} of {dtype}")
-    token, head, inner = t.stride()
-    if inner != 1 and shape[2] > 1:
-        raise ValueError(f"{name}: expected unit stride along the features")
-    return t.data_ptr(), token, head
-
-
-def _heads(q, k, positions, theta, rot, eps, *others):
-    """(descriptor, device index, q's and k's shapes and their type)"""
-    index = _device_of(q, "q", k, positions, *others)
-    shape, t = q.shape, q.dtype
-    if len(shape) != 3 or t not in _DT:
-        raise ValueError("q: expected [T, heads, d] of bfloat16 or float32")
-    T, heads, d = shape
-    k_shape = (T, 0, d)
-    if k is not None:
-        k_shape = k.shape
-        if len(k_shape) != 3 or k_shape[0] != T or k_shape[2] != d or k.dtype != t:
-            raise ValueError(f"keys must be [{T}, heads, {d}] of {t}")
-    if positions is not None:
-        _vector(positions, "positions", T, torch.int32)
-    h = McHeads(T, heads, k_shape[1], d, d if rot is None else rot, _DT[t], eps, theta, _at(positions))
-    return h, index, shape, k_shape, t
-
-
-_NO_ROWS = (None, 0, 0)
-
-
 @_on_stream
 def qk_norm_rope(q, k=None, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None, eps: float = 1e-6,
                  out_q=None, out_k=None, rstd=None, *, stream=None):
@@ -724,27 +635,7 @@ def qk_norm_rope(q, k=None, wq=None, wk=None, positions=None, theta: float = 100
     (all by default, interleaved pairs as in rope_) at `positions` [T] int32 (the
     token's number without).  Returns (yq, yk or None, rstd [T, heads + key heads]
     f32); out_q=q and out_k=k run in place."""
-    h, index, shape, k_shape, t = _heads(q, k, positions, theta, rot, eps, wq, wk, out_q, out_k, rstd)
-    d = shape[2]
-    for w, name in ((wq, "wq"), (wk, "wk")):
-        if w is not None:
-            _vector(w, name, d, t)
-    if k is None and (wk is not None or out_k is not None):
-        raise ValueError("wk and out_k go with k")
-    if out_q is None:
-        out_q = torch.empty(shape, dtype=t, device=q.device)
-    if k is not None and out_k is None:
-        out_k = torch.empty(k_shape, dtype=t, device=q.device)
-    total = (shape[0], shape[1] + k_shape[1])
-    if rstd is None:
-        rstd = torch.empty(total, dtype=torch.float32, device=q.device)
-    elif rstd.shape != total or rstd.dtype != torch.float32 or not rstd.is_contiguous():
-        raise ValueError(f"rstd must be a contiguous {list(total)} tensor of float32")
-    _run(abi.load().mc_head_norm_rope, "mc_head_norm_rope", index, h, *_head_rows(q, "q", shape, t),
-         *(_NO_ROWS if k is None else _head_rows(k, "k", k_shape, t)), _at(wq), _at(wk),
-         *_head_rows(out_q, "out_q", shape, t), *(_NO_ROWS if k is None else _head_rows(out_k, "out_k", k_shape, t)),
-         rstd.data_ptr())
-    return out_q, out_k, rstd
+    return _native("norm_rope", "mc_head_norm_rope", q, k, wq, wk, positions, theta, rot, eps, out_q, out_k, rstd)
 
 
 def head_norm_backward_workspace_size(d: int) -> int:
@@ -763,40 +654,8 @@ def qk_norm_rope_backward(dyq, dyk, q, k, rstd, wq=None, wk=None, positions=None
     dyq or q and dk may be dyk or k (in place).  workspace: a CUDA tensor of
     head_norm_backward_workspace_size(d) bytes, allocated for the call where a weight
     gradient needs one and none is given."""
-    h, index, shape, k_shape, t = _heads(q, k, positions, theta, rot, 0.0, dyq, dyk, rstd, wq, wk, dq, dk, dwq, dwk, workspace)
-    d = shape[2]
-    if (k is None) != (dyk is None) or (k is None and any(x is not None for x in (wk, dk, dwk))):
-        raise ValueError("k, dyk, wk, dk and dwk go together")
-    total = (shape[0], shape[1] + k_shape[1])
-    if rstd.shape != total or rstd.dtype != torch.float32 or not rstd.is_contiguous():
-        raise ValueError(f"rstd must be a contiguous {list(total)} tensor of float32")
-    if dq is None:
-        dq = torch.empty(shape, dtype=t, device=q.device)
-    if k is not None and dk is None:
-        dk = torch.empty(k_shape, dtype=t, device=q.device)
-    if wq is not None:
-        _vector(wq, "wq", d, t)
-        if dwq is None:
-            dwq = torch.empty(d, dtype=torch.float32, device=q.device)
-    if wk is not None:
-        _vector(wk, "wk", d, t)
-        if dwk is None:
-            dwk = torch.empty(d, dtype=torch.float32, device=q.device)
-    nbytes = 0
-    if dwq is not None or dwk is not None:
-        for w, name in ((dwq, "dwq"), (dwk, "dwk")):
-            if w is not None:
-                _vector(w, name, d, torch.float32)
-        if workspace is None:
-            workspace = torch.empty(head_norm_backward_workspace_size(d), dtype=torch.uint8, device=q.device)
-        nbytes = _nbytes(workspace)
-    none = k is None
-    _run(abi.load().mc_head_norm_rope_backward, "mc_head_norm_rope_backward", index, h, *_head_rows(dyq, "dyq", shape, t),
-         *(_NO_ROWS if none else _head_rows(dyk, "dyk", k_shape, t)), *_head_rows(q, "q", shape, t),
-         *(_NO_ROWS if none else _head_rows(k, "k", k_shape, t)), rstd.data_ptr(), _at(wq), _at(wk),
-         *_head_rows(dq, "dq", shape, t), *(_NO_ROWS if none else _head_rows(dk, "dk", k_shape, t)), _at(dwq), _at(dwk),
-         _at(workspace), nbytes)
-    return dq, dk, dwq, dwk
+    return _native("norm_rope_backward", "mc_head_norm_rope_backward", dyq, dyk, q, k, rstd, wq, wk, positions, theta, rot,
+                   dq, dk, dwq, dwk, workspace)
 
 
 @dataclass
@@ -809,11 +668,7 @@ class AdamHparams:
     weight_decay: float = 0.1
 
 
-_ADAM_TENSOR = struct.Struct("@6Pq4i")
 _ADAM_BLOCK = 128                                      # MC_ADAMW_BLOCK
-_ADAM_DT = {**_DT, torch.float8_e4m3fn: abi.MC_F8E4M3}
-_data_ptr, _numel, _is_contiguous, _get_device = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous,
-                                                  torch.Tensor.get_device)
 
 
 def adamw_state(P, bits: int = 32):
@@ -828,9 +683,9 @@ def adamw_state(P, bits: int = 32):
 
 
 @_on_stream
-def _adamw(first, packed, count, hp, grad_scale, status):
-    """The call under its stream; first, a parameter, names the device."""
-    _run(abi.load().mc_adamw_step, "mc_adamw_step", first.get_device(), packed, count, hp, _at(grad_scale), _at(status))
+def _adamw(first, *args):
+    """The call under its stream; first is a parameter."""
+    _native("adamw", "mc_adamw_step", *args, on=first)
 
 
 def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None, v_scales=None, grad_scale=None,
@@ -845,51 +700,8 @@ def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None,
     every gradient (clipping by the global norm).  Tensors of one set of types share
     launches."""
     hp = hp or AdamHparams()
-    n = len(P)
-    if len(G) != n or len(M) != n or len(V) != n:
-        raise ValueError("P, G, M and V must have one length")
-    if (m_scales is None) != (v_scales is None):
-        raise ValueError("m_scales and v_scales go together")
-    if n == 0:
-        return
-    every = [*P, *G, *M, *V]
-    if m_scales is not None:
-        if len(m_scales) != n or len(v_scales) != n:
-            raise ValueError("m_scales and v_scales must have P's length")
-        every += [*m_scales, *v_scales]
-    device = {*map(_get_device, every)}
-    device.update([t.get_device() for t in (grad_scale, status, step) if isinstance(t, torch.Tensor)])
-    if len(device) > 1 or min(device) < 0:
-        raise ValueError("every tensor must be on one CUDA device")
-    if not all(map(_is_contiguous, every)):
-        raise ValueError("every tensor must be contiguous")
-    size = [*map(_numel, every)]
-    if size[:n] != size[n:2 * n] or size[:n] != size[2 * n:3 * n] or size[:n] != size[3 * n:4 * n]:
-        raise ValueError("P, G, M and V must agree in size, tensor by tensor")
-    types = [_ADAM_DT.get(t.dtype) for t in every]
-    if not {*types[:2 * n]} <= {abi.MC_F32, abi.MC_BF16}:
-        raise ValueError("P and G must be bfloat16 or float32")
-    if {*types[2 * n:4 * n]} != {abi.MC_F32 if m_scales is None else abi.MC_F8E4M3}:
-        raise ValueError("M and V must be float32, or float8_e4m3fn with m_scales and v_scales")
-    if m_scales is not None:
-        blocks = [-(-x // _ADAM_BLOCK) for x in size[:n]]
-        if size[4 * n:] != blocks + blocks or {*types[4 * n:]} != {abi.MC_F32}:
-            raise ValueError(f"scales must be float32, one per {_ADAM_BLOCK} values of their tensor")
-    if grad_scale is not None and (grad_scale.numel() != 1 or grad_scale.dtype != torch.float32):
-        raise ValueError("grad_scale must be one float32 value")
-    if status is not None and (status.dtype != torch.int32 or status.numel() < 1):
-        raise ValueError("status must be an int32 tensor")
-    on_device = isinstance(step, torch.Tensor)
-    if on_device and (step.numel() != 1 or step.dtype != torch.int64):
-        raise ValueError("step must be an integer or one int64 value on the device")
-    at = [*map(_data_ptr, every)]
-    if m_scales is None:
-        at += 2 * n * [0]
-    packed = b"".join(map(_ADAM_TENSOR.pack, at[:n], at[n:2 * n], at[2 * n:3 * n], at[3 * n:4 * n], at[4 * n:5 * n],
-                          at[5 * n:], size, types, types[n:], types[2 * n:], n * [0]))
-    h = McAdamHparams(hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, 0 if on_device else step,
-                      step.data_ptr() if on_device else None)
-    _adamw(P[0], packed, n, h, grad_scale, status, stream=stream)
+    _adamw(P[0] if len(P) else None, P, G, M, V, m_scales, v_scales, hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, step,
+           grad_scale, status, stream=stream)
 
 
 def profiler_enable(on: bool = True):

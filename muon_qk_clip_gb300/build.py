@@ -1,8 +1,9 @@
 """Build libmuonclip.so (in-tree) for sm_103a with nvcc.
 
 Each translation unit is compiled in parallel, then linked against the shared
-CUDA runtime.  The library is rebuilt only when a source or header is newer
-than it.  Run as ``python -m muon_qk_clip_gb300.build``.
+CUDA runtime.  Beside it the binding's helper module _host.so (host code) is
+compiled against torch's headers and linked to the library.  Both are rebuilt
+only when a source or header is newer.  Run as ``python -m muon_qk_clip_gb300.build``.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -19,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuonclip.so")
+HOST = os.path.join(PKG, "_host.so")
+HOST_SRC = os.path.join(CSRC, "host.cxx")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -43,10 +47,10 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOST):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
+    deps = sources() + [HOST_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(d) > t for d in deps)
 
@@ -61,14 +65,48 @@ def _compile(src: str, extra) -> str:
     return obj
 
 
+def _compile_host() -> str:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    obj = os.path.join(BUILD, "host.o")
+    cmd = [_gxx(), "-O2", "-std=c++17", "-fPIC", "-c", "-I", os.path.join(home, "include"),
+           "-I", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", os.path.join(os.path.dirname(cuda_lib_dir()), "include"),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", HOST_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {os.path.basename(HOST_SRC)}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_host(obj: str):
+    import torch
+    home = os.path.dirname(torch.__file__)
+    tmp = HOST + ".tmp"
+    cmd = [_gxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-l:libmuonclip.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-L", cuda_lib_dir(), f"-Wl,-rpath-link,{cuda_lib_dir()}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of _host.so failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
+
+
+def _gxx() -> str:
+    return shutil.which("g++") or "g++"
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compile every source for sm_103a and link libmuonclip.so; returns its path."""
+    """Compile every source for sm_103a, link libmuonclip.so, and build _host.so;
+    returns the library's path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        host = ex.submit(_compile_host)
         objs = list(ex.map(lambda s: _compile(s, list(extra)), srcs))
+        host_obj = host.result()
     libdir = cuda_lib_dir()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs, "-L", libdir, "-lcudart",
@@ -77,6 +115,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_host(host_obj)
     if verbose:
         print(f"built {LIB}")
     return LIB

@@ -530,10 +530,11 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
   auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
   if (at(hp->step_device) % 8 || at(grad_scale) % 4 || at(status) % 4)
     return err(MC_ERR_INVALID_ARG, "%s: step_device, grad_scale or status is not aligned to its type", me);
-  std::vector<Span> spans;
-  spans.reserve(6 * (size_t)count + 3);
-  auto span = [&](const char* name, int i, const void* p, int64_t bytes, bool out) {
-    if (bytes > 0) spans.push_back({at(p), at(p) + (uintptr_t)bytes, out, i, name});
+  // memory by operand: a list's tensors often lie in their order
+  std::vector<Span> spans[7];
+  for (auto& x : spans) x.reserve((size_t)count + 1);
+  auto span = [&](int kind, const char* name, int i, const void* p, int64_t bytes, bool out) {
+    if (bytes > 0) spans[kind].push_back({at(p), at(p) + (uintptr_t)bytes, out, i, name});
   };
   // tensors of one set of types share a launch
   std::vector<Tensor> sorted[8];
@@ -552,24 +553,33 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
     if (at(a.p) % ps || at(a.g) % gs || at(a.m) % ss || at(a.v) % ss || at(a.m_scale) % 4 || at(a.v_scale) % 4)
       return err(MC_ERR_INVALID_ARG, "%s: tensor %d: a pointer is not aligned to its type", me, i);
     const int64_t scales = eight ? cdiv(a.n, kBlock) * 4 : 0;
-    span("p", i, a.p, a.n * ps, true);
-    span("g", i, a.g, a.n * gs, false);
-    span("m", i, a.m, a.n * ss, true);
-    span("v", i, a.v, a.n * ss, true);
-    span("m_scale", i, a.m_scale, scales, true);
-    span("v_scale", i, a.v_scale, scales, true);
+    span(0, "p", i, a.p, a.n * ps, true);
+    span(1, "g", i, a.g, a.n * gs, false);
+    span(2, "m", i, a.m, a.n * ss, true);
+    span(3, "v", i, a.v, a.n * ss, true);
+    span(4, "m_scale", i, a.m_scale, scales, true);
+    span(5, "v_scale", i, a.v_scale, scales, true);
     const bool vec = eight ? at(a.p) % 32 == 0 && at(a.g) % 32 == 0 && at(a.m) % 16 == 0 && at(a.v) % 16 == 0
                            : at(a.p) % (4 * ps) == 0 && at(a.g) % (4 * gs) == 0 && at(a.m) % 16 == 0 && at(a.v) % 16 == 0;
     sorted[(a.p_dtype == MC_BF16) + 2 * (a.g_dtype == MC_BF16) + 4 * eight].push_back(
         {a.p, a.g, a.m, a.v, a.m_scale, a.v_scale, a.n, 0u, vec ? 1u : 0u});
   }
-  span("step_device", -1, hp->step_device, hp->step_device ? 8 : 0, false);
-  span("grad_scale", -1, grad_scale, grad_scale ? 4 : 0, false);
-  span("status", -1, status, status ? 4 : 0, true);
+  span(6, "step_device", -1, hp->step_device, hp->step_device ? 8 : 0, false);
+  span(6, "grad_scale", -1, grad_scale, grad_scale ? 4 : 0, false);
+  span(6, "status", -1, status, status ? 4 : 0, true);
   // what is written shares memory with nothing
-  std::sort(spans.begin(), spans.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
+  std::vector<Span> every;
+  every.reserve(6 * (size_t)count + 3);
+  for (auto& x : spans) {
+    if (!std::is_sorted(x.begin(), x.end(), before)) std::sort(x.begin(), x.end(), before);
+    const auto middle = (ptrdiff_t)every.size();
+    every.insert(every.end(), x.begin(), x.end());
+    if (middle > 0 && !x.empty() && before(x.front(), every[(size_t)middle - 1]))
+      std::inplace_merge(every.begin(), every.begin() + middle, every.end(), before);
+  }
   const Span *far = nullptr, *far_out = nullptr;        // of those before, the one (written) that reaches furthest
-  for (const Span& s : spans) {
+  for (const Span& s : every) {
     const Span* with = s.out ? far : far_out;
     if (with && with->hi > s.lo)
       return err(MC_ERR_INVALID_ARG, "%s: %s of tensor %d overlaps %s of tensor %d", me, s.name, s.index, with->name, with->index);
