@@ -52,7 +52,12 @@ constexpr float kLazy = 8.f;
 // Offsets are data on the device: a value below its predecessor or beyond T is
 // taken as its predecessor or T, which keeps every access inside and every
 // sequence apart, and sets MC_STATUS_BAD_OFFSETS.
+//
+// The lists that only the plan reads stay in shared memory where they fit (prompts
+// of 366 tokens in all: 5 us alone, 7 with the lists in the workspace, whose
+// searches are chains of dependent loads).
 constexpr int kPlanThreads = 1024;
+constexpr size_t kPlanLocal = 46 * 1024;
 
 // Inclusive scan over the block; `carry` is the value before its first thread, and
 // becomes that of its last.
@@ -87,6 +92,10 @@ __device__ inline int block_scan(int v, int* warps, int& carry) {
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constant__ PackedPlan p) {
   __shared__ int warps[32];
   __shared__ int most;
+  extern __shared__ int local[];
+  int* bounds = p.local ? local : p.bounds;
+  int* first = p.local ? bounds + p.nseq + 1 : p.first;
+  int* place = p.local ? first + p.nseq : p.place;
   await_previous();
   release_next();
   const int tid = threadIdx.x;
@@ -101,48 +110,45 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int s = s0 + tid;
     const int v = s <= p.nseq ? p.offsets[s] : 0, c = block_scan<true>(min(max(v, 0), p.T), warps, carry);
     if (s <= p.nseq) {
-      p.bounds[s] = c;
+      bounds[s] = c;
       bad |= c != v;
     }
   }
   if (bad) set_status(p.status, MC_STATUS_BAD_OFFSETS);
   // first[s]: blocks of the sequences before s; place[n]: sequences of n blocks
-  for (int c = tid; c <= p.capacity; c += kPlanThreads) p.place[c] = 0;
-  __threadfence();
+  for (int c = tid; c <= p.capacity; c += kPlanThreads) place[c] = 0;
   __syncthreads();
   carry = 0;
   int my_most = 0;
   for (int s0 = 0; s0 < p.nseq; s0 += kPlanThreads) {
     const int s = s0 + tid;
-    const int n = s < p.nseq ? (p.bounds[s + 1] - p.bounds[s] + p.rows - 1) / p.rows : 0;
+    const int n = s < p.nseq ? (bounds[s + 1] - bounds[s] + p.rows - 1) / p.rows : 0;
     const int end = block_scan<false>(n, warps, carry);
-    if (s < p.nseq) p.first[s] = end - n;
-    if (n > 0) atomicAdd(&p.place[n], 1);
+    if (s < p.nseq) first[s] = end - n;
+    if (n > 0) atomicAdd(&place[n], 1);
     my_most = max(my_most, n);
   }
   const int total = carry;
   if (my_most > 0) atomicMax(&most, my_most);
-  __threadfence();
   __syncthreads();
   // place[c], c = number of a block counted from 1: blocks with a larger number
   int above = 0, before = 0;             // sequences of more blocks; blocks of larger numbers
   for (int c0 = most; c0 > 0; c0 -= kPlanThreads) {
     const int c = c0 - tid;
-    const int cnt = block_scan<false>(c > 0 ? p.place[c] : 0, warps, above);    // sequences of at least c blocks
+    const int cnt = block_scan<false>(c > 0 ? place[c] : 0, warps, above);    // sequences of at least c blocks
     const int upto = block_scan<false>(c > 0 ? cnt : 0, warps, before);
     __syncthreads();
-    if (c > 0) p.place[c] = upto - cnt;
+    if (c > 0) place[c] = upto - cnt;
   }
-  __threadfence();
   __syncthreads();
   for (int x = tid; x < total; x += kPlanThreads) {
     int lo = 0, hi = p.nseq;             // the last sequence whose first block is at or before x, and has blocks
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (p.first[mid] <= x) lo = mid; else hi = mid;
+      if (first[mid] <= x) lo = mid; else hi = mid;
     }
-    const int b = x - p.first[lo], start = p.bounds[lo];
-    p.blocks[atomicAdd(&p.place[b + 1], 1)] = make_int4(start, p.bounds[lo + 1] - start, b, packed_pad(start, lo));
+    const int b = x - first[lo], start = bounds[lo];
+    p.blocks[atomicAdd(&place[b + 1], 1)] = make_int4(start, bounds[lo + 1] - start, b, packed_pad(start, lo));
   }
   if (tid == 0) *p.count = total;
 }
@@ -608,7 +614,10 @@ bool encode_rows(CUtensorMap* m, const void* base, int width, int heads, long lo
 }  // namespace packed
 
 cudaError_t launch_packed_plan(const PackedPlan& p, cudaStream_t s) {
-  return launch_behind(pf::plan_kernel, 1u, (unsigned)pf::kPlanThreads, 0, s, p);
+  PackedPlan q = p;
+  const size_t bytes = (2 * (size_t)p.nseq + p.capacity + 2) * 4;
+  q.local = bytes <= pf::kPlanLocal;
+  return launch_behind(pf::plan_kernel, 1u, (unsigned)pf::kPlanThreads, q.local ? bytes : 0, s, q);
 }
 
 cudaError_t launch_packed_fwd(const PackedFwdParams& p, int blocks, cudaStream_t s, char* err, size_t errlen) {

@@ -303,6 +303,7 @@ struct PackedPlan {
   int T, nseq, H;
   int rows;                // per block: 128, or 256 (pairs of them)
   int capacity;            // T / rows + nseq: more blocks there cannot be
+  bool local;              // bounds, first and place in shared memory instead
   int* bounds;             // workspace [nseq + 1]
   int* first;              // workspace [nseq]
   int* place;              // workspace [capacity + 1]

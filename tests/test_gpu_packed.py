@@ -479,3 +479,22 @@ def test_backward_long_group_against_a_plain_form():
         rk[:, h // 3] += ds.t() @ Q / d ** 0.5
         rv[:, h // 3] += p.t() @ DO
     assert (dk.double() - rk).norm() <= 0.004 * rk.norm() and (dv.double() - rv).norm() <= 0.004 * rv.norm()
+
+
+def test_plan_in_the_workspace_equals_that_in_shared_memory():
+    """9000 sequences' lists stay in the workspace, 3000's in shared memory: equal bits, forward
+    and backward."""
+    rng = np.random.RandomState(5)
+    lens = [int(x) for x in rng.randint(0, 5, 9000)]
+    lens[17], lens[8000] = 300, 140
+    args = with_forward(lens, 2, 1, 32, 32)
+    q, k, v, o, lse, do, offsets = args
+    got = mc.qk_attention_packed_backward(*args)
+    for i in range(0, 9000, 3000):
+        part = offsets[i:i + 3001]
+        a, b = int(part[0]), int(part[-1])
+        one = (part - a).contiguous()
+        x, y, _ = mc.qk_attention_packed_forward(q[a:b], k[a:b], v[a:b], one, lse=True)
+        assert torch.equal(x, o[a:b]) and torch.equal(y, lse[:, a:b])
+        alone = mc.qk_attention_packed_backward(q[a:b], k[a:b], v[a:b], x, y, do[a:b], one)
+        assert all(torch.equal(m, n[a:b]) for m, n in zip(alone, got))
