@@ -5,12 +5,14 @@ this package is its binding plus seeded synthetic inputs for tests and the
 benchmark.
 """
 from .abi import MuonClipError  # noqa: F401
-from .binding import (ClipLayer, ClipSegment, Hparams, alloc_workspace,  # noqa: F401
-                      default_hparams, mha_segments, mla_segments, muon_momentum,
-                      muon_newton_schulz, muonclip_step, qk_attention_backward, qk_attention_forward,
-                      qk_clip_apply, qk_max_logit, workspace_size)
+from .binding import (AdamHparams, ClipLayer, ClipSegment, Hparams, adamw_state, adamw_step,  # noqa: F401
+                      alloc_workspace, default_hparams, gqa_segments, mha_segments, mla_segments,
+                      muon_momentum, muon_newton_schulz, muonclip_step, qk_attention_backward,
+                      qk_attention_forward, qk_attention_packed_backward, qk_attention_packed_forward,
+                      qk_clip_apply, qk_max_logit, qk_norm_rope, qk_norm_rope_backward, workspace_size)
 
-__all__ = ["ClipLayer", "ClipSegment", "Hparams", "MuonClipError", "alloc_workspace",
-           "default_hparams", "mha_segments", "mla_segments", "muon_momentum",
-           "muon_newton_schulz", "muonclip_step", "qk_attention_backward", "qk_attention_forward", "qk_clip_apply",
-           "qk_max_logit", "workspace_size"]
+__all__ = ["AdamHparams", "ClipLayer", "ClipSegment", "Hparams", "MuonClipError", "adamw_state", "adamw_step",
+           "alloc_workspace", "default_hparams", "gqa_segments", "mha_segments", "mla_segments",
+           "muon_momentum", "muon_newton_schulz", "muonclip_step", "qk_attention_backward",
+           "qk_attention_forward", "qk_attention_packed_backward", "qk_attention_packed_forward",
+           "qk_clip_apply", "qk_max_logit", "qk_norm_rope", "qk_norm_rope_backward", "workspace_size"]

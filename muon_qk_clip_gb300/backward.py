@@ -8,8 +8,15 @@ muonclip_step takes:
     dW, dX = backward.project_mla_backward(X, W, H, dq, dk, dkr, dv)
     mc.muonclip_step(W_list, [dW[n] for n in names], M_list, hp, layers=[...])
 
-Products run on mc_matmul, norms and rotations on mc_rms_norm_backward and
-mc_rope_backward; torch only lays out operands (transposes, concatenations).
+and of packed sequences with grouped heads, whose norm weights adamw_step takes:
+
+    q, k, v, saved = forward.project_gqa(X, W, H, H_kv, positions)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    dq, dk, dv = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    dW, dX = backward.project_gqa_backward(X, W, dq, dk, dv, saved, positions)
+
+Products run on mc_matmul, norms and rotations on mc_rms_norm_backward,
+mc_rope_backward and mc_head_norm_rope_backward; torch only lays out operands (transposes, concatenations).
 Weight gradients and dX have X's dtype (bf16: fp32 sums rounded once).  Device
 tensors only.
 """
@@ -102,3 +109,19 @@ def _mla(X, W, H, dq, dk, dkr, dv, d_nope, d_rope, d_v, eps, theta, status):
     # one product over the concatenated down-projections, so dX is rounded once
     dX = _product(torch.cat(down, 1), _turned(torch.cat([W["W_KR"], W["W_DKV"], W["W_DQ"]], 0)), status)
     return dW, dX.reshape(B, S, D)
+
+
+def project_gqa_backward(X, W, dq, dk, dv, saved, positions=None, rot=None, theta: float = 10000.0, status=None):
+    """Of project_gqa: dq [T,H,d], dk [T,H_kv,d] and dv [T,H_kv,d_v] to ({name: dW},
+    dX) for W_Q, W_K, W_V and the given norm weights (those in fp32), with the values
+    that it saved and its other arguments.  No gradient is overwritten."""
+    q, k, rstd = saved
+    with _on_device(X, dq, dk, dv, q, k, rstd, *W.values(), *(() if positions is None else (positions,))):
+        T, D = X.shape
+        dq, dk, dwq, dwk = mc.qk_norm_rope_backward(dq, dk, q, k, rstd, W.get("q_norm"), W.get("k_norm"), positions, theta, rot)
+        parts = {"W_Q": dq.reshape(T, -1), "W_K": dk.reshape(T, -1), "W_V": dv.reshape(T, -1)}
+        dW = {n: _weight(d, X, status) for n, d in parts.items()}
+        dW.update({n: d for n, d in (("q_norm", dwq), ("k_norm", dwk)) if d is not None})
+        # one product over the concatenated features, so dX is rounded once
+        dX = _product(torch.cat([*parts.values()], 1), _turned(torch.cat([W[n] for n in parts], 0)), status)
+        return dW, dX

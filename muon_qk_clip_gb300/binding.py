@@ -735,6 +735,13 @@ def mha_segments(Wq, Wk, H: int, alpha: float = 0.5):
     return [ClipSegment(Wq, 0, d, d, alpha), ClipSegment(Wk, 0, d, d, 1.0 - alpha)]
 
 
+def gqa_segments(Wq, H: int):
+    """QK-Clip segments of a layer whose query heads share key heads: the whole factor
+    on the query head's rows, since a key head serves others too."""
+    d = Wq.shape[0] // H
+    return [ClipSegment(Wq, 0, d, d, 1.0)]
+
+
 def mla_segments(W_UQ, W_UKV, H: int, d_nope=128, d_rope=64, d_v=128):
     """QK-Clip segments of an MLA layer: q^C and k^C by sqrt(gamma), q^R by
     gamma; the shared rotary key (W_KR) and the value rows get none."""

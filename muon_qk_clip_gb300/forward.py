@@ -5,7 +5,9 @@ for MHA; the MLA latent projections with RMSNorm and RoPE, [K2-internals]
 "MLA 的特殊处理"), run on the library's own kernels (mc_matmul on the tcgen05
 GEMM core for bf16, mc_rms_norm, mc_rope) to build inputs for qk_max_logit
 and to re-measure S_max after a clip.  It is not part of the MuonClip step: in
-training, S_max comes from the forward pass.  Device tensors only.
+training, S_max comes from the forward pass.  project_gqa makes the features of
+packed sequences with grouped heads, normalised and rotated (mc_head_norm_rope),
+for qk_attention_packed_forward.  Device tensors only.
 """
 from __future__ import annotations
 
@@ -63,3 +65,25 @@ def _mla(X, W, H, d_nope, d_rope, d_v, with_v):
     if with_v:
         return q, kv[..., :d_nope], kr, kv[..., d_nope:]
     return q, kv[..., :d_nope], kr
+
+
+def packed_positions(offsets, T: int):
+    """Place of each of T packed tokens in its sequence, int32 on offsets' device: the
+    tokens from offsets[s] to offsets[s + 1] count from 0."""
+    t = torch.arange(T, dtype=torch.int32, device=offsets.device)
+    s = torch.searchsorted(offsets, t, right=True, out_int32=True) - 1
+    return (t - offsets[s.clamp_(min=0)]).clamp_(min=0)
+
+
+def project_gqa(X, W, H: int, H_kv: int, positions=None, rot=None, theta: float = 10000.0, eps: float = 1e-6):
+    """Features of packed tokens X [T, D] with grouped heads: Q = X W_Q^T [T,H,d] and
+    K = X W_K^T [T,H_kv,d], each head normalised, times W["q_norm"] and W["k_norm"]
+    [d] where given, its last `rot` features (all by default) rotated at `positions`;
+    V = X W_V^T [T,H_kv,d_v].  Returns (q, k, v, saved), saved for
+    backward.project_gqa_backward."""
+    with _on_device(X, *W.values(), *(() if positions is None else (positions,))):
+        T, D = X.shape
+        heads = lambda w, n: mc.matmul(X, w.contiguous()).reshape(T, n, -1)  # noqa: E731
+        q, k, v = heads(W["W_Q"], H), heads(W["W_K"], H_kv), heads(W["W_V"], H_kv)
+        yq, yk, rstd = mc.qk_norm_rope(q, k, W.get("q_norm"), W.get("k_norm"), positions, theta, rot, eps)
+        return yq, yk, v, (q, k, rstd)
