@@ -63,6 +63,7 @@ struct Tensor {
 };
 struct Coef {
   float b1, c1, b2, c2;                           // beta1, 1 - beta1, beta2, 1 - beta2
+  float one;                                      // 1
   float lr, wd, eps;
   float i1, i2;                                   // 1 / (1 - beta1^t), 1 / sqrt(1 - beta2^t)
   double l1, l2;                                  // log beta1, log beta2 (for a step on the device)
@@ -297,11 +298,14 @@ __device__ inline const Tensor& chunk_of(const Launch<N>& a, int step_values, Ch
 }
 __device__ inline Two dup(float x) { return two(x, x); }
 // Two values' step: p, m and v become the new ones, r the root of v.  m and v by
-// operations of one rounding each, as encode.
+// operations of one rounding each, as encode.  (The sum of two packed products, written
+// as one, is contracted to an fma, which turned a code in 10^6 against operations of
+// one rounding each; a factor of 1 that the compiler does not know keeps it apart.
+// Scalar sums took 456 us where this takes 453, 2 x 65521 x 2048 values.)
 __device__ inline void update(const Coef& c, const Chunk& k, Two g, Two& p, Two& m, Two& v, Two& r) {
   g = mul2(g, dup(k.gs));
-  m = add2(mul2(m, dup(c.b1)), mul2(g, dup(c.c1)));
-  v = add2(mul2(v, dup(c.b2)), mul2(mul2(g, g), dup(c.c2)));
+  m = fma2(mul2(m, dup(c.b1)), dup(c.one), mul2(g, dup(c.c1)));
+  v = fma2(mul2(v, dup(c.b2)), dup(c.one), mul2(mul2(g, g), dup(c.c2)));
   float v0, v1, d0, d1, m0, m1;
   untwo(v, v0, v1);
   r = two(__fsqrt_rn(v0), __fsqrt_rn(v1));
@@ -592,6 +596,7 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
   c.c1 = (float)(1.0 - hp->beta1);
   c.b2 = (float)hp->beta2;
   c.c2 = (float)(1.0 - hp->beta2);
+  c.one = 1.f;
   c.lr = (float)hp->lr;
   c.wd = (float)hp->weight_decay;
   c.eps = (float)hp->eps;

@@ -268,3 +268,37 @@ def test_tensor_of_more_than_2_to_31_values():
     mc.adamw_step([p], [g], hp=mc.AdamHparams(lr=0.25, weight_decay=0.0), step=1, **s)
     torch.cuda.synchronize()
     assert torch.all(p[at] == 0.75) and int((p != 0).sum()) == 4 and int((s["M"][0].view(torch.uint8) != 0).sum()) == 4
+
+
+def test_eight_bit_states_equal_operations_of_one_rounding_each():
+    """m, v and their scales have the bits of elementary fp32 operations in the order of the
+    formulas, step after step: no products and sums contracted to one rounding."""
+    n = 1 << 20
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    P = [torch.randn(n, generator=g, device="cuda").to(BF16)]
+    s, hp = mc.adamw_state(P, 8), mc.AdamHparams()
+    m8, v8, ms, vs = (s[k][0].clone() for k in ("M", "V", "m_scales", "v_scales"))
+    rows = lambda t: t.view(-1, 128)  # noqa: E731
+
+    def codes(x, least):
+        scale = (rows(x).abs().amax(1) * torch.tensor(1 / 448, device="cuda")).clamp(min=SCALE_MIN)
+        y = rows(x) * (1.0 / scale)[:, None]
+        if least:
+            y = torch.where((y > 0) & (y < LEAST), torch.full_like(y, LEAST), y)
+        return y.to(F8).flatten(), scale
+
+    for t in range(1, 4):
+        G = (torch.randn(n, generator=g, device="cuda") * 1e-3).to(BF16)
+        mc.adamw_step(P, [G], hp=hp, step=t, **s)
+        gf = G.float()
+        m = (rows(m8.float()) * ms[:, None]).flatten()
+        r = (rows(v8.float()) * vs[:, None]).flatten()
+        a, b = m * hp.beta1, gf * (1.0 - hp.beta1)
+        m = a + b
+        a, b = (r * r) * hp.beta2, (gf * gf) * (1.0 - hp.beta2)
+        v = a + b
+        (m8, ms), (v8, vs) = codes(m, False), codes(v.sqrt(), True)
+        for name, own, want in (("m", s["M"][0], m8), ("v", s["V"][0], v8)):
+            assert torch.equal(own.view(torch.uint8), want.view(torch.uint8)), (t, name)
+        assert torch.equal(s["m_scales"][0], ms) and torch.equal(s["v_scales"][0], vs), t
