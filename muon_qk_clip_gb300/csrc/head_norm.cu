@@ -9,9 +9,14 @@
 //
 // Queries and keys share one launch: a warp takes a token and a range of its
 // query or key heads, and needs the token's sines and cosines once for them.  A
-// head's row lies over the fewest lanes that hold it 16 bytes each (16 lanes for 128
-// bf16 features, two heads per warp), its sums over these lanes' shuffles, several
-// rows' loads in flight.  Bound by memory.
+// head's row lies over the fewest lanes that hold it, 16 bytes each (16 lanes for 128
+// bf16 features, two heads per warp), or four pairs each where rows are not of whole
+// 16 bytes; its sums go over these lanes' shuffles.
+//
+// Bound by memory: 16384 tokens of 32 / 8 heads of 128 in bf16 56 us, 6.0 TB/s (a copy of
+// as much takes 53), gradient 84.5, 5.95; of 256 in fp32 6.3 and 6.0.  Rows of pairs are
+// bound by issue: 8192 tokens of 32 / 8 heads of width 90 in bf16 38.5 us, 3.1 TB/s (of
+// two-byte accesses without copies ahead 133), in fp32 46.5, 5.1.
 //
 // Turns: a pair's frequency in turns per position is kept as a 64-bit fraction
 // of a turn (from fp64 on the host), and its product with the position, taken
@@ -35,12 +40,20 @@ namespace mc {
 namespace {
 namespace hn {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+// The forward's blocks are small: each leaves its places to the next as its warps end.
+// (16384 tokens, 32 / 8 heads of 128, bf16: eight blocks of 128 threads per SM take 56
+// us, six 61, nine with spills 60; four of 256 60, three 65; 64 threads 71 and more.
+// The gradient, whose blocks stay: two of 256 84.5 us, four of 128 85.)
+constexpr int kFrontThreads = 128, kFrontWarps = kFrontThreads / 32;
+constexpr int kThreads = 256, kWarps = kThreads / 32;        // of the gradient
 constexpr int kMaxPairs = MC_HEAD_MAX / 2;
 constexpr int kFlight = 2;                        // rows of a lane per step of the loop
-// Blocks of the gradient that an SM holds at once, and blocks (rows of weight sums)
-// at most: one wave.
-__host__ __device__ constexpr int back_blocks(int nu) { return nu == 1 ? 2 : 1; }
+// Blocks that an SM holds at once; of the gradient, and blocks (rows of weight sums)
+// at most: one wave.  (Gradient of 8192 tokens, 32 / 8 heads, two blocks and one: bf16
+// of width 90 65 us and 78, fp32 of 90 84 and 83, of 192, two 16-byte parts a lane, 133
+// and 125.)
+__host__ __device__ constexpr int front_blocks(int nu) { return nu == 1 ? 8 : nu == 2 ? 7 : 6; }
+__host__ __device__ constexpr int back_blocks(int nu) { return nu == 2 ? 1 : 2; }
 constexpr int kBackGrid = 152 * 2;
 
 struct Side {                                     // queries or keys
@@ -116,6 +129,17 @@ struct Feat<T, 2> {                               // a pair, whatever its alignm
   __device__ static void to(float* p, float v) { *p = v; }
   __device__ static void to(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
   __device__ void load(const T* p) { a = in(p[0]); b = in(p[1]); }
+  __device__ void load_whole(const void* p) {     // aligned to its size
+    if constexpr (sizeof(T) == 4) {
+      const float2 w = *static_cast<const float2*>(p);
+      a = w.x;
+      b = w.y;
+    } else {
+      const uint32_t w = *static_cast<const uint32_t*>(p);
+      a = __uint_as_float(w << 16);
+      b = __uint_as_float(w & 0xffff0000u);
+    }
+  }
   __device__ void zero() { a = b = 0.f; }
   __device__ void ones() { a = b = 1.f; }
   __device__ void get(Two (&x)[1]) const { x[0] = two(a, b); }
@@ -124,6 +148,16 @@ struct Feat<T, 2> {                               // a pair, whatever its alignm
     untwo(x[0], a, b);
     to(p, a);
     to(p + 1, b);
+  }
+  __device__ static void store_whole(T* p, const Two (&x)[1]) {
+    float2 w;
+    untwo(x[0], w.x, w.y);
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float2*>(p) = w;
+    } else {
+      const __nv_bfloat162 r = __floats2bfloat162_rn(w.x, w.y);
+      *reinterpret_cast<__nv_bfloat162*>(p) = r;
+    }
   }
 };
 
@@ -181,46 +215,52 @@ __device__ inline float both(Two v) {
   return a + b;
 }
 
-// A thread's rows on their way: their 16-byte parts are copied asynchronously to
-// places in shared memory that only this thread reads, kDepth steps of F rows ahead,
-// so that loads in flight take no registers.  (With two steps of them in registers the
-// forward took 69 us instead of 65 for 16384 tokens of 32 / 8 heads of 128, the gradient
-// 103 instead of 84.)  Pairs (V = 2, rows of any alignment) are loaded where they are used.
+// A thread's rows on their way: their parts are copied asynchronously to places in
+// shared memory that only this thread reads, kDepth steps of F rows ahead, so that
+// loads in flight take no registers.  (With two steps of them in registers the
+// gradient took 103 us instead of 84.5 for 16384 tokens of 32 / 8 heads of 128.)  Parts
+// are 16 bytes, or pairs where rows are aligned to those only (WHOLE); pairs of any
+// alignment are loaded where they are used.
 constexpr int kDepth = 3;
-template <typename T, int V>
-constexpr bool kAsync = V * sizeof(T) == 16;
-__device__ inline void copy_16b(uint4* to, const void* from, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+template <int BYTES>
+__device__ inline void copy_part(void* to, const void* from, bool there) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(to)), "l"(from), "n"(BYTES), "r"(there ? BYTES : 0) : "memory");
 }
 __device__ inline void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ inline void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
-template <typename T, int V, int NU, int F>
+template <typename T, int V, int NU, bool WHOLE, int F, int THREADS>
 struct Rows {
-  uint4* fifo;                                    // this thread's first place
+  static constexpr int kPart = V * (int)sizeof(T);
+  char* fifo;                                     // this thread's first place
   const T* base;                                  // the lane's first column of its first row (there if left and cols are positive)
   const T* any;                                   // an address of the operand, for copies of nothing
   long long pitch;                                // of rows that this lane meets in turn
   int left;                                       // rows that it meets
   int cols;                                       // columns from base's to the row's end
   int lanes;
+  __device__ char* place(int step, int n, int u) const { return fifo + (((step % kDepth) * F + n) * NU + u) * THREADS * kPart; }
   __device__ void issue(int step) {
-    if constexpr (kAsync<T, V>) {
+    if constexpr (WHOLE) {
 #pragma unroll
       for (int n = 0; n < F; ++n)
 #pragma unroll
         for (int u = 0; u < NU; ++u) {
           const int i = step * F + n, col = V * lanes * u;
           const bool there = i < left && col < cols;
-          copy_16b(fifo + ((step % kDepth) * F + n) * NU * kThreads + u * kThreads, there ? base + i * pitch + col : any, there);
+          copy_part<kPart>(place(step, n, u), there ? base + i * pitch + col : any, there);
         }
     }
   }
   __device__ void get(int step, int n, int u, Two (&x)[V / 2]) const {
     Feat<T, V> f;
-    if constexpr (kAsync<T, V>) {
-      f.load(reinterpret_cast<const T*>(fifo + ((step % kDepth) * F + n) * NU * kThreads + u * kThreads));
+    if constexpr (WHOLE) {
+      if constexpr (V == 2) f.load_whole(place(step, n, u));
+      else f.load(reinterpret_cast<const T*>(place(step, n, u)));
     } else {
       const int i = step * F + n, col = V * lanes * u;
       f.zero();
@@ -228,23 +268,28 @@ struct Rows {
     }
     f.get(x);
   }
+  __device__ static void put(T* p, const Two (&x)[V / 2]) {
+    if constexpr (V == 2 && WHOLE) Feat<T, V>::store_whole(p, x);
+    else Feat<T, V>::store(p, x);
+  }
 };
 
-template <typename T, int V, int NU>
-__global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) head_norm_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint4 fifo[];
+template <typename T, int V, int NU, bool WHOLE>
+__global__ void __launch_bounds__(kFrontThreads, front_blocks(NU)) head_norm_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) char fifo[];
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
-  const long long unit = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const long long unit = (long long)blockIdx.x * kFrontWarps + (threadIdx.x >> 5);
   const int pieces = p.pieces[0] + p.pieces[1];
   if (unit >= (long long)p.T * pieces) return;
   const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[2]), r = (int)unit - t * pieces, side = r >= p.pieces[0];
   const Side& S = p.side[side];
   const int from = (r - side * p.pieces[0]) * p.span, to = min(S.heads, from + p.span), base = side ? p.side[0].heads : 0;
   const int steps = (to - from + kFlight * rows - 1) / (kFlight * rows);
-  Rows<T, V, NU, kFlight> x;
-  x.fifo = fifo + threadIdx.x;
+  using R = Rows<T, V, NU, WHOLE, kFlight, kFrontThreads>;
+  R x;
+  x.fifo = fifo + threadIdx.x * R::kPart;
   x.any = static_cast<const T*>(S.x);
   x.base = x.any + t * S.xt + (from + group) * S.xh + V * sub;
   x.pitch = rows * S.xh;
@@ -310,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) head_norm_kernel(co
           untwo(mul2(v[k], r2), a, b);
           v[k] = two(fmaf(-b, bs[u][k], a * ac[u][k]), fmaf(b, bc[u][k], a * as[u][k]));
         }
-        if (V * p.lanes * u < x.cols) Feat<T, V>::store(y + h * (rows * S.oh) + V * p.lanes * u, v);
+        if (V * p.lanes * u < x.cols) R::put(y + h * (rows * S.oh) + V * p.lanes * u, v);
       }
     }
     if (i + kDepth < steps) x.issue(i + kDepth);
@@ -318,15 +363,16 @@ __global__ void __launch_bounds__(kThreads, NU == 1 ? 3 : 2) head_norm_kernel(co
   }
 }
 
-template <typename T, int V, int NU>
+template <typename T, int V, int NU, bool WHOLE>
 __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint4 fifo[];                 // rows on their way; then [2][rows of all warps][d] weight sums
+  extern __shared__ __align__(16) char fifo[];    // rows on their way; then [2][rows of all warps][d] weight sums
   await_previous();
   release_next();
   const int lane = threadIdx.x & 31, sub = lane & (p.lanes - 1), rows = 32 / p.lanes, group = lane / p.lanes;
   const int warps = (int)gridDim.x * kWarps, all = kWarps * rows;
   constexpr int F = kFlight;
-  float* sums = reinterpret_cast<float*>(fifo + (kAsync<T, V> ? 2 * kDepth * F * NU * kThreads : 0));
+  using R = Rows<T, V, NU, WHOLE, F, kThreads>;
+  float* sums = reinterpret_cast<float*>(fifo + (WHOLE ? 2 * kDepth * F * NU * kThreads * R::kPart : 0));
   // queries, then keys: one side's weight and its sums at a time in registers
 #pragma unroll 1
   for (int side = 0; side < 2; ++side) {
@@ -341,9 +387,9 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
       const int t = (int)fastdiv((uint32_t)unit, p.div_pieces[side]);
       const int from = ((int)unit - t * pieces) * p.span, to = min(S.heads, from + p.span);
       const int steps = (to - from + F * rows - 1) / (F * rows);
-      Rows<T, V, NU, F> x, g;
-      x.fifo = fifo + threadIdx.x;
-      g.fifo = x.fifo + kDepth * F * NU * kThreads;
+      R x, g;
+      x.fifo = fifo + threadIdx.x * R::kPart;
+      g.fifo = x.fifo + kDepth * F * NU * kThreads * R::kPart;
       x.any = static_cast<const T*>(S.x);
       g.any = static_cast<const T*>(S.dy);
       x.base = x.any + t * S.xt + (from + group) * S.xh + V * sub;
@@ -416,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
           for (int u = 0; u < NU; ++u) {
 #pragma unroll
             for (int k = 0; k < V / 2; ++k) a[n][u][k] = mul2(r2, fma2(a[n][u][k], m2, b[n][u][k]));
-            if (V * p.lanes * u < x.cols) Feat<T, V>::store(o + h * (rows * S.oh) + V * p.lanes * u, a[n][u]);
+            if (V * p.lanes * u < x.cols) R::put(o + h * (rows * S.oh) + V * p.lanes * u, a[n][u]);
           }
         }
       }
@@ -493,10 +539,11 @@ Operand piece(const char* name, const void* p, int64_t align, int64_t bytes, boo
 }
 
 // Fills p with what both directions share; checks strides, alignment and overlaps
-// of the operands.  `vec`: rows can be read 16 bytes at a time.
-mc_status fill(const char* me, const mc_heads* h, Operand* ops, int n, Params& p, bool& vec) {
-  const int64_t es = h->dtype == MC_BF16 ? 2 : 4, per = 16 / es;
-  vec = h->d % per == 0;
+// of the operands.  `wide`: features that rows can be read and written in at a time:
+// 16 bytes, a pair, or 1.
+mc_status fill(const char* me, const mc_heads* h, Operand* ops, int n, Params& p, int& wide) {
+  const int64_t es = h->dtype == MC_BF16 ? 2 : 4;
+  wide = h->d % (16 / es) == 0 ? (int)(16 / es) : 2;
   for (int i = 0; i < n; ++i) {
     Operand& o = ops[i];
     if (!o.p) continue;
@@ -507,7 +554,11 @@ mc_status fill(const char* me, const mc_heads* h, Operand* ops, int n, Params& p
     if (o.st < 0 || o.sh < 0) return err(MC_ERR_INVALID_ARG, "%s: %s has a negative stride", me, o.name);
     if (o.st >= (1ll << 40) / (h->T + 1) || o.sh >= (1ll << 40) / (o.heads + 1))
       return err(MC_ERR_UNSUPPORTED, "%s: %s has strides that are too large", me, o.name);
-    vec = vec && at(o.p) % 16 == 0 && o.st % per == 0 && o.sh % per == 0;
+    for (const int w : {wide, 2, 1})
+      if (at(o.p) % (w * es) == 0 && o.st % w == 0 && o.sh % w == 0) {
+        wide = w < wide ? w : wide;
+        break;
+      }
     const int64_t st[2] = {o.st, o.sh}, ext[2] = {h->T, o.heads};
     if (o.out && !distinct_addresses(st, ext, 2, h->d))
       return err(MC_ERR_INVALID_ARG, "%s: elements of %s share addresses", me, o.name);
@@ -565,11 +616,12 @@ mc_status check_shape(const char* me, const mc_heads* h) {
   return MC_OK;
 }
 
-// Lanes per row, and heads per unit of work: as many as leave `most` units or more,
-// but 16 steps of the loop at most (a token's sines cost one or two).
+// Lanes per row, the fewest that hold it in `parts` features each, and heads per unit of
+// work: as many as leave `most` units or more, but 16 steps of the loop at most (a
+// token's sines cost one or two).
 void split(Params& p, int parts, int flight, long long most) {
   p.lanes = 1;
-  while (p.lanes < 32 && p.lanes < parts) p.lanes *= 2;
+  while (p.lanes * parts < p.d) p.lanes *= 2;
   const int step = 32 / p.lanes * flight;
   int steps = 16;
   while (steps > 1 && p.T * cdiv(p.heads, steps * step) < most) steps /= 2;
@@ -581,30 +633,52 @@ void split(Params& p, int parts, int flight, long long most) {
   }
 }
 
-template <typename T, int V, int NU>
+template <typename T, int V, int NU, bool WHOLE>
 cudaError_t run_forward(Params& p, cudaStream_t s) {
-  split(p, p.d / V, kFlight, sm_count() * 32);
+  split(p, V * NU, kFlight, sm_count() * 32);
   const long long units = (long long)p.T * (p.pieces[0] + p.pieces[1]);
-  constexpr size_t smem = kAsync<T, V> ? (size_t)kDepth * kFlight * NU * kThreads * 16 : 0;
-  const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<T, V, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  constexpr size_t smem = WHOLE ? (size_t)kDepth * kFlight * NU * kFrontThreads * V * sizeof(T) : 0;
+  const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<T, V, NU, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_behind(head_norm_kernel<T, V, NU>, (unsigned)cdiv(units, kWarps), kThreads, smem, s, p);
+  return launch_behind(head_norm_kernel<T, V, NU, WHOLE>, (unsigned)cdiv(units, kFrontWarps), kFrontThreads, smem, s, p);
 }
-template <typename T, int V, int NU>
+template <typename T, int V, int NU, bool WHOLE>
 cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
   const int wave = sm_count() * back_blocks(NU), most = wave < kBackGrid ? wave : kBackGrid;
-  split(p, p.d / V, kFlight, 8ll * most * kWarps);      // some units per warp, that the last ones leave few idle
+  split(p, V * NU, kFlight, 8ll * most * kWarps);      // some units per warp, that the last ones leave few idle
   const long long blocks = cdiv((long long)p.T * (p.pieces[0] > p.pieces[1] ? p.pieces[0] : p.pieces[1]), kWarps);
   const int grid = (int)(blocks < most ? blocks : most);
-  constexpr size_t fifo = kAsync<T, V> ? (size_t)2 * kDepth * kFlight * NU * kThreads * 16 : 0, most_sums = 2 * kWarps * MC_HEAD_MAX * 4;
+  constexpr size_t fifo = WHOLE ? (size_t)2 * kDepth * kFlight * NU * kThreads * V * sizeof(T) : 0, most_sums = 2 * kWarps * MC_HEAD_MAX * 4;
   const size_t smem = fifo + (p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0);   // a warp's rows have at most 256 features
   // the limit belongs to the kernel, not to this call: always that of the largest
-  cudaError_t e = cudaFuncSetAttribute(head_norm_back_kernel<T, V, NU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fifo + most_sums));
+  cudaError_t e = cudaFuncSetAttribute(head_norm_back_kernel<T, V, NU, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fifo + most_sums));
   if (e != cudaSuccess) return e;
-  e = launch_behind(head_norm_back_kernel<T, V, NU>, (unsigned)grid, kThreads, smem, s, p);
+  e = launch_behind(head_norm_back_kernel<T, V, NU, WHOLE>, (unsigned)grid, kThreads, smem, s, p);
   if (e != cudaSuccess || !p.part) return e;
   return launch_behind(head_weight_kernel, (unsigned)cdiv(2 * p.d, 32), 1024, 0, s, p.part, dwq, dwk, grid, p.d);
 }
+
+// By the features that rows can be accessed in (16 bytes, a pair, one) and the width.
+template <typename F>
+cudaError_t by_width(const mc_heads* h, int wide, F run) {
+  using B = __nv_bfloat16;
+  if (h->dtype == MC_BF16) return wide == 8 ? run.template go<B, 8, 1, true>() : wide == 2 ? run.template go<B, 2, 4, true>() : run.template go<B, 2, 4, false>();
+  if (wide == 4) return h->d <= 128 ? run.template go<float, 4, 1, true>() : run.template go<float, 4, 2, true>();
+  return wide == 2 ? run.template go<float, 2, 4, true>() : run.template go<float, 2, 4, false>();
+}
+struct Forward {
+  Params& p;
+  cudaStream_t s;
+  template <typename T, int V, int NU, bool WHOLE>
+  cudaError_t go() { return run_forward<T, V, NU, WHOLE>(p, s); }
+};
+struct Backward {
+  Params& p;
+  float *dwq, *dwk;
+  cudaStream_t s;
+  template <typename T, int V, int NU, bool WHOLE>
+  cudaError_t go() { return run_backward<T, V, NU, WHOLE>(p, dwq, dwk, s); }
+};
 
 }  // namespace hn
 }  // namespace
@@ -634,17 +708,14 @@ mc_status mc_head_norm_rope(const mc_heads* h, const void* q, int64_t q_token, i
                    piece("rstd", rstd, 4, h->T * (H + G) * 4, true)};
   Params p;
   memset(&p, 0, sizeof p);
-  bool vec;
-  if ((st = fill(me, h, ops, 8, p, vec)) != MC_OK) return st;
-  vec = vec && at(wq) % 16 == 0 && (!G || at(wk) % 16 == 0);
+  int wide;
+  if ((st = fill(me, h, ops, 8, p, wide)) != MC_OK) return st;
+  if (wide > 2 && (at(wq) % 16 || (G && at(wk) % 16))) wide = 2;
   p.side[0] = {q, nullptr, yq, wq, ops[0].st, ops[0].sh, 0, 0, ops[2].st, ops[2].sh, h->heads_q};
   p.side[1] = {k, nullptr, yk, wk, ops[1].st, ops[1].sh, 0, 0, ops[3].st, ops[3].sh, h->heads_k};
   p.rstd = rstd;
   const cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e;
-  if (h->dtype == MC_BF16) e = vec ? run_forward<__nv_bfloat16, 8, 1>(p, s) : run_forward<__nv_bfloat16, 2, 4>(p, s);
-  else if (vec) e = h->d <= 128 ? run_forward<float, 4, 1>(p, s) : run_forward<float, 4, 2>(p, s);
-  else e = run_forward<float, 2, 4>(p, s);
+  const cudaError_t e = by_width(h, wide, Forward{p, s});
   if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
   return record_error(MC_OK, "");
 }
@@ -695,18 +766,16 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
                    piece("workspace", weights ? workspace : nullptr, 16, (int64_t)need, true)};
   Params p;
   memset(&p, 0, sizeof p);
-  bool vec;
-  if ((st = fill(me, h, ops, 13, p, vec)) != MC_OK) return st;
-  vec = vec && at(wq) % 16 == 0 && (!G || at(wk) % 16 == 0);
+  int wide;
+  if ((st = fill(me, h, ops, 13, p, wide)) != MC_OK) return st;
+  if (wide > 2 && (at(wq) % 16 || (G && at(wk) % 16))) wide = 2;
   p.side[0] = {q, dyq, dq, wq, ops[2].st, ops[2].sh, ops[0].st, ops[0].sh, ops[4].st, ops[4].sh, h->heads_q};
   p.side[1] = {k, dyk, dk, wk, ops[3].st, ops[3].sh, ops[1].st, ops[1].sh, ops[5].st, ops[5].sh, h->heads_k};
   p.rstd = const_cast<float*>(rstd);              // read only
   p.part = weights ? static_cast<float*>(workspace) : nullptr;
   cudaError_t e;
   float* dw = G ? dwk : nullptr;
-  if (h->dtype == MC_BF16) e = vec ? run_backward<__nv_bfloat16, 8, 1>(p, dwq, dw, s) : run_backward<__nv_bfloat16, 2, 4>(p, dwq, dw, s);
-  else if (vec) e = h->d <= 128 ? run_backward<float, 4, 1>(p, dwq, dw, s) : run_backward<float, 4, 2>(p, dwq, dw, s);
-  else e = run_backward<float, 2, 4>(p, dwq, dw, s);
+  e = by_width(h, wide, Backward{p, dwq, dw, s});
   if (e != cudaSuccess) return err(MC_ERR_CUDA, "%s: %s", me, cudaGetErrorString(e));
   return record_error(MC_OK, "");
 }

@@ -112,7 +112,7 @@ def test_parity(T, H, G, d, rot, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("shift", [0, 8, 1])
+@pytest.mark.parametrize("shift", [0, 8, 1, 2])
 def test_views_of_one_projection_and_in_place(dtype, shift):
     """q and k as head ranges of one buffer, aligned or not, normed in place; the values between
     them stay as they are."""
