@@ -362,8 +362,8 @@ typedef struct {
   int64_t v_strides[2];
 } mc_packed_desc;
 
-/* Bytes of workspace that the packed forward (backward = 0) or backward needs (T,
- * nseq, H, H_kv of *a; its pointers are not looked at). */
+/* Bytes of workspace that the packed forward (backward = 0) or backward needs (from
+ * the sizes of *a; its pointers are not looked at). */
 mc_status qk_attention_packed_workspace_size(const mc_packed_desc* a, int32_t backward, size_t* bytes);
 
 /* O^h = softmax(scale Q^h K^h^T) V^h within each sequence ([K2-internals] "核心数学"), with
@@ -400,8 +400,8 @@ typedef struct {
 
 /* Gradients of qk_attention_packed_forward's O with respect to q, k and v.  As in
  * qk_attention_backward: probabilities recomputed from lse, p and ds rounded to bf16
- * as operands, fp32 sums (over a group's heads too) in a fixed order, each gradient
- * rounded once; ds is exactly 0 where a token sees only itself.  Rows that belong to
+ * as operands, fp32 sums (over a group's heads too) in an order fixed by the sizes and
+ * offsets of the call, each gradient rounded once; ds is exactly 0 where a token sees only itself.  Rows that belong to
  * no sequence are left as they were.  A NaN/Inf gradient sets
  * MC_STATUS_NONFINITE_UPDATE; NaN/Inf inputs may reach every gradient of their
  * sequence and head group, and none of another's. */

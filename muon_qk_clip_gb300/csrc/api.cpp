@@ -1144,8 +1144,9 @@ namespace {
 
 // Workspace of the packed attention, in 256-byte aligned parts.
 struct PackedWorkspace {
-  size_t bounds, first, place, blocks, count, nlse, delta, bytes;
+  size_t bounds, first, place, blocks, count, nlse, delta, part, bytes;
   int64_t capacity, padded;
+  int parts;
 };
 PackedWorkspace plan_packed(const mc_packed_desc* a, bool backward, int rows) {
   PackedWorkspace w;
@@ -1155,7 +1156,7 @@ PackedWorkspace plan_packed(const mc_packed_desc* a, bool backward, int rows) {
     at += (size_t)round_up(bytes, 256);
     return from;
   };
-  w.capacity = (int64_t)a->T / rows + a->nseq;
+  w.capacity = std::min<int64_t>((int64_t)a->T / rows + a->nseq, a->T);      // a block has a token
   w.padded = packed_padded_rows(a->T, a->nseq);
   w.count = part(64);
   w.bounds = part(((int64_t)a->nseq + 1) * 4);
@@ -1164,6 +1165,8 @@ PackedWorkspace plan_packed(const mc_packed_desc* a, bool backward, int rows) {
   w.blocks = part(w.capacity * 16);
   w.nlse = part(backward ? a->H * w.padded * 4 : 0);
   w.delta = part(backward ? a->H * w.padded * 4 : 0);
+  w.parts = backward ? packed_parts(a->T, a->nseq, a->H_kv, a->H / a->H_kv) : 1;
+  w.part = part(w.parts > 1 ? (int64_t)a->H_kv * w.parts * a->T * packed_part_pitch(a->d, a->d_v) * 4 : 0);
   w.bytes = at;
   return w;
 }
@@ -1352,7 +1355,9 @@ mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_
   p.nlse = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.nlse);
   p.ndelta = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.delta);
   p.padded = w.padded;
-  p.by_key_head = packed_order(a, 1);
+  p.parts = w.parts;
+  p.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + w.part);
+  p.by_key_head = packed_order(a, p.parts);
   p.by_head = packed_order(a, p.group);
   p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
   p.count = plan.count;
@@ -1361,7 +1366,7 @@ mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_
   char err[256] = {0};
   cudaError_t e;
   {
-    ProfScope ps(kAttnBwd, 3, (cudaStream_t)stream);
+    ProfScope ps(kAttnBwd, p.parts > 1 ? 4 : 3, (cudaStream_t)stream);
     e = launch_packed_plan(plan, (cudaStream_t)stream);
     if (e == cudaSuccess) e = launch_packed_bwd(p, plan.capacity, (cudaStream_t)stream, err, sizeof err);
   }

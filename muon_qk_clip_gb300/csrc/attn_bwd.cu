@@ -24,7 +24,10 @@
 // Packed sequences with grouped heads (attn_packed.cu) take the same passes: an item
 // is then a block of one sequence, from the plan's list, the dK / dV pass goes over
 // the query tiles of every head of the key head's group, and every tile is bounded by
-// its sequence.
+// its sequence.  With few blocks of keys an item takes a part of these query tiles, and
+// a launch of its own (join_kernel) adds the parts' dK and dV up.  16384 tokens in eight
+// documents, 32 / 8 heads of 128: 975 us, 0.98 PFLOP/s of the five products (of the
+// seven that the passes compute 1.37); rows_kernel takes 46 of them, at 6 TB/s.
 //
 // P and dS go from the compute warps to the tensor core through tensor memory
 // (the A operand of dV, dK and dQ), written over the columns of the S / dP that
@@ -95,6 +98,7 @@ struct Geo {
   FastDiv div_h, div_group_items, div_group, div_last;
   // packed sequences only
   int q_heads;          // per key head
+  int parts;            // of a key block's query tiles, at most
   packed::Order order[2];          // of the dK / dV and the dQ pass
   const packed::Block* blocks;     // the plan's list, heaviest first, and its length
   const int* count;
@@ -158,6 +162,7 @@ __device__ inline bool ring_get(const Ring& r, uint32_t n, int& x, volatile int*
 struct Where {
   int b, h, blk, S, row0;
   long long at;
+  int part;                        // dK / dV pass: of the block's query tiles
 };
 template <bool PACKED>
 struct Hand;
@@ -173,6 +178,7 @@ struct Hand<false> {
     w.S = p.S;
     w.row0 = 0;
     w.at = ((long long)w.b * p.H + w.h) * g.sp;
+    w.part = 0;
     return w;
   }
 };
@@ -193,6 +199,11 @@ struct Hand<true> {
     // the last keys of a sequence have the fewest queries: heaviest first from the other end
     w.blk = pass == 0 ? (x.b.len + BM - 1) / BM - 1 - x.b.index : x.b.index;
     w.at = (pass == 0 ? 0 : x.head * g.sp) + x.b.pad;
+    w.part = 0;
+    if (pass == 0) {
+      w.h = x.head / g.parts;
+      w.part = x.head - w.h * g.parts;
+    }
     return w;
   }
 };
@@ -426,7 +437,29 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
   // number of the sequence's tiles
   auto first_tile = [&](int blk) { return p.causal ? (blk * BM) / NQ : 0; };
   auto end_tile = [&](const Where& w) { return PACKED ? (w.S + NQ - 1) / NQ : g.nt; };
-  const int heads = PACKED ? g.q_heads : 1;                // of the queries, per item
+  // The item's query tiles: n of those from t0 to end of every head of the group, from
+  // the lo-th on.
+  struct Span {
+    int t0, end, lo, n, parts;
+  };
+  auto span_of = [&](const Where& w) {
+    Span a;
+    a.t0 = first_tile(w.blk);
+    a.end = end_tile(w);
+    a.lo = 0;
+    a.n = a.end - a.t0;
+    a.parts = 1;
+    if (PACKED) {
+      a.n *= g.q_heads;
+      if (g.parts > 1) {
+        const int all = a.n, per = max((all + g.parts - 1) / g.parts, kPartTiles);
+        a.parts = (all + per - 1) / per;
+        a.lo = w.part * per;
+        a.n = min(per, all - a.lo);          // none: no such part
+      }
+    }
+    return a;
+  };
 
   if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
@@ -435,19 +468,30 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       bool used_kv = false, used_q[kStages] = {}, used_do[kStages] = {};
       uint32_t par_kv = 0, par_q[kStages] = {}, par_do[kStages] = {};
       int next = atomicAdd(p.counter, 1);
-      typename H::Work x = H::draw(p, g, 0, next), x1 = x;
+      auto draw = [&]() {                      // the counter's item, or the next one that has tiles
+        typename H::Work d = H::draw(p, g, 0, next);
+        if (PACKED)
+          while (H::more(g, d) && span_of(H::where(p, g, d, 0)).n <= 0) {
+            next = atomicAdd(p.counter, 1);
+            d = H::draw(p, g, 0, next);
+          }
+        return d;
+      };
+      typename H::Work x = draw(), x1 = x;
       bool ok = ring_put(ring, 0, x, &abort_flag);
       for (uint32_t n = 1; ok && H::more(g, x); x = x1, ++n) {
         const Where w = H::where(p, g, x, 0);
-        const int t0 = first_tile(w.blk), end = end_tile(w);
-        int left = (end - t0) * heads;   // tiles of the item
-        for (int it = t0, hh = 0; left > 0; --left, it = it + 1 < end ? it + 1 : (++hh, t0)) {
-          const int h = PACKED ? w.h * heads + hh : w.h;
+        const Span a = span_of(w);
+        const int t0 = a.t0, end = a.end;
+        int left = a.n;                        // tiles of the item
+        int hh = PACKED ? a.lo / (end - t0) : 0;
+        bool first = true;
+        for (int it = t0 + a.lo - hh * (end - t0); left > 0; --left, first = false, it = it + 1 < end ? it + 1 : (++hh, t0)) {
+          const int h = PACKED ? w.h * g.q_heads + hh : w.h;
           const long long rowbase = PACKED ? h * g.sp + w.at : w.at;
-          const bool first = it == t0 && hh == 0;
           if (left == 2 || (left == 1 && first)) next = atomicAdd(p.counter, 1);       // used a tile later: its latency is hidden
           if (left == 1) {
-            x1 = H::draw(p, g, 0, next);
+            x1 = draw();
             if (!ring_put(ring, n, x1, &abort_flag)) { ok = false; break; }
           }
           if (!mbar_wait(&q_empty[s], ph ^ 1, &abort_flag)) { ok = false; break; }
@@ -544,7 +588,7 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
       if (!H::more(g, x)) break;
       const Where w = H::where(p, g, x, 0);
-      const int nt = (end_tile(w) - first_tile(w.blk)) * heads;
+      const int nt = span_of(w).n;
       // S and dP of the previous item have been read: its last p_full and
       // ds_full were waited for below
       bool ok = warp_wait(kv_full, li & 1, &abort_flag) && scores();
@@ -595,6 +639,9 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       const bool row = key < w.S;
       __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(p.dv) + b * p.dvs[0] + (w.row0 + key) * p.dvs[1] + h * p.dvs[2];
       __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(p.dk) + b * p.dks[0] + (w.row0 + key) * p.dks[1] + h * p.dks[2];
+      // one of several parts: fp32 rows of dV, then dK, that join_kernel adds up
+      const bool parted = PACKED && g.parts > 1 && span_of(w).parts > 1;
+      float* part = PACKED ? p.part + (((long long)h * g.parts + w.part) * p.S + w.row0 + key) * packed_part_pitch(p.d_head, p.d_v) : nullptr;
 #pragma unroll 1
       for (int c = 0; c < 2 * (NCV + NCH); ++c) {
         const bool is_v = c < 2 * NCV;
@@ -607,8 +654,10 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
         const uint32_t from = (is_v ? t_dv : t_dk) + lanes + col;
         if (is_v || PACKED || col < 64 * g.nck) {
           const int n = (is_v ? p.d_v : p.d_head) - col;
-          if (n > 0)
-            bad |= store_rows(from, (is_v ? dv : dk) + col, is_v ? 1.f : p.scale, row, is_v ? wide_v : wide_k, n);
+          if (n > 0) {
+            if (parted) bad |= store_part(from, part + (is_v ? 0 : part_pitch(p.d_v)) + col, is_v ? 1.f : p.scale, row, n);
+            else bad |= store_rows(from, (is_v ? dv : dk) + col, is_v ? 1.f : p.scale, row, is_v ? wide_v : wide_k, n);
+          }
         } else {
           const int f0 = col - p.d_head, n = part_pitch(p.d_shared) - f0;
           if (n > 0)
@@ -641,10 +690,11 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       if (!ring_get(ring, li, x, &abort_flag)) { fail(); break; }
       if (!H::more(g, x)) break;
       const Where w = H::where(p, g, x, 0);
-      const int t0 = first_tile(w.blk), end = end_tile(w);
+      const Span a = span_of(w);
+      const int t0 = a.t0, end = a.end;
       bool ok = true;
-      int left = (end - t0) * heads;
-      for (int it = t0; left > 0; --left, it = it + 1 < end ? it + 1 : t0, ++t) {
+      int left = a.n;
+      for (int it = PACKED ? t0 + a.lo % (end - t0) : t0; left > 0; --left, it = it + 1 < end ? it + 1 : t0, ++t) {
         const float* nl = rowv + s * 2 * NQ + hf * NH + c0;
         const int i0 = it * NQ + hf * NH;
         const int key0 = w.blk * BM + q * 32;
@@ -1400,6 +1450,43 @@ __global__ void __launch_bounds__(kSharedThreads) shared_kernel(const __grid_con
   if (short_store(to, c, p.d_shared, s, 1.f)) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
 }
 
+// dK and dV of the key blocks whose query tiles were divided among items (span_of in
+// dkv_pass), the parts added up in their order: a block of threads per kJoinRows keys of a
+// head, few enough that all of a thread's loads are in flight at once.
+constexpr int kJoinThreads = 256, kJoinRows = 16;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttnBwdParams p, const __grid_constant__ Geo g) {
+  await_previous();
+  const int heads = p.H / g.q_heads, b = blockIdx.x / (BM / kJoinRows), r0 = (blockIdx.x - b * (BM / kJoinRows)) * kJoinRows;
+  const int e = b / heads, h = b - e * heads;
+  if (e >= *g.count) return;
+  const int4 blk = *reinterpret_cast<const int4*>(g.blocks + e);         // start, length, index
+  if (blk.x < 0 || blk.y < 1 || blk.x > p.S - blk.y || blk.z < 0 || blk.z > (blk.y - 1) / BM) return;
+  const int tiles = ((blk.y + BM - 1) / BM - blk.z) * g.q_heads, per = max((tiles + g.parts - 1) / g.parts, kPartTiles);
+  const int parts = (tiles + per - 1) / per;
+  if (parts < 2) return;
+  const int pitch = packed_part_pitch(p.d_head, p.d_v), quads = pitch / 4, of_v = part_pitch(p.d_v);
+  const int rows = min(kJoinRows, blk.y - blk.z * BM - r0);
+  const long long first = blk.x + blk.z * BM + r0;
+  bool bad = false;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < rows * quads; i += kJoinThreads) {
+    const int r = i / quads, c = 4 * (i - r * quads);
+    const long long row = first + r;
+    const float4* src = reinterpret_cast<const float4*>(p.part + ((long long)h * g.parts * p.S + row) * pitch + c);
+    float4 s = src[0];
+#pragma unroll 4
+    for (int k = 1; k < parts; ++k) {
+      const float4 v = src[(long long)k * p.S * quads];
+      s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+    }
+    const bool is_v = c < of_v;
+    __nv_bfloat16* to = is_v ? static_cast<__nv_bfloat16*>(p.dv) + row * p.dvs[1] + h * p.dvs[2]
+                             : static_cast<__nv_bfloat16*>(p.dk) + row * p.dks[1] + h * p.dks[2];
+    bad |= short_store(to, is_v ? c : c - of_v, is_v ? p.d_v : p.d_head, s, 1.f);
+  }
+  if (bad) set_status(p.status, MC_STATUS_NONFINITE_UPDATE);
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1564,6 +1651,8 @@ cudaError_t launch_packed_bwd(const PackedBwdParams& a, int blocks, cudaStream_t
   g.ncv = (a.d_v + 63) / 64;
   g.sp = a.padded;
   g.q_heads = a.group;
+  g.parts = a.parts;
+  p.part = a.part;
   g.order[0] = a.by_key_head;
   g.order[1] = a.by_head;
   g.blocks = a.blocks;
@@ -1584,12 +1673,14 @@ cudaError_t launch_packed_bwd(const PackedBwdParams& a, int blocks, cudaStream_t
   if (ni * nh > 0x7fffffff) { snprintf(err, errlen, "too many rows for one launch"); return cudaErrorInvalidValue; }
   const cudaError_t e = launch_behind(rows_kernel<true>, (unsigned)(ni * nh), 256, 0, s, p, (int)g.sp, (int)ni, (int)nh, a.blocks, a.count);
   if (e != cudaSuccess) return e;
-  const long long items = (long long)blocks * (a.H + Hkv);
+  const long long items = (long long)blocks * (a.H + Hkv * a.parts);
   const int grid = items < sm_count() ? (int)items : sm_count();
   using Launch = cudaError_t (*)(const AttnBwdParams&, const Maps&, const Maps&, const Geo&, int, cudaStream_t);
   static const Launch by_chunks[2][2] = {{launch_passes<1, 1, true>, launch_passes<1, 2, true>},
                                          {launch_passes<2, 1, true>, launch_passes<2, 2, true>}};
-  return by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
+  const cudaError_t passes = by_chunks[g.nch - 1][g.ncv - 1](p, kv, qm, g, grid, s);
+  if (passes != cudaSuccess || a.parts == 1) return passes;
+  return launch_behind(join_kernel, (unsigned)(blocks * Hkv * (BM / kJoinRows)), kJoinThreads, 0, s, p, g);
 }
 
 }  // namespace mc

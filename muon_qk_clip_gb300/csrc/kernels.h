@@ -302,7 +302,7 @@ struct PackedPlan {
   const int* offsets;      // [nseq + 1]
   int T, nseq, H;
   int rows;                // per block: 128, or 256 (pairs of them)
-  int capacity;            // T / rows + nseq: more blocks there cannot be
+  int capacity;            // min(T / rows + nseq, T): more blocks there cannot be
   bool local;              // bounds, first and place in shared memory instead
   int* bounds;             // workspace [nseq + 1]
   int* first;              // workspace [nseq]
@@ -353,8 +353,27 @@ struct PackedBwdParams {
   const packed::Block* blocks;
   const int* count;
   int* counter;            // [2]
+  int parts;               // that a key block's query tiles are divided into at most
+  float* part;             // workspace [H_kv, parts, T, packed_part_pitch]: dV and dK of the parts; not with one
   int32_t* status;
 };
+// Few blocks of keys leave SMs idle behind the one with most query tiles (of every head
+// of a group): the tiles of a block are then divided among several items, of at least
+// kPartTiles each, whose dK and dV are added up by a launch of their own.  As many parts
+// as give an item per SM (of 152), rounded down where items are short, since a part's fp32
+// rows are written and read once more.  (Parts against none: one sequence of 8000 tokens,
+// 8 / 1 heads of 128, three parts, 269 us against 622; of 512, 16 / 1, 33 against 92; of
+// 4000, 32 / 4, two, 302 against 341.  Four sequences of 2039 tokens, 32 / 8, with two
+// parts 77, without 69.  Parts of 4 tiles: 4093 tokens in 31 sequences, 6 / 2, 38 against 35.)
+constexpr int kPartTiles = 8, kPartMost = 16;
+inline int packed_parts(long long T, long long nseq, long long heads_kv, long long group) {
+  const long long blocks = (T + 127) / 128, items = (blocks + nseq / 2) * heads_kv, tiles = (blocks + nseq - 1) / nseq * group;
+  if (items < 1) return 1;
+  const long long n = (152 + (tiles >= 64 ? items - 1 : 0)) / items, most = (blocks * group + kPartTiles - 1) / kPartTiles;
+  const long long p = n < most ? n : most;
+  return (int)(p < 1 ? 1 : p > kPartMost ? kPartMost : p);
+}
+__host__ __device__ inline constexpr int packed_part_pitch(int d, int d_v) { return part_pitch(d) + part_pitch(d_v); }
 cudaError_t launch_packed_bwd(const PackedBwdParams& p, int blocks, cudaStream_t s, char* err, size_t errlen);
 
 // Bounded-wait self-check (one CTA waits on a phase nothing completes).
