@@ -198,3 +198,50 @@ def test_projections_refuse():
         forward.project_gqa(X, W, 1, 1)
     with pytest.raises(ValueError, match="device tensors"):
         backward.project_gqa_backward(X, W, X[:, None], X[:, None], X[:, None], (X, X, X))
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 values per tensor: the last sequence's results have the bits of that sequence
+    alone (forward, backward, head norms), the last values' AdamW step those of a small tensor."""
+    H, G, d, n, count = 32, 1, 128, 37, 15000
+    T = n * count                            # 555,000 tokens, 2.27e9 values of q
+    assert T * H * d > 1 << 31
+    base = mk((n, H, d), 1.0, "big")
+    q = base.repeat(count, 1, 1)
+    k, v = (mk((n, G, d), 1.0, s).repeat(count, 1, 1) for s in ("bk", "bv"))
+    offsets = torch.arange(0, T + 1, n, dtype=torch.int32, device="cuda")
+    one = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    w = mk((d,), 1.0, "bw")
+    pos = forward.packed_positions(offsets, T)
+    yq, yk, rstd = mc.qk_norm_rope(q, k, w, w, pos)
+    sq, sk, srstd = mc.qk_norm_rope(q[:n], k[:n], w, w, pos[:n])
+    assert torch.equal(yq[-n:], sq) and torch.equal(yk[-n:], sk) and torch.equal(rstd[-n:], srstd)
+    o, lse, smax = mc.qk_attention_packed_forward(yq, yk, v, offsets, lse=True)
+    so, slse, ssmax = mc.qk_attention_packed_forward(sq, sk, v[:n], one, lse=True)
+    assert torch.equal(o[-n:], so) and torch.equal(lse[:, -n:], slse) and torch.equal(smax, ssmax)
+    dq, dk, dv = mc.qk_attention_packed_backward(yq, yk, v, o, lse, q, offsets)
+    sdq, sdk, sdv = mc.qk_attention_packed_backward(sq, sk, v[:n], so, slse, q[:n], one)
+    # a group's query tiles may be divided otherwise among items: fp32 sums of 32 x 37 terms in another order, then a rounding
+    assert torch.equal(dq[-n:], sdq)
+    for big, small in ((dk, sdk), (dv, sdv)):
+        gap = (f64(big[-n:]) - f64(small)) / np.max(np.abs(f64(small)))
+        assert np.max(np.abs(gap)) <= 2.0 ** -7
+    del o, lse, yq, dk, dv
+    gq, gk, dwq, _ = mc.qk_norm_rope_backward(dq, sdk.repeat(count, 1, 1), q, k, rstd, w, w, pos, dq=dq)
+    tq, tk, swq, _ = mc.qk_norm_rope_backward(sdq, sdk, q[:n], k[:n], srstd, w, w, pos[:n])
+    assert torch.equal(gq[-n:], tq) and torch.equal(gk[-n:], tk)
+    # fp32 sums of T H terms over at least 152 blocks of 8 warps of a row each: chains of at most T H / 1216 terms and the blocks'
+    terms = sdq.float().abs().unflatten(-1, (-1, 2)).sum(-1, keepdim=True).expand(-1, -1, -1, 2).flatten(-2) * (q[:n].float() * srstd[:, :H, None]).abs()
+    assert np.all(np.abs(f64(dwq) / count - f64(swq)) <= (T * H / 1216 + 400) * 2.0 ** -24 * f64(terms.sum((0, 1))))
+    del gq, dq, rstd
+    for bits in (32, 8):
+        P, Gr = [q.view(-1)], [q.view(-1).clone()]
+        small = [P[0][-4096:].clone()], [Gr[0][-4096:].clone()]
+        s, t = mc.adamw_state(P, bits), mc.adamw_state(small[0], bits)
+        mc.adamw_step(P, Gr, step=1, **s)
+        mc.adamw_step(*small, step=1, **t)
+        assert torch.equal(P[0][-4096:], small[0][0])
+        for name in ("M", "V"):
+            a, b = s[name][0][-4096:], t[name][0]
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        del P, Gr, s
