@@ -1172,8 +1172,16 @@ PackedWorkspace plan_packed(const mc_packed_desc* a, bool backward, int rows) {
 }
 
 // Rows per block of the forward's plan: two tiles share their keys and values, of
-// two heads if a group has them in pairs, else of two blocks of one head.
-int packed_rows(const mc_packed_desc* a) { return a->H / a->H_kv % 2 == 0 ? 128 : 256; }
+// two heads of a group, or of two blocks of one head.  With an odd number of heads the
+// group's last one has a pair of its own with one tile, which costs less than two
+// blocks per head where most sequences have but one: below 80 tokens per head of the
+// group on average.  (Pairs against blocks, 28 / 4 heads of 128: 8000 tokens in 100
+// sequences 72 us and 99, 4000 in 16 40 and 44, in 8 44 and 46; 12 / 4: 4000 in 31 34 and
+// 40, in 10 26 and 25.)
+int packed_rows(const mc_packed_desc* a) {
+  const int group = a->H / a->H_kv;
+  return group % 2 == 0 || (group > 1 && a->T / a->nseq < 80 * group) ? 128 : 256;
+}
 
 mc_status check_packed_shape(const mc_packed_desc* a) {
   if (!a) return fail(MC_ERR_INVALID_ARG, "packed attention: null descriptor");
@@ -1296,7 +1304,7 @@ mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const in
   memset(&p, 0, sizeof p);
   p.T = a->T; p.H = a->H; p.group = a->H / a->H_kv; p.d = a->d; p.d_v = a->d_v;
   const int rows = packed_rows(a);
-  p.pair = rows == 128;
+  p.pairs = rows == 128 ? (p.group + 1) / 2 : 0;
   p.scale = a->scale;
   PackedTensor ts[] = {{"q", a->q, a->q_strides, a->H, a->d, false, p.qs},
                        {"k", a->k, a->k_strides, a->H_kv, a->d, false, p.ks},
@@ -1308,7 +1316,7 @@ mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const in
   p.q = a->q; p.k = a->k; p.v = a->v; p.o = o;
   p.lse = lse;
   p.smax = smax;
-  p.order = packed_order(a, p.pair ? p.group / 2 : p.group);
+  p.order = packed_order(a, p.pairs ? p.pairs : p.group);
   p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
   p.count = plan.count;
   p.counter = plan.counter;

@@ -8,7 +8,8 @@
 //                 of query rows in a list, those with most keys first
 //   fwd_kernel    persistent, one CTA per SM; an item is two 128-row query tiles
 //                 that share their keys and values: the same rows of two heads of a
-//                 group, or (groups of an odd number of heads) 256 rows of one head
+//                 group, or (groups of an odd number of heads, unless their sequences
+//                 are short) 256 rows of one head
 //
 // Warps of fwd_kernel: 0 producer (TMA), 1 MMA issuer, 4..7 output, 8..11 and
 // 12..15 softmax of the two tiles, a thread per query row.  Tensor memory: S of
@@ -183,11 +184,17 @@ __device__ inline float max3f(float a, float b, float c) {
 struct Tile {
   int row0, nkv, head;
 };
-__device__ inline Tile tile_of(const Item& x, bool pair, int t) {
+__device__ inline Tile tile_of(const PackedFwdParams& p, const Item& x, int t) {
   Tile r;
-  r.row0 = pair ? x.b.index * BM : (2 * x.b.index + t) * BM;
-  r.head = pair ? 2 * x.head + t : x.head;
-  r.nkv = r.row0 < x.b.len ? r.row0 / BM + 1 : 0;
+  r.row0 = p.pairs ? x.b.index * BM : (2 * x.b.index + t) * BM;
+  r.head = x.head;
+  bool there = r.row0 < x.b.len;
+  if (p.pairs) {                         // the last pair of a group of an odd number has one head
+    const int key = x.head / p.pairs, at = 2 * (x.head - key * p.pairs) + t;
+    r.head = key * p.group + at;
+    there = there && at < p.group;
+  }
+  r.nkv = there ? r.row0 / BM + 1 : 0;
   return r;
 }
 
@@ -233,11 +240,11 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
   if (ROLE == kIssue && warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      const int count = *p.count, rows = p.pair ? BM : 2 * BM;
+      const int count = *p.count, rows = p.pairs ? BM : 2 * BM;
       uint32_t s = 0, ph = 0, nq[2] = {0, 0};
       uint32_t used_q = 0, par_q[2] = {}, used_kv = 0, par_kv = 0;      // bits: stages used, and their last phase
       auto load_q = [&](const Item& x, int t) -> bool {
-        const Tile tl = tile_of(x, p.pair, t);
+        const Tile tl = tile_of(p, x, t);
         if (!mbar_wait(&q_empty[t], (nq[t] & 1) ^ 1, &abort_flag)) return false;
         mbar_arrive_expect_tx(&q_full[t], NCH * CH);
         for (int c = 0; c < NCH; ++c) load_rows<BM>(qbuf + (t * NCH + c) * CH, &mp.q, &q_full[t], c, tl.head, x.b, tl.row0);
@@ -258,7 +265,7 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
       Item x = item_at(p.blocks, count, p.order, p.T, rows, next), y = x;
       bool ok = ring_put(ring, 0, x, &abort_flag);
       for (uint32_t n = 1; ok && x.head >= 0; x = y, ++n) {
-        const Tile t0 = tile_of(x, p.pair, 0), t1 = tile_of(x, p.pair, 1);
+        const Tile t0 = tile_of(p, x, 0), t1 = tile_of(p, x, 1);
         const int nkv = max(t0.nkv, t1.nkv), head = t0.head / p.group;
         ok = load_q(x, 0);
         for (int j = 0; ok && j < nkv; ++j) {
@@ -320,8 +327,8 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
     int n[2] = {0, 0};                   // key blocks of the item's tiles
     auto next_item = [&](uint32_t li) -> bool {
       if (!ring_get(ring, li, x, &abort_flag)) return false;
-      n[0] = x.head < 0 ? 0 : tile_of(x, p.pair, 0).nkv;
-      n[1] = x.head < 0 ? 0 : tile_of(x, p.pair, 1).nkv;
+      n[0] = x.head < 0 ? 0 : tile_of(p, x, 0).nkv;
+      n[1] = x.head < 0 ? 0 : tile_of(p, x, 1).nkv;
       return true;
     };
     ok = next_item(0);
@@ -387,7 +394,7 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
       if (!(ok = ring_get(ring, li, x, &abort_flag)) || x.head < 0) break;
 #pragma unroll 1
       for (int t = 0; t < 2; ++t) {
-        const Tile tl = tile_of(x, p.pair, t);
+        const Tile tl = tile_of(p, x, t);
         if (tl.nkv == 0) continue;
         const uint32_t par = no[t]++ & 1;
         if (!(ok = warp_wait(&l_full[t], par, &abort_flag) && warp_wait(&o_full[t], par, &abort_flag))) break;
@@ -416,7 +423,7 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
     for (uint32_t li = 0;; ++li) {
       Item x;
       if (!(ok = ring_get(ring, li, x, &abort_flag)) || x.head < 0) break;
-      const Tile tl = tile_of(x, p.pair, t);
+      const Tile tl = tile_of(p, x, t);
       if (tl.nkv == 0) continue;
       float m = -INFINITY, top = -INFINITY;
       unsigned long long l2 = 0;         // two halves of the row sum

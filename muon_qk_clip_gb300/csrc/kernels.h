@@ -324,7 +324,7 @@ struct Order {
 
 struct PackedFwdParams {
   int T, H, group, d, d_v; // group: query heads per key head
-  int pair;                // an item is two heads of a group (else two blocks of rows)
+  int pairs;               // an item is two heads of a group: of so many per key head; 0: two blocks of rows
   float scale;
   const void* q; const void* k; const void* v; void* o;
   long long qs[2], ks[2], vs[2], os[2];            // element strides (token, head)
@@ -361,7 +361,8 @@ struct PackedBwdParams {
 // of a group): the tiles of a block are then divided among several items, of at least
 // kPartTiles each, whose dK and dV are added up by a launch of their own.  As many parts
 // as give an item per SM (of 152), rounded down where items are short, since a part's fp32
-// rows are written and read once more.  (Parts against none: one sequence of 8000 tokens,
+// rows are written and read once more; none where even sequences of twice the average
+// have too few tiles.  (Parts against none: one sequence of 8000 tokens,
 // 8 / 1 heads of 128, three parts, 269 us against 622; of 512, 16 / 1, 33 against 92; of
 // 4000, 32 / 4, two, 302 against 341.  Four sequences of 2039 tokens, 32 / 8, with two
 // parts 77, without 69.  Parts of 4 tiles: 4093 tokens in 31 sequences, 6 / 2, 38 against 35.)
@@ -369,7 +370,7 @@ constexpr int kPartTiles = 8, kPartMost = 16;
 inline int packed_parts(long long T, long long nseq, long long heads_kv, long long group) {
   const long long blocks = (T + 127) / 128, items = (blocks + nseq / 2) * heads_kv, tiles = (blocks + nseq - 1) / nseq * group;
   if (items < 1) return 1;
-  const long long n = (152 + (tiles >= 64 ? items - 1 : 0)) / items, most = (blocks * group + kPartTiles - 1) / kPartTiles;
+  const long long n = (152 + (tiles >= 64 ? items - 1 : 0)) / items, most = (2 * tiles - 1) / kPartTiles;
   const long long p = n < most ? n : most;
   return (int)(p < 1 ? 1 : p > kPartMost ? kPartMost : p);
 }
