@@ -14,7 +14,9 @@
 // rounding.
 //
 // One pass over memory, 22 bytes a value with bf16 p and g and fp32 states, 10.1
-// with 8-bit ones.  A block takes a chunk of one tensor and finds which by a
+// with 8-bit ones: 2 x 65536 x 2048 values 840 us, 7.0 TB/s (a copy reaches 6.8;
+// 55 % are reads), 2 x 65521 x 2048 with 8-bit states 453 us, 6.0 TB/s (four values
+// a thread 825).  A block takes a chunk of one tensor and finds which by a
 // search over the chunks' prefix sums among the launch's parameters.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -42,10 +44,11 @@ constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale of an 8-bi
 // thread's codes are 16 bytes, and eight threads hold a block.
 constexpr int kWide = 4, kWide8 = 16;
 static_assert(kBlock == 8 * kWide8, "eight threads hold a block");
-// Steps per thread block (together a chunk of a tensor): many where that still leaves
-// every SM some thread blocks, so that few loads stand at a block's start with
-// nothing before them.
-constexpr int kLongSteps = 4, kShortSteps = 2, kLongSteps8 = 8, kShortSteps8 = 1;
+// Steps per thread block (together a chunk of a tensor) at most, so that few loads stand
+// at a block's start with nothing before them, and the thread blocks that every SM has
+// left with them: else fewer steps.  (2^24 and 2^25 values with 8-bit states: 34 and 64 us
+// with four, 35 and 64 with two, 42 and 70 with 16; one step for all of 2^26 took 165.)
+constexpr int kSteps = 4, kSteps8 = 8, kPerSm = 4;
 constexpr int kAhead = 2;                         // steps in flight with fp32 states
 constexpr float kLeast = 0x1p-9f;                 // least positive e4m3
 constexpr float kScaleMin = 0x1p-100f;
@@ -618,8 +621,9 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
     std::vector<Tensor>& own = sorted[k];
     long long values = 0;
     for (const Tensor& x : own) values += x.n;
-    const int set = kThreads * (k < 4 ? kWide : kWide8), most = k < 4 ? kLongSteps : kLongSteps8;
-    const int steps = values >= (long long)sm_count() * 16 * most * set ? most : k < 4 ? kShortSteps : kShortSteps8;
+    const int set = kThreads * (k < 4 ? kWide : kWide8);
+    int steps = k < 4 ? kSteps : kSteps8;
+    while (steps > (k < 4 ? kAhead : 1) && values < (long long)sm_count() * kPerSm * steps * set) steps /= 2;
     for (size_t i = 0; i < own.size();) {
       uint32_t chunks = 0;
       size_t j = i;
