@@ -737,7 +737,8 @@ def mha_segments(Wq, Wk, H: int, alpha: float = 0.5):
 
 def gqa_segments(Wq, H: int):
     """QK-Clip segments of a layer whose query heads share key heads: the whole factor
-    on the query head's rows, since a key head serves others too."""
+    on the query head's rows, since a key head serves others too.  (Behind a head norm
+    a factor on the rows changes nothing: such a layer needs no clip.)"""
     d = Wq.shape[0] // H
     return [ClipSegment(Wq, 0, d, d, 1.0)]
 
