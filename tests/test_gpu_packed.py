@@ -498,3 +498,49 @@ def test_plan_in_the_workspace_equals_that_in_shared_memory():
         assert torch.equal(x, o[a:b]) and torch.equal(y, lse[:, a:b])
         alone = mc.qk_attention_packed_backward(q[a:b], k[a:b], v[a:b], x, y, do[a:b], one)
         assert all(torch.equal(m, n[a:b]) for m, n in zip(alone, got))
+
+
+@pytest.mark.parametrize("axis", ["heads", "tokens"])
+def test_broadcast_inputs(axis):
+    """Inputs whose heads, or tokens, share memory are read as the rows that they stand for."""
+    lens, H, G, d = [140, 1, 75], 4, 2, 64
+    q, k, v, do, offsets = features(lens, H, G, d, d)
+    if axis == "heads":
+        views = [t[:, :1].expand_as(t) for t in (q, k, v, do)]
+    else:
+        views = [t[:1].expand_as(t) for t in (q, k, v, do)]
+    whole = [t.contiguous() for t in views]
+    out = []
+    for a, b, c, g in (views, whole):
+        o, lse, smax = mc.qk_attention_packed_forward(a, b, c, offsets, lse=True)
+        out.append((o, lse, smax, *mc.qk_attention_packed_backward(a, b, c, o, lse, g, offsets)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(*out))
+
+
+def test_calls_of_several_host_threads():
+    """Threads on streams of their own, each with other widths and first uses: the bits of calls
+    that each wait for the one before."""
+    import threading
+    shapes = [([300, 40], 4, 2, 64, 64), ([129], 6, 3, 128, 128), ([5] * 20, 3, 1, 80, 48), ([200, 17], 2, 2, 24, 128)]
+    data = [with_forward(*s, seed=i) for i, s in enumerate(shapes)]
+    want = [mc.qk_attention_packed_backward(*a) for a in data]
+    torch.cuda.synchronize()
+    got, errors = [None] * len(shapes), []
+
+    def work(i):
+        try:
+            stream = torch.cuda.Stream()
+            for _ in range(20):
+                q, k, v, o, lse, do, offsets = data[i]
+                o2, lse2, _ = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True, stream=stream)
+                got[i] = mc.qk_attention_packed_backward(q, k, v, o2, lse2, do, offsets, stream=stream)
+            stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(shapes))]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
