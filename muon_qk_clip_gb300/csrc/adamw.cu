@@ -38,7 +38,10 @@ namespace mc {
 namespace {
 namespace aw {
 
-constexpr int kThreads = 256;
+// Small blocks leave their places to the next as their warps end.  (2^27 values, 8-bit
+// states: five blocks of 128 threads per SM 210 us, four 227, six, with spills, 245, two
+// of 256 230; fp32 states 419 and, with 256 threads, 423.)
+constexpr int kThreads = 128;
 constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale of an 8-bit state
 // Values of a thread's step: four with fp32 states; 16 with 8-bit ones, so that a
 // thread's codes are 16 bytes, and eight threads hold a block.
@@ -48,7 +51,7 @@ static_assert(kBlock == 8 * kWide8, "eight threads hold a block");
 // at a block's start with nothing before them, and the thread blocks that every SM has
 // left with them: else fewer steps.  (2^24 and 2^25 values with 8-bit states: 34 and 64 us
 // with four, 35 and 64 with two, 42 and 70 with 16; one step for all of 2^26 took 165.)
-constexpr int kSteps = 4, kSteps8 = 8, kPerSm = 4;
+constexpr int kSteps = 4, kSteps8 = 8, kPerSm = 8;
 constexpr int kAhead = 2;                         // steps in flight with fp32 states
 constexpr float kLeast = 0x1p-9f;                 // least positive e4m3
 constexpr float kScaleMin = 0x1p-100f;
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 
 // The same with 8-bit states.
 template <typename P, typename G, int N>
-__global__ void __launch_bounds__(kThreads, 2) adamw8_kernel(const __grid_constant__ Launch<N> a) {
+__global__ void __launch_bounds__(kThreads, 5) adamw8_kernel(const __grid_constant__ Launch<N> a) {
   await_previous();
   release_next();
   Chunk k;
