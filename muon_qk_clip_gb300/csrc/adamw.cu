@@ -14,9 +14,9 @@
 // rounding.
 //
 // One pass over memory, 22 bytes a value with bf16 p and g and fp32 states, 10.1
-// with 8-bit ones: 2 x 65536 x 2048 values 840 us, 7.0 TB/s (a copy reaches 6.8;
-// 55 % are reads), 2 x 65521 x 2048 with 8-bit states 453 us, 6.0 TB/s (four values
-// a thread 825).  A block takes a chunk of one tensor and finds which by a
+// with 8-bit ones: 2 x 65536 x 2048 values 831 us, 7.1 TB/s (a copy reaches 6.8;
+// 55 % are reads), 2 x 65521 x 2048 with 8-bit states 414 us, 6.6 TB/s (of four
+// values a thread twice that).  A block takes a chunk of one tensor and finds which by a
 // search over the chunks' prefix sums among the launch's parameters.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -49,8 +49,9 @@ constexpr int kWide = 4, kWide8 = 16;
 static_assert(kBlock == 8 * kWide8, "eight threads hold a block");
 // Steps per thread block (together a chunk of a tensor) at most, so that few loads stand
 // at a block's start with nothing before them, and the thread blocks that every SM has
-// left with them: else fewer steps.  (2^24 and 2^25 values with 8-bit states: 34 and 64 us
-// with four, 35 and 64 with two, 42 and 70 with 16; one step for all of 2^26 took 165.)
+// left with them: else fewer steps.  (Blocks of 256 threads, 2^24 and 2^25 values with 8-bit
+// states: 34 and 64 us with four blocks left, 35 and 64 with two, 42 and 70 with 16; one step
+// for all of 2^26 took 165.  More than 8 steps, or 4, gain nothing.)
 constexpr int kSteps = 4, kSteps8 = 8, kPerSm = 8;
 constexpr int kAhead = 2;                         // steps in flight with fp32 states
 constexpr float kLeast = 0x1p-9f;                 // least positive e4m3
@@ -307,7 +308,7 @@ __device__ inline Two dup(float x) { return two(x, x); }
 // operations of one rounding each, as encode.  (The sum of two packed products, written
 // as one, is contracted to an fma, which turned a code in 10^6 against operations of
 // one rounding each; a factor of 1 that the compiler does not know keeps it apart.
-// Scalar sums took 456 us where this takes 453, 2 x 65521 x 2048 values.)
+// Scalar sums took 3 us of 453 more, 2 x 65521 x 2048 values.)
 __device__ inline void update(const Coef& c, const Chunk& k, Two g, Two& p, Two& m, Two& v, Two& r) {
   g = mul2(g, dup(k.gs));
   m = fma2(mul2(m, dup(c.b1)), dup(c.one), mul2(g, dup(c.c1)));
