@@ -226,7 +226,7 @@ def _native(entry, name, *args, on=None):
     index = on.get_device() if isinstance(on, torch.Tensor) else -1
     if index < 0:                                      # refused, or without work
         code, *out = getattr(abi.host(), entry)(*args, 0)
-    elif torch.cuda.current_device() != index:
+    elif torch._C._cuda_getDevice() != index:           # CUDA is initialised: there is a tensor
         with torch.cuda.device(index):
             return _native(entry, name, *args, on=on)
     else:
