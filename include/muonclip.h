@@ -338,6 +338,14 @@ mc_status qk_attention_backward(const mc_attn_desc* attn, const mc_attn_grad* gr
 
 /* ---- Causal attention over packed sequences, with grouped heads ---- */
 
+/* Outputs of the packed calls whose rows of tokens in no sequence are set (o, dq, dk and dv to
+ * zeros, lse to -inf, the logarithm of an empty sum) and not left as they were. */
+#define MC_FILL_O 1
+#define MC_FILL_LSE 2
+#define MC_FILL_DQ 4
+#define MC_FILL_DK 8
+#define MC_FILL_DV 16
+
 /* T tokens that hold nseq sequences one behind the other: sequence s has the tokens
  * offsets[s] .. offsets[s + 1] - 1 (equal offsets: an empty one; tokens before the
  * first offset or behind the last belong to none).  Query head h reads key and value
@@ -360,6 +368,8 @@ typedef struct {
   int64_t q_strides[2];    /* token, head                                       */
   int64_t k_strides[2];
   int64_t v_strides[2];
+  int32_t fill;            /* MC_FILL_* bits; those of the other direction are not looked at */
+  int32_t _pad;
 } mc_packed_desc;
 
 /* Bytes of workspace that the packed forward (backward = 0) or backward needs (from
@@ -371,7 +381,7 @@ mc_status qk_attention_packed_workspace_size(const mc_packed_desc* a, int32_t ba
  * max-combined when accumulate = 1; -inf without any token).  o: device [T, H, d_v],
  * strides as above, must not overlap an input; lse: device [H, T] (natural log of
  * the softmax's denominator) or NULL.  Rows that belong to no sequence are left as
- * they were, in o and lse.  Arithmetic as in qk_attention_forward.  A NaN/Inf in
+ * they were, in o and lse, unless a->fill names the output.  Arithmetic as in qk_attention_forward.  A NaN/Inf in
  * a token's q or k, or a logit that overflows to +Inf or NaN, sets
  * MC_STATUS_NONFINITE_LOGIT (one that overflows to -Inf has weight 0 and need not);
  * NaN/Inf inputs may reach every output of their sequence, and none of another's.  workspace: device, 256-byte aligned, for this
@@ -402,7 +412,8 @@ typedef struct {
  * qk_attention_backward: probabilities recomputed from lse, p and ds rounded to bf16
  * as operands, fp32 sums (over a group's heads too) in an order fixed by the sizes and
  * offsets of the call, each gradient rounded once; ds is exactly 0 where a token sees only itself.  Rows that belong to
- * no sequence are left as they were.  A NaN/Inf gradient sets
+ * no sequence are left as they were, unless a->fill names the output: a product or sum over
+ * all T rows needs them filled.  A NaN/Inf gradient sets
  * MC_STATUS_NONFINITE_UPDATE; NaN/Inf inputs may reach every gradient of their
  * sequence and head group, and none of another's. */
 mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_grad* g, void* workspace,

@@ -80,7 +80,8 @@ class McAttnGrad(ctypes.Structure):
 class McPackedDesc(ctypes.Structure):
     _fields_ = [("T", c_int32), ("nseq", c_int32), ("H", c_int32), ("H_kv", c_int32), ("d", c_int32), ("d_v", c_int32),
                 ("dtype", c_int32), ("scale", c_float), ("offsets", c_void_p), ("q", c_void_p), ("k", c_void_p),
-                ("v", c_void_p), ("q_strides", c_int64 * 2), ("k_strides", c_int64 * 2), ("v_strides", c_int64 * 2)]
+                ("v", c_void_p), ("q_strides", c_int64 * 2), ("k_strides", c_int64 * 2), ("v_strides", c_int64 * 2),
+                ("fill", c_int32), ("_pad", c_int32)]
 
 
 class McPackedGrad(ctypes.Structure):

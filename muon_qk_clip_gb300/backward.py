@@ -114,7 +114,9 @@ def _mla(X, W, H, dq, dk, dkr, dv, d_nope, d_rope, d_v, eps, theta, status):
 def project_gqa_backward(X, W, dq, dk, dv, saved, positions=None, rot=None, theta: float = 10000.0, status=None):
     """Of project_gqa: dq [T,H,d], dk [T,H_kv,d] and dv [T,H_kv,d_v] to ({name: dW},
     dX) for W_Q, W_K, W_V and the given norm weights (those in fp32), with the values
-    that it saved and its other arguments.  No gradient is overwritten."""
+    that it saved and its other arguments.  Sums go over all T tokens: the gradients of
+    those in no sequence must be zeros, as qk_attention_packed_backward allocates them,
+    and their rows of X finite.  No gradient is overwritten."""
     q, k, rstd = saved
     with _on_device(X, dq, dk, dv, q, k, rstd, *W.values(), *(() if positions is None else (positions,))):
         T, D = X.shape

@@ -359,7 +359,8 @@ def qk_attention_packed_forward(q, k, v, offsets, scale=None, out=None, lse=None
     features; query head h reads key head h // (H / H_kv)); offsets [n+1] int32 on
     the device: sequence s has the tokens offsets[s]:offsets[s+1].  Returns (out
     [T,H,dv], lse [H,T] f32 or None, smax [H] f32); pass lse=True to allocate it.
-    Rows of no sequence are not written.  workspace: a CUDA tensor of
+    Rows of tokens in no sequence are zeros (lse: -inf) in an out or lse that the call
+    allocates, and left as they were in one that is given.  workspace: a CUDA tensor of
     packed_workspace_size bytes; without one, one is allocated for the call."""
     return _native("packed_forward", "qk_attention_packed_forward", q, k, v, offsets, scale, out, lse, smax, bool(accumulate),
                    workspace, status)
@@ -370,8 +371,8 @@ def qk_attention_packed_backward(q, k, v, out, lse, dout, offsets, scale=None, d
                                  workspace=None, status=None, *, stream=None):
     """Gradients of qk_attention_packed_forward's output: out, lse as it returned
     them, dout [T,H,dv]; the other arguments as there.  Returns (dq, dk, dv), dk and
-    dv summed over the query heads of a group; rows of no sequence are not written.
-    Outputs are allocated unless given: contiguous, or, of a width that is no
+    dv summed over the query heads of a group; rows of tokens in no sequence are zeros
+    in outputs that the call allocates and left as they were in given ones.  Outputs are allocated unless given: contiguous, or, of a width that is no
     multiple of eight, in rows padded to one.  workspace: a CUDA tensor of
     packed_workspace_size(..., backward=True) bytes; without one, one is allocated."""
     return _native("packed_backward", "qk_attention_packed_backward", q, k, v, out, lse, dout, offsets, scale, dq, dk, dv,

@@ -1320,6 +1320,7 @@ mc_status qk_attention_packed_forward(const mc_packed_desc* a, void* o, const in
   p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
   p.count = plan.count;
   p.counter = plan.counter;
+  p.fill = a->fill;
   p.status = status;
   char err[256] = {0};
   cudaError_t e;
@@ -1370,6 +1371,7 @@ mc_status qk_attention_packed_backward(const mc_packed_desc* a, const mc_packed_
   p.blocks = reinterpret_cast<const packed::Block*>(plan.blocks);
   p.count = plan.count;
   p.counter = plan.counter;
+  p.fill = a->fill;
   p.status = status;
   char err[256] = {0};
   cudaError_t e;

@@ -48,7 +48,7 @@ namespace ab {
 using namespace attn;
 
 constexpr int BM = 128;                  // rows of a work item: keys (dkv) or queries (dq)
-// Warps: 0 producer, 1 MMA issuer, 2 and 3 idle, 4..7 output, 8..15 compute (a
+// Warps: 0 producer, 1 MMA issuer, 2 and 3 idle (packed: rows of no sequence), 4..7 output, 8..15 compute (a
 // warp reads the tensor-memory lanes of its index mod 4).  The launch's 128
 // registers a thread are dealt out again per group of four warps: the sum over
 // the groups, 88 + 72 + 176 + 176, is the launch's 4 x 128.
@@ -102,6 +102,7 @@ struct Geo {
   packed::Order order[2];          // of the dK / dV and the dQ pass
   const packed::Block* blocks;     // the plan's list, heaviest first, and its length
   const int* count;
+  int fill;             // MC_FILL_* bits
 };
 
 // Work order.  Item x is one 128-row block of one (b, h).  Causal blocks differ
@@ -620,6 +621,13 @@ __device__ __forceinline__ void dkv_pass(const AttnBwdParams& p, const Maps& mp,
       __syncwarp();
       mbar_wait(drain, 0, nullptr);
     }
+  } else if (PACKED && ROLE == kIssue) {
+    // ------------------------------------------------------------ rows of no sequence
+    const packed::Outside out = packed::outside_of(g.count, p.S);
+    const int w = 2 * blockIdx.x + warp - 2, warps = 2 * gridDim.x, kv = p.H / g.q_heads;
+    if (g.fill & MC_FILL_DQ) packed::fill_rows(out, p.dq, p.dqs + 1, p.H, p.d_head, w, warps);
+    if (g.fill & MC_FILL_DK) packed::fill_rows(out, p.dk, p.dks + 1, kv, p.d_head, w, warps);
+    if (g.fill & MC_FILL_DV) packed::fill_rows(out, p.dv, p.dvs + 1, kv, p.d_v, w, warps);
   } else if (ROLE == kOutput) {
     // ------------------------------------------------------------ output
     // Warp w: keys 32 q .. 32 q + 31 of the block, every column: dV as soon as the
@@ -1657,6 +1665,7 @@ cudaError_t launch_packed_bwd(const PackedBwdParams& a, int blocks, cudaStream_t
   g.order[1] = a.by_head;
   g.blocks = a.blocks;
   g.count = a.count;
+  g.fill = a.fill;
   const int nq = query_tile(g.nch, g.ncv), nk = key_tile(g.nch, g.ncv), Hkv = a.H / a.group;
   static_assert(query_tile(2, 2) == BM, "the padded rows end with whole blocks of 128");
   Maps kv, qm;

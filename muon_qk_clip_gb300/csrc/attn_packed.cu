@@ -11,7 +11,7 @@
 //                 group, or (groups of an odd number of heads, unless their sequences
 //                 are short) 256 rows of one head
 //
-// Warps of fwd_kernel: 0 producer (TMA), 1 MMA issuer, 4..7 output, 8..11 and
+// Warps of fwd_kernel: 0 producer (TMA), 1 MMA issuer, 2 and 3 rows of no sequence, 4..7 output, 8..11 and
 // 12..15 softmax of the two tiles, a thread per query row.  Tensor memory: S of
 // both tiles (128 columns each; P, in bf16, over its first half) and O of both.
 // Per key block j the tensor core gets, tile by tile, O += P(j) V(j) and S(j + 1) =
@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     }
   }
   if (bad) set_status(p.status, MC_STATUS_BAD_OFFSETS);
+  if (tid == 0) p.count[2] = carry;      // the last offset, made monotone
   // first[s]: blocks of the sequences before s; place[n]: sequences of n blocks
   for (int c = tid; c <= p.capacity; c += kPlanThreads) place[c] = 0;
   __syncthreads();
@@ -159,7 +160,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
     const int b = x - first[lo], start = bounds[lo];
     p.blocks[atomicAdd(&place[b + 1], 1)] = make_int4(start, bounds[lo + 1] - start, b, packed_pad(start, lo));
   }
-  if (tid == 0) *p.count = total;
+  if (tid == 0) {
+    *p.count = total;
+    p.count[1] = bounds[0];
+  }
 }
 
 // ---------------------------------------------------------------- forward
@@ -387,6 +391,12 @@ __device__ __forceinline__ void forward(const PackedFwdParams& p, const Maps& mp
       done(drain);
       mbar_wait(drain, 0, nullptr);
     }
+  } else if (ROLE == kIssue) {
+    // ------------------------------------------------------------ rows of no sequence
+    const Outside out = outside_of(p.count, p.T);
+    const int w = 2 * blockIdx.x + warp - 2, warps = 2 * gridDim.x;
+    if (p.fill & MC_FILL_O) fill_rows(out, p.o, p.os, p.H, p.d_v, w, warps);
+    if (p.lse && (p.fill & MC_FILL_LSE)) fill_lse(out, p.lse, p.H, p.T, w, warps);
   } else if (ROLE == kOutput) {
     // ------------------------------------------------------------ output
     // Warp w: rows 32 q .. 32 q + 31 of both tiles, O / row sum, while the other

@@ -317,7 +317,8 @@ PyObject* packed_forward(Args a) {
   at::Tensor ws = a.maybe("workspace"), status = a.maybe("status");
   const mc_stream_t stream = a.stream();
   one_device(q, {&k, &v, &offsets, &out, &lse, &smax, &ws, &status});
-  const mc_packed_desc d = packed_desc(q, k, v, offsets, scale);
+  mc_packed_desc d = packed_desc(q, k, v, offsets, scale);
+  d.fill = (out.defined() ? 0 : MC_FILL_O) | (lse.defined() ? 0 : MC_FILL_LSE);        // of new ones every row is written
   out = rows_or_new("out", out, q, {q.size(0), q.size(1), v.size(2)}, 8);
   if (lse.defined() || lse_arg == Py_True) lse = whole_or_new("lse", lse, q, {q.size(1), q.size(0)}, at::kFloat);
   if (!smax.defined() && accumulate) bad("accumulate goes with a smax to combine");
@@ -341,7 +342,8 @@ PyObject* packed_backward(Args a) {
   at::Tensor dq = a.maybe("dq"), dk = a.maybe("dk"), dv = a.maybe("dv"), ws = a.maybe("workspace"), status = a.maybe("status");
   const mc_stream_t stream = a.stream();
   one_device(q, {&k, &v, &out, &lse, &dout, &offsets, &dq, &dk, &dv, &ws, &status});
-  const mc_packed_desc d = packed_desc(q, k, v, offsets, scale);
+  mc_packed_desc d = packed_desc(q, k, v, offsets, scale);
+  d.fill = (dq.defined() ? 0 : MC_FILL_DQ) | (dk.defined() ? 0 : MC_FILL_DK) | (dv.defined() ? 0 : MC_FILL_DV);
   const int64_t shape[3] = {q.size(0), q.size(1), v.size(2)};
   rows("out", out, shape, q.scalar_type());
   rows("dout", dout, shape, q.scalar_type());

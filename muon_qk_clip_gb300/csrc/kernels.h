@@ -308,7 +308,7 @@ struct PackedPlan {
   int* first;              // workspace [nseq]
   int* place;              // workspace [capacity + 1]
   int4* blocks;            // workspace [capacity]: start, length, index in the sequence, padded start
-  int* count;              // workspace: blocks
+  int* count;              // workspace [3]: blocks; first token of the first sequence, and behind the last one
   int* counter;            // workspace [2]: the next work items, zeroed
   float* smax;             // [H], set to -inf, or null
   int32_t* status;
@@ -330,6 +330,7 @@ struct PackedFwdParams {
   long long qs[2], ks[2], vs[2], os[2];            // element strides (token, head)
   float* lse;              // [H, T] or null
   float* smax;             // [H], max-combined in place
+  int fill;                // MC_FILL_* bits
   packed::Order order;
   const packed::Block* blocks;
   const int* count;
@@ -349,6 +350,7 @@ struct PackedBwdParams {
   float* nlse;             // workspace [H, padded rows]: -lse log2(e), -inf past a sequence
   float* ndelta;           // workspace [H, padded rows]: -do . o
   long long padded;
+  int fill;                // MC_FILL_* bits
   packed::Order by_key_head, by_head;              // of the two passes
   const packed::Block* blocks;
   const int* count;

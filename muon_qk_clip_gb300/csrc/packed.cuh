@@ -85,6 +85,44 @@ __device__ inline void load_rows(void* dst, const CUtensorMap* map, uint64_t* ba
   tma_load_5d(dst, map, bar, 64 * chunk, head, kFar - n, b.start + first + n, kFar);
 }
 
+// Tokens that belong to no sequence: sequences lie one behind the other, so these are the
+// ones in front of the first and behind the last.  Their rows are set by warps that have nothing else to
+// do, beside the items' work.
+struct Outside {
+  int first, last, n;
+};
+__device__ inline Outside outside_of(const int* count, int T) {
+  Outside x;
+  x.first = min(max(count[1], 0), T);
+  x.last = min(max(count[2], x.first), T);
+  x.n = x.first + T - x.last;
+  return x;
+}
+// Zeros in an output [T, heads, width]; warp `w` of `warps`, half a warp per row.
+__device__ inline void fill_rows(const Outside& x, void* base, const long long* st, int heads, int width, int w, int warps) {
+  const int lane = threadIdx.x & 31, c = 8 * (lane & 15);
+  for (int i = w; i < x.n; i += warps) {
+    const int t = i < x.first ? i : x.last + (i - x.first);
+    for (int h = lane >> 4; h < heads; h += 2) {
+      __nv_bfloat16* row = static_cast<__nv_bfloat16*>(base) + t * st[0] + h * st[1];
+      if (c + 8 <= width) {
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        for (int y = c; y < width; ++y) row[y] = __ushort_as_bfloat16(0);
+      }
+    }
+  }
+}
+// -inf in lse [H, T].
+__device__ inline void fill_lse(const Outside& x, float* lse, int H, int T, int w, int warps) {
+  if (x.n == 0) return;
+  const long long all = (long long)H * x.n;
+  for (long long e = (long long)w * 32 + (threadIdx.x & 31); e < all; e += (long long)warps * 32) {
+    const int h = (int)(e / x.n), i = (int)(e - (long long)h * x.n);
+    lse[(long long)h * T + (i < x.first ? i : x.last + (i - x.first))] = -INFINITY;
+  }
+}
+
 // Host: such a map of [T, heads, width] with strides (token, head), R rows.
 bool encode_rows(CUtensorMap* m, const void* base, int width, int heads, long long T, const long long* st, int rows);
 

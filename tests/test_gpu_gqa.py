@@ -245,3 +245,47 @@ def test_offsets_past_32_bits():
             a, b = s[name][0][-4096:], t[name][0]
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
         del P, Gr, s
+
+
+def test_layer_with_tokens_of_no_sequence():
+    """A fixed T whose offsets leave out the first and the last tokens: they reach no gradient,
+    whatever memory the features' gradients are allocated in; and a captured layer replayed on
+    offsets that leave out more has the bits of eager calls."""
+    lens, lead, tail, H, G, d, D = [90, 0, 61], 20, 85, 4, 2, 64, 192
+    n = sum(lens)
+    T, own = lead + n + tail, slice(lead, lead + n)
+    W = layer(D, H, G, d, d)
+    X, do = mk((T, D), 1.0, "x"), mk((T, H, d), 0.05, "do")
+    offsets = offsets_of(lens) + lead
+    held = [torch.full((T, h, d), float("nan"), dtype=BF16, device="cuda") for h in (H, H, H, G, G, G)]
+    torch.cuda.synchronize()
+    del held
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, smax, dW, dX = run(X, W, H, G, offsets, do, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    x, w = X[own].double().cpu().requires_grad_(True), {m: t.double().cpu().requires_grad_(True) for m, t in W.items()}
+    ref, _ = layer64(x, w, H, G, lens, d)
+    (ref * do[own].double().cpu()).sum().backward()
+    close(o[own], ref, "o")
+    for name in W:
+        close(dW[name], w[name].grad, name)
+    close(dX[own], x.grad, "dX")
+    other = torch.ones(T, dtype=torch.bool, device="cuda")
+    other[own] = False
+    assert torch.all(o[other] == 0) and torch.all(dX[other] == 0)
+    packs = [offsets_of([T, 0]), torch.stack([offsets[0], offsets[1], offsets[3]]), offsets_of([5, 30]) + 7]
+    want = [run(X, W, H, G, p, do) for p in packs]
+    cell = packs[0].clone()
+    run(X, W, H, G, cell, do)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run(X, W, H, G, cell, do)
+    for p, (o1, s1, dW1, dX1) in zip(packs, want):
+        cell.copy_(p)
+        graph.replay()
+        torch.cuda.synchronize()
+        o2, s2, dW2, dX2 = got
+        assert torch.equal(o1, o2) and torch.equal(s1, s2) and torch.equal(dX1, dX2)
+        assert all(torch.equal(dW1[m], dW2[m]) for m in W)

@@ -544,3 +544,56 @@ def test_calls_of_several_host_threads():
     [t.join() for t in threads]
     assert not errors
     assert all(torch.equal(a, b) for x, y in zip(got, want) for a, b in zip(x, y))
+
+
+def poison(*like):
+    """Freed memory of these shapes and types that holds NaN, for the next allocations to find."""
+    held = [torch.full_like(t, float("nan")) for t in like for _ in range(2)]
+    torch.cuda.synchronize()
+    del held
+
+
+@pytest.mark.parametrize("lead,tail", [(0, 37), (150, 0), (3, 700), (0, 0)])
+@pytest.mark.parametrize("H,G,d,dv", [(4, 2, 64, 64), (3, 1, 80, 48), (1, 1, 16, 128)])
+def test_new_outputs_hold_nothing_where_there_is_no_sequence(H, G, d, dv, lead, tail):
+    """Outputs that a call allocates: zeros (lse: -inf) in the rows of tokens in no sequence, whatever
+    the memory held; the other rows as without such tokens.  A given output keeps its rows."""
+    lens = [130, 0, 41]
+    n = sum(lens)
+    q, k, v, do, offsets = features(lens, H, G, d, dv)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+    grads = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+    wide = lambda t: torch.cat([torch.full_like(t[:1], float("nan")).expand(lead, -1, -1), t,  # noqa: E731
+                                torch.full_like(t[:1], float("nan")).expand(tail, -1, -1)])
+    Q, K, V, DO, moved = wide(q), wide(k), wide(v), wide(do), offsets + lead
+    T, own = lead + n + tail, slice(lead, lead + n)
+    other = torch.ones(T, dtype=torch.bool, device="cuda")
+    other[own] = False
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    poison(wide(o), torch.empty(H, T, device="cuda"))
+    O2, L2, s2 = mc.qk_attention_packed_forward(Q, K, V, moved, lse=True, status=st)
+    assert torch.equal(O2[own], o) and torch.equal(L2[:, own], lse) and torch.equal(s2, smax)
+    assert torch.all(O2[other] == 0) and torch.all(L2[:, other] == -float("inf"))
+    poison(Q, K, V)
+    got = mc.qk_attention_packed_backward(Q, K, V, O2, L2, DO, moved, status=st)
+    for x, y in zip(got, grads):
+        assert torch.equal(x[own], y) and torch.all(x[other] == 0)
+    held = torch.full_like(K, 7.0)
+    dq, dk, dvv = mc.qk_attention_packed_backward(Q, K, V, O2, L2, DO, moved, dk=held, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and dk is held and torch.all(held[other] == 7.0)
+    assert torch.all(dq[other] == 0) and torch.all(dvv[other] == 0)
+
+
+def test_only_strangers():
+    """Offsets that leave every token out: outputs of nothing."""
+    q, k, v, do, _ = features([50], 4, 2, 64, 64)
+    for at in (0, 20, 50):
+        offsets = torch.full((4,), at, dtype=torch.int32, device="cuda")
+        poison(q, torch.empty(4, 50, device="cuda"))
+        o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True)
+        poison(q, k, v)
+        grads = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets)
+        torch.cuda.synchronize()
+        assert torch.all(o == 0) and torch.all(lse == -float("inf")) and torch.all(smax == -float("inf"))
+        assert all(torch.all(x == 0) for x in grads)
