@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
   for (int side = 0; side < 2; ++side) {
     const Side& S = p.side[side];
     const int base = side ? p.side[0].heads : 0, pieces = p.pieces[side];
-    Two w[NU][V / 2], dw[NU][V / 2];
+    Two w[NU][V / 2], dw[NU][V / 2];               // (no keys: no weight either, and sums of nothing)
     load_weight<T, V, NU>(p, S.w, sub, w);
 #pragma unroll
     for (int i = 0; i < NU * V / 2; ++i) dw[i / (V / 2)][i % (V / 2)] = 0;
@@ -712,7 +712,7 @@ mc_status mc_head_norm_rope(const mc_heads* h, const void* q, int64_t q_token, i
   if ((st = fill(me, h, ops, 8, p, wide)) != MC_OK) return st;
   if (wide > 2 && (at(wq) % 16 || (G && at(wk) % 16))) wide = 2;
   p.side[0] = {q, nullptr, yq, wq, ops[0].st, ops[0].sh, 0, 0, ops[2].st, ops[2].sh, h->heads_q};
-  p.side[1] = {k, nullptr, yk, wk, ops[1].st, ops[1].sh, 0, 0, ops[3].st, ops[3].sh, h->heads_k};
+  p.side[1] = {k, nullptr, yk, G ? wk : nullptr, ops[1].st, ops[1].sh, 0, 0, ops[3].st, ops[3].sh, h->heads_k};
   p.rstd = rstd;
   const cudaStream_t s = (cudaStream_t)stream;
   const cudaError_t e = by_width(h, wide, Forward{p, s});
@@ -738,7 +738,7 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
   if (st != MC_OK) return st;
   const cudaStream_t s = (cudaStream_t)stream;
   const int64_t es = h->dtype == MC_BF16 ? 2 : 4, H = h->heads_q, G = h->heads_k;
-  if (at(dwq) % 4 || at(dwk) % 4) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
+  if (at(dwq) % 4 || (G && at(dwk) % 4)) return err(MC_ERR_INVALID_ARG, "%s: a pointer is not aligned to its type", me);
   if (h->T == 0) {                                // sums over nothing
     for (float* w : {dwq, G ? dwk : nullptr}) {
       const cudaError_t e = w ? cudaMemsetAsync(w, 0, (size_t)h->d * 4, s) : cudaSuccess;
@@ -770,7 +770,7 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
   if ((st = fill(me, h, ops, 13, p, wide)) != MC_OK) return st;
   if (wide > 2 && (at(wq) % 16 || (G && at(wk) % 16))) wide = 2;
   p.side[0] = {q, dyq, dq, wq, ops[2].st, ops[2].sh, ops[0].st, ops[0].sh, ops[4].st, ops[4].sh, h->heads_q};
-  p.side[1] = {k, dyk, dk, wk, ops[3].st, ops[3].sh, ops[1].st, ops[1].sh, ops[5].st, ops[5].sh, h->heads_k};
+  p.side[1] = {k, dyk, dk, G ? wk : nullptr, ops[3].st, ops[3].sh, ops[1].st, ops[1].sh, ops[5].st, ops[5].sh, h->heads_k};
   p.rstd = const_cast<float*>(rstd);              // read only
   p.part = weights ? static_cast<float*>(workspace) : nullptr;
   cudaError_t e;

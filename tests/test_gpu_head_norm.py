@@ -254,3 +254,25 @@ def test_streams_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip((*want, *grad), (*y, *g)))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_without_keys_their_pointers_are_not_looked_at(dtype):
+    """heads_k of 0 at the C ABI: k, wk, yk, dyk, dk and dwk may be anything, here an odd address of
+    nothing; the results are those of null pointers."""
+    T, H, d = 40, 3, 64
+    q, dy = normal((T, H, d), 1.0, "nk", dtype), normal((T, H, d), 1e-2, "nkd", dtype)
+    w = (1 + normal((d,), 0.2, "nkw", F32)).to(dtype)
+    want = mc.qk_norm_rope(q, None, w)
+    grad = mc.qk_norm_rope_backward(dy, None, q, None, want[2], w)
+    lib, stale = abi.load(), 0x7f0000000001
+    h = abi.McHeads(T, H, 0, d, d, abi.MC_BF16 if dtype == BF16 else abi.MC_F32, EPS, THETA, None)
+    y, dx, rstd = torch.empty_like(q), torch.empty_like(q), torch.empty(T, H, device="cuda")
+    dw, ws = torch.empty(d, device="cuda"), torch.empty(mc.head_norm_backward_workspace_size(d), dtype=torch.uint8, device="cuda")
+    at = lambda t: (t.data_ptr(), H * d, d)  # noqa: E731
+    none, s = (stale, 1, 1), torch.cuda.current_stream().cuda_stream
+    assert lib.mc_head_norm_rope(h, *at(q), *none, w.data_ptr(), stale, *at(y), *none, rstd.data_ptr(), s) == abi.MC_OK
+    assert lib.mc_head_norm_rope_backward(h, *at(dy), *none, *at(q), *none, rstd.data_ptr(), w.data_ptr(), stale, *at(dx), *none,
+                                          dw.data_ptr(), stale, ws.data_ptr(), ws.numel(), s) == abi.MC_OK
+    torch.cuda.synchronize()
+    assert torch.equal(y, want[0]) and torch.equal(rstd, want[2]) and torch.equal(dx, grad[0]) and torch.equal(dw, grad[2])
