@@ -513,6 +513,10 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
 
 /* Values of a tensor per scale of an 8-bit state. */
 #define MC_ADAMW_BLOCK 128
+/* Largest beta1 and beta2 of 8-bit states: each step rounds m and sqrt(v) to the
+ * nearest code, 6 to 12 % from its neighbours, and with larger betas the change of a
+ * step is lost in that rounding (below). */
+#define MC_ADAMW_8BIT_BETA 0.95
 
 /* One parameter tensor of n contiguous values (n = 0: skipped) and its state.
  * p: MC_BF16 or MC_F32, updated in place; g: MC_BF16 or MC_F32, its gradient;
@@ -521,7 +525,16 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
  * hold m and sqrt(v), one scale per MC_ADAMW_BLOCK values (the last block may be
  * shorter): m_scale and v_scale [ceil(n / 128)], value = code * scale, scale =
  * max(max|x| * (1 / 448), 2^-100) over the block, code = e4m3(x * (1 / scale)),
- * rounded to nearest even; a root above zero takes at least the code 2^-9. */
+ * rounded to nearest even; a root above zero takes at least the code 2^-9.
+ *
+ * What rounding to nearest does over many steps (beta1 0.9, beta2 0.95, Gaussian
+ * gradients, against 32-bit states): v settles up to 11 % high and the updates are 4 %
+ * small, with a correlation of 0.995; v follows gradients that fall tenfold.  Beyond 0.95
+ * it does not: at beta2 = 0.98 v stands at twice its value, and where gradients fall
+ * tenfold at 100 times, so larger betas are refused.  It rests on scales that vary from
+ * step to step, as gradients do: a value whose gradient ceases for good in a block whose
+ * largest values stand still keeps its codes, and an update of some tenth of lr.
+ * Parameters of which parts get no gradient for long, or a constant one, want 32 bits. */
 typedef struct {
   void* p;
   const void* g;
@@ -535,7 +548,7 @@ typedef struct {
 } mc_adamw_tensor;
 
 typedef struct {
-  double lr, beta1, beta2;       /* betas in [0, 1)                             */
+  double lr, beta1, beta2;       /* betas in [0, 1), with an 8-bit state up to MC_ADAMW_8BIT_BETA */
   double eps;                    /* >= 0                                        */
   double weight_decay;           /* decoupled                                   */
   int64_t step;                  /* t, 1 for the first step                     */

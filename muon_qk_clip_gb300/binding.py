@@ -695,7 +695,9 @@ def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None,
     what muonclip_step does not take: embeddings, output tables, norm weights.
     P, G: lists of contiguous bf16 or fp32 tensors of any shape, pair by pair of one
     size; M, V: their moments, fp32, or e4m3 (M and the root of V) with m_scales and
-    v_scales, as adamw_state makes them; all updated in place.  step: 1 for the first
+    v_scales, as adamw_state makes them; all updated in place.  8-bit states take betas up to
+    0.95, and want gradients that vary (the C header says what their rounding does over many
+    steps).  step: 1 for the first
     one, or a device int64 tensor of one value that is read when the step runs (for a
     captured step).  grad_scale: a device fp32 tensor of one value that multiplies
     every gradient (clipping by the global norm).  Tensors of one set of types share

@@ -11,7 +11,10 @@
 // spans 2^35 of v within a block, at 2^-4 of the root.  A root above zero never
 // becomes zero (the least code is 2^-9): a forgotten v would divide its next
 // gradient by eps alone.  The parameter's step takes m and v before their
-// rounding.
+// rounding.  A code moves only when a step changes its value by half the way to the
+// next one, 3.1 to 5.6 %: beta2 = 0.95 lowers a root by 2.5 % at most, and v follows its
+// gradients because the blocks' scales, and with them the codes' places, vary from step
+// to step; larger betas are refused.
 //
 // One pass over memory, 22 bytes a value with bf16 p and g and fp32 states, 10.1
 // with 8-bit ones: 2 x 65536 x 2048 values 831 us, 7.1 TB/s (a copy reaches 6.8;
@@ -557,6 +560,9 @@ mc_status step(const mc_adamw_tensor* t, int32_t count, const mc_adamw_hparams* 
       return err(MC_ERR_INVALID_ARG, "%s: tensor %d has dtypes %d, %d, %d", me, i, a.p_dtype, a.g_dtype, a.state_dtype);
     if (a.n == 0) continue;
     const bool eight = a.state_dtype == MC_F8E4M3;
+    if (eight && !(hp->beta1 <= MC_ADAMW_8BIT_BETA && hp->beta2 <= MC_ADAMW_8BIT_BETA))
+      return err(MC_ERR_UNSUPPORTED, "%s: tensor %d: 8-bit states take betas up to %g, these are %g and %g", me, i, MC_ADAMW_8BIT_BETA,
+                 hp->beta1, hp->beta2);
     const size_t ps = a.p_dtype == MC_BF16 ? 2 : 4, gs = a.g_dtype == MC_BF16 ? 2 : 4, ss = eight ? 1 : 4;
     if (!a.p || !a.g || !a.m || !a.v) return err(MC_ERR_INVALID_ARG, "%s: tensor %d: null pointer", me, i);
     if (eight != (a.m_scale != nullptr) || eight != (a.v_scale != nullptr))

@@ -201,6 +201,16 @@ def adamw(lib, *ts, count=None, scale=None, status=None, **kw):
 AT = FAKE + 40 * STEP
 
 
+@pytest.mark.parametrize("kw", [dict(beta1=0.96), dict(beta2=0.98), dict(beta2=0.999), dict(beta1=0.99, beta2=0.9)])
+def test_adamw_refuses_8_bit_states_whose_codes_would_stand_still(lib, kw):
+    assert adamw(lib, tensor(), tensor(1, state_dtype=F8), **kw) == UNS
+    text = lib.mc_last_error().decode()
+    assert "tensor 1" in text and "betas up to 0.95" in text
+    # what is left passes that check: a later refusal is met
+    assert adamw(lib, tensor(0, state_dtype=F8, g=AT), beta1=0.95, beta2=0.95) == INV and "overlaps" in lib.mc_last_error().decode()
+    assert adamw(lib, tensor(0, g=AT), **kw) == INV and "overlaps" in lib.mc_last_error().decode()
+
+
 @pytest.mark.parametrize("kw,needle", [
     (dict(lr=float("nan")), "lr"), (dict(weight_decay=float("inf")), "lr"), (dict(eps=-1e-8), "eps"), (dict(beta1=1.0), "beta"),
     (dict(beta2=-0.1), "beta"), (dict(beta1=float("nan")), "beta"), (dict(step=0), "step"), (dict(count=-1), "need"),
