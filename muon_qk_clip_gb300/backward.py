@@ -25,7 +25,7 @@ from __future__ import annotations
 import torch
 
 from . import binding as mc
-from .forward import _on_device
+from .forward import _gains, _on_device
 
 
 def _turned(t):
@@ -120,7 +120,7 @@ def project_gqa_backward(X, W, dq, dk, dv, saved, positions=None, rot=None, thet
     q, k, rstd = saved
     with _on_device(X, dq, dk, dv, q, k, rstd, *W.values(), *(() if positions is None else (positions,))):
         T, D = X.shape
-        dq, dk, dwq, dwk = mc.qk_norm_rope_backward(dq, dk, q, k, rstd, W.get("q_norm"), W.get("k_norm"), positions, theta, rot)
+        dq, dk, dwq, dwk = mc.qk_norm_rope_backward(dq, dk, q, k, rstd, *_gains(W, X.dtype), positions, theta, rot)
         parts = {"W_Q": dq.reshape(T, -1), "W_K": dk.reshape(T, -1), "W_V": dv.reshape(T, -1)}
         dW = {n: _weight(d, X, status) for n, d in parts.items()}
         dW.update({n: d for n, d in (("q_norm", dwq), ("k_norm", dwk)) if d is not None})

@@ -701,7 +701,8 @@ def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None,
     one, or a device int64 tensor of one value that is read when the step runs (for a
     captured step).  grad_scale: a device fp32 tensor of one value that multiplies
     every gradient (clipping by the global norm).  Tensors of one set of types share
-    launches."""
+    launches.  The new p is rounded to its type once: a bf16 value stays where it is under an
+    update of less than 2^-9 of it, so weights near 1 (of norms) want fp32."""
     hp = hp or AdamHparams()
     _adamw(P[0] if len(P) else None, P, G, M, V, m_scales, v_scales, hp.lr, hp.beta1, hp.beta2, hp.eps, hp.weight_decay, step,
            grad_scale, status, stream=stream)

@@ -75,15 +75,21 @@ def packed_positions(offsets, T: int):
     return (t - offsets[s.clamp_(min=0)]).clamp_(min=0)
 
 
+def _gains(W, dtype):
+    """The norm weights of queries and keys, if any, in the features' type.  (AdamW's in fp32: a bf16
+    weight near 1 has steps of 2^-8 and 2^-7 and stays where it is under updates of 1e-4.)"""
+    return [None if w is None else w.to(dtype) for w in (W.get("q_norm"), W.get("k_norm"))]
+
+
 def project_gqa(X, W, H: int, H_kv: int, positions=None, rot=None, theta: float = 10000.0, eps: float = 1e-6):
     """Features of packed tokens X [T, D] with grouped heads: Q = X W_Q^T [T,H,d] and
     K = X W_K^T [T,H_kv,d], each head normalised, times W["q_norm"] and W["k_norm"]
-    [d] where given, its last `rot` features (all by default) rotated at `positions`;
+    [d] where given (fp32 or X's type: rounded to that for the call), its last `rot` features (all by default) rotated at `positions`;
     V = X W_V^T [T,H_kv,d_v].  Returns (q, k, v, saved), saved for
     backward.project_gqa_backward."""
     with _on_device(X, *W.values(), *(() if positions is None else (positions,))):
         T, D = X.shape
         heads = lambda w, n: mc.matmul(X, w.contiguous()).reshape(T, n, -1)  # noqa: E731
         q, k, v = heads(W["W_Q"], H), heads(W["W_K"], H_kv), heads(W["W_V"], H_kv)
-        yq, yk, rstd = mc.qk_norm_rope(q, k, W.get("q_norm"), W.get("k_norm"), positions, theta, rot, eps)
+        yq, yk, rstd = mc.qk_norm_rope(q, k, *_gains(W, X.dtype), positions, theta, rot, eps)
         return yq, yk, v, (q, k, rstd)

@@ -289,3 +289,33 @@ def test_layer_with_tokens_of_no_sequence():
         o2, s2, dW2, dX2 = got
         assert torch.equal(o1, o2) and torch.equal(s1, s2) and torch.equal(dX1, dX2)
         assert all(torch.equal(dW1[m], dW2[m]) for m in W)
+
+
+def test_norm_weights_move_over_steps():
+    """README's loop: fp32 norm weights near 1, the default learning rate.  Over 12 steps they go where
+    AdamW's formula in 64 bits takes them from the same gradients, and the layer sees them (bf16
+    weights near 1 would stay exactly where they are: half a step of theirs is 2^-9)."""
+    lens, H, G, d, D = [70, 33], 4, 2, 64, 128
+    W = layer(D, H, G, d, d)
+    gains = ["q_norm", "k_norm"]
+    for n in gains:
+        W[n] = 1 + mk((d,), 1e-3, n, F32)
+    X, do, offsets = mk((sum(lens), D), 1.0, "x"), mk((sum(lens), H, d), 0.05, "do"), offsets_of(lens)
+    s, hp = mc.adamw_state([W[n] for n in gains]), mc.AdamHparams()
+    start = {n: W[n].clone() for n in gains}
+    P, M, V = ({n: f for n, f in zip(gains, (f64(W[n]) * k for n in gains))} for k in (1, 0, 0))
+    first = None
+    for t in range(1, 13):
+        o, _, dW, _ = run(X, W, H, G, offsets, do)
+        first = o if first is None else first
+        mc.adamw_step([W[n] for n in gains], [dW[n] for n in gains], hp=hp, step=t, **s)
+        for n in gains:
+            g = f64(dW[n])
+            M[n] = hp.beta1 * M[n] + (1 - hp.beta1) * g
+            V[n] = hp.beta2 * V[n] + (1 - hp.beta2) * g * g
+            P[n] = P[n] - hp.lr * (M[n] / (1 - hp.beta1 ** t) / (np.sqrt(V[n] / (1 - hp.beta2 ** t)) + hp.eps) + hp.weight_decay * P[n])
+    for n in gains:
+        # a step: lr's share of 40 roundings of the update, and one of the weight; m may cancel, v not
+        assert np.max(np.abs(f64(W[n]) - P[n])) <= 12 * (hp.lr * 200 * 2.0 ** -24 + 2.0 ** -23)
+        assert torch.all(W[n] != start[n]) and float((W[n] - start[n]).abs().mean()) > 2 * hp.lr
+    assert not torch.equal(first, run(X, W, H, G, offsets, do)[0])
