@@ -329,3 +329,21 @@ def test_eight_bit_states_follow_32_bit_ones_over_many_steps(gradients):
         u, U = m[part] / (r[part] + 1e-8), M[part] / (np.sqrt(V[part]) + 1e-8)
         assert 0.9 <= np.median(r[part] ** 2 / V[part]) <= 1.22
         assert 0.9 <= np.linalg.norm(u) / np.linalg.norm(U) <= 1.02 and np.dot(u, U) >= 0.99 * np.linalg.norm(u) * np.linalg.norm(U)
+
+
+@pytest.mark.parametrize("beta1,beta2", [(0.9, 0.95), (0.0, 0.999), (0.5, 0.0), (0.999, 0.9999), (1 - 1e-7, 1 - 1e-9)])
+def test_step_on_the_device_at_any_number(beta1, beta2):
+    """The factors of a step that is read on the device, from 1 to numbers whose powers are 0: the
+    update m i1 / (sqrt(v) i2 + eps) of m = v = g = 1 (which they stay, to 2 w) within 4 w for m and
+    v's root, 5 w for i1 (2 ulp and a quotient), 4 w for i2 (half of 2 ulp, root, quotient), 2 w for
+    fma and product and 4 w for the quotient: 20 w."""
+    hp = mc.AdamHparams(lr=1.0, beta1=beta1, beta2=beta2, eps=0.0, weight_decay=0.0)
+    one = lambda: [torch.ones(5, device="cuda")]  # noqa: E731
+    for t in (-3, 0, 1, 2, 3, 10, 1000, 12345, 10 ** 6, (1 << 24) + 1, (1 << 31) + 5, 1 << 40, (1 << 62) + 1, (1 << 63) - 1):
+        P = [torch.zeros(5, device="cuda")]
+        mc.adamw_step(P, one(), one(), one(), hp=hp, step=torch.tensor([t], device="cuda"))
+        torch.cuda.synchronize()
+        n = np.float64(max(t, 1))
+        power = lambda b: np.expm1(n * np.log(b)) if b else -1.0  # noqa: E731
+        u = -1.0 / power(beta1) * np.sqrt(-power(beta2))
+        assert np.all(np.abs(f64(P[0]) + u) <= 20 * W * u), (t, P[0], u)
