@@ -41,10 +41,14 @@ namespace mc {
 namespace {
 namespace aw {
 
-// Small blocks leave their places to the next as their warps end.  (2^27 values, 8-bit
-// states: five blocks of 128 threads per SM 210 us, four 227, six, with spills, 245, two
+// Small blocks leave their places to the next as their warps end.  (2^27 values, bf16, 8-bit
+// states: five blocks of 128 threads per SM 211 us, four 228, six, with spills, 245, two
 // of 256 230; fp32 states 419 and, with 256 threads, 423.)
 constexpr int kThreads = 128;
+// Blocks per SM with 8-bit states, by the parameters' size: five leave 96 registers a thread, of which
+// 16 fp32 values in flight spill.  (2^27 values, five and four blocks: bf16 parameters with bf16 gradients
+// 211 and 228 us, with fp32 ones, of which 12 bytes spill, 235 and 240; fp32 parameters 303 and 281, 341 and 311.)
+__host__ __device__ constexpr int blocks8(int param_bytes) { return param_bytes == 2 ? 5 : 4; }
 constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale of an 8-bit state
 // Values of a thread's step: four with fp32 states; 16 with 8-bit ones, so that a
 // thread's codes are 16 bytes, and eight threads hold a block.
@@ -433,7 +437,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 
 // The same with 8-bit states.
 template <typename P, typename G, int N>
-__global__ void __launch_bounds__(kThreads, 5) adamw8_kernel(const __grid_constant__ Launch<N> a) {
+__global__ void __launch_bounds__(kThreads, blocks8(sizeof(P))) adamw8_kernel(const __grid_constant__ Launch<N> a) {
   await_previous();
   release_next();
   Chunk k;

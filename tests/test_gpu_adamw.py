@@ -347,3 +347,64 @@ def test_step_on_the_device_at_any_number(beta1, beta2):
         power = lambda b: np.expm1(n * np.log(b)) if b else -1.0  # noqa: E731
         u = -1.0 / power(beta1) * np.sqrt(-power(beta2))
         assert np.all(np.abs(f64(P[0]) + u) <= 20 * W * u), (t, P[0], u)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p_dtype", [BF16, F32])
+@pytest.mark.parametrize("g_dtype", [BF16, F32])
+def test_large_dense_tensors(p_dtype, g_dtype, bits):
+    """25 million values in three tensors of odd sizes, one operand of each an element off every
+    alignment: chunks of the most steps, ragged ends inside a late one, scale blocks in all of them.
+    m, v, codes and scales have the bits of elementary fp32 operations; p lies within its rounding and
+    lr's share of 20 roundings of the update."""
+    sizes, off = (12_000_037, 9_000_001, 4_000_003), ("p", "g", "m")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(8)
+
+    def place(x, shifted):
+        held = torch.empty(x.numel() + 32, dtype=x.dtype, device="cuda")
+        got = held[1:1 + x.numel()] if shifted else held[:x.numel()]
+        return got.copy_(x)
+
+    def codes(x, least):
+        n = x.numel()
+        rows = torch.nn.functional.pad(x, (0, -n % 128)).view(-1, 128)
+        scale = (rows.abs().amax(1) * torch.tensor(1 / 448, device="cuda")).clamp(min=SCALE_MIN)
+        y = rows * (1.0 / scale)[:, None]
+        if least:
+            y = torch.where((y > 0) & (y < LEAST), torch.full_like(y, LEAST), y)
+        return y.to(F8).flatten()[:n], scale
+
+    wide = lambda c, s: (c.float() * s.repeat_interleave(128)[:c.numel()])  # noqa: E731
+    P, G, M, V, ms, vs = [], [], [], [], [], []
+    for n, o in zip(sizes, off):
+        loud = torch.exp(torch.randn(n, generator=gen, device="cuda"))
+        P.append(place((torch.randn(n, generator=gen, device="cuda") * 0.02).to(p_dtype), o == "p"))
+        G.append(place((torch.randn(n, generator=gen, device="cuda") * 1e-3 * loud).to(g_dtype), o == "g"))
+        m, r = torch.randn(n, generator=gen, device="cuda") * 3e-4 * loud, 1e-3 * loud * (0.2 + torch.rand(n, generator=gen, device="cuda"))
+        if bits == 8:
+            (m, a), (r, b) = codes(m, False), codes(r, True)
+            ms.append(a)
+            vs.append(b)
+        M.append(place(m, o == "m"))
+        V.append(place(r if bits == 8 else r * r, False))
+    before = [(p.clone(), wide(m, a) if bits == 8 else m.clone(), wide(v, b).square() if bits == 8 else v.clone())
+              for p, m, v, a, b in zip(P, M, V, ms or sizes, vs or sizes)]
+    hp, t = mc.AdamHparams(lr=1e-2), 50
+    mc.adamw_step(P, G, M, V, hp=hp, step=t, m_scales=ms or None, v_scales=vs or None)
+    for i, (p0, m, v) in enumerate(before):
+        g = G[i].float()
+        a, b = m * hp.beta1, g * (1.0 - hp.beta1)
+        m = a + b
+        a, b = v * hp.beta2, (g * g) * (1.0 - hp.beta2)
+        v = a + b
+        if bits == 8:
+            for own, scale, x, least in ((M[i], ms[i], m, False), (V[i], vs[i], v.sqrt(), True)):
+                want, s = codes(x, least)
+                assert torch.equal(own.view(torch.uint8), want.view(torch.uint8)) and torch.equal(scale, s), i
+        else:
+            assert torch.equal(M[i], m) and torch.equal(V[i], v), i
+        u = m.double() / (1 - hp.beta1 ** t) / ((v.double() / (1 - hp.beta2 ** t)).sqrt() + hp.eps)
+        p = p0.double() - hp.lr * (u + hp.weight_decay * p0.double())
+        tol = hp.lr * 20 * W * (u.abs() + p0.double().abs()) + 1.0001 * torch.finfo(p_dtype).eps / 2 * p.abs()
+        assert torch.all((P[i].double() - p).abs() <= tol), i
