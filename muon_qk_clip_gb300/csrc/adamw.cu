@@ -45,10 +45,11 @@ namespace aw {
 // states: five blocks of 128 threads per SM 211 us, four 228, six, with spills, 245, two
 // of 256 230; fp32 states 419 and, with 256 threads, 423.)
 constexpr int kThreads = 128;
-// Blocks per SM with 8-bit states, by the parameters' size: five leave 96 registers a thread, of which
-// 16 fp32 values in flight spill.  (2^27 values, five and four blocks: bf16 parameters with bf16 gradients
-// 211 and 228 us, with fp32 ones, of which 12 bytes spill, 235 and 240; fp32 parameters 303 and 281, 341 and 311.)
-__host__ __device__ constexpr int blocks8(int param_bytes) { return param_bytes == 2 ? 5 : 4; }
+// Blocks per SM with 8-bit states, by the operands' size: five leave 96 registers a thread, of which
+// 16 fp32 values in flight spill.  (2^27 values, five and four blocks: bf16 parameters and gradients
+// 211 and 228 us; bf16 parameters with fp32 gradients 235 to 267, as the spills fall, and 239; fp32
+// parameters 303 and 281, 341 and 311.)
+__host__ __device__ constexpr int blocks8(int bytes) { return bytes == 4 ? 5 : 4; }
 constexpr int kBlock = MC_ADAMW_BLOCK;            // values per scale of an 8-bit state
 // Values of a thread's step: four with fp32 states; 16 with 8-bit ones, so that a
 // thread's codes are 16 bytes, and eight threads hold a block.
@@ -183,6 +184,9 @@ struct Row<float> {
     x[0] = two(__uint_as_float(w[4 * u]), __uint_as_float(w[4 * u + 1]));
     x[1] = two(__uint_as_float(w[4 * u + 2]), __uint_as_float(w[4 * u + 3]));
   }
+  __device__ Four<float> four(int u) const {
+    return {make_float4(__uint_as_float(w[4 * u]), __uint_as_float(w[4 * u + 1]), __uint_as_float(w[4 * u + 2]), __uint_as_float(w[4 * u + 3]))};
+  }
   __device__ void set(int u, const Two (&x)[2]) {
     float e[4];
     untwo(x[0], e[0], e[1]);
@@ -211,6 +215,7 @@ struct Row<__nv_bfloat16> {
 #pragma unroll
     for (int i = 0; i < 2; ++i) x[i] = two(__uint_as_float(w[2 * u + i] << 16), __uint_as_float(w[2 * u + i] & 0xffff0000u));
   }
+  __device__ Four<__nv_bfloat16> four(int u) const { return {make_uint2(w[2 * u], w[2 * u + 1])}; }
   __device__ void set(int u, const Two (&x)[2]) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -348,24 +353,34 @@ __device__ inline void update(const Coef& c, const Chunk& k, Two g, Two& p, Two&
   const Two u = two(__fdividef(m0, d0), __fdividef(m1, d1));
   p = fma2(dup(-c.lr), fma2(dup(c.wd), p, u), p);
 }
-// z <- NaN where one of the first n of four values is not finite.
-__device__ inline void note(const Two (&x)[2], int n, Two& z) {
-  if (n >= 4) {
-    z = fma2(x[0], 0, fma2(x[1], 0, z));
-    return;
+// Zeros, or NaN once one of the values added is not finite: of four stored values, so after their
+// rounding (to bf16 it may take the largest to infinity), the first n.
+template <typename P>
+struct Finite;
+template <>
+struct Finite<float> {
+  Two z = 0;
+  __device__ void add(const Four<float>& x, int n) {
+    if (n >= 4) z = fma2(two(x.w.x, x.w.y), 0, fma2(two(x.w.z, x.w.w), 0, z));
+    else z = fma2(two(n > 0 ? x.w.x : 0.f, n > 1 ? x.w.y : 0.f), 0, fma2(two(n > 2 ? x.w.z : 0.f, 0.f), 0, z));
   }
-  float e[4];
-  untwo(x[0], e[0], e[1]);
-  untwo(x[1], e[2], e[3]);
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < n) z = fma2(dup(e[i]), 0, z);
-}
-__device__ inline void report(Two z, int32_t* status) {
-  float a, b;
-  untwo(z, a, b);
-  if (a != 0.f || b != 0.f) set_status(status, MC_STATUS_NONFINITE_UPDATE);       // NaN differs from 0
-}
+  __device__ bool all() const {
+    float a, b;
+    untwo(z, a, b);
+    return a == 0.f && b == 0.f;
+  }
+};
+template <>
+struct Finite<__nv_bfloat16> {
+  __nv_bfloat162 z = __floats2bfloat162_rn(0.f, 0.f);
+  __device__ void add(const Four<__nv_bfloat16>& x, int n) {
+    uint2 w = x.w;
+    if (n < 4) w = make_uint2(n >= 2 ? w.x : n == 1 ? w.x & 0xffffu : 0u, n == 3 ? w.y & 0xffffu : 0u);
+    const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+    z = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.x), zero, __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&w.y), zero, z));
+  }
+  __device__ bool all() const { return __low2float(z) == 0.f && __high2float(z) == 0.f; }
+};
 
 template <typename P, typename G, int N>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Launch<N> a) {
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   float *m = static_cast<float*>(t.m) + k.first, *v = static_cast<float*>(t.v) + k.first;
   const int n = k.n;
   const bool vec = t.vec;
-  Two z = 0;                                       // zeros, or NaN once a new p is not finite
+  Finite<P> z;
   struct Raw {
     Four<P> p;
     Four<G> g;
@@ -415,10 +430,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       now.v.get(vv);
 #pragma unroll
       for (int x = 0; x < 2; ++x) update(a.c, k, gv[x], pv[x], mv[x], vv[x], rv);
-      note(pv, n - i, z);
       Four<P> np;
       Four<float> nm, nv;
       np.set(pv);
+      z.add(np, n - i);
       nm.set(mv);
       nv.set(vv);
       if (vec && i + 4 <= n) {
@@ -432,12 +447,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       }
     }
   }
-  report(z, a.c.status);
+  if (!z.all()) set_status(a.c.status, MC_STATUS_NONFINITE_UPDATE);
 }
 
 // The same with 8-bit states.
 template <typename P, typename G, int N>
-__global__ void __launch_bounds__(kThreads, blocks8(sizeof(P))) adamw8_kernel(const __grid_constant__ Launch<N> a) {
+__global__ void __launch_bounds__(kThreads, blocks8(sizeof(P) + sizeof(G))) adamw8_kernel(const __grid_constant__ Launch<N> a) {
   await_previous();
   release_next();
   Chunk k;
@@ -449,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, blocks8(sizeof(P))) adamw8_kernel(co
   float *ms = t.ms + k.first / kBlock, *vs = t.vs + k.first / kBlock;
   const int n = k.n;
   const bool vec = t.vec;
-  Two z = 0;
+  Finite<P> z;
   struct Raw {
     Row<P> p;
     Row<G> g;
@@ -495,8 +510,8 @@ __global__ void __launch_bounds__(kThreads, blocks8(sizeof(P))) adamw8_kernel(co
         Two r = mul2(r2[x], dup(now.vs)), v2 = mul2(r, r);
         update(a.c, k, gv[x], pv[x], mv[2 * u + x], v2, rv[2 * u + x]);
       }
-      note(pv, n - i - 4 * u, z);
       now.p.set(u, pv);
+      z.add(now.p.four(u), n - i - 4 * u);
     }
     // values behind the end are zeros: they neither raise a scale nor are stored
     float sm, sv;
@@ -516,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, blocks8(sizeof(P))) adamw8_kernel(co
       vs[i / kBlock] = sv;
     }
   }
-  report(z, a.c.status);
+  if (!z.all()) set_status(a.c.status, MC_STATUS_NONFINITE_UPDATE);
 }
 
 template <typename P, typename G, bool EIGHT, int N>

@@ -408,3 +408,20 @@ def test_large_dense_tensors(p_dtype, g_dtype, bits):
         p = p0.double() - hp.lr * (u + hp.weight_decay * p0.double())
         tol = hp.lr * 20 * W * (u.abs() + p0.double().abs()) + 1.0001 * torch.finfo(p_dtype).eps / 2 * p.abs()
         assert torch.all((P[i].double() - p).abs() <= tol), i
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("at", [0, 17, 1999, 2002])
+def test_overflow_in_the_rounding_of_p_sets_the_status(bits, at):
+    """A step that takes a bf16 value beyond the largest by more than half a step: finite in fp32,
+    infinite as stored.  One that stays below half a step sets nothing."""
+    top = float(torch.finfo(BF16).max)                     # 2^128 - 2^120; infinity begins at 2^128 - 2^119
+    for lr, status in ((2.0 ** 119 * 1.25, abi.MC_STATUS_NONFINITE_UPDATE), (2.0 ** 119 * 0.5, 0)):
+        P, G = [torch.zeros(2003, dtype=BF16, device="cuda")], [torch.zeros(2003, device="cuda")]
+        P[0][at], G[0][at] = top, -1.0
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        s = mc.adamw_state(P, bits)
+        mc.adamw_step(P, G, hp=mc.AdamHparams(lr=lr, weight_decay=0.0), step=1, status=st, **s)
+        torch.cuda.synchronize()
+        assert st.item() == status and bool(torch.isinf(P[0][at])) == bool(status)
+        assert int((P[0] != 0).sum()) == 1
