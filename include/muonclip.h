@@ -525,7 +525,8 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
  * hold m and sqrt(v), one scale per MC_ADAMW_BLOCK values (the last block may be
  * shorter): m_scale and v_scale [ceil(n / 128)], value = code * scale, scale =
  * max(max|x| * (1 / 448), 2^-100) over the block, code = e4m3(x * (1 / scale)),
- * rounded to nearest even; a root above zero takes at least the code 2^-9.
+ * rounded to nearest even; a root above zero takes at least the code 2^-9 (roots below
+ * 2^-74 have squares below fp32's range and may become 0, as v may in a 32-bit state).
  *
  * What rounding to nearest does over many steps (beta1 0.9, beta2 0.95, Gaussian
  * gradients, against 32-bit states): v settles up to 11 % high and the updates are 4 %

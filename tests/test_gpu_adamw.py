@@ -425,3 +425,24 @@ def test_overflow_in_the_rounding_of_p_sets_the_status(bits, at):
         torch.cuda.synchronize()
         assert st.item() == status and bool(torch.isinf(P[0][at])) == bool(status)
         assert int((P[0] != 0).sum()) == 1
+
+
+def test_small_roots_stay_above_zero_while_their_squares_are_in_range():
+    """Blocks whose scale is 2^e, every positive code among them, without a gradient: a root of 2^-74 or
+    more does not become zero, in one step or in 400 (which lower the scale by 2^-15); smaller ones may,
+    as v may in a 32-bit state, since their squares are below 2^-149."""
+    codes = torch.arange(1, 127, dtype=torch.uint8, device="cuda").view(F8)      # 2^-9 .. 448
+    for e in (0, -40, -65, -66, -80, -100):
+        V = torch.zeros(128, dtype=F8, device="cuda")
+        V[:126] = codes
+        r0 = f64(V.float()) * 2.0 ** e
+        s = dict(M=[torch.zeros(128, dtype=F8, device="cuda")], V=[V], m_scales=[torch.ones(1, device="cuda")],
+                 v_scales=[torch.full((1,), 2.0 ** e, device="cuda")])
+        wide = dict(M=[torch.zeros(128, device="cuda")], V=[torch.tensor(r0 * r0).float().cuda()])
+        for t in range(400 if e >= -40 else 1):
+            for state in (s, wide):
+                mc.adamw_step([torch.ones(128, device="cuda")], [torch.zeros(128, device="cuda")], step=t + 1, **state)
+        torch.cuda.synchronize()
+        safe, r = r0 >= 2.0 ** -74, values(s["V"][0], s["v_scales"][0])
+        assert np.all(r[safe] > 0) and np.all(r[r0 == 0] == 0)
+        assert np.all(f64(wide["V"][0])[safe] > 0)
