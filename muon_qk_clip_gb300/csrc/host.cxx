@@ -5,6 +5,7 @@
 // argument raises ValueError here, the library's own code is returned to it.
 // (In Python the checks and descriptors of one token's head norms took 24 us, those
 // of AdamW over 122 tensors 185.)
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 #include <ATen/ATen.h>
 
@@ -21,6 +22,7 @@ namespace {
 struct Bad : std::runtime_error {
   using std::runtime_error::runtime_error;
 };
+struct Raised {};                        // Python's own error is set
 [[noreturn]] void bad(const std::string& what) { throw Bad(what); }
 
 // The positional arguments of a call, taken in order.
@@ -48,22 +50,22 @@ struct Args {
     if (o == Py_None) return none;
     if (!PyLong_Check(o)) bad(std::string(name) + " must be an integer");
     const long long x = PyLong_AsLongLong(o);
-    if (x == -1 && PyErr_Occurred()) throw std::exception();
+    if (x == -1 && PyErr_Occurred()) throw Raised();
     return x;
   }
   double real() {
     const double x = PyFloat_AsDouble(next());
-    if (x == -1.0 && PyErr_Occurred()) throw std::exception();
+    if (x == -1.0 && PyErr_Occurred()) throw Raised();
     return x;
   }
   int64_t whole() {
     const long long x = PyLong_AsLongLong(next());
-    if (x == -1 && PyErr_Occurred()) throw std::exception();
+    if (x == -1 && PyErr_Occurred()) throw Raised();
     return x;
   }
   mc_stream_t stream() {
     const unsigned long long x = PyLong_AsUnsignedLongLong(next());
-    if (PyErr_Occurred()) throw std::exception();
+    if (PyErr_Occurred()) throw Raised();
     return reinterpret_cast<mc_stream_t>(static_cast<uintptr_t>(x));
   }
 };
@@ -269,7 +271,7 @@ mc_packed_desc packed_desc(const at::Tensor& q, const at::Tensor& k, const at::T
     d.scale = (float)(1.0 / std::sqrt((double)q.size(2)));
   } else {
     const double x = PyFloat_AsDouble(scale);            // beyond fp32: inf, which the library refuses
-    if (x == -1.0 && PyErr_Occurred()) throw std::exception();
+    if (x == -1.0 && PyErr_Occurred()) throw Raised();
     d.scale = (float)x;
   }
   d.offsets = static_cast<const int32_t*>(ptr(offsets));
@@ -408,7 +410,7 @@ PyObject* adamw(Args a) {
     hp.step_device = static_cast<const int64_t*>(counted.data_ptr());
   } else {
     hp.step = PyLong_AsLongLong(step);
-    if (hp.step == -1 && PyErr_Occurred()) throw std::exception();
+    if (hp.step == -1 && PyErr_Occurred()) throw Raised();
   }
   const Py_ssize_t n = P.n;
   if (G.n != n || M.n != n || V.n != n) bad("P, G, M and V must have one length");
@@ -460,16 +462,20 @@ PyObject* adamw(Args a) {
   return Py_BuildValue("(i)", code);
 }
 
+// torch's errors become the Python exceptions that they are elsewhere (an allocation that fails:
+// torch.cuda.OutOfMemoryError).
 template <PyObject* (*F)(Args)>
 PyObject* entry(PyObject*, PyObject* const* at, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
   try {
     return F(Args{at, count});
   } catch (const Bad& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const std::exception& e) {
-    if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
+    return nullptr;
+  } catch (const Raised&) {
+    return nullptr;
   }
-  return nullptr;
+  END_HANDLE_TH_ERRORS
 }
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(entry<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {ENTRY(norm_rope),      ENTRY(norm_rope_backward), ENTRY(packed_size), ENTRY(packed_forward),

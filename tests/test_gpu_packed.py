@@ -597,3 +597,17 @@ def test_only_strangers():
         torch.cuda.synchronize()
         assert torch.all(o == 0) and torch.all(lse == -float("inf")) and torch.all(smax == -float("inf"))
         assert all(torch.all(x == 0) for x in grads)
+
+
+def test_allocation_that_fails_raises_torchs_error():
+    """Views of a few values that stand for more rows than memory holds: the outputs cannot be allocated,
+    torch says so, and the next call works."""
+    x = torch.ones(1, 1, 128, dtype=BF16, device="cuda")
+    q, k = x.expand(1 << 28, 16, 128), x.expand(1 << 28, 1, 128)           # 1.1 TB of q
+    offsets = torch.tensor([0, 1 << 28], dtype=torch.int32, device="cuda")
+    for call in (lambda: mc.qk_attention_packed_forward(q, k, k, offsets), lambda: mc.qk_norm_rope(q, k)):
+        with pytest.raises(torch.cuda.OutOfMemoryError):
+            call()
+    y, _, _ = mc.qk_norm_rope(x)
+    torch.cuda.synchronize()
+    assert torch.isfinite(y).all()
