@@ -3,12 +3,13 @@
 Each translation unit is compiled in parallel, then linked against the shared
 CUDA runtime.  Beside it the binding's helper module _host.so (host code) is
 compiled against torch's headers and linked to the library.  Both are rebuilt
-only when a source or header is newer.  Run as ``python -m muon_qk_clip_gb300.build``.
+only when a source or header is newer, or torch is another version.  Run as ``python -m muon_qk_clip_gb300.build``.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
@@ -23,6 +24,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuonclip.so")
 HOST = os.path.join(PKG, "_host.so")
 HOST_SRC = os.path.join(CSRC, "host.cxx")
+HOST_TORCH = os.path.join(BUILD, "host.torch")         # the torch that _host.so was compiled against
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -47,8 +49,11 @@ def sources():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOST):
+    if not os.path.exists(LIB) or not os.path.exists(HOST) or not os.path.exists(HOST_TORCH):
         return True
+    with open(HOST_TORCH) as f:
+        if f.read() != importlib.metadata.version("torch"):
+            return True
     t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
     deps = sources() + [HOST_SRC] + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh")) \
         + glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
@@ -90,6 +95,8 @@ def _link_host(obj: str):
     if r.returncode != 0:
         raise RuntimeError(f"link of _host.so failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, HOST)
+    with open(HOST_TORCH, "w") as f:
+        f.write(importlib.metadata.version("torch"))
 
 
 def _gxx() -> str:

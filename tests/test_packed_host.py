@@ -303,3 +303,14 @@ def test_struct_layouts(tmp_path):
     subprocess.run(["gcc", "-std=c99", str(src), "-o", str(tmp_path / "l")], check=True)
     got = subprocess.run([str(tmp_path / "l")], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == want
+
+
+def test_another_torch_makes_the_build_stale(lib, monkeypatch, tmp_path):
+    """_host.so is compiled against one torch's headers: with another version it is built again."""
+    from muon_qk_clip_gb300 import build
+    assert not build._stale()
+    other = tmp_path / "host.torch"
+    monkeypatch.setattr(build, "HOST_TORCH", str(other))
+    assert build._stale()
+    other.write_text("0.0")
+    assert build._stale()
