@@ -319,3 +319,24 @@ def test_norm_weights_move_over_steps():
         assert np.max(np.abs(f64(W[n]) - P[n])) <= 12 * (hp.lr * 200 * 2.0 ** -24 + 2.0 ** -23)
         assert torch.all(W[n] != start[n]) and float((W[n] - start[n]).abs().mean()) > 2 * hp.lr
     assert not torch.equal(first, run(X, W, H, G, offsets, do)[0])
+
+
+@pytest.mark.parametrize("lens,H,G,d,dv,rot", [([60, 9], 4, 2, 36, 20, 36), ([131], 3, 1, 90, 33, 30), ([40, 17], 1, 1, 18, 17, 0)])
+def test_layer_of_widths_that_are_no_multiple_of_eight(lens, H, G, d, dv, rot):
+    """The layer's features come in rows that the packed attention takes, its gradients in rows that
+    the projections' take."""
+    D, T = 64, sum(lens)
+    W, X, do = layer(D, H, G, d, dv), mk((T, D), 1.0, "x"), mk((T, H, dv), 0.05, "do")
+    held = torch.zeros((T, H, (dv + 7) // 8 * 8), dtype=BF16, device="cuda")[..., :dv]
+    held.copy_(do)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    o, _, dW, dX = run(X, W, H, G, offsets_of(lens), held, rot, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    x, w = X.double().cpu().requires_grad_(True), {n: t.double().cpu().requires_grad_(True) for n, t in W.items()}
+    ref, _ = layer64(x, w, H, G, lens, rot)
+    (ref * do.double().cpu()).sum().backward()
+    close(o, ref, "o")
+    for n in W:
+        close(dW[n], w[n].grad, n)
+    close(dX, x.grad, "dX")

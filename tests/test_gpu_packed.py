@@ -611,3 +611,34 @@ def test_allocation_that_fails_raises_torchs_error():
     y, _, _ = mc.qk_norm_rope(x)
     torch.cuda.synchronize()
     assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("lens,H,G,d,dv", [([70, 1, 200], 4, 2, 17, 33), ([300], 6, 2, 90, 20), ([129, 15], 1, 1, 127, 125),
+                                           ([512], 16, 1, 30, 18), ([5] * 40, 3, 1, 100, 63)])
+def test_widths_that_are_no_multiple_of_eight(lens, H, G, d, dv):
+    """Rows padded to whole 16 bytes: what lies behind the features (NaN here) is neither read nor
+    written, and outputs that the call allocates have such rows."""
+    def pad(t, fill):
+        held = torch.full((*t.shape[:2], (t.shape[2] + 7) // 8 * 8 + 8), fill, dtype=BF16, device="cuda")
+        held[..., :t.shape[2]] = t
+        return held[..., :t.shape[2]], held[..., t.shape[2]:]
+
+    q, k, v, do, offsets = features(lens, H, G, d, dv, seed=d, sharp=4.0)
+    (q, _), (k, _), (v, _), (do, _) = (pad(t, float("nan")) for t in (q, k, v, do))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and got[0].stride(1) % 8 == 0
+    check_forward(got, q, k, v, offsets)
+    out, rest = pad(torch.zeros_like(got[0]), 7.0)
+    mc.qk_attention_packed_forward(q, k, v, offsets, out=out)
+    assert torch.equal(out, got[0]) and torch.all(rest == 7.0)
+    o, lse, _ = got
+    args = (q, k, v, o, lse, do, offsets)
+    grads = mc.qk_attention_packed_backward(*args, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    check_backward(grads, *args)
+    held = [pad(torch.zeros_like(t), 7.0) for t in (q, k, v)]
+    again = mc.qk_attention_packed_backward(*args, dq=held[0][0], dk=held[1][0], dv=held[2][0])
+    assert all(torch.equal(x, y) for x, y in zip(again, grads)) and all(torch.all(r == 7.0) for _, r in held)
