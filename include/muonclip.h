@@ -474,6 +474,8 @@ typedef struct {
   float eps;                     /* >= 0                                         */
   double theta;                  /* >= 1e-6                                      */
   const int32_t* positions;      /* device [T], any values; NULL: token t is at t */
+  int32_t no_norm;               /* 1: the heads are not normalised: rstd is 1, and no pointer to it is looked at */
+  int32_t _pad;
 } mc_heads;
 
 /* Per token and head, fp32 arithmetic:

@@ -92,7 +92,8 @@ class McPackedGrad(ctypes.Structure):
 
 class McHeads(ctypes.Structure):
     _fields_ = [("T", c_int64), ("heads_q", c_int32), ("heads_k", c_int32), ("d", c_int32), ("rot", c_int32),
-                ("dtype", c_int32), ("eps", c_float), ("theta", c_double), ("positions", c_void_p)]
+                ("dtype", c_int32), ("eps", c_float), ("theta", c_double), ("positions", c_void_p),
+                ("no_norm", c_int32), ("_pad", c_int32)]
 
 
 class McAdamTensor(ctypes.Structure):

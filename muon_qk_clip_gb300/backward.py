@@ -118,9 +118,9 @@ def project_gqa_backward(X, W, dq, dk, dv, saved, positions=None, rot=None, thet
     those in no sequence must be zeros, as qk_attention_packed_backward allocates them,
     and their rows of X finite.  No gradient is overwritten."""
     q, k, rstd = saved
-    with _on_device(X, dq, dk, dv, q, k, rstd, *W.values(), *(() if positions is None else (positions,))):
+    with _on_device(X, dq, dk, dv, q, k, *W.values(), *(t for t in (rstd, positions) if t is not None)):
         T, D = X.shape
-        dq, dk, dwq, dwk = mc.qk_norm_rope_backward(dq, dk, q, k, rstd, *_gains(W, X.dtype), positions, theta, rot)
+        dq, dk, dwq, dwk = mc.qk_norm_rope_backward(dq, dk, q, k, rstd, *_gains(W, X.dtype), positions, theta, rot, norm=rstd is not None)
         parts = {"W_Q": dq.reshape(T, -1), "W_K": dk.reshape(T, -1), "W_V": dv.reshape(T, -1)}
         dW = {n: _weight(d, X, status) for n, d in parts.items()}
         dW.update({n: d for n, d in (("q_norm", dwq), ("k_norm", dwk)) if d is not None})

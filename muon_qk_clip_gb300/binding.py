@@ -629,14 +629,16 @@ def rms_norm_backward_workspace_size(cols: int) -> int:
 
 @_on_stream
 def qk_norm_rope(q, k=None, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None, eps: float = 1e-6,
-                 out_q=None, out_k=None, rstd=None, *, stream=None):
+                 out_q=None, out_k=None, rstd=None, norm=True, *, stream=None):
     """RMS norm of every head of q [T, heads, d] and k [T, key heads, d] (bf16 or
     fp32, features with unit stride, other strides free: views of one projection),
     times wq, wk [d] if given, then the rotary embedding of the last `rot` features
     (all by default, interleaved pairs as in rope_) at `positions` [T] int32 (the
     token's number without).  Returns (yq, yk or None, rstd [T, heads + key heads]
-    f32); out_q=q and out_k=k run in place."""
-    return _native("norm_rope", "mc_head_norm_rope", q, k, wq, wk, positions, theta, rot, eps, out_q, out_k, rstd)
+    f32); out_q=q and out_k=k run in place.  norm=False leaves the norm out (weights and
+    rotation alone), and rstd is None."""
+    return _native("norm_rope", "mc_head_norm_rope", q, k, wq, wk, positions, theta, rot, eps, out_q, out_k, rstd,
+                   bool(norm))
 
 
 def head_norm_backward_workspace_size(d: int) -> int:
@@ -648,15 +650,15 @@ def head_norm_backward_workspace_size(d: int) -> int:
 
 @_on_stream
 def qk_norm_rope_backward(dyq, dyk, q, k, rstd, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None,
-                          dq=None, dk=None, dwq=None, dwk=None, workspace=None, *, stream=None):
-    """Gradient of qk_norm_rope given its inputs, the rstd that it returned and the
-    outputs' gradients (dyk and k None without keys): (dq, dk or None, dwq, dwk), the
+                          dq=None, dk=None, dwq=None, dwk=None, workspace=None, norm=True, *, stream=None):
+    """Gradient of qk_norm_rope given its inputs, the rstd that it returned (None with
+    norm=False) and the outputs' gradients (dyk and k None without keys): (dq, dk or None, dwq, dwk), the
     weights' [d] f32, None without a weight unless one is given to write.  dq may be
     dyq or q and dk may be dyk or k (in place).  workspace: a CUDA tensor of
     head_norm_backward_workspace_size(d) bytes, allocated for the call where a weight
     gradient needs one and none is given."""
     return _native("norm_rope_backward", "mc_head_norm_rope_backward", dyq, dyk, q, k, rstd, wq, wk, positions, theta, rot,
-                   dq, dk, dwq, dwk, workspace)
+                   dq, dk, dwq, dwk, workspace, bool(norm))
 
 
 @dataclass

@@ -68,7 +68,7 @@ struct Params {
   Side side[2];
   unsigned long long turn[kMaxPairs];             // of pair k, in 2^-64 turns per position
   const int* positions;                           // or null: the token's number
-  float* rstd;                                    // [T, heads of both]
+  float* rstd;                                    // [T, heads of both]; null without a norm
   float* part;                                    // gradient: [blocks][2][d] weight sums, or null
   int T, d, rot, heads;
   int lanes;                                      // per row: a power of two
@@ -274,7 +274,9 @@ struct Rows {
   }
 };
 
-template <typename T, int V, int NU, bool WHOLE>
+// NORM: false for heads that are rotated (and weighted) only.  A kernel of its own: the choice at
+// run time took a hundredth of the gradient's time.
+template <typename T, int V, int NU, bool WHOLE, bool NORM>
 __global__ void __launch_bounds__(kFrontThreads, front_blocks(NU)) head_norm_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) char fifo[];
   await_previous();
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(kFrontThreads, front_blocks(NU)) head_norm_ker
     for (int n = 0; n < kFlight; ++n) {
       const int h = i * kFlight + n;               // of this lane's rows
       if (h >= x.left) continue;
-      const float rstd = rsqrtf(fmaf(sums[n], p.inv_d, p.eps));
-      if (sub == 0) rstds[h * rows] = rstd;
+      const float rstd = NORM ? rsqrtf(fmaf(sums[n], p.inv_d, p.eps)) : 1.f;
+      if (NORM && sub == 0) rstds[h * rows] = rstd;
       const Two r2 = two(rstd, rstd);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
@@ -363,7 +365,7 @@ __global__ void __launch_bounds__(kFrontThreads, front_blocks(NU)) head_norm_ker
   }
 }
 
-template <typename T, int V, int NU, bool WHOLE>
+template <typename T, int V, int NU, bool WHOLE, bool NORM>
 __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) char fifo[];    // rows on their way; then [2][rows of all warps][d] weight sums
   await_previous();
@@ -412,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
       float r[F], r1[F];                          // rstd of this step's rows, and of the next one's
       auto load_r = [&](int i) {
 #pragma unroll
-        for (int n = 0; n < F; ++n) r1[n] = i * F + n < x.left ? rs[(i * F + n) * rows] : 0.f;
+        for (int n = 0; n < F; ++n) r1[n] = !NORM ? 1.f : i * F + n < x.left ? rs[(i * F + n) * rows] : 0.f;
       };
       load_r(0);
       Turn<V, NU, sizeof(T) == 2> turn;
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, back_blocks(NU)) head_norm_back_kern
 #pragma unroll
           for (int u = 0; u < NU; ++u) {
 #pragma unroll
-            for (int k = 0; k < V / 2; ++k) a[n][u][k] = mul2(r2, fma2(a[n][u][k], m2, b[n][u][k]));
+            for (int k = 0; k < V / 2; ++k) a[n][u][k] = NORM ? mul2(r2, fma2(a[n][u][k], m2, b[n][u][k])) : b[n][u][k];
             if (V * p.lanes * u < x.cols) R::put(o + h * (rows * S.oh) + V * p.lanes * u, a[n][u]);
           }
         }
@@ -638,9 +640,10 @@ cudaError_t run_forward(Params& p, cudaStream_t s) {
   split(p, V * NU, kFlight, sm_count() * 32);
   const long long units = (long long)p.T * (p.pieces[0] + p.pieces[1]);
   constexpr size_t smem = WHOLE ? (size_t)kDepth * kFlight * NU * kFrontThreads * V * sizeof(T) : 0;
-  const cudaError_t e = cudaFuncSetAttribute(head_norm_kernel<T, V, NU, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const auto kernel = p.rstd ? head_norm_kernel<T, V, NU, WHOLE, true> : head_norm_kernel<T, V, NU, WHOLE, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_behind(head_norm_kernel<T, V, NU, WHOLE>, (unsigned)cdiv(units, kFrontWarps), kFrontThreads, smem, s, p);
+  return launch_behind(kernel, (unsigned)cdiv(units, kFrontWarps), kFrontThreads, smem, s, p);
 }
 template <typename T, int V, int NU, bool WHOLE>
 cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
@@ -651,9 +654,10 @@ cudaError_t run_backward(Params& p, float* dwq, float* dwk, cudaStream_t s) {
   constexpr size_t fifo = WHOLE ? (size_t)2 * kDepth * kFlight * NU * kThreads * V * sizeof(T) : 0, most_sums = 2 * kWarps * MC_HEAD_MAX * 4;
   const size_t smem = fifo + (p.part ? (size_t)2 * kWarps * (32 / p.lanes) * p.d * 4 : 0);   // a warp's rows have at most 256 features
   // the limit belongs to the kernel, not to this call: always that of the largest
-  cudaError_t e = cudaFuncSetAttribute(head_norm_back_kernel<T, V, NU, WHOLE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fifo + most_sums));
+  const auto kernel = p.rstd ? head_norm_back_kernel<T, V, NU, WHOLE, true> : head_norm_back_kernel<T, V, NU, WHOLE, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(fifo + most_sums));
   if (e != cudaSuccess) return e;
-  e = launch_behind(head_norm_back_kernel<T, V, NU, WHOLE>, (unsigned)grid, kThreads, smem, s, p);
+  e = launch_behind(kernel, (unsigned)grid, kThreads, smem, s, p);
   if (e != cudaSuccess || !p.part) return e;
   return launch_behind(head_weight_kernel, (unsigned)cdiv(2 * p.d, 32), 1024, 0, s, p.part, dwq, dwk, grid, p.d);
 }
@@ -697,7 +701,8 @@ mc_status mc_head_norm_rope(const mc_heads* h, const void* q, int64_t q_token, i
   if (st != MC_OK) return st;
   if (h->T == 0) return record_error(MC_OK, "");
   const int64_t es = h->dtype == MC_BF16 ? 2 : 4, H = h->heads_q, G = h->heads_k;
-  if (!q || !yq || !rstd || (G && (!k || !yk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  if (h->no_norm) rstd = nullptr;
+  if (!q || !yq || (!rstd && !h->no_norm) || (G && (!k || !yk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
   Operand ops[] = {rows_of("q", q, q_token, q_head, H),
                    rows_of("k", k, k_token, k_head, G),
                    rows_of("yq", yq, yq_token, yq_head, H, true, q, q),
@@ -746,7 +751,8 @@ mc_status mc_head_norm_rope_backward(const mc_heads* h, const void* dyq, int64_t
     }
     return record_error(MC_OK, "");
   }
-  if (!dyq || !q || !rstd || !dq || (G && (!dyk || !k || !dk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
+  if (h->no_norm) rstd = nullptr;
+  if (!dyq || !q || (!rstd && !h->no_norm) || !dq || (G && (!dyk || !k || !dk))) return err(MC_ERR_INVALID_ARG, "%s: null pointer", me);
   const bool weights = dwq || (G && dwk);
   const size_t need = (size_t)kBackGrid * 2 * h->d * 4;
   if (weights && (!workspace || at(workspace) % 16 || workspace_bytes < need))

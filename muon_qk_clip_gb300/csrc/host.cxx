@@ -182,9 +182,12 @@ PyObject* norm_rope(Args a) {
   const int64_t rot = a.number("rot", q.dim() ? q.sizes().back() : 0);
   const double eps = a.real();
   at::Tensor out_q = a.maybe("out_q"), out_k = a.maybe("out_k"), rstd = a.maybe("rstd");
+  const bool norm = a.whole() != 0;
   const mc_stream_t stream = a.stream();
   one_device(q, {&k, &wq, &wk, &positions, &out_q, &out_k, &rstd});
-  const Heads s = heads_of(q, k, positions, theta, rot, eps);
+  Heads s = heads_of(q, k, positions, theta, rot, eps);
+  s.h.no_norm = !norm;
+  if (!norm && rstd.defined()) bad("rstd goes with a norm");
   rows("q", q, s.q, s.type);
   if (k.defined()) rows("k", k, s.k, s.type);
   else if (wk.defined() || out_k.defined()) bad("wk and out_k go with k");
@@ -192,7 +195,7 @@ PyObject* norm_rope(Args a) {
   if (wk.defined()) whole_tensor("wk", wk, {s.q[2]}, s.type);
   out_q = rows_or_new("out_q", out_q, q, s.q);
   if (k.defined()) out_k = rows_or_new("out_k", out_k, k, s.k);
-  rstd = whole_or_new("rstd", rstd, q, {s.q[0], s.q[1] + s.k[1]}, at::kFloat);
+  if (norm) rstd = whole_or_new("rstd", rstd, q, {s.q[0], s.q[1] + s.k[1]}, at::kFloat);
   const View x = view(q), y = view(k), xo = view(out_q), yo = view(out_k);
   const int code = called([&] {
     return mc_head_norm_rope(&s.h, x.p, x.token, x.head, y.p, y.token, y.head, ptr(wq), ptr(wk), xo.p, xo.token, xo.head, yo.p, yo.token,
@@ -202,19 +205,22 @@ PyObject* norm_rope(Args a) {
 }
 
 PyObject* norm_rope_backward(Args a) {
-  const at::Tensor dyq = a.tensor("dyq"), dyk = a.maybe("dyk"), q = a.tensor("q"), k = a.maybe("k"), rstd = a.tensor("rstd"), wq = a.maybe("wq"),
+  const at::Tensor dyq = a.tensor("dyq"), dyk = a.maybe("dyk"), q = a.tensor("q"), k = a.maybe("k"), rstd = a.maybe("rstd"), wq = a.maybe("wq"),
                    wk = a.maybe("wk"), positions = a.maybe("positions");
   const double theta = a.real();
   const int64_t rot = a.number("rot", q.dim() ? q.sizes().back() : 0);
   at::Tensor dq = a.maybe("dq"), dk = a.maybe("dk"), dwq = a.maybe("dwq"), dwk = a.maybe("dwk"), ws = a.maybe("workspace");
+  const bool norm = a.whole() != 0;
   const mc_stream_t stream = a.stream();
   one_device(q, {&dyq, &dyk, &k, &rstd, &wq, &wk, &positions, &dq, &dk, &dwq, &dwk, &ws});
-  const Heads s = heads_of(q, k, positions, theta, rot, 0.0);
+  Heads s = heads_of(q, k, positions, theta, rot, 0.0);
+  s.h.no_norm = !norm;
+  if (norm != rstd.defined()) bad(norm ? "rstd must be a tensor" : "rstd goes with a norm");
   if (k.defined() != dyk.defined() || (!k.defined() && (wk.defined() || dk.defined() || dwk.defined())))
     bad("k, dyk, wk, dk and dwk go together");
   rows("q", q, s.q, s.type);
   rows("dyq", dyq, s.q, s.type);
-  whole_tensor("rstd", rstd, {s.q[0], s.q[1] + s.k[1]}, at::kFloat);
+  if (rstd.defined()) whole_tensor("rstd", rstd, {s.q[0], s.q[1] + s.k[1]}, at::kFloat);
   dq = rows_or_new("dq", dq, q, s.q);
   if (k.defined()) {
     rows("k", k, s.k, s.type);

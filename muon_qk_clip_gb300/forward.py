@@ -93,19 +93,20 @@ def _heads(X, w, n):
     return mc.matmul(X, w.contiguous(), out=out).unflatten(1, (n, -1))
 
 
-def project_gqa(X, W, H: int, H_kv: int, positions=None, rot=None, theta: float = 10000.0, eps: float = 1e-6):
+def project_gqa(X, W, H: int, H_kv: int, positions=None, rot=None, theta: float = 10000.0, eps: float = 1e-6, norm=True):
     """Features of packed tokens X [T, D] with grouped heads: Q = X W_Q^T [T,H,d] and
     K = X W_K^T [T,H_kv,d], each head normalised, times W["q_norm"] and W["k_norm"]
     [d] where given (fp32 or X's type: rounded to that for the call), its last `rot` features (all by default) rotated at `positions`;
     V = X W_V^T [T,H_kv,d_v].  Returns (q, k, v, saved), saved for
     backward.project_gqa_backward.  Heads of a width that is no multiple of eight lie in
-    rows padded to one."""
+    rows padded to one.  norm=False: heads without a norm, whose logits may grow (QK-Clip's
+    layers: gqa_segments)."""
     with _on_device(X, *W.values(), *(() if positions is None else (positions,))):
         T = X.shape[0]
         q, k, v = _heads(X, W["W_Q"], H), _heads(X, W["W_K"], H_kv), _heads(X, W["W_V"], H_kv)
         d, dv = q.shape[2], v.shape[2]
         yq, yk, rstd = mc.qk_norm_rope(q, k, *_gains(W, X.dtype), positions, theta, rot, eps,
-                                       out_q=_padded(X, T, H, d), out_k=_padded(X, T, H_kv, d))
+                                       out_q=_padded(X, T, H, d), out_k=_padded(X, T, H_kv, d), norm=norm)
         if dv % 8:
             v = _padded(X, T, H_kv, dv).copy_(v)
         return yq, yk, v, (q, k, rstd)

@@ -52,12 +52,13 @@ def run(X, W, H, G, offsets, do, rot=None, status=None):
     return o, smax, dW, dX
 
 
-def layer64(x, w, H, G, lens, rot, theta=10000.0, eps=1e-6):
+def layer64(x, w, H, G, lens, rot, theta=10000.0, eps=1e-6, norm=True):
     """Output [T, H, dv] and S_max [H] in 64 bits."""
     T = x.shape[0]
     def heads(weight, n, gain):
         z = (x @ weight.T).view(T, n, -1)
-        z = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps)
+        if norm:
+            z = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps)
         z = z if gain is None else z * gain
         pos = torch.cat([torch.arange(n_) for n_ in lens]).double()
         ang = pos[:, None, None] * theta ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
@@ -340,3 +341,35 @@ def test_layer_of_widths_that_are_no_multiple_of_eight(lens, H, G, d, dv, rot):
     for n in W:
         close(dW[n], w[n].grad, n)
     close(dX, x.grad, "dX")
+
+
+@pytest.mark.parametrize("lens,H,G,d,dv,rot", [([37, 100, 0, 1, 62], 4, 2, 64, 64, 64), ([129, 15], 3, 1, 80, 48, 40)])
+def test_layer_without_head_norms_and_its_clip(lens, H, G, d, dv, rot):
+    """Plain rotary heads, whose logits may grow: gradients against fp64 autograd, and QK-Clip by the
+    forward's S_max on the query heads' rows brings the layer's S_max to tau."""
+    D, T = 192, sum(lens)
+    W = {n: t * 0.7 for n, t in layer(D, H, G, d, dv, norm=False).items()}
+    X, do, offsets = mk((T, D), 1.0, "x"), mk((T, H, dv), 0.05, "do"), offsets_of(lens)
+    pos = forward.packed_positions(offsets, T)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v, saved = forward.project_gqa(X, W, H, G, pos, rot, norm=False)
+    o, lse, smax = mc.qk_attention_packed_forward(q, k, v, offsets, lse=True, status=st)
+    dq, dk, dvv = mc.qk_attention_packed_backward(q, k, v, o, lse, do, offsets, status=st)
+    dW, dX = backward.project_gqa_backward(X, W, dq, dk, dvv, saved, pos, rot, status=st)
+    torch.cuda.synchronize()
+    assert st.item() == 0 and set(dW) == set(W)
+    x, w = X.double().cpu().requires_grad_(True), {n: t.double().cpu().requires_grad_(True) for n, t in W.items()}
+    ref, best = layer64(x, w, H, G, lens, rot, norm=False)
+    (ref * do.double().cpu()).sum().backward()
+    for got, want, name in [(o, ref, "o"), (dX, x.grad, "dX")] + [(dW[n], w[n].grad, n) for n in W]:
+        close(got, want, name)
+    # a logit: roundings of q and k behind the products and behind the rotation, 4 of 2^-8 of a norm each
+    reach = lambda t: float(t.float().norm(dim=-1).max())  # noqa: E731
+    most = 4 * 2.0 ** -8 * reach(q) * reach(k) / np.sqrt(d)
+    assert np.max(np.abs(f64(smax) - best.detach().numpy())) <= most
+    tau = float(smax.max()) * 0.5
+    mc.qk_clip_apply(smax, tau, mc.gqa_segments(W["W_Q"], H))
+    q, k, v, _ = forward.project_gqa(X, W, H, G, pos, rot, norm=False)
+    _, _, after = mc.qk_attention_packed_forward(q, k, v, offsets)
+    torch.cuda.synchronize()
+    assert np.all(np.abs(f64(after) - np.minimum(f64(smax), tau)) <= 2 * most)

@@ -276,3 +276,41 @@ def test_without_keys_their_pointers_are_not_looked_at(dtype):
                                           dw.data_ptr(), stale, ws.data_ptr(), ws.numel(), s) == abi.MC_OK
     torch.cuda.synchronize()
     assert torch.equal(y, want[0]) and torch.equal(rstd, want[2]) and torch.equal(dx, grad[0]) and torch.equal(dw, grad[2])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,H,G,d,rot", [(1, 1, 1, 2, 2), (33, 5, 2, 80, 80), (7, 2, 2, 90, 30), (130, 4, 0, 64, 0), (300, 9, 1, 256, 128)])
+def test_without_the_norm(T, H, G, d, rot, dtype):
+    """Rotation and weights alone: y = R (x w), dx = w R^T dy, dw = sum R^T dy x; bounds as with the
+    norm, which takes more roundings.  Infinite features reach their own rows of y and dw, no dx."""
+    q, k = normal((T, H, d), 2.0, "q", dtype), normal((T, G, d), 0.5, "k", dtype) if G else None
+    wq, wk = ((1 + normal((d,), 0.2, n, F32)).to(dtype) for n in ("wq", "wk"))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 37 % 1009
+    dyq, dyk = normal((T, H, d), 1e-2, "dq", dtype), normal((T, G, d), 1e-2, "dk", dtype) if G else None
+    cos, sin = turns(pos.cpu().numpy(), rot)
+    more = (32 if dtype == BF16 else 20) * W
+    for weights in (True, False):
+        a, b = (wq, wk if G else None) if weights else (None, None)
+        yq, yk, rstd = mc.qk_norm_rope(q, k, a, b, positions=pos, rot=rot, norm=False)
+        grads = mc.qk_norm_rope_backward(dyq, dyk, q, k, None, a, b, positions=pos, rot=rot, norm=False)
+        torch.cuda.synchronize()
+        assert rstd is None
+        for x, w, y, dy, dx, dw in ((q, a, yq, dyq, grads[0], grads[2]), (k, b, yk, dyk, grads[1], grads[3])):
+            if x is None:
+                continue
+            wt = np.ones(d) if w is None else f64(w)
+            want, s = rotated(f64(x) * wt, cos, sin)
+            assert_rounded_within(y, want, more * s + 1e-40)
+            dz, s = rotated(f64(dy), cos, -sin)
+            assert_rounded_within(dx, dz * wt, more * s * np.abs(wt) + 1e-40)
+            if w is not None:
+                n = x.shape[0] * x.shape[1]
+                assert np.all(np.abs(f64(dw) - (dz * f64(x)).sum((0, 1))) <= (n + 80) * W * (s * np.abs(f64(x))).sum((0, 1)))
+    clean = mc.qk_norm_rope_backward(dyq, None, q, None, None, rot=rot, norm=False)
+    q[0, 0] = float("inf")
+    bad = mc.qk_norm_rope_backward(dyq, None, q, None, None, rot=rot, norm=False)
+    assert torch.equal(clean[0], bad[0])
+    with pytest.raises(ValueError, match="rstd"):
+        mc.qk_norm_rope_backward(dyq, None, q, None, None, rot=rot)
+    with pytest.raises(ValueError, match="rstd"):
+        mc.qk_norm_rope(q, rstd=torch.empty(T, H, device="cuda"), norm=False)
