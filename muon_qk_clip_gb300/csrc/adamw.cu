@@ -314,9 +314,11 @@ __device__ inline float one_minus_power(long long t, const float (&l)[2]) {
   const float y = th * l[0], r = fmaf(th, l[0], -y) + fmaf(th, l[1], tl * l[0]), e = expm1f(y);
   return -fmaf(r, 1.f + e, e);
 }
-// The step's factors.  With a step on the device one thread of the block works its two out, in fp32,
-// while the block's first loads are on their way.  (2^27 values in bf16: 418 us with 32-bit states and
-// 212 with 8-bit ones, as with a step from the host; every thread for itself in fp64 702 and 234.)
+// The step's factors.  With a step on the device one thread of the block works its two out, in fp32.
+// (2^27 values in bf16: 418 us with 32-bit states and 212 with 8-bit ones, as with a step from the
+// host; every thread for itself in fp64 702 and 234.)  With 8-bit states they stand behind the block's first
+// loads (in front of them 216), with 32-bit ones in front (behind them 122 vectors of 7168, with a step
+// from the host, took 4.0 us of a graph instead of 3.6).
 __device__ inline void factors(const Coef& a, Chunk& c) {
   c.gs = a.grad_scale ? *a.grad_scale : 1.f;
   c.i1 = a.i1;
@@ -389,6 +391,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   Chunk k;
   constexpr int kSet = kThreads * kWide;
   const Tensor& t = chunk_of(a, kSet, k);
+  factors(a.c, k);
   P* p = static_cast<P*>(t.p) + k.first;
   const G* g = static_cast<const G*>(t.g) + k.first;
   float *m = static_cast<float*>(t.m) + k.first, *v = static_cast<float*>(t.v) + k.first;
@@ -415,7 +418,6 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   };
 #pragma unroll
   for (int s = 0; s < kAhead; ++s) load((s * kThreads + threadIdx.x) * kWide, raw[s]);
-  factors(a.c, k);
   for (int s0 = 0; s0 < a.steps; s0 += kAhead) {
 #pragma unroll
     for (int s = 0; s < kAhead; ++s) {
