@@ -17,8 +17,8 @@
 // to step; larger betas are refused.
 //
 // One pass over memory, 22 bytes a value with bf16 p and g and fp32 states, 10.1
-// with 8-bit ones: 2 x 65536 x 2048 values 831 us, 7.1 TB/s (a copy reaches 6.8;
-// 55 % are reads), 2 x 65521 x 2048 with 8-bit states 414 us, 6.6 TB/s (of four
+// with 8-bit ones: 2 x 65536 x 2048 values 833 us, 7.1 TB/s (a copy reaches 6.8;
+// 55 % are reads), 2 x 65521 x 2048 with 8-bit states 411 us, 6.6 TB/s (of four
 // values a thread twice that).  A block takes a chunk of one tensor and finds which by a
 // search over the chunks' prefix sums among the launch's parameters.
 #include <cuda_bf16.h>

@@ -26,8 +26,9 @@
 // the query tiles of every head of the key head's group, and every tile is bounded by
 // its sequence.  With few blocks of keys an item takes a part of these query tiles, and
 // a launch of its own (join_kernel) adds the parts' dK and dV up.  16384 tokens in eight
-// documents, 32 / 8 heads of 128: 975 us, 0.98 PFLOP/s of the five products (of the
-// seven that the passes compute 1.37); rows_kernel takes 46 of them, at 6 TB/s.
+// documents, 32 / 8 heads of 128: 890 us at first and 1010 in a long run of calls, under
+// the power limit, 1.07 and 0.94 PFLOP/s of the five products (of the seven that the passes
+// compute 1.50 and 1.32); rows_kernel takes 46 of them, at 6 TB/s.
 //
 // P and dS go from the compute warps to the tensor core through tensor memory
 // (the A operand of dV, dK and dQ), written over the columns of the S / dP that

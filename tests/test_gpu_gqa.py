@@ -52,13 +52,12 @@ def run(X, W, H, G, offsets, do, rot=None, status=None):
     return o, smax, dW, dX
 
 
-def layer64(x, w, H, G, lens, rot, theta=10000.0, eps=1e-6, norm=True):
+def layer64(x, w, H, G, lens, rot, theta=10000.0, eps=1e-6):
     """Output [T, H, dv] and S_max [H] in 64 bits."""
     T = x.shape[0]
     def heads(weight, n, gain):
         z = (x @ weight.T).view(T, n, -1)
-        if norm:
-            z = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps)
+        z = z / torch.sqrt(z.pow(2).mean(-1, keepdim=True) + eps)
         z = z if gain is None else z * gain
         pos = torch.cat([torch.arange(n_) for n_ in lens]).double()
         ang = pos[:, None, None] * theta ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
@@ -359,7 +358,9 @@ def test_layer_without_head_norms_and_its_clip(lens, H, G, d, dv, rot):
     torch.cuda.synchronize()
     assert st.item() == 0 and set(dW) == set(W)
     x, w = X.double().cpu().requires_grad_(True), {n: t.double().cpu().requires_grad_(True) for n, t in W.items()}
-    ref, best = layer64(x, w, H, G, lens, rot, norm=False)
+    # in 64 bits, x / sqrt(mean + 1e300) * 1e150 is x: a head that is not normalised
+    one = {n: torch.full((d,), 1e150, dtype=torch.float64) for n in ("q_norm", "k_norm")}
+    ref, best = layer64(x, {**w, **one}, H, G, lens, rot, eps=1e300)
     (ref * do.double().cpu()).sum().backward()
     for got, want, name in [(o, ref, "o"), (dX, x.grad, "dX")] + [(dW[n], w[n].grad, n) for n in W]:
         close(got, want, name)
