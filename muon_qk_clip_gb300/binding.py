@@ -372,8 +372,9 @@ def qk_attention_packed_backward(q, k, v, out, lse, dout, offsets, scale=None, d
     """Gradients of qk_attention_packed_forward's output: out, lse as it returned
     them, dout [T,H,dv]; the other arguments as there.  Returns (dq, dk, dv), dk and
     dv summed over the query heads of a group; rows of tokens in no sequence are zeros
-    in outputs that the call allocates and left as they were in given ones.  Outputs are allocated unless given: contiguous, or, of a width that is no
-    multiple of eight, in rows padded to one.  workspace: a CUDA tensor of
+    in outputs that the call allocates and left as they were in given ones.  Outputs are
+    allocated unless given: contiguous, or, of a width that is no multiple of eight, in
+    rows padded to one.  workspace: a CUDA tensor of
     packed_workspace_size(..., backward=True) bytes; without one, one is allocated."""
     return _native("packed_backward", "qk_attention_packed_backward", q, k, v, out, lse, dout, offsets, scale, dq, dk, dv,
                    workspace, status)
@@ -652,8 +653,8 @@ def head_norm_backward_workspace_size(d: int) -> int:
 def qk_norm_rope_backward(dyq, dyk, q, k, rstd, wq=None, wk=None, positions=None, theta: float = 10000.0, rot=None,
                           dq=None, dk=None, dwq=None, dwk=None, workspace=None, norm=True, *, stream=None):
     """Gradient of qk_norm_rope given its inputs, the rstd that it returned (None with
-    norm=False) and the outputs' gradients (dyk and k None without keys): (dq, dk or None, dwq, dwk), the
-    weights' [d] f32, None without a weight unless one is given to write.  dq may be
+    norm=False) and the outputs' gradients (dyk and k None without keys): (dq, dk or
+    None, dwq, dwk), the weights' [d] f32, None without a weight unless one is given to write.  dq may be
     dyq or q and dk may be dyk or k (in place).  workspace: a CUDA tensor of
     head_norm_backward_workspace_size(d) bytes, allocated for the call where a weight
     gradient needs one and none is given."""
@@ -697,10 +698,9 @@ def adamw_step(P, G, M, V, hp: AdamHparams | None = None, step=1, m_scales=None,
     what muonclip_step does not take: embeddings, output tables, norm weights.
     P, G: lists of contiguous bf16 or fp32 tensors of any shape, pair by pair of one
     size; M, V: their moments, fp32, or e4m3 (M and the root of V) with m_scales and
-    v_scales, as adamw_state makes them; all updated in place.  8-bit states take betas up to
-    0.95, and want gradients that vary (the C header says what their rounding does over many
-    steps).  step: 1 for the first
-    one, or a device int64 tensor of one value that is read when the step runs (for a
+    v_scales, as adamw_state makes them; all updated in place.  8-bit states take
+    betas up to 0.95, and want gradients that vary (the C header says what their
+    rounding does over many steps).  step: 1 for the first one, or a device int64 tensor of one value that is read when the step runs (for a
     captured step).  grad_scale: a device fp32 tensor of one value that multiplies
     every gradient (clipping by the global norm).  Tensors of one set of types share
     launches.  The new p is rounded to its type once: a bf16 value stays where it is under an

@@ -10,8 +10,8 @@
 // The root is stored, not v: it is what divides, and e4m3's 2^-9 .. 448 then
 // spans 2^35 of v within a block, at 2^-4 of the root.  A root above zero never
 // becomes zero (the least code is 2^-9) while its square is in fp32's range, from 2^-74 up:
-// a forgotten v would divide its next gradient by eps alone.  The parameter's step takes m and v before their
-// rounding.  A code moves only when a step changes its value by half the way to the
+// a forgotten v would divide its next gradient by eps alone.  The parameter's step takes
+// m and v before their rounding.  A code moves only when a step changes its value by half the way to the
 // next one, 3.1 to 5.6 %: beta2 = 0.95 lowers a root by 2.5 % at most, and v follows its
 // gradients because the blocks' scales, and with them the codes' places, vary from step
 // to step; larger betas are refused.

@@ -24,9 +24,9 @@
 // 16384 tokens in eight documents, 32 / 8 heads of 128, 300 us at first and 320 in a long
 // run of calls, under the power limit, 1.27 and 1.19 PFLOP/s; 24571 in one, 16 / 2 heads,
 // 1500 and 1600 us, 1.65 and 1.54 (measured peak 1.93; the tensor pipe is 67 % active, the
-// exponentials' a third).  Beyond the long one's rate the documents take some 4 us for each of the
-// 14 items of an SM, where one item's end and the next one's start do not overlap.  The first scores of the next item behind the last
-// products of one (323 to 321 us in one run), P handed over in halves (319; the long one 1648 to
+// exponentials' a third).  Beyond the long one's rate the documents take some 4 us for each
+// of an SM's 14 items (as a whole; its parts are not measured).  The first scores of the
+// next item behind the last products of one (323 to 321 us in one run), P handed over in halves (319; the long one 1648 to
 // 1605), finite checks on the diagonal's blocks alone and these by groups of 32
 // columns (307; 1550) were kept in that order.
 //

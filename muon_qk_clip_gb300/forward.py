@@ -96,8 +96,8 @@ def _heads(X, w, n):
 def project_gqa(X, W, H: int, H_kv: int, positions=None, rot=None, theta: float = 10000.0, eps: float = 1e-6, norm=True):
     """Features of packed tokens X [T, D] with grouped heads: Q = X W_Q^T [T,H,d] and
     K = X W_K^T [T,H_kv,d], each head normalised, times W["q_norm"] and W["k_norm"]
-    [d] where given (fp32 or X's type: rounded to that for the call), its last `rot` features (all by default) rotated at `positions`;
-    V = X W_V^T [T,H_kv,d_v].  Returns (q, k, v, saved), saved for
+    [d] where given (fp32 or X's type: rounded to that for the call), its last `rot`
+    features (all by default) rotated at `positions`; V = X W_V^T [T,H_kv,d_v].  Returns (q, k, v, saved), saved for
     backward.project_gqa_backward.  Heads of a width that is no multiple of eight lie in
     rows padded to one.  norm=False: heads without a norm, whose logits may grow (QK-Clip's
     layers: gqa_segments)."""
